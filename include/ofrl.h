@@ -457,6 +457,142 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
                                            int32_t state_stride, int32_t batch, const float* q_taken, float tau,
                                            float* v_out, float* loss_out, float* grad_out, void* stream);
 
+/* ---- sequence memory: the gated delta rule over packed episodes ---------- */
+
+/* A recurrent memory for states that are not Markov: an associative state
+ * S [v_dim, k_dim] per value head, zero (or given) when an episode starts,
+ *
+ *   S_t = a_t S_{t-1} + u_t k_t^T,  a_t = exp(g_t),
+ *   u_t = beta_t (v_t - a_t S_{t-1} k_t),   o_t = scale S_t q_t,
+ *
+ * so S_t k_t moves from its decayed prediction toward v_t by beta_t |k_t|^2.
+ * With unit keys and beta in [0, 1] the state stays bounded; larger
+ * beta |k|^2 is computed as it stands.  g_t = -inf forgets everything before
+ * t.  No counterpart on the pages, whose networks see one transition at a
+ * time.
+ *
+ * Tokens are transitions in buffer order: token t of episode e lies between
+ * episode_ends[e - 1] (0 for the first) and episode_ends[e], the convention of
+ * ofrl_replay, except that an episode may be empty (its end repeats the one
+ * before; its final state is its initial one).  The ends are device data: an
+ * end below its predecessor or above `tokens` is counted in
+ * OFRL_STAT_BAD_INDEX by the forward call, and what that call writes is then
+ * unspecified (every access stays in bounds).  Tokens at and after the last
+ * end belong to no episode; their outputs and gradients are not written.
+ *
+ * Value head h reads query and key head h / (v_heads / k_heads); dq and dk
+ * sum over the value heads of a group, in a fixed order. */
+enum { OFRL_DTYPE_F32 = 0, OFRL_DTYPE_BF16 = 1 };
+
+typedef struct {
+    int32_t k_heads;   /* query and key heads, 1 .. 1024 */
+    int32_t v_heads;   /* value heads, a multiple of k_heads, at most 1024 */
+    int32_t k_dim;     /* 8 .. 128, a multiple of 8 */
+    int32_t v_dim;     /* 8 .. 128, a multiple of 8 */
+    int32_t dtype;     /* OFRL_DTYPE_* of every token buffer (q k v g beta out and gradients); states are fp32 */
+} ofrl_delta_shape;
+
+/* Tokens of one call, device.  A stride is the distance between tokens in
+ * elements; heads are contiguous within a token.  q, k, v: 16-byte aligned,
+ * strides multiples of 16 bytes; g, beta: any stride >= v_heads. */
+typedef struct {
+    const void* q;       /* [tokens][k_heads, k_dim] */
+    const void* k;       /* [tokens][k_heads, k_dim] */
+    const void* v;       /* [tokens][v_heads, v_dim] */
+    const void* g;       /* [tokens][v_heads] log decay */
+    const void* beta;    /* [tokens][v_heads] write strength */
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+    int64_t tokens;      /* 0 .. 2^31-1 */
+    float scale;         /* of the outputs, finite */
+} ofrl_delta_tokens;
+
+/* Gradients of one call, device, written (not accumulated): same layouts,
+ * alignments and stride rules as the tokens they belong to. */
+typedef struct {
+    void* dq;
+    void* dk;
+    void* dv;
+    void* dg;
+    void* dbeta;
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+} ofrl_delta_grads;
+
+typedef struct ofrl_delta ofrl_delta;
+
+/* Create the workspace for sequences of up to max_tokens tokens in up to
+ * max_episodes episodes (only ofrl_delta_backward uses memory that grows with
+ * them: backward = 0 reserves none of it and refuses that call).  The only
+ * allocating call; binds to the current device.  One ofrl_delta must not be
+ * used by two calls that overlap on the GPU. */
+ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens, int32_t max_episodes,
+                              int32_t backward, ofrl_delta** out);
+ofrl_status ofrl_delta_destroy(ofrl_delta* ctx);
+
+/* As ofrl_poll_status, of the ofrl_delta's own status word. */
+ofrl_status ofrl_delta_poll_status(ofrl_delta* ctx, void* stream, int32_t* words_out);
+
+/* Bytes of device memory ofrl_delta_create reserves, or -1 for bad arguments. */
+int64_t ofrl_delta_workspace_bytes(const ofrl_delta_shape* shape, int64_t max_tokens, int32_t max_episodes,
+                                   int32_t backward);
+
+/* Bytes of the `saved` buffer (device, 256-byte aligned, the caller's) that
+ * hands a forward call's per-chunk states to its backward call, or -1. */
+int64_t ofrl_delta_saved_bytes(const ofrl_delta_shape* shape, int64_t tokens, int32_t num_episodes);
+
+/* Forward over packed episodes.  episode_ends: device [num_episodes].
+ * init_state: device fp32 [num_episodes, v_heads, v_dim, k_dim], 16-byte
+ * aligned, or NULL (zero).  out: device [tokens, v_heads, v_dim], contiguous,
+ * 16-byte aligned.  final_state: as init_state, or NULL; may be init_state.
+ * saved: device, ofrl_delta_saved_bytes, or NULL (no backward will follow). */
+ofrl_status ofrl_delta_forward(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* episode_ends,
+                               int32_t num_episodes, const float* init_state, void* out, float* final_state,
+                               void* saved, void* stream);
+
+/* Backward of the forward call that filled `saved` with the same tokens and
+ * ends: dout as `out`; d_final: gradient of final_state, fp32, or NULL (zero);
+ * d_init: gradient of init_state, fp32, or NULL (not wanted); may be d_final. */
+ofrl_status ofrl_delta_backward(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* episode_ends,
+                                int32_t num_episodes, const void* saved, const void* dout, const float* d_final,
+                                const ofrl_delta_grads* grads, float* d_init, void* stream);
+
+/* One token for each of in->tokens environments, each with a state of its
+ * own: state_in, state_out device fp32 [slots, v_heads, v_dim, k_dim], 16-byte
+ * aligned (the same buffer updates in place); slot_idx: device int32
+ * [tokens], the state of each token, or NULL (token i has state i, slots >=
+ * tokens).  Two tokens of one call must not name one slot.  A slot outside
+ * [0, slots) is counted in OFRL_STAT_BAD_INDEX: its token's output is zero
+ * and no state is written.  With slot_idx, slots of state_out that no token
+ * names are left as they are. */
+ofrl_status ofrl_delta_step(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* slot_idx, int32_t slots,
+                            const float* state_in, float* state_out, void* out, void* stream);
+
+/* ---- gradients kept in many tensors ---------------------------------------- */
+
+/* A list of n device tensors (host arrays of pointers, element counts and
+ * OFRL_DTYPE_* types; a size may be 0 and its pointer then NULL; pointers
+ * aligned to their element; n 1 .. 2^20).  Creating it copies the list to the
+ * device (the only allocation; the scratch of the calls below is part of it);
+ * the tensors stay the caller's and must outlive it.  One list must not be
+ * used by two calls that overlap on the GPU. */
+typedef struct ofrl_tensors ofrl_tensors;
+ofrl_status ofrl_tensors_create(const void* const* ptrs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
+                                ofrl_tensors** out);
+ofrl_status ofrl_tensors_destroy(ofrl_tensors* list);
+
+/* norm_out[0] (device fp32) = the 2-norm over all elements of all tensors:
+ * fp32 squares summed in a fixed order.  Next to ofrl_adam_step, whose
+ * grad_norm it is: each parameter tensor's step then clips by the global
+ * norm.  Non-finite elements make it non-finite. */
+ofrl_status ofrl_global_norm(ofrl_tensors* list, float* norm_out, void* stream);
+
+/* The norm n as above, then every element times s = (n > max_norm && n > 0)
+ * ? max_norm / n : 1 ("DQN Backward-Path NaN Audit", the clip formula),
+ * rounded to its tensor's type.  out: a list with the same sizes and types
+ * that receives the result (it must not overlap `list`), or NULL: in place.
+ * max_norm > 0 (+inf: s = 1). */
+ofrl_status ofrl_global_norm_clip(ofrl_tensors* list, float max_norm, float* norm_out, ofrl_tensors* out,
+                                  void* stream);
+
 /* ---- measurement hooks (not part of the method) ----------------------- */
 
 /* Phases of ofrl_train_step, in launch order. */

@@ -15,6 +15,13 @@ Functions (same names as the C entry points, without the ofrl_ prefix):
   budgeted_clip_saxpy(...)      budgeted per-source clip + SAXPY, norms
   adam_step(...)                Adam with the safety clip
   train_step(...)               the fused step composed of the above
+  DeltaRule(...)                ofrl_delta_create / _destroy / _poll_status
+  delta_forward(...)            gated delta rule over packed episodes
+  delta_backward(...)           its gradients
+  delta_step(...)               one token for each environment
+  TensorList(...)               ofrl_tensors_create / _destroy
+  global_norm(...)              2-norm over many tensors
+  global_norm_clip(...)         the norm, and every tensor clipped by it
 """
 import ctypes as C
 from dataclasses import dataclass, field
@@ -65,7 +72,7 @@ def _stream(stream=None):
     return C.c_void_p(s.cuda_stream)
 
 
-F32, I32 = torch.float32, torch.int32
+F32, I32, BF16 = torch.float32, torch.int32, torch.bfloat16
 
 
 @dataclass
@@ -495,6 +502,197 @@ class StepGraph:
             self.close()
         except Exception:
             pass
+
+
+# ---- sequence memory (gated delta rule) --------------------------------------------------------------------------
+
+DTYPE = {"fp32": _abi.DTYPE_F32, "bf16": _abi.DTYPE_BF16}
+_TORCH_DTYPE = {"fp32": F32, "bf16": BF16}
+
+
+class DeltaRule:
+    """Workspace of the gated delta rule for one head layout (ofrl_delta_create); the only allocation.
+
+    backward=False reserves no memory for delta_backward, which is then refused."""
+
+    def __init__(self, k_heads: int, v_heads: int, k_dim: int, v_dim: int, dtype: str = "bf16",
+                 max_tokens: int = 16384, max_episodes: int = 1024, backward: bool = True):
+        self._lib = _abi.load()
+        self.shape = _abi.DeltaShape(k_heads, v_heads, k_dim, v_dim, DTYPE[dtype])
+        self.k_heads, self.v_heads, self.k_dim, self.v_dim = k_heads, v_heads, k_dim, v_dim
+        self.dtype = _TORCH_DTYPE[dtype]
+        self.max_tokens, self.max_episodes, self.backward = max_tokens, max_episodes, bool(backward)
+        self.handle = None
+        h = C.c_void_p()
+        _abi.check("ofrl_delta_create", self._lib.ofrl_delta_create(
+            C.byref(self.shape), max_tokens, max_episodes, int(self.backward), C.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            _abi.check("ofrl_delta_destroy", self._lib.ofrl_delta_destroy(self.handle))
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def poll_status(self, stream=None):
+        words = (C.c_int32 * _abi.STAT_WORDS)()
+        _abi.check("ofrl_delta_poll_status", self._lib.ofrl_delta_poll_status(self.handle, _stream(stream), words))
+        return {"bad_index": words[_abi.STAT_BAD_INDEX]}
+
+    def workspace_bytes(self) -> int:
+        return int(self._lib.ofrl_delta_workspace_bytes(C.byref(self.shape), self.max_tokens, self.max_episodes,
+                                                        int(self.backward)))
+
+    def saved(self, tokens: int, episodes: int) -> torch.Tensor:
+        """A buffer for the states that delta_forward hands to delta_backward."""
+        n = int(self._lib.ofrl_delta_saved_bytes(C.byref(self.shape), tokens, episodes))
+        if n < 0:
+            raise ValueError(f"ofrl_delta_saved_bytes: invalid arguments (tokens={tokens}, episodes={episodes})")
+        return torch.empty(max(n, 1), device="cuda", dtype=torch.uint8)
+
+
+def _rows(t: torch.Tensor, dtype, tail, rows: int, name: str):
+    """Address and row stride (elements) of a CUDA tensor [rows, *tail] whose rows are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (rows, *tail):
+        raise ValueError(f"{name} must be {(rows, *tail)}, got {tuple(t.shape)}")
+    inner, want = 1, []
+    for n in reversed(tail):
+        want.insert(0, inner)
+        inner *= n
+    if rows and any(n > 1 and s != w for n, s, w in zip(tail, t.stride()[1:], want)):
+        raise ValueError(f"{name} must have dense rows (heads and channels contiguous within a token)")
+    return t.data_ptr(), t.stride(0) if rows > 1 else inner
+
+
+def _dense(t: Optional[torch.Tensor], dtype, shape, name: str):
+    p = _ptr(t, dtype, name)
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return p
+
+
+def _delta_tokens(ctx: DeltaRule, q, k, v, g, beta, scale):
+    n = int(q.shape[0])
+    qk, vv, hv = (ctx.k_heads, ctx.k_dim), (ctx.v_heads, ctx.v_dim), (ctx.v_heads,)
+    rows = [_rows(t, ctx.dtype, tail, n, name) for t, tail, name in
+            ((q, qk, "q"), (k, qk, "k"), (v, vv, "v"), (g, hv, "g"), (beta, hv, "beta"))]
+    return _abi.DeltaTokens(*[r[0] for r in rows], *[r[1] for r in rows], n,
+                            ctx.k_dim ** -0.5 if scale is None else scale), n
+
+
+def delta_forward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, out, scale=None, init_state=None, final_state=None,
+                  saved=None, stream=None):
+    """The gated delta rule over packed episodes: q, k [tokens, k_heads, k_dim], v and out [tokens, v_heads, v_dim],
+    g (log decay) and beta [tokens, v_heads] (out contiguous; the others may be slices with dense rows);
+    episode_ends int32 [episodes].  scale: of the outputs (k_dim ** -0.5).  init_state, final_state: float32
+    [episodes, v_heads, v_dim, k_dim].  saved: ctx.saved(tokens, episodes), filled for delta_backward."""
+    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ne = int(episode_ends.numel())
+    state = (ne, ctx.v_heads, ctx.v_dim, ctx.k_dim)
+    _saved_ok(ctx, saved, n, ne)
+    _abi.check("ofrl_delta_forward", ctx._lib.ofrl_delta_forward(
+        ctx.handle, C.byref(t), _ptr(episode_ends, I32, "episode_ends"), ne,
+        _dense(init_state, F32, state, "init_state"), _dense(out, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "out"),
+        _dense(final_state, F32, state, "final_state"), _ptr(saved, torch.uint8, "saved"), _stream(stream)))
+
+
+def _saved_ok(ctx: DeltaRule, saved, tokens: int, episodes: int):
+    if saved is None:
+        return
+    need = int(ctx._lib.ofrl_delta_saved_bytes(C.byref(ctx.shape), tokens, episodes))
+    if saved.numel() < need:
+        raise ValueError(f"saved has {saved.numel()} bytes, {need} are needed: use ctx.saved(tokens, episodes)")
+
+
+def delta_backward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, saved, dout, dq, dk, dv, dg, dbeta, scale=None,
+                   d_final=None, d_init=None, stream=None):
+    """Gradients of the delta_forward call that filled `saved`, with the same inputs: of out in dout (contiguous), of
+    final_state in d_final (None: zero); written to dq, dk, dv, dg, dbeta (slices with dense rows) and d_init."""
+    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ne = int(episode_ends.numel())
+    if saved is None:
+        raise TypeError("saved must be the buffer that delta_forward filled")
+    _saved_ok(ctx, saved, n, ne)
+    qk, vv, hv = (ctx.k_heads, ctx.k_dim), (ctx.v_heads, ctx.v_dim), (ctx.v_heads,)
+    state = (ne, ctx.v_heads, ctx.v_dim, ctx.k_dim)
+    rows = [_rows(x, ctx.dtype, tail, n, name) for x, tail, name in
+            ((dq, qk, "dq"), (dk, qk, "dk"), (dv, vv, "dv"), (dg, hv, "dg"), (dbeta, hv, "dbeta"))]
+    grads = _abi.DeltaGrads(*[r[0] for r in rows], *[r[1] for r in rows])
+    _abi.check("ofrl_delta_backward", ctx._lib.ofrl_delta_backward(
+        ctx.handle, C.byref(t), _ptr(episode_ends, I32, "episode_ends"), ne, _ptr(saved, torch.uint8, "saved"),
+        _dense(dout, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "dout"), _dense(d_final, F32, state, "d_final"),
+        C.byref(grads), _dense(d_init, F32, state, "d_init"), _stream(stream)))
+
+
+def delta_step(ctx: DeltaRule, q, k, v, g, beta, state, out, scale=None, new_state=None, slots=None, stream=None):
+    """One token for each environment: tensors as delta_forward's with tokens = environments; state float32 [slots,
+    v_heads, v_dim, k_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each
+    token (None: token i has state i)."""
+    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ns = int(state.shape[0])
+    shape = (ns, ctx.v_heads, ctx.v_dim, ctx.k_dim)
+    to = state if new_state is None else new_state
+    _abi.check("ofrl_delta_step", ctx._lib.ofrl_delta_step(
+        ctx.handle, C.byref(t), _dense(slots, I32, (n,), "slots"), ns, _dense(state, F32, shape, "state"),
+        _dense(to, F32, shape, "new_state"), _dense(out, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "out"),
+        _stream(stream)))
+
+
+# ---- gradients kept in many tensors --------------------------------------------------------------------------------
+
+
+class TensorList:
+    """A list of contiguous float32 or bfloat16 CUDA tensors (ofrl_tensors_create): what global_norm and
+    global_norm_clip read and write.  It holds the tensors; their memory must stay where it is."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self._lib = _abi.load()
+        self.handle = None
+        self.tensors = list(tensors)
+        n = len(self.tensors)
+        ptrs, sizes, dtypes = (C.c_void_p * max(n, 1))(), (C.c_int64 * max(n, 1))(), (C.c_int32 * max(n, 1))()
+        codes = {F32: _abi.DTYPE_F32, BF16: _abi.DTYPE_BF16}
+        for i, t in enumerate(self.tensors):
+            p = _ptr(t, None, "tensor")
+            if t.dtype not in codes:
+                raise TypeError(f"tensor {i} must be float32 or bfloat16, got {t.dtype}")
+            ptrs[i], sizes[i], dtypes[i] = p.value, t.numel(), codes[t.dtype]
+        h = C.c_void_p()
+        _abi.check("ofrl_tensors_create", self._lib.ofrl_tensors_create(ptrs, sizes, dtypes, n, C.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            _abi.check("ofrl_tensors_destroy", self._lib.ofrl_tensors_destroy(self.handle))
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def global_norm(tensors: TensorList, norm_out, stream=None):
+    """norm_out[0] = the 2-norm over all elements of all tensors (adam_step's grad_norm)."""
+    _abi.check("ofrl_global_norm", tensors._lib.ofrl_global_norm(
+        tensors.handle, _dense(norm_out, F32, (1,), "norm_out"), _stream(stream)))
+
+
+def global_norm_clip(tensors: TensorList, max_norm: float, norm_out, out: Optional[TensorList] = None, stream=None):
+    """global_norm, then every element times min(1, max_norm / norm), in place or into the tensors of `out`."""
+    _abi.check("ofrl_global_norm_clip", tensors._lib.ofrl_global_norm_clip(
+        tensors.handle, max_norm, _dense(norm_out, F32, (1,), "norm_out"), None if out is None else out.handle,
+        _stream(stream)))
 
 
 def train_step_kernels(ctx: Context, batch: Batch, rows: int, n_nets: int = 1) -> int:

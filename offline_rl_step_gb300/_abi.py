@@ -46,6 +46,26 @@ class Opt(C.Structure):
                 ("sanitize_sources", C.c_int32)]
 
 
+DTYPE_F32, DTYPE_BF16 = 0, 1
+
+
+class DeltaShape(C.Structure):
+    _fields_ = [("k_heads", C.c_int32), ("v_heads", C.c_int32), ("k_dim", C.c_int32), ("v_dim", C.c_int32),
+                ("dtype", C.c_int32)]
+
+
+class DeltaTokens(C.Structure):
+    _fields_ = [("q", vp), ("k", vp), ("v", vp), ("g", vp), ("beta", vp), ("q_stride", C.c_int64),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("g_stride", C.c_int64),
+                ("beta_stride", C.c_int64), ("tokens", C.c_int64), ("scale", C.c_float)]
+
+
+class DeltaGrads(C.Structure):
+    _fields_ = [("dq", vp), ("dk", vp), ("dv", vp), ("dg", vp), ("dbeta", vp), ("q_stride", C.c_int64),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("g_stride", C.c_int64),
+                ("beta_stride", C.c_int64)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "ofrl_create": (C.c_int32, [C.POINTER(VShape), C.c_int32, C.c_int32, C.POINTER(vp)]),
@@ -87,6 +107,20 @@ SIGNATURES = {
     "ofrl_selftest_umma": (C.c_int32, [vp, vp, vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
                                        C.c_int32, vp, vp]),
     "ofrl_selftest_barrier": (C.c_int32, [vp, C.c_uint64, C.c_int32]),
+    "ofrl_delta_create": (C.c_int32, [C.POINTER(DeltaShape), C.c_int64, C.c_int32, C.c_int32, C.POINTER(vp)]),
+    "ofrl_delta_destroy": (C.c_int32, [vp]),
+    "ofrl_delta_poll_status": (C.c_int32, [vp, vp, C.POINTER(C.c_int32)]),
+    "ofrl_delta_workspace_bytes": (C.c_int64, [C.POINTER(DeltaShape), C.c_int64, C.c_int32, C.c_int32]),
+    "ofrl_delta_saved_bytes": (C.c_int64, [C.POINTER(DeltaShape), C.c_int64, C.c_int32]),
+    "ofrl_delta_forward": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, vp, vp]),
+    "ofrl_delta_backward": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, C.POINTER(DeltaGrads),
+                                        vp, vp]),
+    "ofrl_delta_step": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, vp]),
+    "ofrl_tensors_create": (C.c_int32, [C.POINTER(vp), C.POINTER(C.c_int64), C.POINTER(C.c_int32), C.c_int32,
+                                        C.POINTER(vp)]),
+    "ofrl_tensors_destroy": (C.c_int32, [vp]),
+    "ofrl_global_norm": (C.c_int32, [vp, vp, vp]),
+    "ofrl_global_norm_clip": (C.c_int32, [vp, C.c_float, vp, vp, vp]),
     "ofrl_profile_begin": (C.c_int32, [vp, C.c_int32]),
     "ofrl_profile_end": (C.c_int32, [vp, C.POINTER(C.c_float), C.POINTER(C.c_int32)]),
 }
