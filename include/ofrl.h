@@ -520,8 +520,8 @@ typedef struct {
 typedef struct ofrl_delta ofrl_delta;
 
 /* Create the workspace for sequences of up to max_tokens tokens in up to
- * max_episodes episodes (only ofrl_delta_backward uses memory that grows with
- * them: backward = 0 reserves none of it and refuses that call).  The only
+ * max_episodes episodes (0 of each is enough for ofrl_delta_step alone;
+ * backward = 0 reserves less and refuses ofrl_delta_backward).  The only
  * allocating call; binds to the current device.  One ofrl_delta must not be
  * used by two calls that overlap on the GPU. */
 ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens, int32_t max_episodes,

@@ -14,8 +14,7 @@ struct ofrl_delta {
     void* base;          // the single cudaMalloc of the context
     int64_t bytes;
     int32_t* status;     // [OFRL_STAT_WORDS]
-    float* scratch;      // per-CTA work arrays
-    float* grad_acc;     // [max_tokens][2][k_heads * k_dim] gradients summed over a head group
+    uint8_t* scratch;    // what lies between the launches of one call
 };
 
 namespace ofrl {
@@ -59,8 +58,7 @@ struct SeqLaunch {
     const float* d_final;
     ofrl_delta_grads grads;
     float* d_init;
-    float* scratch;
-    float* grad_acc;
+    uint8_t* scratch;
     int32_t* status;
     int num_sms;
 };
@@ -81,7 +79,7 @@ cudaError_t launch_forward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_backward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_step(const StepLaunch& a, cudaStream_t st);
 int64_t saved_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episodes);
-int64_t scratch_bytes(const ofrl_delta_shape& s, int num_sms);
+int64_t scratch_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episodes, bool backward);
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x);

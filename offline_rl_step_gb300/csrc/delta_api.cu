@@ -33,16 +33,15 @@ bool counts_ok(int64_t tokens, int64_t episodes) {
 int64_t elem_size(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_F32 ? 4 : 2; }
 
 struct Layout {
-    int64_t off_status, off_scratch, off_acc, total;
+    int64_t off_status, off_scratch, total;
 };
 
-Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_episodes, bool backward, int num_sms) {
+Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_episodes, bool backward) {
     Layout L;
     int64_t o = 0;
     auto take = [&](int64_t bytes) { const int64_t at = o; o = round_up(o + bytes, 256); return at; };
     L.off_status = take((int64_t)OFRL_STAT_WORDS * 4);
-    L.off_scratch = take(scratch_bytes(s, num_sms));
-    L.off_acc = take(backward ? max_tokens * 2 * s.k_heads * s.k_dim * 4 : 0);
+    L.off_scratch = take(scratch_bytes(s, max_tokens, max_episodes, backward));
     L.total = o;
     return L;
 }
@@ -106,7 +105,6 @@ SeqLaunch base_launch(const ofrl_delta* ctx, const ofrl_delta_tokens* in, const 
     a.ends = ends;
     a.episodes = episodes;
     a.scratch = ctx->scratch;
-    a.grad_acc = ctx->grad_acc;
     a.status = ctx->status;
     a.num_sms = ctx->num_sms;
     return a;
@@ -120,9 +118,7 @@ int64_t ofrl_delta_workspace_bytes(const ofrl_delta_shape* shape, int64_t max_to
                                    int32_t backward) {
     if (check_shape(shape) != OFRL_OK || !counts_ok(max_tokens, max_episodes) || (backward != 0 && backward != 1))
         return -1;
-    int device = 0;
-    const int sms = sm_count(&device);
-    return layout_of(*shape, max_tokens, max_episodes, backward != 0, sms).total;
+    return layout_of(*shape, max_tokens, max_episodes, backward != 0).total;
 }
 
 int64_t ofrl_delta_saved_bytes(const ofrl_delta_shape* shape, int64_t tokens, int32_t num_episodes) {
@@ -145,7 +141,7 @@ ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens,
         delete ctx;
         return OFRL_ECUDA;
     }
-    const Layout L = layout_of(*shape, max_tokens, max_episodes, backward != 0, ctx->num_sms);
+    const Layout L = layout_of(*shape, max_tokens, max_episodes, backward != 0);
     ctx->shape = *shape;
     ctx->max_tokens = max_tokens;
     ctx->max_episodes = max_episodes;
@@ -158,8 +154,7 @@ ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens,
     }
     char* b = static_cast<char*>(ctx->base);
     ctx->status = reinterpret_cast<int32_t*>(b + L.off_status);
-    ctx->scratch = reinterpret_cast<float*>(b + L.off_scratch);
-    ctx->grad_acc = reinterpret_cast<float*>(b + L.off_acc);
+    ctx->scratch = reinterpret_cast<uint8_t*>(b + L.off_scratch);
     if (cudaMemset(ctx->status, 0, OFRL_STAT_WORDS * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(ctx->base);
         delete ctx;
