@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kChainThreads) delta_forward_kernel(const __gr
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) g[n][k][i] = f[n][k][i];
                         const int dvp = pad_dim(dv);
-                        store_image<kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, g, row0 / 8,
+                        store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, g, row0 / 8,
                                                     dvp / 8);
                         if (lane == 0) a.state_unit[at * 8 + row0 / 16] = s_inv;
                     }
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kChainThreads) delta_reverse_kernel(const __gr
                     uint32_t f[NM][KS][4];
                     to_frags<NM>(S, s_up, f);
                     gemm<KS, 8, NM, NT, false>(U, f, kimg, St::kKey, CG, 0);
-                    store_image<kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, f, row0 / 8,
+                    store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, f, row0 / 8,
                                                 dvp / 8);
                     if (lane == 0) a.state_unit[at * 8 + row0 / 16] = s_inv;
                 }

@@ -1,6 +1,6 @@
-// Gradients of q, k, log decay and write strength, chunk by chunk: everything
-// that contracts over the value channels (see delta_seq.cu for the formulas
-// and delta_mma.cuh for the scaled quantities).  One CTA of eight warps per
+// Gradients of q, k, log decay and write strength for fp32 tokens, chunk by
+// chunk: everything that contracts over the value channels (see delta_seq.cu
+// for the formulas and delta_mma.cuh for the scaled quantities).  One CTA of eight warps per
 // (chunk, key head), looping over the group's value heads, whose gradients it
 // adds up in registers; warp (rb, hf) has the token rows 16 rb .. and, of
 // each product's columns, half hf.
@@ -535,10 +535,9 @@ cudaError_t run(const GradArgs& g, int64_t grid, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t pick(const GradArgs& g, int64_t grid, cudaStream_t st) {
-    if (g.shape.k_dim > 64) return g.shape.v_dim > 64 ? run<T, 128, 128>(g, grid, st) : run<T, 128, 64>(g, grid, st);
-    return g.shape.v_dim > 64 ? run<T, 64, 128>(g, grid, st) : run<T, 64, 64>(g, grid, st);
+    if (g.shape.k_dim > 64) return g.shape.v_dim > 64 ? run<float, 128, 128>(g, grid, st) : run<float, 128, 64>(g, grid, st);
+    return g.shape.v_dim > 64 ? run<float, 64, 128>(g, grid, st) : run<float, 64, 64>(g, grid, st);
 }
 
 }  // namespace
@@ -564,7 +563,7 @@ cudaError_t launch_grad(const SeqLaunch& a, const Prepared& p, const Images& fwd
     g.status = a.status;
     const int64_t grid = slots_of(a.in.tokens, a.episodes) * a.shape.k_heads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return a.shape.dtype == OFRL_DTYPE_F32 ? pick<float>(g, grid, st) : pick<__nv_bfloat16>(g, grid, st);
+    return pick(g, grid, st);
 }
 
 }  // namespace delta

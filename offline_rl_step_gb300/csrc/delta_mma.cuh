@@ -202,9 +202,9 @@ struct Prepared {
 
 // Per (slot, value head): the state before a chunk [v_dim_pad][k_dim_pad] and
 // U^T (or R^T) [v_dim_pad][64] as images of token_planes() planes, and the
-// powers of two of their blocks of 16 rows (8 floats).  A state's image is cut
-// into slices of 32 columns, each contiguous.  Rows at and after v_dim
-// rounded up to 16 are never written.
+// powers of two of their blocks of 16 rows (8 floats).  A state's image of
+// two planes is cut into slices of 32 columns, each contiguous.  Rows at and
+// after v_dim rounded up to 16 are never written.
 constexpr int kSliceCols = 32;
 struct Images {
     uint8_t* state;
@@ -217,6 +217,7 @@ struct Images {
 cudaError_t launch_prep(const SeqLaunch& a, const Prepared& to, int planes, cudaStream_t st);
 cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Images& img, int planes, cudaStream_t st);
 cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st);
+cudaError_t launch_grad_tc(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
 cudaError_t launch_grad(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
 
 // Episode of a slot: the last e with start(e) / 64 + e <= slot, by a 32-ary

@@ -86,7 +86,8 @@ cudaError_t launch_backward(const SeqLaunch& a, cudaStream_t st) {
     const Prepared p = prepared_at(a.saved, z);
     const Images fwd = images_at(a.saved + prepared_bytes(z), z), rev = images_at(a.scratch, z);
     const cudaError_t e = launch_chain_reverse(a, p, rev, st);
-    return e == cudaSuccess ? launch_grad(a, p, fwd, rev, st) : e;
+    if (e != cudaSuccess) return e;
+    return a.shape.dtype == OFRL_DTYPE_F32 ? launch_grad(a, p, fwd, rev, st) : launch_grad_tc(a, p, fwd, rev, st);
 }
 
 }  // namespace delta
