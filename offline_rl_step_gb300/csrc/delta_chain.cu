@@ -12,8 +12,8 @@
 // (columns = tokens; gamma, rest, beta scale columns).  So a warp owns 16
 // value channels for the whole episode: S lives in its registers as mma
 // accumulators, whose layout is that of the next product's A operand, and
-// nothing passes between warps.  One more warp keeps a ring of stages filled
-// by bulk copies.  tcgen05 would run these products faster but needs each
+// nothing but a largest magnitude passes between warps.  Bulk copies keep a
+// ring of stages filled.  tcgen05 would run these products faster but needs each
 // intermediate through TMEM and a CTA-wide hand-over per product, four per
 // chunk, for 64-column tiles.
 
@@ -23,9 +23,7 @@ namespace ofrl {
 namespace delta {
 namespace {
 
-constexpr int kWarps = 4;                         // computing warps, 16 value channels each
-constexpr int kSlice = kWarps * 16;               // value channels per CTA
-constexpr int kChainThreads = (kWarps + 1) * 32;
+// NW: computing warps of a CTA, 16 value channels each.
 constexpr uint64_t kWaitNs = 1000000000ull;       // a wait gives up after 1 s
 
 struct ChainArgs {
@@ -43,41 +41,43 @@ struct ChainArgs {
     int64_t row_stride;
     uint8_t* state_img;      // per (slot, head): S (forward) or dS (backward) before the chunk is taken in, or null
     uint8_t* vec_img;        // per (slot, head): U (forward) or R (backward)
-    float* state_unit;       // [slot][head][8]: powers of two of their 16-row blocks
+    float* state_unit;       // [slot][head]: their powers of two
     float* vec_unit;
     int32_t* status;
 };
 
-template <typename T>
-__host__ __device__ constexpr int row_pitch() { return kSlice * (int)sizeof(T) + 16; }
-
-// One stage: K^ and Q^ planes, T^T / P / vectors (/ second planes), token rows.
-template <typename T, int DK, int NM>
+// One stage of the ring: K^ and Q^ planes, T^T / P / vectors (/ second planes).
+// Beside the ring each warp has two buffers of its token rows (64 tokens, 16
+// channels) and, for bf16, one to turn its outputs around.
+template <typename T, int DK, int NM, int NW>
 struct Stage {
     static constexpr int NT = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kKey = kChunk * DK * 2;
     static constexpr int kKeys = 2 * NT * kKey;
     static constexpr int kPairs = NM == 2 ? (int)kPairBytes : (int)kPairFirst;
-    static constexpr int kRows = kChunk * row_pitch<T>();
-    static constexpr int kBytes = (kKeys + kPairs + kRows + 127) / 128 * 128;
-    static constexpr int kOut = sizeof(T) == 2 ? kWarps * kChunk * 48 : 0;     // staging of bf16 outputs
+    static constexpr int kBytes = kKeys + kPairs;
+    static constexpr int kPitch = 16 * (int)sizeof(T) + 16;      // of a token's channels: no bank conflicts
+    static constexpr int kRows = kChunk * kPitch;
+    static constexpr int kWarp = (sizeof(T) == 2 ? 3 : 2) * kRows;
     // three stages where two CTAs then share an SM, else two where they fit
-    static constexpr int kCount = 3 * kBytes <= 100 * 1024 ? 3 : 2 * kBytes + kOut <= 226 * 1024 ? 2 : 1;
-    static constexpr int kShared = kCount * kBytes + kOut;
+    static constexpr int kCount = 3 * kBytes + NW * kWarp <= 111 * 1024   ? 3
+                                  : 2 * kBytes + NW * kWarp <= 226 * 1024 ? 2
+                                                                          : 1;
+    static constexpr int kShared = kCount * kBytes + NW * kWarp;
     static_assert(kShared <= 226 * 1024, "shared memory");
 };
 
 // Token rows of one chunk, transposed: x[t][z] = row value at (channel row4 +
 // (z >> 1) * 8 of the warp, token 8 t + col2 + (z & 1)).
-template <typename T>
-__device__ __forceinline__ void load_transposed(const uint8_t* rows, float (&x)[8][4], int warp) {
+template <typename T, int PITCH>
+__device__ __forceinline__ void load_transposed(const uint8_t* rows, float (&x)[8][4]) {
     const int lane = threadIdx.x & 31;
     if constexpr (sizeof(T) == 2) {
         const int m = lane >> 3, r = lane & 7;
 #pragma unroll
         for (int t = 0; t < 8; t += 2) {
             uint32_t f[4];   // matrices: (token group t + (m >> 1), channel half m & 1)
-            ldsm4t(f, umma::smem_u32(rows) + ((t + (m >> 1)) * 8 + r) * row_pitch<T>() + (warp * 2 + (m & 1)) * 16);
+            ldsm4t(f, umma::smem_u32(rows) + ((t + (m >> 1)) * 8 + r) * PITCH + (m & 1) * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 v = unpack_b(f[i]);
@@ -91,8 +91,8 @@ __device__ __forceinline__ void load_transposed(const uint8_t* rows, float (&x)[
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int z = 0; z < 4; ++z)
-                x[t][z] = *reinterpret_cast<const float*>(rows + (t * 8 + col2 + (z & 1)) * row_pitch<T>() +
-                                                          (warp * 16 + row4 + (z >> 1) * 8) * 4);
+                x[t][z] = *reinterpret_cast<const float*>(rows + (t * 8 + col2 + (z & 1)) * PITCH +
+                                                          (row4 + (z >> 1) * 8) * 4);
     }
 }
 
@@ -178,15 +178,15 @@ __device__ __forceinline__ void store_state(float* to, const float (&s)[NT][4], 
 }
 
 struct Work {
-    int e, head, khead, slice;
+    int e, head, khead, row0;      // row0: the CTA's first value channel
     Span sp;
     int chunks;
     int64_t slot0;
 };
-__device__ __forceinline__ Work work_of(const ChainArgs& a) {
+__device__ __forceinline__ Work work_of(const ChainArgs& a, int width) {
     Work w;
-    const int hv = a.shape.v_heads, slices = (a.shape.v_dim + kSlice - 1) / kSlice;
-    w.slice = blockIdx.x % slices;
+    const int hv = a.shape.v_heads, slices = (a.shape.v_dim + width - 1) / width;
+    w.row0 = blockIdx.x % slices * width;
     const int64_t item = blockIdx.x / slices;
     w.e = (int)(item / hv);
     w.head = (int)(item % hv);
@@ -197,362 +197,413 @@ __device__ __forceinline__ Work work_of(const ChainArgs& a) {
     return w;
 }
 
-// The copying warp: chunks in the order of the pass, one stage each.
-template <typename T, int DK, int NM, bool REVERSE>
-__device__ __forceinline__ void copy_chunks(const ChainArgs& a, const Work& w, uint8_t* ring, uint64_t* full,
-                                            uint64_t* empty, volatile int* dead) {
-    using St = Stage<T, DK, NM>;
-    const int lane = threadIdx.x & 31;
-    const int dv = a.shape.v_dim;
-    const int channels = min(kSlice, dv - w.slice * kSlice);
-    for (int n = 0; n < w.chunks; ++n) {
-        const int st = n % St::kCount;
-        const int c = REVERSE ? w.chunks - 1 - n : n;
-        bool ok = true;
-        if (n >= St::kCount) ok = umma::mbar_wait(&empty[st], (uint32_t)(n / St::kCount - 1) & 1u, kWaitNs);
-        if (__any_sync(0xffffffffu, !ok) || *dead) {      // wind down: wait, within limits, for copies in flight
-            *dead = 1;
-            for (int k = max(n - St::kCount, 0); k < n; ++k)
-                umma::mbar_wait(&full[k % St::kCount], (uint32_t)(k / St::kCount) & 1u, kWaitNs);
-            return;
-        }
-        const int rows = min(kChunk, w.sp.len - c * kChunk);
-        uint8_t* s = ring + st * St::kBytes;
-        const int64_t slot = w.slot0 + c;
-        const uint32_t row_bytes = (uint32_t)(channels * sizeof(T));
-        if (lane == 0) {
-            umma::mbar_expect_tx(&full[st], (uint32_t)(St::kKeys + St::kPairs) + (uint32_t)rows * row_bytes);
-            umma::bulk_g2s(s, a.keys + (slot * a.shape.k_heads + w.khead) * KeyImage::bytes(DK, St::NT), St::kKeys,
-                           &full[st]);
-            umma::bulk_g2s(s + St::kKeys, a.pairs + (slot * a.shape.v_heads + w.head) * kPairBytes, St::kPairs,
-                           &full[st]);
-        }
-        __syncwarp();
-        const T* from = static_cast<const T*>(a.rows) + ((int64_t)w.sp.start + c * kChunk) * a.row_stride +
-                        (int64_t)w.head * dv + w.slice * kSlice;
-        for (int r = lane; r < rows; r += 32)
-            umma::bulk_g2s(s + St::kKeys + St::kPairs + r * row_pitch<T>(), from + r * a.row_stride, row_bytes, &full[st]);
-    }
-}
+// Barriers of a CTA's ring, and what its computing warps exchange.
+struct Ring {
+    uint64_t full[3], empty[3];
+    int dead;             // a wait gave up
+    float most[2][8];     // per warp: largest magnitudes
+};
 
-// Wait of a computing warp for stage st; false: give up.
-__device__ __forceinline__ bool stage_ready(uint64_t* full, int st, int turn, volatile int* dead) {
-    const bool ok = umma::mbar_wait(&full[st], (uint32_t)turn & 1u, kWaitNs);
-    if (__any_sync(0xffffffffu, !ok)) *dead = 1;
-    return __all_sync(0xffffffffu, ok);
-}
-
-// NM: planes of S, X, U (and of T and P).  SAVE: S and U go to images for the
-// backward pass (NS planes).
-template <typename T, int DK, int NM, bool SAVE>
-__global__ void __launch_bounds__(kChainThreads) delta_forward_kernel(const __grid_constant__ ChainArgs a) {
-    using St = Stage<T, DK, NM>;
-    constexpr int NT = St::NT, CG = DK / 8, KS = DK / 16;
-    constexpr int NO = sizeof(T) == 4 ? 2 : 1;      // planes of the operands that only the outputs see
-    constexpr int NS = NT;                          // planes of the saved images
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[3], empty[3];
-    __shared__ int dead;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Work w = work_of(a);
+template <int NW>
+__device__ __forceinline__ void ring_init(Ring& r) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
-            umma::mbar_init(&full[i], 1);
-            umma::mbar_init(&empty[i], kWarps);
+            umma::mbar_init(&r.full[i], 1);
+            umma::mbar_init(&r.empty[i], NW);
         }
-        dead = 0;
+        r.dead = 0;
         umma::fence_mbar_init();
     }
     __syncthreads();
-    if (warp == kWarps) {
-        copy_chunks<T, DK, NM, false>(a, w, smem, full, empty, &dead);
-    } else {
+}
+
+// The first warp fills the ring: the copies of turn n of the pass, once every
+// warp is done with what its stage held.  (A warp for the copies alone would
+// leave three warps on one of the SM's four register files, and a third of
+// the registers of every warp unused.)
+template <typename St, int DK, bool REVERSE>
+__device__ __forceinline__ void copy_chunk(const ChainArgs& a, const Work& w, uint8_t* smem, Ring& r, int n) {
+    if (n >= w.chunks || *(volatile int*)&r.dead) return;
+    const int st = n % St::kCount;
+    const int c = REVERSE ? w.chunks - 1 - n : n;
+    bool ok = true;
+    if (n >= St::kCount) ok = umma::mbar_wait(&r.empty[st], (uint32_t)(n / St::kCount - 1) & 1u, kWaitNs);
+    if (__any_sync(0xffffffffu, !ok)) {      // what is in flight has been waited for, or its own wait gives up
+        r.dead = 1;
+        return;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        uint8_t* s = smem + st * St::kBytes;
+        const int64_t slot = w.slot0 + c;
+        umma::mbar_expect_tx(&r.full[st], (uint32_t)St::kBytes);
+        umma::bulk_g2s(s, a.keys + (slot * a.shape.k_heads + w.khead) * KeyImage::bytes(DK, St::NT), St::kKeys, &r.full[st]);
+        umma::bulk_g2s(s + St::kKeys, a.pairs + (slot * a.shape.v_heads + w.head) * kPairBytes, St::kPairs, &r.full[st]);
+    }
+    __syncwarp();
+}
+
+// A warp's own token rows of chunk c: asynchronous 16-byte copies, one group
+// per chunk whether or not there is anything to copy.
+template <typename St, typename T>
+__device__ __forceinline__ void copy_rows(const ChainArgs& a, const Work& w, uint8_t* to, int c, int row0) {
+    if (c >= 0 && c < w.chunks) {
+        const int lane = threadIdx.x & 31;
+        const int rows = min(kChunk, w.sp.len - c * kChunk);
+        constexpr int kVecs = sizeof(T);      // 16-byte pieces of 16 channels: 2 or 4
+        const int piece = lane % kVecs;
+        const bool on = row0 + piece * (16 / (int)sizeof(T)) < a.shape.v_dim;
+        const T* from = static_cast<const T*>(a.rows) + ((int64_t)w.sp.start + c * kChunk) * a.row_stride +
+                        (int64_t)w.head * a.shape.v_dim + row0 + piece * (16 / sizeof(T));
+        const uint32_t dst = umma::smem_u32(to) + piece * 16;
+#pragma unroll
+        for (int i = 0; i < kChunk * kVecs / 32; ++i) {
+            const int row = lane / kVecs + i * (32 / kVecs);
+            if (on && row < rows)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + row * St::kPitch),
+                             "l"(from + row * a.row_stride)
+                             : "memory");
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void rows_ready() {      // all but the newest group
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+}
+
+// Wait of a computing warp for a stage.  After a wait that gave up nothing
+// waits any more: the pass runs on over what shared memory holds (warps that
+// meet at a barrier all get there) and the CTA reports it.
+__device__ __forceinline__ void stage_ready(Ring& r, int st, int turn) {
+    if (*(volatile int*)&r.dead) return;
+    const bool ok = umma::mbar_wait(&r.full[st], (uint32_t)turn & 1u, kWaitNs);
+    if (__any_sync(0xffffffffu, !ok)) r.dead = 1;
+    __syncwarp();
+}
+
+// Largest of the computing warps' values (which: 0 and 1 in turn).
+template <int NW>
+__device__ __forceinline__ float across(Ring& r, int which, float v) {
+    if ((threadIdx.x & 31) == 0) r.most[which][threadIdx.x >> 5] = v;
+    asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+    float m = r.most[which][0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) m = fmaxf(m, r.most[which][i]);
+    return m;
+}
+
+// Zero what was never copied: tokens past the chunk's end, channels past v_dim.
+__device__ __forceinline__ void mask_rows(float (&x)[8][4], int rows, int channels) {
+    const int lane = threadIdx.x & 31, row4 = lane >> 2, col2 = (lane & 3) * 2;
+    if (rows == kChunk && channels >= 16) return;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            if (t * 8 + col2 + (z & 1) >= rows || row4 + (z >> 1) * 8 >= channels) x[t][z] = 0.0f;
+}
+
+template <int NA, int NB, int KA>
+__device__ __forceinline__ void first_planes(const uint32_t (&a)[NA][KA][4], uint32_t (&b)[NB][KA][4]) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < KA; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[n][k][i] = a[n][k][i];
+}
+
+// s[t] = keep s[t] + inv (f b [+ g h]) for the tiles of a state, four at a time.
+template <int DK, int NM, int NT, bool TWO>
+__device__ __forceinline__ void update_state(float (&s)[DK / 8][4], float keep, float inv, const uint32_t (&f)[NM][4][4],
+                                             uint32_t b, const uint32_t (&g)[NM][4][4], uint32_t h) {
+#pragma unroll
+    for (int t = 0; t < DK / 8; t += 4) {
+        float d[4][4];
+        zero(d);
+        gemm<4, 4, NM, NT, true>(d, f, b, kChunk * DK * 2, DK / 8, t);
+        if constexpr (TWO) gemm<4, 4, NM, NT, true>(d, g, h, kChunk * DK * 2, DK / 8, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) s[t + i][z] = keep * s[t + i][z] + inv * d[i][z];
+    }
+}
+
+template <int NW>
+constexpr int min_ctas() { return NW == 4 ? 2 : 1; }
+
+// NM: planes of S, X, U (and of T and P).  SAVE: S and U go to images for the
+// backward pass; the CTA then has every value channel, so that an image has
+// one power of two.
+template <typename T, int DK, int NM, int NW, bool SAVE>
+__global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(const __grid_constant__ ChainArgs a) {
+    using St = Stage<T, DK, NM, NW>;
+    constexpr int NT = St::NT, CG = DK / 8, KS = DK / 16;
+    constexpr int NO = NT;      // planes of the operands that only the outputs see, and of the saved images
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Ring ring;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Work w = work_of(a, NW * 16);
+    ring_init<NW>(ring);
+    uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
+    if (warp == 0)
+        for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n);
+    {
         const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
-        const int row0 = w.slice * kSlice + warp * 16;
-        const int row4 = lane >> 2, col2 = (lane & 3) * 2;
+        const int row0 = w.row0 + warp * 16;
         const int64_t states = ((int64_t)w.e * hv + w.head) * dv * dk;
         float S[DK / 8][4];
+        copy_rows<St, T>(a, w, mine, 0, row0);
         load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
         for (int c = 0; c < w.chunks; ++c) {
             const int st = c % St::kCount;
-            if (!stage_ready(full, st, c / St::kCount, &dead)) break;
+            copy_rows<St, T>(a, w, mine + ((c + 1) & 1) * St::kRows, c + 1, row0);
+            if (St::kCount == 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c);
+            stage_ready(ring, st, c / St::kCount);
+            if (!SAVE && row0 >= dv) {
+                if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
+                continue;
+            }
+            if (St::kCount > 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c + St::kCount - 1);
             const uint8_t* s = smem + st * St::kBytes;
             const uint32_t kimg = umma::smem_u32(s), qimg = kimg + NT * St::kKey, pair = kimg + St::kKeys;
             const float* vec = reinterpret_cast<const float*>(s + St::kKeys + 2 * kSquare);
             const int rows = min(kChunk, w.sp.len - c * kChunk);
-            if (row0 < dv) {
-                const int64_t at = (w.slot0 + c) * hv + w.head;
-                float X[8][4], O[8][4];
-                zero(X);
-                zero(O);
-                const float s_up = scale_up(tile_max(S)), s_inv = pow2_inv(s_up);
-                {
-                    uint32_t f[NM][KS][4];
-                    to_frags<NM>(S, s_up, f);
-                    gemm<KS, 8, NM, NT, false>(X, f, kimg, St::kKey, CG, 0);
-                    if constexpr (NO == NM) {
-                        gemm<KS, 8, NM, NT, false>(O, f, qimg, St::kKey, CG, 0);
-                    } else {
-                        uint32_t f0[1][KS][4];
-#pragma unroll
-                        for (int k = 0; k < KS; ++k)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) f0[0][k][i] = f[0][k][i];
-                        gemm<KS, 8, 1, NT, false>(O, f0, qimg, St::kKey, CG, 0);
-                    }
-                    if constexpr (SAVE) {
-                        uint32_t g[NS][KS][4];
-#pragma unroll
-                        for (int n = 0; n < NS; ++n)
-#pragma unroll
-                            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) g[n][k][i] = f[n][k][i];
-                        const int dvp = pad_dim(dv);
-                        store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, g, row0 / 8,
-                                                    dvp / 8);
-                        if (lane == 0) a.state_unit[at * 8 + row0 / 16] = s_inv;
-                    }
+            const int64_t at = (w.slot0 + c) * hv + w.head;
+            float X[8][4], O[8][4];
+            zero(X);
+            zero(O);
+            float s_max = tile_max(S);
+            if constexpr (SAVE) s_max = across<NW>(ring, 0, s_max);
+            const float s_up = scale_up(s_max), s_inv = pow2_inv(s_up);
+            {
+                uint32_t f[NM][KS][4];
+                to_frags<NM>(S, s_up, f);
+                gemm<KS, 8, NM, NT, false>(X, f, kimg, St::kKey, CG, 0);
+                uint32_t f0[NO][KS][4];
+                first_planes(f, f0);
+                gemm<KS, 8, NO, NT, false>(O, f0, qimg, St::kKey, CG, 0);
+                if constexpr (SAVE) {
+                    const int64_t plane = (int64_t)NW * 16 * DK * 2;
+                    store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NO * plane, plane, f0, row0 / 8, NW * 2);
+                    if (threadIdx.x == 0) a.state_unit[at] = s_inv;
                 }
-                {
-                    float V[8][4];
-                    load_transposed<T>(s + St::kKeys + St::kPairs, V, warp);
+            }
+            {
+                float V[8][4];
+                rows_ready();
+                load_transposed<T, St::kPitch>(mine + (c & 1) * St::kRows, V);
+                mask_rows(V, rows, dv - row0);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 8; ++t) {
+                    const float2 xv = vec2(vec, V_XV, t), xs = vec2(vec, V_XS, t);
+                    const float f[2] = {xv.x, xv.y}, g[2] = {xs.x * s_inv, xs.y * s_inv};
 #pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int i = t * 8 + col2 + z;
-                            const float gam = vec[V_GAM * kChunk + i] * s_inv, kinv = vec[V_KINV * kChunk + i];
-                            const float y = vec[V_BETA * kChunk + i] * vec[V_TINV * kChunk + i];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const bool on = i < rows && row0 + row4 + 8 * h < dv;   // else never copied
-                                X[t][2 * h + z] = on ? y * (V[t][2 * h + z] * kinv - gam * X[t][2 * h + z]) : 0.0f;
-                            }
-                        }
+                    for (int z = 0; z < 4; ++z) X[t][z] = f[z & 1] * V[t][z] - g[z & 1] * X[t][z];
                 }
-                float U[8][4];
+            }
+            float U[8][4];
+            zero(U);
+            const float x_up = scale_up(tile_max(X)), x_inv = pow2_inv(x_up);
+            {
+                uint32_t f[NM][4][4];
+                to_frags<NM>(X, x_up, f);
+                gemm<4, 8, NM, NM, true>(U, f, pair, (int)kPairFirst, 8, 0);
+            }
+            float u_max = tile_max(U) * x_inv * vec[V_MISC * kChunk];
+            if constexpr (SAVE) u_max = across<NW>(ring, 1, u_max);
+            const float u_up = scale_up(u_max), u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
+            // X now holds rest U, what the state takes in
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 r = vec2(vec, V_REST, t);
+                const float f[2] = {r.x * u_f, r.y * u_f};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) X[t][z] = U[t][z] * f[z & 1];
+            }
+            {
+                uint32_t f[NO][4][4];
+                to_frags<NO>(U, u_f, f);
+                if constexpr (SAVE) {
+                    const int64_t plane = (int64_t)NW * 16 * kChunk * 2;
+                    store_image<NT == 1 ? 1 : 8>(a.vec_img + at * NO * plane, plane, f, row0 / 8, NW * 2);
+                    if (threadIdx.x == 0) a.vec_unit[at] = u_inv;
+                }
                 zero(U);
-                {
-                    const float up = scale_up(tile_max(X)), inv = pow2_inv(up);
-                    uint32_t f[NM][4][4];
-                    to_frags<NM>(X, up, f);
-                    gemm<4, 8, NM, NM, true>(U, f, pair, (int)kPairFirst, 8, 0);
+                gemm<4, 8, NO, NO, false>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
+            }
+            const float p_inv = u_inv * (1.0f / kPScale);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < 8; ++t) {
+                const float2 os = vec2(vec, V_OS, t), qs = vec2(vec, V_QS, t);
+                const float f[2] = {os.x * s_inv, os.y * s_inv}, g[2] = {qs.x * p_inv, qs.y * p_inv};
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) U[t][z] *= inv;
-                }
-                // X now holds rest U, what the state takes in
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) X[t][z] = U[t][z] * vec[V_REST * kChunk + t * 8 + col2 + (z & 1)];
-                const float up = scale_up(fmaxf(tile_max(U), tile_max(X))), inv = pow2_inv(up);
-                {
-                    uint32_t f[NO][4][4];
-                    to_frags<NO>(U, up, f);
-                    zero(U);
-                    gemm<4, 8, NO, NO, false>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
-                    if constexpr (SAVE) {
-                        const int dvp = pad_dim(dv);
-                        store_image<8>(a.vec_img + at * NS * dvp * kChunk * 2, (int64_t)dvp * kChunk * 2, f, row0 / 8, dvp / 8);
-                        if (lane == 0) a.vec_unit[at * 8 + row0 / 16] = inv;
-                    }
-                }
-                const float p_inv = inv * (1.0f / kPScale);
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int i = t * 8 + col2 + (z & 1);
-                        O[t][z] = vec[V_QS * kChunk + i] * (vec[V_GAM * kChunk + i] * s_inv * O[t][z] + p_inv * U[t][z]);
-                    }
-                {
-                    uint32_t f[NM][4][4];
-                    to_frags<NM>(X, up, f);
-                    const float keep = vec[V_GAM * kChunk + kChunk - 1];
-#pragma unroll
-                    for (int t = 0; t < DK / 8; t += 4) {
-                        float d[4][4];
-                        zero(d);
-                        gemm<4, 4, NM, NT, true>(d, f, kimg, St::kKey, CG, t);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) S[t + i][z] = keep * S[t + i][z] + inv * d[i][z];
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(&empty[st]);
+                for (int z = 0; z < 4; ++z) O[t][z] = f[z & 1] * O[t][z] + g[z & 1] * U[t][z];
+            }
+            {
+                uint32_t f[NM][4][4];
+                to_frags<NM>(X, 1.0f, f);
+                update_state<DK, NM, NT, false>(S, vec[V_GAM * kChunk + kChunk - 1], u_inv, f, kimg, f, kimg);
+            }
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
+            if (row0 < dv)
                 store_transposed<T>(O, static_cast<T*>(a.out) + ((int64_t)w.sp.start + c * kChunk) * a.out_stride +
                                            (int64_t)w.head * dv + row0,
-                                    a.out_stride, rows, dv - row0, smem + St::kCount * St::kBytes + warp * kChunk * 48);
-            } else if (lane == 0) {
-                umma::mbar_arrive(&empty[st]);
-            }
+                                    a.out_stride, rows, dv - row0, mine + 2 * St::kRows);
         }
         if (a.last) store_state(a.last + states, S, row0, dv, dk);
     }
     __syncthreads();
-    if (threadIdx.x == 0 && dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
 }
 
-template <typename T, int DK, int NM>
-__global__ void __launch_bounds__(kChainThreads) delta_reverse_kernel(const __grid_constant__ ChainArgs a) {
-    using St = Stage<T, DK, NM>;
-    constexpr int NT = St::NT, CG = DK / 8, KS = DK / 16, NS = NT;
+template <typename T, int DK, int NW>
+__global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(const __grid_constant__ ChainArgs a) {
+    constexpr int NM = sizeof(T) == 4 ? 2 : 1;
+    using St = Stage<T, DK, NM, NW>;
+    constexpr int NT = St::NT, CG = DK / 8, KS = DK / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[3], empty[3];
-    __shared__ int dead;
+    __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Work w = work_of(a);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) {
-            umma::mbar_init(&full[i], 1);
-            umma::mbar_init(&empty[i], kWarps);
-        }
-        dead = 0;
-        umma::fence_mbar_init();
-    }
-    __syncthreads();
-    if (warp == kWarps) {
-        copy_chunks<T, DK, NM, true>(a, w, smem, full, empty, &dead);
-    } else {
+    const Work w = work_of(a, NW * 16);
+    ring_init<NW>(ring);
+    uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
+    if (warp == 0)
+        for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, true>(a, w, smem, ring, n);
+    {
         const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
-        const int row0 = w.slice * kSlice + warp * 16;
-        const int row4 = lane >> 2, col2 = (lane & 3) * 2;
-        const int dvp = pad_dim(dv);
+        const int row0 = warp * 16;
         const int64_t states = ((int64_t)w.e * hv + w.head) * dv * dk;
         float S[DK / 8][4];
+        copy_rows<St, T>(a, w, mine, w.chunks - 1, row0);
         load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
         for (int n = 0; n < w.chunks; ++n) {
             const int st = n % St::kCount, c = w.chunks - 1 - n;
-            if (!stage_ready(full, st, n / St::kCount, &dead)) break;
+            copy_rows<St, T>(a, w, mine + ((n + 1) & 1) * St::kRows, c - 1, row0);
+            if (St::kCount == 1 && warp == 0) copy_chunk<St, DK, true>(a, w, smem, ring, n);
+            stage_ready(ring, st, n / St::kCount);
             const uint8_t* s = smem + st * St::kBytes;
             const uint32_t kimg = umma::smem_u32(s), qimg = kimg + NT * St::kKey, pair = kimg + St::kKeys;
             const float* vec = reinterpret_cast<const float*>(s + St::kKeys + 2 * kSquare);
             const int rows = min(kChunk, w.sp.len - c * kChunk);
-            if (row0 < dv) {
-                const int64_t at = (w.slot0 + c) * hv + w.head;
-                float U[8][4];
-                zero(U);
-                const float s_up = scale_up(tile_max(S)), s_inv = pow2_inv(s_up);
-                {
-                    uint32_t f[NM][KS][4];
-                    to_frags<NM>(S, s_up, f);
-                    gemm<KS, 8, NM, NT, false>(U, f, kimg, St::kKey, CG, 0);
-                    store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NS * dvp * DK * 2, (int64_t)dvp * DK * 2, f, row0 / 8,
-                                                dvp / 8);
-                    if (lane == 0) a.state_unit[at * 8 + row0 / 16] = s_inv;
+            const int64_t at = (w.slot0 + c) * hv + w.head;
+            if (St::kCount > 1 && warp == 0) copy_chunk<St, DK, true>(a, w, smem, ring, n + St::kCount - 1);
+            float U[8][4];
+            zero(U);
+            const float s_up = scale_up(across<NW>(ring, 0, tile_max(S))), s_inv = pow2_inv(s_up);
+            {
+                uint32_t f[NM][KS][4];
+                to_frags<NM>(S, s_up, f);
+                gemm<KS, 8, NM, NT, false>(U, f, kimg, St::kKey, CG, 0);
+                const int64_t plane = (int64_t)NW * 16 * DK * 2;
+                store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NT * plane, plane, f, row0 / 8, NW * 2);
+                if (threadIdx.x == 0) a.state_unit[at] = s_inv;
+            }
+            float dO[8][4];       // dout scale kq
+            rows_ready();
+            load_transposed<T, St::kPitch>(mine + (n & 1) * St::kRows, dO);
+            mask_rows(dO, rows, dv - row0);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 qs = vec2(vec, V_QS, t);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) dO[t][z] *= z & 1 ? qs.y : qs.x;
+            }
+            {
+                const float up = scale_up(tile_max(dO)), inv = pow2_inv(up) * (1.0f / kPScale);
+                uint32_t f[NM][4][4];
+                to_frags<NM>(dO, up, f);
+                float d[8][4];
+                zero(d);
+                gemm<4, 8, NM, NM, true>(d, f, pair + kSquare, (int)kPairFirst, 8, 0);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const float2 r = vec2(vec, V_REST, t);
+                    const float f2[2] = {r.x * s_inv, r.y * s_inv};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) U[t][z] = f2[z & 1] * U[t][z] + inv * d[t][z];
                 }
-                float dO[8][4];       // dout scale kq
-                load_transposed<T>(s + St::kKeys + St::kPairs, dO, warp);
+            }
+            float R[8][4];
+            zero(R);
+            {
+                const float up = scale_up(tile_max(U)), inv = pow2_inv(up);
+                uint32_t f[NM][4][4];
+                to_frags<NM>(U, up, f);
+                gemm<4, 8, NM, NM, false>(R, f, pair, (int)kPairFirst, 8, 0);
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 8; ++t) {
+                    const float2 ti = vec2(vec, V_TINV, t);
+                    const float f2[2] = {ti.x * inv, ti.y * inv};
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int i = t * 8 + col2 + (z & 1);
-                        const bool on = i < rows && row0 + row4 + (z >> 1) * 8 < dv;
-                        dO[t][z] = on ? dO[t][z] * vec[V_QS * kChunk + i] : 0.0f;
-                        U[t][z] *= vec[V_REST * kChunk + i] * s_inv;
-                    }
-                {
-                    const float up = scale_up(tile_max(dO)), inv = pow2_inv(up) * (1.0f / kPScale);
-                    uint32_t f[NM][4][4];
-                    to_frags<NM>(dO, up, f);
-                    float d[8][4];
-                    zero(d);
-                    gemm<4, 8, NM, NM, true>(d, f, pair + kSquare, (int)kPairFirst, 8, 0);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) U[t][z] += inv * d[t][z];
+                    for (int z = 0; z < 4; ++z) R[t][z] *= f2[z & 1];
                 }
-                float R[8][4];
-                zero(R);
-                {
-                    const float up = scale_up(tile_max(U)), inv = pow2_inv(up);
-                    uint32_t f[NM][4][4];
-                    to_frags<NM>(U, up, f);
-                    gemm<4, 8, NM, NM, false>(R, f, pair, (int)kPairFirst, 8, 0);
+            }
+            {
+                const float up = scale_up(across<NW>(ring, 1, tile_max(R)));
+                uint32_t f[NT][4][4];
+                to_frags<NT>(R, up, f);
+                const int64_t plane = (int64_t)NW * 16 * kChunk * 2;
+                store_image<NT == 1 ? 1 : 8>(a.vec_img + at * NT * plane, plane, f, row0 / 8, NW * 2);
+                if (threadIdx.x == 0) a.vec_unit[at] = pow2_inv(up);
+            }
+            // dv in R; gamma dO and -gamma dv^ for the state
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < 8; ++t) {
+                const float2 g = vec2(vec, V_GAM, t), dvf = vec2(vec, V_DV, t), dsf = vec2(vec, V_DS, t);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) R[t][z] *= inv * vec[V_TINV * kChunk + t * 8 + col2 + (z & 1)];
+                for (int z = 0; z < 4; ++z) {
+                    dO[t][z] *= z & 1 ? g.y : g.x;
+                    U[t][z] = -R[t][z] * (z & 1 ? dsf.y : dsf.x);
+                    R[t][z] *= z & 1 ? dvf.y : dvf.x;
                 }
-                {
-                    const float up = scale_up(tile_max(R));
-                    uint32_t f[NS][4][4];
-                    to_frags<NS>(R, up, f);
-                    store_image<8>(a.vec_img + at * NS * dvp * kChunk * 2, (int64_t)dvp * kChunk * 2, f, row0 / 8, dvp / 8);
-                    if (lane == 0) a.vec_unit[at * 8 + row0 / 16] = pow2_inv(up);
-                }
-                // dv^ in R; gamma dO and gamma dv^ for the state
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int i = t * 8 + col2 + (z & 1);
-                        const float gam = vec[V_GAM * kChunk + i];
-                        R[t][z] *= vec[V_BETA * kChunk + i];
-                        dO[t][z] *= gam;
-                        U[t][z] = -gam * R[t][z];
-                        R[t][z] *= vec[V_KINV * kChunk + i];
-                    }
-                {
-                    const float up = scale_up(fmaxf(tile_max(dO), tile_max(U))), inv = pow2_inv(up);
-                    uint32_t f[NM][4][4], g[NM][4][4];
-                    to_frags<NM>(dO, up, f);
-                    to_frags<NM>(U, up, g);
-                    const float keep = vec[V_GAM * kChunk + kChunk - 1];
-#pragma unroll
-                    for (int t = 0; t < DK / 8; t += 4) {
-                        float d[4][4];
-                        zero(d);
-                        gemm<4, 4, NM, NT, true>(d, f, qimg, St::kKey, CG, t);
-                        gemm<4, 4, NM, NT, true>(d, g, kimg, St::kKey, CG, t);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) S[t + i][z] = keep * S[t + i][z] + inv * d[i][z];
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(&empty[st]);
+            }
+            {
+                const float up = scale_up(fmaxf(tile_max(dO), tile_max(U))), inv = pow2_inv(up);
+                uint32_t f[NM][4][4], g[NM][4][4];
+                to_frags<NM>(dO, up, f);
+                to_frags<NM>(U, up, g);
+                update_state<DK, NM, NT, true>(S, vec[V_GAM * kChunk + kChunk - 1], inv, f, qimg, g, kimg);
+            }
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
+            if (row0 < dv)
                 store_transposed<T>(R, static_cast<T*>(a.out) + ((int64_t)w.sp.start + c * kChunk) * a.out_stride +
                                            (int64_t)w.head * dv + row0,
-                                    a.out_stride, rows, dv - row0, smem + St::kCount * St::kBytes + warp * kChunk * 48);
-            } else if (lane == 0) {
-                umma::mbar_arrive(&empty[st]);
-            }
+                                    a.out_stride, rows, dv - row0, mine + 2 * St::kRows);
         }
         if (a.last) store_state(a.last + states, S, row0, dv, dk);
     }
     __syncthreads();
-    if (threadIdx.x == 0 && dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
 }
 
 template <typename K>
-cudaError_t go(K kernel, int smem, const ChainArgs& c, cudaStream_t st) {
-    const int slices = (c.shape.v_dim + kSlice - 1) / kSlice;
+cudaError_t go(K kernel, int nw, int smem, const ChainArgs& c, cudaStream_t st) {
+    const int slices = (c.shape.v_dim + nw * 16 - 1) / (nw * 16);
     const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * slices;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)grid, kChainThreads, smem, st>>>(c);
+    kernel<<<(unsigned)grid, nw * 32, smem, st>>>(c);
     return cudaGetLastError();
 }
 
 template <typename T, int DK, int NM>
 cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
-    return c.state_img ? go(delta_forward_kernel<T, DK, NM, true>, Stage<T, DK, NM>::kShared, c, st)
-                       : go(delta_forward_kernel<T, DK, NM, false>, Stage<T, DK, NM>::kShared, c, st);
+    if (!c.state_img) return go(delta_forward_kernel<T, DK, NM, 4, false>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
+    return c.shape.v_dim > 64
+               ? go(delta_forward_kernel<T, DK, NM, 8, true>, 8, Stage<T, DK, NM, 8>::kShared, c, st)
+               : go(delta_forward_kernel<T, DK, NM, 4, true>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
 }
-template <typename T, int DK, int NM>
+template <typename T, int DK>
 cudaError_t reverse(const ChainArgs& c, cudaStream_t st) {
-    return go(delta_reverse_kernel<T, DK, NM>, Stage<T, DK, NM>::kShared, c, st);
+    constexpr int NM = sizeof(T) == 4 ? 2 : 1;
+    return c.shape.v_dim > 64 ? go(delta_reverse_kernel<T, DK, 8>, 8, Stage<T, DK, NM, 8>::kShared, c, st)
+                              : go(delta_reverse_kernel<T, DK, 4>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
 }
 
 ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
@@ -596,8 +647,8 @@ cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Im
     c.rows = a.dout;
     c.row_stride = (int64_t)a.shape.v_heads * a.shape.v_dim;
     const bool wide = a.shape.k_dim > 64;
-    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? reverse<float, 128, 2>(c, st) : reverse<float, 64, 2>(c, st);
-    return wide ? reverse<__nv_bfloat16, 128, 1>(c, st) : reverse<__nv_bfloat16, 64, 1>(c, st);
+    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? reverse<float, 128>(c, st) : reverse<float, 64>(c, st);
+    return wide ? reverse<__nv_bfloat16, 128>(c, st) : reverse<__nv_bfloat16, 64>(c, st);
 }
 
 }  // namespace delta

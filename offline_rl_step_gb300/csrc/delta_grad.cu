@@ -43,37 +43,6 @@ __device__ __forceinline__ float pow2f(int e) {
 }
 // x 2^e for |e| <= 252.
 __device__ __forceinline__ float times_pow2(float x, int e) { return x * pow2f(e / 2) * pow2f(e - e / 2); }
-// 2^e as two halves, e <= 0 (zero below 2^-24).
-__device__ __forceinline__ uint32_t half_pow2(int e) {
-    const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
-    return h | h << 16;
-}
-__device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t f) {
-    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-// Two images' powers of two per block of 16 rows: the largest product's
-// exponent, and every block's distance below it.
-struct Units {
-    int top;
-    int below[8];
-};
-template <int KV>
-__device__ __forceinline__ Units units(const float* a, const float* b, int blocks) {
-    Units u;
-    u.top = -1000;
-#pragma unroll
-    for (int i = 0; i < KV; ++i)
-        if (i < blocks) {
-            u.below[i] = exponent(a[i]) + (b != nullptr ? exponent(b[i]) : 0);
-            u.top = max(u.top, u.below[i]);
-        }
-#pragma unroll
-    for (int i = 0; i < KV; ++i) u.below[i] -= u.top;
-    return u;
-}
-
 template <typename T, int DK, int DV>
 struct GradShared {
     static constexpr int NT = sizeof(T) == 4 ? 2 : 1;
@@ -190,10 +159,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
     uint32_t slice_turn = 0;     // slices taken so far, over all heads
     for (int g = 0; g < group; ++g) {
         const int head = khead * group + g;
-        const float* su = a.s_unit + (at0 + head) * 8;
-        const float* uu = a.u_unit + (at0 + head) * 8;
-        const float* du = a.d_unit + (at0 + head) * 8;
-        const float* ru = a.r_unit + (at0 + head) * 8;
+        const float su = a.s_unit[at0 + head], uu = a.u_unit[at0 + head], du = a.d_unit[at0 + head],
+                    ru = a.r_unit[at0 + head];
         ok &= umma::mbar_wait(&bar_head, (uint32_t)g & 1u, kWaitNs);
         const float *gam = vec + V_GAM * kChunk, *rest = vec + V_REST * kChunk, *beta = vec + V_BETA * kChunk;
         const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk;
@@ -234,7 +201,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
                             if (i < rows && c < dv) {
                                 const float2 r = unpack_h(f[z]);
                                 const T* p = pv + i * a.in.v_stride + c;
-                                rv[z & 1] += (r.x * to_f(p[0]) + r.y * to_f(p[1])) * ru[k];
+                                rv[z & 1] += (r.x * to_f(p[0]) + r.y * to_f(p[1])) * ru;
                             }
                         }
                     }
@@ -247,29 +214,20 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
         float n1[4][4], n2[4][4];
         zero(n1);
         zero(n2);
-        int n1_exp, n2_exp;
-        {
-            const Units wo = units<KV>(uu, nullptr, blocks), wr = units<KV>(uu, ru, blocks);
-            n1_exp = wo.top + o_exp;
-            n2_exp = wr.top;
+        const int n1_exp = exponent(uu) + o_exp, n2_exp = exponent(uu) + exponent(ru);
 #pragma unroll
-            for (int k = 0; k < KV; ++k) {
-                if (k >= blocks) continue;
-                uint32_t f1[NT][1][4], f2[NT][1][4];
-                const uint32_t p1 = half_pow2(wo.below[k]), p2 = half_pow2(wr.below[k]);
+        for (int k = 0; k < KV; ++k) {
+            if (k >= blocks) continue;
+            uint32_t f1[NT][1][4], f2[NT][1][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    ldsm4t(f2[n][0], radr + n * Sh::kVec + ((2 * k + (m8 >> 1)) * 8 + 2 * rb + (m8 & 1)) * kTile + r8 * 16);
+            for (int n = 0; n < NT; ++n) {
+                ldsm4t(f2[n][0], radr + n * Sh::kVec + ((2 * k + (m8 >> 1)) * 8 + 2 * rb + (m8 & 1)) * kTile + r8 * 16);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        f1[n][0][z] = mul_h2(fo[n][k][z], p1);
-                        f2[n][0][z] = mul_h2(f2[n][0][z], p2);
-                    }
-                }
-                const uint32_t b = uadr + 2 * k * 8 * kTile;
-                gemm<1, 4, NT, NT, true>(n1, f1, b, Sh::kVec, 8, 4 * hf);
-                gemm<1, 4, NT, NT, true>(n2, f2, b, Sh::kVec, 8, 4 * hf);
+                for (int z = 0; z < 4; ++z) f1[n][0][z] = fo[n][k][z];
             }
+            const uint32_t b = uadr + 2 * k * 8 * kTile;
+            gemm<1, 4, NT, NT, true>(n1, f1, b, Sh::kVec, 8, 4 * hf);
+            gemm<1, 4, NT, NT, true>(n2, f2, b, Sh::kVec, 8, 4 * hf);
         }
         // dPD in n1, M in n2; row and column sums of N; the beta sum
         float rn[2] = {0.0f, 0.0f}, rbeta[2] = {0.0f, 0.0f};
@@ -331,7 +289,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
             }
         __syncthreads();
 
-        const Units ws = units<KV>(su, nullptr, blocks), wk = units<KV>(su, ru, blocks), wc = units<KV>(du, uu, blocks);
+        const int q_exp = exponent(su) + o_exp, k_exp = exponent(su) + exponent(ru), c_exp = exponent(du) + exponent(uu);
         float dotq[2] = {0, 0}, dotk[2] = {0, 0}, dotc[2] = {0, 0}, ss = 0.0f;
 #pragma unroll
         for (int n = 0; n < SL; ++n) {
@@ -347,18 +305,13 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
             for (int k = 0; k < KV; ++k) {
                 if (k >= blocks) continue;
                 uint32_t f1[NT][1][4], f2[NT][1][4], f3[NT][1][4];
-                const uint32_t p1 = half_pow2(ws.below[k]), p2 = half_pow2(wk.below[k]), p3 = half_pow2(wc.below[k]);
 #pragma unroll
                 for (int p = 0; p < NT; ++p) {
                     const uint32_t at = p * Sh::kVec + ((2 * k + (m8 >> 1)) * 8 + 2 * rb + (m8 & 1)) * kTile + r8 * 16;
                     ldsm4t(f2[p][0], radr + at);
                     ldsm4t(f3[p][0], uadr + at);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        f1[p][0][z] = mul_h2(fo[p][k][z], p1);
-                        f2[p][0][z] = mul_h2(f2[p][0][z], p2);
-                        f3[p][0][z] = mul_h2(f3[p][0][z], p3);
-                    }
+                    for (int z = 0; z < 4; ++z) f1[p][0][z] = fo[p][k][z];
                 }
                 gemm<1, 2, NT, NT, true>(sq, f1, sadr + 2 * k * SG * kTile, Sh::kSl, SG, 2 * hf);
                 gemm<1, 2, NT, NT, true>(sk, f2, sadr + 2 * k * SG * kTile, Sh::kSl, SG, 2 * hf);
@@ -366,7 +319,6 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
             }
             // <S_0, dS_1>: two elements of one row per turn
             for (int x = threadIdx.x; x < blocks * 16 * kSliceCols / 2; x += kGradThreads) {
-                const int block = x / (16 * kSliceCols / 2);
                 float2 s = make_float2(0, 0), d = make_float2(0, 0);
 #pragma unroll
                 for (int p = 0; p < NT; ++p) {
@@ -378,7 +330,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
                     d.x += d1.x;
                     d.y += d1.y;
                 }
-                ss += (s.x * su[block]) * (d.x * du[block]) + (s.y * su[block]) * (d.y * du[block]);
+                ss += (s.x * su) * (d.x * du) + (s.y * su) * (d.y * du);
             }
             // products with the chunk's own keys and queries
             float a1[2][4], a2[2][4], a3[2][4];
@@ -430,9 +382,9 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const float kz = z ? kx.y : kx.x, qz = z ? qx.y : qx.x;
-                        const float q = times_pow2(sq[t][2 * h + z], ws.top + o_exp) * gam[i];
-                        const float k = times_pow2(sk[t][2 * h + z], wk.top) * -gam[i];     // without beta
-                        const float c = times_pow2(sc[t][2 * h + z], wc.top) * rest[i];
+                        const float q = times_pow2(sq[t][2 * h + z], q_exp) * gam[i];
+                        const float k = times_pow2(sk[t][2 * h + z], k_exp) * -gam[i];     // without beta
+                        const float c = times_pow2(sc[t][2 * h + z], c_exp) * rest[i];
                         dotq[h] += qz * q;
                         dotk[h] += kz * k;
                         dotc[h] += kz * c;

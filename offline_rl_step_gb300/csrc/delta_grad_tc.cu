@@ -2,8 +2,9 @@
 // (delta_grad.cu has the formulas and does the same for fp32 tokens, whose
 // two-plane operands do not fit beside each other in shared memory).
 //
-// One CTA of eight warps per (chunk, key head), looping over the group's
-// value heads.  Accumulator rows are tokens twice: rows 0 .. 63 belong to dq,
+// Persistent CTAs of eight warps take (chunk, key head) items in turn and loop
+// over the group's value heads; the next head's operands are copied in while
+// this one's results leave TMEM.  Accumulator rows are tokens twice: rows 0 .. 63 belong to dq,
 // rows 64 .. 127 to dk, so each of these is one 128-row product:
 //   N   = [dO; R] U^T                 (64 columns)
 //   ST  = [dO; R] S_0                 (DK columns)
@@ -40,48 +41,45 @@ struct GradTcArgs {
     const float *s_unit, *u_unit, *d_unit, *r_unit;
     const __nv_bfloat16* dout;
     ofrl_delta_grads grads;
+    int64_t items;
+    int num_sms;
     int32_t* status;
 };
 
 template <int DK, int DV>
 struct Lay {
     static constexpr int kKey = kChunk * DK * 2;        // one of K^, Q^
-    static constexpr int kVec = DV * kChunk * 2;        // one of U^T, R^T; half of an A image
+    static constexpr int kVec = DV * kChunk * 2;        // U^T, or R^T, or dO^T
     static constexpr int kState = DV * DK * 2;
     // [ . ; X] operands start 8 column groups before X: what lies there is
     // read, so X sits behind buffers at least that large
-    static constexpr int off_au = 0;                    // [dO; R] for N
-    static constexpr int off_as = off_au + 2 * kVec;    // [dO; R] for ST
-    static constexpr int off_uh = off_as + 2 * kVec;    // U for SC
-    static constexpr int off_u = off_uh + kVec;         // U^T as it came
+    static constexpr int off_a = 0;                     // [dO; R]: column groups of tokens, row groups of channels
+    static constexpr int off_u = off_a + 2 * kVec;      // U^T, likewise
     static constexpr int off_s = off_u + kVec;
     static constexpr int off_d = off_s + kState;
-    static constexpr int off_k = off_d + kState;        // K^, Q^
-    static constexpr int off_pem = off_k + 2 * kKey;    // PD, E, M: [8 column groups][24 row groups]
+    static constexpr int off_k = off_d + kState;        // K^, Q^ of two items
+    static constexpr int off_pem = off_k + 4 * kKey;    // PD, E, M: [8 column groups][24 row groups]
     static constexpr int kPem = 8 * 24 * kTile;
-    static constexpr int off_vec = off_pem + kPem;
-    static constexpr int off_sum = off_vec + kVecBytes;
-    static constexpr int kBytes = off_sum + (2 * 4 * kChunk + 64) * 4;
+    static constexpr int off_vec = off_pem + kPem;      // of two heads
+    static constexpr int off_sum = off_vec + 2 * kVecBytes;
+    static constexpr int kBytes = off_sum + (2 * 4 * kChunk + 2 * kChunk) * 4;
     static_assert(off_pem >= 8 * 24 * kTile, "rows before PD");
     // TMEM columns
     static constexpr int t_st = 0, t_in = DK, t_sc = 2 * DK, t_n = 3 * DK;
     static constexpr int kCols = 3 * DK + kChunk <= 256 ? 256 : 512;
+    static constexpr int kCtas = 2 * (kBytes + 2048) <= 227 * 1024 && kCols == 256 ? 2 : 1;
 };
 
 __device__ __forceinline__ int exponent(float pow2) { return (int)((__float_as_uint(pow2) >> 23) & 255u) - 127; }
 __device__ __forceinline__ float pow2f(int e) {
     return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
 }
-__device__ __forceinline__ uint32_t half_pow2(int e) {      // two halves 2^e, e <= 0
-    const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
-    return h | h << 16;
-}
-__device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t f) {
-    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-__device__ __forceinline__ uint4 mul_h8(uint4 x, uint32_t f) {
-    return make_uint4(mul_h2(x.x, f), mul_h2(x.y, f), mul_h2(x.z, f), mul_h2(x.w, f));
+// f 2^e, |e| <= 252.
+__device__ __forceinline__ float times_pow2(float f, int e) { return f * pow2f(e / 2) * pow2f(e - e / 2); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -108,30 +106,51 @@ __device__ __forceinline__ void mma_run(uint32_t d, uint32_t a, uint32_t a_lbo, 
                       idesc, (accumulate || k > 0) ? 1u : 0u);
 }
 
+struct Item {
+    int64_t slot, tok;
+    int khead, rows;      // rows 0: none left
+};
+
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, DK == 64 && DV == 64 ? 2 : 1)
-delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
+__global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
     using L = Lay<DK, DV>;
-    constexpr int CG = DK / 8, VB = DV / 16, VM = DV / 64, H = DK / 2;
+    constexpr int CG = DK / 8, VM = DV / 64, H = DK / 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar_keys, bar_head, bar_n, bar_s, bar_i, bar_c;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_at[3];
-    __shared__ float s_unit[4][8];          // powers of two of S_0, U, dS_1, R
-    __shared__ int s_oexp[8];               // of dO per 8 tokens
+    __shared__ Item s_next;
+    __shared__ int s_dead, s_oexp[8];       // exponents of dO per 8 tokens
+    __shared__ float s_part[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = a.shape.k_heads, hv = a.shape.v_heads, group = hv / hk, dk = a.shape.k_dim, dv = a.shape.v_dim;
-    const int64_t slot = blockIdx.x / hk;
-    const int khead = blockIdx.x % hk;
+    const int blocks = (dv + 15) / 16;
+    const uint32_t base = umma::smem_u32(smem);
+    uint8_t *ado = smem + L::off_a, *pem = smem + L::off_pem;
+    float* sums = reinterpret_cast<float*>(smem + L::off_sum);      // [2 halves][4][64]
+    float* red = sums + 2 * 4 * kChunk;                             // [2][64] R v
+    enum { R_Q, R_ST, R_IN, R_COL };
+
+    // the first item at or after n with tokens, by one whole warp
+    auto find = [&](int64_t n) {
+        Item it = {0, 0, 0, 0};
+        for (; n < a.items; n += gridDim.x) {
+            it.slot = n / hk;
+            it.khead = (int)(n % hk);
+            const int32_t tokens = (int32_t)a.in.tokens;
+            const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)it.slot);
+            const Span sp = span_of(a.ends, e, tokens);
+            const int c = (int)it.slot - (sp.start / kChunk + e);
+            it.rows = c < 0 ? 0 : min(sp.len - c * kChunk, kChunk);
+            it.tok = (int64_t)sp.start + c * kChunk;
+            if (it.rows > 0) break;
+            it.rows = 0;
+        }
+        if (lane == 0) s_next = it;
+    };
     if (warp == 0) {
-        const int32_t tokens = (int32_t)a.in.tokens;
-        const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)slot);
-        const Span sp = span_of(a.ends, e, tokens);
-        const int c = (int)slot - (sp.start / kChunk + e);
+        find(blockIdx.x);
         if (lane == 0) {
-            s_at[0] = sp.start + c * kChunk;
-            s_at[1] = c < 0 ? 0 : min(sp.len - c * kChunk, kChunk);
-            s_at[2] = 0;
+            s_dead = 0;
             umma::mbar_init(&bar_keys, 1);
             umma::mbar_init(&bar_head, 1);
             umma::mbar_init(&bar_n, 1);
@@ -142,260 +161,237 @@ delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
         }
     }
     __syncthreads();
-    const int rows = s_at[1];
-    if (rows <= 0) return;
-    const int64_t tok = s_at[0], at0 = slot * hv;
-    const int blocks = (dv + 15) / 16;
-    uint8_t *au = smem + L::off_au, *as = smem + L::off_as, *uh = smem + L::off_uh, *pem = smem + L::off_pem;
-    const uint8_t *kimg = smem + L::off_k, *qimg = kimg + L::kKey;
-    const uint32_t base = umma::smem_u32(smem);
-    float* vec = reinterpret_cast<float*>(smem + L::off_vec);
-    float* sums = reinterpret_cast<float*>(smem + L::off_sum);      // [2 halves][4][64]
-    float* red = sums + 2 * 4 * kChunk;                             // [64]
-    enum { R_Q, R_ST, R_IN, R_COL };
+    Item it = s_next;
+    if (it.rows <= 0) return;
+    if (warp == 1) umma::tmem_alloc(&s_tmem, L::kCols);
 
-    auto copy_head = [&](int head) {
-        umma::mbar_expect_tx(&bar_head, L::kVec + 2 * L::kState + kVecBytes);
-        umma::bulk_g2s(vec, a.pairs + (at0 + head) * kPairBytes + 2 * kSquare, kVecBytes, &bar_head);
-        umma::bulk_g2s(smem + L::off_u, a.u_img + (at0 + head) * L::kVec, L::kVec, &bar_head);
-        umma::bulk_g2s(smem + L::off_s, a.s_img + (at0 + head) * L::kState, L::kState, &bar_head);
-        umma::bulk_g2s(smem + L::off_d, a.d_img + (at0 + head) * L::kState, L::kState, &bar_head);
+    auto copy_keys = [&](const Item& x, int turn) {
+        umma::mbar_expect_tx(&bar_keys, 2 * L::kKey);
+        umma::bulk_g2s(smem + L::off_k + (turn & 1) * 2 * L::kKey, a.keys + (x.slot * hk + x.khead) * KeyImage::bytes(DK, 1),
+                       2 * L::kKey, &bar_keys);
+    };
+    auto copy_head = [&](const Item& x, int head, int turn) {
+        const int64_t at = x.slot * hv + head;
+        umma::mbar_expect_tx(&bar_head, 2 * L::kVec + 2 * L::kState + kVecBytes);
+        umma::bulk_g2s(smem + L::off_vec + (turn & 1) * kVecBytes, a.pairs + at * kPairBytes + 2 * kSquare, kVecBytes, &bar_head);
+        umma::bulk_g2s(smem + L::off_a + L::kVec, a.r_img + at * L::kVec, L::kVec, &bar_head);
+        umma::bulk_g2s(smem + L::off_u, a.u_img + at * L::kVec, L::kVec, &bar_head);
+        umma::bulk_g2s(smem + L::off_s, a.s_img + at * L::kState, L::kState, &bar_head);
+        umma::bulk_g2s(smem + L::off_d, a.d_img + at * L::kState, L::kState, &bar_head);
+    };
+    // what this thread converts: tokens 8 warp .. + 7, channels 2 lane, + 1 of every 64
+    uint32_t xo[VM][8], xv[VM][8];
+    float un[4];      // powers of two of S_0, U, dS_1, R
+    auto load_head = [&](const Item& x, int head) {
+        const __nv_bfloat16* po = a.dout + (x.tok * hv + head) * dv;
+        const __nv_bfloat16* pv = static_cast<const __nv_bfloat16*>(a.in.v) + x.tok * a.in.v_stride + (int64_t)head * dv;
+#pragma unroll
+        for (int m = 0; m < VM; ++m) {
+            const int ch = m * 64 + 2 * lane;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int j = warp * 8 + t;
+                const bool on = j < x.rows && ch < dv;
+                xo[m][t] = on ? *reinterpret_cast<const uint32_t*>(po + (int64_t)j * hv * dv + ch) : 0u;
+                xv[m][t] = on ? *reinterpret_cast<const uint32_t*>(pv + j * a.in.v_stride + ch) : 0u;
+            }
+        }
+        const int64_t at = x.slot * hv + head;
+        un[0] = a.s_unit[at];
+        un[1] = a.u_unit[at];
+        un[2] = a.d_unit[at];
+        un[3] = a.r_unit[at];
     };
     if (threadIdx.x == 0) {
-        umma::mbar_expect_tx(&bar_keys, 2 * L::kKey);
-        umma::bulk_g2s(smem + L::off_k, a.keys + (slot * hk + khead) * KeyImage::bytes(DK, 1), 2 * L::kKey, &bar_keys);
-        copy_head(khead * group);
+        copy_keys(it, 0);
+        copy_head(it, it.khead * group, 0);
     }
-    if (warp == 1) umma::tmem_alloc(&s_tmem, L::kCols);
-    bool ok = true;
+    load_head(it, it.khead * group);
 
-    auto wait_mma = [&](uint64_t* bar, int turn) {
+    const int row = (warp & 3) * 32 + lane;      // accumulator row
+    const int i = row & 63, half = warp >> 2;    // token, column half
+    const bool isk = row >= 64;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int turn) {
         ok &= umma::mbar_wait(bar, (uint32_t)turn & 1u, kWaitNs);
         __syncwarp();
         umma::fence_after_sync();
     };
-    const int row = (warp & 3) * 32 + lane;      // accumulator row
-    const int i = row & 63, half = warp >> 2;    // token, column half
-    const bool isk = row >= 64;
     float acc[H];
+    int turn = 0, g = 0;                         // heads taken; head of the group
+    int items = 0;
+    int64_t at_item = it.slot * hk + it.khead;
+    while (true) {
+        const int head = it.khead * group + g;
+        const bool last = g + 1 == group;
+        if (g == 0) {
 #pragma unroll
-    for (int c = 0; c < H; ++c) acc[c] = 0.0f;
-
-    for (int g = 0; g < group; ++g) {
-        const int head = khead * group + g;
-        // what this warp converts: tokens 8 warp .. + 7, channels 2 lane, + 1 of every 64
-        uint32_t xo[VM][8], xv[VM][8];
-        uint4 xr[VM][2];
-        {
-            const __nv_bfloat16* po = a.dout + (tok * hv + head) * dv;
-            const __nv_bfloat16* pv = static_cast<const __nv_bfloat16*>(a.in.v) + tok * a.in.v_stride + (int64_t)head * dv;
-            const uint8_t* pr = a.r_img + (at0 + head) * L::kVec;
-#pragma unroll
-            for (int m = 0; m < VM; ++m) {
-                const int ch = m * 64 + 2 * lane;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const int j = warp * 8 + t;
-                    const bool on = j < rows && ch < dv;
-                    xo[m][t] = on ? *reinterpret_cast<const uint32_t*>(po + (int64_t)j * hv * dv + ch) : 0u;
-                    xv[m][t] = on ? *reinterpret_cast<const uint32_t*>(pv + j * a.in.v_stride + ch) : 0u;
-                }
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-                    xr[m][z] = ch < blocks * 16
-                                   ? *reinterpret_cast<const uint4*>(pr + ((ch >> 3) * 8 + warp) * kTile + ((ch + z) & 7) * 16)
-                                   : make_uint4(0, 0, 0, 0);
-            }
+            for (int c = 0; c < H; ++c) acc[c] = 0.0f;
+            wait(&bar_keys, items);
         }
-        if (threadIdx.x < 32) {
-            const float* p = threadIdx.x < 8    ? a.s_unit
-                             : threadIdx.x < 16 ? a.u_unit
-                             : threadIdx.x < 24 ? a.d_unit
-                                                : a.r_unit;
-            const int b = threadIdx.x & 7;
-            s_unit[threadIdx.x >> 3][b] = b < blocks ? p[(at0 + head) * 8 + b] : 0.0f;
-        }
-        ok &= umma::mbar_wait(&bar_head, (uint32_t)g & 1u, kWaitNs);
-        __syncthreads();
+        wait(&bar_head, turn);
+        const float* vec = reinterpret_cast<const float*>(smem + L::off_vec + (turn & 1) * kVecBytes);
+        const uint8_t *kimg = smem + L::off_k + (items & 1) * 2 * L::kKey, *qimg = kimg + L::kKey;
         const float *gam = vec + V_GAM * kChunk, *rest = vec + V_REST * kChunk, *beta = vec + V_BETA * kChunk;
         const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk;
-        // exponents of the products' units: the largest, and below it per block
-        int top_o = -1000, top_os = -1000, top_r = -1000, top_rs = -1000, top_c = -1000;
-#pragma unroll
-        for (int b = 0; b < VB; ++b)
-            if (b < blocks) {
-                const int es = exponent(s_unit[0][b]), eu = exponent(s_unit[1][b]), ed = exponent(s_unit[2][b]),
-                          er = exponent(s_unit[3][b]);
-                top_o = max(top_o, eu);
-                top_os = max(top_os, es);
-                top_r = max(top_r, eu + er);
-                top_rs = max(top_rs, es + er);
-                top_c = max(top_c, ed + eu);
-            }
+        const int es = exponent(un[0]), eu = exponent(un[1]), ed = exponent(un[2]), er = exponent(un[3]);
+        const float s_d = un[0], d_d = un[2];
         {
-            float mx = 0.0f, qs[8];
+            float mx = 0.0f, qs[8], rv[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) qs[t] = vec[V_QS * kChunk + warp * 8 + t];
+            for (int t = 0; t < 8; ++t) {
+                qs[t] = vec[V_QS * kChunk + warp * 8 + t];
+                rv[t] = 0.0f;
+            }
 #pragma unroll
             for (int m = 0; m < VM; ++m)
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const float2 x = unpack_b(xo[m][t]);
-                    mx = fmaxf(mx, fmaxf(fabsf(x.x * qs[t]), fabsf(x.y * qs[t])));
+                    mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)) * fabsf(qs[t]));
                 }
             const float up = scale_up(warp_max(mx));
             if (lane == 0) s_oexp[warp] = -exponent(up);
-            float rv[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) rv[t] = 0.0f;
+            for (int t = 0; t < 8; ++t) qs[t] *= up;
 #pragma unroll
             for (int m = 0; m < VM; ++m) {
-                const int ch = m * 64 + 2 * lane, b = ch >> 4;
+                const int ch = m * 64 + 2 * lane;
                 if (ch >= blocks * 16) continue;
-                const int es = exponent(s_unit[0][b]), eu = exponent(s_unit[1][b]), ed = exponent(s_unit[2][b]),
-                          er = exponent(s_unit[3][b]);
-                const uint32_t fo = half_pow2(eu - top_o), fos = half_pow2(es - top_os), fr = half_pow2(eu + er - top_r),
-                               frs = half_pow2(es + er - top_rs), fc = half_pow2(ed + eu - top_c);
-                const float ru = s_unit[3][b];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     uint32_t h[4];
 #pragma unroll
                     for (int t = 0; t < 8; t += 2) {
                         const float2 x0 = unpack_b(xo[m][t]), x1 = unpack_b(xo[m][t + 1]);
-                        h[t / 2] = pack_h((z ? x0.y : x0.x) * (qs[t] * up), (z ? x1.y : x1.x) * (qs[t + 1] * up));
+                        h[t / 2] = pack_h((z ? x0.y : x0.x) * qs[t], (z ? x1.y : x1.x) * qs[t + 1]);
                     }
-                    const uint4 o = make_uint4(h[0], h[1], h[2], h[3]);
-                    const int rg = ch >> 3, r = (ch + z) & 7;
-                    const int at_o = (warp * (DV / 8) + rg) * kTile + r * 16, at_r = ((8 + warp) * (DV / 8) + rg) * kTile + r * 16;
-                    *reinterpret_cast<uint4*>(au + at_o) = mul_h8(o, fo);
-                    *reinterpret_cast<uint4*>(as + at_o) = mul_h8(o, fos);
-                    *reinterpret_cast<uint4*>(au + at_r) = mul_h8(xr[m][z], fr);
-                    *reinterpret_cast<uint4*>(as + at_r) = mul_h8(xr[m][z], frs);
-                    const uint4 u = *reinterpret_cast<const uint4*>(smem + L::off_u + (rg * 8 + warp) * kTile + r * 16);
-                    *reinterpret_cast<uint4*>(uh + at_o) = mul_h8(u, fc);
-                    const uint32_t w[4] = {xr[m][z].x, xr[m][z].y, xr[m][z].z, xr[m][z].w};
+                    uint8_t* to = ado + (warp * (DV / 8) + (ch >> 3)) * kTile + ((ch + z) & 7) * 16;
+                    *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                    const uint4 r = *reinterpret_cast<const uint4*>(to + L::kVec);
+                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
                         const float2 rr = unpack_h(w[t / 2]), v = unpack_b(xv[m][t]);
-                        rv[t] += (t & 1 ? rr.y : rr.x) * ru * (z ? v.y : v.x);
+                        rv[t] += (t & 1 ? rr.y : rr.x) * (z ? v.y : v.x);
                     }
                 }
             }
             // sums over the warp's lanes: lane l ends with token l & 7's
 #pragma unroll
             for (int o = 4, n = 4; n >= 1; o >>= 1, n >>= 1) {
-                const bool up2 = (lane & o) != 0;
+                const bool hi = (lane & o) != 0;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     if (t < n) {
-                        const float keep = up2 ? rv[t + n] : rv[t], give = up2 ? rv[t] : rv[t + n];
+                        const float keep = hi ? rv[t + n] : rv[t], give = hi ? rv[t] : rv[t + n];
                         rv[t] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                     }
             }
             rv[0] += __shfl_xor_sync(0xffffffffu, rv[0], 8);
             rv[0] += __shfl_xor_sync(0xffffffffu, rv[0], 16);
-            if (lane < 8) red[warp * 8 + lane] = rv[0];      // R v, v unscaled
+            if (lane < 8) red[(turn & 1) * kChunk + warp * 8 + lane] = rv[0] * un[3];      // R v, v unscaled
         }
         umma::fence_smem_to_async();
         umma::fence_before_sync();
         __syncthreads();
         umma::fence_after_sync();
         const uint32_t tmem = s_tmem;
+        constexpr uint32_t kA = (DV / 8) * kTile;       // bytes of a column group of tokens
         if (threadIdx.x == 0) {
-            if (g == 0) ok &= umma::mbar_wait(&bar_keys, 0, kWaitNs);
             const uint32_t id_n = umma::instr_desc(umma::kTypeF16, true, true, 128, kChunk);
             const uint32_t id_s = umma::instr_desc(umma::kTypeF16, true, true, 128, DK);
-            constexpr uint32_t kA = (DV / 8) * kTile;       // A images: column groups of tokens
-            mma_run(tmem + L::t_n, base + L::off_au, kTile, kA, 2 * kTile, base + L::off_u, 8 * kTile, kTile,
-                    2 * 8 * kTile, id_n, blocks, false);
+            mma_run(tmem + L::t_n, base + L::off_a, kTile, kA, 2 * kTile, base + L::off_u, kTile, kA, 2 * kTile, id_n,
+                    blocks, false);
             umma::commit(&bar_n);
-            mma_run(tmem + L::t_st, base + L::off_as, kTile, kA, 2 * kTile, base + L::off_s, CG * kTile, kTile,
+            mma_run(tmem + L::t_st, base + L::off_a, kTile, kA, 2 * kTile, base + L::off_s, CG * kTile, kTile,
                     2 * CG * kTile, id_s, blocks, false);
-            mma_run(tmem + L::t_sc, base + L::off_uh - 8 * kA, kTile, kA, 2 * kTile, base + L::off_d, CG * kTile, kTile,
+            mma_run(tmem + L::t_sc, base + L::off_u - 8 * kA, kTile, kA, 2 * kTile, base + L::off_d, CG * kTile, kTile,
                     2 * CG * kTile, id_s, blocks, false);
             umma::commit(&bar_s);
         }
+        if (warp == 1 && last) find(at_item + gridDim.x);
         // <S_0, dS_1> meanwhile: 8 elements of one row per turn
         float ss = 0.0f;
         for (int x = threadIdx.x; x < blocks * 2 * CG * 8; x += kThreads) {
-            const int b = x / (2 * CG * 8);
             const uint4 s = reinterpret_cast<const uint4*>(smem + L::off_s)[x], d = reinterpret_cast<const uint4*>(smem + L::off_d)[x];
             const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, dw[4] = {d.x, d.y, d.z, d.w};
-            float p = 0.0f;
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
                 const float2 f = unpack_h(sw[z]), h = unpack_h(dw[z]);
-                p += f.x * h.x + f.y * h.y;
+                ss += f.x * h.x + f.y * h.y;
             }
-            ss += p * s_unit[0][b] * s_unit[2][b];
         }
         ss = warp_sum(ss);
 
         // N -> PD, E, M
-        wait_mma(&bar_n, g);
+        wait(&bar_n, turn);
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         float n[32];
         tmem_ld32(lanes + L::t_n + half * 32, n);
         const int oexp = s_oexp[i >> 3];
-        {
-            const int e = isk ? top_r : top_o + oexp;
-            const float f1 = pow2f(e / 2), f2 = (isk ? -1.0f : 1.0f) * pow2f(e - e / 2);
-            const float gi = ghi[i], li = glo[i];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const int j = half * 32 + c;
-                const bool in = isk ? j < i : j <= i;
-                n[c] = in ? n[c] * f1 * f2 * exp2f((gi - ghi[j]) + (li - glo[j])) : 0.0f;
-            }
-        }
         const float bi = beta[i];
         float mx = 0.0f;
+        {
+            const float f = times_pow2(isk ? -1.0f : 1.0f, eu + (isk ? er : oexp));
+            const float gi = ghi[i], li = glo[i];
+            const int most = (isk ? i : i + 1) - half * 32;     // columns of this half that count
 #pragma unroll
-        for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fabsf(n[c]));
+            for (int c = 0; c < 32; c += 4) {
+                const float4 h4 = *reinterpret_cast<const float4*>(ghi + half * 32 + c);
+                const float4 l4 = *reinterpret_cast<const float4*>(glo + half * 32 + c);
+                const float gh[4] = {h4.x, h4.y, h4.z, h4.w}, gl[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    n[c + z] = c + z < most ? n[c + z] * f * ex2((gi - gh[z]) + (li - gl[z])) : 0.0f;
+                    mx = fmaxf(mx, fabsf(n[c + z]));
+                }
+            }
+        }
         {
             // warps of dk rows: E for IN, M = beta E for COL together with PD
             const float m1 = warp_max(isk ? fabsf(bi) * mx : mx), m2 = warp_max(mx);
             if (lane == 0) {
-                sums[warp * 3] = m1;
-                sums[warp * 3 + 1] = isk ? m2 : 0.0f;
-                sums[warp * 3 + 2] = ss;
+                sums[warp * 4] = m1;
+                sums[warp * 4 + 1] = isk ? m2 : 0.0f;
+                sums[warp * 4 + 2] = ss;
             }
         }
         __syncthreads();
         float m1 = 0.0f, m2 = 0.0f, sdot = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            m1 = fmaxf(m1, sums[w * 3]);
-            m2 = fmaxf(m2, sums[w * 3 + 1]);
-            sdot += sums[w * 3 + 2];
+            const float4 x = reinterpret_cast<const float4*>(sums)[w];
+            m1 = fmaxf(m1, x.x);
+            m2 = fmaxf(m2, x.y);
+            sdot += x.z;
         }
+        sdot = sdot * s_d * d_d;
         const float p_up = scale_up(m1), p_inv = pow2_inv(p_up), e_up = scale_up(m2), e_inv = pow2_inv(e_up);
+        constexpr uint32_t kP = 24 * kTile;
         {
-            const int rg = row >> 3, r = row & 7;
             const float s1 = isk ? e_up : p_up, s2 = bi * p_up;
+            uint8_t* to = pem + half * 4 * kP + (row >> 3) * kTile + (row & 7) * 16;
 #pragma unroll
             for (int c = 0; c < 32; c += 8) {
-                const int cg = half * 4 + c / 8;
-                uint4 v = make_uint4(pack_h(n[c] * s1, n[c + 1] * s1), pack_h(n[c + 2] * s1, n[c + 3] * s1),
-                                     pack_h(n[c + 4] * s1, n[c + 5] * s1), pack_h(n[c + 6] * s1, n[c + 7] * s1));
-                *reinterpret_cast<uint4*>(pem + (cg * 24 + rg) * kTile + r * 16) = v;
-                if (isk) {
-                    v = make_uint4(pack_h(n[c] * s2, n[c + 1] * s2), pack_h(n[c + 2] * s2, n[c + 3] * s2),
+                *reinterpret_cast<uint4*>(to + c / 8 * kP) =
+                    make_uint4(pack_h(n[c] * s1, n[c + 1] * s1), pack_h(n[c + 2] * s1, n[c + 3] * s1),
+                               pack_h(n[c + 4] * s1, n[c + 5] * s1), pack_h(n[c + 6] * s1, n[c + 7] * s1));
+                if (isk)
+                    *reinterpret_cast<uint4*>(to + c / 8 * kP + 8 * kTile) =
+                        make_uint4(pack_h(n[c] * s2, n[c + 1] * s2), pack_h(n[c + 2] * s2, n[c + 3] * s2),
                                    pack_h(n[c + 4] * s2, n[c + 5] * s2), pack_h(n[c + 6] * s2, n[c + 7] * s2));
-                    *reinterpret_cast<uint4*>(pem + (cg * 24 + 8 + rg) * kTile + r * 16) = v;
-                }
             }
         }
         umma::fence_smem_to_async();
         umma::fence_before_sync();
         __syncthreads();
         umma::fence_after_sync();
-        constexpr uint32_t kP = 24 * kTile;
+        const uint32_t kadr = umma::smem_u32(kimg);
         if (threadIdx.x == 0) {
             const uint32_t id = umma::instr_desc(umma::kTypeF16, false, true, 128, DK);
-            mma_run(tmem + L::t_in, base + L::off_pem, kP, kTile, 2 * kP, base + L::off_k, CG * kTile, kTile,
-                    2 * CG * kTile, id, 4, false);
+            mma_run(tmem + L::t_in, base + L::off_pem, kP, kTile, 2 * kP, kadr, CG * kTile, kTile, 2 * CG * kTile, id, 4,
+                    false);
             umma::commit(&bar_i);
         }
 
@@ -415,77 +411,68 @@ delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
             }
             return d;
         };
-        const float gi = gam[i];
+        const float gi = gam[i], bm = isk ? bi : 1.0f;
         float dst = 0.0f, din = 0.0f, dcol = 0.0f;
-        wait_mma(&bar_s, g);
+        wait(&bar_s, turn);
         {
-            const int e = isk ? top_rs : top_os + oexp;
-            const float f1 = pow2f(e / 2), f2 = (isk ? -gi : gi) * pow2f(e - e / 2), bm = isk ? bi : 1.0f;
-            const int ec = top_c;
-            const float c1 = pow2f(ec / 2), c2 = rest[i] * pow2f(ec - ec / 2);
+            const float f = times_pow2(isk ? -gi : gi, es + (isk ? er : oexp)), fb = f * bm;
 #pragma unroll
             for (int c0 = 0; c0 < H; c0 += 32) {
                 float v[32];
                 tmem_ld32(lanes + L::t_st + half * H + c0, v);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    v[c] = v[c] * f1 * f2;
-                    acc[c0 + c] += bm * v[c];
-                }
-                dst += dot_row(v, c0);
-                if (isk) {
-                    tmem_ld32(lanes + L::t_sc + half * H + c0, v);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        v[c] = v[c] * c1 * c2;
-                        acc[c0 + c] += v[c];
-                    }
-                    dcol += dot_row(v, c0);
-                }
+                for (int c = 0; c < 32; ++c) acc[c0 + c] += fb * v[c];
+                dst += f * dot_row(v, c0);
             }
         }
         umma::fence_before_sync();
         __syncthreads();
         umma::fence_after_sync();
+        // the products over channels are done: room for the next head's operands
+        const Item nx = last ? s_next : it;
+        const int nhead = nx.khead * group + (last ? 0 : g + 1);
         if (threadIdx.x == 0) {
             const uint32_t id = umma::instr_desc(umma::kTypeF16, true, true, 128, DK);
-            mma_run(tmem + L::t_st, base + L::off_pem - 8 * kP, kTile, kP, 2 * kTile, base + L::off_k + L::kKey,
-                    CG * kTile, kTile, 2 * CG * kTile, id, 4, false);
-            mma_run(tmem + L::t_st, base + L::off_pem + 16 * kTile - 8 * kP, kTile, kP, 2 * kTile, base + L::off_k,
-                    CG * kTile, kTile, 2 * CG * kTile, id, 4, true);
+            mma_run(tmem + L::t_st, base + L::off_pem - 8 * kP, kTile, kP, 2 * kTile, kadr + L::kKey, CG * kTile, kTile,
+                    2 * CG * kTile, id, 4, false);
+            mma_run(tmem + L::t_st, base + L::off_pem + 16 * kTile - 8 * kP, kTile, kP, 2 * kTile, kadr, CG * kTile, kTile,
+                    2 * CG * kTile, id, 4, true);
             umma::commit(&bar_c);
+            if (nx.rows > 0) {
+                copy_head(nx, nhead, turn + 1);
+                if (last) copy_keys(nx, items + 1);
+            }
         }
-        wait_mma(&bar_i, g);
+        if (nx.rows > 0) load_head(nx, nhead);
+        wait(&bar_i, turn);
         {
-            const float f = isk ? e_inv : p_inv, bm = isk ? bi : 1.0f;
+            const float f = isk ? e_inv : p_inv, fb = f * bm;
 #pragma unroll
             for (int c0 = 0; c0 < H; c0 += 32) {
                 float v[32];
                 tmem_ld32(lanes + L::t_in + half * H + c0, v);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    v[c] *= f;
-                    acc[c0 + c] += bm * v[c];
-                }
-                din += dot_row(v, c0);
+                for (int c = 0; c < 32; ++c) acc[c0 + c] += fb * v[c];
+                din += f * dot_row(v, c0);
             }
         }
-        wait_mma(&bar_c, g);
+        wait(&bar_c, turn);
         if (isk) {
+            const float f = times_pow2(rest[i], ed + eu);
 #pragma unroll
             for (int c0 = 0; c0 < H; c0 += 32) {
-                float v[32];
-                tmem_ld32(lanes + L::t_st + half * H + c0, v);
+                float v[32], w[32];
+                tmem_ld32(lanes + L::t_sc + half * H + c0, v);
+                tmem_ld32(lanes + L::t_st + half * H + c0, w);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    v[c] *= p_inv;
+                    v[c] = v[c] * f + w[c] * p_inv;
                     acc[c0 + c] += v[c];
                 }
                 dcol += dot_row(v, c0);
             }
         }
-        // [half][..][token]: q (dq), k (state part without beta), k (IN without beta), k (column part);
-        // dq rows keep the state part apart as well
+        // [half][..][token]: q (dq), k (state part without beta), k (IN without beta), k (column part)
         if (!isk) {
             sums[(half * 4 + R_Q) * kChunk + i] = dst + din;
         } else {
@@ -494,14 +481,14 @@ delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
             sums[(half * 4 + R_COL) * kChunk + i] = dcol;
         }
         // sum over tokens of the state parts' dots, times beta for k
-        const float sd = warp_sum(isk ? bi * dst : dst);
-        __shared__ float s_part[8];
+        const float sd = warp_sum(bm * dst);
         if (lane == 0) s_part[warp] = sd;
-        if (!ok) s_at[2] = 1;
+        if (!ok) s_dead = 1;
         umma::fence_before_sync();
         __syncthreads();
         umma::fence_after_sync();
-        if (warp == 0 && s_at[2] == 0) {
+        const bool dead = s_dead != 0;
+        if (warp == 0 && !dead) {
             float total = gam[kChunk - 1] * sdot;
 #pragma unroll
             for (int w = 0; w < 8; ++w) total += s_part[w];
@@ -512,9 +499,9 @@ delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
                 auto two = [&](int x) { return sums[x * kChunk + t] + sums[(4 + x) * kChunk + t]; };
                 const float k0 = two(R_ST) + two(R_IN), kinv = vec[V_KINV * kChunk + t], kap = pow2_inv(kinv);
                 dG[z] = two(R_Q) + beta[t] * k0 - two(R_COL);
-                if (t < rows)
-                    static_cast<__nv_bfloat16*>(a.grads.dbeta)[(tok + t) * a.grads.beta_stride + head] =
-                        __float2bfloat16_rn((red[t] * kinv + k0) * kap * kap);
+                if (t < it.rows)
+                    static_cast<__nv_bfloat16*>(a.grads.dbeta)[(it.tok + t) * a.grads.beta_stride + head] =
+                        __float2bfloat16_rn((red[(turn & 1) * kChunk + t] * kinv + k0) * kap * kap);
             }
             float run = dG[0] + dG[1];
 #pragma unroll
@@ -527,41 +514,55 @@ delta_grad_tc_kernel(const __grid_constant__ GradTcArgs a) {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int t = 2 * lane + z;
-                if (t < rows)
-                    static_cast<__nv_bfloat16*>(a.grads.dg)[(tok + t) * a.grads.g_stride + head] =
+                if (t < it.rows)
+                    static_cast<__nv_bfloat16*>(a.grads.dg)[(it.tok + t) * a.grads.g_stride + head] =
                         __float2bfloat16_rn(total - (z ? before + dG[0] : before));
             }
         }
-        if (g + 1 < group) {
-            __syncthreads();
-            if (threadIdx.x == 0) copy_head(head + 1);
+        if (last && !dead && i < it.rows) {
+            const float f = vec[(isk ? V_KINV : V_QINV) * kChunk + i];
+            __nv_bfloat16* to = isk ? static_cast<__nv_bfloat16*>(a.grads.dk) + (it.tok + i) * a.grads.k_stride
+                                    : static_cast<__nv_bfloat16*>(a.grads.dq) + (it.tok + i) * a.grads.q_stride;
+            to += (int64_t)it.khead * dk + half * H;
+#pragma unroll
+            for (int c = 0; c < H; c += 8)
+                if (half * H + c < dk)
+                    *reinterpret_cast<uint4*>(to + c) =
+                        make_uint4(pack_b(acc[c] * f, acc[c + 1] * f), pack_b(acc[c + 2] * f, acc[c + 3] * f),
+                                   pack_b(acc[c + 4] * f, acc[c + 5] * f), pack_b(acc[c + 6] * f, acc[c + 7] * f));
+        }
+        ++turn;
+        if (!last) {
+            ++g;
+        } else {
+            at_item = nx.slot * hk + nx.khead;
+            it = nx;
+            g = 0;
+            ++items;
+        }
+        if (nx.rows <= 0) break;
+        if (dead) {      // wind down: wait, within limits, for the copies in flight
+            umma::mbar_wait(&bar_head, (uint32_t)turn & 1u, kWaitNs);
+            if (last) umma::mbar_wait(&bar_keys, (uint32_t)items & 1u, kWaitNs);
+            break;
         }
     }
-    if (s_at[2] == 0 && i < rows) {
-        const float f = vec[(isk ? V_KINV : V_QINV) * kChunk + i];
-        __nv_bfloat16* to = isk ? static_cast<__nv_bfloat16*>(a.grads.dk) + (tok + i) * a.grads.k_stride
-                                : static_cast<__nv_bfloat16*>(a.grads.dq) + (tok + i) * a.grads.q_stride;
-        to += (int64_t)khead * dk + half * H;
-#pragma unroll
-        for (int c = 0; c < H; c += 8)
-            if (half * H + c < dk)
-                *reinterpret_cast<uint4*>(to + c) =
-                    make_uint4(pack_b(acc[c] * f, acc[c + 1] * f), pack_b(acc[c + 2] * f, acc[c + 3] * f),
-                               pack_b(acc[c + 4] * f, acc[c + 5] * f), pack_b(acc[c + 6] * f, acc[c + 7] * f));
-    }
     __syncthreads();
-    if (s_at[2] && threadIdx.x == 0) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    if (s_dead && threadIdx.x == 0) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
     if (warp == 1) umma::tmem_dealloc(s_tmem, L::kCols);
 }
 
 template <int DK, int DV>
-cudaError_t run(const GradTcArgs& g, int64_t grid, cudaStream_t st) {
+cudaError_t run(const GradTcArgs& g, cudaStream_t st) {
     constexpr int smem = Lay<DK, DV>::kBytes;
     static_assert(smem <= 226 * 1024, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(delta_grad_tc_kernel<DK, DV>);
     if (e != cudaSuccess) return e;
-    delta_grad_tc_kernel<DK, DV><<<(unsigned)grid, kThreads, smem, st>>>(g);
+    const int64_t most = (int64_t)g.num_sms * Lay<DK, DV>::kCtas;
+    const unsigned grid = (unsigned)(g.items < most ? g.items : most);
+    if (grid == 0) return cudaSuccess;
+    delta_grad_tc_kernel<DK, DV><<<grid, kThreads, smem, st>>>(g);
     return cudaGetLastError();
 }
 
@@ -586,10 +587,10 @@ cudaError_t launch_grad_tc(const SeqLaunch& a, const Prepared& p, const Images& 
     g.dout = static_cast<const __nv_bfloat16*>(a.dout);
     g.grads = a.grads;
     g.status = a.status;
-    const int64_t grid = slots_of(a.in.tokens, a.episodes) * a.shape.k_heads;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    if (a.shape.k_dim > 64) return a.shape.v_dim > 64 ? run<128, 128>(g, grid, st) : run<128, 64>(g, grid, st);
-    return a.shape.v_dim > 64 ? run<64, 128>(g, grid, st) : run<64, 64>(g, grid, st);
+    g.items = slots_of(a.in.tokens, a.episodes) * a.shape.k_heads;
+    g.num_sms = a.num_sms;
+    if (a.shape.k_dim > 64) return a.shape.v_dim > 64 ? run<128, 128>(g, st) : run<128, 64>(g, st);
+    return a.shape.v_dim > 64 ? run<64, 128>(g, st) : run<64, 64>(g, st);
 }
 
 }  // namespace delta

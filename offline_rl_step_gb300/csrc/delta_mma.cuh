@@ -104,6 +104,11 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// Columns 8 t + 2 (lane & 3), + 1 of vector `which`.
+__device__ __forceinline__ float2 vec2(const float* vec, int which, int t) {
+    return *reinterpret_cast<const float2*>(vec + which * kChunk + t * 8 + (threadIdx.x & 3) * 2);
+}
+
 // Accumulator tiles x[t] (16 rows x 8 columns each, NT of them side by side)
 // times s as A operands: N planes of NT/2 fragments.
 template <int N, int NT>
@@ -186,7 +191,24 @@ struct KeyImage {      // per (slot, key head): K^ planes, then Q^ planes
 // T^T rows j (16 of them share a power of two), columns i, of T = (1 + A)^-1;
 // P times kPScale, rows i, columns j.
 constexpr float kPScale = 32.0f;     // |q^ k^| < 4 * 128: P below 2^14
-enum Vec { V_GAM, V_REST, V_BETA, V_TINV, V_KINV, V_QS, V_QINV, V_GHI, V_GLO, V_COUNT };
+enum Vec {
+    V_GAM,      // gamma
+    V_REST,     // exp(G_last - G_j)
+    V_BETA,     // beta^
+    V_TINV,     // unit of T^T's row
+    V_QS,       // scale kq (0 past the chunk's end)
+    V_QINV,     // 1 / kq
+    V_KINV,     // 1 / kappa
+    V_GHI,      // G (log2) as a sum of two floats
+    V_GLO,
+    V_XV,       // beta^ tinv / kappa: of v in beta x, ready for T^T
+    V_XS,       // beta^ tinv gamma: of S k in it
+    V_OS,       // scale kq gamma
+    V_DV,       // beta^ / kappa
+    V_DS,       // beta^ gamma
+    V_MISC,     // [0]: the largest of rest and 1
+    V_COUNT
+};
 constexpr int kVecBytes = V_COUNT * kChunk * 4;
 constexpr int64_t kPairFirst = 2 * kSquare + kVecBytes;
 constexpr int64_t kPairBytes = 4 * kSquare + kVecBytes;
@@ -201,10 +223,11 @@ struct Prepared {
 };
 
 // Per (slot, value head): the state before a chunk [v_dim_pad][k_dim_pad] and
-// U^T (or R^T) [v_dim_pad][64] as images of token_planes() planes, and the
-// powers of two of their blocks of 16 rows (8 floats).  A state's image of
-// two planes is cut into slices of 32 columns, each contiguous.  Rows at and
-// after v_dim rounded up to 16 are never written.
+// U^T (or R^T) [v_dim_pad][64] as images of token_planes() planes, each with
+// one power of two (state_unit, vec_unit).  Images of two planes: the state's
+// cut into slices of 32 columns, each contiguous, U^T's with its blocks in row
+// order.  Images of one plane: the state's blocks in row order, U^T's column
+// group by column group.
 constexpr int kSliceCols = 32;
 struct Images {
     uint8_t* state;

@@ -210,19 +210,28 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
             }
             const double total = __shfl_sync(0xffffffffu, sum, 31);
             const double G[2] = {sum - g[1], sum};
+            float most = 1.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 const float hi = (float)G[i];
                 vec[V_GHI * kChunk + t] = hi;
                 vec[V_GLO * kChunk + t] = (float)(G[i] - (double)hi);
-                vec[V_GAM * kChunk + t] = exp2f(hi);
-                vec[V_REST * kChunk + t] = exp2f((float)(total - G[i]));
-                vec[V_BETA * kChunk + t] = b[i] * kap[t] * kap[t];
+                const float gam = exp2f(hi), rest = exp2f((float)(total - G[i]));
+                const float bk = b[i] * kap[t] * kap[t], qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
+                vec[V_GAM * kChunk + t] = gam;
+                vec[V_REST * kChunk + t] = rest;
+                vec[V_BETA * kChunk + t] = bk;
                 vec[V_KINV * kChunk + t] = pow2_inv(kap[t]);
                 vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
-                vec[V_QS * kChunk + t] = t < rows ? a.in.scale * kqv[t] : 0.0f;
+                vec[V_QS * kChunk + t] = qs;
+                vec[V_OS * kChunk + t] = qs * gam;
+                vec[V_DV * kChunk + t] = b[i] * kap[t];
+                vec[V_DS * kChunk + t] = bk * gam;
+                most = fmaxf(most, rest);
             }
+            most = warp_max(most);
+            if (lane == 0) vec[V_MISC * kChunk] = most;
         }
         __syncthreads();
         const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk, *beta = vec + V_BETA * kChunk;
@@ -372,7 +381,13 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
 #pragma unroll
         for (int r = 0; r < 4; ++r) mx = fmaxf(mx, tile_max(tb[r]));
         const float up = scale_up(mx);
-        if (lane < 16) vec[V_TINV * kChunk + warp * 16 + lane] = pow2_inv(up);
+        if (lane < 16) {
+            const int j = warp * 16 + lane;
+            const float inv = pow2_inv(up);
+            vec[V_TINV * kChunk + j] = inv;
+            vec[V_XV * kChunk + j] = vec[V_DV * kChunk + j] * inv;
+            vec[V_XS * kChunk + j] = vec[V_DS * kChunk + j] * inv;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll

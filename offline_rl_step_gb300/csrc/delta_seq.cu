@@ -43,7 +43,7 @@ Sizes sizes_of(const ofrl_delta_shape& s, int64_t slots) {
     z.pairs = round_up(slots * s.v_heads * kPairBytes, 256);
     z.state = round_up(slots * s.v_heads * planes * dv * dk * 2, 256);
     z.vec = round_up(slots * s.v_heads * planes * dv * kChunk * 2, 256);
-    z.units = round_up(slots * s.v_heads * 8 * 4, 256);
+    z.units = round_up(slots * s.v_heads * 4, 256);
     return z;
 }
 
