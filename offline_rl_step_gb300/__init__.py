@@ -24,6 +24,7 @@ Functions (same names as the C entry points, without the ofrl_ prefix):
   global_norm_clip(...)         the norm, and every tensor clipped by it
 """
 import ctypes as C
+import struct
 from dataclasses import dataclass, field
 from typing import List, Optional, Sequence
 
@@ -522,6 +523,8 @@ class DeltaRule:
         self.k_heads, self.v_heads, self.k_dim, self.v_dim = k_heads, v_heads, k_dim, v_dim
         self.dtype = _TORCH_DTYPE[dtype]
         self.max_tokens, self.max_episodes, self.backward = max_tokens, max_episodes, bool(backward)
+        self.shape_ref = C.byref(self.shape)
+        self.device = torch.cuda.current_device()
         self.handle = None
         h = C.c_void_p()
         _abi.check("ofrl_delta_create", self._lib.ofrl_delta_create(
@@ -556,37 +559,63 @@ class DeltaRule:
         return torch.empty(max(n, 1), device="cuda", dtype=torch.uint8)
 
 
-def _rows(t: torch.Tensor, dtype, tail, rows: int, name: str):
-    """Address and row stride (elements) of a CUDA tensor [rows, *tail] whose rows are dense."""
+def _rows(t: torch.Tensor, dtype, shape, name: str):
+    """Address and row stride (elements) of a CUDA tensor [tokens, ...] whose rows are dense."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, *tail):
-        raise ValueError(f"{name} must be {(rows, *tail)}, got {tuple(t.shape)}")
-    inner, want = 1, []
-    for n in reversed(tail):
-        want.insert(0, inner)
-        inner *= n
-    if rows and any(n > 1 and s != w for n, s, w in zip(tail, t.stride()[1:], want)):
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if len(shape) == 3:
+        d = shape[2]
+        dense = (st[2] == 1 or d == 1) and (st[1] == d or shape[1] == 1)
+        width = shape[1] * d
+    else:
+        dense = st[1] == 1 or shape[1] == 1
+        width = shape[1]
+    if not dense and shape[0]:
         raise ValueError(f"{name} must have dense rows (heads and channels contiguous within a token)")
-    return t.data_ptr(), t.stride(0) if rows > 1 else inner
+    return t.data_ptr(), st[0] if shape[0] > 1 else width
 
 
 def _dense(t: Optional[torch.Tensor], dtype, shape, name: str):
-    p = _ptr(t, dtype, name)
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return p
+    """Address of a contiguous CUDA tensor of this shape (0 for None)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _delta_tokens(ctx: DeltaRule, q, k, v, g, beta, scale):
-    n = int(q.shape[0])
-    qk, vv, hv = (ctx.k_heads, ctx.k_dim), (ctx.v_heads, ctx.v_dim), (ctx.v_heads,)
-    rows = [_rows(t, ctx.dtype, tail, n, name) for t, tail, name in
-            ((q, qk, "q"), (k, qk, "k"), (v, vv, "v"), (g, hv, "g"), (beta, hv, "beta"))]
-    return _abi.DeltaTokens(*[r[0] for r in rows], *[r[1] for r in rows], n,
-                            ctx.k_dim ** -0.5 if scale is None else scale), n
+    """The packed ofrl_delta_tokens, the token count and the three shapes."""
+    dt = ctx.dtype
+    n = len(q)
+    qk, vv, hv = (n, ctx.k_heads, ctx.k_dim), (n, ctx.v_heads, ctx.v_dim), (n, ctx.v_heads)
+    q, qs = _rows(q, dt, qk, "q")
+    k, ks = _rows(k, dt, qk, "k")
+    v, vs = _rows(v, dt, vv, "v")
+    g, gs = _rows(g, dt, hv, "g")
+    beta, bs = _rows(beta, dt, hv, "beta")
+    if scale is None:
+        scale = ctx.k_dim ** -0.5
+    return _pack_tokens(q, k, v, g, beta, qs, ks, vs, gs, bs, n, scale), n, qk, vv, hv
+
+
+_pack_tokens = struct.Struct(_abi.DELTA_TOKENS_FMT).pack
+_pack_grads = struct.Struct(_abi.DELTA_GRADS_FMT).pack
 
 
 def delta_forward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, out, scale=None, init_state=None, final_state=None,
@@ -595,56 +624,64 @@ def delta_forward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, out, scale=Non
     g (log decay) and beta [tokens, v_heads] (out contiguous; the others may be slices with dense rows);
     episode_ends int32 [episodes].  scale: of the outputs (k_dim ** -0.5).  init_state, final_state: float32
     [episodes, v_heads, v_dim, k_dim].  saved: ctx.saved(tokens, episodes), filled for delta_backward."""
-    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
-    ne = int(episode_ends.numel())
+    t, n, _, vv, _ = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ne = episode_ends.numel()
     state = (ne, ctx.v_heads, ctx.v_dim, ctx.k_dim)
-    _saved_ok(ctx, saved, n, ne)
-    _abi.check("ofrl_delta_forward", ctx._lib.ofrl_delta_forward(
-        ctx.handle, C.byref(t), _ptr(episode_ends, I32, "episode_ends"), ne,
-        _dense(init_state, F32, state, "init_state"), _dense(out, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "out"),
-        _dense(final_state, F32, state, "final_state"), _ptr(saved, torch.uint8, "saved"), _stream(stream)))
+    code = ctx._lib.ofrl_delta_forward(
+        ctx.handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne,
+        _dense(init_state, F32, state, "init_state"), _dense(out, ctx.dtype, vv, "out"),
+        _dense(final_state, F32, state, "final_state"), _saved_ptr(ctx, saved, n, ne), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_delta_forward", code)
 
 
-def _saved_ok(ctx: DeltaRule, saved, tokens: int, episodes: int):
+def _saved_ptr(ctx: DeltaRule, saved, tokens: int, episodes: int):
     if saved is None:
-        return
-    need = int(ctx._lib.ofrl_delta_saved_bytes(C.byref(ctx.shape), tokens, episodes))
+        return 0
+    need = ctx._lib.ofrl_delta_saved_bytes(ctx.shape_ref, tokens, episodes)
     if saved.numel() < need:
         raise ValueError(f"saved has {saved.numel()} bytes, {need} are needed: use ctx.saved(tokens, episodes)")
+    return _dense(saved, torch.uint8, saved.shape, "saved")
 
 
 def delta_backward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, saved, dout, dq, dk, dv, dg, dbeta, scale=None,
                    d_final=None, d_init=None, stream=None):
     """Gradients of the delta_forward call that filled `saved`, with the same inputs: of out in dout (contiguous), of
     final_state in d_final (None: zero); written to dq, dk, dv, dg, dbeta (slices with dense rows) and d_init."""
-    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
-    ne = int(episode_ends.numel())
+    t, n, qk, vv, hv = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ne = episode_ends.numel()
     if saved is None:
         raise TypeError("saved must be the buffer that delta_forward filled")
-    _saved_ok(ctx, saved, n, ne)
-    qk, vv, hv = (ctx.k_heads, ctx.k_dim), (ctx.v_heads, ctx.v_dim), (ctx.v_heads,)
+    dt = ctx.dtype
     state = (ne, ctx.v_heads, ctx.v_dim, ctx.k_dim)
-    rows = [_rows(x, ctx.dtype, tail, n, name) for x, tail, name in
-            ((dq, qk, "dq"), (dk, qk, "dk"), (dv, vv, "dv"), (dg, hv, "dg"), (dbeta, hv, "dbeta"))]
-    grads = _abi.DeltaGrads(*[r[0] for r in rows], *[r[1] for r in rows])
-    _abi.check("ofrl_delta_backward", ctx._lib.ofrl_delta_backward(
-        ctx.handle, C.byref(t), _ptr(episode_ends, I32, "episode_ends"), ne, _ptr(saved, torch.uint8, "saved"),
-        _dense(dout, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "dout"), _dense(d_final, F32, state, "d_final"),
-        C.byref(grads), _dense(d_init, F32, state, "d_init"), _stream(stream)))
+    dq, qs = _rows(dq, dt, qk, "dq")
+    dk, ks = _rows(dk, dt, qk, "dk")
+    dv, vs = _rows(dv, dt, vv, "dv")
+    dg, gs = _rows(dg, dt, hv, "dg")
+    dbeta, bs = _rows(dbeta, dt, hv, "dbeta")
+    code = ctx._lib.ofrl_delta_backward(
+        ctx.handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _saved_ptr(ctx, saved, n, ne),
+        _dense(dout, dt, vv, "dout"), _dense(d_final, F32, state, "d_final"),
+        _pack_grads(dq, dk, dv, dg, dbeta, qs, ks, vs, gs, bs), _dense(d_init, F32, state, "d_init"),
+        _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_delta_backward", code)
 
 
 def delta_step(ctx: DeltaRule, q, k, v, g, beta, state, out, scale=None, new_state=None, slots=None, stream=None):
     """One token for each environment: tensors as delta_forward's with tokens = environments; state float32 [slots,
     v_heads, v_dim, k_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each
     token (None: token i has state i)."""
-    t, n = _delta_tokens(ctx, q, k, v, g, beta, scale)
-    ns = int(state.shape[0])
+    t, n, _, vv, _ = _delta_tokens(ctx, q, k, v, g, beta, scale)
+    ns = len(state)
     shape = (ns, ctx.v_heads, ctx.v_dim, ctx.k_dim)
-    to = state if new_state is None else new_state
-    _abi.check("ofrl_delta_step", ctx._lib.ofrl_delta_step(
-        ctx.handle, C.byref(t), _dense(slots, I32, (n,), "slots"), ns, _dense(state, F32, shape, "state"),
-        _dense(to, F32, shape, "new_state"), _dense(out, ctx.dtype, (n, ctx.v_heads, ctx.v_dim), "out"),
-        _stream(stream)))
+    at = _dense(state, F32, shape, "state")
+    code = ctx._lib.ofrl_delta_step(
+        ctx.handle, t, 0 if slots is None else _dense(slots, I32, (n,), "slots"), ns, at,
+        at if new_state is None else _dense(new_state, F32, shape, "new_state"), _dense(out, ctx.dtype, vv, "out"),
+        _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_delta_step", code)
 
 
 # ---- gradients kept in many tensors --------------------------------------------------------------------------------
@@ -658,6 +695,7 @@ class TensorList:
         self._lib = _abi.load()
         self.handle = None
         self.tensors = list(tensors)
+        self.device = torch.cuda.current_device()
         n = len(self.tensors)
         ptrs, sizes, dtypes = (C.c_void_p * max(n, 1))(), (C.c_int64 * max(n, 1))(), (C.c_int32 * max(n, 1))()
         codes = {F32: _abi.DTYPE_F32, BF16: _abi.DTYPE_BF16}
@@ -684,15 +722,19 @@ class TensorList:
 
 def global_norm(tensors: TensorList, norm_out, stream=None):
     """norm_out[0] = the 2-norm over all elements of all tensors (adam_step's grad_norm)."""
-    _abi.check("ofrl_global_norm", tensors._lib.ofrl_global_norm(
-        tensors.handle, _dense(norm_out, F32, (1,), "norm_out"), _stream(stream)))
+    code = tensors._lib.ofrl_global_norm(tensors.handle, _dense(norm_out, F32, (1,), "norm_out"),
+                                         _raw_stream(stream, tensors.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_global_norm", code)
 
 
 def global_norm_clip(tensors: TensorList, max_norm: float, norm_out, out: Optional[TensorList] = None, stream=None):
     """global_norm, then every element times min(1, max_norm / norm), in place or into the tensors of `out`."""
-    _abi.check("ofrl_global_norm_clip", tensors._lib.ofrl_global_norm_clip(
+    code = tensors._lib.ofrl_global_norm_clip(
         tensors.handle, max_norm, _dense(norm_out, F32, (1,), "norm_out"), None if out is None else out.handle,
-        _stream(stream)))
+        _raw_stream(stream, tensors.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_global_norm_clip", code)
 
 
 def train_step_kernels(ctx: Context, batch: Batch, rows: int, n_nets: int = 1) -> int:

@@ -66,6 +66,11 @@ class DeltaGrads(C.Structure):
                 ("beta_stride", C.c_int64)]
 
 
+# struct formats of ofrl_delta_tokens and ofrl_delta_grads: packing one is several times cheaper than filling a
+# ctypes Structure, and a call on one token costs little else on the host
+DELTA_TOKENS_FMT = "5Q6qf4x"
+DELTA_GRADS_FMT = "5Q5q"
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "ofrl_create": (C.c_int32, [C.POINTER(VShape), C.c_int32, C.c_int32, C.POINTER(vp)]),
@@ -112,10 +117,10 @@ SIGNATURES = {
     "ofrl_delta_poll_status": (C.c_int32, [vp, vp, C.POINTER(C.c_int32)]),
     "ofrl_delta_workspace_bytes": (C.c_int64, [C.POINTER(DeltaShape), C.c_int64, C.c_int32, C.c_int32]),
     "ofrl_delta_saved_bytes": (C.c_int64, [C.POINTER(DeltaShape), C.c_int64, C.c_int32]),
-    "ofrl_delta_forward": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, vp, vp]),
-    "ofrl_delta_backward": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, C.POINTER(DeltaGrads),
-                                        vp, vp]),
-    "ofrl_delta_step": (C.c_int32, [vp, C.POINTER(DeltaTokens), vp, C.c_int32, vp, vp, vp, vp]),
+    # token and gradient structs are passed as packed bytes (see DELTA_TOKENS_FMT)
+    "ofrl_delta_forward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, vp, vp]),
+    "ofrl_delta_backward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, C.c_char_p, vp, vp]),
+    "ofrl_delta_step": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, vp]),
     "ofrl_tensors_create": (C.c_int32, [C.POINTER(vp), C.POINTER(C.c_int64), C.POINTER(C.c_int32), C.c_int32,
                                         C.POINTER(vp)]),
     "ofrl_tensors_destroy": (C.c_int32, [vp]),

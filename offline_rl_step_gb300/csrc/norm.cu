@@ -1,11 +1,17 @@
 // The 2-norm over many tensors, and clipping by it.
 //
 // The list is cut on the host into segments of at most kSegment elements of
-// one tensor; CTA b takes segments b, b + grid, ...  Squares are fp32; a
-// thread adds those of one segment into a plain fp32 sum of at most
-// kSegment / kThreads terms and carries the sums as an unevaluated pair
-// (two-sum), so the error does not grow with the number of segments.  The
-// order of every addition is fixed by the list alone.
+// one tensor; a warp takes every W-th segment, W the launch's warps.  Squares
+// are fp32; a lane adds those of one segment into a plain fp32 sum of at most
+// kSegment / 32 terms and carries the sums as an unevaluated pair (two-sum),
+// so the error does not grow with the number of segments.  The order of every
+// addition is fixed by the list alone.
+//
+// The factor needs every element, so each is read twice.  A list of up to
+// kClusterElems elements is one launch of a cluster of eight CTAs, whose sums
+// meet in distributed shared memory; a longer one is a launch for the norm
+// (its last CTA adds up) and one that scales, from the end of the list, whose
+// segments L2 still holds.  Bound by HBM for long lists, by latency for short.
 
 #include <cmath>
 #include <cstring>
@@ -17,9 +23,12 @@ namespace ofrl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSegment = 8192;
+constexpr int kSegment = 2048;
 constexpr int kMaxList = 1 << 20;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 6;
+constexpr int kCluster = 8;
+constexpr int kClusterThreads = 512;
+constexpr int64_t kClusterElems = 1 << 18;
 
 struct Segment {
     uint64_t ptr;
@@ -29,12 +38,12 @@ struct Segment {
 
 struct NormState {
     unsigned int ticket;    // CTAs done; the last one resets it
-    float norm, scale;
+    float scale;
 };
 
 struct NormLaunch {
     const Segment* seg;
-    const Segment* out;     // clip: same shape as seg
+    const Segment* out;     // clip: same shape as seg; null: the norm alone
     int64_t n_seg;
     double* partial;        // [grid]
     NormState* state;
@@ -49,37 +58,160 @@ __device__ __forceinline__ void pair_add(float& s, float& c, float x) {
     s = t;
 }
 
+// Sum over the block's warps of a value per lane; every thread gets it.
+template <int WARPS>
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double warp_part[kThreads / 32];
+    __shared__ double warp_part[WARPS];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
     if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = v;
     __syncthreads();
     double r = 0.0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) r += warp_part[i];
-    __syncthreads();
+    for (int i = 0; i < WARPS; ++i) r += warp_part[i];
     return r;
 }
 
-__device__ __forceinline__ float load_elem(uint64_t p, int32_t dtype, int i) {
-    return dtype == OFRL_DTYPE_F32 ? reinterpret_cast<const float*>(p)[i]
-                                   : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+// Elements before the first 16-byte boundary, at most n.
+template <typename T>
+__device__ __forceinline__ int head_of(uint64_t p, int n) {
+    const int h = (int)((16 - (p & 15)) & 15) / (int)sizeof(T);
+    return h < n ? h : n;
+}
+__device__ __forceinline__ float2 halves(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ float squares(uint64_t ptr, int count) {
+    const int lane = threadIdx.x & 31;
+    const T* p = reinterpret_cast<const T*>(ptr);
+    const int head = head_of<T>(ptr, count);
+    constexpr int kVec = 16 / sizeof(T);
+    const int vecs = (count - head) / kVec, rest = head + vecs * kVec;
+    const uint4* v = reinterpret_cast<const uint4*>(p + head);
+    float x = 0.0f;
+    auto add = [&](const uint4& u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                const float e = __uint_as_float(w[i]);
+                x = fmaf(e, e, x);
+            } else {
+                const float2 e = halves(w[i]);
+                x = fmaf(e.x, e.x, x);
+                x = fmaf(e.y, e.y, x);
+            }
+        }
+    };
+    constexpr int kAtOnce = 8;
+    int i = lane;
+    for (; i + 32 * (kAtOnce - 1) < vecs; i += 32 * kAtOnce) {
+        uint4 u[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) u[k] = v[i + 32 * k];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) add(u[k]);
+    }
+    for (; i < vecs; i += 32) add(v[i]);
+    // fewer than kVec elements before and after the vectors
+    const int at = lane < head ? lane : rest + lane - head;
+    if (lane < head || at < count) {
+        const float e = value(p[at]);
+        x = fmaf(e, e, x);
+    }
+    return x;
+}
+
+// Squares of this warp's segments.
+__device__ __forceinline__ double norm_part(const NormLaunch& a, int64_t warp, int64_t warps) {
+    float s = 0.0f, c = 0.0f;
+    Segment g = {0, 0, 0}, next = {0, 0, 0};
+    if (warp < a.n_seg) next = a.seg[warp];
+    for (int64_t k = warp; k < a.n_seg; k += warps) {
+        g = next;
+        if (k + warps < a.n_seg) next = a.seg[k + warps];
+        pair_add(s, c, g.dtype == OFRL_DTYPE_F32 ? squares<float>(g.ptr, g.count) : squares<__nv_bfloat16>(g.ptr, g.count));
+    }
+    // once s is infinite or NaN, the remainder c is NaN and says nothing
+    return isfinite(s) ? (double)s + (double)c : (double)s;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_segment(uint64_t from, uint64_t to, int count, float f) {
+    const int lane = threadIdx.x & 31;
+    const T* p = reinterpret_cast<const T*>(from);
+    T* q = reinterpret_cast<T*>(to);
+    auto one = [&](int i) {
+        if constexpr (sizeof(T) == 4)
+            q[i] = p[i] * f;
+        else
+            q[i] = __float2bfloat16_rn(value(p[i]) * f);
+    };
+    if ((from ^ to) & 15) {      // no common boundary: element by element
+        for (int i = lane; i < count; i += 32) one(i);
+        return;
+    }
+    const int head = head_of<T>(from, count);
+    constexpr int kVec = 16 / sizeof(T);
+    const int vecs = (count - head) / kVec, rest = head + vecs * kVec;
+    const uint4* v = reinterpret_cast<const uint4*>(p + head);
+    uint4* w = reinterpret_cast<uint4*>(q + head);
+    auto times = [&](uint4 u) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            } else {
+                const float2 e = halves(x[i]);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(e.x * f, e.y * f);
+                x[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        return u;
+    };
+    constexpr int kAtOnce = 8;
+    int i = lane;
+    for (; i + 32 * (kAtOnce - 1) < vecs; i += 32 * kAtOnce) {
+        uint4 u[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) u[k] = v[i + 32 * k];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) w[i + 32 * k] = times(u[k]);
+    }
+    for (; i < vecs; i += 32) w[i] = times(v[i]);
+    const int at = lane < head ? lane : rest + lane - head;
+    if (lane < head || at < count) one(at);
+}
+
+// Scales this warp's segments, the last ones first.
+__device__ __forceinline__ void scale_part(const NormLaunch& a, int64_t warp, int64_t warps, float f) {
+    if (a.out == nullptr || (f == 1.0f && a.out == a.seg) || warp >= a.n_seg) return;
+    int64_t k = warp + (a.n_seg - 1 - warp) / warps * warps;
+    Segment next = a.seg[k];
+    uint64_t next_to = a.out[k].ptr;
+    for (; k >= 0; k -= warps) {
+        const Segment g = next;
+        const uint64_t to = next_to;
+        if (k >= warps) {
+            next = a.seg[k - warps];
+            next_to = a.out[k - warps].ptr;
+        }
+        if (g.dtype == OFRL_DTYPE_F32)
+            scale_segment<float>(g.ptr, to, g.count, f);
+        else
+            scale_segment<__nv_bfloat16>(g.ptr, to, g.count, f);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormLaunch a) {
-    float s = 0.0f, c = 0.0f;
-    for (int64_t k = blockIdx.x; k < a.n_seg; k += gridDim.x) {
-        const Segment g = a.seg[k];
-        float x = 0.0f;
-        for (int i = threadIdx.x; i < g.count; i += kThreads) {
-            const float e = load_elem(g.ptr, g.dtype, i);
-            x = fmaf(e, e, x);
-        }
-        pair_add(s, c, x);
-    }
-    // once s is infinite or NaN, the remainder c is NaN and says nothing
-    const double part = block_sum(isfinite(s) ? (double)s + (double)c : (double)s);
+    constexpr int W = kThreads / 32;
+    const double part = block_sum<W>(norm_part(a, blockIdx.x * (int64_t)W + (threadIdx.x >> 5), gridDim.x * (int64_t)W));
     __shared__ bool last;
     if (threadIdx.x == 0) {
         a.partial[blockIdx.x] = part;
@@ -87,34 +219,47 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         last = atomicAdd(&a.state->ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
+    pdl_trigger();
     if (!last) return;
     __threadfence();
     double sum = 0.0;
     for (int b = threadIdx.x; b < gridDim.x; b += kThreads) sum += __ldcg(a.partial + b);
-    sum = block_sum(sum);
+    sum = block_sum<W>(sum);
     if (threadIdx.x == 0) {
         const float norm = (float)sqrt(sum);
-        a.state->norm = norm;
         a.state->scale = clip_scale(norm, a.max_norm);
         a.state->ticket = 0;
         a.norm_out[0] = norm;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ NormLaunch a) {
-    const float f = a.state->scale;
-    for (int64_t k = blockIdx.x; k < a.n_seg; k += gridDim.x) {
-        const Segment g = a.seg[k];
-        const uint64_t to = a.out[k].ptr;
-        if (f == 1.0f && to == g.ptr) continue;
-        for (int i = threadIdx.x; i < g.count; i += kThreads) {
-            const float e = load_elem(g.ptr, g.dtype, i) * f;
-            if (g.dtype == OFRL_DTYPE_F32)
-                reinterpret_cast<float*>(to)[i] = e;
-            else
-                reinterpret_cast<__nv_bfloat16*>(to)[i] = __float2bfloat16_rn(e);
-        }
+__global__ void __launch_bounds__(kThreads) scale_kernel(NormLaunch a) {
+    constexpr int W = kThreads / 32;
+    pdl_wait();
+    scale_part(a, blockIdx.x * (int64_t)W + (threadIdx.x >> 5), gridDim.x * (int64_t)W, a.state->scale);
+}
+
+// Both in one cluster.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+norm_cluster_kernel(const __grid_constant__ NormLaunch a) {
+    constexpr int W = kClusterThreads / 32;
+    __shared__ double parts[kCluster];
+    const int64_t warp = blockIdx.x * (int64_t)W + (threadIdx.x >> 5), warps = kCluster * (int64_t)W;
+    const double part = block_sum<W>(norm_part(a, warp, warps));
+    if (threadIdx.x < kCluster) {      // this CTA's part to every CTA
+        uint32_t at;
+        const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&parts[blockIdx.x]));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(part) : "memory");
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kCluster; ++i) sum += parts[i];
+    const float norm = (float)sqrt(sum);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.norm_out[0] = norm;
+    scale_part(a, warp, warps, clip_scale(norm, a.max_norm));
 }
 
 }  // namespace
@@ -127,7 +272,7 @@ struct ofrl_tensors {
     int64_t* sizes;         // host copies: what a clip's two lists must share
     int32_t* dtypes;
     int64_t n_seg;
-    int grid;
+    int grid;               // 0: one cluster
     void* base;             // the single cudaMalloc
     ofrl::Segment* seg;
     double* partial;
@@ -163,6 +308,19 @@ NormLaunch args_of(const ofrl_tensors* l, float* norm_out) {
     return a;
 }
 
+ofrl_status launch(const ofrl_tensors* l, const NormLaunch& a, cudaStream_t st) {
+    cudaError_t e;
+    if (l->grid == 0) {
+        norm_cluster_kernel<<<kCluster, kClusterThreads, 0, st>>>(a);
+        e = cudaGetLastError();
+    } else {
+        norm_kernel<<<l->grid, kThreads, 0, st>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && a.out != nullptr) e = launch_pdl(scale_kernel, dim3(l->grid), dim3(kThreads), 0, st, a);
+    }
+    return e == cudaSuccess ? OFRL_OK : OFRL_ECUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -172,13 +330,14 @@ ofrl_status ofrl_tensors_create(const void* const* ptrs, const int64_t* sizes, c
     if (out == nullptr) return OFRL_EINVAL;
     *out = nullptr;
     if (ptrs == nullptr || sizes == nullptr || dtypes == nullptr || n < 1 || n > kMaxList) return OFRL_EINVAL;
-    int64_t n_seg = 0;
+    int64_t n_seg = 0, elems = 0;
     for (int32_t i = 0; i < n; ++i) {
         if (sizes[i] < 0 || sizes[i] > (int64_t)1 << 40) return OFRL_EINVAL;
         if (dtypes[i] != OFRL_DTYPE_F32 && dtypes[i] != OFRL_DTYPE_BF16) return OFRL_EINVAL;
         const uintptr_t p = reinterpret_cast<uintptr_t>(ptrs[i]);
         if (sizes[i] > 0 && (p == 0 || (p & (dtypes[i] == OFRL_DTYPE_F32 ? 3u : 1u)))) return OFRL_EINVAL;
         n_seg += (sizes[i] + kSegment - 1) / kSegment;
+        elems += sizes[i];
     }
     ofrl_tensors* l = new (std::nothrow) ofrl_tensors;
     if (l == nullptr) return OFRL_ECUDA;
@@ -204,8 +363,8 @@ ofrl_status ofrl_tensors_create(const void* const* ptrs, const int64_t* sizes, c
             host[k++] = {(uint64_t)reinterpret_cast<uintptr_t>(ptrs[i]) + (uint64_t)(at * elem),
                          (int32_t)(sizes[i] - at < kSegment ? sizes[i] - at : kSegment), dtypes[i]};
     }
-    const int64_t most = (int64_t)l->num_sms * kCtasPerSm;
-    l->grid = (int)(n_seg < 1 ? 1 : n_seg < most ? n_seg : most);
+    const int64_t most = (int64_t)l->num_sms * kCtasPerSm, want = (n_seg + kThreads / 32 - 1) / (kThreads / 32);
+    l->grid = elems <= kClusterElems ? 0 : (int)(want < most ? want : most);
     const int64_t seg_bytes = (n_seg * (int64_t)sizeof(Segment) + 255) / 256 * 256;
     const int64_t part_bytes = (l->grid * (int64_t)sizeof(double) + 255) / 256 * 256;
     if (cudaMalloc(&l->base, (size_t)(seg_bytes + part_bytes + 256)) != cudaSuccess) {
@@ -244,8 +403,7 @@ ofrl_status ofrl_global_norm(ofrl_tensors* list, float* norm_out, void* stream) 
     const ofrl_status s = check_list(list);
     if (s != OFRL_OK) return s;
     if (norm_out == nullptr) return OFRL_EINVAL;
-    norm_kernel<<<list->grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(args_of(list, norm_out));
-    return cudaGetLastError() == cudaSuccess ? OFRL_OK : OFRL_ECUDA;
+    return launch(list, args_of(list, norm_out), static_cast<cudaStream_t>(stream));
 }
 
 ofrl_status ofrl_global_norm_clip(ofrl_tensors* list, float max_norm, float* norm_out, ofrl_tensors* out,
@@ -261,10 +419,7 @@ ofrl_status ofrl_global_norm_clip(ofrl_tensors* list, float max_norm, float* nor
     NormLaunch a = args_of(list, norm_out);
     a.max_norm = max_norm;
     a.out = out != nullptr ? out->seg : list->seg;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    norm_kernel<<<list->grid, kThreads, 0, st>>>(a);
-    scale_kernel<<<list->grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? OFRL_OK : OFRL_ECUDA;
+    return launch(list, a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
