@@ -347,8 +347,6 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
     const Work w = work_of(a, NW * 16);
     ring_init<NW>(ring);
     uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
-    if (warp == 0)
-        for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n);
     {
         const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
         const int row0 = w.row0 + warp * 16;
@@ -356,6 +354,9 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
         float S[DK / 8][4];
         copy_rows<St, T>(a, w, mine, 0, row0);
         load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
+        pdl_wait();      // what the preparing kernel leaves
+        if (warp == 0)
+            for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n);
         for (int c = 0; c < w.chunks; ++c) {
             const int st = c % St::kCount;
             copy_rows<St, T>(a, w, mine + ((c + 1) & 1) * St::kRows, c + 1, row0);
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Work w = work_of(a, NW * 16);
+    pdl_trigger();
     ring_init<NW>(ring);
     uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
     if (warp == 0)
@@ -581,29 +583,30 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
 }
 
 template <typename K>
-cudaError_t go(K kernel, int nw, int smem, const ChainArgs& c, cudaStream_t st) {
+cudaError_t go(K kernel, int nw, int smem, bool early, const ChainArgs& c, cudaStream_t st) {
     const int slices = (c.shape.v_dim + nw * 16 - 1) / (nw * 16);
     const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * slices;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(kernel);
     if (e != cudaSuccess) return e;
+    if (early) return launch_pdl(kernel, dim3((unsigned)grid), dim3(nw * 32), smem, st, c);
     kernel<<<(unsigned)grid, nw * 32, smem, st>>>(c);
     return cudaGetLastError();
 }
 
 template <typename T, int DK, int NM>
 cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
-    if (!c.state_img) return go(delta_forward_kernel<T, DK, NM, 4, false>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
+    if (!c.state_img) return go(delta_forward_kernel<T, DK, NM, 4, false>, 4, Stage<T, DK, NM, 4>::kShared, true, c, st);
     return c.shape.v_dim > 64
-               ? go(delta_forward_kernel<T, DK, NM, 8, true>, 8, Stage<T, DK, NM, 8>::kShared, c, st)
-               : go(delta_forward_kernel<T, DK, NM, 4, true>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
+               ? go(delta_forward_kernel<T, DK, NM, 8, true>, 8, Stage<T, DK, NM, 8>::kShared, true, c, st)
+               : go(delta_forward_kernel<T, DK, NM, 4, true>, 4, Stage<T, DK, NM, 4>::kShared, true, c, st);
 }
 template <typename T, int DK>
 cudaError_t reverse(const ChainArgs& c, cudaStream_t st) {
     constexpr int NM = sizeof(T) == 4 ? 2 : 1;
-    return c.shape.v_dim > 64 ? go(delta_reverse_kernel<T, DK, 8>, 8, Stage<T, DK, NM, 8>::kShared, c, st)
-                              : go(delta_reverse_kernel<T, DK, 4>, 4, Stage<T, DK, NM, 4>::kShared, c, st);
+    return c.shape.v_dim > 64 ? go(delta_reverse_kernel<T, DK, 8>, 8, Stage<T, DK, NM, 8>::kShared, false, c, st)
+                              : go(delta_reverse_kernel<T, DK, 4>, 4, Stage<T, DK, NM, 4>::kShared, false, c, st);
 }
 
 ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {

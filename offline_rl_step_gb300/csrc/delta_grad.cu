@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
             umma::fence_mbar_init();
         }
     }
+    pdl_wait();      // what the backward chain leaves
     __syncthreads();
     const int rows = s_at[1];
     if (rows <= 0) return;
@@ -483,8 +484,7 @@ cudaError_t run(const GradArgs& g, int64_t grid, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<T, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(delta_grad_kernel<T, DK, DV>);
     if (e != cudaSuccess) return e;
-    delta_grad_kernel<T, DK, DV><<<(unsigned)grid, kGradThreads, smem, st>>>(g);
-    return cudaGetLastError();
+    return launch_pdl(delta_grad_kernel<T, DK, DV>, dim3((unsigned)grid), dim3(kGradThreads), smem, st, g);
 }
 
 cudaError_t pick(const GradArgs& g, int64_t grid, cudaStream_t st) {

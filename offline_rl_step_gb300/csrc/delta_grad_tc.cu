@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             umma::fence_mbar_init();
         }
     }
+    pdl_wait();      // what the backward chain leaves
     __syncthreads();
     Item it = s_next;
     if (it.rows <= 0) return;
@@ -562,8 +563,7 @@ cudaError_t run(const GradTcArgs& g, cudaStream_t st) {
     const int64_t most = (int64_t)g.num_sms * Lay<DK, DV>::kCtas;
     const unsigned grid = (unsigned)(g.items < most ? g.items : most);
     if (grid == 0) return cudaSuccess;
-    delta_grad_tc_kernel<DK, DV><<<grid, kThreads, smem, st>>>(g);
-    return cudaGetLastError();
+    return launch_pdl(delta_grad_tc_kernel<DK, DV>, dim3(grid), dim3(kThreads), smem, st, g);
 }
 
 }  // namespace

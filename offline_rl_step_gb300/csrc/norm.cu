@@ -45,7 +45,7 @@ struct NormLaunch {
     const Segment* seg;
     const Segment* out;     // clip: same shape as seg; null: the norm alone
     int64_t n_seg;
-    double* partial;        // [grid]
+    float4* partial;        // [grid]
     NormState* state;
     float max_norm;
     float* norm_out;
@@ -58,19 +58,43 @@ __device__ __forceinline__ void pair_add(float& s, float& c, float x) {
     s = t;
 }
 
-// Sum over the block's warps of a value per lane; every thread gets it.
+// A sum of squares over lanes: pairs for those from 1 on, times kDown so that
+// 2^24 of them do not overflow, and for the ones below, as they are.
+struct Sums {
+    float s, c, big_s, big_c;
+};
+constexpr float kDown = 1.0f / (1 << 24), kDownRoot = 1.0f / (1 << 12);
+
+__device__ __forceinline__ Sums sums_of(float s, float c) {
+    return s >= 1.0f ? Sums{0.0f, 0.0f, s * kDown, c * kDown} : Sums{s, c, 0.0f, 0.0f};      // a NaN stays below
+}
+__device__ __forceinline__ void add(Sums& a, const Sums& b) {
+    pair_add(a.s, a.c, b.s);
+    a.c += b.c;
+    pair_add(a.big_s, a.big_c, b.big_s);
+    a.big_c += b.big_c;
+}
+// Once a sum is infinite or NaN, its remainder is NaN and says nothing.
+__device__ __forceinline__ float root(const Sums& a) {
+    const float low = isfinite(a.s) ? a.s + a.c : a.s, big = isfinite(a.big_s) ? a.big_s + a.big_c : a.big_s;
+    return big > 0.0f ? sqrtf(big + low * kDown) / kDownRoot : sqrtf(low);
+}
+__device__ __forceinline__ Sums warp_sums(Sums a, int from = 16) {
+    for (int o = from; o > 0; o >>= 1)
+        add(a, {__shfl_down_sync(0xffffffffu, a.s, o), __shfl_down_sync(0xffffffffu, a.c, o),
+                __shfl_down_sync(0xffffffffu, a.big_s, o), __shfl_down_sync(0xffffffffu, a.big_c, o)});
+    return a;      // lane 0's
+}
+
+// Sum over the block; thread 0 has it.
 template <int WARPS>
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double warp_part[WARPS];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ Sums block_sums(Sums a) {
+    __shared__ Sums part[WARPS];
+    a = warp_sums(a);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double r = 0.0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) r += warp_part[i];
-    return r;
+    if (threadIdx.x < 32) a = warp_sums(threadIdx.x < WARPS ? part[threadIdx.x] : Sums{0, 0, 0, 0}, WARPS / 2);
+    return a;
 }
 
 // Elements before the first 16-byte boundary, at most n.
@@ -94,7 +118,7 @@ __device__ __forceinline__ float squares(uint64_t ptr, int count) {
     const int vecs = (count - head) / kVec, rest = head + vecs * kVec;
     const uint4* v = reinterpret_cast<const uint4*>(p + head);
     float x = 0.0f;
-    auto add = [&](const uint4& u) {
+    auto take = [&](const uint4& u) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -115,9 +139,9 @@ __device__ __forceinline__ float squares(uint64_t ptr, int count) {
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) u[k] = v[i + 32 * k];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) add(u[k]);
+        for (int k = 0; k < kAtOnce; ++k) take(u[k]);
     }
-    for (; i < vecs; i += 32) add(v[i]);
+    for (; i < vecs; i += 32) take(v[i]);
     // fewer than kVec elements before and after the vectors
     const int at = lane < head ? lane : rest + lane - head;
     if (lane < head || at < count) {
@@ -128,7 +152,7 @@ __device__ __forceinline__ float squares(uint64_t ptr, int count) {
 }
 
 // Squares of this warp's segments.
-__device__ __forceinline__ double norm_part(const NormLaunch& a, int64_t warp, int64_t warps) {
+__device__ __forceinline__ Sums norm_part(const NormLaunch& a, int64_t warp, int64_t warps) {
     float s = 0.0f, c = 0.0f;
     Segment g = {0, 0, 0}, next = {0, 0, 0};
     if (warp < a.n_seg) next = a.seg[warp];
@@ -137,8 +161,7 @@ __device__ __forceinline__ double norm_part(const NormLaunch& a, int64_t warp, i
         if (k + warps < a.n_seg) next = a.seg[k + warps];
         pair_add(s, c, g.dtype == OFRL_DTYPE_F32 ? squares<float>(g.ptr, g.count) : squares<__nv_bfloat16>(g.ptr, g.count));
     }
-    // once s is infinite or NaN, the remainder c is NaN and says nothing
-    return isfinite(s) ? (double)s + (double)c : (double)s;
+    return sums_of(s, c);
 }
 
 template <typename T>
@@ -211,22 +234,26 @@ __device__ __forceinline__ void scale_part(const NormLaunch& a, int64_t warp, in
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int W = kThreads / 32;
-    const double part = block_sum<W>(norm_part(a, blockIdx.x * (int64_t)W + (threadIdx.x >> 5), gridDim.x * (int64_t)W));
+    const Sums part = block_sums<W>(norm_part(a, blockIdx.x * (int64_t)W + (threadIdx.x >> 5), gridDim.x * (int64_t)W));
     __shared__ bool last;
     if (threadIdx.x == 0) {
-        a.partial[blockIdx.x] = part;
+        a.partial[blockIdx.x] = make_float4(part.s, part.c, part.big_s, part.big_c);
         __threadfence();
         last = atomicAdd(&a.state->ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
-    pdl_trigger();
+    if (a.out != nullptr) pdl_trigger();      // scale_kernel is next
     if (!last) return;
     __threadfence();
-    double sum = 0.0;
-    for (int b = threadIdx.x; b < gridDim.x; b += kThreads) sum += __ldcg(a.partial + b);
-    sum = block_sum<W>(sum);
+    Sums p = {0, 0, 0, 0};
+    for (int b = threadIdx.x; b < gridDim.x; b += kThreads) {
+        const float4 x = __ldcg(a.partial + b);
+        add(p, {x.x, x.y, x.z, x.w});
+    }
+    __syncthreads();
+    p = block_sums<W>(p);
     if (threadIdx.x == 0) {
-        const float norm = (float)sqrt(sum);
+        const float norm = root(p);
         a.state->scale = clip_scale(norm, a.max_norm);
         a.state->ticket = 0;
         a.norm_out[0] = norm;
@@ -243,21 +270,26 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(NormLaunch a) {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
 norm_cluster_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int W = kClusterThreads / 32;
-    __shared__ double parts[kCluster];
+    __shared__ __align__(16) float4 parts[kCluster];
     const int64_t warp = blockIdx.x * (int64_t)W + (threadIdx.x >> 5), warps = kCluster * (int64_t)W;
-    const double part = block_sum<W>(norm_part(a, warp, warps));
-    if (threadIdx.x < kCluster) {      // this CTA's part to every CTA
-        uint32_t at;
-        const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&parts[blockIdx.x]));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(threadIdx.x));
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(part) : "memory");
+    const Sums part = block_sums<W>(norm_part(a, warp, warps));
+    if (threadIdx.x < 32) {      // this CTA's part to every CTA
+        const float s = __shfl_sync(0xffffffffu, part.s, 0), c = __shfl_sync(0xffffffffu, part.c, 0),
+                    bs = __shfl_sync(0xffffffffu, part.big_s, 0), bc = __shfl_sync(0xffffffffu, part.big_c, 0);
+        if (threadIdx.x < kCluster) {
+            uint32_t at;
+            const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&parts[blockIdx.x]));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(threadIdx.x));
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(s), "f"(c), "f"(bs), "f"(bc)
+                         : "memory");
+        }
     }
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    double sum = 0.0;
+    Sums p = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kCluster; ++i) sum += parts[i];
-    const float norm = (float)sqrt(sum);
+    for (int i = 0; i < kCluster; ++i) add(p, {parts[i].x, parts[i].y, parts[i].z, parts[i].w});
+    const float norm = root(p);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.norm_out[0] = norm;
     scale_part(a, warp, warps, clip_scale(norm, a.max_norm));
 }
@@ -275,7 +307,7 @@ struct ofrl_tensors {
     int grid;               // 0: one cluster
     void* base;             // the single cudaMalloc
     ofrl::Segment* seg;
-    double* partial;
+    float4* partial;
     ofrl::NormState* state;
 };
 
@@ -366,7 +398,7 @@ ofrl_status ofrl_tensors_create(const void* const* ptrs, const int64_t* sizes, c
     const int64_t most = (int64_t)l->num_sms * kCtasPerSm, want = (n_seg + kThreads / 32 - 1) / (kThreads / 32);
     l->grid = elems <= kClusterElems ? 0 : (int)(want < most ? want : most);
     const int64_t seg_bytes = (n_seg * (int64_t)sizeof(Segment) + 255) / 256 * 256;
-    const int64_t part_bytes = (l->grid * (int64_t)sizeof(double) + 255) / 256 * 256;
+    const int64_t part_bytes = (l->grid * (int64_t)sizeof(float4) + 255) / 256 * 256;
     if (cudaMalloc(&l->base, (size_t)(seg_bytes + part_bytes + 256)) != cudaSuccess) {
         cudaGetLastError();
         delete[] host;
@@ -375,7 +407,7 @@ ofrl_status ofrl_tensors_create(const void* const* ptrs, const int64_t* sizes, c
     }
     char* b = static_cast<char*>(l->base);
     l->seg = reinterpret_cast<Segment*>(b);
-    l->partial = reinterpret_cast<double*>(b + seg_bytes);
+    l->partial = reinterpret_cast<float4*>(b + seg_bytes);
     l->state = reinterpret_cast<NormState*>(b + seg_bytes + part_bytes);
     const bool ok = cudaMemset(l->state, 0, sizeof(NormState)) == cudaSuccess &&
                     cudaMemcpy(l->seg, host, n_seg * sizeof(Segment), cudaMemcpyHostToDevice) == cudaSuccess &&
