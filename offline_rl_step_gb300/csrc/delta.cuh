@@ -14,6 +14,7 @@ struct ofrl_delta {
     void* base;          // the single cudaMalloc of the context
     int64_t bytes;
     int32_t* status;     // [OFRL_STAT_WORDS]
+    unsigned* counter;   // work counter of the gradient kernel
     uint8_t* scratch;    // what lies between the launches of one call
 };
 
@@ -59,6 +60,7 @@ struct SeqLaunch {
     ofrl_delta_grads grads;
     float* d_init;
     uint8_t* scratch;
+    unsigned* counter;
     int32_t* status;
     int num_sms;
 };

@@ -33,7 +33,7 @@ bool counts_ok(int64_t tokens, int64_t episodes) {
 int64_t elem_size(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_F32 ? 4 : 2; }
 
 struct Layout {
-    int64_t off_status, off_scratch, total;
+    int64_t off_status, off_counter, off_scratch, total;
 };
 
 Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_episodes, bool backward) {
@@ -41,6 +41,7 @@ Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_epis
     int64_t o = 0;
     auto take = [&](int64_t bytes) { const int64_t at = o; o = round_up(o + bytes, 256); return at; };
     L.off_status = take((int64_t)OFRL_STAT_WORDS * 4);
+    L.off_counter = take(4);
     L.off_scratch = take(scratch_bytes(s, max_tokens, max_episodes, backward));
     L.total = o;
     return L;
@@ -105,6 +106,7 @@ SeqLaunch base_launch(const ofrl_delta* ctx, const ofrl_delta_tokens* in, const 
     a.ends = ends;
     a.episodes = episodes;
     a.scratch = ctx->scratch;
+    a.counter = ctx->counter;
     a.status = ctx->status;
     a.num_sms = ctx->num_sms;
     return a;
@@ -154,6 +156,7 @@ ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens,
     }
     char* b = static_cast<char*>(ctx->base);
     ctx->status = reinterpret_cast<int32_t*>(b + L.off_status);
+    ctx->counter = reinterpret_cast<unsigned*>(b + L.off_counter);
     ctx->scratch = reinterpret_cast<uint8_t*>(b + L.off_scratch);
     if (cudaMemset(ctx->status, 0, OFRL_STAT_WORDS * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(ctx->base);

@@ -43,6 +43,7 @@ struct ChainArgs {
     uint8_t* vec_img;        // per (slot, head): U (forward) or R (backward)
     float* state_unit;       // [slot][head]: their powers of two
     float* vec_unit;
+    unsigned* counter;       // backward: zeroed for the gradient kernel
     int32_t* status;
 };
 
@@ -470,6 +471,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Work w = work_of(a, NW * 16);
     pdl_trigger();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     ring_init<NW>(ring);
     uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
     if (warp == 0)
@@ -621,6 +623,7 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
     c.vec_img = img.vec;
     c.state_unit = img.state_unit;
     c.vec_unit = img.vec_unit;
+    c.counter = a.counter;
     c.status = a.status;
     return c;
 }

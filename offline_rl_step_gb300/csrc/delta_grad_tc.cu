@@ -2,8 +2,8 @@
 // (delta_grad.cu has the formulas and does the same for fp32 tokens, whose
 // two-plane operands do not fit beside each other in shared memory).
 //
-// Persistent CTAs of eight warps take (chunk, key head) items in turn and loop
-// over the group's value heads; the next head's operands are copied in while
+// Persistent CTAs of eight warps take (chunk, key head) items from a counter
+// and loop over the group's value heads; the next head's operands are copied in while
 // this one's results leave TMEM.  Accumulator rows are tokens twice: rows 0 .. 63 belong to dq,
 // rows 64 .. 127 to dk, so each of these is one 128-row product:
 //   N   = [dO; R] U^T                 (64 columns)
@@ -42,6 +42,7 @@ struct GradTcArgs {
     const __nv_bfloat16* dout;
     ofrl_delta_grads grads;
     int64_t items;
+    unsigned* next;      // zero at the start of the launch
     int num_sms;
     int32_t* status;
 };
@@ -130,12 +131,16 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
     float* red = sums + 2 * 4 * kChunk;                             // [2][64] R v
     enum { R_Q, R_ST, R_IN, R_COL };
 
-    // the first item at or after n with tokens, by one whole warp
-    auto find = [&](int64_t n) {
+    // the next item with tokens, by one whole warp
+    auto find = [&]() {
         Item it = {0, 0, 0, 0};
-        for (; n < a.items; n += gridDim.x) {
-            it.slot = n / hk;
-            it.khead = (int)(n % hk);
+        while (true) {
+            unsigned n = 0;
+            if (lane == 0) n = atomicAdd(a.next, 1u);
+            n = __shfl_sync(0xffffffffu, n, 0);
+            if (n >= a.items) break;
+            it.slot = n / (unsigned)hk;
+            it.khead = (int)(n % (unsigned)hk);
             const int32_t tokens = (int32_t)a.in.tokens;
             const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)it.slot);
             const Span sp = span_of(a.ends, e, tokens);
@@ -147,8 +152,9 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
         }
         if (lane == 0) s_next = it;
     };
+    pdl_wait();      // what the backward chain leaves
     if (warp == 0) {
-        find(blockIdx.x);
+        find();
         if (lane == 0) {
             s_dead = 0;
             umma::mbar_init(&bar_keys, 1);
@@ -160,7 +166,6 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             umma::fence_mbar_init();
         }
     }
-    pdl_wait();      // what the backward chain leaves
     __syncthreads();
     Item it = s_next;
     if (it.rows <= 0) return;
@@ -221,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
     float acc[H];
     int turn = 0, g = 0;                         // heads taken; head of the group
     int items = 0;
-    int64_t at_item = it.slot * hk + it.khead;
     while (true) {
         const int head = it.khead * group + g;
         const bool last = g + 1 == group;
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
                     2 * CG * kTile, id_s, blocks, false);
             umma::commit(&bar_s);
         }
-        if (warp == 1 && last) find(at_item + gridDim.x);
+        if (warp == 1 && last) find();
         // <S_0, dS_1> meanwhile: 8 elements of one row per turn
         float ss = 0.0f;
         for (int x = threadIdx.x; x < blocks * 2 * CG * 8; x += kThreads) {
@@ -536,7 +540,6 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
         if (!last) {
             ++g;
         } else {
-            at_item = nx.slot * hk + nx.khead;
             it = nx;
             g = 0;
             ++items;
@@ -588,6 +591,7 @@ cudaError_t launch_grad_tc(const SeqLaunch& a, const Prepared& p, const Images& 
     g.grads = a.grads;
     g.status = a.status;
     g.items = slots_of(a.in.tokens, a.episodes) * a.shape.k_heads;
+    g.next = a.counter;
     g.num_sms = a.num_sms;
     if (a.shape.k_dim > 64) return a.shape.v_dim > 64 ? run<128, 128>(g, st) : run<128, 64>(g, st);
     return a.shape.v_dim > 64 ? run<64, 128>(g, st) : run<64, 64>(g, st);

@@ -34,25 +34,32 @@ struct PrepArgs {
     int32_t* status;
 };
 
+// Eight elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_b(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
     }
-}
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[sizeof(T) / 2 - 1].x, v[sizeof(T) / 2 - 1].y,
+                               v[sizeof(T) / 2 - 1].z, v[sizeof(T) / 2 - 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = unpack_b(w[i / 2]);
+                x[i] = i & 1 ? f.y : f.x;
+            }
+        }
+    }
+};
 
 // Power of two that divides a row: its largest magnitude becomes [1, 2).
 __device__ __forceinline__ float row_unit(float amax) {
@@ -138,42 +145,71 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
             }
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
-    // group, so that a store of 8 lanes fills one 8x8 block.
-    {
-        uint8_t* keys = a.keys + (slot * hk + khead) * KeyImage::bytes(DK, NT);
-        const bool leave = head % group == 0;
-        const int r = lane & 7, c4 = lane >> 3;
+    // group, so that a store of 8 lanes fills one 8x8 block.  All of a warp's
+    // loads (of a half of them, for fp32) go out before the first is used, and
+    // the first warp adds up its log decays while they are under way.
+    Two G[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, total = {0.0f, 0.0f};
+    uint8_t* keys = a.keys + (slot * hk + khead) * KeyImage::bytes(DK, NT);
+    const bool leave = head % group == 0;
+    constexpr int kBatch = NT == 1 ? 4 : 2;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int rg = warp * 2 + (w & 1);
-            const bool isq = w >= 2;
-            const int row = rg * 8 + r;
+    for (int w0 = 0; w0 < 4; w0 += kBatch) {
+        const int r = lane & 7, c4 = lane >> 3;
+        Raw<T> raw[kBatch][CG / 4];
+#pragma unroll
+        for (int w = 0; w < kBatch; ++w) {
+            const int row = (warp * 2 + (w & 1)) * 8 + r;
+            const bool isq = w0 + w >= 2;
             const T* p = isq ? static_cast<const T*>(a.in.q) + (tok + row) * a.in.q_stride + (int64_t)khead * dk
                              : static_cast<const T*>(a.in.k) + (tok + row) * a.in.k_stride + (int64_t)khead * dk;
-            float x[CG / 4][8];
-            float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < CG / 4; ++i) {
                 const int col = (c4 + 4 * i) * 8;
                 if (row < rows && col < dk)
-                    load8<T>(p + col, x[i]);
+                    raw[w][i].load(p + col);
                 else
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) x[i][z] = 0.0f;
+                    raw[w][i].clear();
             }
+        }
+        if (w0 == 0 && warp == 0) {
+            Two g[2];
 #pragma unroll
-            for (int i = 0; i < CG / 4; ++i)
+            for (int i = 0; i < 2; ++i) g[i] = two_log2(gin[i] < kMinLogDecay ? kMinLogDecay : gin[i]);      // a NaN stays
+            Two sum = two_add(g[0], g[1]);
 #pragma unroll
-                for (int z = 0; z < 8; ++z) m = fmaxf(m, fabsf(x[i][z]));
+            for (int o = 1; o < 32; o <<= 1) {
+                const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+                if (lane >= o) sum = two_add(up, sum);
+            }
+            total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+            Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+            if (lane == 0) before = {0.0f, 0.0f};
+            G[0] = two_add(before, g[0]);
+            G[1] = sum;
+        }
+#pragma unroll
+        for (int w = 0; w < kBatch; ++w) {
+            const int rg = warp * 2 + (w & 1);
+            const bool isq = w0 + w >= 2;
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CG / 4; ++i) {
+                float x[8];
+                raw[w][i].get(x);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) m = fmaxf(m, fabsf(x[z]));
+            }
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
             const float unit = row_unit(m), inv = pow2_inv(unit);
-            if (c4 == 0) (isq ? kqv : kap)[row] = unit;
+            if (c4 == 0) (isq ? kqv : kap)[rg * 8 + r] = unit;
 #pragma unroll
             for (int i = 0; i < CG / 4; ++i) {
+                float x[8];
+                raw[w][i].get(x);
                 uint32_t pl[4][NT];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) planes_h<NT>(x[i][2 * z] * inv, x[i][2 * z + 1] * inv, pl[z]);
+                for (int z = 0; z < 4; ++z) planes_h<NT>(x[2 * z] * inv, x[2 * z + 1] * inv, pl[z]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint4 v = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
@@ -186,21 +222,6 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
     }
     __syncthreads();
     if (warp == 0) {
-        Two g[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            g[i] = two_log2(gin[i] < kMinLogDecay ? kMinLogDecay : gin[i]);      // a NaN stays
-        }
-        Two sum = two_add(g[0], g[1]);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
-            if (lane >= o) sum = two_add(up, sum);
-        }
-        const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
-        Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
-        if (lane == 0) before = {0.0f, 0.0f};
-        const Two G[2] = {two_add(before, g[0]), sum};
         float most = 1.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
