@@ -16,6 +16,7 @@ struct ofrl_delta {
     int32_t* status;     // [OFRL_STAT_WORDS]
     unsigned* counter;   // work counter of the gradient kernel
     uint8_t* scratch;    // what lies between the launches of one call
+    uint8_t* parts;      // of a forward pass over parts of episodes
 };
 
 namespace ofrl {
@@ -60,6 +61,7 @@ struct SeqLaunch {
     ofrl_delta_grads grads;
     float* d_init;
     uint8_t* scratch;
+    uint8_t* parts;
     unsigned* counter;
     int32_t* status;
     int num_sms;
@@ -81,6 +83,7 @@ cudaError_t launch_forward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_backward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_step(const StepLaunch& a, cudaStream_t st);
 int64_t saved_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episodes);
+int64_t parts_bytes(const ofrl_delta_shape& s, int64_t tokens, int num_sms);
 int64_t scratch_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episodes, bool backward);
 
 template <typename T>

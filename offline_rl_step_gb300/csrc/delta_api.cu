@@ -33,16 +33,17 @@ bool counts_ok(int64_t tokens, int64_t episodes) {
 int64_t elem_size(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_F32 ? 4 : 2; }
 
 struct Layout {
-    int64_t off_status, off_counter, off_scratch, total;
+    int64_t off_status, off_counter, off_scratch, off_parts, total;
 };
 
-Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_episodes, bool backward) {
+Layout layout_of(const ofrl_delta_shape& s, int64_t max_tokens, int64_t max_episodes, bool backward, int num_sms) {
     Layout L;
     int64_t o = 0;
     auto take = [&](int64_t bytes) { const int64_t at = o; o = round_up(o + bytes, 256); return at; };
     L.off_status = take((int64_t)OFRL_STAT_WORDS * 4);
     L.off_counter = take(4);
     L.off_scratch = take(scratch_bytes(s, max_tokens, max_episodes, backward));
+    L.off_parts = take(parts_bytes(s, max_tokens, num_sms));
     L.total = o;
     return L;
 }
@@ -106,6 +107,7 @@ SeqLaunch base_launch(const ofrl_delta* ctx, const ofrl_delta_tokens* in, const 
     a.ends = ends;
     a.episodes = episodes;
     a.scratch = ctx->scratch;
+    a.parts = ctx->parts;
     a.counter = ctx->counter;
     a.status = ctx->status;
     a.num_sms = ctx->num_sms;
@@ -120,7 +122,8 @@ int64_t ofrl_delta_workspace_bytes(const ofrl_delta_shape* shape, int64_t max_to
                                    int32_t backward) {
     if (check_shape(shape) != OFRL_OK || !counts_ok(max_tokens, max_episodes) || (backward != 0 && backward != 1))
         return -1;
-    return layout_of(*shape, max_tokens, max_episodes, backward != 0).total;
+    int device = 0;
+    return layout_of(*shape, max_tokens, max_episodes, backward != 0, sm_count(&device)).total;
 }
 
 int64_t ofrl_delta_saved_bytes(const ofrl_delta_shape* shape, int64_t tokens, int32_t num_episodes) {
@@ -143,7 +146,7 @@ ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens,
         delete ctx;
         return OFRL_ECUDA;
     }
-    const Layout L = layout_of(*shape, max_tokens, max_episodes, backward != 0);
+    const Layout L = layout_of(*shape, max_tokens, max_episodes, backward != 0, ctx->num_sms);
     ctx->shape = *shape;
     ctx->max_tokens = max_tokens;
     ctx->max_episodes = max_episodes;
@@ -158,6 +161,7 @@ ofrl_status ofrl_delta_create(const ofrl_delta_shape* shape, int64_t max_tokens,
     ctx->status = reinterpret_cast<int32_t*>(b + L.off_status);
     ctx->counter = reinterpret_cast<unsigned*>(b + L.off_counter);
     ctx->scratch = reinterpret_cast<uint8_t*>(b + L.off_scratch);
+    ctx->parts = reinterpret_cast<uint8_t*>(b + L.off_parts);
     if (cudaMemset(ctx->status, 0, OFRL_STAT_WORDS * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
         cudaFree(ctx->base);
         delete ctx;

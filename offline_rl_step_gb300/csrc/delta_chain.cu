@@ -17,6 +17,8 @@
 // intermediate through TMEM and a CTA-wide hand-over per product, four per
 // chunk, for 64-column tiles.
 
+#include <cmath>
+
 #include "delta_mma.cuh"
 
 namespace ofrl {
@@ -43,6 +45,11 @@ struct ChainArgs {
     uint8_t* vec_img;        // per (slot, head): U (forward) or R (backward)
     float* state_unit;       // [slot][head]: their powers of two
     float* vec_unit;
+    // forward over parts of an episode (segments > 1)
+    int32_t segments;
+    float* seg_state;        // [episode][head][segments][v_dim][k_dim] states at the parts' starts
+    uint8_t* seg_map;        // [episode][head][segments] images of the parts' maps, two planes
+    float* seg_unit;         // [episode][head][segments][8] their powers of two per 16 rows
     unsigned* counter;       // backward: zeroed for the gradient kernel
     int32_t* status;
 };
@@ -180,21 +187,31 @@ __device__ __forceinline__ void store_state(float* to, const float (&s)[NT][4], 
 
 struct Work {
     int e, head, khead, row0;      // row0: the CTA's first value channel
-    Span sp;
+    int seg;
+    Span sp;                       // of the CTA's part of the episode
     int chunks;
     int64_t slot0;
 };
-__device__ __forceinline__ Work work_of(const ChainArgs& a, int width) {
+// A CTA's rows, part, head and episode, rows changing fastest.
+__device__ __forceinline__ Work work_of(const ChainArgs& a, int slices, int width, int segments, int in_all) {
     Work w;
-    const int hv = a.shape.v_heads, slices = (a.shape.v_dim + width - 1) / width;
+    const int hv = a.shape.v_heads;
     w.row0 = blockIdx.x % slices * width;
-    const int64_t item = blockIdx.x / slices;
+    w.seg = blockIdx.x / slices % segments;
+    const int64_t item = blockIdx.x / slices / segments;
     w.e = (int)(item / hv);
     w.head = (int)(item % hv);
     w.khead = w.head / (hv / a.shape.k_heads);
     w.sp = span_of(a.ends, w.e, (int32_t)a.in.tokens);
     w.chunks = (w.sp.len + kChunk - 1) / kChunk;
     w.slot0 = w.sp.start / kChunk + w.e;
+    if (in_all > 1) {      // the episode's chunks in equal parts, the last ones perhaps empty
+        const int per = (w.chunks + in_all - 1) / in_all, from = min(w.seg * per, w.chunks);
+        w.chunks = min(per, w.chunks - from);
+        w.sp.start += from * kChunk;
+        w.sp.len = min(w.sp.len - from * kChunk, w.chunks * kChunk);
+        w.slot0 += from;
+    }
     return w;
 }
 
@@ -334,18 +351,30 @@ __device__ __forceinline__ void update_state(float (&s)[DK / 8][4], float keep, 
 template <int NW>
 constexpr int min_ctas() { return NW == 4 ? 2 : 1; }
 
-// NM: planes of S, X, U (and of T and P).  SAVE: S and U go to images for the
+// What a forward pass leaves.  kOutputs: outputs, of a whole episode or of a
+// part that starts from seg_state.  kSave: also S and U as images for the
 // backward pass; the CTA then has every value channel, so that an image has
-// one power of two.
-template <typename T, int DK, int NM, int NW, bool SAVE>
+// one power of two.  kSummary: of a part, no outputs but what it does to any
+// state before it, S -> S M + B: the recurrence is linear, so B is its end
+// from the zero state and the rows of M are its ends from the unit vectors
+// with v = 0.  The value channels and after them the rows of M are the
+// pass's rows.  The first part starts from the episode's own state and needs
+// no M.
+enum Pass { kOutputs, kSave, kSummary };
+
+// NM: planes of S, X, U (and of T and P).
+template <typename T, int DK, int NM, int NW, int PASS>
 __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(const __grid_constant__ ChainArgs a) {
     using St = Stage<T, DK, NM, NW>;
     constexpr int NT = St::NT, CG = DK / 8, KS = DK / 16;
     constexpr int NO = NT;      // planes of the operands that only the outputs see, and of the saved images
+    constexpr bool SAVE = PASS == kSave, SUMMARY = PASS == kSummary;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Work w = work_of(a, NW * 16);
+    const int v_pad = (a.shape.v_dim + NW * 16 - 1) / (NW * 16) * (NW * 16);
+    const Work w = work_of(a, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
+                           a.segments);
     ring_init<NW>(ring);
     uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
     {
@@ -354,8 +383,21 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
         const int64_t states = ((int64_t)w.e * hv + w.head) * dv * dk;
         float S[DK / 8][4];
         copy_rows<St, T>(a, w, mine, 0, row0);
-        load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
-        pdl_wait();      // what the preparing kernel leaves
+        const int64_t part = ((int64_t)w.e * hv + w.head) * a.segments + w.seg;
+        // the summaries keep a copy of the first part's start: the last part of
+        // the pass that follows may write the caller's buffer it came from
+        const bool given = SUMMARY ? w.seg == 0 : a.segments == 1;
+        if (given) load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
+        pdl_wait();      // what the launch before leaves
+        if (!given) load_state(SUMMARY ? nullptr : a.seg_state + part * dv * dk, S, row0, dv, dk);
+        if (SUMMARY && given && row0 < v_pad) store_state(a.seg_state + part * dv * dk, S, row0, dv, dk);
+        if (SUMMARY && row0 >= v_pad)
+#pragma unroll
+            for (int t = 0; t < DK / 8; ++t)
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    S[t][z] = row0 - v_pad + (lane >> 2) + (z >> 1) * 8 == t * 8 + (lane & 3) * 2 + (z & 1) ? 1.0f : 0.0f;
+        if (SUMMARY && w.seg == 0 && w.row0 >= v_pad) return;
         if (warp == 0)
             for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n);
         for (int c = 0; c < w.chunks; ++c) {
@@ -363,7 +405,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
             copy_rows<St, T>(a, w, mine + ((c + 1) & 1) * St::kRows, c + 1, row0);
             if (St::kCount == 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c);
             stage_ready(ring, st, c / St::kCount);
-            if (!SAVE && row0 >= dv) {
+            if (PASS == kOutputs && row0 >= dv) {
                 if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
                 continue;
             }
@@ -385,7 +427,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                 gemm<KS, 8, NM, NT, false>(X, f, kimg, St::kKey, CG, 0);
                 uint32_t f0[NO][KS][4];
                 first_planes(f, f0);
-                gemm<KS, 8, NO, NT, false>(O, f0, qimg, St::kKey, CG, 0);
+                if constexpr (!SUMMARY) gemm<KS, 8, NO, NT, false>(O, f0, qimg, St::kKey, CG, 0);
                 if constexpr (SAVE) {
                     const int64_t plane = (int64_t)NW * 16 * DK * 2;
                     store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NO * plane, plane, f0, row0 / 8, NW * 2);
@@ -424,7 +466,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
 #pragma unroll
                 for (int z = 0; z < 4; ++z) X[t][z] = U[t][z] * f[z & 1];
             }
-            {
+            if constexpr (!SUMMARY) {
                 uint32_t f[NO][4][4];
                 to_frags<NO>(U, u_f, f);
                 if constexpr (SAVE) {
@@ -435,13 +477,15 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                 zero(U);
                 gemm<4, 8, NO, NO, false>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
             }
-            const float p_inv = u_inv * (1.0f / kPScale);
+            if constexpr (!SUMMARY) {
+                const float p_inv = u_inv * (1.0f / kPScale);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const float2 os = vec2(vec, V_OS, t), qs = vec2(vec, V_QS, t);
-                const float f[2] = {os.x * s_inv, os.y * s_inv}, g[2] = {qs.x * p_inv, qs.y * p_inv};
+                for (int t = 0; t < 8; ++t) {
+                    const float2 os = vec2(vec, V_OS, t), qs = vec2(vec, V_QS, t);
+                    const float f[2] = {os.x * s_inv, os.y * s_inv}, g[2] = {qs.x * p_inv, qs.y * p_inv};
 #pragma unroll
-                for (int z = 0; z < 4; ++z) O[t][z] = f[z & 1] * O[t][z] + g[z & 1] * U[t][z];
+                    for (int z = 0; z < 4; ++z) O[t][z] = f[z & 1] * O[t][z] + g[z & 1] * U[t][z];
+                }
             }
             {
                 uint32_t f[NM][4][4];
@@ -450,12 +494,24 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
             }
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
-            if (row0 < dv)
+            if (!SUMMARY && row0 < dv)
                 store_transposed<T>(O, static_cast<T*>(a.out) + ((int64_t)w.sp.start + c * kChunk) * a.out_stride +
                                            (int64_t)w.head * dv + row0,
                                     a.out_stride, rows, dv - row0, mine + 2 * St::kRows);
         }
-        if (a.last) store_state(a.last + states, S, row0, dv, dk);
+        if (SUMMARY) {
+            if (row0 < v_pad) {
+                store_state(a.seg_state + (part + 1) * dv * dk, S, row0, dv, dk);
+            } else {
+                const float up = scale_up(tile_max(S));
+                uint32_t f[2][KS][4];
+                to_frags<2>(S, up, f);
+                store_image<CG>(a.seg_map + part * 2 * DK * DK * 2, DK * DK * 2, f, (row0 - v_pad) / 8, CG);
+                if (lane == 0) a.seg_unit[part * 8 + (row0 - v_pad) / 16] = pow2_inv(up);
+            }
+        } else if (a.last && w.seg == a.segments - 1) {
+            store_state(a.last + states, S, row0, dv, dk);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
@@ -469,7 +525,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Work w = work_of(a, NW * 16);
+    const Work w = work_of(a, 1, NW * 16, 1, 1);
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     ring_init<NW>(ring);
@@ -584,10 +640,76 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
 }
 
+// The parts' starts from their summaries, in order: S_{g+1} = S_g M_g + B_g,
+// where seg_state holds B_g at g + 1 before and S_{g+1} after.  A warp has 16
+// rows of S; M_g's two planes come through shared memory, copied a part ahead.
+template <int DK>
+struct Join {
+    static constexpr int kMap = 2 * DK * DK * 2;
+    static constexpr int kShared = 2 * kMap;
+};
+template <int DK>
+__global__ void __launch_bounds__(128) delta_join_kernel(const __grid_constant__ ChainArgs a) {
+    constexpr int CG = DK / 8, KS = DK / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5;
+    const int dk = a.shape.k_dim, dv = a.shape.v_dim;
+    const int slices = (dv + 63) / 64;
+    const int64_t item = blockIdx.x / slices;      // episode and head
+    const int row0 = blockIdx.x % slices * 64 + warp * 16;
+    auto copy = [&](int g) {
+        if (g < a.segments - 1) {
+            const uint8_t* from = a.seg_map + (item * a.segments + g) * Join<DK>::kMap;
+            const uint32_t to = umma::smem_u32(smem) + (g & 1) * Join<DK>::kMap;
+            for (int i = threadIdx.x * 16; i < Join<DK>::kMap; i += 128 * 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i), "l"(from + i) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    pdl_trigger();
+    pdl_wait();
+    copy(1);
+    float S[DK / 8][4];
+    load_state(a.seg_state + (item * a.segments + 1) * dv * dk, S, row0, dv, dk);
+    for (int g = 1; g < a.segments - 1; ++g) {
+        copy(g + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        float* to = a.seg_state + (item * a.segments + g + 1) * dv * dk;
+        const float* unit = a.seg_unit + (item * a.segments + g) * 8;
+        float N[DK / 8][4];
+        load_state(to, N, row0, dv, dk);
+        // the maps' units belong to their rows, S's columns
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const float u = unit[k];
+#pragma unroll
+            for (int t = 2 * k; t < 2 * k + 2; ++t)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) S[t][z] *= u;
+        }
+        const float up = scale_up(tile_max(S)), inv = pow2_inv(up);
+        uint32_t f[2][KS][4];
+        to_frags<2>(S, up, f);
+        const uint32_t map = umma::smem_u32(smem) + (g & 1) * Join<DK>::kMap;
+#pragma unroll
+        for (int t = 0; t < DK / 8; t += 4) {
+            float d[4][4];
+            zero(d);
+            gemm<KS, 4, 2, 2, true>(d, f, map, DK * DK * 2, CG, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) S[t + i][z] = N[t + i][z] + inv * d[i][z];
+        }
+        store_state(to, S, row0, dv, dk);
+        __syncthreads();
+    }
+}
+
 template <typename K>
-cudaError_t go(K kernel, int nw, int smem, bool early, const ChainArgs& c, cudaStream_t st) {
-    const int slices = (c.shape.v_dim + nw * 16 - 1) / (nw * 16);
-    const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * slices;
+cudaError_t go(K kernel, int nw, int smem, bool early, int per_head, const ChainArgs& c, cudaStream_t st) {
+    const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * per_head;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(kernel);
@@ -599,16 +721,26 @@ cudaError_t go(K kernel, int nw, int smem, bool early, const ChainArgs& c, cudaS
 
 template <typename T, int DK, int NM>
 cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
-    if (!c.state_img) return go(delta_forward_kernel<T, DK, NM, 4, false>, 4, Stage<T, DK, NM, 4>::kShared, true, c, st);
-    return c.shape.v_dim > 64
-               ? go(delta_forward_kernel<T, DK, NM, 8, true>, 8, Stage<T, DK, NM, 8>::kShared, true, c, st)
-               : go(delta_forward_kernel<T, DK, NM, 4, true>, 4, Stage<T, DK, NM, 4>::kShared, true, c, st);
+    using S4 = Stage<T, DK, NM, 4>;
+    const int slices = (c.shape.v_dim + 63) / 64;
+    if (c.state_img)
+        return c.shape.v_dim > 64
+                   ? go(delta_forward_kernel<T, DK, NM, 8, kSave>, 8, Stage<T, DK, NM, 8>::kShared, true, 1, c, st)
+                   : go(delta_forward_kernel<T, DK, NM, 4, kSave>, 4, S4::kShared, true, 1, c, st);
+    if (c.segments > 1) {
+        cudaError_t e = go(delta_forward_kernel<T, DK, NM, 4, kSummary>, 4, S4::kShared, true,
+                           (slices + DK / 64) * (c.segments - 1), c, st);
+        if (e == cudaSuccess && c.segments > 2)
+            e = go(delta_join_kernel<DK>, 4, Join<DK>::kShared, true, slices, c, st);
+        if (e != cudaSuccess) return e;
+    }
+    return go(delta_forward_kernel<T, DK, NM, 4, kOutputs>, 4, S4::kShared, true, slices * c.segments, c, st);
 }
 template <typename T, int DK>
 cudaError_t reverse(const ChainArgs& c, cudaStream_t st) {
     constexpr int NM = sizeof(T) == 4 ? 2 : 1;
-    return c.shape.v_dim > 64 ? go(delta_reverse_kernel<T, DK, 8>, 8, Stage<T, DK, NM, 8>::kShared, false, c, st)
-                              : go(delta_reverse_kernel<T, DK, 4>, 4, Stage<T, DK, NM, 4>::kShared, false, c, st);
+    return c.shape.v_dim > 64 ? go(delta_reverse_kernel<T, DK, 8>, 8, Stage<T, DK, NM, 8>::kShared, false, 1, c, st)
+                              : go(delta_reverse_kernel<T, DK, 4>, 4, Stage<T, DK, NM, 4>::kShared, false, 1, c, st);
 }
 
 ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
@@ -623,6 +755,10 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
     c.vec_img = img.vec;
     c.state_unit = img.state_unit;
     c.vec_unit = img.vec_unit;
+    c.segments = 1;
+    c.seg_state = nullptr;
+    c.seg_map = nullptr;
+    c.seg_unit = nullptr;
     c.counter = a.counter;
     c.status = a.status;
     return c;
@@ -630,8 +766,36 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
 
 }  // namespace
 
+// Parts of an episode.  A forward pass takes one CTA per head and 64 value
+// channels; where these leave most SMs idle and episodes are long, each is cut
+// into parts: summaries of all parts at once, the short chain over them, then
+// all parts at once.  That is about 1.7 times the work and a step of the chain
+// over parts costs about 0.4 chunks' time, so n chunks in g parts take about
+// 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, if the SMs hold as
+// many summaries (two CTAs each).  One sequence of 32768 tokens, four heads of
+// 128: 2100 us whole, see the table of cases for the time in parts.
+int segments_of(const SeqLaunch& a) {
+    const int64_t items = (int64_t)a.episodes * a.shape.v_heads;
+    const int rows = (a.shape.v_dim + 63) / 64 + (a.shape.k_dim + 63) / 64;
+    const double chunks = (double)a.in.tokens / kChunk / a.episodes;
+    const int64_t room = 2 * (int64_t)a.num_sms / (items * rows) + 1;
+    const int64_t best = (int64_t)(2.0 * std::sqrt(chunks));
+    const int64_t g = best < room ? best : room;
+    return g >= 4 && chunks >= 12.0 ? (int)g : 1;
+}
+
 cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Images& img, int planes, cudaStream_t st) {
     ChainArgs c = base_args(a, p, img);
+    if (!a.saved) {
+        c.segments = segments_of(a);
+        const int dkp = pad_dim(a.shape.k_dim);
+        const int64_t parts = (int64_t)a.episodes * a.shape.v_heads * c.segments;
+        uint8_t* at = a.parts;
+        c.seg_state = reinterpret_cast<float*>(at);
+        at += (parts * a.shape.v_dim * a.shape.k_dim * 4 + 255) / 256 * 256;
+        c.seg_map = at;
+        c.seg_unit = reinterpret_cast<float*>(at + parts * 2 * dkp * dkp * 2);
+    }
     c.first = a.init;
     c.last = a.final_state;
     c.out = a.out;

@@ -207,6 +207,28 @@ def test_final_state_may_be_the_initial_one_and_tokens_past_the_last_end_stay():
     ctx.close()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", [([3000], 1, 2, 64, 64), ([2000, 0, 70, 1500], 1, 1, 128, 128),
+                                                 ([1000], 1, 1, 40, 104), ([5001], 2, 2, 128, 24)])
+def test_long_episodes(dtype, lengths, hk, hv, dk, dv):
+    """Few heads and long episodes: read in parts, with the states in one buffer that is replaced."""
+    import offline_rl_step_gb300 as ofrl
+    need_gpu()
+    d = inputs(lengths, hk, hv, dk, dv, seed=37, rnd=ROUND[dtype])
+    t, n = sum(lengths), len(lengths)
+    out, final = delta.forward(*[d[x] for x in NAMES], ends_of(lengths), 0.3, init=d["init"])
+    ctx = ofrl.DeltaRule(hk, hv, dk, dv, dtype, max_tokens=t, max_episodes=n, backward=False)
+    x, ends = [_dev(d[name], dtype) for name in NAMES], torch.from_numpy(ends_of(lengths)).cuda()
+    got = torch.full((t, hv, dv), float("nan"), device="cuda", dtype=DT[dtype])
+    state = _dev(d["init"])
+    ofrl.delta_forward(ctx, *x, ends, got, scale=0.3, init_state=state, final_state=state)
+    check(_host(got), out, BOUND[dtype], "out")
+    check(_host(state), final, STATE_BOUND, "final")
+    ofrl.delta_forward(ctx, *x, ends, got, scale=0.3, init_state=_dev(d["init"]))
+    check(_host(got), out, BOUND[dtype], "out alone")
+    ctx.close()
+
+
 def test_another_stream():
     import offline_rl_step_gb300 as ofrl
     need_gpu()
