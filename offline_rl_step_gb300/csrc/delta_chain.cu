@@ -641,22 +641,26 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
 }
 
 // The parts' starts from their summaries, in order: S_{g+1} = S_g M_g + B_g,
-// where seg_state holds B_g at g + 1 before and S_{g+1} after.  A warp has 16
-// rows of S; M_g's two planes come through shared memory, copied a part ahead.
+// where seg_state holds B_g at g + 1 before and S_{g+1} after.  A chain of one
+// product per part, so a CTA takes few rows and splits the columns: warp w
+// makes columns w DK / 4 .. of 16 rows, and the rows come together again
+// through shared memory.  M_g's two planes are copied a part ahead.
 template <int DK>
 struct Join {
     static constexpr int kMap = 2 * DK * DK * 2;
-    static constexpr int kShared = 2 * kMap;
+    static constexpr int kPitch = DK + 8;      // floats
+    static constexpr int kShared = 2 * kMap + 16 * kPitch * 4;
 };
 template <int DK>
 __global__ void __launch_bounds__(128) delta_join_kernel(const __grid_constant__ ChainArgs a) {
-    constexpr int CG = DK / 8, KS = DK / 16;
+    constexpr int CG = DK / 8, KS = DK / 16, NT = DK / 32, P = Join<DK>::kPitch;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int warp = threadIdx.x >> 5;
+    float* rows = reinterpret_cast<float*>(smem + 2 * Join<DK>::kMap);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row4 = lane >> 2, col2 = (lane & 3) * 2;
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
-    const int slices = (dv + 63) / 64;
+    const int slices = (dv + 15) / 16;
     const int64_t item = blockIdx.x / slices;      // episode and head
-    const int row0 = blockIdx.x % slices * 64 + warp * 16;
+    const int row0 = blockIdx.x % slices * 16;
     auto copy = [&](int g) {
         if (g < a.segments - 1) {
             const uint8_t* from = a.seg_map + (item * a.segments + g) * Join<DK>::kMap;
@@ -666,44 +670,73 @@ __global__ void __launch_bounds__(128) delta_join_kernel(const __grid_constant__
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // this warp's tiles of a state: rows row4, row4 + 8, columns (warp NT + t) 8 + col2
+    auto load = [&](int g, float (&x)[NT][4]) {
+        const float* from = a.seg_state + (item * a.segments + g) * dv * dk;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = row0 + row4 + 8 * h, c = (warp * NT + t) * 8 + col2;
+                float2 v = make_float2(0.0f, 0.0f);
+                if (r < dv && c < dk) v = *reinterpret_cast<const float2*>(from + (int64_t)r * dk + c);
+                x[t][2 * h] = v.x;
+                x[t][2 * h + 1] = v.y;
+            }
+    };
+    auto share = [&](const float (&x)[NT][4]) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(rows + (row4 + 8 * h) * P + (warp * NT + t) * 8 + col2) =
+                    make_float2(x[t][2 * h], x[t][2 * h + 1]);
+    };
     pdl_trigger();
     pdl_wait();
     copy(1);
-    float S[DK / 8][4];
-    load_state(a.seg_state + (item * a.segments + 1) * dv * dk, S, row0, dv, dk);
+    float N[NT][4];
+    load(1, N);
+    share(N);
+    load(2, N);
     for (int g = 1; g < a.segments - 1; ++g) {
         copy(g + 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        float* to = a.seg_state + (item * a.segments + g + 1) * dv * dk;
         const float* unit = a.seg_unit + (item * a.segments + g) * 8;
-        float N[DK / 8][4];
-        load_state(to, N, row0, dv, dk);
-        // the maps' units belong to their rows, S's columns
+        float S[DK / 8][4];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            const float u = unit[k];
+        for (int t = 0; t < DK / 8; ++t) {      // the maps' units belong to their rows, S's columns
+            const float u = unit[t / 2];
 #pragma unroll
-            for (int t = 2 * k; t < 2 * k + 2; ++t)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) S[t][z] *= u;
+            for (int h = 0; h < 2; ++h) {
+                const float2 v = *reinterpret_cast<const float2*>(rows + (row4 + 8 * h) * P + t * 8 + col2);
+                S[t][2 * h] = v.x * u;
+                S[t][2 * h + 1] = v.y * u;
+            }
         }
         const float up = scale_up(tile_max(S)), inv = pow2_inv(up);
         uint32_t f[2][KS][4];
         to_frags<2>(S, up, f);
-        const uint32_t map = umma::smem_u32(smem) + (g & 1) * Join<DK>::kMap;
+        float d[NT][4];
+        zero(d);
+        gemm<KS, NT, 2, 2, true>(d, f, umma::smem_u32(smem) + (g & 1) * Join<DK>::kMap, DK * DK * 2, CG, warp * NT);
 #pragma unroll
-        for (int t = 0; t < DK / 8; t += 4) {
-            float d[4][4];
-            zero(d);
-            gemm<KS, 4, 2, 2, true>(d, f, map, DK * DK * 2, CG, t);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int z = 0; z < 4; ++z) d[t][z] = N[t][z] + inv * d[t][z];
+        if (g + 2 < a.segments) load(g + 2, N);
+        float* to = a.seg_state + (item * a.segments + g + 1) * dv * dk;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) S[t + i][z] = N[t + i][z] + inv * d[i][z];
-        }
-        store_state(to, S, row0, dv, dk);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = row0 + row4 + 8 * h, c = (warp * NT + t) * 8 + col2;
+                if (r < dv && c < dk)
+                    *reinterpret_cast<float2*>(to + (int64_t)r * dk + c) = make_float2(d[t][2 * h], d[t][2 * h + 1]);
+            }
         __syncthreads();
+        share(d);
     }
 }
 
@@ -731,7 +764,7 @@ cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
         cudaError_t e = go(delta_forward_kernel<T, DK, NM, 4, kSummary>, 4, S4::kShared, true,
                            (slices + DK / 64) * (c.segments - 1), c, st);
         if (e == cudaSuccess && c.segments > 2)
-            e = go(delta_join_kernel<DK>, 4, Join<DK>::kShared, true, slices, c, st);
+            e = go(delta_join_kernel<DK>, 4, Join<DK>::kShared, true, (c.shape.v_dim + 15) / 16, c, st);
         if (e != cudaSuccess) return e;
     }
     return go(delta_forward_kernel<T, DK, NM, 4, kOutputs>, 4, S4::kShared, true, slices * c.segments, c, st);

@@ -74,13 +74,10 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
     const int khead = blockIdx.x % hk;
     __shared__ int s_at[3];
     if (warp == 0) {
-        const int32_t tokens = (int32_t)a.in.tokens;
-        const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)slot);
-        const Span sp = span_of(a.ends, e, tokens);
-        const int c = (int)slot - (sp.start / kChunk + e);
+        const Chunk c = chunk_of(a.ends, a.episodes, (int32_t)a.in.tokens, (int32_t)slot);
         if (lane == 0) {
-            s_at[0] = sp.start + c * kChunk;
-            s_at[1] = c < 0 ? 0 : min(sp.len - c * kChunk, kChunk);
+            s_at[0] = (int)c.tok;
+            s_at[1] = c.rows;
             s_at[2] = 0;
             umma::mbar_init(&bar_keys, 1);
             umma::mbar_init(&bar_head, 1);

@@ -141,12 +141,9 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             if (n >= a.items) break;
             it.slot = n / (unsigned)hk;
             it.khead = (int)(n % (unsigned)hk);
-            const int32_t tokens = (int32_t)a.in.tokens;
-            const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)it.slot);
-            const Span sp = span_of(a.ends, e, tokens);
-            const int c = (int)it.slot - (sp.start / kChunk + e);
-            it.rows = c < 0 ? 0 : min(sp.len - c * kChunk, kChunk);
-            it.tok = (int64_t)sp.start + c * kChunk;
+            const Chunk c = chunk_of(a.ends, a.episodes, (int32_t)a.in.tokens, (int32_t)it.slot);
+            it.rows = c.rows;
+            it.tok = c.tok;
             if (it.rows > 0) break;
             it.rows = 0;
         }

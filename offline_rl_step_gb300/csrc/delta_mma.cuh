@@ -243,25 +243,36 @@ cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Im
 cudaError_t launch_grad_tc(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
 cudaError_t launch_grad(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
 
-// Episode of a slot: the last e with start(e) / 64 + e <= slot, by a 32-ary
-// search of one warp.
-__device__ __forceinline__ int episode_of(const int32_t* ends, int32_t episodes, int32_t tokens, int32_t slot) {
+// The chunk of a slot.
+struct Chunk {
+    int64_t tok;      // its first token
+    int rows;         // its tokens; 0: the slot is unused
+};
+
+// By one whole warp: the episode of slot s is the last e with start(e) / 64 +
+// e <= s, found by a 32-ary search.  Lanes of the last round hold neighbouring
+// episodes' starts, so the episode's range comes along with it.
+__device__ __forceinline__ Chunk chunk_of(const int32_t* ends, int32_t episodes, int32_t tokens, int32_t slot) {
     const int lane = threadIdx.x & 31;
     int lo = 0, n = episodes;      // the answer lies in [lo, lo + n)
-    while (n > 1) {
+    int32_t start;
+    int last;
+    while (true) {
         const int step = (n + 31) / 32;
         const int e = lo + lane * step;
-        bool below = false;
-        if (lane * step < n) {
-            const int32_t start = e > 0 ? min(max(ends[e - 1], 0), tokens) : 0;
-            below = start / kChunk + e <= slot;
-        }
-        const unsigned hits = __ballot_sync(0xffffffffu, below);
-        const int last = hits ? 31 - __clz(hits) : 0;
+        const bool in = lane * step < n;
+        start = in && e > 0 ? min(max(ends[e - 1], 0), tokens) : 0;
+        const unsigned hits = __ballot_sync(0xffffffffu, in && start / kChunk + e <= slot);
+        last = hits ? 31 - __clz(hits) : 0;
         lo += last * step;
+        if (step == 1) break;
         n = min(step, n - last * step);
     }
-    return lo;
+    const int32_t from = __shfl_sync(0xffffffffu, start, last), next = __shfl_sync(0xffffffffu, start, (last + 1) & 31);
+    const int32_t end = last + 1 < n ? next : ends[lo];
+    const int32_t to = min(max(end, from), tokens);
+    const int c = slot - (from / kChunk + lo);
+    return {(int64_t)from + c * kChunk, c < 0 ? 0 : min(to - from - c * kChunk, kChunk)};
 }
 
 }  // namespace delta

@@ -128,21 +128,19 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < a.episodes; e += kPrepThreads)
             if (span_bad(a.ends, e, tokens)) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, 1);
-    const int e = episode_of(a.ends, a.episodes, tokens, (int32_t)slot);      // by every warp
-    const Span sp = span_of(a.ends, e, tokens);
-    const int chunk = (int)slot - (sp.start / kChunk + e);
-    const int rows = chunk < 0 ? 0 : min(sp.len - chunk * kChunk, kChunk);
+    const Chunk at = chunk_of(a.ends, a.episodes, tokens, (int32_t)slot);      // by every warp
+    const int rows = at.rows;
     if (rows <= 0) return;
-    const int64_t tok = (int64_t)sp.start + chunk * kChunk;
+    const int64_t tok = at.tok;
 
-    float gin[2] = {0.0f, 0.0f}, bin[2] = {0.0f, 0.0f};      // first warp: tokens 2 lane, + 1
+    T gin[2], bin[2];      // first warp: tokens 2 lane, + 1 (past the end: the last one's, not used)
     if (warp == 0)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (2 * lane + i < rows) {
-                gin[i] = to_f(static_cast<const T*>(a.in.g)[(tok + 2 * lane + i) * a.in.g_stride + head]);
-                bin[i] = to_f(static_cast<const T*>(a.in.beta)[(tok + 2 * lane + i) * a.in.beta_stride + head]);
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int64_t t = tok + min(2 * lane + i, rows - 1);
+            gin[i] = static_cast<const T*>(a.in.g)[t * a.in.g_stride + head];
+            bin[i] = static_cast<const T*>(a.in.beta)[t * a.in.beta_stride + head];
+        }
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
     // group, so that a store of 8 lanes fills one 8x8 block.  All of a warp's
@@ -158,23 +156,23 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
         Raw<T> raw[kBatch][CG / 4];
 #pragma unroll
         for (int w = 0; w < kBatch; ++w) {
-            const int row = (warp * 2 + (w & 1)) * 8 + r;
-            const bool isq = w0 + w >= 2;
+            const int row = min((warp * 2 + (w & 1)) * 8 + r, rows - 1);      // rows and columns that are not there
+            const bool isq = w0 + w >= 2;                                     // become zero below
             const T* p = isq ? static_cast<const T*>(a.in.q) + (tok + row) * a.in.q_stride + (int64_t)khead * dk
                              : static_cast<const T*>(a.in.k) + (tok + row) * a.in.k_stride + (int64_t)khead * dk;
 #pragma unroll
             for (int i = 0; i < CG / 4; ++i) {
                 const int col = (c4 + 4 * i) * 8;
-                if (row < rows && col < dk)
-                    raw[w][i].load(p + col);
-                else
-                    raw[w][i].clear();
+                raw[w][i].load(p + (col < dk ? col : 0));
             }
         }
         if (w0 == 0 && warp == 0) {
             Two g[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) g[i] = two_log2(gin[i] < kMinLogDecay ? kMinLogDecay : gin[i]);      // a NaN stays
+            for (int i = 0; i < 2; ++i) {
+                const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
+                g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
+            }
             Two sum = two_add(g[0], g[1]);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -194,6 +192,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
             float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < CG / 4; ++i) {
+                if (rg * 8 + r >= rows || (c4 + 4 * i) * 8 >= dk) raw[w][i].clear();
                 float x[8];
                 raw[w][i].get(x);
 #pragma unroll
@@ -227,7 +226,8 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
             const float gam = exp2f(G[i].h + G[i].l), rest = exp2f((total.h - G[i].h) + (total.l - G[i].l));
-            const float bk = bin[i] * kap[t] * kap[t], qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
+            const float b = t < rows ? to_f(bin[i]) : 0.0f;
+            const float bk = b * kap[t] * kap[t], qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
             vec[V_GHI * kChunk + t] = G[i].h;
             vec[V_GLO * kChunk + t] = G[i].l;
             vec[V_GAM * kChunk + t] = gam;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
             vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
             vec[V_QS * kChunk + t] = qs;
             vec[V_OS * kChunk + t] = qs * gam;
-            vec[V_DV * kChunk + t] = bin[i] * kap[t];
+            vec[V_DV * kChunk + t] = b * kap[t];
             vec[V_DS * kChunk + t] = bk * gam;
             most = fmaxf(most, rest);
         }
