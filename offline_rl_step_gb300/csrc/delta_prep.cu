@@ -109,7 +109,7 @@ struct PrepShared {
 
 // T: token type; DK: padded key width; NM: planes of T and P.
 template <typename T, int DK, int NM>
-__global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kernel(const __grid_constant__ PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kernel(const __grid_constant__ PrepArgs a) {
     using Sh = PrepShared<T, DK, NM>;
     constexpr int NT = Sh::NT, NB = Sh::NB, CG = DK / 8, KS = DK / 16, kKey = Sh::kKey, kPitch = Sh::kPitch;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -133,23 +133,20 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
     if (rows <= 0) return;
     const int64_t tok = at.tok;
 
-    T gin[2], bin[2];      // first warp: tokens 2 lane, + 1 (past the end: the last one's, not used)
-    if (warp == 0)
+    T gin[2], bin[2];      // tokens 2 lane, + 1 (past the end: the last one's, not used), in every warp
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t t = tok + min(2 * lane + i, rows - 1);
-            gin[i] = static_cast<const T*>(a.in.g)[t * a.in.g_stride + head];
-            bin[i] = static_cast<const T*>(a.in.beta)[t * a.in.beta_stride + head];
-        }
+    for (int i = 0; i < 2; ++i) {
+        const int64_t t = tok + min(2 * lane + i, rows - 1);
+        gin[i] = static_cast<const T*>(a.in.g)[t * a.in.g_stride + head];
+        bin[i] = static_cast<const T*>(a.in.beta)[t * a.in.beta_stride + head];
+    }
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
     // group, so that a store of 8 lanes fills one 8x8 block.  All of a warp's
-    // loads (of a half of them, for fp32) go out before the first is used, and
-    // the first warp adds up its log decays while they are under way.
-    Two G[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, total = {0.0f, 0.0f};
+    // loads (of a half of them, where registers are short) go out before the first is used.
     uint8_t* keys = a.keys + (slot * hk + khead) * KeyImage::bytes(DK, NT);
     const bool leave = head % group == 0;
-    constexpr int kBatch = NT == 1 ? 4 : 2;
+    constexpr int kBatch = NT * DK > 64 ? 2 : 4;      // registers
 #pragma unroll
     for (int w0 = 0; w0 < 4; w0 += kBatch) {
         const int r = lane & 7, c4 = lane >> 3;
@@ -165,25 +162,6 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
                 const int col = (c4 + 4 * i) * 8;
                 raw[w][i].load(p + (col < dk ? col : 0));
             }
-        }
-        if (w0 == 0 && warp == 0) {
-            Two g[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
-                g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
-            }
-            Two sum = two_add(g[0], g[1]);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
-                if (lane >= o) sum = two_add(up, sum);
-            }
-            total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
-            Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
-            if (lane == 0) before = {0.0f, 0.0f};
-            G[0] = two_add(before, g[0]);
-            G[1] = sum;
         }
 #pragma unroll
         for (int w = 0; w < kBatch; ++w) {
@@ -220,99 +198,129 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 4 : 3) delta_prep_kern
         }
     }
     __syncthreads();
-    if (warp == 0) {
-        float most = 1.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            const float gam = exp2f(G[i].h + G[i].l), rest = exp2f((total.h - G[i].h) + (total.l - G[i].l));
-            const float b = t < rows ? to_f(bin[i]) : 0.0f;
-            const float bk = b * kap[t] * kap[t], qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
-            vec[V_GHI * kChunk + t] = G[i].h;
-            vec[V_GLO * kChunk + t] = G[i].l;
-            vec[V_GAM * kChunk + t] = gam;
-            vec[V_REST * kChunk + t] = rest;
-            vec[V_BETA * kChunk + t] = bk;
-            vec[V_KINV * kChunk + t] = pow2_inv(kap[t]);
-            vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
-            vec[V_QS * kChunk + t] = qs;
-            vec[V_OS * kChunk + t] = qs * gam;
-            vec[V_DV * kChunk + t] = b * kap[t];
-            vec[V_DS * kChunk + t] = bk * gam;
-            most = fmaxf(most, rest);
-        }
-        most = warp_max(most);
-        if (lane == 0) vec[V_MISC * kChunk] = most;
-    }
-
     // K K^T rows of block `warp`, Q K^T rows of block 3 - warp: five 16x16
     // blocks on or below the diagonal for every warp.
     const int rk = warp, rq = 3 - warp;
     const int m4 = lane >> 3, r8 = lane & 7;
-    float kk[8][4], qk[8][4];
-    zero(kk);
-    zero(qk);
-    {
-        const uint32_t kb = umma::smem_u32(kimg), qb = umma::smem_u32(qimg);
+    const uint32_t kb = umma::smem_u32(kimg), qb = umma::smem_u32(qimg);
+    auto product = [&](float (&x)[8][4], uint32_t from, int rg) {      // rows of block rg of an image times K^T
+        zero(x);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            uint32_t fk[NT][4], fq[NT][4];
+            uint32_t fa[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {   // A operands: row halves (m4 & 1), k halves (m4 >> 1)
-                const int at = n * kKey + ((2 * rk + (m4 & 1)) * CG + 2 * k + (m4 >> 1)) * kTile + r8 * 16;
-                ldsm4(fk[n], kb + at);
-                ldsm4(fq[n], qb + at + 2 * (rq - rk) * CG * kTile);
-            }
+            for (int n = 0; n < NT; ++n)      // row halves (m4 & 1), k halves (m4 >> 1)
+                ldsm4(fa[n], from + n * kKey + ((2 * rg + (m4 & 1)) * CG + 2 * k + (m4 >> 1)) * kTile + r8 * 16);
 #pragma unroll
-            for (int t = 0; t < 8; t += 2)
+            for (int t = 0; t < 8; t += 2) {
+                if (t > 2 * rg) continue;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    if (t > 2 * rk && t > 2 * rq) continue;
                     uint32_t f[4];
                     ldsm4(f, kb + j * kKey + ((t + (m4 >> 1)) * CG + 2 * k + (m4 & 1)) * kTile + r8 * 16);
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
                         if (i + j < NT) {
-                            if (t <= 2 * rk) {
-                                mma_h(kk[t], fk[i], f[0], f[1]);
-                                mma_h(kk[t + 1], fk[i], f[2], f[3]);
-                            }
-                            if (t <= 2 * rq) {
-                                mma_h(qk[t], fq[i], f[0], f[1]);
-                                mma_h(qk[t + 1], fq[i], f[2], f[3]);
-                            }
+                            mma_h(x[t], fa[i], f[0], f[1]);
+                            mma_h(x[t + 1], fa[i], f[2], f[3]);
                         }
                 }
+            }
+        }
+    };
+    float qk[8][4];
+    product(qk, qb, rq);
+    {
+        // Running sums of the log decays, in every warp (the instructions fit
+        // between the products' latencies); a warp leaves the vectors of its 16
+        // tokens.
+        Two g[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
+            g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
+        }
+        Two sum = two_add(g[0], g[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+            const Two both = two_add(up, sum);
+            if (lane >= o) sum = both;
+        }
+        const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+        Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+        if (lane == 0) before = {0.0f, 0.0f};
+        const Two G[2] = {two_add(before, g[0]), sum};
+        float gam[2], rest[2], most = 1.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            gam[i] = exp2f(G[i].h + G[i].l);
+            rest[i] = exp2f((total.h - G[i].h) + (total.l - G[i].l));
+            most = fmaxf(most, rest[i]);
+        }
+        most = warp_max(most);
+        if ((lane >> 3) == warp) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const float b = t < rows ? to_f(bin[i]) : 0.0f, k = kap[t];
+                const float bk = b * k * k, qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
+                vec[V_GHI * kChunk + t] = G[i].h;
+                vec[V_GLO * kChunk + t] = G[i].l;
+                vec[V_GAM * kChunk + t] = gam[i];
+                vec[V_REST * kChunk + t] = rest[i];
+                vec[V_BETA * kChunk + t] = bk;
+                vec[V_KINV * kChunk + t] = pow2_inv(k);
+                vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
+                vec[V_QS * kChunk + t] = qs;
+                vec[V_OS * kChunk + t] = qs * gam[i];
+                vec[V_DV * kChunk + t] = b * k;
+                vec[V_DS * kChunk + t] = bk * gam[i];
+                if (t == 0) vec[V_MISC * kChunk] = most;
+            }
         }
     }
-    __syncthreads();      // the keys' place is free, the vectors are there
-
+    __syncthreads();      // the vectors are there
     const int row4 = lane >> 2, col2 = (lane & 3) * 2;
     uint8_t* pairs = a.pairs + (slot * hv + head) * kPairBytes;
     const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk, *beta = vec + V_BETA * kChunk;
-    // P to global memory; A's blocks below the diagonal as images, the
-    // diagonal block as floats, column by column
+    // P to global memory
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int ik = rk * 16 + row4 + 8 * h, iq = rq * 16 + row4 + 8 * h;
-        const float gk = ghi[ik], lk = glo[ik], bk = beta[ik], gq = ghi[iq], lq = glo[iq];
+        const int iq = rq * 16 + row4 + 8 * h;
+        const float gq = ghi[iq], lq = glo[iq];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const float2 gj = vec2(vec, V_GHI, t), lj = vec2(vec, V_GLO, t);
             float p[2] = {0.0f, 0.0f};
-            if (t <= 2 * rq + 1)
+            if (t <= 2 * rq + 1) {
+                const float2 gj = vec2(vec, V_GHI, t), lj = vec2(vec, V_GLO, t);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const float d = exp_2<NM>((gq - (z ? gj.y : gj.x)) + (lq - (z ? lj.y : lj.x))) * kPScale;
                     if (t * 8 + col2 + z <= iq) p[z] = qk[t][2 * h + z] * d;
                 }
+            }
             uint32_t pl[NM];
             planes_h<NM>(p[0], p[1], pl);
 #pragma unroll
             for (int n = 0; n < NM; ++n)
                 *reinterpret_cast<uint32_t*>(pairs + kSquare + n * kPairFirst + ((2 * rq + h) * 8 + t) * kTile + lane * 4) =
                     pl[n];
+        }
+    }
+    float kk[8][4];
+    product(kk, kb, rk);
+    __syncthreads();      // the keys' place is free
+    // A's blocks below the diagonal as images, the diagonal block as floats,
+    // column by column
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int ik = rk * 16 + row4 + 8 * h;
+        const float gk = ghi[ik], lk = glo[ik], bk = beta[ik];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
             if (t > 2 * rk + 1) continue;
+            const float2 gj = vec2(vec, V_GHI, t), lj = vec2(vec, V_GLO, t);
             float x[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z)
