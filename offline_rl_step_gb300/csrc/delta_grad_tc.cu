@@ -60,7 +60,8 @@ struct Lay {
     static constexpr int off_d = off_s + kState;
     static constexpr int off_k = off_d + kState;        // K^, Q^ of two items
     static constexpr int off_pem = off_k + 4 * kKey;    // PD, E, M: [8 column groups][24 row groups]
-    static constexpr int kPem = 8 * 24 * kTile;
+    static constexpr int kPem = 8 * 24 * kTile;          // (also where dq and dk are turned around)
+    static_assert(kPem >= 8 * 32 * 80, "staging");
     static constexpr int off_vec = off_pem + kPem;      // of two heads
     static constexpr int off_sum = off_vec + 2 * kVecBytes;
     static constexpr int kBytes = off_sum + (2 * 4 * kChunk + 2 * kChunk) * 4;
@@ -102,9 +103,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 __device__ __forceinline__ void mma_run(uint32_t d, uint32_t a, uint32_t a_lbo, uint32_t a_sbo, uint32_t a_step,
                                         uint32_t b, uint32_t b_lbo, uint32_t b_sbo, uint32_t b_step, uint32_t idesc,
                                         int steps, bool accumulate) {
-    for (int k = 0; k < steps; ++k)
-        umma::mma_f16(d, umma::smem_desc(a + k * a_step, a_lbo, a_sbo), umma::smem_desc(b + k * b_step, b_lbo, b_sbo),
-                      idesc, (accumulate || k > 0) ? 1u : 0u);
+    uint64_t da = umma::smem_desc(a, a_lbo, a_sbo), db = umma::smem_desc(b, b_lbo, b_sbo);
+#pragma unroll 4
+    for (int k = 0; k < steps; ++k) {      // the address field does not overflow: it holds 18 bits of bytes
+        umma::mma_f16(d, da, db, idesc, (accumulate || k > 0) ? 1u : 0u);
+        da += a_step >> 4;
+        db += b_step >> 4;
+    }
 }
 
 struct Item {
@@ -315,14 +320,31 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
         if (warp == 1 && last) find();
         // <S_0, dS_1> meanwhile: 8 elements of one row per turn
         float ss = 0.0f;
-        for (int x = threadIdx.x; x < blocks * 2 * CG * 8; x += kThreads) {
-            const uint4 s = reinterpret_cast<const uint4*>(smem + L::off_s)[x], d = reinterpret_cast<const uint4*>(smem + L::off_d)[x];
-            const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, dw[4] = {d.x, d.y, d.z, d.w};
+        {
+            constexpr int kAtOnce = 4;
+            const uint4 *ps = reinterpret_cast<const uint4*>(smem + L::off_s), *pd = reinterpret_cast<const uint4*>(smem + L::off_d);
+            float part[kAtOnce] = {};
+            for (int x0 = threadIdx.x; x0 < blocks * 2 * CG * 8; x0 += kAtOnce * kThreads) {
+                uint4 sv[kAtOnce], dv4[kAtOnce];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const float2 f = unpack_h(sw[z]), h = unpack_h(dw[z]);
-                ss += f.x * h.x + f.y * h.y;
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int x = x0 + k * kThreads;
+                    const bool in = x < blocks * 2 * CG * 8;
+                    sv[k] = in ? ps[x] : make_uint4(0, 0, 0, 0);
+                    dv4[k] = in ? pd[x] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const uint32_t sw[4] = {sv[k].x, sv[k].y, sv[k].z, sv[k].w}, dw[4] = {dv4[k].x, dv4[k].y, dv4[k].z, dv4[k].w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 f = unpack_h(sw[z]), h = unpack_h(dw[z]);
+                        part[k] += f.x * h.x + f.y * h.y;
+                    }
+                }
             }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) ss += part[k];
         }
         ss = warp_sum(ss);
 
@@ -521,17 +543,33 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
                         __float2bfloat16_rn(total - (z ? before + dG[0] : before));
             }
         }
-        if (last && !dead && i < it.rows) {
+        if (last && !dead) {
+            // 32 rows of 32 channels at a time, turned around in shared memory
+            // (what IN and COL read is done with) for whole sectors
             const float f = vec[(isk ? V_KINV : V_QINV) * kChunk + i];
-            __nv_bfloat16* to = isk ? static_cast<__nv_bfloat16*>(a.grads.dk) + (it.tok + i) * a.grads.k_stride
-                                    : static_cast<__nv_bfloat16*>(a.grads.dq) + (it.tok + i) * a.grads.q_stride;
-            to += (int64_t)it.khead * dk + half * H;
+            uint8_t* stage = pem + warp * 32 * 80;
+            const int64_t stride = isk ? a.grads.k_stride : a.grads.q_stride;
+            const int row0 = (warp & 1) * 32;      // token of the warp's first row
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(isk ? a.grads.dk : a.grads.dq) + (it.tok + row0) * stride +
+                                (int64_t)it.khead * dk + half * H;
 #pragma unroll
-            for (int c = 0; c < H; c += 8)
-                if (half * H + c < dk)
-                    *reinterpret_cast<uint4*>(to + c) =
-                        make_uint4(pack_b(acc[c] * f, acc[c + 1] * f), pack_b(acc[c + 2] * f, acc[c + 3] * f),
-                                   pack_b(acc[c + 4] * f, acc[c + 5] * f), pack_b(acc[c + 6] * f, acc[c + 7] * f));
+            for (int c0 = 0; c0 < H; c0 += 32) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 8)
+                    *reinterpret_cast<uint4*>(stage + lane * 80 + c * 2) =
+                        make_uint4(pack_b(acc[c0 + c] * f, acc[c0 + c + 1] * f), pack_b(acc[c0 + c + 2] * f, acc[c0 + c + 3] * f),
+                                   pack_b(acc[c0 + c + 4] * f, acc[c0 + c + 5] * f), pack_b(acc[c0 + c + 6] * f, acc[c0 + c + 7] * f));
+                __syncwarp();
+                const int c = c0 + (lane & 3) * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = k * 8 + (lane >> 2);
+                    if (row0 + r < it.rows && half * H + c < dk)
+                        *reinterpret_cast<uint4*>(to + r * stride + c) =
+                            *reinterpret_cast<const uint4*>(stage + r * 80 + (lane & 3) * 16);
+                }
+                __syncwarp();
+            }
         }
         ++turn;
         if (!last) {
