@@ -112,6 +112,10 @@ __device__ __forceinline__ void mma_run(uint32_t d, uint32_t a, uint32_t a_lbo, 
     }
 }
 
+__device__ __forceinline__ void prefetch(const uint8_t* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 struct Item {
     int64_t slot, tok;
     int khead, rows;      // rows 0: none left
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             if (lane == 0) n = atomicAdd(a.next, 1u);
             n = __shfl_sync(0xffffffffu, n, 0);
             if (n >= a.items) break;
+            n = (unsigned)a.items - 1 - n;      // the backward chain's last images are still in L2
             it.slot = n / (unsigned)hk;
             it.khead = (int)(n % (unsigned)hk);
             const Chunk c = chunk_of(a.ends, a.episodes, (int32_t)a.in.tokens, (int32_t)it.slot);
@@ -209,6 +214,24 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
         un[1] = a.u_unit[at];
         un[2] = a.d_unit[at];
         un[3] = a.r_unit[at];
+    };
+    auto ahead = [&](const Item& x, int head, bool keys) {      // by one whole warp
+        const int64_t at = x.slot * hv + head;
+        if (lane == 0) {
+            if (keys) prefetch(a.keys + (x.slot * hk + x.khead) * KeyImage::bytes(DK, 1), 2 * L::kKey);
+            prefetch(a.r_img + at * L::kVec, L::kVec);
+            prefetch(a.u_img + at * L::kVec, L::kVec);
+            prefetch(a.s_img + at * L::kState, L::kState);
+            prefetch(a.d_img + at * L::kState, L::kState);
+            prefetch(a.pairs + at * kPairBytes + 2 * kSquare, kVecBytes);
+        }
+        const __nv_bfloat16* po = a.dout + (x.tok * hv + head) * dv;
+        const __nv_bfloat16* pv = static_cast<const __nv_bfloat16*>(a.in.v) + x.tok * a.in.v_stride + (int64_t)head * dv;
+        for (int j = lane; j < x.rows; j += 32)
+            for (int c = 0; c < dv; c += 64) {      // 128 bytes
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(po + (int64_t)j * hv * dv + c));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(pv + j * a.in.v_stride + c));
+            }
     };
     if (threadIdx.x == 0) {
         copy_keys(it, 0);
@@ -317,7 +340,15 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
                     2 * CG * kTile, id_s, blocks, false);
             umma::commit(&bar_s);
         }
-        if (warp == 1 && last) find();
+        if (warp == 1) {
+            // where the next head's operands are, and into L2 with them: they
+            // can be copied only when this head's products are through, and
+            // HBM's latency under load is most of a head's time
+            if (last) find();
+            __syncwarp();
+            const Item p = last ? s_next : it;
+            if (p.rows > 0) ahead(p, p.khead * group + (last ? 0 : g + 1), last);
+        }
         // <S_0, dS_1> meanwhile: 8 elements of one row per turn
         float ss = 0.0f;
         {
