@@ -7,14 +7,20 @@
 // once, but leaves a chunk's heads in a row: twice the latency, half the
 // CTAs to hide it.)
 //
+// [Q; K] K^T is one 128 x 64 product on tcgen05, read back a row per thread:
+// two warps make P's rows, two A's, while the decays are added up before.
+//
 // T.  1 + A is unit lower triangular with blocks of 16.  Warp w inverts the
-// diagonal block w by forward substitution (a lane per column) and then owns
-// T's block column w: transposed, its blocks are mma accumulators of the warp
-// and feed the next product as its A operand without leaving registers,
+// diagonal block w by forward substitution (a lane per column) and then makes
+// T's block column w, transposed, block after block:
 //   T_rw^T = -(sum_{s=w}^{r-1} T_sw^T A_rs^T) T_rr^T.
-// Substitution, not a series of powers of A: with correlated keys the powers
-// grow before they cancel.  The block products use bf16 planes (two, or three
-// where 22 bits are kept): T's elements have no bound known beforehand.
+// T^T's blocks lie on and above the diagonal of the image that holds A's below
+// it.  Substitution, not a series of powers of A: with correlated keys the
+// powers grow before they cancel.  The block products use bf16 planes (two, or
+// three where 22 bits are kept): T's elements have no bound known beforehand.
+//
+// Six CTAs share an SM's instruction cache at different places of a kernel
+// that runs through once, so its loops stay rolled where the work is the same.
 
 #include "delta_mma.cuh"
 
@@ -23,6 +29,7 @@ namespace delta {
 namespace {
 
 constexpr int kPrepThreads = 128;
+constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct PrepArgs {
     ofrl_delta_shape shape;
@@ -98,9 +105,9 @@ template <typename T, int DK, int NM>
 struct PrepShared {
     static constexpr int NT = sizeof(T) == 4 ? 2 : 1, NB = NM + 1;      // NB: bf16 planes inside the inversion
     static constexpr int kKey = kChunk * DK * 2;
-    // K^ and Q^ planes; afterwards, in the same place, A's blocks below the
-    // diagonal, T's diagonal blocks and their fp32 form
-    static constexpr int off_t = NB * kSquare, off_diag = off_t + NB * 16 * kTile;
+    // planes of Q^ and K^; afterwards, in the same place, A's blocks below the
+    // diagonal with T^T's on and above it, and the diagonal blocks in fp32
+    static constexpr int off_diag = NB * kSquare;
     static constexpr int kPitch = 20;      // floats between columns of a diagonal block
     static constexpr int kAfter = off_diag + 4 * 16 * kPitch * 4;
     static constexpr int off_vec = 2 * NT * kKey > kAfter ? 2 * NT * kKey : kAfter;
@@ -113,7 +120,9 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     using Sh = PrepShared<T, DK, NM>;
     constexpr int NT = Sh::NT, NB = Sh::NB, CG = DK / 8, KS = DK / 16, kKey = Sh::kKey, kPitch = Sh::kPitch;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *kimg = smem, *qimg = smem + NT * kKey, *aimg = smem, *timg = smem + Sh::off_t;
+    uint8_t* aimg = smem;      // [plane][Q^, K^] before
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ uint32_t s_tmem;
     float* diag = reinterpret_cast<float*>(smem + Sh::off_diag);
     float* vec = reinterpret_cast<float*>(smem + Sh::off_vec);
     float* kap = vec + V_COUNT * kChunk;
@@ -133,6 +142,11 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     if (rows <= 0) return;
     const int64_t tok = at.tok;
 
+    if (threadIdx.x == 0) {
+        umma::mbar_init(&bar, 1);
+        umma::fence_mbar_init();
+    }
+    if (warp == 3) umma::tmem_alloc(&s_tmem, kChunk);
     T gin[2], bin[2];      // tokens 2 lane, + 1 (past the end: the last one's, not used), in every warp
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -143,18 +157,18 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
     // group, so that a store of 8 lanes fills one 8x8 block.  All of a warp's
-    // loads (of a half of them, where registers are short) go out before the first is used.
+    // loads of one of them go out before the first is used.
     uint8_t* keys = a.keys + (slot * hk + khead) * KeyImage::bytes(DK, NT);
     const bool leave = head % group == 0;
-    constexpr int kBatch = NT * DK > 64 ? 2 : 4;      // registers
-#pragma unroll
+    constexpr int kBatch = 2;      // K's rows, then Q's
+#pragma unroll 1
     for (int w0 = 0; w0 < 4; w0 += kBatch) {
         const int r = lane & 7, c4 = lane >> 3;
         Raw<T> raw[kBatch][CG / 4];
 #pragma unroll
         for (int w = 0; w < kBatch; ++w) {
             const int row = min((warp * 2 + (w & 1)) * 8 + r, rows - 1);      // rows and columns that are not there
-            const bool isq = w0 + w >= 2;                                     // become zero below
+            const bool isq = w0 > 0;                                          // become zero below
             const T* p = isq ? static_cast<const T*>(a.in.q) + (tok + row) * a.in.q_stride + (int64_t)khead * dk
                              : static_cast<const T*>(a.in.k) + (tok + row) * a.in.k_stride + (int64_t)khead * dk;
 #pragma unroll
@@ -166,7 +180,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
 #pragma unroll
         for (int w = 0; w < kBatch; ++w) {
             const int rg = warp * 2 + (w & 1);
-            const bool isq = w0 + w >= 2;
+            const bool isq = w0 > 0;
             float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < CG / 4; ++i) {
@@ -191,49 +205,40 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
                 for (int n = 0; n < NT; ++n) {
                     const uint4 v = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
                     const int at = n * kKey + (rg * CG + c4 + 4 * i) * kTile + r * 16;
-                    *reinterpret_cast<uint4*>((isq ? qimg : kimg) + at) = v;
+                    *reinterpret_cast<uint4*>(smem + (isq ? 0 : kKey) + n * kKey + at) = v;
                     if (leave) *reinterpret_cast<uint4*>(keys + (isq ? NT * kKey : 0) + at) = v;
                 }
             }
         }
     }
+    umma::fence_smem_to_async();
+    umma::fence_before_sync();
     __syncthreads();
-    // K K^T rows of block `warp`, Q K^T rows of block 3 - warp: five 16x16
-    // blocks on or below the diagonal for every warp.
-    const int rk = warp, rq = 3 - warp;
-    const int m4 = lane >> 3, r8 = lane & 7;
-    const uint32_t kb = umma::smem_u32(kimg), qb = umma::smem_u32(qimg);
-    auto product = [&](float (&x)[8][4], uint32_t from, int rg) {      // rows of block rg of an image times K^T
-        zero(x);
+    umma::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    if (threadIdx.x == 0) {
+        constexpr uint32_t kId = umma::instr_desc(umma::kTypeF16, false, false, 128, kChunk);
+        const uint32_t base = umma::smem_u32(smem);
+        bool first = true;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            uint32_t fa[NT][4];
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)      // row halves (m4 & 1), k halves (m4 >> 1)
-                ldsm4(fa[n], from + n * kKey + ((2 * rg + (m4 & 1)) * CG + 2 * k + (m4 >> 1)) * kTile + r8 * 16);
+            for (int j = 0; j < NT; ++j)
+                if (i + j < NT) {
+                    const uint64_t da = umma::smem_desc(base + i * 2 * kKey, kTile, CG * kTile);
+                    const uint64_t db = umma::smem_desc(base + j * 2 * kKey + kKey, kTile, CG * kTile);
 #pragma unroll
-            for (int t = 0; t < 8; t += 2) {
-                if (t > 2 * rg) continue;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint32_t f[4];
-                    ldsm4(f, kb + j * kKey + ((t + (m4 >> 1)) * CG + 2 * k + (m4 & 1)) * kTile + r8 * 16);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        if (i + j < NT) {
-                            mma_h(x[t], fa[i], f[0], f[1]);
-                            mma_h(x[t + 1], fa[i], f[2], f[3]);
-                        }
+                    for (int k = 0; k < KS; ++k) {
+                        umma::mma_f16(tmem, da + k * (2 * kTile / 16), db + k * (2 * kTile / 16), kId, first ? 0u : 1u);
+                        first = false;
+                    }
                 }
-            }
-        }
-    };
-    float qk[8][4];
-    product(qk, qb, rq);
+        umma::commit(&bar);
+    }
+    __syncwarp();
     {
-        // Running sums of the log decays, in every warp (the instructions fit
-        // between the products' latencies); a warp leaves the vectors of its 16
-        // tokens.
+        // Running sums of the log decays, in every warp; a warp leaves the
+        // vectors of its 16 tokens.
         Two g[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -281,67 +286,82 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         }
     }
     __syncthreads();      // the vectors are there
-    const int row4 = lane >> 2, col2 = (lane & 3) * 2;
+    // a wait that gives up leaves this chunk's results wrong, and says so
+    if (!umma::mbar_wait(&bar, 0, kWaitNs)) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    __syncwarp();
+    umma::fence_after_sync();
+    const int m4 = lane >> 3, r8 = lane & 7;
     uint8_t* pairs = a.pairs + (slot * hv + head) * kPairBytes;
-    const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk, *beta = vec + V_BETA * kChunk;
-    // P to global memory
+    {
+        // Row i of P (warps 0, 1) or of A (2, 3), 16 columns at a time: P to
+        // global memory, A's blocks below the diagonal as images, the diagonal
+        // block as floats, column by column.  The keys' place is free.
+        const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk;
+        const int i = (warp & 1) * 32 + lane, ib = i >> 4;
+        const bool isk = warp >= 2;
+        const float gi = ghi[i], li = glo[i], f = isk ? vec[V_BETA * kChunk + i] : kPScale;
+        const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
+        const int at = (i >> 3) * 8 * kTile + (i & 7) * 16;      // of column 0 in an image
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb >= 2 && (warp & 1) == 0) {      // rows 0 .. 31 end before
+                if (!isk)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int iq = rq * 16 + row4 + 8 * h;
-        const float gq = ghi[iq], lq = glo[iq];
+                    for (int n = 0; n < 2 * NM; ++n)
+                        *reinterpret_cast<uint4*>(pairs + kSquare + (n >> 1) * kPairFirst + at + (2 * jb + (n & 1)) * kTile) =
+                            make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            float x[16];
+            umma::tmem_ld16(row + jb * 16, x);
+            umma::tmem_ld_wait();
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            float p[2] = {0.0f, 0.0f};
-            if (t <= 2 * rq + 1) {
-                const float2 gj = vec2(vec, V_GHI, t), lj = vec2(vec, V_GLO, t);
+            for (int c = 0; c < 16; c += 4) {
+                const float4 h4 = *reinterpret_cast<const float4*>(ghi + jb * 16 + c);
+                const float4 l4 = *reinterpret_cast<const float4*>(glo + jb * 16 + c);
+                const float gh[4] = {h4.x, h4.y, h4.z, h4.w}, gl[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float d = exp_2<NM>((gq - (z ? gj.y : gj.x)) + (lq - (z ? lj.y : lj.x))) * kPScale;
-                    if (t * 8 + col2 + z <= iq) p[z] = qk[t][2 * h + z] * d;
+                for (int z = 0; z < 4; ++z) {
+                    const int j = jb * 16 + c + z;
+                    const float y = x[c + z] * f * exp_2<NM>((gi - gh[z]) + (li - gl[z]));
+                    x[c + z] = j < i + (isk ? 0 : 1) ? y : 0.0f;
                 }
             }
-            uint32_t pl[NM];
-            planes_h<NM>(p[0], p[1], pl);
+            if (!isk) {
 #pragma unroll
-            for (int n = 0; n < NM; ++n)
-                *reinterpret_cast<uint32_t*>(pairs + kSquare + n * kPairFirst + ((2 * rq + h) * 8 + t) * kTile + lane * 4) =
-                    pl[n];
-        }
-    }
-    float kk[8][4];
-    product(kk, kb, rk);
-    __syncthreads();      // the keys' place is free
-    // A's blocks below the diagonal as images, the diagonal block as floats,
-    // column by column
+                for (int c = 0; c < 16; c += 8) {
+                    uint32_t pl[4][NM];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int ik = rk * 16 + row4 + 8 * h;
-        const float gk = ghi[ik], lk = glo[ik], bk = beta[ik];
+                    for (int z = 0; z < 4; ++z) planes_h<NM>(x[c + 2 * z], x[c + 2 * z + 1], pl[z]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (t > 2 * rk + 1) continue;
-            const float2 gj = vec2(vec, V_GHI, t), lj = vec2(vec, V_GLO, t);
-            float x[2];
+                    for (int n = 0; n < NM; ++n)
+                        *reinterpret_cast<uint4*>(pairs + kSquare + n * kPairFirst + at + (2 * jb + c / 8) * kTile) =
+                            make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+                }
+            } else if (jb < ib) {
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
-                x[z] = bk * kk[t][2 * h + z] * exp_2<NM>((gk - (z ? gj.y : gj.x)) + (lk - (z ? lj.y : lj.x)));
-            if (t < 2 * rk) {
-                uint32_t bl[NB];
-                planes_b<NB>(x[0], x[1], bl);
+                for (int c = 0; c < 16; c += 8) {
+                    uint32_t pl[4][NB];
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    *reinterpret_cast<uint32_t*>(aimg + n * kSquare + ((2 * rk + h) * 8 + t) * kTile + lane * 4) = bl[n];
-            } else {
+                    for (int z = 0; z < 4; ++z) planes_b<NB>(x[c + 2 * z], x[c + 2 * z + 1], pl[z]);
 #pragma unroll
-                for (int z = 0; z < 2; ++z)
-                    diag[(rk * 16 + (t - 2 * rk) * 8 + col2 + z) * kPitch + row4 + 8 * h] = x[z];      // [j][i]
+                    for (int n = 0; n < NB; ++n)
+                        *reinterpret_cast<uint4*>(aimg + n * kSquare + at + (2 * jb + c / 8) * kTile) =
+                            make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+                }
+            } else if (jb == ib) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) diag[(ib * 16 + c) * kPitch + (i & 15)] = x[c];      // [j][i]
             }
+            __syncwarp();
         }
     }
-    __syncwarp();
-    float* D = diag + warp * 16 * kPitch;
+    umma::fence_before_sync();
+    __syncthreads();
+    const uint32_t ab = umma::smem_u32(aimg);
     {
         // column c of the inverse: when x_j is known, it leaves every later row
+        const float* D = diag + warp * 16 * kPitch;
         const int c = lane & 15;
         float x[16];
 #pragma unroll
@@ -356,121 +376,130 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
                 for (int z = 0; z < 4; ++z)
                     if (4 * q + z > j) x[4 * q + z] = fmaf(-av[z], x[j], x[4 * q + z]);
             }
-        __syncwarp();
-        if (lane < 16)
+        if (lane < 16)      // row c of T_ww^T
 #pragma unroll
-            for (int q = 0; q < 4; ++q)      // now T^T: row j, column i
-                *reinterpret_cast<float4*>(D + c * kPitch + 4 * q) =
-                    make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        __syncwarp();
-    }
-    // own diagonal block, transposed, as accumulator tiles; and as the B
-    // operand T_rr [n = i][k = j] for the other warps
-    float tb[4][2][4];            // T_rw^T for r = 0 .. 3
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pl[4][NB];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) zero(tb[r]);
+                for (int z = 0; z < 4; ++z) planes_b<NB>(x[8 * h + 2 * z], x[8 * h + 2 * z + 1], pl[z]);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t pl[NB];
-            // rows i = row4 + 8 h, columns j = 8 t + col2: element T[i][j] = D[j][i]
-            planes_b<NB>(D[(t * 8 + col2) * kPitch + row4 + 8 * h], D[(t * 8 + col2 + 1) * kPitch + row4 + 8 * h], pl);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-                *reinterpret_cast<uint32_t*>(timg + ((n * 4 + warp) * 4 + h * 2 + t) * kTile + lane * 4) = pl[n];
-        }
-    __syncthreads();
-    {
-        uint32_t tp[3][NB][4];    // planes of the blocks so far as A operands
-        const uint32_t ab = umma::smem_u32(aimg), tbase = umma::smem_u32(timg);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w != warp) continue;      // w is a constant below: registers are indexed statically
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) tb[w][t][z] = D[(row4 + (z >> 1) * 8) * kPitch + t * 8 + col2 + (z & 1)];
-#pragma unroll
-            for (int r = w + 1; r < 4; ++r) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {      // planes of the block made last
-                    uint32_t pl[NB];
-                    const float* x = tb[r - 1][i >> 1] + (i & 1) * 2;
-                    planes_b<NB>(x[0], x[1], pl);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) tp[r - 1][n][i] = pl[n];
-                }
-                float z[2][4];
-                zero(z);
-#pragma unroll
-                for (int s = w; s < r; ++s)
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        uint32_t f[4];
-                        ldsm4(f, ab + j * kSquare + ((2 * r + (m4 >> 1)) * 8 + 2 * s + (m4 & 1)) * kTile + r8 * 16);
-#pragma unroll
-                        for (int i = 0; i < NB; ++i)
-                            if (i + j < NB) {
-                                mma_b(z[0], tp[s][i], f[0], f[1]);
-                                mma_b(z[1], tp[s][i], f[2], f[3]);
-                            }
-                    }
-                uint32_t zp[NB][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pl[NB];
-                    const float* x = z[i >> 1] + (i & 1) * 2;
-                    planes_b<NB>(-x[0], -x[1], pl);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) zp[n][i] = pl[n];
-                }
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    uint32_t f[4];
-                    ldsm4(f, tbase + ((j * 4 + r) * 4 + (m4 >> 1) * 2 + (m4 & 1)) * kTile + r8 * 16);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i)
-                        if (i + j < NB) {
-                            mma_b(tb[r][0], zp[i], f[0], f[1]);
-                            mma_b(tb[r][1], zp[i], f[2], f[3]);
-                        }
-                }
+                for (int n = 0; n < NB; ++n)
+                    *reinterpret_cast<uint4*>(aimg + n * kSquare + ((2 * warp + (c >> 3)) * 8 + 2 * warp + h) * kTile +
+                                              (c & 7) * 16) = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
             }
+    }
+    __syncthreads();
+    // block (row block, column block) of the image as a fragment
+    auto block = [&](uint32_t (&f)[NB][4], int rb, int cb, bool rows_first) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int hi = m4 >> 1, lo = m4 & 1;
+            ldsm4(f[n], ab + n * kSquare + ((2 * rb + (rows_first ? lo : hi)) * 8 + 2 * cb + (rows_first ? hi : lo)) * kTile + r8 * 16);
         }
-    }
-    // block column of T^T to global memory, with its power of two
-    float mx = 0.0f;
+    };
+#pragma unroll 1
+    for (int r = warp + 1; r < 4; ++r) {
+        float z[2][4];
+        zero(z);
+#pragma unroll 1
+        for (int t = warp; t < r; ++t) {
+            uint32_t ft[NB][4], fa[NB][4];
+            block(ft, warp, t, true);        // T_tw^T, an A operand
+            block(fa, r, t, false);          // A_rt, [n][k]
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+            for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+                for (int j = 0; j < NB; ++j)
+                    if (i + j < NB) {
+                        mma_b(z[0], ft[i], fa[j][0], fa[j][1]);
+                        mma_b(z[1], ft[i], fa[j][2], fa[j][3]);
+                    }
+        }
+        uint32_t zp[NB][4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) mx = fmaxf(mx, fabsf(tb[r][t][z]));
-    const float up = scale_up(warp_max(mx));
-    if (lane < 16) {
-        const int j = warp * 16 + lane;
-        const float inv = pow2_inv(up);
-        vec[V_TINV * kChunk + j] = inv;
-        vec[V_XV * kChunk + j] = vec[V_DV * kChunk + j] * inv;
-        vec[V_XS * kChunk + j] = vec[V_DS * kChunk + j] * inv;
-    }
+        for (int i = 0; i < 4; ++i) {
+            uint32_t pl[NB];
+            const float* x = z[i >> 1] + (i & 1) * 2;
+            planes_b<NB>(-x[0], -x[1], pl);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+            for (int n = 0; n < NB; ++n) zp[n][i] = pl[n];
+        }
+        float tb[2][4];
+        zero(tb);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            uint32_t f[4];      // T_rr^T is stored [k][n]
+            ldsm4t(f, ab + j * kSquare + ((2 * r + (m4 & 1)) * 8 + 2 * r + (m4 >> 1)) * kTile + r8 * 16);
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                if (i + j < NB) {
+                    mma_b(tb[0], zp[i], f[0], f[1]);
+                    mma_b(tb[1], zp[i], f[2], f[3]);
+                }
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t pl[NM];
-                planes_h<NM>(tb[r][t][2 * h] * up, tb[r][t][2 * h + 1] * up, pl);
+                uint32_t pl[NB];
+                planes_b<NB>(tb[t][2 * h], tb[t][2 * h + 1], pl);
 #pragma unroll
-                for (int n = 0; n < NM; ++n)
-                    *reinterpret_cast<uint32_t*>(pairs + n * kPairFirst + ((2 * warp + h) * 8 + 2 * r + t) * kTile +
-                                                 lane * 4) = pl[n];
+                for (int n = 0; n < NB; ++n)
+                    *reinterpret_cast<uint32_t*>(aimg + n * kSquare + ((2 * warp + h) * 8 + 2 * r + t) * kTile + lane * 4) = pl[n];
             }
+        __syncwarp();
+    }
+    // block row `warp` of T^T to global memory, with its power of two: a lane
+    // takes eight columns of a row, four times
+    {
+        float x[4][8];
+        float mx = 0.0f;
+        const int row = lane & 15;
+        const int at = ((2 * warp + (row >> 3)) * 8) * kTile + (row & 7) * 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int cg = 2 * k + (lane >> 4);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) x[k][z] = 0.0f;
+            if (k >= warp)
+#pragma unroll
+                for (int n = NB - 1; n >= 0; --n) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(aimg + n * kSquare + at + cg * kTile);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 f = unpack_b(w[z]);
+                        x[k][2 * z] += f.x;
+                        x[k][2 * z + 1] += f.y;
+                    }
+                }
+#pragma unroll
+            for (int z = 0; z < 8; ++z) mx = fmaxf(mx, fabsf(x[k][z]));
+        }
+        const float up = scale_up(warp_max(mx));
+        if (lane < 16) {
+            const int j = warp * 16 + lane;
+            const float inv = pow2_inv(up);
+            vec[V_TINV * kChunk + j] = inv;
+            vec[V_XV * kChunk + j] = vec[V_DV * kChunk + j] * inv;
+            vec[V_XS * kChunk + j] = vec[V_DS * kChunk + j] * inv;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t pl[4][NM];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) planes_h<NM>(x[k][2 * z] * up, x[k][2 * z + 1] * up, pl[z]);
+#pragma unroll
+            for (int n = 0; n < NM; ++n)
+                *reinterpret_cast<uint4*>(pairs + n * kPairFirst + at + (2 * k + (lane >> 4)) * kTile) =
+                    make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+        }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < kVecBytes / 16; i += kPrepThreads)
         reinterpret_cast<uint4*>(pairs + 2 * kSquare)[i] = reinterpret_cast<const uint4*>(vec)[i];
+    umma::fence_after_sync();
+    if (warp == 3) umma::tmem_dealloc(tmem, kChunk);
 }
 
 template <typename T, int DK, int NM>
