@@ -559,37 +559,45 @@ class DeltaRule:
         return torch.empty(max(n, 1), device="cuda", dtype=torch.uint8)
 
 
-def _rows(t: torch.Tensor, dtype, shape, name: str):
-    """Address and row stride (elements) of a CUDA tensor [tokens, ...] whose rows are dense."""
+def _refuse(t, dtype, shape, name: str):
+    """Raise for a tensor that is not a CUDA tensor of this type and shape."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    st = t.stride()
-    if len(shape) == 3:
-        d = shape[2]
-        dense = (st[2] == 1 or d == 1) and (st[1] == d or shape[1] == 1)
-        width = shape[1] * d
-    else:
-        dense = st[1] == 1 or shape[1] == 1
-        width = shape[1]
-    if not dense and shape[0]:
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows3(t: torch.Tensor, dtype, shape, name: str):
+    """Address and row stride (elements) of a CUDA tensor [tokens, heads, channels] whose rows are dense."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+            _refuse(t, dtype, shape, name)
+    s0, s1, s2 = t.stride()
+    n, h, d = shape
+    if n and (s2 != 1 and d > 1 or s1 != d and h > 1):
         raise ValueError(f"{name} must have dense rows (heads and channels contiguous within a token)")
-    return t.data_ptr(), st[0] if shape[0] > 1 else width
+    return t.data_ptr(), s0 if n > 1 else h * d
+
+
+def _rows2(t: torch.Tensor, dtype, shape, name: str):
+    """Address and row stride (elements) of a CUDA tensor [tokens, heads] whose rows are dense."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+            _refuse(t, dtype, shape, name)
+    s0, s1 = t.stride()
+    n, h = shape
+    if n and s1 != 1 and h > 1:
+        raise ValueError(f"{name} must have dense rows (heads contiguous within a token)")
+    return t.data_ptr(), s0 if n > 1 else h
 
 
 def _dense(t: Optional[torch.Tensor], dtype, shape, name: str):
     """Address of a contiguous CUDA tensor of this shape (0 for None)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _refuse(t, dtype, shape, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -602,16 +610,17 @@ def _raw_stream(stream, device: int) -> int:
 def _delta_tokens(ctx: DeltaRule, q, k, v, g, beta, scale):
     """The packed ofrl_delta_tokens, the token count and the three shapes."""
     dt = ctx.dtype
-    n = len(q)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _refuse(q, dt, ("tokens", ctx.k_heads, ctx.k_dim), "q")
+    n = q.shape[0]
     qk, vv, hv = (n, ctx.k_heads, ctx.k_dim), (n, ctx.v_heads, ctx.v_dim), (n, ctx.v_heads)
-    q, qs = _rows(q, dt, qk, "q")
-    k, ks = _rows(k, dt, qk, "k")
-    v, vs = _rows(v, dt, vv, "v")
-    g, gs = _rows(g, dt, hv, "g")
-    beta, bs = _rows(beta, dt, hv, "beta")
-    if scale is None:
-        scale = ctx.k_dim ** -0.5
-    return _pack_tokens(q, k, v, g, beta, qs, ks, vs, gs, bs, n, scale), n, qk, vv, hv
+    q, qs = _rows3(q, dt, qk, "q")
+    k, ks = _rows3(k, dt, qk, "k")
+    v, vs = _rows3(v, dt, vv, "v")
+    g, gs = _rows2(g, dt, hv, "g")
+    beta, bs = _rows2(beta, dt, hv, "beta")
+    return (_pack_tokens(q, k, v, g, beta, qs, ks, vs, gs, bs, n, ctx.k_dim ** -0.5 if scale is None else scale),
+            n, qk, vv, hv)
 
 
 _pack_tokens = struct.Struct(_abi.DELTA_TOKENS_FMT).pack
@@ -654,11 +663,11 @@ def delta_backward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, saved, dout, 
         raise TypeError("saved must be the buffer that delta_forward filled")
     dt = ctx.dtype
     state = (ne, ctx.v_heads, ctx.v_dim, ctx.k_dim)
-    dq, qs = _rows(dq, dt, qk, "dq")
-    dk, ks = _rows(dk, dt, qk, "dk")
-    dv, vs = _rows(dv, dt, vv, "dv")
-    dg, gs = _rows(dg, dt, hv, "dg")
-    dbeta, bs = _rows(dbeta, dt, hv, "dbeta")
+    dq, qs = _rows3(dq, dt, qk, "dq")
+    dk, ks = _rows3(dk, dt, qk, "dk")
+    dv, vs = _rows3(dv, dt, vv, "dv")
+    dg, gs = _rows2(dg, dt, hv, "dg")
+    dbeta, bs = _rows2(dbeta, dt, hv, "dbeta")
     code = ctx._lib.ofrl_delta_backward(
         ctx.handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _saved_ptr(ctx, saved, n, ne),
         _dense(dout, dt, vv, "dout"), _dense(d_final, F32, state, "d_final"),
@@ -673,7 +682,7 @@ def delta_step(ctx: DeltaRule, q, k, v, g, beta, state, out, scale=None, new_sta
     v_heads, v_dim, k_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each
     token (None: token i has state i)."""
     t, n, _, vv, _ = _delta_tokens(ctx, q, k, v, g, beta, scale)
-    ns = len(state)
+    ns = state.shape[0]
     shape = (ns, ctx.v_heads, ctx.v_dim, ctx.k_dim)
     at = _dense(state, F32, shape, "state")
     code = ctx._lib.ofrl_delta_step(

@@ -2,6 +2,8 @@
 // their context.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 struct ofrl_delta {
@@ -78,6 +80,21 @@ struct StepLaunch {
     int32_t* status;
     int num_sms;
 };
+
+// Opt a kernel into its dynamic shared memory and the largest carveout, once
+// per device (the calls cost a few microseconds).
+template <typename K>
+inline cudaError_t opt_in(K kernel, int smem, std::atomic<uint64_t>& done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = set_max_shared_carveout(kernel);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 cudaError_t launch_forward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_backward(const SeqLaunch& a, cudaStream_t st);

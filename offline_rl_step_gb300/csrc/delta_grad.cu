@@ -478,8 +478,8 @@ template <typename T, int DK, int DV>
 cudaError_t run(const GradArgs& g, int64_t grid, cudaStream_t st) {
     constexpr int smem = GradShared<T, DK, DV>::kBytes;
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<T, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = set_max_shared_carveout(delta_grad_kernel<T, DK, DV>);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = opt_in(delta_grad_kernel<T, DK, DV>, smem, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(delta_grad_kernel<T, DK, DV>, dim3((unsigned)grid), dim3(kGradThreads), smem, st, g);
 }

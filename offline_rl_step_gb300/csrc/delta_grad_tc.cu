@@ -626,8 +626,8 @@ template <int DK, int DV>
 cudaError_t run(const GradTcArgs& g, cudaStream_t st) {
     constexpr int smem = Lay<DK, DV>::kBytes;
     static_assert(smem <= 226 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = set_max_shared_carveout(delta_grad_tc_kernel<DK, DV>);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = opt_in(delta_grad_tc_kernel<DK, DV>, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)g.num_sms * Lay<DK, DV>::kCtas;
     const unsigned grid = (unsigned)(g.items < most ? g.items : most);

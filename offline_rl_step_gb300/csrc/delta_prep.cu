@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
 template <typename T, int DK, int NM>
 cudaError_t run(const PrepArgs& p, int64_t grid, cudaStream_t st) {
     constexpr int smem = PrepShared<T, DK, NM>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<T, DK, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = set_max_shared_carveout(delta_prep_kernel<T, DK, NM>);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = opt_in(delta_prep_kernel<T, DK, NM>, smem, done);
     if (e != cudaSuccess) return e;
     delta_prep_kernel<T, DK, NM><<<(unsigned)grid, kPrepThreads, smem, st>>>(p);
     return cudaGetLastError();
