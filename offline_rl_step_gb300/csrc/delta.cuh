@@ -98,6 +98,7 @@ inline cudaError_t opt_in(K kernel, int smem, std::atomic<uint64_t>& done) {
 
 cudaError_t launch_forward(const SeqLaunch& a, cudaStream_t st);
 cudaError_t launch_backward(const SeqLaunch& a, cudaStream_t st);
+cudaError_t launch_recur(const SeqLaunch& a, cudaStream_t st);      // forward, token by token
 cudaError_t launch_step(const StepLaunch& a, cudaStream_t st);
 int64_t saved_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episodes);
 int64_t parts_bytes(const ofrl_delta_shape& s, int64_t tokens, int num_sms);
