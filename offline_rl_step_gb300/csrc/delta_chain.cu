@@ -13,9 +13,7 @@
 // value channels for the whole episode: S lives in its registers as mma
 // accumulators, whose layout is that of the next product's A operand, and
 // nothing but a largest magnitude passes between warps.  Bulk copies keep a
-// ring of stages filled.  tcgen05 would run these products faster but needs each
-// intermediate through TMEM and a CTA-wide hand-over per product, four per
-// chunk, for 64-column tiles.
+// ring of stages filled.
 
 #include <cmath>
 
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                 if constexpr (!SUMMARY) gemm<KS, 8, NO, NT, false>(O, f0, qimg, St::kKey, CG, 0);
                 if constexpr (SAVE) {
                     const int64_t plane = (int64_t)NW * 16 * DK * 2;
-                    store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NO * plane, plane, f0, row0 / 8, NW * 2);
+                    store_image<NT == 1 ? 1 : kSliceCols / 8>(a.state_img + at * NO * plane, plane, f0, row0 / 8, NW * 2);
                     if (threadIdx.x == 0) a.state_unit[at] = s_inv;
                 }
             }
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
                 to_frags<NM>(S, s_up, f);
                 gemm<KS, 8, NM, NT, false>(U, f, kimg, St::kKey, CG, 0);
                 const int64_t plane = (int64_t)NW * 16 * DK * 2;
-                store_image<NT == 1 ? CG : kSliceCols / 8>(a.state_img + at * NT * plane, plane, f, row0 / 8, NW * 2);
+                store_image<NT == 1 ? 1 : kSliceCols / 8>(a.state_img + at * NT * plane, plane, f, row0 / 8, NW * 2);
                 if (threadIdx.x == 0) a.state_unit[at] = s_inv;
             }
             float dO[8][4];       // dout scale kq
@@ -799,6 +797,12 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
 
 }  // namespace
 
+// Whether a pass fills tcgen05's 128 rows: more than 64 value channels, and
+// operands of one plane (two do not fit in shared memory).  With 64 channels
+// or fewer half the rows would be empty, and four warps of mma.sync hold the
+// state in registers without any exchange.
+bool rows_of_tcgen05(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_BF16 && s.v_dim > 64; }
+
 // Parts of an episode.  A forward pass takes one CTA per head and 64 value
 // channels; where these leave most SMs idle and episodes are long, each is cut
 // into parts: summaries of all parts at once, the short chain over them, then
@@ -835,6 +839,7 @@ cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Im
     c.out_stride = (int64_t)a.shape.v_heads * a.shape.v_dim;
     c.rows = a.in.v;
     c.row_stride = a.in.v_stride;
+    if (rows_of_tcgen05(a.shape) && planes == 1 && c.segments == 1) return launch_chain_forward_tc(a, p, img, st);
     const bool wide = a.shape.k_dim > 64;
     if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? forward<float, 128, 2>(c, st) : forward<float, 64, 2>(c, st);
     if (planes == 2) return wide ? forward<__nv_bfloat16, 128, 2>(c, st) : forward<__nv_bfloat16, 64, 2>(c, st);
@@ -842,6 +847,7 @@ cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Im
 }
 
 cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st) {
+    if (rows_of_tcgen05(a.shape)) return launch_chain_reverse_tc(a, p, img, st);
     ChainArgs c = base_args(a, p, img);
     c.first = a.d_final;
     c.last = a.d_init;

@@ -334,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             mma_run(tmem + L::t_n, base + L::off_a, kTile, kA, 2 * kTile, base + L::off_u, kTile, kA, 2 * kTile, id_n,
                     blocks, false);
             umma::commit(&bar_n);
-            mma_run(tmem + L::t_st, base + L::off_a, kTile, kA, 2 * kTile, base + L::off_s, CG * kTile, kTile,
-                    2 * CG * kTile, id_s, blocks, false);
-            mma_run(tmem + L::t_sc, base + L::off_u - 8 * kA, kTile, kA, 2 * kTile, base + L::off_d, CG * kTile, kTile,
-                    2 * CG * kTile, id_s, blocks, false);
+            mma_run(tmem + L::t_st, base + L::off_a, kTile, kA, 2 * kTile, base + L::off_s, kTile, kA, 2 * kTile, id_s,
+                    blocks, false);
+            mma_run(tmem + L::t_sc, base + L::off_u - 8 * kA, kTile, kA, 2 * kTile, base + L::off_d, kTile, kA, 2 * kTile,
+                    id_s, blocks, false);
             umma::commit(&bar_s);
         }
         if (warp == 1) {
@@ -355,12 +355,12 @@ __global__ void __launch_bounds__(kThreads, Lay<DK, DV>::kCtas) delta_grad_tc_ke
             constexpr int kAtOnce = 4;
             const uint4 *ps = reinterpret_cast<const uint4*>(smem + L::off_s), *pd = reinterpret_cast<const uint4*>(smem + L::off_d);
             float part[kAtOnce] = {};
-            for (int x0 = threadIdx.x; x0 < blocks * 2 * CG * 8; x0 += kAtOnce * kThreads) {
+            for (int x0 = threadIdx.x; x0 < DV * DK / 8; x0 += kAtOnce * kThreads) {
                 uint4 sv[kAtOnce], dv4[kAtOnce];
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
                     const int x = x0 + k * kThreads;
-                    const bool in = x < blocks * 2 * CG * 8;
+                    const bool in = x < DV * DK / 8;
                     sv[k] = in ? ps[x] : make_uint4(0, 0, 0, 0);
                     dv4[k] = in ? pd[x] : make_uint4(0, 0, 0, 0);
                 }

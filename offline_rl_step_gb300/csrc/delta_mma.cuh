@@ -226,8 +226,7 @@ struct Prepared {
 // U^T (or R^T) [v_dim_pad][64] as images of token_planes() planes, each with
 // one power of two (state_unit, vec_unit).  Images of two planes: the state's
 // cut into slices of 32 columns, each contiguous, U^T's with its blocks in row
-// order.  Images of one plane: the state's blocks in row order, U^T's column
-// group by column group.
+// order.  Images of one plane: blocks column group by column group.
 constexpr int kSliceCols = 32;
 struct Images {
     uint8_t* state;
@@ -239,6 +238,8 @@ struct Images {
 // planes: of T and P, and of every intermediate of the forward pass (1 or 2).
 cudaError_t launch_prep(const SeqLaunch& a, const Prepared& to, int planes, cudaStream_t st);
 cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Images& img, int planes, cudaStream_t st);
+cudaError_t launch_chain_forward_tc(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st);
+cudaError_t launch_chain_reverse_tc(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st);
 cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st);
 cudaError_t launch_grad_tc(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
 cudaError_t launch_grad(const SeqLaunch& a, const Prepared& p, const Images& fwd, const Images& rev, cudaStream_t st);
