@@ -21,7 +21,9 @@ namespace ofrl {
 namespace delta {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;                    // two warpgroups for the tokens, two for the state
+constexpr int kTokThreads = 256;
+constexpr int kHalf = kChunk / 2;                // tokens of a thread
 constexpr int kRows = 128;                       // accumulator rows: value channels
 constexpr int kCol = (kRows / 8) * kTile;        // bytes of a column group of an operand image
 constexpr int kTok = kRows * kChunk * 2;         // [rows][64 tokens] image
@@ -58,23 +60,26 @@ struct Smem {
     static constexpr int off_c = off_b + kTok;           // forward: rest U; backward: gamma dO
     static constexpr int off_d = off_c + kTok;           // backward: -gamma dv
     static constexpr int off_stage = off_d + kTok;
-    static constexpr int off_row = off_stage + 2 * kStage;      // per row: powers of two
+    static constexpr int off_turn = off_stage + 2 * kStage;     // a warp's 32 channels x 32 tokens, turned around
+    static constexpr int off_row = off_turn + kTok;             // largest magnitudes of halves of rows
     static constexpr int kBytes = off_row + 4 * kRows * 4;
     static_assert(kBytes <= 226 * 1024, "shared memory");
 };
 
 struct Bars {
     uint64_t full[2], empty[2];
-    uint64_t s_ready, o_done, u_ready;      // between the warpgroups
+    uint64_t s_ready, o_done, u_ready;      // between the tokens' warps and the state's
     uint64_t a, b, t, s, p;                 // products done
     int dead;
     uint32_t tmem;
-    float most[2][4];
+    float most[2][8];
+    float s_inv, u_inv;                     // 1 / power of two of the state, of U
+    float o_inv[2], r_inv;                  // backward: of gamma dO, of -gamma dv
 };
 
 template <int BAR>
 __device__ __forceinline__ void group_sync() {
-    asm volatile("bar.sync %0, 128;" ::"n"(BAR) : "memory");
+    asm volatile("bar.sync %0, 256;" ::"n"(BAR) : "memory");
 }
 
 // Wait of a whole warp; once one has given up, none waits and the pass runs on
@@ -100,30 +105,34 @@ __device__ __forceinline__ void mma_run(uint32_t d, uint64_t a, uint32_t a_step,
         if (k < steps) umma::mma_f16(d, a + (uint64_t)k * (a_step >> 4), b + (uint64_t)k * (b_step >> 4), id, k > 0 ? 1u : 0u);
 }
 
-// x[0 .. 63] times f as the row of a [rows][64] operand image.
-__device__ __forceinline__ void put_row(uint8_t* img, int row, const float (&x)[64], float f) {
-    uint8_t* to = img + (row >> 3) * kTile + (row & 7) * 16;
-#pragma unroll
-    for (int c = 0; c < 64; c += 8)
-        *reinterpret_cast<uint4*>(to + c / 8 * kCol) =
-            make_uint4(pack_h(x[c] * f, x[c + 1] * f), pack_h(x[c + 2] * f, x[c + 3] * f), pack_h(x[c + 4] * f, x[c + 5] * f),
-                       pack_h(x[c + 6] * f, x[c + 7] * f));
-}
+// Largest of a row half's magnitudes.
 template <int N>
-__device__ __forceinline__ float row_max(const float (&x)[N]) {
+__device__ __forceinline__ float half_max(const float (&x)[N]) {
     float m[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int c = 0; c < N; ++c) m[c & 3] = fmaxf(m[c & 3], fabsf(x[c]));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-
-// Largest of a warpgroup's values.
+// Largest of the values of all warps that meet here.
+__device__ __forceinline__ float all_max(const float (&most)[8]) {
+    return fmaxf(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])),
+                 fmaxf(fmaxf(most[4], most[5]), fmaxf(most[6], most[7])));
+}
 template <int BAR>
-__device__ __forceinline__ float group_max(float (&most)[4], float v) {
+__device__ __forceinline__ float group_max(float (&most)[8], float v) {
     v = warp_max(v);
-    if ((threadIdx.x & 31) == 0) most[(threadIdx.x >> 5) & 3] = v;
+    if ((threadIdx.x & 31) == 0) most[(threadIdx.x >> 5) & 7] = v;
     group_sync<BAR>();
-    return fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    return all_max(most);
+}
+// x times f as N columns of a row of an operand image that begins at `to`.
+template <int N>
+__device__ __forceinline__ void put_cols(uint8_t* to, const float (&x)[N], float f) {
+#pragma unroll
+    for (int c = 0; c < N; c += 8)
+        *reinterpret_cast<uint4*>(to + c / 8 * kCol) =
+            make_uint4(pack_h(x[c] * f, x[c + 1] * f), pack_h(x[c + 2] * f, x[c + 3] * f), pack_h(x[c + 4] * f, x[c + 5] * f),
+                       pack_h(x[c + 6] * f, x[c + 7] * f));
 }
 
 struct Episode {
@@ -154,66 +163,126 @@ __device__ __forceinline__ void copy_stage(const TcArgs& a, const Episode& w, ui
                    &b.full[n & 1]);
 }
 
-// Channel `row` of a chunk's tokens; zero past their end and past v_dim.
-__device__ __forceinline__ void load_tokens(const TcArgs& a, const Episode& w, int c, int row, uint16_t (&x)[64]) {
-    const int rows = w.sp.len - c * kChunk;
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.rows) + ((int64_t)w.sp.start + c * kChunk) * a.row_stride +
-                        (int64_t)w.head * a.shape.v_dim + row;
-    const bool on = row < a.shape.v_dim && c >= 0 && c < w.chunks;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) x[i] = on && i < rows ? p[i * a.row_stride] : (uint16_t)0;
+// A warp's 32 tokens of 32 channels pass through shared memory to be turned
+// around: in global memory a lane has 16 bytes of a token, eight channels; in
+// the pass it has a channel and all tokens.  Element pairs go through
+// ldmatrix / stmatrix with transposition: matrix m of eight tokens takes
+// channels 8 j + 2 m, + 1 from the lanes with lane % 4 = j, so that a lane's
+// four registers are its 16 bytes.  A channel's row is 64 bytes in 16-byte
+// units; unit i is at i ^ turn_swap(channel), which puts the eight rows of a
+// matrix, and eight neighbouring channels, into different banks.
+__device__ __forceinline__ int turn_swap(int ch) { return ((ch >> 1) ^ (ch >> 3)) & 3; }
+struct Turn {
+    uint8_t* mine;          // this lane's channel's row
+    uint32_t matrix;        // shared address of the row that this lane names for ldmatrix / stmatrix
+    int mine_swap, matrix_swap;
+    int token, channel;     // of this lane's 16 bytes: token of eight, first channel
+};
+__device__ __forceinline__ Turn turn_of(uint8_t* area) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = lane >> 3, r = lane & 7;
+    const int ch = 8 * (r >> 1) + 2 * m + (r & 1);
+    uint8_t* tile = area + warp * 2048;
+    Turn t;
+    t.mine = tile + lane * 64;
+    t.mine_swap = turn_swap(lane);
+    t.matrix = umma::smem_u32(tile + ch * 64);
+    t.matrix_swap = turn_swap(ch);
+    t.token = (warp >> 2) * kHalf + (lane >> 2);
+    t.channel = (warp & 3) * 32 + (lane & 3) * 8;
+    return t;
 }
-__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-
-__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, int c, int row, const float (&x)[64]) {
-    if (row >= a.shape.v_dim) return;
-    const int rows = w.sp.len - c * kChunk;
-    __nv_bfloat16* p = a.out + ((int64_t)w.sp.start + c * kChunk) * a.out_stride + (int64_t)w.head * a.shape.v_dim + row;
+__device__ __forceinline__ void load_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c, uint4 (&v)[4]) {
+    const bool in = c >= 0 && t.channel < a.shape.v_dim;
+    const __nv_bfloat16* from = a.rows + ((int64_t)w.sp.start + (int64_t)c * kChunk + t.token) * a.row_stride +
+                                (int64_t)w.head * a.shape.v_dim + t.channel;
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-        if (i < rows) p[i * a.out_stride] = __float2bfloat16_rn(x[i]);
+    for (int i = 0; i < 4; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (in && c * kChunk + t.token + 8 * i < w.sp.len)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(from + (int64_t)(8 * i) * a.row_stride));
+    }
+}
+__device__ __forceinline__ void turn_in(const Turn& t, const uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         t.matrix + ((i ^ t.matrix_swap) << 4)),
+                     "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                     : "memory");
+    __syncwarp();
+}
+// Tokens 8 i .. 8 i + 7 of this lane's channel.
+__device__ __forceinline__ void eight_tokens(const Turn& t, int i, float (&x)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(t.mine + ((i ^ t.mine_swap) << 4));
+    const uint32_t r[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        x[2 * z] = __uint_as_float(r[z] << 16);
+        x[2 * z + 1] = __uint_as_float(r[z] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c, const float (&x)[kHalf]) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float* y = x + 8 * i;
+        *reinterpret_cast<uint4*>(t.mine + ((i ^ t.mine_swap) << 4)) =
+            make_uint4(pack_b(y[0], y[1]), pack_b(y[2], y[3]), pack_b(y[4], y[5]), pack_b(y[6], y[7]));
+    }
+    __syncwarp();
+    const bool in = t.channel < a.shape.v_dim;
+    __nv_bfloat16* to = a.out + ((int64_t)w.sp.start + (int64_t)c * kChunk + t.token) * a.out_stride +
+                        (int64_t)w.head * a.shape.v_dim + t.channel;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 q;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(t.matrix + ((i ^ t.matrix_swap) << 4))
+                     : "memory");
+        if (in && c * kChunk + t.token + 8 * i < w.sp.len)
+            *reinterpret_cast<uint4*>(to + (int64_t)(8 * i) * a.out_stride) = q;
+    }
+    __syncwarp();
 }
 
-// Four columns' values of a vector.
-__device__ __forceinline__ void four(const float* vec, int which, int c, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(vec + which * kChunk + c);
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
+// Values of a vector at N columns.
+template <int N>
+__device__ __forceinline__ void cols_of(const float* vec, int which, int c, float (&x)[N]) {
+#pragma unroll
+    for (int z = 0; z < N; z += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(vec + which * kChunk + c + z);
+        x[z] = v.x;
+        x[z + 1] = v.y;
+        x[z + 2] = v.z;
+        x[z + 3] = v.w;
+    }
 }
 
-template <int DK>
-__device__ __forceinline__ void load_row(const float* from, float (&s)[DK], int row, int dv, int dk) {
+// N columns of a row of a state, from column `col`.
+template <int N>
+__device__ __forceinline__ void load_row(const float* from, float (&s)[N], int row, int col, int dv, int dk) {
 #pragma unroll
-    for (int c = 0; c < DK; c += 4) {
+    for (int c = 0; c < N; c += 4) {
         float4 v = make_float4(0, 0, 0, 0);
-        if (from != nullptr && row < dv && c < dk) v = *reinterpret_cast<const float4*>(from + (int64_t)row * dk + c);
+        if (from != nullptr && row < dv && col + c < dk)
+            v = *reinterpret_cast<const float4*>(from + (int64_t)row * dk + col + c);
         s[c] = v.x;
         s[c + 1] = v.y;
         s[c + 2] = v.z;
         s[c + 3] = v.w;
     }
 }
-template <int DK>
-__device__ __forceinline__ void put_state(uint8_t* img, int row, const float (&s)[DK], float f) {
-    uint8_t* to = img + (row >> 3) * kTile + (row & 7) * 16;
-#pragma unroll
-    for (int c = 0; c < DK; c += 8)
-        *reinterpret_cast<uint4*>(to + c / 8 * kCol) =
-            make_uint4(pack_h(s[c] * f, s[c + 1] * f), pack_h(s[c + 2] * f, s[c + 3] * f), pack_h(s[c + 4] * f, s[c + 5] * f),
-                       pack_h(s[c + 6] * f, s[c + 7] * f));
-}
 
 __device__ __forceinline__ void init_bars(Bars& b) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(&b.full[i], 1);
-            umma::mbar_init(&b.empty[i], 8);
+            umma::mbar_init(&b.empty[i], kThreads / 32);
         }
         umma::mbar_init(&b.s_ready, 1);
         umma::mbar_init(&b.u_ready, 1);
-        umma::mbar_init(&b.o_done, 4);
+        umma::mbar_init(&b.o_done, 8);
         umma::mbar_init(&b.a, 1);
         umma::mbar_init(&b.b, 1);
         umma::mbar_init(&b.t, 1);
@@ -230,84 +299,100 @@ constexpr int t_x = 0, t_q = 64, t_u = 128, t_o = 192, t_s = 256, t_s2 = 384;
 template <int DK, bool SAVE>
 __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid_constant__ TcArgs a) {
     using S = Smem<DK>;
-    constexpr int CG = DK / 8, KS = DK / 16;
+    constexpr int CG = DK / 8, KS = DK / 16, NS = DK / 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) Bars b;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     init_bars(b);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
-    float* s_row = reinterpret_cast<float*>(smem + S::off_row);      // 1 / power of two of the state's rows
-    float* u_row = s_row + kRows;                                    // of U's
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = b.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t base = umma::smem_u32(smem);
+    const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
     auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
-    if (warp < 4) {
-        uint16_t v[64];
-        load_tokens(a, w, 0, row, v);
+    if (threadIdx.x < kTokThreads) {
+        const Turn turn = turn_of(smem + S::off_turn);
+        const int col = half * kHalf;
+        float* row_most = reinterpret_cast<float*>(smem + S::off_row);
+        const int at = at_row + half * (kHalf / 8) * kCol;
+        uint4 v[4];
+        load_tokens(a, w, turn, 0, v);
         pdl_wait();
-        if (threadIdx.x == 0 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, 0);
+        if (threadIdx.x == 32 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, 0);
         constexpr uint32_t kIdT = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
         constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
         for (int n = 0; n < w.chunks; ++n) {
             const float* vec = vec_of(n);
-            wait(b, &b.full[n & 1], n >> 1);
-            wait(b, &b.s_ready, n);
-            wait(b, &b.a, n);
-            if (threadIdx.x == 0 && n + 1 < w.chunks) {
+            const uint32_t pair = keys_at(n) + 2 * S::kKey;
+            turn_in(turn, v);
+            load_tokens(a, w, turn, n + 1, v);
+            if (threadIdx.x == 32 && n + 1 < w.chunks) {
                 if (n > 0 && !b.dead && !umma::mbar_wait(&b.empty[(n + 1) & 1], (uint32_t)((n + 1) / 2 - 1) & 1u, kWaitNs)) b.dead = 1;
                 if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, n + 1);
             }
             __syncwarp();
-            const float s_inv = s_row[row];
-            float x[64];
-            tmem_row(mine + t_x, x);
+            wait(b, &b.full[n & 1], n >> 1);
+            float x[kHalf];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                float f[4], g[4];
-                four(vec, V_XV, c, f);
-                four(vec, V_XS, c, g);
+            for (int i = 0; i < 4; ++i) {
+                float f[8], t[8];
+                cols_of(vec, V_XV, col + 8 * i, f);
+                eight_tokens(turn, i, t);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) x[c + z] = f[z] * widen(v[c + z]) - (g[z] * s_inv) * x[c + z];
+                for (int z = 0; z < 8; ++z) x[8 * i + z] = f[z] * t[z];
             }
-            const float x_up = scale_up(row_max(x)), x_inv = pow2_inv(x_up);
-            put_row(smem + S::off_a, row, x, x_up);
+            wait(b, &b.s_ready, n);
+            wait(b, &b.a, n);
+            const float s_inv = b.s_inv;
+            {
+                float y[kHalf];
+                tmem_row(mine + t_x + col, y);
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 4) {
+                    float g[4];
+                    cols_of(vec, V_XS, col + c, g);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[c + z] -= (g[z] * s_inv) * y[c + z];
+                }
+            }
+            row_most[half * kRows + row] = half_max(x);
+            if (SAVE && threadIdx.x == 0) umma::bulk_wait_read();      // U's image of the chunk before
+            group_sync<1>();
+            const float x_up = scale_up(fmaxf(row_most[row], row_most[kRows + row])), x_inv = pow2_inv(x_up);
+            put_cols(smem + S::off_a + at, x, x_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
             umma::fence_after_sync();
-            const uint32_t pair = keys_at(n) + 2 * S::kKey;
             if (threadIdx.x == 0) {
                 mma_run(tmem + t_u, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol, umma::smem_desc(pair, 8 * kTile, kTile),
                         2 * 8 * kTile, kIdT, 4);
                 umma::commit(&b.t);
-                if (SAVE) umma::bulk_wait_read();      // U's image of the chunk before
             }
-            load_tokens(a, w, n + 1, row, v);
             __syncwarp();
-            if (SAVE) group_sync<1>();
             wait(b, &b.t, n);
-            tmem_row(mine + t_u, x);
-            float u_max = row_max(x) * x_inv * vec[V_MISC * kChunk];
-            if (SAVE) u_max = group_max<1>(b.most[0], u_max);
-            const float u_up = scale_up(u_max), u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
-            put_row(smem + S::off_b, row, x, u_f);
+            tmem_row(mine + t_u + col, x);
+            const float u_up = scale_up(group_max<1>(b.most[0], half_max(x) * x_inv * vec[V_MISC * kChunk]));
+            const float u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
+            {
+                float y[kHalf];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                float f[4];
-                four(vec, V_REST, c, f);
+                for (int c = 0; c < kHalf; c += 4) {
+                    float f[4];
+                    cols_of(vec, V_REST, col + c, f);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) x[c + z] *= f[z];
+                    for (int z = 0; z < 4; ++z) y[c + z] = x[c + z] * f[z];
+                }
+                put_cols(smem + S::off_c + at, y, u_f);
             }
-            put_row(smem + S::off_c, row, x, u_f);
-            u_row[row] = u_inv;
+            if (threadIdx.x == 0) b.u_inv = u_inv;
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
@@ -317,83 +402,94 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
                 mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
                         umma::smem_desc(keys_at(n), CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
                 umma::commit(&b.s);
+            }
+            __syncwarp();
+            put_cols(smem + S::off_b + at, x, u_f);
+            umma::fence_smem_to_async();
+            umma::fence_before_sync();
+            group_sync<1>();
+            umma::fence_after_sync();
+            if (threadIdx.x == 0) {
                 mma_run(tmem + t_o, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol,
                         umma::smem_desc(pair + kSquare, kTile, 8 * kTile), 2 * kTile, kIdP, 4);
                 umma::commit(&b.p);
                 if (SAVE) {
-                    const int64_t at = (w.slot0 + n) * a.shape.v_heads + w.head;
-                    umma::bulk_s2g(a.vec_img + at * kTok, smem + S::off_b, kTok);
+                    const int64_t to = (w.slot0 + n) * a.shape.v_heads + w.head;
+                    umma::bulk_s2g(a.vec_img + to * kTok, smem + S::off_b, kTok);
                     umma::bulk_commit();
-                    a.vec_unit[at] = u_inv;
+                    a.vec_unit[to] = u_inv;
                 }
             }
             __syncwarp();
             wait(b, &b.b, n);
             wait(b, &b.p, n);
             const float p_inv = u_inv * (1.0f / kPScale);
-            float o[64];
-            tmem_row(mine + t_q, x);
-            tmem_row(mine + t_o, o);
+            float o[kHalf];
+            tmem_row(mine + t_q + col, x);
+            tmem_row(mine + t_o + col, o);
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&b.o_done);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kHalf; c += 4) {
                 float f[4], g[4];
-                four(vec, V_OS, c, f);
-                four(vec, V_QS, c, g);
+                cols_of(vec, V_OS, col + c, f);
+                cols_of(vec, V_QS, col + c, g);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) o[c + z] = (f[z] * s_inv) * x[c + z] + (g[z] * p_inv) * o[c + z];
             }
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
-            store_tokens(a, w, n, row, o);
+            store_tokens(a, w, turn, n, o);
         }
         if (SAVE && threadIdx.x == 0) umma::bulk_wait_read();
     } else {
-        float s[DK];
-        load_row(a.first ? a.first + w.states : nullptr, s, row, dv, dk);
+        float s[NS];
+        const int col = half * NS;
+        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
+        load_row(a.first ? a.first + w.states : nullptr, s, row, col, dv, dk);
         pdl_wait();
         constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         for (int n = 0; n < w.chunks; ++n) {
             if (n > 0) wait(b, &b.b, n - 1);      // what read the image is done
-            float most = row_max(s);
-            if (SAVE) {
-                if (threadIdx.x == 128) umma::bulk_wait_read();      // the image of the chunk before
-                most = group_max<2>(b.most[1], most);
-            }
-            const float up = scale_up(most), inv = pow2_inv(up);
-            put_state(smem + S::off_s, row, s, up);
-            s_row[row] = inv;
+            if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
+            const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
+            put_cols(mine_s, s, up);
+            if (threadIdx.x == kTokThreads) b.s_inv = inv;
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<2>();
             umma::fence_after_sync();
             wait(b, &b.full[n & 1], n >> 1);
-            if (n > 0) wait(b, &b.o_done, n - 1);
-            if (threadIdx.x == 128) {
-                umma::mbar_arrive(&b.s_ready);
+            if (warp == kTokThreads / 32) {
                 const uint64_t sd = umma::smem_desc(base + S::off_s, kCol, kTile);
-                mma_run(tmem + t_x, sd, 2 * kCol, umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
-                umma::commit(&b.a);
-                mma_run(tmem + t_q, sd, 2 * kCol, umma::smem_desc(keys_at(n) + S::kKey, kTile, CG * kTile), 2 * kTile, kIdA, KS);
-                umma::commit(&b.b);
-                if (SAVE) {
-                    const int64_t at = (w.slot0 + n) * a.shape.v_heads + w.head;
-                    umma::bulk_s2g(a.state_img + at * S::kState, smem + S::off_s, S::kState);
-                    umma::bulk_commit();
-                    a.state_unit[at] = inv;
+                if (lane == 0) {
+                    umma::mbar_arrive(&b.s_ready);
+                    mma_run(tmem + t_x, sd, 2 * kCol, umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
+                    umma::commit(&b.a);
                 }
+                __syncwarp();
+                if (n > 0) wait(b, &b.o_done, n - 1);
+                if (lane == 0) {
+                    mma_run(tmem + t_q, sd, 2 * kCol, umma::smem_desc(keys_at(n) + S::kKey, kTile, CG * kTile), 2 * kTile, kIdA, KS);
+                    umma::commit(&b.b);
+                    if (SAVE) {
+                        const int64_t to = (w.slot0 + n) * a.shape.v_heads + w.head;
+                        umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
+                        umma::bulk_commit();
+                        a.state_unit[to] = inv;
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
             const float keep = vec_of(n)[V_GAM * kChunk + kChunk - 1];
             wait(b, &b.u_ready, n);
             wait(b, &b.s, n);
-            const float u_inv = u_row[row];
+            const float u_inv = b.u_inv;
 #pragma unroll
-            for (int c = 0; c < DK; c += 32) {
+            for (int c = 0; c < NS; c += 32) {
                 float d[32];
-                tmem_row(mine + t_s + c, d);
+                tmem_row(mine + t_s + col + c, d);
 #pragma unroll
                 for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + u_inv * d[z];
             }
@@ -401,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
         }
-        if (SAVE && threadIdx.x == 128) umma::bulk_wait_read();
+        if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();
     }
     __syncthreads();
     umma::fence_after_sync();
@@ -412,31 +508,34 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
 template <int DK>
 __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid_constant__ TcArgs a) {
     using S = Smem<DK>;
-    constexpr int CG = DK / 8, KS = DK / 16;
+    constexpr int CG = DK / 8, KS = DK / 16, NS = DK / 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) Bars b;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     init_bars(b);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
-    float* s_row = reinterpret_cast<float*>(smem + S::off_row);      // 1 / power of two of the state's rows
-    float* o_row = s_row + kRows;                                    // of gamma dO's, for two chunks
-    float* r_row = o_row + 2 * kRows;                                // of gamma dv's
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = b.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t base = umma::smem_u32(smem);
+    const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
+    float* o_row = reinterpret_cast<float*>(smem + S::off_row);      // largest magnitudes: [half][row] of gamma dO
+    float* r_row = o_row + 2 * kRows;                                // and of dO scale kq, then of gamma dv
     auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
-    if (warp < 4) {
-        uint16_t v[64];
-        load_tokens(a, w, w.chunks - 1, row, v);
-        if (threadIdx.x == 0 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
+    if (threadIdx.x < kTokThreads) {
+        const Turn turn = turn_of(smem + S::off_turn);
+        const int col = half * kHalf;
+        const int at = at_row + half * (kHalf / 8) * kCol;
+        uint4 v[4];
+        load_tokens(a, w, turn, w.chunks - 1, v);
+        if (threadIdx.x == 32 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
         constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
         constexpr uint32_t kIdT = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
@@ -444,27 +543,29 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
             const int c0 = w.chunks - 1 - n;
             const float* vec = vec_of(n);
             const uint32_t pair = keys_at(n) + 2 * S::kKey;
+            turn_in(turn, v);
+            load_tokens(a, w, turn, c0 - 1, v);
             wait(b, &b.full[n & 1], n >> 1);
-            if (n > 0) wait(b, &b.s, n - 1);      // what read the images below is done
             // dO scale kq, for P; and times gamma, for the state
-            float x[64], y[64];
+            float x[kHalf], y[kHalf];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                float f[4], g[4];
-                four(vec, V_QS, c, f);
-                four(vec, V_GAM, c, g);
+            for (int i = 0; i < 4; ++i) {
+                float f[8], g[8], t[8];
+                cols_of(vec, V_QS, col + 8 * i, f);
+                cols_of(vec, V_GAM, col + 8 * i, g);
+                eight_tokens(turn, i, t);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    x[c + z] = widen(v[c + z]) * f[z];
-                    y[c + z] = x[c + z] * g[z];
+                for (int z = 0; z < 8; ++z) {
+                    x[8 * i + z] = t[z] * f[z];
+                    y[8 * i + z] = x[8 * i + z] * g[z];
                 }
             }
-            const float a_up = scale_up(row_max(x)), a_inv = pow2_inv(a_up);
-            put_row(smem + S::off_a, row, x, a_up);
-            const float o_up = scale_up(row_max(y));
-            put_row(smem + S::off_c, row, y, o_up);
-            o_row[(n & 1) * kRows + row] = pow2_inv(o_up);
+            if (n > 0) wait(b, &b.s, n - 1);      // what read the images below is done
+            r_row[half * kRows + row] = half_max(x);
             if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
+            const float o_up = scale_up(group_max<1>(b.most[0], half_max(y)));
+            const float a_up = scale_up(fmaxf(r_row[row], r_row[kRows + row])), a_inv = pow2_inv(a_up);
+            put_cols(smem + S::off_a + at, x, a_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
@@ -473,28 +574,32 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 mma_run(tmem + t_q, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
                         umma::smem_desc(pair + kSquare, 8 * kTile, kTile), 2 * 8 * kTile, kIdP, 4);
                 umma::commit(&b.b);
+                b.o_inv[n & 1] = pow2_inv(o_up);
             }
             __syncwarp();
+            put_cols(smem + S::off_c + at, y, o_up);
             wait(b, &b.b, n);
-            tmem_row(mine + t_q, y);
+            tmem_row(mine + t_q + col, y);
             wait(b, &b.s_ready, n);
-            wait(b, &b.a, n);
-            if (threadIdx.x == 0 && n + 1 < w.chunks) {
+            if (threadIdx.x == 32 && n + 1 < w.chunks) {
                 if (n > 0 && !b.dead && !umma::mbar_wait(&b.empty[(n + 1) & 1], (uint32_t)((n + 1) / 2 - 1) & 1u, kWaitNs)) b.dead = 1;
                 if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, w.chunks - 2 - n);
             }
             __syncwarp();
-            const float s_inv = s_row[row], p_inv = a_inv * (1.0f / kPScale);
-            tmem_row(mine + t_x, x);
+            wait(b, &b.a, n);
+            const float s_inv = b.s_inv, p_inv = a_inv * (1.0f / kPScale);
+            tmem_row(mine + t_x + col, x);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kHalf; c += 4) {
                 float f[4];
-                four(vec, V_REST, c, f);
+                cols_of(vec, V_REST, col + c, f);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) x[c + z] = (f[z] * s_inv) * x[c + z] + p_inv * y[c + z];
             }
-            const float u_up = scale_up(row_max(x)), u_inv = pow2_inv(u_up);
-            put_row(smem + S::off_b, row, x, u_up);
+            o_row[half * kRows + row] = half_max(x);
+            group_sync<1>();
+            const float u_up = scale_up(fmaxf(o_row[row], o_row[kRows + row])), u_inv = pow2_inv(u_up);
+            put_cols(smem + S::off_b + at, x, u_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
@@ -503,104 +608,113 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 mma_run(tmem + t_u, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol, umma::smem_desc(pair, kTile, 8 * kTile),
                         2 * kTile, kIdT, 4);
                 umma::commit(&b.t);
+                // beside it: dO's part of the state's next gradient
+                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
             }
             __syncwarp();
-            load_tokens(a, w, c0 - 1, row, v);
             wait(b, &b.t, n);
-            tmem_row(mine + t_u, x);
+            tmem_row(mine + t_u + col, x);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kHalf; c += 4) {
                 float f[4], g[4];
-                four(vec, V_TINV, c, f);
-                four(vec, V_DS, c, g);
+                cols_of(vec, V_TINV, col + c, f);
+                cols_of(vec, V_DS, col + c, g);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     x[c + z] *= f[z] * u_inv;
                     y[c + z] = -x[c + z] * g[z];
                 }
             }
-            const float r_up = scale_up(row_max(y));
-            put_row(smem + S::off_d, row, y, r_up);
-            r_row[row] = pow2_inv(r_up);
-            const float i_up = scale_up(group_max<1>(b.most[0], row_max(x)));
-            put_row(smem + S::off_b, row, x, i_up);
+            const float i_most = warp_max(half_max(x));
+            const float r_up = scale_up(group_max<1>(b.most[0], half_max(y)));
+            if (lane == 0) r_row[warp] = i_most;
+            if (threadIdx.x == 0) b.r_inv = pow2_inv(r_up);
+            put_cols(smem + S::off_d + at, y, r_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
             umma::fence_after_sync();
             if (threadIdx.x == 0) {
                 umma::mbar_arrive(&b.u_ready);
-                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
                 mma_run(tmem + t_s2, umma::smem_desc(base + S::off_d, kCol, kTile), 2 * kCol,
                         umma::smem_desc(keys_at(n), CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
                 umma::commit(&b.s);
-                const int64_t at = (w.slot0 + c0) * a.shape.v_heads + w.head;
-                umma::bulk_s2g(a.vec_img + at * kTok, smem + S::off_b, kTok);
+            }
+            __syncwarp();
+            const float i_up = scale_up(all_max(*reinterpret_cast<const float(*)[8]>(r_row)));
+            put_cols(smem + S::off_b + at, x, i_up);
+            umma::fence_smem_to_async();
+            group_sync<1>();
+            if (threadIdx.x == 0) {
+                const int64_t to = (w.slot0 + c0) * a.shape.v_heads + w.head;
+                umma::bulk_s2g(a.vec_img + to * kTok, smem + S::off_b, kTok);
                 umma::bulk_commit();
-                a.vec_unit[at] = pow2_inv(i_up);
+                a.vec_unit[to] = pow2_inv(i_up);
             }
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kHalf; c += 4) {
                 float f[4];
-                four(vec, V_DV, c, f);
+                cols_of(vec, V_DV, col + c, f);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) x[c + z] *= f[z];
             }
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
-            store_tokens(a, w, c0, row, x);
+            store_tokens(a, w, turn, c0, x);
         }
         if (threadIdx.x == 0) umma::bulk_wait_read();
     } else {
-        float s[DK];
-        load_row(a.first ? a.first + w.states : nullptr, s, row, dv, dk);
+        float s[NS];
+        const int col = half * NS;
+        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
+        load_row(a.first ? a.first + w.states : nullptr, s, row, col, dv, dk);
         constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         for (int n = 0; n < w.chunks; ++n) {
             const int c0 = w.chunks - 1 - n;
-            if (threadIdx.x == 128) umma::bulk_wait_read();      // the image of the chunk before
-            const float up = scale_up(group_max<2>(b.most[1], row_max(s))), inv = pow2_inv(up);
-            put_state(smem + S::off_s, row, s, up);
-            s_row[row] = inv;
+            if (threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
+            const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
+            put_cols(mine_s, s, up);
+            if (threadIdx.x == kTokThreads) b.s_inv = inv;
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<2>();
             umma::fence_after_sync();
             wait(b, &b.full[n & 1], n >> 1);
-            if (threadIdx.x == 128) {
+            if (threadIdx.x == kTokThreads) {
                 umma::mbar_arrive(&b.s_ready);
                 mma_run(tmem + t_x, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
                         umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
                 umma::commit(&b.a);
-                const int64_t at = (w.slot0 + c0) * a.shape.v_heads + w.head;
-                umma::bulk_s2g(a.state_img + at * S::kState, smem + S::off_s, S::kState);
+                const int64_t to = (w.slot0 + c0) * a.shape.v_heads + w.head;
+                umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
                 umma::bulk_commit();
-                a.state_unit[at] = inv;
+                a.state_unit[to] = inv;
             }
             __syncwarp();
             const float keep = vec_of(n)[V_GAM * kChunk + kChunk - 1];
             wait(b, &b.u_ready, n);
             wait(b, &b.s, n);
-            const float o_inv = o_row[(n & 1) * kRows + row], r_inv = r_row[row];
+            const float o_inv = b.o_inv[n & 1], r_inv = b.r_inv;
 #pragma unroll
-            for (int c = 0; c < DK; c += 32) {
-                float d[32], e[32];
-                tmem_row(mine + t_s + c, d);
-                tmem_row(mine + t_s2 + c, e);
+            for (int c = 0; c < NS; c += 16) {
+                float d[16], e[16];
+                tmem_row(mine + t_s + col + c, d);
+                tmem_row(mine + t_s2 + col + c, e);
 #pragma unroll
-                for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + (o_inv * d[z] + r_inv * e[z]);
+                for (int z = 0; z < 16; ++z) s[c + z] = keep * s[c + z] + (o_inv * d[z] + r_inv * e[z]);
             }
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
         }
-        if (threadIdx.x == 128) umma::bulk_wait_read();
+        if (threadIdx.x == kTokThreads) umma::bulk_wait_read();
         if (a.last && row < dv) {
             float* to = a.last + w.states + (int64_t)row * dk;
 #pragma unroll
-            for (int c = 0; c < DK; c += 4)
-                if (c < dk) *reinterpret_cast<float4*>(to + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
+            for (int c = 0; c < NS; c += 4)
+                if (col + c < dk) *reinterpret_cast<float4*>(to + col + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
         }
     }
     __syncthreads();
