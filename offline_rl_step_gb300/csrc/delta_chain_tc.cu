@@ -67,14 +67,15 @@ struct Smem {
 };
 
 struct Bars {
-    uint64_t full[2], empty[2];
-    uint64_t s_ready, o_done, u_ready;      // between the tokens' warps and the state's
-    uint64_t a, b, t, s, p;                 // products done
+    uint64_t full[2];
+    uint64_t s_ready, u_ready;              // from the state's warps, from the tokens'
+    uint64_t free[2];                       // forward: [0], t_o may be written; backward: a stage's vectors are read
+    uint64_t d[2];                          // backward: dO's product with P done
+    uint64_t a, b, c, t, s, p;              // products done
     int dead;
     uint32_t tmem;
-    float most[2][8];
-    float s_inv, u_inv;                     // 1 / power of two of the state, of U
-    float o_inv[2], r_inv;                  // backward: of gamma dO, of -gamma dv
+    float most[3][8], more[8];
+    float s_inv, u_inv, a_inv[2], r_inv;    // 1 / powers of two: the state, U, dO, -gamma dv
 };
 
 template <int BAR>
@@ -179,7 +180,7 @@ struct Turn {
     int token, channel;     // of this lane's 16 bytes: token of eight, first channel
 };
 __device__ __forceinline__ Turn turn_of(uint8_t* area) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = lane >> 3, r = lane & 7;
+    const int warp = (threadIdx.x >> 5) & 7, lane = threadIdx.x & 31, m = lane >> 3, r = lane & 7;
     const int ch = 8 * (r >> 1) + 2 * m + (r & 1);
     uint8_t* tile = area + warp * 2048;
     Turn t;
@@ -221,14 +222,12 @@ __device__ __forceinline__ void eight_tokens(const Turn& t, int i, float (&x)[8]
         x[2 * z + 1] = __uint_as_float(r[z] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c, const float (&x)[kHalf]) {
+// h: this channel's tokens in pairs.
+__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c, const uint32_t (&h)[kHalf / 2]) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float* y = x + 8 * i;
-        *reinterpret_cast<uint4*>(t.mine + ((i ^ t.mine_swap) << 4)) =
-            make_uint4(pack_b(y[0], y[1]), pack_b(y[2], y[3]), pack_b(y[4], y[5]), pack_b(y[6], y[7]));
-    }
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(t.mine + ((i ^ t.mine_swap) << 4)) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
     __syncwarp();
     const bool in = t.channel < a.shape.v_dim;
     __nv_bfloat16* to = a.out + ((int64_t)w.sp.start + (int64_t)c * kChunk + t.token) * a.out_stride +
@@ -274,20 +273,11 @@ __device__ __forceinline__ void load_row(const float* from, float (&s)[N], int r
     }
 }
 
-__device__ __forceinline__ void init_bars(Bars& b) {
+__device__ __forceinline__ void init_bars(Bars& b, int free) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(&b.full[i], 1);
-            umma::mbar_init(&b.empty[i], kThreads / 32);
-        }
-        umma::mbar_init(&b.s_ready, 1);
-        umma::mbar_init(&b.u_ready, 1);
-        umma::mbar_init(&b.o_done, 8);
-        umma::mbar_init(&b.a, 1);
-        umma::mbar_init(&b.b, 1);
-        umma::mbar_init(&b.t, 1);
-        umma::mbar_init(&b.s, 1);
-        umma::mbar_init(&b.p, 1);
+        uint64_t* one[] = {&b.full[0], &b.full[1], &b.s_ready, &b.u_ready, &b.a, &b.b, &b.c, &b.t, &b.s, &b.p, &b.d[0], &b.d[1]};
+        for (uint64_t* m : one) umma::mbar_init(m, 1);
+        for (int i = 0; i < 2; ++i) umma::mbar_init(&b.free[i], free);
         b.dead = 0;
         umma::fence_mbar_init();
     }
@@ -305,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
-    init_bars(b);
+    init_bars(b, 1);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
@@ -313,31 +303,23 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     const uint32_t tmem = b.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t base = umma::smem_u32(smem);
     const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
+    const int col = half * kHalf, at = at_row + half * (kHalf / 8) * kCol;      // of its tokens
+    float* row_most = reinterpret_cast<float*>(smem + S::off_row);
     auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
     if (threadIdx.x < kTokThreads) {
         const Turn turn = turn_of(smem + S::off_turn);
-        const int col = half * kHalf;
-        float* row_most = reinterpret_cast<float*>(smem + S::off_row);
-        const int at = at_row + half * (kHalf / 8) * kCol;
         uint4 v[4];
         load_tokens(a, w, turn, 0, v);
-        pdl_wait();
-        if (threadIdx.x == 32 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, 0);
         constexpr uint32_t kIdT = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
         constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
+        pdl_wait();
         for (int n = 0; n < w.chunks; ++n) {
             const float* vec = vec_of(n);
             const uint32_t pair = keys_at(n) + 2 * S::kKey;
             turn_in(turn, v);
-            load_tokens(a, w, turn, n + 1, v);
-            if (threadIdx.x == 32 && n + 1 < w.chunks) {
-                if (n > 0 && !b.dead && !umma::mbar_wait(&b.empty[(n + 1) & 1], (uint32_t)((n + 1) / 2 - 1) & 1u, kWaitNs)) b.dead = 1;
-                if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, n + 1);
-            }
-            __syncwarp();
             wait(b, &b.full[n & 1], n >> 1);
             float x[kHalf];
 #pragma unroll
@@ -363,7 +345,6 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
                 }
             }
             row_most[half * kRows + row] = half_max(x);
-            if (SAVE && threadIdx.x == 0) umma::bulk_wait_read();      // U's image of the chunk before
             group_sync<1>();
             const float x_up = scale_up(fmaxf(row_most[row], row_most[kRows + row])), x_inv = pow2_inv(x_up);
             put_cols(smem + S::off_a + at, x, x_up);
@@ -375,6 +356,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
                 mma_run(tmem + t_u, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol, umma::smem_desc(pair, 8 * kTile, kTile),
                         2 * 8 * kTile, kIdT, 4);
                 umma::commit(&b.t);
+                if (SAVE) umma::bulk_wait_read();      // U's image of the chunk before
             }
             __syncwarp();
             wait(b, &b.t, n);
@@ -404,98 +386,118 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
                 umma::commit(&b.s);
             }
             __syncwarp();
+            load_tokens(a, w, turn, n + 1, v);
+            if (n > 0) wait(b, &b.p, n - 1);      // what read the image below is done
             put_cols(smem + S::off_b + at, x, u_f);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
             umma::fence_after_sync();
-            if (threadIdx.x == 0) {
-                mma_run(tmem + t_o, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(pair + kSquare, kTile, 8 * kTile), 2 * kTile, kIdP, 4);
-                umma::commit(&b.p);
-                if (SAVE) {
-                    const int64_t to = (w.slot0 + n) * a.shape.v_heads + w.head;
-                    umma::bulk_s2g(a.vec_img + to * kTok, smem + S::off_b, kTok);
-                    umma::bulk_commit();
-                    a.vec_unit[to] = u_inv;
-                }
-            }
-            __syncwarp();
-            wait(b, &b.b, n);
-            wait(b, &b.p, n);
-            const float p_inv = u_inv * (1.0f / kPScale);
-            float o[kHalf];
-            tmem_row(mine + t_q + col, x);
-            tmem_row(mine + t_o + col, o);
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.o_done);
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 4) {
-                float f[4], g[4];
-                cols_of(vec, V_OS, col + c, f);
-                cols_of(vec, V_QS, col + c, g);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) o[c + z] = (f[z] * s_inv) * x[c + z] + (g[z] * p_inv) * o[c + z];
-            }
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
-            store_tokens(a, w, turn, n, o);
-        }
-        if (SAVE && threadIdx.x == 0) umma::bulk_wait_read();
-    } else {
-        float s[NS];
-        const int col = half * NS;
-        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
-        load_row(a.first ? a.first + w.states : nullptr, s, row, col, dv, dk);
-        pdl_wait();
-        constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
-        for (int n = 0; n < w.chunks; ++n) {
-            if (n > 0) wait(b, &b.b, n - 1);      // what read the image is done
-            if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
-            const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
-            put_cols(mine_s, s, up);
-            if (threadIdx.x == kTokThreads) b.s_inv = inv;
-            umma::fence_smem_to_async();
-            umma::fence_before_sync();
-            group_sync<2>();
-            umma::fence_after_sync();
-            wait(b, &b.full[n & 1], n >> 1);
-            if (warp == kTokThreads / 32) {
-                const uint64_t sd = umma::smem_desc(base + S::off_s, kCol, kTile);
+            if (warp == 0) {
+                wait(b, &b.free[0], n);
                 if (lane == 0) {
-                    umma::mbar_arrive(&b.s_ready);
-                    mma_run(tmem + t_x, sd, 2 * kCol, umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
-                    umma::commit(&b.a);
-                }
-                __syncwarp();
-                if (n > 0) wait(b, &b.o_done, n - 1);
-                if (lane == 0) {
-                    mma_run(tmem + t_q, sd, 2 * kCol, umma::smem_desc(keys_at(n) + S::kKey, kTile, CG * kTile), 2 * kTile, kIdA, KS);
-                    umma::commit(&b.b);
+                    mma_run(tmem + t_o, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol,
+                            umma::smem_desc(pair + kSquare, kTile, 8 * kTile), 2 * kTile, kIdP, 4);
+                    umma::commit(&b.p);
                     if (SAVE) {
                         const int64_t to = (w.slot0 + n) * a.shape.v_heads + w.head;
-                        umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
+                        umma::bulk_s2g(a.vec_img + to * kTok, smem + S::off_b, kTok);
                         umma::bulk_commit();
-                        a.state_unit[to] = inv;
+                        a.vec_unit[to] = u_inv;
                     }
                 }
                 __syncwarp();
             }
-            const float keep = vec_of(n)[V_GAM * kChunk + kChunk - 1];
-            wait(b, &b.u_ready, n);
-            wait(b, &b.s, n);
-            const float u_inv = b.u_inv;
+        }
+        if (SAVE && threadIdx.x == 0) umma::bulk_wait_read();
+    } else {
+        // Turn n: the state before chunk n; then the outputs of chunk n - 1.
+        const Turn turn = turn_of(smem + S::off_d);
+        float s[NS], inv = 0.0f, u_inv = 0.0f;
+        const int s_col = half * NS;
+        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
+        load_row(a.first ? a.first + w.states : nullptr, s, row, s_col, dv, dk);
+        pdl_wait();
+        if (threadIdx.x == kTokThreads && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, 0);
+        constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
+        for (int n = 0; n <= w.chunks && w.chunks > 0; ++n) {
+            const float inv_before = inv;
+            if (n > 0) {
+                wait(b, &b.full[(n - 1) & 1], (n - 1) >> 1);
+                wait(b, &b.u_ready, n - 1);
+                wait(b, &b.s, n - 1);
+                u_inv = b.u_inv;
+            }
+            if (n < w.chunks) {
+                if (n > 0) {
+                    const float keep = vec_of(n - 1)[V_GAM * kChunk + kChunk - 1];
 #pragma unroll
-            for (int c = 0; c < NS; c += 32) {
-                float d[32];
-                tmem_row(mine + t_s + col + c, d);
+                    for (int c = 0; c < NS; c += 32) {
+                        float d[32];
+                        tmem_row(mine + t_s + s_col + c, d);
 #pragma unroll
-                for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + u_inv * d[z];
+                        for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + u_inv * d[z];
+                    }
+                    wait(b, &b.b, n - 1);      // what read the image is done
+                }
+                if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
+                const float up = scale_up(group_max<2>(b.most[1], half_max(s)));
+                inv = pow2_inv(up);
+                put_cols(mine_s, s, up);
+                if (threadIdx.x == kTokThreads) b.s_inv = inv;
+                umma::fence_smem_to_async();
+                umma::fence_before_sync();
+                group_sync<2>();
+                umma::fence_after_sync();
+                if (warp == kTokThreads / 32) {
+                    wait(b, &b.full[n & 1], n >> 1);
+                    if (lane == 0) {
+                        umma::mbar_arrive(&b.s_ready);
+                        mma_run(tmem + t_x, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
+                                umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
+                        umma::commit(&b.a);
+                        if (SAVE) {
+                            const int64_t to = (w.slot0 + n) * a.shape.v_heads + w.head;
+                            umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
+                            umma::bulk_commit();
+                            a.state_unit[to] = inv;
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (n > 0) {
+                const float* vec = vec_of(n - 1);
+                wait(b, &b.b, n - 1);
+                wait(b, &b.p, n - 1);
+                const float p_inv = u_inv * (1.0f / kPScale);
+                uint32_t h[kHalf / 2];
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 16) {
+                    float x[16], o[16], f[16], g[16];
+                    umma::tmem_ld16(mine + t_q + col + c, x);
+                    umma::tmem_ld16(mine + t_o + col + c, o);
+                    umma::tmem_ld_wait();
+                    cols_of(vec, V_OS, col + c, f);
+                    cols_of(vec, V_QS, col + c, g);
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) o[z] = (f[z] * inv_before) * x[z] + (g[z] * p_inv) * o[z];
+#pragma unroll
+                    for (int z = 0; z < 16; z += 2) h[(c + z) / 2] = pack_b(o[z], o[z + 1]);
+                }
+                store_tokens(a, w, turn, n - 1, h);
             }
             umma::fence_before_sync();
+            group_sync<2>();
+            umma::fence_after_sync();
+            if (threadIdx.x == kTokThreads && n < w.chunks) {
+                umma::mbar_arrive(&b.free[0]);
+                mma_run(tmem + t_q, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(keys_at(n) + S::kKey, kTile, CG * kTile), 2 * kTile, kIdA, KS);
+                umma::commit(&b.b);
+                if (n + 1 < w.chunks) copy_stage<DK>(a, w, smem, b, n + 1, n + 1);
+            }
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
         }
         if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();
     }
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
-    init_bars(b);
+    init_bars(b, kTokThreads / 32);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
@@ -524,70 +526,26 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     const uint32_t tmem = b.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t base = umma::smem_u32(smem);
     const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
-    float* o_row = reinterpret_cast<float*>(smem + S::off_row);      // largest magnitudes: [half][row] of gamma dO
-    float* r_row = o_row + 2 * kRows;                                // and of dO scale kq, then of gamma dv
+    const int col = half * kHalf, at = at_row + half * (kHalf / 8) * kCol;      // of its tokens
+    float* row_most = reinterpret_cast<float*>(smem + S::off_row);
     auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
     if (threadIdx.x < kTokThreads) {
         const Turn turn = turn_of(smem + S::off_turn);
-        const int col = half * kHalf;
-        const int at = at_row + half * (kHalf / 8) * kCol;
-        uint4 v[4];
-        load_tokens(a, w, turn, w.chunks - 1, v);
-        if (threadIdx.x == 32 && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
-        constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
         constexpr uint32_t kIdT = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
         for (int n = 0; n < w.chunks; ++n) {
             const int c0 = w.chunks - 1 - n;
             const float* vec = vec_of(n);
             const uint32_t pair = keys_at(n) + 2 * S::kKey;
-            turn_in(turn, v);
-            load_tokens(a, w, turn, c0 - 1, v);
             wait(b, &b.full[n & 1], n >> 1);
-            // dO scale kq, for P; and times gamma, for the state
+            wait(b, &b.d[n & 1], n >> 1);
             float x[kHalf], y[kHalf];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[8], g[8], t[8];
-                cols_of(vec, V_QS, col + 8 * i, f);
-                cols_of(vec, V_GAM, col + 8 * i, g);
-                eight_tokens(turn, i, t);
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    x[8 * i + z] = t[z] * f[z];
-                    y[8 * i + z] = x[8 * i + z] * g[z];
-                }
-            }
-            if (n > 0) wait(b, &b.s, n - 1);      // what read the images below is done
-            r_row[half * kRows + row] = half_max(x);
-            if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
-            const float o_up = scale_up(group_max<1>(b.most[0], half_max(y)));
-            const float a_up = scale_up(fmaxf(r_row[row], r_row[kRows + row])), a_inv = pow2_inv(a_up);
-            put_cols(smem + S::off_a + at, x, a_up);
-            umma::fence_smem_to_async();
-            umma::fence_before_sync();
-            group_sync<1>();
-            umma::fence_after_sync();
-            if (threadIdx.x == 0) {
-                mma_run(tmem + t_q, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(pair + kSquare, 8 * kTile, kTile), 2 * 8 * kTile, kIdP, 4);
-                umma::commit(&b.b);
-                b.o_inv[n & 1] = pow2_inv(o_up);
-            }
-            __syncwarp();
-            put_cols(smem + S::off_c + at, y, o_up);
-            wait(b, &b.b, n);
-            tmem_row(mine + t_q + col, y);
+            tmem_row(mine + ((n & 1) ? t_o : t_q) + col, y);
             wait(b, &b.s_ready, n);
-            if (threadIdx.x == 32 && n + 1 < w.chunks) {
-                if (n > 0 && !b.dead && !umma::mbar_wait(&b.empty[(n + 1) & 1], (uint32_t)((n + 1) / 2 - 1) & 1u, kWaitNs)) b.dead = 1;
-                if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, w.chunks - 2 - n);
-            }
-            __syncwarp();
             wait(b, &b.a, n);
-            const float s_inv = b.s_inv, p_inv = a_inv * (1.0f / kPScale);
+            const float s_inv = b.s_inv, p_inv = b.a_inv[n & 1] * (1.0f / kPScale);
             tmem_row(mine + t_x + col, x);
 #pragma unroll
             for (int c = 0; c < kHalf; c += 4) {
@@ -596,9 +554,10 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
 #pragma unroll
                 for (int z = 0; z < 4; ++z) x[c + z] = (f[z] * s_inv) * x[c + z] + p_inv * y[c + z];
             }
-            o_row[half * kRows + row] = half_max(x);
+            row_most[half * kRows + row] = half_max(x);
+            if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
             group_sync<1>();
-            const float u_up = scale_up(fmaxf(o_row[row], o_row[kRows + row])), u_inv = pow2_inv(u_up);
+            const float u_up = scale_up(fmaxf(row_most[row], row_most[kRows + row])), u_inv = pow2_inv(u_up);
             put_cols(smem + S::off_b + at, x, u_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
@@ -608,9 +567,6 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 mma_run(tmem + t_u, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol, umma::smem_desc(pair, kTile, 8 * kTile),
                         2 * kTile, kIdT, 4);
                 umma::commit(&b.t);
-                // beside it: dO's part of the state's next gradient
-                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
             }
             __syncwarp();
             wait(b, &b.t, n);
@@ -627,8 +583,9 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 }
             }
             const float i_most = warp_max(half_max(x));
+            if (lane == 0) b.more[warp] = i_most;
             const float r_up = scale_up(group_max<1>(b.most[0], half_max(y)));
-            if (lane == 0) r_row[warp] = i_most;
+            const float i_up = scale_up(all_max(b.more));
             if (threadIdx.x == 0) b.r_inv = pow2_inv(r_up);
             put_cols(smem + S::off_d + at, y, r_up);
             umma::fence_smem_to_async();
@@ -642,8 +599,17 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 umma::commit(&b.s);
             }
             __syncwarp();
-            const float i_up = scale_up(all_max(*reinterpret_cast<const float(*)[8]>(r_row)));
             put_cols(smem + S::off_b + at, x, i_up);
+            uint32_t h[kHalf / 2];
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 4) {
+                float f[4];
+                cols_of(vec, V_DV, col + c, f);
+                h[c / 2] = pack_b(x[c] * f[0], x[c + 1] * f[1]);
+                h[c / 2 + 1] = pack_b(x[c + 2] * f[2], x[c + 3] * f[3]);
+            }
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&b.free[n & 1]);
             umma::fence_smem_to_async();
             group_sync<1>();
             if (threadIdx.x == 0) {
@@ -653,27 +619,73 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 a.vec_unit[to] = pow2_inv(i_up);
             }
             __syncwarp();
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 4) {
-                float f[4];
-                cols_of(vec, V_DV, col + c, f);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) x[c + z] *= f[z];
-            }
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
-            store_tokens(a, w, turn, c0, x);
+            store_tokens(a, w, turn, c0, h);
         }
         if (threadIdx.x == 0) umma::bulk_wait_read();
     } else {
-        float s[NS];
-        const int col = half * NS;
-        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
-        load_row(a.first ? a.first + w.states : nullptr, s, row, col, dv, dk);
+        // Turn n: the state's gradient after chunk n (counted from the last);
+        // then dO of the chunk that comes next, in the place of its operand.
+        const Turn turn = turn_of(smem + S::off_a);
         constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
+        constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
+        constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
+        float o_inv = 0.0f;
+        // dO scale kq, for P; and times gamma, for the state
+        auto take_dout = [&](int n, const uint4(&v)[4]) {
+            const float* vec = vec_of(n);
+            turn_in(turn, v);
+            wait(b, &b.full[n & 1], n >> 1);
+            float x[kHalf], o_most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8], g[8], t[8];
+                cols_of(vec, V_QS, col + 8 * i, f);
+                cols_of(vec, V_GAM, col + 8 * i, g);
+                eight_tokens(turn, i, t);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    x[8 * i + z] = t[z] * f[z];
+                    o_most = fmaxf(o_most, fabsf(x[8 * i + z] * g[z]));
+                }
+            }
+            o_most = warp_max(o_most);
+            if (lane == 0) b.most[1][warp - 8] = o_most;
+            const float a_up = scale_up(group_max<2>(b.most[2], half_max(x)));
+            const float o_up = scale_up(all_max(b.most[1]));
+            put_cols(smem + S::off_a + at, x, a_up);
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 4) {
+                float g[4];
+                cols_of(vec, V_GAM, col + c, g);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[c + z] *= g[z];
+            }
+            put_cols(smem + S::off_c + at, x, o_up);
+            umma::fence_smem_to_async();
+            umma::fence_before_sync();
+            group_sync<2>();
+            umma::fence_after_sync();
+            if (threadIdx.x == kTokThreads) {
+                b.a_inv[n & 1] = pow2_inv(a_up);
+                mma_run(tmem + ((n & 1) ? t_o : t_q), umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(keys_at(n) + 2 * S::kKey + kSquare, 8 * kTile, kTile), 2 * 8 * kTile, kIdP, 4);
+                umma::commit(&b.d[n & 1]);
+            }
+            __syncwarp();
+            o_inv = pow2_inv(o_up);
+        };
+        float s[NS];
+        const int s_col = half * NS;
+        uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
+        if (w.chunks > 0) {
+            uint4 v[4];
+            if (threadIdx.x == kTokThreads) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
+            load_tokens(a, w, turn, w.chunks - 1, v);
+            take_dout(0, v);
+        }
+        load_row(a.first ? a.first + w.states : nullptr, s, row, s_col, dv, dk);
         for (int n = 0; n < w.chunks; ++n) {
             const int c0 = w.chunks - 1 - n;
-            if (threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
             const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
             put_cols(mine_s, s, up);
             if (threadIdx.x == kTokThreads) b.s_inv = inv;
@@ -681,40 +693,56 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
             umma::fence_before_sync();
             group_sync<2>();
             umma::fence_after_sync();
-            wait(b, &b.full[n & 1], n >> 1);
             if (threadIdx.x == kTokThreads) {
                 umma::mbar_arrive(&b.s_ready);
                 mma_run(tmem + t_x, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
                         umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
                 umma::commit(&b.a);
+                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
+                umma::commit(&b.c);
                 const int64_t to = (w.slot0 + c0) * a.shape.v_heads + w.head;
                 umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
                 umma::bulk_commit();
                 a.state_unit[to] = inv;
             }
             __syncwarp();
+            const float o_inv_now = o_inv;
+            if (n + 1 < w.chunks) {
+                uint4 v[4];
+                load_tokens(a, w, turn, c0 - 1, v);
+                if (threadIdx.x == kTokThreads) {
+                    if (n > 0 && !b.dead && !umma::mbar_wait(&b.free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, kWaitNs)) b.dead = 1;
+                    if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, c0 - 1);
+                }
+                __syncwarp();
+                wait(b, &b.c, n);
+                wait(b, &b.d[n & 1], n >> 1);
+                take_dout(n + 1, v);
+            }
             const float keep = vec_of(n)[V_GAM * kChunk + kChunk - 1];
             wait(b, &b.u_ready, n);
             wait(b, &b.s, n);
-            const float o_inv = b.o_inv[n & 1], r_inv = b.r_inv;
+            wait(b, &b.c, n);
+            const float r_inv = b.r_inv;
 #pragma unroll
             for (int c = 0; c < NS; c += 16) {
                 float d[16], e[16];
-                tmem_row(mine + t_s + col + c, d);
-                tmem_row(mine + t_s2 + col + c, e);
+                umma::tmem_ld16(mine + t_s + s_col + c, d);
+                umma::tmem_ld16(mine + t_s2 + s_col + c, e);
+                umma::tmem_ld_wait();
 #pragma unroll
-                for (int z = 0; z < 16; ++z) s[c + z] = keep * s[c + z] + (o_inv * d[z] + r_inv * e[z]);
+                for (int z = 0; z < 16; ++z) s[c + z] = keep * s[c + z] + (o_inv_now * d[z] + r_inv * e[z]);
             }
             umma::fence_before_sync();
+            if (threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the state's image
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.empty[n & 1]);
         }
-        if (threadIdx.x == kTokThreads) umma::bulk_wait_read();
         if (a.last && row < dv) {
             float* to = a.last + w.states + (int64_t)row * dk;
 #pragma unroll
             for (int c = 0; c < NS; c += 4)
-                if (col + c < dk) *reinterpret_cast<float4*>(to + col + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
+                if (s_col + c < dk) *reinterpret_cast<float4*>(to + s_col + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
         }
     }
     __syncthreads();
