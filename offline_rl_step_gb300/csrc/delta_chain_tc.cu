@@ -69,13 +69,13 @@ struct Smem {
 struct Bars {
     uint64_t full[2];
     uint64_t s_ready, u_ready;              // from the state's warps, from the tokens'
-    uint64_t free[2];                       // forward: [0], t_o may be written; backward: a stage's vectors are read
-    uint64_t d[2];                          // backward: dO's product with P done
-    uint64_t a, b, c, t, s, p;              // products done
+    uint64_t free;                          // forward: t_q and t_o are read
+    uint64_t a, b, t, s, p;              // products done
     int dead;
     uint32_t tmem;
-    float most[3][8], more[8];
-    float s_inv, u_inv, a_inv[2], r_inv;    // 1 / powers of two: the state, U, dO, -gamma dv
+    float most[2][8], more[8];
+    float s_inv, u_inv, o_inv[2], r_inv;    // 1 / powers of two: the state, U, gamma dO, -gamma dv
+    alignas(16) float dv_f[2][kChunk];      // backward: factors of dv
 };
 
 template <int BAR>
@@ -273,11 +273,10 @@ __device__ __forceinline__ void load_row(const float* from, float (&s)[N], int r
     }
 }
 
-__device__ __forceinline__ void init_bars(Bars& b, int free) {
+__device__ __forceinline__ void init_bars(Bars& b) {
     if (threadIdx.x == 0) {
-        uint64_t* one[] = {&b.full[0], &b.full[1], &b.s_ready, &b.u_ready, &b.a, &b.b, &b.c, &b.t, &b.s, &b.p, &b.d[0], &b.d[1]};
-        for (uint64_t* m : one) umma::mbar_init(m, 1);
-        for (int i = 0; i < 2; ++i) umma::mbar_init(&b.free[i], free);
+        uint64_t* all[] = {&b.full[0], &b.full[1], &b.s_ready, &b.u_ready, &b.free, &b.a, &b.b, &b.t, &b.s, &b.p};
+        for (uint64_t* m : all) umma::mbar_init(m, 1);
         b.dead = 0;
         umma::fence_mbar_init();
     }
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
-    init_bars(b, 1);
+    init_bars(b);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             group_sync<1>();
             umma::fence_after_sync();
             if (warp == 0) {
-                wait(b, &b.free[0], n);
+                wait(b, &b.free, n);
                 if (lane == 0) {
                     mma_run(tmem + t_o, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol,
                             umma::smem_desc(pair + kSquare, kTile, 8 * kTile), 2 * kTile, kIdP, 4);
@@ -491,7 +490,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             group_sync<2>();
             umma::fence_after_sync();
             if (threadIdx.x == kTokThreads && n < w.chunks) {
-                umma::mbar_arrive(&b.free[0]);
+                umma::mbar_arrive(&b.free);
                 mma_run(tmem + t_q, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
                         umma::smem_desc(keys_at(n) + S::kKey, kTile, CG * kTile), 2 * kTile, kIdA, KS);
                 umma::commit(&b.b);
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
-    init_bars(b, kTokThreads / 32);
+    init_bars(b);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
@@ -532,20 +531,58 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
     if (threadIdx.x < kTokThreads) {
-        const Turn turn = turn_of(smem + S::off_turn);
+        // dO is turned around in the place of its operand
+        const Turn turn = turn_of(smem + S::off_a);
+        uint4 v[4];
+        load_tokens(a, w, turn, w.chunks - 1, v);
+        constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
         constexpr uint32_t kIdT = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
         constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
         for (int n = 0; n < w.chunks; ++n) {
             const int c0 = w.chunks - 1 - n;
             const float* vec = vec_of(n);
             const uint32_t pair = keys_at(n) + 2 * S::kKey;
+            float* u_most = row_most + (n & 1) * 2 * kRows;
+            turn_in(turn, v);
             wait(b, &b.full[n & 1], n >> 1);
-            wait(b, &b.d[n & 1], n >> 1);
+            // dO scale kq, for P; and times gamma, for the state
             float x[kHalf], y[kHalf];
-            tmem_row(mine + ((n & 1) ? t_o : t_q) + col, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8], g[8], t[8];
+                cols_of(vec, V_QS, col + 8 * i, f);
+                cols_of(vec, V_GAM, col + 8 * i, g);
+                eight_tokens(turn, i, t);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    x[8 * i + z] = t[z] * f[z];
+                    y[8 * i + z] = x[8 * i + z] * g[z];
+                }
+            }
+            const float o_most = warp_max(half_max(y));
+            if (lane == 0) b.more[warp] = o_most;
+            if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
+            const float a_up = scale_up(group_max<1>(b.most[0], half_max(x))), p_inv = pow2_inv(a_up) * (1.0f / kPScale);
+            const float o_up = scale_up(all_max(b.more));
+            put_cols(smem + S::off_a + at, x, a_up);
+            umma::fence_smem_to_async();
+            umma::fence_before_sync();
+            group_sync<1>();
+            umma::fence_after_sync();
+            if (threadIdx.x == 0) {
+                mma_run(tmem + t_q, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(pair + kSquare, 8 * kTile, kTile), 2 * 8 * kTile, kIdP, 4);
+                umma::commit(&b.b);
+                b.o_inv[n & 1] = pow2_inv(o_up);
+            }
+            __syncwarp();
+            if (n > 0) wait(b, &b.s, n - 1);      // what read the image below is done
+            put_cols(smem + S::off_c + at, y, o_up);
+            wait(b, &b.b, n);
+            tmem_row(mine + t_q + col, y);
             wait(b, &b.s_ready, n);
             wait(b, &b.a, n);
-            const float s_inv = b.s_inv, p_inv = b.a_inv[n & 1] * (1.0f / kPScale);
+            const float s_inv = b.s_inv;
             tmem_row(mine + t_x + col, x);
 #pragma unroll
             for (int c = 0; c < kHalf; c += 4) {
@@ -554,23 +591,27 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
 #pragma unroll
                 for (int z = 0; z < 4; ++z) x[c + z] = (f[z] * s_inv) * x[c + z] + p_inv * y[c + z];
             }
-            row_most[half * kRows + row] = half_max(x);
-            if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
+            u_most[half * kRows + row] = half_max(x);
             group_sync<1>();
-            const float u_up = scale_up(fmaxf(row_most[row], row_most[kRows + row])), u_inv = pow2_inv(u_up);
+            const float u_up = scale_up(fmaxf(u_most[row], u_most[kRows + row])), u_inv = pow2_inv(u_up);
             put_cols(smem + S::off_b + at, x, u_up);
             umma::fence_smem_to_async();
             umma::fence_before_sync();
             group_sync<1>();
             umma::fence_after_sync();
+            const uint32_t t_r = (n & 1) ? t_o : t_u;
             if (threadIdx.x == 0) {
-                mma_run(tmem + t_u, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol, umma::smem_desc(pair, kTile, 8 * kTile),
+                mma_run(tmem + t_r, umma::smem_desc(base + S::off_b, kCol, kTile), 2 * kCol, umma::smem_desc(pair, kTile, 8 * kTile),
                         2 * kTile, kIdT, 4);
                 umma::commit(&b.t);
+                // beside it: dO's part of the state's next gradient
+                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
             }
             __syncwarp();
+            load_tokens(a, w, turn, c0 - 1, v);
             wait(b, &b.t, n);
-            tmem_row(mine + t_u + col, x);
+            tmem_row(mine + t_r + col, x);
 #pragma unroll
             for (int c = 0; c < kHalf; c += 4) {
                 float f[4], g[4];
@@ -600,16 +641,6 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
             }
             __syncwarp();
             put_cols(smem + S::off_b + at, x, i_up);
-            uint32_t h[kHalf / 2];
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 4) {
-                float f[4];
-                cols_of(vec, V_DV, col + c, f);
-                h[c / 2] = pack_b(x[c] * f[0], x[c + 1] * f[1]);
-                h[c / 2 + 1] = pack_b(x[c + 2] * f[2], x[c + 3] * f[3]);
-            }
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&b.free[n & 1]);
             umma::fence_smem_to_async();
             group_sync<1>();
             if (threadIdx.x == 0) {
@@ -619,125 +650,91 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 a.vec_unit[to] = pow2_inv(i_up);
             }
             __syncwarp();
-            store_tokens(a, w, turn, c0, h);
         }
         if (threadIdx.x == 0) umma::bulk_wait_read();
     } else {
-        // Turn n: the state's gradient after chunk n (counted from the last);
-        // then dO of the chunk that comes next, in the place of its operand.
-        const Turn turn = turn_of(smem + S::off_a);
-        constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
-        constexpr uint32_t kIdP = umma::instr_desc(umma::kTypeF16, false, true, kRows, kChunk);
-        constexpr uint32_t kIdS = umma::instr_desc(umma::kTypeF16, false, true, kRows, DK);
-        float o_inv = 0.0f;
-        // dO scale kq, for P; and times gamma, for the state
-        auto take_dout = [&](int n, const uint4(&v)[4]) {
-            const float* vec = vec_of(n);
-            turn_in(turn, v);
-            wait(b, &b.full[n & 1], n >> 1);
-            float x[kHalf], o_most = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[8], g[8], t[8];
-                cols_of(vec, V_QS, col + 8 * i, f);
-                cols_of(vec, V_GAM, col + 8 * i, g);
-                eight_tokens(turn, i, t);
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    x[8 * i + z] = t[z] * f[z];
-                    o_most = fmaxf(o_most, fabsf(x[8 * i + z] * g[z]));
-                }
-            }
-            o_most = warp_max(o_most);
-            if (lane == 0) b.most[1][warp - 8] = o_most;
-            const float a_up = scale_up(group_max<2>(b.most[2], half_max(x)));
-            const float o_up = scale_up(all_max(b.most[1]));
-            put_cols(smem + S::off_a + at, x, a_up);
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 4) {
-                float g[4];
-                cols_of(vec, V_GAM, col + c, g);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) x[c + z] *= g[z];
-            }
-            put_cols(smem + S::off_c + at, x, o_up);
-            umma::fence_smem_to_async();
-            umma::fence_before_sync();
-            group_sync<2>();
-            umma::fence_after_sync();
-            if (threadIdx.x == kTokThreads) {
-                b.a_inv[n & 1] = pow2_inv(a_up);
-                mma_run(tmem + ((n & 1) ? t_o : t_q), umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(keys_at(n) + 2 * S::kKey + kSquare, 8 * kTile, kTile), 2 * 8 * kTile, kIdP, 4);
-                umma::commit(&b.d[n & 1]);
-            }
-            __syncwarp();
-            o_inv = pow2_inv(o_up);
-        };
+        // Turn n (chunks are counted from the last): the state's gradient after
+        // chunk n; then dv of chunk n - 1, from the product that the tokens'
+        // warps made R of.
+        const Turn turn = turn_of(smem + S::off_turn);
         float s[NS];
         const int s_col = half * NS;
         uint8_t* mine_s = smem + S::off_s + at_row + half * (NS / 8) * kCol;
-        if (w.chunks > 0) {
-            uint4 v[4];
-            if (threadIdx.x == kTokThreads) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
-            load_tokens(a, w, turn, w.chunks - 1, v);
-            take_dout(0, v);
-        }
+        if (threadIdx.x == kTokThreads && w.chunks > 0) copy_stage<DK>(a, w, smem, b, 0, w.chunks - 1);
         load_row(a.first ? a.first + w.states : nullptr, s, row, s_col, dv, dk);
-        for (int n = 0; n < w.chunks; ++n) {
+        constexpr uint32_t kIdA = umma::instr_desc(umma::kTypeF16, false, false, kRows, kChunk);
+        for (int n = 0; n <= w.chunks && w.chunks > 0; ++n) {
             const int c0 = w.chunks - 1 - n;
-            const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
-            put_cols(mine_s, s, up);
-            if (threadIdx.x == kTokThreads) b.s_inv = inv;
-            umma::fence_smem_to_async();
-            umma::fence_before_sync();
-            group_sync<2>();
-            umma::fence_after_sync();
-            if (threadIdx.x == kTokThreads) {
-                umma::mbar_arrive(&b.s_ready);
-                mma_run(tmem + t_x, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
-                umma::commit(&b.a);
-                mma_run(tmem + t_s, umma::smem_desc(base + S::off_c, kCol, kTile), 2 * kCol,
-                        umma::smem_desc(keys_at(n) + S::kKey, CG * kTile, kTile), 2 * CG * kTile, kIdS, 4);
-                umma::commit(&b.c);
-                const int64_t to = (w.slot0 + c0) * a.shape.v_heads + w.head;
-                umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
-                umma::bulk_commit();
-                a.state_unit[to] = inv;
-            }
-            __syncwarp();
-            const float o_inv_now = o_inv;
-            if (n + 1 < w.chunks) {
-                uint4 v[4];
-                load_tokens(a, w, turn, c0 - 1, v);
-                if (threadIdx.x == kTokThreads) {
-                    if (n > 0 && !b.dead && !umma::mbar_wait(&b.free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, kWaitNs)) b.dead = 1;
-                    if (!b.dead) copy_stage<DK>(a, w, smem, b, n + 1, c0 - 1);
+            float* dv_f = b.dv_f[n & 1];
+            if (n > 0) {
+                const float* vec = vec_of(n - 1);
+                wait(b, &b.full[(n - 1) & 1], (n - 1) >> 1);
+                const float keep = vec[V_GAM * kChunk + kChunk - 1];
+                const int i = threadIdx.x - kTokThreads;
+                if (i < kChunk) dv_f[i] = vec[V_TINV * kChunk + i] * vec[V_DV * kChunk + i];
+                wait(b, &b.u_ready, n - 1);
+                wait(b, &b.s, n - 1);
+                const float o_inv = b.o_inv[(n - 1) & 1], r_inv = b.r_inv;
+#pragma unroll
+                for (int c = 0; c < NS; c += 16) {
+                    float d[16], e[16];
+                    umma::tmem_ld16(mine + t_s + s_col + c, d);
+                    umma::tmem_ld16(mine + t_s2 + s_col + c, e);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) s[c + z] = keep * s[c + z] + (o_inv * d[z] + r_inv * e[z]);
                 }
+            }
+            if (threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the image of the chunk before
+            const float up = scale_up(group_max<2>(b.most[1], half_max(s))), inv = pow2_inv(up);
+            if (n < w.chunks) {
+                // nothing reads the stage of the chunk before any more
+                if (threadIdx.x == kTokThreads + 32 && n + 1 < w.chunks) copy_stage<DK>(a, w, smem, b, n + 1, c0 - 1);
                 __syncwarp();
-                wait(b, &b.c, n);
-                wait(b, &b.d[n & 1], n >> 1);
-                take_dout(n + 1, v);
+                put_cols(mine_s, s, up);
+                if (threadIdx.x == kTokThreads) b.s_inv = inv;
+                umma::fence_smem_to_async();
+                umma::fence_before_sync();
+                group_sync<2>();
+                umma::fence_after_sync();
+                if (warp == kTokThreads / 32) {
+                    wait(b, &b.full[n & 1], n >> 1);
+                    if (lane == 0) {
+                        umma::mbar_arrive(&b.s_ready);
+                        mma_run(tmem + t_x, umma::smem_desc(base + S::off_s, kCol, kTile), 2 * kCol,
+                                umma::smem_desc(keys_at(n), kTile, CG * kTile), 2 * kTile, kIdA, KS);
+                        umma::commit(&b.a);
+                        const int64_t to = (w.slot0 + c0) * a.shape.v_heads + w.head;
+                        umma::bulk_s2g(a.state_img + to * S::kState, smem + S::off_s, S::kState);
+                        umma::bulk_commit();
+                        a.state_unit[to] = inv;
+                    }
+                    __syncwarp();
+                }
             }
-            const float keep = vec_of(n)[V_GAM * kChunk + kChunk - 1];
-            wait(b, &b.u_ready, n);
-            wait(b, &b.s, n);
-            wait(b, &b.c, n);
-            const float r_inv = b.r_inv;
+            if (n > 0) {
+                const float* u_most = row_most + ((n - 1) & 1) * 2 * kRows;
+                const float u_inv = pow2_inv(scale_up(fmaxf(u_most[row], u_most[kRows + row])));
+                const uint32_t t_r = ((n - 1) & 1) ? t_o : t_u;
+                uint32_t h[kHalf / 2];
 #pragma unroll
-            for (int c = 0; c < NS; c += 16) {
-                float d[16], e[16];
-                umma::tmem_ld16(mine + t_s + s_col + c, d);
-                umma::tmem_ld16(mine + t_s2 + s_col + c, e);
-                umma::tmem_ld_wait();
+                for (int c = 0; c < kHalf; c += 16) {
+                    float x[16], f[16];
+                    umma::tmem_ld16(mine + t_r + col + c, x);
+                    umma::tmem_ld_wait();
 #pragma unroll
-                for (int z = 0; z < 16; ++z) s[c + z] = keep * s[c + z] + (o_inv_now * d[z] + r_inv * e[z]);
+                    for (int z = 0; z < 16; z += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(dv_f + col + c + z);
+                        f[z] = q.x, f[z + 1] = q.y, f[z + 2] = q.z, f[z + 3] = q.w;
+                    }
+#pragma unroll
+                    for (int z = 0; z < 16; z += 2) h[(c + z) / 2] = pack_b(x[z] * (f[z] * u_inv), x[z + 1] * (f[z + 1] * u_inv));
+                }
+                umma::fence_before_sync();
+                store_tokens(a, w, turn, c0 + 1, h);
             }
-            umma::fence_before_sync();
-            if (threadIdx.x == kTokThreads) umma::bulk_wait_read();      // the state's image
-            __syncwarp();
         }
+        if (threadIdx.x == kTokThreads) umma::bulk_wait_read();
         if (a.last && row < dv) {
             float* to = a.last + w.states + (int64_t)row * dk;
 #pragma unroll
