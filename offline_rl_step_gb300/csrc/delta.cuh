@@ -69,6 +69,11 @@ struct SeqLaunch {
     int num_sms;
 };
 
+// Threads of a CTA that goes token by token, and the state rows it has there
+// with `lanes` lanes to a row, two rows to a lane group.
+constexpr int kStepThreads = 128, kRecurRows = 2;
+constexpr int recur_rows(int lanes) { return kStepThreads / lanes * kRecurRows; }
+
 struct StepLaunch {
     ofrl_delta_shape shape;
     ofrl_delta_tokens in;

@@ -799,9 +799,20 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
 
 // Whether a pass fills tcgen05's 128 rows: more than 64 value channels, and
 // operands of one plane (two do not fit in shared memory).  With 64 channels
-// or fewer half the rows would be empty, and four warps of mma.sync hold the
-// state in registers without any exchange.
+// or fewer half the rows would be empty: a chunk takes a CTA 4.4 us there
+// however many rows are filled, against 3 us for four warps of mma.sync that
+// hold 64 channels' state in registers.  About 65k ragged transitions, four
+// heads of 128 x 128, forward and reverse: 137 + 161 us, on mma.sync 197 + 206.
 bool rows_of_tcgen05(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_BF16 && s.v_dim > 64; }
+
+// A forward pass that saves nothing has less to convert, and where two CTAs per
+// head still find an SM each, mma.sync on 64 channels in each is the faster one:
+// 32 heads of 2000 tokens of 128 x 128 118 us against 131, 64 heads of 512 40.3
+// against 44.4; but 256 heads of 64 tokens 31.8 against 25.4, 400 of 300 143
+// against 107.
+bool forward_on_tcgen05(const SeqLaunch& a) {
+    return rows_of_tcgen05(a.shape) && (a.saved || 2LL * a.episodes * a.shape.v_heads > a.num_sms);
+}
 
 // Parts of an episode.  A forward pass takes one CTA per head and 64 value
 // channels; where these leave most SMs idle and episodes are long, each is cut
@@ -839,7 +850,7 @@ cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Im
     c.out_stride = (int64_t)a.shape.v_heads * a.shape.v_dim;
     c.rows = a.in.v;
     c.row_stride = a.in.v_stride;
-    if (rows_of_tcgen05(a.shape) && planes == 1 && c.segments == 1) return launch_chain_forward_tc(a, p, img, st);
+    if (forward_on_tcgen05(a) && planes == 1 && c.segments == 1) return launch_chain_forward_tc(a, p, img, st);
     const bool wide = a.shape.k_dim > 64;
     if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? forward<float, 128, 2>(c, st) : forward<float, 64, 2>(c, st);
     if (planes == 2) return wide ? forward<__nv_bfloat16, 128, 2>(c, st) : forward<__nv_bfloat16, 64, 2>(c, st);

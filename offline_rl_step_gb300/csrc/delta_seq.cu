@@ -25,6 +25,8 @@
 // episode forward and, for gradients, back; delta_grad.cu then takes every
 // chunk by itself.  This file lays out the buffers between them.
 
+#include <algorithm>
+
 #include "delta_mma.cuh"
 
 namespace ofrl {
@@ -55,11 +57,31 @@ Images images_at(uint8_t* p, const Sizes& z) {
 int64_t prepared_bytes(const Sizes& z) { return z.keys + z.pairs; }
 int64_t images_bytes(const Sizes& z) { return z.state + z.vec + 2 * z.units; }
 
-// Whether token by token is the faster way: a token costs about 0.25 us there,
-// a chunk 3 us on top of the chunked path's 14 us.  The host knows the mean
-// length only; the bound on the tokens keeps the worst case, all of them in
-// one episode, at 4 ms.
-bool recurrent(const SeqLaunch& a) { return a.in.tokens <= 48LL * a.episodes && a.in.tokens <= 16384; }
+// bf16 outputs need 11 significand bits of every operand, fp32 outputs 22;
+// final states are fp32 whatever the tokens are.
+int planes_of(const SeqLaunch& a) { return a.shape.dtype == OFRL_DTYPE_F32 || a.final_state ? 2 : 1; }
+
+// Whether token by token is the faster way, by estimates of both in us.  Token
+// by token: a step of an episode takes 0.28 us, a CTA costs 3.7 ns of the whole
+// GPU's time to start and 32 lanes' share of a token 0.11 ns.  Chunked: 10.4 us
+// for two launches and one chunk (13.8 with two planes), then 25 ns for each
+// chunk of a head, times the planes, twice for more than 64 channels.  The host
+// knows the mean length only and takes the longest episode for twice that; the
+// bound on the tokens keeps the worst case, all of them in one episode, at 2 ms.
+// Measured, two heads of 64, fp32, token by token / chunked: 16 episodes of 16
+// tokens 7.2 / 13.8 us, of 48 16.4 / 14.6; 1024 of 4 47.7 / 129.7; 256 of 32
+// 68.7 / 40.2.  Four heads of 128, bf16: 16 of 4 7.8 / 13.3, 64 of 16 68.9 / 22.2.
+bool recurrent(const SeqLaunch& a) {
+    if (a.in.tokens > 8192) return false;
+    const int lanes = a.shape.k_dim > 64 ? 32 : a.shape.k_dim > 32 ? 16 : 8;
+    const int rows = recur_rows(lanes), planes = planes_of(a);
+    const double heads = (double)a.episodes * a.shape.v_heads, length = (double)a.in.tokens / a.episodes;
+    const double ctas = heads * ((a.shape.v_dim + rows - 1) / rows);
+    const double token = 2.7 + std::max(0.28 * 2 * length, 0.0037 * ctas + 1.1e-4 * heads * length * a.shape.v_dim * lanes / 32);
+    const double chunks = heads * std::max(1.0, length / kChunk);
+    const bool wide = a.shape.k_dim > 64 || a.shape.v_dim > 64;
+    return token < (planes == 2 ? 13.8 : 10.4) + 0.025 * chunks * planes * (wide ? 2 : 1);
+}
 
 }  // namespace
 
@@ -89,9 +111,7 @@ cudaError_t launch_forward(const SeqLaunch& a, cudaStream_t st) {
     const Prepared p = prepared_at(a.saved ? a.saved : a.scratch, z);
     Images img = {};
     if (a.saved) img = images_at(a.saved + prepared_bytes(z), z);
-    // bf16 outputs need 11 significand bits of every operand, fp32 outputs 22;
-    // final states are fp32 whatever the tokens are
-    const int planes = a.shape.dtype == OFRL_DTYPE_F32 || a.final_state ? 2 : 1;
+    const int planes = planes_of(a);
     const cudaError_t e = launch_prep(a, p, planes, st);
     return e == cudaSuccess ? launch_chain_forward(a, p, img, planes, st) : e;
 }

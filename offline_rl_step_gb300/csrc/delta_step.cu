@@ -8,7 +8,6 @@ namespace ofrl {
 namespace delta {
 namespace {
 
-constexpr int kStepThreads = 128;
 constexpr int kAtOnce = 4;         // rows of one lane group, all in flight at once
 
 // One CTA: kAtOnce rows per lane group of one (token, value head) state.  A
@@ -102,19 +101,17 @@ cudaError_t run_step(const StepLaunch& a, cudaStream_t st) {
 
 // Short episodes, token by token: the same recurrence with the state in
 // registers.  A lane group has kRecurRows rows; a token costs two dot products
-// over the group's lanes and the update, about 0.25 us in all, so
+// over the group's lanes and the update, about 0.28 us in all, so
 // episodes of a few dozen tokens are through before the chunked path's two
-// launches would be (16 episodes of 16 tokens, two heads of 64, fp32: see the
-// table of cases).  Tokens are loaded kAhead at a time, a round ahead.
-constexpr int kRecurRows = 2, kAhead = 4;
-
-template <int LANES>
-constexpr int recur_rows() { return kStepThreads / LANES * kRecurRows; }
+// launches would be (16 episodes of 16 tokens, two heads of 64, fp32: 7.0 us
+// against 13.8).  What bounds it is that step's latency; with many episodes the
+// shuffles of its dot products, 0.11 ns for 32 lanes' share of a token.  Tokens are loaded kAhead at a time, a round ahead.
+constexpr int kAhead = 4;
 
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kStepThreads) delta_recur_kernel(const __grid_constant__ SeqLaunch a) {
     const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
-    constexpr int kRows = recur_rows<LANES>(), kGroups = kStepThreads / LANES;
+    constexpr int kRows = recur_rows(LANES), kGroups = kStepThreads / LANES;
     const unsigned slices = (unsigned)(dv + kRows - 1) / kRows;
     const unsigned item = blockIdx.x / slices;
     const int row0 = (int)(blockIdx.x - item * slices) * kRows + (int)threadIdx.x / LANES;
@@ -207,7 +204,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_recur_kernel(const __grid_
 
 template <typename T, int LANES>
 cudaError_t go_recur(const SeqLaunch& a, cudaStream_t st) {
-    const int rows = recur_rows<LANES>(), slices = (a.shape.v_dim + rows - 1) / rows;
+    const int rows = recur_rows(LANES), slices = (a.shape.v_dim + rows - 1) / rows;
     const int64_t grid = (int64_t)a.episodes * a.shape.v_heads * slices;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     delta_recur_kernel<T, LANES><<<(unsigned)grid, kStepThreads, 0, st>>>(a);
