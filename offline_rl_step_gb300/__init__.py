@@ -545,7 +545,7 @@ class DeltaRule:
     def poll_status(self, stream=None):
         words = (C.c_int32 * _abi.STAT_WORDS)()
         _abi.check("ofrl_delta_poll_status", self._lib.ofrl_delta_poll_status(self.handle, _stream(stream), words))
-        return {"bad_index": words[_abi.STAT_BAD_INDEX]}
+        return {"bad_index": words[_abi.STAT_BAD_INDEX], "timeout": words[_abi.STAT_TIMEOUT]}
 
     def workspace_bytes(self) -> int:
         return int(self._lib.ofrl_delta_workspace_bytes(C.byref(self.shape), self.max_tokens, self.max_episodes,
