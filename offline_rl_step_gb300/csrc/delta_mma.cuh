@@ -138,7 +138,11 @@ __device__ __forceinline__ float tile_max(const float (&x)[NT][4]) {
 // CG column groups in shared memory at `b` (NB planes of `plane` bytes).
 // TRANS: the image's rows run along k (else along n).  Planes i of a and j of
 // b are multiplied when i + j < max(NA, NB): what is dropped is below 2^-22.
-// KFROM..KTO: the k steps of 16 that are taken.
+// The tensor cores cut off what a sum cannot hold, so the small products come
+// first, for all k, while the sums are small: fp32 gradients of the keys over
+// 256 tokens end 4.2e-7 off, 6.0e-7 with all products of a k step together (the
+// error lies to one side), for 6% more time from reading plane 0 twice.
+// KTO: the k steps of 16 that are taken.
 template <int KTO, int NT, int NA, int NB, bool TRANS, int KA>
 __device__ __forceinline__ void gemm(float (&d)[NT][4], const uint32_t (&a)[NA][KA][4], uint32_t b, int plane, int CG,
                                      int t0) {
@@ -146,26 +150,26 @@ __device__ __forceinline__ void gemm(float (&d)[NT][4], const uint32_t (&a)[NA][
     const int m = lane >> 3, r = lane & 7;
     constexpr int NP = NA > NB ? NA : NB;
 #pragma unroll
-    for (int k = 0; k < KTO; ++k)
+    for (int ij = NP - 1; ij >= 0; --ij)
 #pragma unroll
-        for (int t = 0; t < NT; t += 2)
+        for (int k = 0; k < KTO; ++k)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                // matrices 0, 1: k halves of tile t; 2, 3: of tile t + 1
-                const int kg = 2 * k + (m & 1), ng = t0 + t + (m >> 1);
-                const uint32_t at = b + j * plane + (TRANS ? kg * CG + ng : ng * CG + kg) * kTile + r * 16;
-                uint32_t f[4];
-                if (TRANS)
-                    ldsm4t(f, at);
-                else
-                    ldsm4(f, at);
+            for (int t = 0; t < NT; t += 2)
 #pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    if (i + j < NP) {
-                        mma_h(d[t], a[i][k], f[0], f[1]);
-                        mma_h(d[t + 1], a[i][k], f[2], f[3]);
-                    }
-            }
+                for (int j = 0; j < NB; ++j) {
+                    const int i = ij - j;
+                    if (i < 0 || i >= NA) continue;
+                    // matrices 0, 1: k halves of tile t; 2, 3: of tile t + 1
+                    const int kg = 2 * k + (m & 1), ng = t0 + t + (m >> 1);
+                    const uint32_t at = b + j * plane + (TRANS ? kg * CG + ng : ng * CG + kg) * kTile + r * 16;
+                    uint32_t f[4];
+                    if (TRANS)
+                        ldsm4t(f, at);
+                    else
+                        ldsm4(f, at);
+                    mma_h(d[t], a[i][k], f[0], f[1]);
+                    mma_h(d[t + 1], a[i][k], f[2], f[3]);
+                }
 }
 
 template <int NT>
