@@ -41,17 +41,18 @@ struct PrepArgs {
     int32_t* status;
 };
 
-// Eight elements as they lie in memory.
+// 16 bytes into shared memory behind the thread's back; zeros where !in.
+__device__ __forceinline__ void cp16(uint32_t to, const void* from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
+// Eight elements as they lie in memory, 16 bytes in each place.
 template <typename T>
 struct Raw {
     uint4 v[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p) {
+    __device__ __forceinline__ void load(const uint8_t* p, int step) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = *reinterpret_cast<const uint4*>(p + i * step);
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[sizeof(T) / 2 - 1].x, v[sizeof(T) / 2 - 1].y,
@@ -156,58 +157,91 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     }
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
-    // group, so that a store of 8 lanes fills one 8x8 block.  All of a warp's
-    // loads of one of them go out before the first is used.
+    // group, so that a store of 8 lanes fills one 8x8 block.  Raw elements go to
+    // where their planes will be, all of them asked for at once; while they
+    // come, the decays are added up.  Rows and columns that are not there are
+    // zero.
     uint8_t* keys = a.keys + (slot * hk + khead) * KeyImage::bytes(DK, NT);
     const bool leave = head % group == 0;
-    constexpr int kBatch = 2;      // K's rows, then Q's
-#pragma unroll 1
-    for (int w0 = 0; w0 < 4; w0 += kBatch) {
-        const int r = lane & 7, c4 = lane >> 3;
-        Raw<T> raw[kBatch][CG / 4];
+    const int r = lane & 7, c4 = lane >> 3;
+    const uint32_t sm = umma::smem_u32(smem);
 #pragma unroll
-        for (int w = 0; w < kBatch; ++w) {
-            const int row = min((warp * 2 + (w & 1)) * 8 + r, rows - 1);      // rows and columns that are not there
-            const bool isq = w0 > 0;                                          // become zero below
-            const T* p = isq ? static_cast<const T*>(a.in.q) + (tok + row) * a.in.q_stride + (int64_t)khead * dk
-                             : static_cast<const T*>(a.in.k) + (tok + row) * a.in.k_stride + (int64_t)khead * dk;
+    for (int w = 0; w < 4; ++w) {
+        const int rg = warp * 2 + (w & 1), row = rg * 8 + r;
+        const bool isq = w >= 2;
+        const int64_t t = tok + min(row, rows - 1);
+        const T* p = isq ? static_cast<const T*>(a.in.q) + t * a.in.q_stride + (int64_t)khead * dk
+                         : static_cast<const T*>(a.in.k) + t * a.in.k_stride + (int64_t)khead * dk;
 #pragma unroll
-            for (int i = 0; i < CG / 4; ++i) {
-                const int col = (c4 + 4 * i) * 8;
-                raw[w][i].load(p + (col < dk ? col : 0));
-            }
+        for (int i = 0; i < CG / 4; ++i) {
+            const int col = (c4 + 4 * i) * 8;
+            const bool in = row < rows && col < dk;
+            const uint32_t to = sm + (isq ? 0 : kKey) + (rg * CG + c4 + 4 * i) * kTile + r * 16;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cp16(to + n * 2 * kKey, p + (in ? col + n * (16 / (int)sizeof(T)) : 0), in);
         }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    // Running sums of the log decays, in every warp; a warp leaves the vectors
+    // of its 16 tokens.
+    Two g[2];
 #pragma unroll
-        for (int w = 0; w < kBatch; ++w) {
-            const int rg = warp * 2 + (w & 1);
-            const bool isq = w0 > 0;
-            float m = 0.0f;
+    for (int i = 0; i < 2; ++i) {
+        const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
+        g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
+    }
+    Two sum = two_add(g[0], g[1]);
 #pragma unroll
-            for (int i = 0; i < CG / 4; ++i) {
-                if (rg * 8 + r >= rows || (c4 + 4 * i) * 8 >= dk) raw[w][i].clear();
-                float x[8];
-                raw[w][i].get(x);
+    for (int o = 1; o < 32; o <<= 1) {
+        const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+        const Two both = two_add(up, sum);
+        if (lane >= o) sum = both;
+    }
+    const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+    Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+    if (lane == 0) before = {0.0f, 0.0f};
+    const Two G[2] = {two_add(before, g[0]), sum};
+    float gam[2], rest[2], most = 1.0f;
 #pragma unroll
-                for (int z = 0; z < 8; ++z) m = fmaxf(m, fabsf(x[z]));
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float unit = row_unit(m), inv = pow2_inv(unit);
-            if (c4 == 0) (isq ? kqv : kap)[rg * 8 + r] = unit;
+    for (int i = 0; i < 2; ++i) {
+        gam[i] = exp2f(G[i].h + G[i].l);
+        rest[i] = exp2f((total.h - G[i].h) + (total.l - G[i].l));
+        most = fmaxf(most, rest[i]);
+    }
+    most = warp_max(most);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");      // a lane reads its own copies only
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {
+        const int rg = warp * 2 + (w & 1);
+        const bool isq = w >= 2;
+        uint8_t* to = smem + (isq ? 0 : kKey) + (rg * CG + c4) * kTile + r * 16;
+        Raw<T> raw[CG / 4];
+        float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < CG / 4; ++i) {
-                float x[8];
-                raw[w][i].get(x);
-                uint32_t pl[4][NT];
+        for (int i = 0; i < CG / 4; ++i) {
+            raw[i].load(to + 4 * i * kTile, 2 * kKey);
+            float x[8];
+            raw[i].get(x);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) planes_h<NT>(x[2 * z] * inv, x[2 * z + 1] * inv, pl[z]);
+            for (int z = 0; z < 8; ++z) m = fmaxf(m, fabsf(x[z]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const float unit = row_unit(m), inv = pow2_inv(unit);
+        if (c4 == 0) (isq ? kqv : kap)[rg * 8 + r] = unit;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 v = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
-                    const int at = n * kKey + (rg * CG + c4 + 4 * i) * kTile + r * 16;
-                    *reinterpret_cast<uint4*>(smem + (isq ? 0 : kKey) + n * kKey + at) = v;
-                    if (leave) *reinterpret_cast<uint4*>(keys + (isq ? NT * kKey : 0) + at) = v;
-                }
+        for (int i = 0; i < CG / 4; ++i) {
+            float x[8];
+            raw[i].get(x);
+            uint32_t pl[4][NT];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) planes_h<NT>(x[2 * z] * inv, x[2 * z + 1] * inv, pl[z]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+                *reinterpret_cast<uint4*>(to + 4 * i * kTile + n * 2 * kKey) = v;
+                if (leave)
+                    *reinterpret_cast<uint4*>(keys + (isq ? NT * kKey : 0) + n * kKey + (rg * CG + c4 + 4 * i) * kTile + r * 16) = v;
             }
         }
     }
@@ -236,53 +270,24 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         umma::commit(&bar);
     }
     __syncwarp();
-    {
-        // Running sums of the log decays, in every warp; a warp leaves the
-        // vectors of its 16 tokens.
-        Two g[2];
+    if ((lane >> 3) == warp) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
-            g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
-        }
-        Two sum = two_add(g[0], g[1]);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
-            const Two both = two_add(up, sum);
-            if (lane >= o) sum = both;
-        }
-        const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
-        Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
-        if (lane == 0) before = {0.0f, 0.0f};
-        const Two G[2] = {two_add(before, g[0]), sum};
-        float gam[2], rest[2], most = 1.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            gam[i] = exp2f(G[i].h + G[i].l);
-            rest[i] = exp2f((total.h - G[i].h) + (total.l - G[i].l));
-            most = fmaxf(most, rest[i]);
-        }
-        most = warp_max(most);
-        if ((lane >> 3) == warp) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                const float b = t < rows ? to_f(bin[i]) : 0.0f, k = kap[t];
-                const float bk = b * k * k, qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
-                vec[V_GHI * kChunk + t] = G[i].h;
-                vec[V_GLO * kChunk + t] = G[i].l;
-                vec[V_GAM * kChunk + t] = gam[i];
-                vec[V_REST * kChunk + t] = rest[i];
-                vec[V_BETA * kChunk + t] = bk;
-                vec[V_KINV * kChunk + t] = pow2_inv(k);
-                vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
-                vec[V_QS * kChunk + t] = qs;
-                vec[V_OS * kChunk + t] = qs * gam[i];
-                vec[V_DV * kChunk + t] = b * k;
-                vec[V_DS * kChunk + t] = bk * gam[i];
-                if (t == 0) vec[V_MISC * kChunk] = most;
-            }
+            const int t = 2 * lane + i;
+            const float b = t < rows ? to_f(bin[i]) : 0.0f, k = kap[t];
+            const float bk = b * k * k, qs = t < rows ? a.in.scale * kqv[t] : 0.0f;
+            vec[V_GHI * kChunk + t] = G[i].h;
+            vec[V_GLO * kChunk + t] = G[i].l;
+            vec[V_GAM * kChunk + t] = gam[i];
+            vec[V_REST * kChunk + t] = rest[i];
+            vec[V_BETA * kChunk + t] = bk;
+            vec[V_KINV * kChunk + t] = pow2_inv(k);
+            vec[V_QINV * kChunk + t] = pow2_inv(kqv[t]);
+            vec[V_QS * kChunk + t] = qs;
+            vec[V_OS * kChunk + t] = qs * gam[i];
+            vec[V_DV * kChunk + t] = b * k;
+            vec[V_DS * kChunk + t] = bk * gam[i];
+            if (t == 0) vec[V_MISC * kChunk] = most;
         }
     }
     __syncthreads();      // the vectors are there
