@@ -15,6 +15,7 @@
 // nothing but a largest magnitude passes between warps.  Bulk copies keep a
 // ring of stages filled.
 
+#include <algorithm>
 #include <cmath>
 
 #include "delta_mma.cuh"
@@ -814,28 +815,42 @@ bool forward_on_tcgen05(const SeqLaunch& a) {
     return rows_of_tcgen05(a.shape) && (a.saved || 2LL * a.episodes * a.shape.v_heads > a.num_sms);
 }
 
+// CTAs of the forward pass that share an SM.
+template <typename T, int DK, int NM>
+constexpr int together() { return Stage<T, DK, NM, 4>::kShared <= 112 * 1024 ? 2 : 1; }
+int forward_together(const ofrl_delta_shape& s, int planes) {
+    const bool wide = s.k_dim > 64;
+    if (s.dtype == OFRL_DTYPE_F32) return wide ? together<float, 128, 2>() : together<float, 64, 2>();
+    if (planes == 2) return wide ? together<__nv_bfloat16, 128, 2>() : together<__nv_bfloat16, 64, 2>();
+    return wide ? together<__nv_bfloat16, 128, 1>() : together<__nv_bfloat16, 64, 1>();
+}
+
 // Parts of an episode.  A forward pass takes one CTA per head and 64 value
 // channels; where these leave most SMs idle and episodes are long, each is cut
 // into parts: summaries of all parts at once, the short chain over them, then
 // all parts at once.  That is about 1.7 times the work and a step of the chain
 // over parts costs about 0.4 chunks' time, so n chunks in g parts take about
-// 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, if the SMs hold as
-// many summaries (two CTAs each).  One sequence of 32768 tokens, four heads of
-// 128: 2100 us whole, see the table of cases for the time in parts.
-int segments_of(const SeqLaunch& a) {
+// 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, but no more than the
+// SMs hold at once in the last pass (a few CTAs more would be a second round).
+// One sequence of 32768 tokens, four heads of 128, with its final state: 2100 us
+// whole, 427 in 20 parts (160 CTAs on 152 SMs), 362 in 19.  Three of 1000 tokens,
+// two heads of 64, fp32: 73 us whole, 38 in 7 parts of 3 chunks, 33 in 8 of 2.
+int segments_of(const SeqLaunch& a, int planes) {
     const int64_t items = (int64_t)a.episodes * a.shape.v_heads;
-    const int rows = (a.shape.v_dim + 63) / 64 + (a.shape.k_dim + 63) / 64;
+    const int slices = (a.shape.v_dim + 63) / 64;
     const double chunks = (double)a.in.tokens / kChunk / a.episodes;
-    const int64_t room = 2 * (int64_t)a.num_sms / (items * rows) + 1;
-    const int64_t best = (int64_t)(2.0 * std::sqrt(chunks));
-    const int64_t g = best < room ? best : room;
-    return g >= 4 && chunks >= 12.0 ? (int)g : 1;
+    const int64_t room = (int64_t)forward_together(a.shape, planes) * a.num_sms / (items * slices);
+    if (room < 4 || chunks < 12.0) return 1;
+    // whole chunks to a part
+    const double part = std::max(std::round(0.5 * std::sqrt(chunks)), std::ceil(chunks / (double)room));
+    const int g = (int)std::ceil(chunks / part);
+    return g >= 4 ? g : 1;
 }
 
 cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Images& img, int planes, cudaStream_t st) {
     ChainArgs c = base_args(a, p, img);
     if (!a.saved) {
-        c.segments = segments_of(a);
+        c.segments = segments_of(a, planes);
         const int dkp = pad_dim(a.shape.k_dim);
         const int64_t parts = (int64_t)a.episodes * a.shape.v_heads * c.segments;
         uint8_t* at = a.parts;

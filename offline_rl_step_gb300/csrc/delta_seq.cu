@@ -92,8 +92,8 @@ int64_t scratch_bytes(const ofrl_delta_shape& s, int64_t tokens, int64_t episode
     return f > b ? f : b;
 }
 
-// Room for the parts of a forward pass: segments_of() makes at most 2 num_sms +
-// (episodes x heads) of them, with fewer episodes x heads than 2 num_sms / 3.
+// Room for the parts of a forward pass: segments_of() makes no more of them
+// than the SMs hold CTAs, two each.
 int64_t parts_bytes(const ofrl_delta_shape& s, int64_t tokens, int num_sms) {
     if (tokens < 12 * kChunk) return 0;
     const int64_t dk = pad_dim(s.k_dim);
