@@ -752,7 +752,7 @@ cudaError_t go(int nw, int smem, bool early, int per_head, const ChainArgs& c, c
 }
 
 template <typename T, int DK, int NM>
-cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
+cudaError_t forward(const ChainArgs& c, int num_sms, cudaStream_t st) {
     using S4 = Stage<T, DK, NM, 4>;
     const int slices = (c.shape.v_dim + 63) / 64;
     if (c.state_img)
@@ -766,6 +766,14 @@ cudaError_t forward(const ChainArgs& c, cudaStream_t st) {
             e = go<delta_join_kernel<DK>>(4, Join<DK>::kShared, true, (c.shape.v_dim + 15) / 16, c, st);
         if (e != cudaSuccess) return e;
     }
+    // More than 64 channels: two CTAs of four warps per head, or one of eight,
+    // which reads keys and pairs once, where heads alone fill the SMs (bf16 with
+    // one plane is on tcgen05 then).  400 heads of 300 tokens of 128 x 128, fp32:
+    // 330 us against 275; 462 ragged ones of 40 x 72 126 against 108; 80 heads
+    // of 64 x 96 87 against 88.
+    if constexpr (NM == 2)
+        if (c.segments == 1 && c.shape.v_dim > 64 && (int64_t)c.episodes * c.shape.v_heads >= num_sms)
+            return go<delta_forward_kernel<T, DK, NM, 8, kOutputs>>(8, Stage<T, DK, NM, 8>::kShared, true, 1, c, st);
     return go<delta_forward_kernel<T, DK, NM, 4, kOutputs>>(4, S4::kShared, true, slices * c.segments, c, st);
 }
 template <typename T, int DK>
@@ -867,9 +875,9 @@ cudaError_t launch_chain_forward(const SeqLaunch& a, const Prepared& p, const Im
     c.row_stride = a.in.v_stride;
     if (forward_on_tcgen05(a) && planes == 1 && c.segments == 1) return launch_chain_forward_tc(a, p, img, st);
     const bool wide = a.shape.k_dim > 64;
-    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? forward<float, 128, 2>(c, st) : forward<float, 64, 2>(c, st);
-    if (planes == 2) return wide ? forward<__nv_bfloat16, 128, 2>(c, st) : forward<__nv_bfloat16, 64, 2>(c, st);
-    return wide ? forward<__nv_bfloat16, 128, 1>(c, st) : forward<__nv_bfloat16, 64, 1>(c, st);
+    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? forward<float, 128, 2>(c, a.num_sms, st) : forward<float, 64, 2>(c, a.num_sms, st);
+    if (planes == 2) return wide ? forward<__nv_bfloat16, 128, 2>(c, a.num_sms, st) : forward<__nv_bfloat16, 64, 2>(c, a.num_sms, st);
+    return wide ? forward<__nv_bfloat16, 128, 1>(c, a.num_sms, st) : forward<__nv_bfloat16, 64, 1>(c, a.num_sms, st);
 }
 
 cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st) {
