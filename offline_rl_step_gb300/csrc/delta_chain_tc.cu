@@ -2,18 +2,25 @@
 // than 64 value channels, on tcgen05 (delta_chain.cu has the formulas and the
 // passes for everything else).
 //
-// The value channels are the 128 accumulator rows, so a thread has a row: no
-// value passes between threads but the largest magnitude of a saved image.
-// One warpgroup ("tokens") turns the products over a chunk's tokens into the
-// next one's operand, the other ("state") keeps the state's rows in its
-// registers and makes them an operand; operands go through shared memory,
-// where they also are the images the backward pass wants.  Per chunk,
-// forward:
-//   X = S [K; Q]^T -> x -> U = x T^T -> dS = (rest U) K -> S     (the chain)
-//                                    -> O2 = U P^T -> outputs    (beside it)
-// About 3.5 us a chunk of 128 x 128 go down to the latency of three products
-// and three conversions; mma.sync with 16 rows a warp reads every operand
-// eight times from shared memory instead.
+// The value channels are the 128 accumulator rows.  Two warpgroups ("tokens")
+// turn the products over a chunk's tokens into the next one's operand, two
+// ("state") keep the state's rows in their registers and make them an operand;
+// a thread has a row and half of the columns.  Operands go through shared
+// memory, where they also are the images that the gradients want.  Per chunk:
+//   forward   X = S K^T -> x -> U = x T^T -> S += (rest U) K            (the chain)
+//             beside it S Q^T, U P^T -> outputs
+//   backward  X = dS K^T, dO P -> dU -> R = dU T -> dS -= (gamma dv) K  (the chain)
+//             beside it dS += (gamma dO) Q, R -> dv
+// What is beside the chain is made by the warps that would wait: outputs and dv
+// of a chunk by the state's warps after they have left the next chunk's state,
+// dO's operands by the tokens' warps while the state is on its way.
+//
+// Bound by the chain's latency, three products (0.3 to 0.8 us each with their
+// operands' reads) and three conversions: 4 us a chunk of 128 x 128 forward, 5
+// back.  About 65k ragged transitions, four heads of 128 x 128: 137 us forward
+// (4.3 TB/s in all), 161 us back.  With two warpgroups and every token element
+// read and written by itself 219 and 285; with outputs and dv by the tokens'
+// warps 164 and 165.
 
 #include "delta_mma.cuh"
 
@@ -223,11 +230,13 @@ __device__ __forceinline__ void eight_tokens(const Turn& t, int i, float (&x)[8]
     }
 }
 // h: this channel's tokens in pairs.
-__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c, const uint32_t (&h)[kHalf / 2]) {
+__device__ __forceinline__ void store_tokens(const TcArgs& a, const Episode& w, const Turn& t, int c,
+                                             const uint32_t (&h)[kHalf / 2]) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(t.mine + ((i ^ t.mine_swap) << 4)) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        *reinterpret_cast<uint4*>(t.mine + ((i ^ t.mine_swap) << 4)) =
+            make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
     __syncwarp();
     const bool in = t.channel < a.shape.v_dim;
     __nv_bfloat16* to = a.out + ((int64_t)w.sp.start + (int64_t)c * kChunk + t.token) * a.out_stride +
@@ -304,7 +313,9 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
     const int col = half * kHalf, at = at_row + half * (kHalf / 8) * kCol;      // of its tokens
     float* row_most = reinterpret_cast<float*>(smem + S::off_row);
-    auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
+    auto vec_of = [&](int n) {
+        return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare);
+    };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
     if (threadIdx.x < kTokThreads) {
@@ -352,8 +363,8 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             group_sync<1>();
             umma::fence_after_sync();
             if (threadIdx.x == 0) {
-                mma_run(tmem + t_u, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol, umma::smem_desc(pair, 8 * kTile, kTile),
-                        2 * 8 * kTile, kIdT, 4);
+                mma_run(tmem + t_u, umma::smem_desc(base + S::off_a, kCol, kTile), 2 * kCol,
+                        umma::smem_desc(pair, 8 * kTile, kTile), 2 * 8 * kTile, kIdT, 4);
                 umma::commit(&b.t);
                 if (SAVE) umma::bulk_wait_read();      // U's image of the chunk before
             }
@@ -527,7 +538,9 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     const int at_row = (row >> 3) * kTile + (row & 7) * 16;      // of a row in an operand image
     const int col = half * kHalf, at = at_row + half * (kHalf / 8) * kCol;      // of its tokens
     float* row_most = reinterpret_cast<float*>(smem + S::off_row);
-    auto vec_of = [&](int n) { return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare); };
+    auto vec_of = [&](int n) {
+        return reinterpret_cast<const float*>(smem + S::off_stage + (n & 1) * S::kStage + 2 * S::kKey + 2 * kSquare);
+    };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
     if (threadIdx.x < kTokThreads) {

@@ -1,9 +1,9 @@
 // Gradients of q, k, log decay and write strength for fp32 tokens, chunk by
 // chunk: everything that contracts over the value channels (see delta_seq.cu
-// for the formulas and delta_mma.cuh for the scaled quantities).  One CTA of eight warps per
-// (chunk, key head), looping over the group's value heads, whose gradients it
-// adds up in registers; warp (rb, hf) has the token rows 16 rb .. and, of
-// each product's columns, half hf.
+// for the formulas and delta_mma.cuh for the scaled quantities).  One CTA of
+// eight warps per (chunk, key head), looping over the group's value heads, whose
+// gradients it adds up in registers; warp (rb, hf) has the token rows 16 rb ..
+// and, of each product's columns, half hf.
 //
 // Per value head, with N1 = dO U^T and N2 = R U^T:
 //   dPD_ij = D_ij N1_ij (j <= i),  E_ij = -D_ij N2_ij (j < i),  M_ij = beta_i E_ij
@@ -13,6 +13,10 @@
 //   N_ij = dPD_ij (q_i k_j) + M_ij (k_i k_j)
 // (k, v, beta, U, dO scaled as in delta_mma.cuh, dO with scale and kq in it).
 // The states come in slices of 32 key channels.
+//
+// mma.sync with two planes, three products for each one: bound by them and by
+// the operands' reads from shared memory.  640 CTAs of 64 x 64 (16384 tokens)
+// 66 us.
 
 #include "delta_mma.cuh"
 
