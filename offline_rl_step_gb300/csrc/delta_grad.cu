@@ -16,7 +16,7 @@
 //
 // mma.sync with two planes, three products for each one: bound by them and by
 // the operands' reads from shared memory.  640 CTAs of 64 x 64 (16384 tokens)
-// 66 us.
+// 61 us.
 
 #include "delta_mma.cuh"
 
@@ -132,6 +132,24 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
         copy_head(khead * group);
         for (int n = 0; n < Sh::kRing && n < SL; ++n) copy_slice(khead * group, n);
     }
+    // dO rows i0, i0 + 8 of this thread, as they are; the first head's come while
+    // the keys do, where registers allow
+    float x[2 * KV][4];
+    auto load_dout = [&](int head) {
+        const T* po = static_cast<const T*>(a.dout) + (tok * hv + head) * dv;
+#pragma unroll
+        for (int t = 0; t < 2 * KV; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = rb * 16 + row4 + 8 * h, c = t * 8 + col2;
+                float2 v = make_float2(0.0f, 0.0f);
+                if (i < rows && c < dv) v = *reinterpret_cast<const float2*>(po + (int64_t)i * hv * dv + c);
+                x[t][2 * h] = v.x;
+                x[t][2 * h + 1] = v.y;
+            }
+    };
+    constexpr bool kEarly = KV <= 4;
+    if (kEarly) load_dout(khead * group);
     bool ok = true;      // a wait that gave up: computing goes on with what is there, nothing is written
     ok &= umma::mbar_wait(&bar_keys, 0, kWaitNs);
 
@@ -163,6 +181,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
         const int head = khead * group + g;
         const float su = a.s_unit[at0 + head], uu = a.u_unit[at0 + head], du = a.d_unit[at0 + head],
                     ru = a.r_unit[at0 + head];
+        if (!kEarly || g > 0) load_dout(head);
         ok &= umma::mbar_wait(&bar_head, (uint32_t)g & 1u, kWaitNs);
         const float *gam = vec + V_GAM * kChunk, *rest = vec + V_REST * kChunk, *beta = vec + V_BETA * kChunk;
         const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk;
@@ -173,18 +192,14 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
         int o_exp;
         float rv[2] = {0.0f, 0.0f};
         {
-            float x[2 * KV][4];
-            const T* po = static_cast<const T*>(a.dout) + (tok * hv + head) * dv;
             const T* pv = static_cast<const T*>(a.in.v) + tok * a.in.v_stride + (int64_t)head * dv;
 #pragma unroll
             for (int t = 0; t < 2 * KV; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int i = i0 + 8 * h, c = t * 8 + col2;
-                    const bool on = i < rows && c < dv;
-                    const float f = vec[V_QS * kChunk + i];
-                    x[t][2 * h] = on ? to_f(po[(int64_t)i * hv * dv + c]) * f : 0.0f;
-                    x[t][2 * h + 1] = on ? to_f(po[(int64_t)i * hv * dv + c + 1]) * f : 0.0f;
+                    const float f = vec[V_QS * kChunk + i0 + 8 * h];
+                    x[t][2 * h] *= f;
+                    x[t][2 * h + 1] *= f;
                 }
             const float up = scale_up(tile_max(x));
             o_exp = -exponent(up);
