@@ -10,9 +10,9 @@
 // [Q; K] K^T is one 128 x 64 product on tcgen05, read back a row per thread:
 // two warps make P's rows, two A's, while the decays are added up before.
 //
-// T.  1 + A is unit lower triangular with blocks of 16.  Warp w inverts the
-// diagonal block w by forward substitution (a lane per column) and then makes
-// T's block column w, transposed, block after block:
+// T.  1 + A is unit lower triangular with blocks of 16.  The diagonal blocks are
+// inverted by forward substitution (a lane per column); then warp w makes T's
+// block column w, transposed, block after block:
 //   T_rw^T = -(sum_{s=w}^{r-1} T_sw^T A_rs^T) T_rr^T.
 // T^T's blocks lie on and above the diagonal of the image that holds A's below
 // it.  Substitution, not a series of powers of A: with correlated keys the
@@ -153,13 +153,18 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         umma::fence_mbar_init();
     }
     if (warp == 3) umma::tmem_alloc(&s_tmem, kChunk);
-    T gin[2], bin[2];      // tokens 2 lane, + 1 (past the end: the last one's, not used), in every warp
+    // One warp adds up the decays and two invert the diagonal blocks; which ones
+    // changes from CTA to CTA, so that every scheduler of an SM gets its share.
+    const int chosen = (int)(blockIdx.x * 0x9E3779B1u >> 30);
+    const bool adds = warp == chosen, inverts = (warp >> 1) == (chosen & 1);
+    T gin[2], bin[2];      // tokens 2 lane, + 1 (past the end: the last one's, not used)
+    if (adds)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t t = tok + min(2 * lane + i, rows - 1);
-        gin[i] = static_cast<const T*>(a.in.g)[t * a.in.g_stride + head];
-        bin[i] = static_cast<const T*>(a.in.beta)[t * a.in.beta_stride + head];
-    }
+        for (int i = 0; i < 2; ++i) {
+            const int64_t t = tok + min(2 * lane + i, rows - 1);
+            gin[i] = static_cast<const T*>(a.in.g)[t * a.in.g_stride + head];
+            bin[i] = static_cast<const T*>(a.in.beta)[t * a.in.beta_stride + head];
+        }
 
     // K and Q: a warp takes eight rows at a time, lane = row + 8 * column
     // group, so that a store of 8 lanes fills one 8x8 block.  Raw elements go to
@@ -187,33 +192,36 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    // Running sums of the log decays, in every warp; a warp leaves the vectors
-    // of its 16 tokens.
-    Two g[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
-        g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
-    }
-    Two sum = two_add(g[0], g[1]);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
-        const Two both = two_add(up, sum);
-        if (lane >= o) sum = both;
-    }
-    const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
-    Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
-    if (lane == 0) before = {0.0f, 0.0f};
-    const Two G[2] = {two_add(before, g[0]), sum};
+    // Running sums of the log decays.
+    Two G[2];
     float gam[2], rest[2], most = 1.0f;
+    if (adds) {
+        Two g[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        gam[i] = exp2f(G[i].h + G[i].l);
-        rest[i] = exp2f((total.h - G[i].h) + (total.l - G[i].l));
-        most = fmaxf(most, rest[i]);
+        for (int i = 0; i < 2; ++i) {
+            const float x = 2 * lane + i < rows ? to_f(gin[i]) : 0.0f;
+            g[i] = two_log2(x < kMinLogDecay ? kMinLogDecay : x);      // a NaN stays
+        }
+        Two sum = two_add(g[0], g[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Two up = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+            const Two both = two_add(up, sum);
+            if (lane >= o) sum = both;
+        }
+        const Two total = {__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+        Two before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+        if (lane == 0) before = {0.0f, 0.0f};
+        G[0] = two_add(before, g[0]);
+        G[1] = sum;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            gam[i] = exp2f(G[i].h + G[i].l);
+            rest[i] = exp2f((total.h - G[i].h) + (total.l - G[i].l));
+            most = fmaxf(most, rest[i]);
+        }
+        most = warp_max(most);
     }
-    most = warp_max(most);
     asm volatile("cp.async.wait_group 0;" ::: "memory");      // a lane reads its own copies only
 #pragma unroll 1
     for (int w = 0; w < 4; ++w) {
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         umma::commit(&bar);
     }
     __syncwarp();
-    if ((lane >> 3) == warp) {
+    if (adds) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
@@ -369,10 +377,10 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     umma::fence_before_sync();
     __syncthreads();
     const uint32_t ab = umma::smem_u32(aimg);
-    {
+    if (inverts) {
         // column c of the inverse: when x_j is known, it leaves every later row
-        const float* D = diag + warp * 16 * kPitch;
-        const int c = lane & 15;
+        const int c = lane & 15, w = 2 * (warp & 1) + (lane >> 4);
+        const float* D = diag + w * 16 * kPitch;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
@@ -386,17 +394,17 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
                 for (int z = 0; z < 4; ++z)
                     if (4 * q + z > j) x[4 * q + z] = fmaf(-av[z], x[j], x[4 * q + z]);
             }
-        if (lane < 16)      // row c of T_ww^T
+        // row c of T_ww^T
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pl[4][NB];
+        for (int h = 0; h < 2; ++h) {
+            uint32_t pl[4][NB];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) planes_b<NB>(x[8 * h + 2 * z], x[8 * h + 2 * z + 1], pl[z]);
+            for (int z = 0; z < 4; ++z) planes_b<NB>(x[8 * h + 2 * z], x[8 * h + 2 * z + 1], pl[z]);
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    *reinterpret_cast<uint4*>(aimg + n * kSquare + ((2 * warp + (c >> 3)) * 8 + 2 * warp + h) * kTile +
-                                              (c & 7) * 16) = make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
-            }
+            for (int n = 0; n < NB; ++n)
+                *reinterpret_cast<uint4*>(aimg + n * kSquare + ((2 * w + (c >> 3)) * 8 + 2 * w + h) * kTile + (c & 7) * 16) =
+                    make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+        }
     }
     __syncthreads();
     // block (row block, column block) of the image as a fragment
