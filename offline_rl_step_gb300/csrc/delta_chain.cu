@@ -529,8 +529,9 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Work w = work_of(a, 1, NW * 16, 1, 1);
+    pdl_wait();
     pdl_trigger();
+    const Work w = work_of(a, 1, NW * 16, 1, 1);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     ring_init<NW>(ring);
     uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
@@ -746,15 +747,13 @@ __global__ void __launch_bounds__(128) delta_join_kernel(const __grid_constant__
 }
 
 template <auto KERNEL>
-cudaError_t go(int nw, int smem, bool early, int per_head, const ChainArgs& c, cudaStream_t st) {
+cudaError_t go(int nw, int smem, int per_head, const ChainArgs& c, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * per_head;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     const cudaError_t e = opt_in(KERNEL, smem, done);
     if (e != cudaSuccess) return e;
-    if (early) return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(nw * 32), smem, st, c);
-    KERNEL<<<(unsigned)grid, nw * 32, smem, st>>>(c);
-    return cudaGetLastError();
+    return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(nw * 32), smem, st, c);
 }
 
 template <typename T, int DK, int NM>
@@ -763,13 +762,13 @@ cudaError_t forward(const ChainArgs& c, int num_sms, cudaStream_t st) {
     const int slices = (c.shape.v_dim + 63) / 64;
     if (c.state_img)
         return c.shape.v_dim > 64
-                   ? go<delta_forward_kernel<T, DK, NM, 8, kSave>>(8, Stage<T, DK, NM, 8>::kShared, true, 1, c, st)
-                   : go<delta_forward_kernel<T, DK, NM, 4, kSave>>(4, S4::kShared, true, 1, c, st);
+                   ? go<delta_forward_kernel<T, DK, NM, 8, kSave>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st)
+                   : go<delta_forward_kernel<T, DK, NM, 4, kSave>>(4, S4::kShared, 1, c, st);
     if (c.segments > 1) {
-        cudaError_t e = go<delta_forward_kernel<T, DK, NM, 4, kSummary>>(4, S4::kShared, true,
+        cudaError_t e = go<delta_forward_kernel<T, DK, NM, 4, kSummary>>(4, S4::kShared,
                            (slices + DK / 64) * (c.segments - 1), c, st);
         if (e == cudaSuccess && c.segments > 2)
-            e = go<delta_join_kernel<DK>>(4, Join<DK>::kShared, true, (c.shape.v_dim + 15) / 16, c, st);
+            e = go<delta_join_kernel<DK>>(4, Join<DK>::kShared, (c.shape.v_dim + 15) / 16, c, st);
         if (e != cudaSuccess) return e;
     }
     // More than 64 channels: two CTAs of four warps per head, or one of eight,
@@ -779,14 +778,14 @@ cudaError_t forward(const ChainArgs& c, int num_sms, cudaStream_t st) {
     // of 64 x 96 87 against 88.
     if constexpr (NM == 2)
         if (c.segments == 1 && c.shape.v_dim > 64 && (int64_t)c.episodes * c.shape.v_heads >= num_sms)
-            return go<delta_forward_kernel<T, DK, NM, 8, kOutputs>>(8, Stage<T, DK, NM, 8>::kShared, true, 1, c, st);
-    return go<delta_forward_kernel<T, DK, NM, 4, kOutputs>>(4, S4::kShared, true, slices * c.segments, c, st);
+            return go<delta_forward_kernel<T, DK, NM, 8, kOutputs>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st);
+    return go<delta_forward_kernel<T, DK, NM, 4, kOutputs>>(4, S4::kShared, slices * c.segments, c, st);
 }
 template <typename T, int DK>
 cudaError_t reverse(const ChainArgs& c, cudaStream_t st) {
     constexpr int NM = sizeof(T) == 4 ? 2 : 1;
-    return c.shape.v_dim > 64 ? go<delta_reverse_kernel<T, DK, 8>>(8, Stage<T, DK, NM, 8>::kShared, false, 1, c, st)
-                              : go<delta_reverse_kernel<T, DK, 4>>(4, Stage<T, DK, NM, 4>::kShared, false, 1, c, st);
+    return c.shape.v_dim > 64 ? go<delta_reverse_kernel<T, DK, 8>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st)
+                              : go<delta_reverse_kernel<T, DK, 4>>(4, Stage<T, DK, NM, 4>::kShared, 1, c, st);
 }
 
 ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {

@@ -524,9 +524,10 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) Bars b;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
+    pdl_wait();
+    pdl_trigger();
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
-    pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     init_bars(b);
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
@@ -762,14 +763,12 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
 }
 
 template <auto KERNEL, int DK>
-cudaError_t go(const TcArgs& c, int64_t grid, bool early, cudaStream_t st) {
+cudaError_t go(const TcArgs& c, int64_t grid, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     const cudaError_t e = opt_in(KERNEL, Smem<DK>::kBytes, done);
     if (e != cudaSuccess) return e;
-    if (early) return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(kThreads), Smem<DK>::kBytes, st, c);
-    KERNEL<<<(unsigned)grid, kThreads, Smem<DK>::kBytes, st>>>(c);
-    return cudaGetLastError();
+    return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(kThreads), Smem<DK>::kBytes, st, c);
 }
 
 TcArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
@@ -800,10 +799,10 @@ cudaError_t launch_chain_forward_tc(const SeqLaunch& a, const Prepared& p, const
     c.row_stride = a.in.v_stride;
     const int64_t grid = (int64_t)a.episodes * a.shape.v_heads;
     if (a.shape.k_dim > 64)
-        return a.saved ? go<delta_forward_tc_kernel<128, true>, 128>(c, grid, true, st)
-                       : go<delta_forward_tc_kernel<128, false>, 128>(c, grid, true, st);
-    return a.saved ? go<delta_forward_tc_kernel<64, true>, 64>(c, grid, true, st)
-                   : go<delta_forward_tc_kernel<64, false>, 64>(c, grid, true, st);
+        return a.saved ? go<delta_forward_tc_kernel<128, true>, 128>(c, grid, st)
+                       : go<delta_forward_tc_kernel<128, false>, 128>(c, grid, st);
+    return a.saved ? go<delta_forward_tc_kernel<64, true>, 64>(c, grid, st)
+                   : go<delta_forward_tc_kernel<64, false>, 64>(c, grid, st);
 }
 
 cudaError_t launch_chain_reverse_tc(const SeqLaunch& a, const Prepared& p, const Images& img, cudaStream_t st) {
@@ -815,8 +814,8 @@ cudaError_t launch_chain_reverse_tc(const SeqLaunch& a, const Prepared& p, const
     c.rows = static_cast<const __nv_bfloat16*>(a.dout);
     c.row_stride = (int64_t)a.shape.v_heads * a.shape.v_dim;
     const int64_t grid = (int64_t)a.episodes * a.shape.v_heads;
-    return a.shape.k_dim > 64 ? go<delta_reverse_tc_kernel<128>, 128>(c, grid, false, st)
-                              : go<delta_reverse_tc_kernel<64>, 64>(c, grid, false, st);
+    return a.shape.k_dim > 64 ? go<delta_reverse_tc_kernel<128>, 128>(c, grid, st)
+                              : go<delta_reverse_tc_kernel<64>, 64>(c, grid, st);
 }
 
 }  // namespace delta

@@ -139,6 +139,9 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     const int64_t slot = blockIdx.x / hv;
     const int head = blockIdx.x % hv, khead = head / group;
     const int32_t tokens = (int32_t)a.in.tokens;
+    // The chain that follows reads the caller's buffers before it waits for this
+    // kernel: what came before has to be done by then.
+    pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < a.episodes; e += kPrepThreads)
@@ -526,8 +529,7 @@ cudaError_t run(const PrepArgs& p, int64_t grid, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = opt_in(delta_prep_kernel<T, DK, NM>, smem, done);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<T, DK, NM><<<(unsigned)grid, kPrepThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(delta_prep_kernel<T, DK, NM>, dim3((unsigned)grid), dim3(kPrepThreads), smem, st, p);
 }
 
 }  // namespace
