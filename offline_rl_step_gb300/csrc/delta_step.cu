@@ -22,6 +22,7 @@ constexpr int step_rows() { return kStepThreads / LANES * kAtOnce; }
 
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const __grid_constant__ StepLaunch a) {
+    pdl_wait();
     const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
     constexpr int kRows = step_rows<LANES>();
     const unsigned slices = (unsigned)(dv + kRows - 1) / kRows;
@@ -91,8 +92,7 @@ cudaError_t go(const StepLaunch& a, cudaStream_t st) {
     const int rows = step_rows<LANES>(), slices = (a.shape.v_dim + rows - 1) / rows;
     const int64_t grid = a.in.tokens * a.shape.v_heads * slices;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    delta_step_kernel<T, LANES><<<(unsigned)grid, kStepThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(delta_step_kernel<T, LANES>, dim3((unsigned)grid), dim3(kStepThreads), 0, st, a);
 }
 
 template <typename T>
@@ -112,6 +112,7 @@ constexpr int kAhead = 4;
 
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kStepThreads) delta_recur_kernel(const __grid_constant__ SeqLaunch a) {
+    pdl_wait();
     const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
     constexpr int kRows = recur_rows(LANES), kGroups = kStepThreads / LANES;
     const unsigned slices = (unsigned)(dv + kRows - 1) / kRows;
@@ -209,8 +210,7 @@ cudaError_t go_recur(const SeqLaunch& a, cudaStream_t st) {
     const int rows = recur_rows(LANES), slices = (a.shape.v_dim + rows - 1) / rows;
     const int64_t grid = (int64_t)a.episodes * a.shape.v_heads * slices;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    delta_recur_kernel<T, LANES><<<(unsigned)grid, kStepThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(delta_recur_kernel<T, LANES>, dim3((unsigned)grid), dim3(kStepThreads), 0, st, a);
 }
 
 template <typename T>

@@ -238,6 +238,7 @@ __device__ __forceinline__ void scale_part(const NormLaunch& a, int64_t warp, in
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int W = kThreads / 32;
+    pdl_wait();
     const Sums part = block_sums<W>(norm_part(a, blockIdx.x * (int64_t)W + (threadIdx.x >> 5), gridDim.x * (int64_t)W));
     __shared__ bool last;
     if (threadIdx.x == 0) {
@@ -332,6 +333,7 @@ norm_cluster_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int W = kClusterThreads / 32;
     __shared__ __align__(16) float4 parts[kCluster];
     const int64_t warp = blockIdx.x * (int64_t)W + (threadIdx.x >> 5), warps = kCluster * (int64_t)W;
+    pdl_wait();
     const bool once = a.n_seg <= warps;
     Held held;
     Segment g = {0, 0, 0};
@@ -424,11 +426,9 @@ NormLaunch args_of(const ofrl_tensors* l, float* norm_out) {
 ofrl_status launch(const ofrl_tensors* l, const NormLaunch& a, cudaStream_t st) {
     cudaError_t e;
     if (l->grid == 0) {
-        norm_cluster_kernel<<<kCluster, kClusterThreads, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_pdl(norm_cluster_kernel, dim3(kCluster), dim3(kClusterThreads), 0, st, a);
     } else {
-        norm_kernel<<<l->grid, kThreads, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_pdl(norm_kernel, dim3(l->grid), dim3(kThreads), 0, st, a);
         if (e == cudaSuccess && a.out != nullptr) e = launch_pdl(scale_kernel, dim3(l->grid), dim3(kThreads), 0, st, a);
     }
     return e == cudaSuccess ? OFRL_OK : OFRL_ECUDA;
