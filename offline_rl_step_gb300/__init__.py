@@ -509,6 +509,7 @@ class StepGraph:
 
 DTYPE = {"fp32": _abi.DTYPE_F32, "bf16": _abi.DTYPE_BF16}
 _TORCH_DTYPE = {"fp32": F32, "bf16": BF16}
+_TENSOR = torch.Tensor      # looked up for every argument of every call
 
 
 class DeltaRule:
@@ -570,7 +571,7 @@ def _refuse(t, dtype, shape, name: str):
 
 def _rows3(t: torch.Tensor, dtype, shape, name: str):
     """Address and row stride (elements) of a CUDA tensor [tokens, heads, channels] whose rows are dense."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
             _refuse(t, dtype, shape, name)
     s0, s1, s2 = t.stride()
@@ -582,7 +583,7 @@ def _rows3(t: torch.Tensor, dtype, shape, name: str):
 
 def _rows2(t: torch.Tensor, dtype, shape, name: str):
     """Address and row stride (elements) of a CUDA tensor [tokens, heads] whose rows are dense."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
             _refuse(t, dtype, shape, name)
     s0, s1 = t.stride()
@@ -596,15 +597,19 @@ def _dense(t: Optional[torch.Tensor], dtype, shape, name: str):
     """Address of a contiguous CUDA tensor of this shape (0 for None)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
-        _refuse(t, dtype, shape, name)
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+            _refuse(t, dtype, shape, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # absent where torch has no CUDA
+
+
 def _raw_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 def _delta_tokens(ctx: DeltaRule, q, k, v, g, beta, scale):
