@@ -45,3 +45,64 @@ def test_parts_that_do_not_divide_evenly(dtype, lengths):
     d = inputs(lengths, 1, 2, 64, 64, seed=len(lengths), rnd=ROUND[dtype])
     for states in (False, True):
         _compare(_run(d, lengths, dtype, states=states, grads=False), _want(d, lengths, states=states), dtype)
+
+
+def test_captured_after_copies_and_other_streams():
+    """Calls captured behind a copy, a fill and another stream's work give what direct calls give."""
+    import torch
+    import offline_rl_step_gb300 as ofrl
+    need_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    n, heads, dim = 200, 2, 64
+    ctx = ofrl.DeltaRule(heads, heads, dim, dim, "fp32", max_tokens=n, max_episodes=2)
+    ends = torch.tensor([70, n], device="cuda", dtype=torch.int32)
+    src = [new(n, heads, dim) / 8, new(n, heads, dim) / 8, new(n, heads, dim), -new(n, heads).abs(), new(n, heads).sigmoid()]
+    x = [torch.zeros_like(t) for t in src]
+    dout, out, state = new(n, heads, dim), torch.empty(n, heads, dim, device="cuda"), new(n, heads, dim, dim)
+    acted = torch.empty(n, heads, dim, device="cuda")
+    grads = [torch.empty_like(t) for t in src]
+    saved, norm = ctx.saved(n, 2), torch.zeros(1, device="cuda")
+    lists = [ofrl.TensorList([t]) for t in (grads[0], new(1 << 19))]
+    host = [t.cpu().pin_memory() for t in src]
+    other = torch.cuda.Stream()
+
+    def step():
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            for a, b in zip(x[:3], host[:3]):
+                a.copy_(b, non_blocking=True)
+        for a, b in zip(x[3:], host[3:]):
+            a.copy_(b, non_blocking=True)
+        torch.cuda.current_stream().wait_stream(other)
+        ofrl.delta_forward(ctx, *x, ends, out, saved=saved)
+        for t in grads:
+            t.zero_()
+        ofrl.delta_backward(ctx, *x, ends, saved, dout, *grads)
+        norm.zero_()
+        ofrl.global_norm(lists[0], norm)
+        state.copy_(init)
+        ofrl.delta_step(ctx, *x, state, acted)
+        for t in lists[1].tensors:
+            t.copy_(large)
+        ofrl.global_norm_clip(lists[1], 1.0, norm2)
+        return [out, *grads, norm, state, acted, *lists[1].tensors, norm2]
+
+    init, large, norm2 = state.clone(), lists[1].tensors[0].clone(), torch.zeros(1, device="cuda")
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        want = [t.clone() for t in step()]
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = step()
+        for t in got:
+            t.fill_(float("nan"))
+        for a in x:
+            a.zero_()
+        for _ in range(3):
+            graph.replay()
+        stream.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    ctx.close()
