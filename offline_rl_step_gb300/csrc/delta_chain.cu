@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
             {
                 uint32_t f[NM][4][4];
                 to_frags<NM>(X, x_up, f);
-                gemm<4, 8, NM, NM, true>(U, f, pair, (int)kPairFirst, 8, 0);
+                gemm<4, 8, NM, NM, true, kUpper>(U, f, pair, (int)kPairFirst, 8, 0);
             }
             float u_max = tile_max(U) * x_inv * vec[V_MISC * kChunk];
             if constexpr (SAVE) u_max = across<NW>(ring, 1, u_max);
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                     if (threadIdx.x == 0) a.vec_unit[at] = u_inv;
                 }
                 zero(U);
-                gemm<4, 8, NO, NO, false>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
+                gemm<4, 8, NO, NO, false, kUpper>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
             }
             if constexpr (!SUMMARY) {
                 const float p_inv = u_inv * (1.0f / kPScale);
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
                 to_frags<NM>(dO, up, f);
                 float d[8][4];
                 zero(d);
-                gemm<4, 8, NM, NM, true>(d, f, pair + kSquare, (int)kPairFirst, 8, 0);
+                gemm<4, 8, NM, NM, true, kLower>(d, f, pair + kSquare, (int)kPairFirst, 8, 0);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const float2 r = vec2(vec, V_REST, t);
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
                 const float up = scale_up(tile_max(U)), inv = pow2_inv(up);
                 uint32_t f[NM][4][4];
                 to_frags<NM>(U, up, f);
-                gemm<4, 8, NM, NM, false>(R, f, pair, (int)kPairFirst, 8, 0);
+                gemm<4, 8, NM, NM, false, kLower>(R, f, pair, (int)kPairFirst, 8, 0);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const float2 ti = vec2(vec, V_TINV, t);

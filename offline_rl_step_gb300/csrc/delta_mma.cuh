@@ -142,8 +142,10 @@ __device__ __forceinline__ float tile_max(const float (&x)[NT][4]) {
 // first, for all k, while the sums are small: fp32 gradients of the keys over
 // 256 tokens end 4.2e-7 off, 6.0e-7 with all products of a k step together (the
 // error lies to one side), for 6% more time from reading plane 0 twice.
-// KTO: the k steps of 16 that are taken.
-template <int KTO, int NT, int NA, int NB, bool TRANS, int KA>
+// KTO: the k steps of 16 that are taken.  TRI: what B is zero for and need not
+// be multiplied, nothing, columns before the row (kUpper) or after it (kLower).
+enum Tri { kFull, kUpper, kLower };
+template <int KTO, int NT, int NA, int NB, bool TRANS, Tri TRI = kFull, int KA>
 __device__ __forceinline__ void gemm(float (&d)[NT][4], const uint32_t (&a)[NA][KA][4], uint32_t b, int plane, int CG,
                                      int t0) {
     const int lane = threadIdx.x & 31;
@@ -158,7 +160,7 @@ __device__ __forceinline__ void gemm(float (&d)[NT][4], const uint32_t (&a)[NA][
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     const int i = ij - j;
-                    if (i < 0 || i >= NA) continue;
+                    if (i < 0 || i >= NA || (TRI == kUpper && t < 2 * k) || (TRI == kLower && t > 2 * k + 1)) continue;
                     // matrices 0, 1: k halves of tile t; 2, 3: of tile t + 1
                     const int kg = 2 * k + (m & 1), ng = t0 + t + (m >> 1);
                     const uint32_t at = b + j * plane + (TRANS ? kg * CG + ng : ng * CG + kg) * kTile + r * 16;
