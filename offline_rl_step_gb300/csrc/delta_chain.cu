@@ -18,7 +18,8 @@
 //
 // Bound by the latency of a chunk's products and conversions, one after the
 // other: 3 us a chunk of 64 x 64 with one plane, 64 episodes of 256 tokens and
-// two heads 12 us forward and 13.5 us back (24 and 26 us with two planes).
+// two heads 11.5 us forward, 13 when it saves, and 13.5 us back (24 and 23 us
+// with two planes).  Leaving out the zero blocks of T and P took 3 to 10% off.
 
 #include <algorithm>
 #include <cmath>
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
 // product per part, so a CTA takes few rows and splits the columns: warp w
 // makes columns w DK / 4 .. of 16 rows, and the rows come together again
 // through shared memory.  M_g's two planes are copied a part ahead.  Bound by the
-// latency of a step, 2 us: 20 parts of four heads of 128 x 128 38 us.
+// latency of a step, 2 us: 19 parts of four heads of 128 x 128 36 us.
 template <int DK>
 struct Join {
     static constexpr int kMap = 2 * DK * DK * 2;
@@ -846,7 +847,7 @@ int forward_together(const ofrl_delta_shape& s, int planes) {
 // 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, but no more than the
 // SMs hold at once in the last pass (a few CTAs more would be a second round).
 // One sequence of 32768 tokens, four heads of 128, with its final state: 2100 us
-// whole, 427 in 20 parts (160 CTAs on 152 SMs), 362 in 19.  Three of 1000 tokens,
+// whole, 341 in 19 parts, in 20 (160 CTAs on 152 SMs) 65 more.  Three of 1000 tokens,
 // two heads of 64, fp32: 73 us whole, 38 in 7 parts of 3 chunks, 33 in 8 of 2.
 int segments_of(const SeqLaunch& a, int planes) {
     const int64_t items = (int64_t)a.episodes * a.shape.v_heads;

@@ -65,7 +65,7 @@ struct Smem {
     static constexpr int off_a = off_s + kState;         // forward: x; backward: dO
     static constexpr int off_b = off_a + kTok;           // forward: U; backward: dU, then R
     static constexpr int off_c = off_b + kTok;           // forward: rest U; backward: gamma dO
-    static constexpr int off_d = off_c + kTok;           // backward: -gamma dv
+    static constexpr int off_d = off_c + kTok;           // forward: outputs turned around; backward: -gamma dv
     static constexpr int off_stage = off_d + kTok;
     static constexpr int off_turn = off_stage + 2 * kStage;     // a warp's 32 channels x 32 tokens, turned around
     static constexpr int off_row = off_turn + kTok;             // largest magnitudes of halves of rows
