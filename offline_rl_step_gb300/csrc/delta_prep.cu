@@ -24,8 +24,9 @@
 //
 // Bound by the latency of that sequence: 16 thousand cycles a CTA, six at a
 // time, the schedulers busy for half of them.  640 CTAs of 64-wide bf16 heads
-// (16384 tokens) 15 us; 5008 of 128-wide ones (65k ragged tokens) 86 us, 2.8
-// TB/s of HBM.  Keys and queries through registers before the decays: 101 us.
+// (16384 tokens) 15 us; 5008 of 128-wide ones (65k ragged tokens) 81 us, 3.0
+// TB/s of HBM.  Keys and queries through registers before the decays: 101 us;
+// decays in every warp and a diagonal block to each: 86.
 
 #include "delta_mma.cuh"
 
