@@ -50,6 +50,7 @@ struct ChainArgs {
     uint8_t* vec_img;        // per (slot, head): U (forward) or R (backward)
     float* state_unit;       // [slot][head]: their powers of two
     float* vec_unit;
+    int32_t stages;          // of the ring
     // forward over parts of an episode (segments > 1)
     int32_t segments;
     float* seg_state;        // [episode][head][segments][v_dim][k_dim] states at the parts' starts
@@ -245,12 +246,12 @@ __device__ __forceinline__ void ring_init(Ring& r) {
 // leave three warps on one of the SM's four register files, and a third of
 // the registers of every warp unused.)
 template <typename St, int DK, bool REVERSE>
-__device__ __forceinline__ void copy_chunk(const ChainArgs& a, const Work& w, uint8_t* smem, Ring& r, int n) {
+__device__ __forceinline__ void copy_chunk(const ChainArgs& a, const Work& w, uint8_t* smem, Ring& r, int n, int st,
+                                           int before) {
     if (n >= w.chunks || *(volatile int*)&r.dead) return;
-    const int st = n % St::kCount;
     const int c = REVERSE ? w.chunks - 1 - n : n;
     bool ok = true;
-    if (n >= St::kCount) ok = umma::mbar_wait(&r.empty[st], (uint32_t)(n / St::kCount - 1) & 1u, kWaitNs);
+    if (before >= 0) ok = umma::mbar_wait(&r.empty[st], (uint32_t)before & 1u, kWaitNs);
     if (__any_sync(0xffffffffu, !ok)) {      // what is in flight has been waited for, or its own wait gives up
         r.dead = 1;
         return;
@@ -381,7 +382,8 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
     const Work w = work_of(a, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
                            a.segments);
     ring_init<NW>(ring);
-    uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
+    const int stages = a.stages;
+    uint8_t* mine = smem + stages * St::kBytes + warp * St::kWarp;
     {
         const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
         const int row0 = w.row0 + warp * 16;
@@ -404,17 +406,20 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                     S[t][z] = row0 - v_pad + (lane >> 2) + (z >> 1) * 8 == t * 8 + (lane & 3) * 2 + (z & 1) ? 1.0f : 0.0f;
         if (SUMMARY && w.seg == 0 && w.row0 >= v_pad) return;
         if (warp == 0)
-            for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n);
+            for (int n = 0; n < stages - 1; ++n) copy_chunk<St, DK, false>(a, w, smem, ring, n, n, -1);
+        int st = stages - 1, turn = -1;      // of the chunk before
         for (int c = 0; c < w.chunks; ++c) {
-            const int st = c % St::kCount;
+            const int st_before = st, turn_before = turn;
+            if (++st == stages) st = 0, ++turn;
             copy_rows<St, T>(a, w, mine + ((c + 1) & 1) * St::kRows, c + 1, row0);
-            if (St::kCount == 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c);
-            stage_ready(ring, st, c / St::kCount);
+            if (stages == 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c, 0, c - 1);
+            stage_ready(ring, st, turn);
             if (PASS == kOutputs && row0 >= dv) {
                 if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
                 continue;
             }
-            if (St::kCount > 1 && warp == 0) copy_chunk<St, DK, false>(a, w, smem, ring, c + St::kCount - 1);
+            if (stages > 1 && warp == 0)
+                copy_chunk<St, DK, false>(a, w, smem, ring, c + stages - 1, st_before, turn_before);
             const uint8_t* s = smem + st * St::kBytes;
             const uint32_t kimg = umma::smem_u32(s), qimg = kimg + NT * St::kKey, pair = kimg + St::kKeys;
             const float* vec = reinterpret_cast<const float*>(s + St::kKeys + 2 * kSquare);
@@ -535,9 +540,10 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     const Work w = work_of(a, 1, NW * 16, 1, 1);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     ring_init<NW>(ring);
-    uint8_t* mine = smem + St::kCount * St::kBytes + warp * St::kWarp;
+    const int stages = a.stages;
+    uint8_t* mine = smem + stages * St::kBytes + warp * St::kWarp;
     if (warp == 0)
-        for (int n = 0; n < St::kCount - 1; ++n) copy_chunk<St, DK, true>(a, w, smem, ring, n);
+        for (int n = 0; n < stages - 1; ++n) copy_chunk<St, DK, true>(a, w, smem, ring, n, n, -1);
     {
         const int dk = a.shape.k_dim, dv = a.shape.v_dim, hv = a.shape.v_heads;
         const int row0 = warp * 16;
@@ -545,17 +551,20 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
         float S[DK / 8][4];
         copy_rows<St, T>(a, w, mine, w.chunks - 1, row0);
         load_state(a.first ? a.first + states : nullptr, S, row0, dv, dk);
+        int st = stages - 1, turn = -1;      // of the chunk before
         for (int n = 0; n < w.chunks; ++n) {
-            const int st = n % St::kCount, c = w.chunks - 1 - n;
+            const int c = w.chunks - 1 - n, st_before = st, turn_before = turn;
+            if (++st == stages) st = 0, ++turn;
             copy_rows<St, T>(a, w, mine + ((n + 1) & 1) * St::kRows, c - 1, row0);
-            if (St::kCount == 1 && warp == 0) copy_chunk<St, DK, true>(a, w, smem, ring, n);
-            stage_ready(ring, st, n / St::kCount);
+            if (stages == 1 && warp == 0) copy_chunk<St, DK, true>(a, w, smem, ring, n, 0, n - 1);
+            stage_ready(ring, st, turn);
             const uint8_t* s = smem + st * St::kBytes;
             const uint32_t kimg = umma::smem_u32(s), qimg = kimg + NT * St::kKey, pair = kimg + St::kKeys;
             const float* vec = reinterpret_cast<const float*>(s + St::kKeys + 2 * kSquare);
             const int rows = min(kChunk, w.sp.len - c * kChunk);
             const int64_t at = (w.slot0 + c) * hv + w.head;
-            if (St::kCount > 1 && warp == 0) copy_chunk<St, DK, true>(a, w, smem, ring, n + St::kCount - 1);
+            if (stages > 1 && warp == 0)
+                copy_chunk<St, DK, true>(a, w, smem, ring, n + stages - 1, st_before, turn_before);
             float U[8][4];
             zero(U);
             const float s_up = scale_up(across<NW>(ring, 0, tile_max(S))), s_inv = pow2_inv(s_up);
@@ -748,28 +757,50 @@ __global__ void __launch_bounds__(128) delta_join_kernel(const __grid_constant__
 }
 
 template <auto KERNEL>
-cudaError_t go(int nw, int smem, int per_head, const ChainArgs& c, cudaStream_t st) {
+cudaError_t go(int nw, int smem, int most, int per_head, const ChainArgs& c, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * per_head;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = opt_in(KERNEL, smem, done);
+    const cudaError_t e = opt_in(KERNEL, most, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(KERNEL, dim3((unsigned)grid), dim3(nw * 32), smem, st, c);
+}
+
+// Whether one stage is enough for a pass whose ring would keep a second CTA off
+// the SM: where there are CTAs for more than one on each, and either no more than
+// two (else a second round begins), or episodes of one chunk, which has nothing
+// to copy ahead.  Read / one stage, us: 1000 heads of 30 tokens of 128 x 64,
+// bf16, 55.1 / 47.0; 240 heads of 500 89.7 / 82.0; 160 of 300 of 64 x 64, fp32,
+// 64.2 / 54.9; but 400 heads of 300 tokens 90.3 / 94.3, 120 of 200 33.7 / 36.3.
+bool one_stage(const ChainArgs& c, int64_t grid, int num_sms) {
+    return grid > num_sms && c.segments == 1 && (grid <= 2LL * num_sms || c.in.tokens <= (int64_t)kChunk * c.episodes);
+}
+
+// A pass over chunks with its ring.
+template <auto KERNEL, typename St, int NW>
+cudaError_t go_ring(int per_head, ChainArgs c, int num_sms, cudaStream_t st) {
+    constexpr int kOne = St::kBytes + NW * St::kWarp;
+    const int64_t grid = (int64_t)c.episodes * c.shape.v_heads * per_head;
+    const bool one = NW == 4 && St::kShared > 112 * 1024 && kOne <= 112 * 1024 && one_stage(c, grid, num_sms);
+    c.stages = one ? 1 : St::kCount;
+    return go<KERNEL>(NW, one ? kOne : St::kShared, St::kShared, per_head, c, st);
 }
 
 template <typename T, int DK, int NM>
 cudaError_t forward(const ChainArgs& c, int num_sms, cudaStream_t st) {
     using S4 = Stage<T, DK, NM, 4>;
+    using S8 = Stage<T, DK, NM, 8>;
     const int slices = (c.shape.v_dim + 63) / 64;
-    if (c.state_img)
-        return c.shape.v_dim > 64
-                   ? go<delta_forward_kernel<T, DK, NM, 8, kSave>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st)
-                   : go<delta_forward_kernel<T, DK, NM, 4, kSave>>(4, S4::kShared, 1, c, st);
+    if (c.state_img) {
+        if constexpr (NM == 2)      // with one plane, more than 64 channels are on tcgen05
+            if (c.shape.v_dim > 64) return go_ring<delta_forward_kernel<T, DK, NM, 8, kSave>, S8, 8>(1, c, num_sms, st);
+        return go_ring<delta_forward_kernel<T, DK, NM, 4, kSave>, S4, 4>(1, c, num_sms, st);
+    }
     if (c.segments > 1) {
-        cudaError_t e = go<delta_forward_kernel<T, DK, NM, 4, kSummary>>(4, S4::kShared,
-                           (slices + DK / 64) * (c.segments - 1), c, st);
+        cudaError_t e = go_ring<delta_forward_kernel<T, DK, NM, 4, kSummary>, S4, 4>(
+            (slices + DK / 64) * (c.segments - 1), c, num_sms, st);
         if (e == cudaSuccess && c.segments > 2)
-            e = go<delta_join_kernel<DK>>(4, Join<DK>::kShared, (c.shape.v_dim + 15) / 16, c, st);
+            e = go<delta_join_kernel<DK>>(4, Join<DK>::kShared, Join<DK>::kShared, (c.shape.v_dim + 15) / 16, c, st);
         if (e != cudaSuccess) return e;
     }
     // More than 64 channels: two CTAs of four warps per head, or one of eight,
@@ -779,14 +810,15 @@ cudaError_t forward(const ChainArgs& c, int num_sms, cudaStream_t st) {
     // of 64 x 96 87 against 88.
     if constexpr (NM == 2)
         if (c.segments == 1 && c.shape.v_dim > 64 && (int64_t)c.episodes * c.shape.v_heads >= num_sms)
-            return go<delta_forward_kernel<T, DK, NM, 8, kOutputs>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st);
-    return go<delta_forward_kernel<T, DK, NM, 4, kOutputs>>(4, S4::kShared, slices * c.segments, c, st);
+            return go_ring<delta_forward_kernel<T, DK, NM, 8, kOutputs>, S8, 8>(1, c, num_sms, st);
+    return go_ring<delta_forward_kernel<T, DK, NM, 4, kOutputs>, S4, 4>(slices * c.segments, c, num_sms, st);
 }
 template <typename T, int DK>
-cudaError_t reverse(const ChainArgs& c, cudaStream_t st) {
+cudaError_t reverse(const ChainArgs& c, int num_sms, cudaStream_t st) {
     constexpr int NM = sizeof(T) == 4 ? 2 : 1;
-    return c.shape.v_dim > 64 ? go<delta_reverse_kernel<T, DK, 8>>(8, Stage<T, DK, NM, 8>::kShared, 1, c, st)
-                              : go<delta_reverse_kernel<T, DK, 4>>(4, Stage<T, DK, NM, 4>::kShared, 1, c, st);
+    if constexpr (NM == 2)
+        if (c.shape.v_dim > 64) return go_ring<delta_reverse_kernel<T, DK, 8>, Stage<T, DK, NM, 8>, 8>(1, c, num_sms, st);
+    return go_ring<delta_reverse_kernel<T, DK, 4>, Stage<T, DK, NM, 4>, 4>(1, c, num_sms, st);
 }
 
 ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
@@ -897,8 +929,8 @@ cudaError_t launch_chain_reverse(const SeqLaunch& a, const Prepared& p, const Im
     c.rows = a.dout;
     c.row_stride = (int64_t)a.shape.v_heads * a.shape.v_dim;
     const bool wide = a.shape.k_dim > 64;
-    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? reverse<float, 128>(c, st) : reverse<float, 64>(c, st);
-    return wide ? reverse<__nv_bfloat16, 128>(c, st) : reverse<__nv_bfloat16, 64>(c, st);
+    if (a.shape.dtype == OFRL_DTYPE_F32) return wide ? reverse<float, 128>(c, a.num_sms, st) : reverse<float, 64>(c, a.num_sms, st);
+    return wide ? reverse<__nv_bfloat16, 128>(c, a.num_sms, st) : reverse<__nv_bfloat16, 64>(c, a.num_sms, st);
 }
 
 }  // namespace delta
