@@ -879,7 +879,7 @@ int forward_together(const ofrl_delta_shape& s, int planes) {
 // 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, but no more than the
 // SMs hold at once in the last pass (a few CTAs more would be a second round).
 // One sequence of 32768 tokens, four heads of 128, with its final state: 2100 us
-// whole, 341 in 19 parts, in 20 (160 CTAs on 152 SMs) 65 more.  Three of 1000 tokens,
+// whole, 346 in 19 parts, in 20 (160 CTAs on 152 SMs) 65 more.  Three of 1000 tokens,
 // two heads of 64, fp32: 73 us whole, 38 in 7 parts of 3 chunks, 33 in 8 of 2.
 int segments_of(const SeqLaunch& a, int planes) {
     const int64_t items = (int64_t)a.episodes * a.shape.v_heads;

@@ -14,6 +14,8 @@
 // segments L2 still holds.  Bound by HBM for long lists, by latency for short:
 // 150 million elements in 640 tensors, fp32, 106 us for the norm and 179 us for
 // the scaling (5.7 and 6.7 TB/s); 120 thousand elements in 17 tensors 6.1 us.
+// (Hints that keep the list's end in L2 and pass the rest through: 295 us in all
+// against 285; streaming stores 286; four or eight CTAs an SM 291.)
 
 #include <cmath>
 #include <cstring>
