@@ -335,6 +335,9 @@ norm_cluster_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int W = kClusterThreads / 32;
     __shared__ __align__(16) float4 parts[kCluster];
     const int64_t warp = blockIdx.x * (int64_t)W + (threadIdx.x >> 5), warps = kCluster * (int64_t)W;
+    // a CTA's shared memory may be written from outside only once the CTA runs:
+    // every CTA says so here and waits for the others before it sends its part
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_wait();
     const bool once = a.n_seg <= warps;
     Held held;
@@ -352,6 +355,8 @@ norm_cluster_kernel(const __grid_constant__ NormLaunch a) {
         mine_part = norm_part(a, warp, warps);
     }
     const Sums part = block_sums<W>(mine_part);
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (threadIdx.x < 32) {      // this CTA's part to every CTA
         const float s = __shfl_sync(0xffffffffu, part.s, 0), c = __shfl_sync(0xffffffffu, part.c, 0),
                     bs = __shfl_sync(0xffffffffu, part.big_s, 0), bc = __shfl_sync(0xffffffffu, part.big_c, 0);

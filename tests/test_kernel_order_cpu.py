@@ -1,0 +1,30 @@
+"""Orders inside kernels that no run can show to be missing, read from their sources: a violation faults or hangs only
+when CTAs happen to start in an unlucky order, so it is not to be found out on a GPU."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "offline_rl_step_gb300", "csrc")
+
+
+def kernel_body(file, name):
+    """The kernel's text from its opening brace to the closing one, without comments."""
+    text = open(os.path.join(CSRC, file)).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    at = re.search(r"__global__[^;{]*?\b" + name + r"\s*\(", text, re.S).end()
+    at = text.index("{", at)
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+    raise AssertionError(f"{name}: no closing brace")
+
+
+def test_cluster_runs_before_its_shared_memory_is_written_from_outside():
+    body = kernel_body("norm.cu", "norm_cluster_kernel")
+    first = body.index("st.shared::cluster")
+    before = body[:first]
+    assert "barrier.cluster.arrive" in before and "barrier.cluster.wait" in before
+    assert before.index("barrier.cluster.arrive") < before.index("barrier.cluster.wait")
+    # and once more after it, before the parts are read
+    assert "barrier.cluster.arrive" in body[first:] and "barrier.cluster.wait" in body[first:]
