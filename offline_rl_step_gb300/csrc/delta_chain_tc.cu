@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     const Episode w = episode(a);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     init_bars(b);
+    // before the wait below: the kernel before lets this one go when all its CTAs have their TMEM
     if (warp == 0) umma::tmem_alloc(&b.tmem, 512);
     umma::fence_before_sync();
     __syncthreads();

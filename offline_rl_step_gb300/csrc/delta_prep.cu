@@ -141,9 +141,8 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     const int head = blockIdx.x % hv, khead = head / group;
     const int32_t tokens = (int32_t)a.in.tokens;
     // The chain that follows reads the caller's buffers before it waits for this
-    // kernel: what came before has to be done by then.
+    // kernel: what came before has to be done when it is let go, below.
     pdl_wait();
-    pdl_trigger();
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < a.episodes; e += kPrepThreads)
             if (span_bad(a.ends, e, tokens)) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, 1);
@@ -156,7 +155,13 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         umma::mbar_init(&bar, 1);
         umma::fence_mbar_init();
     }
-    if (warp == 3) umma::tmem_alloc(&s_tmem, kChunk);
+    if (warp == 3) {
+        umma::tmem_alloc(&s_tmem, kChunk);
+        // Only now may the chain start: on tcgen05 it takes all of an SM's TMEM
+        // before it waits for this kernel, and a CTA here that had none yet would
+        // wait for the chain in turn.  (So no other warp lets it go, either.)
+        pdl_trigger();
+    }
     // One warp adds up the decays and two invert the diagonal blocks; which ones
     // changes from CTA to CTA, so that every scheduler of an SM gets its share.
     const int chosen = (int)(blockIdx.x * 0x9E3779B1u >> 30);

@@ -28,3 +28,18 @@ def test_cluster_runs_before_its_shared_memory_is_written_from_outside():
     assert before.index("barrier.cluster.arrive") < before.index("barrier.cluster.wait")
     # and once more after it, before the parts are read
     assert "barrier.cluster.arrive" in body[first:] and "barrier.cluster.wait" in body[first:]
+
+
+def test_tmem_is_not_taken_ahead_of_a_kernel_that_still_needs_it():
+    """A kernel that takes TMEM before it waits for its predecessor may share an SM with CTAs of the predecessor: those
+    have to have theirs before they let it start, or each waits for the other."""
+    for file, name in (("delta_chain_tc.cu", "delta_reverse_tc_kernel"), ("delta_grad_tc.cu", "delta_grad_tc_kernel"),
+                       ("delta_prep.cu", "delta_prep_kernel")):
+        body = kernel_body(file, name)
+        assert body.index("pdl_wait()") < body.index("tmem_alloc("), name
+    forward, prep = kernel_body("delta_chain_tc.cu", "delta_forward_tc_kernel"), kernel_body("delta_prep.cu", "delta_prep_kernel")
+    if forward.index("tmem_alloc(") < forward.index("pdl_wait()"):
+        assert prep.count("pdl_trigger()") == 1
+        assert prep.index("tmem_alloc(") < prep.index("pdl_trigger()")
+        # the same warp does both, one after the other
+        assert re.search(r"if \(warp == 3\) \{\s*umma::tmem_alloc\([^;]*;\s*pdl_trigger\(\);\s*\}", prep)
