@@ -225,6 +225,7 @@ __device__ __forceinline__ Work work_of(const ChainArgs& a, int slices, int widt
 struct Ring {
     uint64_t full[3], empty[3];
     int dead;             // a wait gave up
+    int copied;           // turns whose copies were started
     float most[2][8];     // per warp: largest magnitudes
 };
 
@@ -236,6 +237,7 @@ __device__ __forceinline__ void ring_init(Ring& r) {
             umma::mbar_init(&r.empty[i], NW);
         }
         r.dead = 0;
+        r.copied = 0;
         umma::fence_mbar_init();
     }
     __syncthreads();
@@ -248,15 +250,17 @@ __device__ __forceinline__ void ring_init(Ring& r) {
 template <typename St, int DK, bool REVERSE>
 __device__ __forceinline__ void copy_chunk(const ChainArgs& a, const Work& w, uint8_t* smem, Ring& r, int n, int st,
                                            int before) {
-    if (n >= w.chunks || *(volatile int*)&r.dead) return;
+    if (n >= w.chunks) return;
     const int c = REVERSE ? w.chunks - 1 - n : n;
-    bool ok = true;
-    if (before >= 0) ok = umma::mbar_wait(&r.empty[st], (uint32_t)before & 1u, kWaitNs);
-    if (__any_sync(0xffffffffu, !ok)) {      // what is in flight has been waited for, or its own wait gives up
+    // lanes may see another warp set `dead` at different times: they decide together
+    bool ok = !*(volatile int*)&r.dead;
+    if (ok && before >= 0) ok = umma::mbar_wait(&r.empty[st], (uint32_t)before & 1u, kWaitNs);
+    if (__any_sync(0xffffffffu, !ok)) {
         r.dead = 1;
         return;
     }
     if ((threadIdx.x & 31) == 0) {
+        r.copied = n + 1;
         uint8_t* s = smem + st * St::kBytes;
         const int64_t slot = w.slot0 + c;
         umma::mbar_expect_tx(&r.full[st], (uint32_t)St::kBytes);
@@ -299,10 +303,22 @@ __device__ __forceinline__ void rows_ready() {      // all but the newest group
 // waits any more: the pass runs on over what shared memory holds (warps that
 // meet at a barrier all get there) and the CTA reports it.
 __device__ __forceinline__ void stage_ready(Ring& r, int st, int turn) {
-    if (*(volatile int*)&r.dead) return;
-    const bool ok = umma::mbar_wait(&r.full[st], (uint32_t)turn & 1u, kWaitNs);
+    const bool ok = *(volatile int*)&r.dead || umma::mbar_wait(&r.full[st], (uint32_t)turn & 1u, kWaitNs);
     if (__any_sync(0xffffffffu, !ok)) r.dead = 1;
     __syncwarp();
+}
+
+// End of a CTA.  After a wait that gave up, copies may still be on their way
+// into its shared memory: those of the ring's last turns are waited for, again
+// with a limit, and the token rows' without one.
+__device__ __forceinline__ void ring_end(const ChainArgs& a, Ring& r, int stages) {
+    __syncthreads();
+    if (!r.dead) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (threadIdx.x != 0) return;
+    for (int n = max(r.copied - stages, 0); n < r.copied; ++n)
+        umma::mbar_wait(&r.full[n % stages], (uint32_t)(n / stages) & 1u, kWaitNs);
+    atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
 }
 
 // Largest of the computing warps' values (which: 0 and 1 in turn).
@@ -523,8 +539,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
             store_state(a.last + states, S, row0, dv, dk);
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    ring_end(a, ring, stages);
 }
 
 template <typename T, int DK, int NW>
@@ -651,8 +666,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
         }
         if (a.last) store_state(a.last + states, S, row0, dv, dk);
     }
-    __syncthreads();
-    if (threadIdx.x == 0 && ring.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+    ring_end(a, ring, stages);
 }
 
 // The parts' starts from their summaries, in order: S_{g+1} = S_g M_g + B_g,

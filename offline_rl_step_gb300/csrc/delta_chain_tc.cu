@@ -78,7 +78,9 @@ struct Bars {
     uint64_t s_ready, u_ready;              // from the state's warps, from the tokens'
     uint64_t free;                          // forward: t_q and t_o are read
     uint64_t a, b, t, s, p;              // products done
+    uint64_t done[2];                       // after a wait that gave up: everything a thread issued is done
     int dead;
+    int copied;                             // chunks whose copies were started
     uint32_t tmem;
     float most[2][8], more[8];
     float s_inv, u_inv, o_inv[2], r_inv;    // 1 / powers of two: the state, U, gamma dO, -gamma dv
@@ -164,6 +166,7 @@ template <int DK>
 __device__ __forceinline__ void copy_stage(const TcArgs& a, const Episode& w, uint8_t* smem, Bars& b, int n, int c) {
     using S = Smem<DK>;
     const int64_t slot = w.slot0 + c;
+    b.copied = n + 1;
     uint8_t* to = smem + S::off_stage + (n & 1) * S::kStage;
     umma::mbar_expect_tx(&b.full[n & 1], S::kStage);
     umma::bulk_g2s(to, a.keys + (slot * a.shape.k_heads + w.khead) * KeyImage::bytes(DK, 1), 2 * S::kKey, &b.full[n & 1]);
@@ -284,11 +287,35 @@ __device__ __forceinline__ void load_row(const float* from, float (&s)[N], int r
 
 __device__ __forceinline__ void init_bars(Bars& b) {
     if (threadIdx.x == 0) {
-        uint64_t* all[] = {&b.full[0], &b.full[1], &b.s_ready, &b.u_ready, &b.free, &b.a, &b.b, &b.t, &b.s, &b.p};
+        uint64_t* all[] = {&b.full[0], &b.full[1], &b.s_ready, &b.u_ready, &b.free, &b.a,
+                           &b.b,       &b.t,       &b.s,       &b.p,       &b.done[0], &b.done[1]};
         for (uint64_t* m : all) umma::mbar_init(m, 1);
         b.dead = 0;
+        b.copied = 0;
         umma::fence_mbar_init();
     }
+}
+
+// End of a CTA.  After a wait that gave up, products and copies may still be on
+// their way: they are waited for, again with a limit, before TMEM and shared
+// memory are given back.
+__device__ __forceinline__ void finish(const TcArgs& a, Bars& b, uint32_t tmem) {
+    __syncthreads();
+    umma::fence_after_sync();
+    if (b.dead) {
+        if (threadIdx.x % kTokThreads == 0) {      // the threads that issue the products
+            uint64_t* bar = &b.done[threadIdx.x / kTokThreads];
+            umma::commit(bar);
+            umma::mbar_wait(bar, 0, kWaitNs);
+        }
+        if (threadIdx.x == 0) {
+            for (int n = max(b.copied - 2, 0); n < b.copied; ++n)
+                umma::mbar_wait(&b.full[n & 1], (uint32_t)(n >> 1) & 1u, kWaitNs);
+            atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x < 32) umma::tmem_dealloc(tmem, 512);
 }
 
 // TMEM columns.
@@ -512,10 +539,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
         }
         if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();
     }
-    __syncthreads();
-    umma::fence_after_sync();
-    if (threadIdx.x == 0 && b.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
-    if (warp == 0) umma::tmem_dealloc(tmem, 512);
+    finish(a, b, tmem);
 }
 
 template <int DK>
@@ -757,10 +781,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 if (s_col + c < dk) *reinterpret_cast<float4*>(to + s_col + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
         }
     }
-    __syncthreads();
-    umma::fence_after_sync();
-    if (threadIdx.x == 0 && b.dead) atomicAdd(a.status + OFRL_STAT_TIMEOUT, 1);
-    if (warp == 0) umma::tmem_dealloc(tmem, 512);
+    finish(a, b, tmem);
 }
 
 template <auto KERNEL, int DK>

@@ -526,7 +526,10 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     for (int i = threadIdx.x; i < kVecBytes / 16; i += kPrepThreads)
         reinterpret_cast<uint4*>(pairs + 2 * kSquare)[i] = reinterpret_cast<const uint4*>(vec)[i];
     umma::fence_after_sync();
-    if (warp == 3) umma::tmem_dealloc(tmem, kChunk);
+    if (warp == 3) {
+        umma::mbar_wait(&bar, 0, kWaitNs);      // a product that was given up on may still write
+        umma::tmem_dealloc(tmem, kChunk);
+    }
 }
 
 template <typename T, int DK, int NM>
