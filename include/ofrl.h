@@ -468,8 +468,9 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  * so S_t k_t moves from its decayed prediction toward v_t by beta_t |k_t|^2.
  * With unit keys and beta in [0, 1] the state stays bounded; larger
  * beta |k|^2 is computed as it stands.  g_t = -inf forgets everything before
- * t.  No counterpart on the pages, whose networks see one transition at a
- * time.
+ * t; g_t > 0 lets the state grow (the sum of 64 consecutive log decays has to
+ * stay below 88, where exp leaves fp32).  No counterpart on the pages, whose
+ * networks see one transition at a time.
  *
  * Tokens are transitions in buffer order: token t of episode e lies between
  * episode_ends[e - 1] (0 for the first) and episode_ends[e], the convention of

@@ -481,14 +481,16 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                 to_frags<NM>(X, x_up, f);
                 gemm<4, 8, NM, NM, true, kUpper>(U, f, pair, (int)kPairFirst, 8, 0);
             }
-            float u_max = tile_max(U) * x_inv * vec[V_MISC * kChunk];
+            float u_max = tile_max(U) * x_inv;
             if constexpr (SAVE) u_max = across<NW>(ring, 1, u_max);
             const float u_up = scale_up(u_max), u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
+            // rest U, with a power of two of its own where states grow
+            const float r_up = scale_up(u_max * vec[V_MISC * kChunk + kMost]), r_inv = pow2_inv(r_up), r_f = r_up * x_inv;
             // X now holds rest U, what the state takes in
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 const float2 r = vec2(vec, V_REST, t);
-                const float f[2] = {r.x * u_f, r.y * u_f};
+                const float f[2] = {r.x * r_f, r.y * r_f};
 #pragma unroll
                 for (int z = 0; z < 4; ++z) X[t][z] = U[t][z] * f[z & 1];
             }
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                 gemm<4, 8, NO, NO, false, kUpper>(U, f, pair + kSquare, (int)kPairFirst, 8, 0);
             }
             if constexpr (!SUMMARY) {
-                const float p_inv = u_inv * (1.0f / kPScale);
+                const float p_inv = u_inv * vec[V_MISC * kChunk + kPUnit];
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const float2 os = vec2(vec, V_OS, t), qs = vec2(vec, V_QS, t);
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
             {
                 uint32_t f[NM][4][4];
                 to_frags<NM>(X, 1.0f, f);
-                update_state<DK, NM, NT, false>(S, vec[V_GAM * kChunk + kChunk - 1], u_inv, f, kimg, f, kimg);
+                update_state<DK, NM, NT, false>(S, vec[V_GAM * kChunk + kChunk - 1], r_inv, f, kimg, f, kimg);
             }
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(&ring.empty[st]);
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
                 for (int z = 0; z < 4; ++z) dO[t][z] *= z & 1 ? qs.y : qs.x;
             }
             {
-                const float up = scale_up(tile_max(dO)), inv = pow2_inv(up) * (1.0f / kPScale);
+                const float up = scale_up(tile_max(dO)), inv = pow2_inv(up) * vec[V_MISC * kChunk + kPUnit];
                 uint32_t f[NM][4][4];
                 to_frags<NM>(dO, up, f);
                 float d[8][4];

@@ -83,7 +83,8 @@ struct Bars {
     int copied;                             // chunks whose copies were started
     uint32_t tmem;
     float most[2][8], more[8];
-    float s_inv, u_inv, o_inv[2], r_inv;    // 1 / powers of two: the state, U, gamma dO, -gamma dv
+    // 1 / powers of two: the state, U, gamma dO, and what the state takes in (rest U or -gamma dv)
+    float s_inv, u_inv, o_inv[2], r_inv;
     alignas(16) float dv_f[2][kChunk];      // backward: factors of dv
 };
 
@@ -399,9 +400,12 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             __syncwarp();
             wait(b, &b.t, n);
             tmem_row(mine + t_u + col, x);
-            const float u_up = scale_up(group_max<1>(b.most[0], half_max(x) * x_inv * vec[V_MISC * kChunk]));
+            const float u_max = group_max<1>(b.most[0], half_max(x) * x_inv), u_up = scale_up(u_max);
             const float u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
             {
+                // rest U, with a power of two of its own where states grow
+                const float r_up = scale_up(u_max * vec[V_MISC * kChunk + kMost]), r_f = r_up * x_inv;
+                if (threadIdx.x == 0) b.r_inv = pow2_inv(r_up);
                 float y[kHalf];
 #pragma unroll
                 for (int c = 0; c < kHalf; c += 4) {
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
 #pragma unroll
                     for (int z = 0; z < 4; ++z) y[c + z] = x[c + z] * f[z];
                 }
-                put_cols(smem + S::off_c + at, y, u_f);
+                put_cols(smem + S::off_c + at, y, r_f);
             }
             if (threadIdx.x == 0) b.u_inv = u_inv;
             umma::fence_smem_to_async();
@@ -468,13 +472,13 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             }
             if (n < w.chunks) {
                 if (n > 0) {
-                    const float keep = vec_of(n - 1)[V_GAM * kChunk + kChunk - 1];
+                    const float keep = vec_of(n - 1)[V_GAM * kChunk + kChunk - 1], r_inv = b.r_inv;
 #pragma unroll
                     for (int c = 0; c < NS; c += 32) {
                         float d[32];
                         tmem_row(mine + t_s + s_col + c, d);
 #pragma unroll
-                        for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + u_inv * d[z];
+                        for (int z = 0; z < 32; ++z) s[c + z] = keep * s[c + z] + r_inv * d[z];
                     }
                     wait(b, &b.b, n - 1);      // what read the image is done
                 }
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
                 const float* vec = vec_of(n - 1);
                 wait(b, &b.b, n - 1);
                 wait(b, &b.p, n - 1);
-                const float p_inv = u_inv * (1.0f / kPScale);
+                const float p_inv = u_inv * vec[V_MISC * kChunk + kPUnit];
                 uint32_t h[kHalf / 2];
 #pragma unroll
                 for (int c = 0; c < kHalf; c += 16) {
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
             const float o_most = warp_max(half_max(y));
             if (lane == 0) b.more[warp] = o_most;
             if (threadIdx.x == 0) umma::bulk_wait_read();      // R's image of the chunk before
-            const float a_up = scale_up(group_max<1>(b.most[0], half_max(x))), p_inv = pow2_inv(a_up) * (1.0f / kPScale);
+            const float a_up = scale_up(group_max<1>(b.most[0], half_max(x))), p_inv = pow2_inv(a_up) * vec[V_MISC * kChunk + kPUnit];
             const float o_up = scale_up(all_max(b.more));
             put_cols(smem + S::off_a + at, x, a_up);
             umma::fence_smem_to_async();

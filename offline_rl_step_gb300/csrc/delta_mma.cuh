@@ -195,8 +195,9 @@ struct KeyImage {      // per (slot, key head): K^ planes, then Q^ planes
 };
 // Per (slot, value head): (T^T) plane 0, P plane 0, vectors, then planes 1.
 // T^T rows j (16 of them share a power of two), columns i, of T = (1 + A)^-1;
-// P times kPScale, rows i, columns j.
-constexpr float kPScale = 32.0f;     // |q^ k^| < 4 * 128: P below 2^14
+// P rows i, columns j, divided by the chunk's unit of P.
+constexpr float kPScale = 32.0f;     // |q^ k^| < 4 * 128: P below 2^14 where no decay D_ij is above 1
+constexpr int kMost = 0, kPUnit = 1;      // in V_MISC
 enum Vec {
     V_GAM,      // gamma
     V_REST,     // exp(G_last - G_j)
@@ -212,7 +213,7 @@ enum Vec {
     V_OS,       // scale kq gamma
     V_DV,       // beta^ / kappa
     V_DS,       // beta^ gamma
-    V_MISC,     // [0]: the largest of rest and 1
+    V_MISC,     // [0]: the largest of rest and 1; [1]: P's unit
     V_COUNT
 };
 constexpr int kVecBytes = V_COUNT * kChunk * 4;

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     asm volatile("cp.async.commit_group;" ::: "memory");
     // Running sums of the log decays.
     Two G[2];
-    float gam[2], rest[2], most = 1.0f;
+    float gam[2], rest[2], most = 1.0f, p_unit = 1.0f / kPScale;
     if (adds) {
         Two g[2];
 #pragma unroll
@@ -230,6 +230,22 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
             most = fmaxf(most, rest[i]);
         }
         most = warp_max(most);
+        if (__any_sync(0xffffffffu, g[0].h > 0.0f || g[1].h > 0.0f)) {
+            // States may grow.  Of the decays D_ij, j <= i, the largest is
+            // that of the largest rise of G: P is divided by a power of two no
+            // smaller than it.  (Without growth D is at most 1, and P's unit
+            // does not depend on the decays.)
+            float low = fminf(G[0].h, G[1].h);      // of this lane's tokens and those before
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, low, o);
+                if (lane >= o) low = fminf(low, up);
+            }
+            const float below = __shfl_up_sync(0xffffffffu, low, 1);      // of the lanes before
+            float rise = fmaxf(G[1].h - G[0].h, 0.0f);
+            if (lane > 0) rise = fmaxf(rise, fmaxf(G[0].h, G[1].h) - below);
+            p_unit *= __uint_as_float((uint32_t)(127 + (int)ceilf(fminf(warp_max(rise), 120.0f))) << 23);
+        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");      // a lane reads its own copies only
 #pragma unroll 1
@@ -309,7 +325,10 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
             vec[V_OS * kChunk + t] = qs * gam[i];
             vec[V_DV * kChunk + t] = b * k;
             vec[V_DS * kChunk + t] = bk * gam[i];
-            if (t == 0) vec[V_MISC * kChunk] = most;
+            if (t == 0) {
+                vec[V_MISC * kChunk + kMost] = most;
+                vec[V_MISC * kChunk + kPUnit] = p_unit;
+            }
         }
     }
     __syncthreads();      // the vectors are there
@@ -326,7 +345,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         const float *ghi = vec + V_GHI * kChunk, *glo = vec + V_GLO * kChunk;
         const int i = (warp & 1) * 32 + lane, ib = i >> 4;
         const bool isk = warp >= 2;
-        const float gi = ghi[i], li = glo[i], f = isk ? vec[V_BETA * kChunk + i] : kPScale;
+        const float gi = ghi[i], li = glo[i], f = isk ? vec[V_BETA * kChunk + i] : pow2_inv(vec[V_MISC * kChunk + kPUnit]);
         const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
         const int at = (i >> 3) * 8 * kTile + (i & 7) * 16;      // of column 0 in an image
 #pragma unroll 1
