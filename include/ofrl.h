@@ -481,6 +481,13 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  * unspecified (every access stays in bounds).  Tokens at and after the last
  * end belong to no episode; their outputs and gradients are not written.
  *
+ * What is not finite stays where the recurrence takes it: an element of v in
+ * its channel, k, g or beta of a token in all channels of the head, reach the
+ * outputs and states from that token on, q its own output alone, and nothing
+ * reaches an earlier token, another channel or another episode.  Gradients
+ * keep to that for v; a q, k, g, beta or dout that is not finite may reach any
+ * gradient of its episode.
+ *
  * Value head h reads query and key head h / (v_heads / k_heads); dq and dk
  * sum over the value heads of a group, in a fixed order. */
 enum { OFRL_DTYPE_F32 = 0, OFRL_DTYPE_BF16 = 1 };

@@ -22,9 +22,10 @@
 // with two planes).  Leaving out the zero blocks of T and P took 3 to 10% off.
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
-#include "delta_mma.cuh"
+#include "delta_redo.cuh"
 
 namespace ofrl {
 namespace delta {
@@ -79,6 +80,8 @@ struct Stage {
                                                                           : 1;
     static constexpr int kShared = kCount * kBytes + NW * kWarp;
     static_assert(kShared <= 226 * 1024, "shared memory");
+    // what goes over an episode again has the state and U there in fp32
+    static_assert(kBytes + NW * kWarp >= NW * 16 * (DK + kChunk) * 4, "shared memory");
 };
 
 // Token rows of one chunk, transposed: x[t][z] = row value at (channel row4 +
@@ -199,12 +202,12 @@ struct Work {
     int64_t slot0;
 };
 // A CTA's rows, part, head and episode, rows changing fastest.
-__device__ __forceinline__ Work work_of(const ChainArgs& a, int slices, int width, int segments, int in_all) {
+__device__ __forceinline__ Work work_of(const ChainArgs& a, unsigned block, int slices, int width, int segments, int in_all) {
     Work w;
     const int hv = a.shape.v_heads;
-    w.row0 = blockIdx.x % slices * width;
-    w.seg = blockIdx.x / slices % segments;
-    const int64_t item = blockIdx.x / slices / segments;
+    w.row0 = block % slices * width;
+    w.seg = block / slices % segments;
+    const int64_t item = block / slices / segments;
     w.e = (int)(item / hv);
     w.head = (int)(item % hv);
     w.khead = w.head / (hv / a.shape.k_heads);
@@ -384,6 +387,57 @@ constexpr int min_ctas() { return NW == 4 ? 2 : 1; }
 // no M.
 enum Pass { kOutputs, kSave, kSummary };
 
+// The pass once more (see delta_redo.cuh), over shared memory that nothing uses
+// any more.  Registers kept for it over the pass are registers that the pass
+// lacks, so what it needs is worked out anew.  Reading block and thread anew too
+// lets the 64-wide and the one-plane passes keep their registers as they were;
+// the 128-wide ones with two planes then spill 150 to 220 bytes more, 28 without
+// (32768 tokens in parts 380 us, 359 without, 348 before there was all this).
+template <typename T, int DK, int NM, int NW, int PASS>
+__device__ __forceinline__ void redo_pass(const ChainArgs& a, uint8_t* smem) {
+    constexpr bool SAVE = PASS == kSave, SUMMARY = PASS == kSummary;
+    constexpr int NO = sizeof(T) == 4 ? 2 : 1;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    const int hv = a.shape.v_heads, dk = a.shape.k_dim, dv = a.shape.v_dim;
+    const int v_pad = (dv + NW * 16 - 1) / (NW * 16) * (NW * 16);
+    constexpr bool kFresh = DK == 64 || NM == 1;
+    const Work w = work_of(a, kFresh ? fresh_block() : blockIdx.x, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
+                           a.segments);
+    const int64_t states = ((int64_t)w.e * hv + w.head) * dv * dk, part = ((int64_t)w.e * hv + w.head) * a.segments + w.seg;
+    const int64_t at = w.slot0 * hv + w.head;
+    const bool given = SUMMARY ? w.seg == 0 : a.segments == 1;
+    Redo r;
+    r.tid = (int)(kFresh ? fresh_thread() : threadIdx.x);
+    r.threads = NW * 32;
+    r.in = &a.in;
+    r.v = a.rows;
+    r.v_stride = a.row_stride;
+    r.out = SUMMARY ? nullptr : a.out;
+    r.out_stride = a.out_stride;
+    r.sp = w.sp;
+    r.head = w.head;
+    r.khead = w.khead;
+    r.v_heads = hv;
+    r.dk = dk;
+    r.dv = dv;
+    r.row0 = w.row0;
+    r.rows = NW * 16;
+    r.map0 = SUMMARY ? v_pad : INT_MAX;
+    r.first = given ? (a.first ? a.first + states : nullptr) : SUMMARY ? nullptr : a.seg_state + part * dv * dk;
+    r.last = SUMMARY ? a.seg_state + (part + 1) * dv * dk : a.last && w.seg == a.segments - 1 ? a.last + states : nullptr;
+    r.map = SUMMARY ? a.seg_map + part * 2 * DK * DK * 2 : nullptr;
+    r.map_unit = SUMMARY ? a.seg_unit + part * 8 : nullptr;
+    r.state_img = SAVE ? a.state_img + at * NO * NW * 16 * DK * 2 : nullptr;
+    r.vec_img = SAVE ? a.vec_img + at * NO * NW * 16 * kChunk * 2 : nullptr;
+    r.state_unit = SAVE ? a.state_unit + at : nullptr;
+    r.vec_unit = SAVE ? a.vec_unit + at : nullptr;
+    r.pairs = a.pairs + at * kPairBytes;
+    r.planes = NO;
+    float* state = reinterpret_cast<float*>(smem);
+    redo_rows<T, DK>(r, state, state + NW * 16 * DK);
+}
+
 // NM: planes of S, X, U (and of T and P).
 template <typename T, int DK, int NM, int NW, int PASS>
 __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(const __grid_constant__ ChainArgs a) {
@@ -395,7 +449,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
     __shared__ Ring ring;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v_pad = (a.shape.v_dim + NW * 16 - 1) / (NW * 16) * (NW * 16);
-    const Work w = work_of(a, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
+    const Work w = work_of(a, blockIdx.x, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
                            a.segments);
     ring_init<NW>(ring);
     const int stages = a.stages;
@@ -527,6 +581,11 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                                            (int64_t)w.head * dv + row0,
                                     a.out_stride, rows, dv - row0, mine + 2 * St::kRows);
         }
+        const bool again = __syncthreads_or(!(isfinite(S[0][0]) && isfinite(S[0][2])));      // of two rows
+        if (again && !ring.dead) {
+            redo_pass<T, DK, NM, NW, PASS>(a, smem);
+            return;
+        }
         if (SUMMARY) {
             if (row0 < v_pad) {
                 store_state(a.seg_state + (part + 1) * dv * dk, S, row0, dv, dk);
@@ -554,7 +613,7 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_reverse_kernel(
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const Work w = work_of(a, 1, NW * 16, 1, 1);
+    const Work w = work_of(a, blockIdx.x, 1, NW * 16, 1, 1);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     ring_init<NW>(ring);
     const int stages = a.stages;

@@ -22,7 +22,9 @@
 // read and written by itself 219 and 285; with outputs and dv by the tokens'
 // warps 164 and 165.
 
-#include "delta_mma.cuh"
+#include <climits>
+
+#include "delta_redo.cuh"
 
 namespace ofrl {
 namespace delta {
@@ -136,6 +138,30 @@ __device__ __forceinline__ float group_max(float (&most)[8], float v) {
     group_sync<BAR>();
     return all_max(most);
 }
+// The same, NaN if one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b, float c = 0.0f) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+template <int N>
+__device__ __forceinline__ float half_max_nan(const float (&x)[N]) {
+    float m[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+        m[0] = max_nan(m[0], fabsf(x[c]), fabsf(x[c + 1]));
+        m[1] = max_nan(m[1], fabsf(x[c + 2]), fabsf(x[c + 3]));
+    }
+    return max_nan(m[0], m[1]);
+}
+template <int BAR>
+__device__ __forceinline__ float group_max_nan(float (&most)[8], float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) most[(threadIdx.x >> 5) & 7] = v;
+    group_sync<BAR>();
+    return max_nan(max_nan(max_nan(most[0], most[1], most[2]), most[3], most[4]), max_nan(most[5], most[6], most[7]));
+}
 // x times f as N columns of a row of an operand image that begins at `to`.
 template <int N>
 __device__ __forceinline__ void put_cols(uint8_t* to, const float (&x)[N], float f) {
@@ -151,10 +177,10 @@ struct Episode {
     Span sp;
     int64_t slot0, states;
 };
-__device__ __forceinline__ Episode episode(const TcArgs& a) {
+__device__ __forceinline__ Episode episode(const TcArgs& a, unsigned block) {
     Episode w;
-    const int hv = a.shape.v_heads, e = blockIdx.x / hv;
-    w.head = blockIdx.x % hv;
+    const int hv = a.shape.v_heads, e = block / hv;
+    w.head = block % hv;
     w.khead = w.head / (hv / a.shape.k_heads);
     w.sp = span_of(a.ends, e, (int32_t)a.in.tokens);
     w.chunks = (w.sp.len + kChunk - 1) / kChunk;
@@ -300,8 +326,7 @@ __device__ __forceinline__ void init_bars(Bars& b) {
 // End of a CTA.  After a wait that gave up, products and copies may still be on
 // their way: they are waited for, again with a limit, before TMEM and shared
 // memory are given back.
-__device__ __forceinline__ void finish(const TcArgs& a, Bars& b, uint32_t tmem) {
-    __syncthreads();
+__device__ __forceinline__ void finish(const TcArgs& a, Bars& b, uint32_t tmem) {      // all warps have met
     umma::fence_after_sync();
     if (b.dead) {
         if (threadIdx.x % kTokThreads == 0) {      // the threads that issue the products
@@ -319,6 +344,47 @@ __device__ __forceinline__ void finish(const TcArgs& a, Bars& b, uint32_t tmem) 
     if (threadIdx.x < 32) umma::tmem_dealloc(tmem, 512);
 }
 
+// The forward pass once more (see delta_redo.cuh), over shared memory and
+// images that nothing uses any more.
+template <int DK, bool SAVE>
+__device__ __forceinline__ void redo_pass(const TcArgs& a, uint8_t* smem) {
+    using S = Smem<DK>;
+    static_assert(S::kBytes >= kRows * (DK + kChunk) * 4, "shared memory");
+    asm volatile("cp.async.bulk.wait_group 0;\n\tfence.proxy.async;" ::: "memory");      // images on their way
+    __syncthreads();
+    const Episode w = episode(a, fresh_block());
+    const int64_t at = w.slot0 * a.shape.v_heads + w.head;
+    Redo r;
+    r.tid = (int)fresh_thread();
+    r.threads = kThreads;
+    r.in = &a.in;
+    r.v = a.rows;
+    r.v_stride = a.row_stride;
+    r.out = a.out;
+    r.out_stride = a.out_stride;
+    r.sp = w.sp;
+    r.head = w.head;
+    r.khead = w.khead;
+    r.v_heads = a.shape.v_heads;
+    r.dk = a.shape.k_dim;
+    r.dv = a.shape.v_dim;
+    r.row0 = 0;
+    r.rows = kRows;
+    r.map0 = INT_MAX;
+    r.first = a.first ? a.first + w.states : nullptr;
+    r.last = nullptr;
+    r.map = nullptr;
+    r.map_unit = nullptr;
+    r.state_img = SAVE ? a.state_img + at * S::kState : nullptr;
+    r.vec_img = SAVE ? a.vec_img + at * kTok : nullptr;
+    r.state_unit = SAVE ? a.state_unit + at : nullptr;
+    r.vec_unit = SAVE ? a.vec_unit + at : nullptr;
+    r.pairs = a.pairs + at * kPairBytes;
+    r.planes = 1;
+    float* state = reinterpret_cast<float*>(smem);
+    redo_rows<__nv_bfloat16, DK>(r, state, state + kRows * DK);
+}
+
 // TMEM columns.
 constexpr int t_x = 0, t_q = 64, t_u = 128, t_o = 192, t_s = 256, t_s2 = 384;
 
@@ -329,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) Bars b;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
-    const Episode w = episode(a);
+    const Episode w = episode(a, blockIdx.x);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     init_bars(b);
     // before the wait below: the kernel before lets this one go when all its CTAs have their TMEM
@@ -347,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
     };
     auto keys_at = [&](int n) { return base + S::off_stage + (n & 1) * S::kStage; };
 
+    bool finite = true;
     if (threadIdx.x < kTokThreads) {
         const Turn turn = turn_of(smem + S::off_turn);
         uint4 v[4];
@@ -400,7 +467,8 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
             __syncwarp();
             wait(b, &b.t, n);
             tmem_row(mine + t_u + col, x);
-            const float u_max = group_max<1>(b.most[0], half_max(x) * x_inv), u_up = scale_up(u_max);
+            const float u_max = group_max_nan<1>(b.most[0], half_max_nan(x) * x_inv), u_up = scale_up(u_max);
+            finite &= u_max < INFINITY;
             const float u_inv = pow2_inv(u_up), u_f = u_up * x_inv;
             {
                 // rest U, with a power of two of its own where states grow
@@ -543,6 +611,7 @@ __global__ void __launch_bounds__(kThreads) delta_forward_tc_kernel(const __grid
         }
         if (SAVE && threadIdx.x == kTokThreads) umma::bulk_wait_read();
     }
+    if (__syncthreads_or(!finite) && !b.dead) redo_pass<DK, SAVE>(a, smem);
     finish(a, b, tmem);
 }
 
@@ -555,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, half = (warp >> 2) & 1;
     pdl_wait();
     pdl_trigger();
-    const Episode w = episode(a);
+    const Episode w = episode(a, blockIdx.x);
     const int dk = a.shape.k_dim, dv = a.shape.v_dim;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     init_bars(b);
@@ -785,6 +854,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_tc_kernel(const __grid
                 if (s_col + c < dk) *reinterpret_cast<float4*>(to + s_col + c) = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
         }
     }
+    __syncthreads();
     finish(a, b, tmem);
 }
 
