@@ -47,13 +47,13 @@ __device__ __forceinline__ float pow2f(int e) {
 }
 // x 2^e for |e| <= 252.
 __device__ __forceinline__ float times_pow2(float x, int e) { return x * pow2f(e / 2) * pow2f(e - e / 2); }
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 struct GradShared {
-    static constexpr int NT = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int NT = 2;                             // planes of the images
     static constexpr int kKey = kChunk * DK * 2;
     static constexpr int kVec = DV * kChunk * 2;             // one plane of U^T or R^T
     static constexpr int kSl = DV * kSliceCols * 2;          // one plane of a state's slice
-    static constexpr int kRing = NT == 2 && DK == 128 && DV == 128 ? 1 : 2;
+    static constexpr int kRing = DK == 128 && DV == 128 ? 1 : 2;
     static constexpr int off_u = 2 * NT * kKey;
     static constexpr int off_r = off_u + NT * kVec;
     static constexpr int off_ring = off_r + NT * kVec;
@@ -65,9 +65,9 @@ struct GradShared {
     static constexpr int kBytes = off_sum + kSums;
 };
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_constant__ GradArgs a) {
-    using Sh = GradShared<T, DK, DV>;
+    using Sh = GradShared<DK, DV>;
     constexpr int NT = Sh::NT, CG = DK / 8, KS = DK / 16, KV = DV / 16, SL = DK / kSliceCols, SG = kSliceCols / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar_keys, bar_head, bar_slice[2];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
     // the keys do, where registers allow
     float x[2 * KV][4];
     auto load_dout = [&](int head) {
-        const T* po = static_cast<const T*>(a.dout) + (tok * hv + head) * dv;
+        const float* po = static_cast<const float*>(a.dout) + (tok * hv + head) * dv;
 #pragma unroll
         for (int t = 0; t < 2 * KV; ++t)
 #pragma unroll
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
         int o_exp;
         float rv[2] = {0.0f, 0.0f};
         {
-            const T* pv = static_cast<const T*>(a.in.v) + tok * a.in.v_stride + (int64_t)head * dv;
+            const float* pv = static_cast<const float*>(a.in.v) + tok * a.in.v_stride + (int64_t)head * dv;
 #pragma unroll
             for (int t = 0; t < 2 * KV; ++t)
 #pragma unroll
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
                             const int i = i0 + 8 * (z & 1), c = k * 16 + 8 * (z >> 1) + col2;
                             if (i < rows && c < dv) {
                                 const float2 r = unpack_h(f[z]);
-                                const T* p = pv + i * a.in.v_stride + c;
-                                rv[z & 1] += (r.x * to_f(p[0]) + r.y * to_f(p[1])) * ru;
+                                const float* p = pv + i * a.in.v_stride + c;
+                                rv[z & 1] += (r.x * p[0] + r.y * p[1]) * ru;
                             }
                         }
                     }
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
                         (q + beta[i] * k) - row(R_COL);
                 const float kap = pow2_inv(vec[V_KINV * kChunk + i]);
                 if (i < rows && s_at[2] == 0)
-                    static_cast<T*>(a.grads.dbeta)[(tok + i) * a.grads.beta_stride + head] =
-                        from_f<T>((row(R_RV) + k + row(R_BETA)) * kap * kap);
+                    static_cast<float*>(a.grads.dbeta)[(tok + i) * a.grads.beta_stride + head] =
+                        (row(R_RV) + k + row(R_BETA)) * kap * kap;
             }
             float sdot = 0.0f;
 #pragma unroll
@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
             for (int z = 0; z < 2; ++z) {
                 const int i = 2 * lane + z;
                 if (i < rows && s_at[2] == 0)
-                    static_cast<T*>(a.grads.dg)[(tok + i) * a.grads.g_stride + head] =
-                        from_f<T>(total - (z ? before + dG[0] : before));
+                    static_cast<float*>(a.grads.dg)[(tok + i) * a.grads.g_stride + head] =
+                        total - (z ? before + dG[0] : before);
             }
         }
         if (g + 1 < group) {
@@ -484,28 +484,28 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(const __grid_c
                 const int i = rb * 16 + row4 + 8 * h, c = n * kSliceCols + (2 * hf + t) * 8 + col2;
                 if (i >= rows || c >= dk) continue;
                 const float qi = vec[V_QINV * kChunk + i], ki = vec[V_KINV * kChunk + i];
-                T* pq = static_cast<T*>(a.grads.dq) + (tok + i) * a.grads.q_stride + (int64_t)khead * dk + c;
-                T* pk = static_cast<T*>(a.grads.dk) + (tok + i) * a.grads.k_stride + (int64_t)khead * dk + c;
-                pq[0] = from_f<T>(dq[n][t][2 * h] * qi);
-                pq[1] = from_f<T>(dq[n][t][2 * h + 1] * qi);
-                pk[0] = from_f<T>(dkk[n][t][2 * h] * ki);
-                pk[1] = from_f<T>(dkk[n][t][2 * h + 1] * ki);
+                float* pq = static_cast<float*>(a.grads.dq) + (tok + i) * a.grads.q_stride + (int64_t)khead * dk + c;
+                float* pk = static_cast<float*>(a.grads.dk) + (tok + i) * a.grads.k_stride + (int64_t)khead * dk + c;
+                pq[0] = dq[n][t][2 * h] * qi;
+                pq[1] = dq[n][t][2 * h + 1] * qi;
+                pk[0] = dkk[n][t][2 * h] * ki;
+                pk[1] = dkk[n][t][2 * h + 1] * ki;
             }
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t run(const GradArgs& g, int64_t grid, cudaStream_t st) {
-    constexpr int smem = GradShared<T, DK, DV>::kBytes;
+    constexpr int smem = GradShared<DK, DV>::kBytes;
     static_assert(smem <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = opt_in(delta_grad_kernel<T, DK, DV>, smem, done);
+    const cudaError_t e = opt_in(delta_grad_kernel<DK, DV>, smem, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(delta_grad_kernel<T, DK, DV>, dim3((unsigned)grid), dim3(kGradThreads), smem, st, g);
+    return launch_pdl(delta_grad_kernel<DK, DV>, dim3((unsigned)grid), dim3(kGradThreads), smem, st, g);
 }
 
 cudaError_t pick(const GradArgs& g, int64_t grid, cudaStream_t st) {
-    if (g.shape.k_dim > 64) return g.shape.v_dim > 64 ? run<float, 128, 128>(g, grid, st) : run<float, 128, 64>(g, grid, st);
-    return g.shape.v_dim > 64 ? run<float, 64, 128>(g, grid, st) : run<float, 64, 64>(g, grid, st);
+    if (g.shape.k_dim > 64) return g.shape.v_dim > 64 ? run<128, 128>(g, grid, st) : run<128, 64>(g, grid, st);
+    return g.shape.v_dim > 64 ? run<64, 128>(g, grid, st) : run<64, 64>(g, grid, st);
 }
 
 }  // namespace
