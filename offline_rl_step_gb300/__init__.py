@@ -734,9 +734,18 @@ class TensorList:
             pass
 
 
+def _open(tensors: TensorList, name: str):
+    """The handle of a list that is open (NULL would say that there is none)."""
+    if not isinstance(tensors, TensorList):
+        raise TypeError(f"{name} must be a TensorList")
+    if tensors.handle is None:
+        raise ValueError(f"{name} is closed")
+    return tensors.handle
+
+
 def global_norm(tensors: TensorList, norm_out, stream=None):
     """norm_out[0] = the 2-norm over all elements of all tensors (adam_step's grad_norm)."""
-    code = tensors._lib.ofrl_global_norm(tensors.handle, _dense(norm_out, F32, (1,), "norm_out"),
+    code = tensors._lib.ofrl_global_norm(_open(tensors, "tensors"), _dense(norm_out, F32, (1,), "norm_out"),
                                          _raw_stream(stream, tensors.device))
     if code != _abi.OK:
         _abi.check("ofrl_global_norm", code)
@@ -745,7 +754,8 @@ def global_norm(tensors: TensorList, norm_out, stream=None):
 def global_norm_clip(tensors: TensorList, max_norm: float, norm_out, out: Optional[TensorList] = None, stream=None):
     """global_norm, then every element times min(1, max_norm / norm), in place or into the tensors of `out`."""
     code = tensors._lib.ofrl_global_norm_clip(
-        tensors.handle, max_norm, _dense(norm_out, F32, (1,), "norm_out"), None if out is None else out.handle,
+        _open(tensors, "tensors"), max_norm, _dense(norm_out, F32, (1,), "norm_out"),
+        None if out is None else _open(out, "out"),
         _raw_stream(stream, tensors.device))
     if code != _abi.OK:
         _abi.check("ofrl_global_norm_clip", code)
