@@ -466,11 +466,20 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  *   u_t = beta_t (v_t - a_t S_{t-1} k_t),   o_t = scale S_t q_t,
  *
  * so S_t k_t moves from its decayed prediction toward v_t by beta_t |k_t|^2.
- * With unit keys and beta in [0, 1] the state stays bounded; larger
- * beta |k|^2 is computed as it stands.  g_t = -inf forgets everything before
- * t; g_t > 0 lets the state grow (the sum of 64 consecutive log decays has to
- * stay below 88, where exp leaves fp32).  No counterpart on the pages, whose
- * networks see one transition at a time.
+ * With unit keys and beta in [0, 1] the state stays bounded.  g_t = -inf forgets
+ * everything before t; g_t > 0, or beta |k|^2 above two, lets the state grow.
+ * Where it grows by more than 2^16 within 64 tokens (2^24 where outputs and
+ * states asked for are all bf16) a forward call goes over the episode token by
+ * token, about a microsecond each.  Beyond 2^20 (fp32 tokens) or 2^24 (bf16)
+ * within 64 tokens, gradients of these tokens and of those before them in the
+ * episode are NaN.  No counterpart on the pages, whose networks see one
+ * transition at a time.
+ *
+ * What is kept of operands: fp32 tokens 22 bits and bf16 tokens 11, relative to
+ * the largest element of a row of q or k, and of up to 64 tokens of v, states and
+ * what is made of them; sums, decays and states are fp32, and with bf16 tokens
+ * states asked for are made from 22 bits, d_init from 11.  Rows of q and k whose
+ * largest element lies outside 2^-60 .. 2^60 keep fewer.
  *
  * Tokens are transitions in buffer order: token t of episode e lies between
  * episode_ends[e - 1] (0 for the first) and episode_ends[e], the convention of

@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
     }
     // block row `warp` of T^T to global memory, with its power of two: a lane
     // takes eight columns of a row, four times
+    float t_most = 0.0f;
     {
         float x[4][8];
         float mx = 0.0f;
@@ -522,7 +523,8 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
 #pragma unroll
             for (int z = 0; z < 8; ++z) mx = fmaxf(mx, fabsf(x[k][z]));
         }
-        const float up = scale_up(warp_max(mx));
+        t_most = warp_max(mx);
+        const float up = scale_up(t_most);
         if (lane < 16) {
             const int j = warp * 16 + lane;
             const float inv = pow2_inv(up);
@@ -541,7 +543,24 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
                     make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
         }
     }
-    __syncthreads();
+    // A chunk within which states grow, by g or by beta |k|^2 above two, beyond what
+    // operands under one power of two hold: x becomes NaN, which makes the chain go
+    // over the episode token by token (delta_redo.cuh).  Gradients have no such
+    // way: beyond their limit, scale kq becomes NaN and with it the gradients of
+    // this chunk and those before it.  Outputs of a chunk's first tokens were 3e-5
+    // of their size off after growth of 2^18 in fp32 and 1e-2 after 2^28 in bf16,
+    // gradients 8e-7 and 3.6e-4 (fp32) and 1.7e-3 both times, all of them wrong
+    // after 2^37.
+    constexpr float kReads = NM == 2 ? 0x1p16f : 0x1p24f, kLearns = sizeof(T) == 4 ? 0x1p20f : 0x1p24f;
+    const float grows = fmaxf(t_most, vec[V_MISC * kChunk + kPUnit] * kPScale);
+    if (__syncthreads_or(grows > kReads)) {
+        const bool learns = !__syncthreads_or(grows > kLearns);
+        if (threadIdx.x < kChunk) {
+            vec[V_XV * kChunk + threadIdx.x] = NAN;
+            if (!learns) vec[V_QS * kChunk + threadIdx.x] = NAN;
+        }
+        __syncthreads();
+    }
     for (int i = threadIdx.x; i < kVecBytes / 16; i += kPrepThreads)
         reinterpret_cast<uint4*>(pairs + 2 * kSquare)[i] = reinterpret_cast<const uint4*>(vec)[i];
     umma::fence_after_sync();
