@@ -468,9 +468,9 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  * so S_t k_t moves from its decayed prediction toward v_t by beta_t |k_t|^2.
  * With unit keys and beta in [0, 1] the state stays bounded.  g_t = -inf forgets
  * everything before t; g_t > 0, or beta |k|^2 above two, lets the state grow.
- * Where it grows by more than 2^16 within 64 tokens (2^24 where outputs and
- * states asked for are all bf16) a forward call goes over the episode token by
- * token, about a microsecond each.  Beyond 2^20 (fp32 tokens) or 2^24 (bf16)
+ * Where it grows by more than 2^16 within 64 tokens (2^24 with bf16 tokens and
+ * no final_state) a forward call goes over the episode token by token, about a
+ * microsecond each.  Beyond 2^20 (fp32 tokens) or 2^24 (bf16)
  * within 64 tokens, gradients of these tokens and of those before them in the
  * episode are NaN.  No counterpart on the pages, whose networks see one
  * transition at a time.
@@ -478,8 +478,8 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  * What is kept of operands: fp32 tokens 22 bits and bf16 tokens 11, relative to
  * the largest element of a row of q or k, and of up to 64 tokens of v, states and
  * what is made of them; sums, decays and states are fp32, and with bf16 tokens
- * states asked for are made from 22 bits, d_init from 11.  Rows of q and k whose
- * largest element lies outside 2^-60 .. 2^60 keep fewer.
+ * states asked for are made from 22 bits, d_init from 11.  Rows of k whose largest
+ * element lies outside 2^-60 .. 2^60 keep fewer.
  *
  * Tokens are transitions in buffer order: token t of episode e lies between
  * episode_ends[e - 1] (0 for the first) and episode_ends[e], the convention of

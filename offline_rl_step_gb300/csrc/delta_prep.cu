@@ -75,11 +75,12 @@ struct Raw {
     }
 };
 
-// Power of two that divides a row: its largest magnitude becomes [1, 2).
-__device__ __forceinline__ float row_unit(float amax) {
+// Power of two, 2^-most to 2^most, that divides a row: its largest magnitude
+// becomes [1, 2).  A key's is squared beside beta and stays within 2^60.
+__device__ __forceinline__ float row_unit(float amax, int most) {
     const int e = (int)((__float_as_uint(amax) >> 23) & 255u);
     if (e == 255 || amax == 0.0f) return 1.0f;
-    return __uint_as_float((uint32_t)min(max(e, 127 - 60), 127 + 60) << 23);
+    return __uint_as_float((uint32_t)min(max(e, 127 - most), 127 + most) << 23);
 }
 
 // Unevaluated pairs of floats for running sums of log decays: a difference
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kPrepThreads, NM == 1 ? 6 : 4) delta_prep_kern
         }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const float unit = row_unit(m), inv = pow2_inv(unit);
+        const float unit = row_unit(m, isq ? 126 : 60), inv = pow2_inv(unit);
         if (c4 == 0) (isq ? kqv : kap)[rg * 8 + r] = unit;
 #pragma unroll
         for (int i = 0; i < CG / 4; ++i) {
