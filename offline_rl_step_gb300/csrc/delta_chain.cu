@@ -22,7 +22,6 @@
 // with two planes).  Leaving out the zero blocks of T and P took 3 to 10% off.
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 
 #include "delta_redo.cuh"
@@ -388,34 +387,36 @@ constexpr int min_ctas() { return NW == 4 ? 2 : 1; }
 enum Pass { kOutputs, kSave, kSummary };
 
 // The pass once more (see delta_redo.cuh), over shared memory that nothing uses
-// any more.  Registers kept for it over the pass are registers that the pass
-// lacks, so what it needs is worked out anew.  Reading block and thread anew too
-// lets the 64-wide and the one-plane passes keep their registers as they were;
-// the 128-wide ones with two planes then spill 150 to 220 bytes more, 28 without
-// (32768 tokens in parts 380 us, 359 without, 348 before there was all this).
+// any more.  A part of an episode is gone over from the episode's beginning: its
+// own start comes from summaries that were not finite either, which also spoils
+// what has one power of two with them.  (The first part's start is kept beside the
+// others: the caller's buffer may be that of the final states.)
+//
+// Registers kept for this over the pass are registers that the pass lacks, so
+// what it needs is worked out anew.  Reading block and thread anew too lets the
+// 64-wide and the one-plane passes keep their registers as they were; the 128-wide
+// ones with two planes then spill 220 bytes, 28 without.
 template <typename T, int DK, int NM, int NW, int PASS>
 __device__ __forceinline__ void redo_pass(const ChainArgs& a, uint8_t* smem) {
-    constexpr bool SAVE = PASS == kSave, SUMMARY = PASS == kSummary;
+    constexpr bool SAVE = PASS == kSave;
     constexpr int NO = sizeof(T) == 4 ? 2 : 1;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     const int hv = a.shape.v_heads, dk = a.shape.k_dim, dv = a.shape.v_dim;
-    const int v_pad = (dv + NW * 16 - 1) / (NW * 16) * (NW * 16);
     constexpr bool kFresh = DK == 64 || NM == 1;
-    const Work w = work_of(a, kFresh ? fresh_block() : blockIdx.x, (SUMMARY ? v_pad + DK : v_pad) / (NW * 16), NW * 16, SUMMARY ? a.segments - 1 : a.segments,
-                           a.segments);
-    const int64_t states = ((int64_t)w.e * hv + w.head) * dv * dk, part = ((int64_t)w.e * hv + w.head) * a.segments + w.seg;
-    const int64_t at = w.slot0 * hv + w.head;
-    const bool given = SUMMARY ? w.seg == 0 : a.segments == 1;
+    const Work w = work_of(a, kFresh ? fresh_block() : blockIdx.x, (dv + NW * 16 - 1) / (NW * 16), NW * 16, a.segments, a.segments);
+    const int64_t item = (int64_t)w.e * hv + w.head, at = w.slot0 * hv + w.head;
     Redo r;
     r.tid = (int)(kFresh ? fresh_thread() : threadIdx.x);
     r.threads = NW * 32;
     r.in = &a.in;
     r.v = a.rows;
     r.v_stride = a.row_stride;
-    r.out = SUMMARY ? nullptr : a.out;
+    r.out = a.out;
     r.out_stride = a.out_stride;
-    r.sp = w.sp;
+    r.sp = span_of(a.ends, w.e, (int32_t)a.in.tokens);
+    r.skip = w.sp.start - r.sp.start;
+    r.sp.len = r.skip + w.sp.len;
     r.head = w.head;
     r.khead = w.khead;
     r.v_heads = hv;
@@ -423,11 +424,8 @@ __device__ __forceinline__ void redo_pass(const ChainArgs& a, uint8_t* smem) {
     r.dv = dv;
     r.row0 = w.row0;
     r.rows = NW * 16;
-    r.map0 = SUMMARY ? v_pad : INT_MAX;
-    r.first = given ? (a.first ? a.first + states : nullptr) : SUMMARY ? nullptr : a.seg_state + part * dv * dk;
-    r.last = SUMMARY ? a.seg_state + (part + 1) * dv * dk : a.last && w.seg == a.segments - 1 ? a.last + states : nullptr;
-    r.map = SUMMARY ? a.seg_map + part * 2 * DK * DK * 2 : nullptr;
-    r.map_unit = SUMMARY ? a.seg_unit + part * 8 : nullptr;
+    r.first = a.segments > 1 ? a.seg_state + item * a.segments * dv * dk : a.first ? a.first + item * dv * dk : nullptr;
+    r.last = a.last && w.seg == a.segments - 1 ? a.last + item * dv * dk : nullptr;
     r.state_img = SAVE ? a.state_img + at * NO * NW * 16 * DK * 2 : nullptr;
     r.vec_img = SAVE ? a.vec_img + at * NO * NW * 16 * kChunk * 2 : nullptr;
     r.state_unit = SAVE ? a.state_unit + at : nullptr;
@@ -581,10 +579,12 @@ __global__ void __launch_bounds__(NW * 32, min_ctas<NW>()) delta_forward_kernel(
                                            (int64_t)w.head * dv + row0,
                                     a.out_stride, rows, dv - row0, mine + 2 * St::kRows);
         }
-        const bool again = __syncthreads_or(!(isfinite(S[0][0]) && isfinite(S[0][2])));      // of two rows
-        if (again && !ring.dead) {
-            redo_pass<T, DK, NM, NW, PASS>(a, smem);
-            return;
+        if constexpr (!SUMMARY) {
+            const bool again = __syncthreads_or(!(isfinite(S[0][0]) && isfinite(S[0][2])));      // of two rows
+            if (again && !ring.dead) {
+                redo_pass<T, DK, NM, NW, PASS>(a, smem);
+                return;
+            }
         }
         if (SUMMARY) {
             if (row0 < v_pad) {

@@ -22,8 +22,6 @@
 // read and written by itself 219 and 285; with outputs and dv by the tokens'
 // warps 164 and 165.
 
-#include <climits>
-
 #include "delta_redo.cuh"
 
 namespace ofrl {
@@ -363,6 +361,7 @@ __device__ __forceinline__ void redo_pass(const TcArgs& a, uint8_t* smem) {
     r.out = a.out;
     r.out_stride = a.out_stride;
     r.sp = w.sp;
+    r.skip = 0;
     r.head = w.head;
     r.khead = w.khead;
     r.v_heads = a.shape.v_heads;
@@ -370,11 +369,8 @@ __device__ __forceinline__ void redo_pass(const TcArgs& a, uint8_t* smem) {
     r.dv = a.shape.v_dim;
     r.row0 = 0;
     r.rows = kRows;
-    r.map0 = INT_MAX;
     r.first = a.first ? a.first + w.states : nullptr;
     r.last = nullptr;
-    r.map = nullptr;
-    r.map_unit = nullptr;
     r.state_img = SAVE ? a.state_img + at * S::kState : nullptr;
     r.vec_img = SAVE ? a.vec_img + at * kTok : nullptr;
     r.state_unit = SAVE ? a.state_unit + at : nullptr;

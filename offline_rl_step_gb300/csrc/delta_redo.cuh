@@ -1,4 +1,6 @@
-// What a chain does for an episode with tokens or states that are not finite.
+// What a chain does for an episode with tokens or states that are not finite,
+// or with a chunk within which states grow beyond its operands' range (the
+// preparing kernel makes such a chunk's x NaN).
 //
 // The zeros of T and P are multiplied like everything else, so within a chunk a
 // NaN or an infinity reaches the tokens before it.  Where v, k, g or beta of a
@@ -8,11 +10,12 @@
 // tcgen05, where the last state is not made, at every chunk's largest u), and a
 // CTA that finds one not finite goes over its rows of the episode again, token by
 // token as the recurrence is written, and replaces what it left.  A q that is not
-// finite stays with its token.  What this costs calls that have nothing of the
-// kind: 64 episodes of 256 tokens 26.3 us with and without, about 65k ragged
-// transitions learn 590 us against 584, 32768 tokens in parts 359 against 348 (see
-// redo_pass in delta_chain.cu).  Sealing such channels within the pass cost 7 to
-// 13% of it.
+// finite stays with its token.
+//
+// What this costs calls that have nothing of the kind: 64 episodes of 256 tokens
+// 26.3 us with and without, about 65k ragged transitions learn 589 us against 583,
+// 32768 tokens in parts 350 against 347.  Sealing such channels within the pass
+// cost 7 to 13% of it.
 #pragma once
 
 #include "delta_mma.cuh"
@@ -24,16 +27,14 @@ struct Redo {
     int tid, threads;
     const ofrl_delta_tokens* in;
     const void* v;                  // of token 0
-    void* out;                      // of token 0, or null: no outputs
+    void* out;
     int64_t v_stride, out_stride;
     Span sp;
+    int skip;                       // tokens whose outputs are there already
     int head, khead, v_heads, dk, dv;
     int row0, rows;                 // the CTA's first row, and how many it has
-    int map0;                       // rows from here on are those of a map: unit vectors, with v = 0
     const float* first;             // the episode's and head's state, or null
     float* last;                    // where its state goes afterwards, or null
-    uint8_t* map;                   // where the map's image goes, two planes, and its powers of two per 16 rows
-    float* map_unit;
     // images for the gradients, or null
     uint8_t *state_img, *vec_img;   // of the first chunk and this head
     float *state_unit, *vec_unit;
@@ -73,8 +74,8 @@ __device__ __forceinline__ float cta_most(const Redo& a, const float* x, int n, 
     return m;
 }
 
-// [rows][cols] floats as an image of `planes` planes, `plane` bytes each, its columns in slices of SG groups.
-__device__ __forceinline__ void put_image(const Redo& a, uint8_t* img, const float* x, int rows, int cols, int SG, int planes, int plane, float up) {
+// [rows][cols] floats as an image of `planes` planes, its columns in slices of SG groups.
+__device__ __forceinline__ void put_image(const Redo& a, uint8_t* img, const float* x, int rows, int cols, int SG, int planes, float up) {
     const int RG = rows / 8;
 #pragma unroll 1
     for (int i = a.tid; i < rows * cols; i += a.threads) {
@@ -84,7 +85,7 @@ __device__ __forceinline__ void put_image(const Redo& a, uint8_t* img, const flo
 #pragma unroll 1
         for (int n = 0; n < planes; ++n) {
             const __half h = __float2half_rn(y);
-            *reinterpret_cast<__half*>(to + (int64_t)n * plane) = h;
+            *reinterpret_cast<__half*>(to + (int64_t)n * rows * cols * 2) = h;
             y -= __half2float(h);
         }
     }
@@ -100,9 +101,7 @@ __device__ __forceinline__ void redo_rows(const Redo& a, float* state, float* u)
     for (int i = a.tid; i < a.rows * DK; i += a.threads) {
         const int r = a.row0 + i / DK, c = i % DK;
         float x = 0.0f;
-        if (r >= a.map0)
-            x = r - a.map0 == c ? 1.0f : 0.0f;
-        else if (a.first != nullptr && r < a.dv && c < a.dk)
+        if (a.first != nullptr && r < a.dv && c < a.dk)
             x = a.first[(int64_t)r * a.dk + c];
         state[i] = x;
     }
@@ -113,7 +112,7 @@ __device__ __forceinline__ void redo_rows(const Redo& a, float* state, float* u)
         if (a.state_img != nullptr) {
             const float up = scale_up(cta_most(a, state, a.rows * DK, &red));
             put_image(a, a.state_img + at * a.planes * a.rows * DK * 2, state, a.rows, DK, a.planes == 2 ? kSliceCols / 8 : 1,
-                      a.planes, a.rows * DK * 2, up);
+                      a.planes, up);
             if (a.tid == 0) a.state_unit[at] = pow2_inv(up);
 #pragma unroll 1
             for (int i = a.tid; i < a.rows * kChunk; i += a.threads) u[i] = 0.0f;
@@ -132,8 +131,7 @@ __device__ __forceinline__ void redo_rows(const Redo& a, float* state, float* u)
 #pragma unroll 1
             for (int r = warp; r < a.rows; r += warps) {
                 const int row = a.row0 + r;
-                const bool value = row < a.dv;
-                if (!value && row < a.map0) continue;      // no row: zero, and stays so
+                if (row >= a.dv) break;      // no row: zero, and stays so
                 float* s = state + r * DK;
                 float sk = 0.0f, sq = 0.0f, kq = 0.0f;
 #pragma unroll 1
@@ -146,12 +144,12 @@ __device__ __forceinline__ void redo_rows(const Redo& a, float* state, float* u)
                 sk = warp_sum(sk);
                 sq = warp_sum(sq);
                 kq = warp_sum(kq);
-                const float v = value ? to_f(static_cast<const T*>(a.v)[tok * a.v_stride + (int64_t)a.head * a.dv + row]) : 0.0f;
+                const float v = to_f(static_cast<const T*>(a.v)[tok * a.v_stride + (int64_t)a.head * a.dv + row]);
                 const float x = beta * (v - decay * sk);
 #pragma unroll 1
                 for (int c = lane; c < a.dk; c += 32) s[c] = decay * s[c] + x * to_f(k[c]);
                 if (lane == 0) {
-                    if (a.out != nullptr && value)
+                    if (t >= a.skip)
                         static_cast<T*>(a.out)[tok * a.out_stride + (int64_t)a.head * a.dv + row] =
                             from_f<T>(a.in->scale * (decay * sq + x * kq));
                     if (a.state_img != nullptr) u[r * kChunk + t - t0] = kappa * x;
@@ -162,26 +160,16 @@ __device__ __forceinline__ void redo_rows(const Redo& a, float* state, float* u)
         if (a.state_img != nullptr) {
             const float up = scale_up(cta_most(a, u, a.rows * kChunk, &red));
             put_image(a, a.vec_img + at * a.planes * a.rows * kChunk * 2, u, a.rows, kChunk, a.planes == 2 ? 8 : 1, a.planes,
-                      a.rows * kChunk * 2, up);
+                      up);
             if (a.tid == 0) a.vec_unit[at] = pow2_inv(up);
             __syncthreads();
         }
     }
-    if (a.map != nullptr && a.row0 >= a.map0) {
-        for (int r = 0; r < a.rows; r += 16) {
-            const float up = scale_up(cta_most(a, state + r * DK, 16 * DK, &red));
-            const int row = a.row0 + r - a.map0;
-            put_image(a, a.map + row * DK * 2, state + r * DK, 16, DK, DK / 8, 2, DK * DK * 2, up);
-            if (a.tid == 0) a.map_unit[row / 16] = pow2_inv(up);
-        }
-    } else if (a.last != nullptr) {
-        // the join scales what it reads: there, infinities too leave their row only
-#pragma unroll 1
+    if (a.last != nullptr)
         for (int i = a.tid; i < a.rows * DK; i += a.threads) {
             const int r = a.row0 + i / DK, c = i % DK;
-            if (r < a.dv && c < a.dk) a.last[(int64_t)r * a.dk + c] = a.map != nullptr ? nan_if_not_finite(state[i]) : state[i];
+            if (r < a.dv && c < a.dk) a.last[(int64_t)r * a.dk + c] = state[i];
         }
-    }
 }
 
 }  // namespace delta

@@ -108,3 +108,21 @@ def test_gradients_are_right_or_not_finite(dtype, hk, hv, dk, dv, g, strength):
                         limit += 2.0 ** -11 * np.linalg.norm(sizes[name][at.start - lo:at.stop - lo])
                     assert np.linalg.norm(x[at] - y[at]) <= limit, (name, e, off(x[at], y[at]))
         lo = hi
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128)])
+def test_growth_within_one_part_of_a_long_episode(dtype, dk, dv):
+    """Read in parts: growth of 2^40 within one of them, which the parts after it start from."""
+    need_gpu()
+    lengths = [1000]
+    d = _inputs(dtype, 1, 1, dk, dv, 0, 0, lengths)
+    d["g"][400:460] = ROUND[dtype](np.float32(0.46))
+    d["g"][500:560] = ROUND[dtype](np.float32(-0.46))
+    for states in (True, False):
+        out, final = _run(d, lengths, dtype, states=states, grads=False)[:2]
+        want = _want(d, lengths, states=states)
+        for t in range(0, 1000, 8):
+            assert off(out[t:t + 8], want[0][t:t + 8]) <= max(BOUND[dtype], 2e-5), (t, off(out[t:t + 8], want[0][t:t + 8]))
+        if states:
+            assert off(final, want[1]) <= 2 * STATE_BOUND
