@@ -469,8 +469,8 @@ ofrl_status ofrl_iql_value_fwd_bwd_noalloc(const ofrl_vshape* shape, const float
  * With unit keys and beta in [0, 1] the state stays bounded.  g_t = -inf forgets
  * everything before t; g_t > 0, or beta |k|^2 above two, lets the state grow.
  * Where it grows by more than 2^16 within 64 tokens (2^24 with bf16 tokens and
- * no final_state) a forward call goes over the episode token by token, about a
- * microsecond each.  Beyond 2^20 (fp32 tokens) or 2^24 (bf16)
+ * no final_state) a forward call goes over the episode token by token, 1.5 to 3
+ * microseconds each.  Beyond 2^20 (fp32 tokens) or 2^24 (bf16)
  * within 64 tokens, gradients of these tokens and of those before them in the
  * episode are NaN.  No counterpart on the pages, whose networks see one
  * transition at a time.

@@ -79,8 +79,8 @@ struct Stage {
                                                                           : 1;
     static constexpr int kShared = kCount * kBytes + NW * kWarp;
     static_assert(kShared <= 226 * 1024, "shared memory");
-    // what goes over an episode again has the state and U there in fp32
-    static_assert(kBytes + NW * kWarp >= NW * 16 * (DK + kChunk) * 4, "shared memory");
+    // what goes over an episode again takes its place
+    static_assert(kBytes + NW * kWarp >= redo_bytes<DK>(NW * 16), "shared memory");
 };
 
 // Token rows of one chunk, transposed: x[t][z] = row value at (channel row4 +
@@ -432,8 +432,7 @@ __device__ __forceinline__ void redo_pass(const ChainArgs& a, uint8_t* smem) {
     r.vec_unit = SAVE ? a.vec_unit + at : nullptr;
     r.pairs = a.pairs + at * kPairBytes;
     r.planes = NO;
-    float* state = reinterpret_cast<float*>(smem);
-    redo_rows<T, DK>(r, state, state + NW * 16 * DK);
+    redo_rows<T, DK>(r, reinterpret_cast<float*>(smem));
 }
 
 // NM: planes of S, X, U (and of T and P).
@@ -924,7 +923,7 @@ ChainArgs base_args(const SeqLaunch& a, const Prepared& p, const Images& img) {
 // or fewer half the rows would be empty: a chunk takes a CTA 4.4 us there
 // however many rows are filled, against 3 us for four warps of mma.sync that
 // hold 64 channels' state in registers.  About 65k ragged transitions, four
-// heads of 128 x 128, forward and reverse: 137 + 161 us, on mma.sync 197 + 206.
+// heads of 128 x 128, forward and reverse: 143 + 162 us, on mma.sync 197 + 206.
 bool rows_of_tcgen05(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_BF16 && s.v_dim > 64; }
 
 // A forward pass that saves nothing has less to convert, and where two CTAs per
@@ -954,7 +953,7 @@ int forward_together(const ofrl_delta_shape& s, int planes) {
 // 1.7 n / g + 0.4 g instead of n; g = 2 sqrt(n) is best, but no more than the
 // SMs hold at once in the last pass (a few CTAs more would be a second round).
 // One sequence of 32768 tokens, four heads of 128, with its final state: 2100 us
-// whole, 346 in 19 parts, in 20 (160 CTAs on 152 SMs) 65 more.  Three of 1000 tokens,
+// whole, 350 in 19 parts, in 20 (160 CTAs on 152 SMs) 65 more.  Three of 1000 tokens,
 // two heads of 64, fp32: 73 us whole, 38 in 7 parts of 3 chunks, 33 in 8 of 2.
 int segments_of(const SeqLaunch& a, int planes) {
     const int64_t items = (int64_t)a.episodes * a.shape.v_heads;

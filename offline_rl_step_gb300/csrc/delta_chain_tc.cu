@@ -17,8 +17,8 @@
 //
 // Bound by the chain's latency, three products (0.3 to 0.8 us each with their
 // operands' reads) and three conversions: 4 us a chunk of 128 x 128 forward, 5
-// back.  About 65k ragged transitions, four heads of 128 x 128: 137 us forward
-// (4.3 TB/s in all), 161 us back.  With two warpgroups and every token element
+// back.  About 65k ragged transitions, four heads of 128 x 128: 143 us forward
+// (4.1 TB/s in all), 162 us back.  With two warpgroups and every token element
 // read and written by itself 219 and 285; with outputs and dv by the tokens'
 // warps 164 and 165.
 
@@ -347,7 +347,7 @@ __device__ __forceinline__ void finish(const TcArgs& a, Bars& b, uint32_t tmem) 
 template <int DK, bool SAVE>
 __device__ __forceinline__ void redo_pass(const TcArgs& a, uint8_t* smem) {
     using S = Smem<DK>;
-    static_assert(S::kBytes >= kRows * (DK + kChunk) * 4, "shared memory");
+    static_assert(S::kBytes >= redo_bytes<DK>(kRows), "shared memory");
     asm volatile("cp.async.bulk.wait_group 0;\n\tfence.proxy.async;" ::: "memory");      // images on their way
     __syncthreads();
     const Episode w = episode(a, fresh_block());
@@ -377,8 +377,7 @@ __device__ __forceinline__ void redo_pass(const TcArgs& a, uint8_t* smem) {
     r.vec_unit = SAVE ? a.vec_unit + at : nullptr;
     r.pairs = a.pairs + at * kPairBytes;
     r.planes = 1;
-    float* state = reinterpret_cast<float*>(smem);
-    redo_rows<__nv_bfloat16, DK>(r, state, state + kRows * DK);
+    redo_rows<__nv_bfloat16, DK>(r, reinterpret_cast<float*>(smem));
 }
 
 // TMEM columns.
