@@ -20,10 +20,14 @@
 //   <S_0, dS_0> = gamma_last <S_0, dS_1> + sum_i [q_i (state part of dq_i) + k_i (state part of the row part)]:
 // S_0 enters times exp(G) only.  The second form of dg_i is taken: it is exactly zero where S_0 is.
 //
-// Three or five launches: delta_prep.cu makes per chunk what needs no state
-// (T, P, scaled keys and queries); delta_chain.cu walks the chunks of every
-// episode forward and, for gradients, back; delta_grad.cu then takes every
-// chunk by itself.  This file lays out the buffers between them.
+// Read: one launch where token by token is taken (delta_step.cu), else two, or
+// four in parts (delta_chain.cu).  Learn: two forward and two back.
+// delta_prep.cu makes per chunk what needs no state (T, P, scaled keys and
+// queries); delta_chain.cu and delta_chain_tc.cu walk the chunks of every episode
+// forward and, for gradients, back; delta_grad.cu and delta_grad_tc.cu then take
+// every chunk by itself; delta_redo.cuh goes over an episode whose states do not
+// stay finite or within the chunks' range.  This file lays out the buffers between
+// them.
 
 #include <algorithm>
 
@@ -67,7 +71,9 @@ int planes_of(const SeqLaunch& a) { return a.shape.dtype == OFRL_DTYPE_F32 || a.
 // for two launches and one chunk (13.8 with two planes), then 25 ns for each
 // chunk of a head, times the planes, twice for more than 64 channels.  The host
 // knows the mean length only and takes the longest episode for twice that; the
-// bound on the tokens keeps the worst case, all of them in one episode, at 2 ms.
+// bound on the tokens keeps the worst case, all of them in one episode, at 2 ms
+// (one episode of 3801 tokens among 199 of one, one head of 64, fp32: 1100 us,
+// chunked 298; one of 7600 among 399, 8 x 8: 1774 and 588).
 // Measured, two heads of 64, fp32, token by token / chunked: 16 episodes of 16
 // tokens 7.2 / 13.8 us, of 48 16.4 / 14.6; 1024 of 4 47.7 / 129.7; 256 of 32
 // 68.7 / 40.2.  Four heads of 128, bf16: 16 of 4 7.8 / 13.3, 64 of 16 68.9 / 22.2.
