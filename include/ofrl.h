@@ -583,6 +583,243 @@ ofrl_status ofrl_delta_backward(ofrl_delta* ctx, const ofrl_delta_tokens* in, co
 ofrl_status ofrl_delta_step(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* slot_idx, int32_t slots,
                             const float* state_in, float* state_out, void* out, void* stream);
 
+/* ---- state space blocks over packed episodes ------------------------------- */
+
+/* The other sequence memory, and what stands around either one in a block:
+ *
+ *   short causal convolution    ofrl_conv_*       before the memory
+ *   selective scan              ofrl_scan_*       the memory: decays per channel and state
+ *   gated norm                  ofrl_gated_norm   after it
+ *   residual norm               ofrl_residual_norm    before the next block
+ *
+ * Episodes are packed as for the gated delta rule: token t of episode e lies
+ * between episode_ends[e - 1] (0 for the first) and episode_ends[e], device
+ * int32, ascending, equal ends for an empty episode.  An end below its
+ * predecessor or above `tokens` is counted in OFRL_STAT_BAD_INDEX by the
+ * forward call, whose results are then unspecified (every access stays in
+ * bounds).  Tokens at and after the last end belong to no episode; their
+ * outputs and gradients are not written.
+ *
+ * Token buffers ("rows") have a stride, the distance between tokens in
+ * elements, and contiguous elements within a token.  They are 16-byte aligned
+ * with strides that are multiples of 16 bytes, except b and c of the scan,
+ * which have any alignment and stride.  Token types are OFRL_DTYPE_*; weights,
+ * their gradients, the scan's states and all arithmetic are fp32, and sums that
+ * run over tokens are added in an order fixed by the sizes.  Outputs must not
+ * overlap inputs unless said otherwise.  No counterpart on the pages, whose
+ * networks see one transition at a time. */
+
+/* out_t = act(bias + sum_{j < width} weight[j] x_{t - width + 1 + j}) per
+ * channel, within an episode; before its first token stand the width - 1
+ * inputs of init_state, oldest first, or zeros.  What is not finite stays in
+ * its channel and in the `width` tokens from its own on. */
+enum { OFRL_ACT_NONE = 0, OFRL_ACT_SILU = 1 };
+typedef struct {
+    int32_t channels;     /* 8 .. 65536, a multiple of 8 */
+    int32_t width;        /* 2 .. 4 */
+    int32_t activation;   /* OFRL_ACT_* */
+    int32_t dtype;        /* OFRL_DTYPE_* of x, out, their gradients and the states */
+} ofrl_conv_shape;
+
+typedef struct {
+    const void* x;          /* [tokens][channels] */
+    const float* weight;    /* [channels, width] */
+    const float* bias;      /* [channels] or NULL */
+    int64_t x_stride;
+    int64_t tokens;         /* 0 .. 2^31-1 */
+} ofrl_conv_tokens;
+
+/* Gradients, written (not accumulated). */
+typedef struct {
+    void* dx;               /* [tokens][channels] */
+    float* dweight;         /* [channels, width] */
+    float* dbias;           /* [channels] or NULL: not wanted */
+    int64_t x_stride;
+} ofrl_conv_grads;
+
+typedef struct ofrl_conv ofrl_conv;
+
+/* The workspace for calls of up to max_tokens tokens in up to max_episodes
+ * episodes (0 of each is enough for ofrl_conv_step; backward = 0 refuses
+ * ofrl_conv_backward).  The only allocating call; binds to the current device.
+ * One ofrl_conv must not be used by two calls that overlap on the GPU. */
+ofrl_status ofrl_conv_create(const ofrl_conv_shape* shape, int64_t max_tokens, int32_t max_episodes, int32_t backward,
+                             ofrl_conv** out);
+ofrl_status ofrl_conv_destroy(ofrl_conv* ctx);
+ofrl_status ofrl_conv_poll_status(ofrl_conv* ctx, void* stream, int32_t* words_out);
+int64_t ofrl_conv_workspace_bytes(const ofrl_conv_shape* shape, int64_t max_tokens, int32_t max_episodes,
+                                  int32_t backward);
+
+/* init_state, final_state: [num_episodes, channels, width - 1] in the tokens'
+ * type, or NULL (zeros; not wanted).  final_state holds each episode's last
+ * width - 1 inputs (an episode of fewer ends on its initial ones); it may be
+ * init_state only where no backward call follows. */
+ofrl_status ofrl_conv_forward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
+                              int32_t num_episodes, const void* init_state, void* out, int64_t out_stride,
+                              void* final_state, void* stream);
+
+/* Gradients of the forward call with the same inputs: dout rows of out's
+ * gradient; d_final: gradient of final_state, in the tokens' type, or NULL;
+ * d_init: gradient of init_state, fp32, or NULL (not wanted). */
+ofrl_status ofrl_conv_backward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
+                               int32_t num_episodes, const void* init_state, const void* dout, int64_t dout_stride,
+                               const void* d_final, const ofrl_conv_grads* grads, float* d_init, void* stream);
+
+/* One token for each of in->tokens environments: state_in, state_out [slots,
+ * channels, width - 1] (the same buffer updates in place); slot_idx as
+ * ofrl_delta_step's. */
+ofrl_status ofrl_conv_step(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* slot_idx, int32_t slots,
+                           const void* state_in, void* state_out, void* out, int64_t out_stride, void* stream);
+
+/* Per channel d and state n, with B and C of the channel's group
+ * (d / (channels / groups)):
+ *
+ *   delta_t = softplus(dt_t + dt_bias)           (or dt_t + dt_bias)
+ *   h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t B_t[n] x_t
+ *   y_t = sum_n C_t[n] h_t[n] + D x_t,   out_t = y_t silu(z_t)   (z NULL: y_t)
+ *
+ * The state is zero, or init_state, when an episode starts.  What is not finite
+ * stays where the recurrence takes it: x, dt and z of a channel in that
+ * channel, B and C of a token in their group, from that token on and within
+ * the episode.  Gradients keep to the episode, those of A, D and dt_bias,
+ * which sum over tokens, excepted. */
+typedef struct {
+    int32_t channels;     /* 8 .. 65536 */
+    int32_t state_dim;    /* N: 4 .. 64, a multiple of 4 */
+    int32_t groups;       /* divides channels; channels / groups a multiple of 8 */
+    int32_t dtype;        /* OFRL_DTYPE_* of every token buffer */
+    int32_t softplus;     /* 1: delta = softplus(dt + dt_bias); 0: dt + dt_bias */
+} ofrl_scan_shape;
+
+typedef struct {
+    const void* x;          /* [tokens][channels] */
+    const void* dt;         /* [tokens][channels] */
+    const void* b;          /* [tokens][groups, N] */
+    const void* c;          /* [tokens][groups, N] */
+    const void* z;          /* [tokens][channels] or NULL */
+    const float* a;         /* [channels, N], 16-byte aligned; negative for states that decay */
+    const float* d;         /* [channels] or NULL (zero) */
+    const float* dt_bias;   /* [channels] or NULL (zero) */
+    int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+    int64_t tokens;         /* 0 .. 2^31-1 */
+} ofrl_scan_tokens;
+
+/* Gradients, written (not accumulated); same layouts, alignments and stride
+ * rules as what they belong to.  dz is NULL where z is; dd and ddt_bias may be
+ * NULL (not wanted). */
+typedef struct {
+    void* dx;
+    void* ddt;
+    void* db;
+    void* dc;
+    void* dz;
+    float* da;
+    float* dd;
+    float* ddt_bias;
+    int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+} ofrl_scan_grads;
+
+typedef struct ofrl_scan ofrl_scan;
+
+/* As ofrl_conv_create and its companions. */
+ofrl_status ofrl_scan_create(const ofrl_scan_shape* shape, int64_t max_tokens, int32_t max_episodes, int32_t backward,
+                             ofrl_scan** out);
+ofrl_status ofrl_scan_destroy(ofrl_scan* ctx);
+ofrl_status ofrl_scan_poll_status(ofrl_scan* ctx, void* stream, int32_t* words_out);
+int64_t ofrl_scan_workspace_bytes(const ofrl_scan_shape* shape, int64_t max_tokens, int32_t max_episodes,
+                                  int32_t backward);
+
+/* Bytes of the `saved` buffer (device, 16-byte aligned, the caller's) that
+ * hands a forward call's states to its backward call, or -1. */
+int64_t ofrl_scan_saved_bytes(const ofrl_scan_shape* shape, int64_t tokens);
+
+/* init_state, final_state: device fp32 [num_episodes, channels, N], 16-byte
+ * aligned, or NULL (zero; not wanted); the same buffer only where no backward
+ * call follows.  saved: as above, or NULL (no backward call will follow). */
+ofrl_status ofrl_scan_forward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* episode_ends,
+                              int32_t num_episodes, const float* init_state, void* out, int64_t out_stride,
+                              float* final_state, void* saved, void* stream);
+
+/* Gradients of the forward call that filled `saved` with the same inputs: dout
+ * rows of out's gradient; d_final: gradient of final_state, or NULL (zero);
+ * d_init: gradient of init_state, or NULL (not wanted); may be d_final. */
+ofrl_status ofrl_scan_backward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* episode_ends,
+                               int32_t num_episodes, const float* init_state, const void* saved, const void* dout,
+                               int64_t dout_stride, const float* d_final, const ofrl_scan_grads* grads, float* d_init,
+                               void* stream);
+
+/* One token for each of in->tokens environments: state_in, state_out fp32
+ * [slots, channels, N], 16-byte aligned (the same buffer updates in place);
+ * slot_idx as ofrl_delta_step's. */
+ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* slot_idx, int32_t slots,
+                           const float* state_in, float* state_out, void* out, int64_t out_stride, void* stream);
+
+/* Norms of rows: rms(v) = sqrt(mean(v^2) + eps) over each of `groups` equal
+ * groups of a row's channels.
+ *
+ *   gated norm      gate_first = 0:  out = weight x / rms(x) silu(z)
+ *                   gate_first = 1:  out = weight u / rms(u),  u = x silu(z)
+ *   residual norm   h = residual + scale x,  residual_out = h,  out = weight h / rms(h)
+ *
+ * A row is read whole before its outputs are written, so in a forward call out
+ * may be x (same stride), and residual_out may be residual where no backward
+ * call follows.  What is not finite stays in its row and group (and in the
+ * sums over rows that are the weights' gradients). */
+typedef struct {
+    int32_t channels;        /* 8 .. 65536 */
+    int32_t groups;          /* divides channels; channels / groups a multiple of 8, at most 8192 */
+    int32_t dtype;           /* OFRL_DTYPE_* of x, z, out and their gradients */
+    int32_t residual_dtype;  /* of residual, residual_out and their gradients: OFRL_DTYPE_F32 or dtype */
+} ofrl_norm_shape;
+
+typedef struct {
+    const void* x;           /* [rows][channels] */
+    const void* z;           /* [rows][channels] */
+    const float* weight;     /* [channels], 16-byte aligned */
+    int64_t x_stride, z_stride;
+    int64_t rows;            /* 0 .. 2^31-1 */
+    float eps;               /* > 0, finite */
+    int32_t gate_first;
+} ofrl_gated_rows;
+
+typedef struct {
+    const void* x;           /* [rows][channels] */
+    const void* residual;    /* [rows][channels] */
+    const float* scale;      /* [channels], 16-byte aligned, or NULL (one) */
+    const float* weight;     /* [channels], 16-byte aligned */
+    int64_t x_stride, residual_stride;
+    int64_t rows;
+    float eps;
+} ofrl_residual_rows;
+
+typedef struct ofrl_norm ofrl_norm;
+
+/* The workspace (its size does not depend on the rows; backward = 0 refuses the
+ * backward calls).  The only allocating call; binds to the current device. */
+ofrl_status ofrl_norm_create(const ofrl_norm_shape* shape, int32_t backward, ofrl_norm** out);
+ofrl_status ofrl_norm_destroy(ofrl_norm* ctx);
+int64_t ofrl_norm_workspace_bytes(const ofrl_norm_shape* shape, int32_t backward);
+
+ofrl_status ofrl_gated_norm(ofrl_norm* ctx, const ofrl_gated_rows* in, void* out, int64_t out_stride, void* stream);
+
+/* dx, dz rows, dweight fp32 [channels], written (not accumulated); dx may be
+ * dout and dz may be z (same strides). */
+ofrl_status ofrl_gated_norm_backward(ofrl_norm* ctx, const ofrl_gated_rows* in, const void* dout, int64_t dout_stride,
+                                     void* dx, int64_t dx_stride, void* dz, int64_t dz_stride, float* dweight,
+                                     void* stream);
+
+ofrl_status ofrl_residual_norm(ofrl_norm* ctx, const ofrl_residual_rows* in, void* residual_out,
+                               int64_t residual_out_stride, void* out, int64_t out_stride, void* stream);
+
+/* d_residual_out: gradient of residual_out, or NULL (zero).  dx; dresidual, in
+ * the residual's type; dweight and dscale (NULL where scale is) fp32
+ * [channels]; written (not accumulated).  dx may be dout and dresidual may be
+ * d_residual_out (same strides). */
+ofrl_status ofrl_residual_norm_backward(ofrl_norm* ctx, const ofrl_residual_rows* in, const void* dout,
+                                        int64_t dout_stride, const void* d_residual_out, int64_t d_residual_out_stride,
+                                        void* dx, int64_t dx_stride, void* dresidual, int64_t dresidual_stride,
+                                        float* dweight, float* dscale, void* stream);
+
 /* ---- gradients kept in many tensors ---------------------------------------- */
 
 /* A list of n device tensors (host arrays of pointers, element counts and

@@ -19,6 +19,19 @@ Functions (same names as the C entry points, without the ofrl_ prefix):
   delta_forward(...)            gated delta rule over packed episodes
   delta_backward(...)           its gradients
   delta_step(...)               one token for each environment
+  CausalConv(...)               ofrl_conv_create / _destroy / _poll_status
+  conv_forward(...)             short causal convolution over packed episodes
+  conv_backward(...)            its gradients
+  conv_step(...)                one token for each environment
+  SelectiveScan(...)            ofrl_scan_create / _destroy / _poll_status
+  scan_forward(...)             selective scan over packed episodes
+  scan_backward(...)            its gradients
+  scan_step(...)                one token for each environment
+  BlockNorm(...)                ofrl_norm_create / _destroy
+  gated_norm(...)               norm of a block's output with its gate
+  gated_norm_backward(...)      its gradients
+  residual_norm(...)            residual + scale x, and its norm
+  residual_norm_backward(...)   its gradients
   TensorList(...)               ofrl_tensors_create / _destroy
   global_norm(...)              2-norm over many tensors
   global_norm_clip(...)         the norm, and every tensor clipped by it
@@ -696,6 +709,368 @@ def delta_step(ctx: DeltaRule, q, k, v, g, beta, state, out, scale=None, new_sta
         _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_delta_step", code)
+
+
+# ---- state space blocks ----------------------------------------------------------------------------------------------
+
+ACTIVATION = {"none": _abi.ACT_NONE, "silu": _abi.ACT_SILU}
+
+
+class _Workspace:
+    """A handle of the library with its device, closed at most once."""
+
+    def _create(self, name: str, *args):
+        self._lib = _abi.load()
+        self._name = name
+        self.handle = None
+        self.device = torch.cuda.current_device()
+        h = C.c_void_p()
+        _abi.check(f"ofrl_{name}_create", getattr(self._lib, f"ofrl_{name}_create")(*args, C.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            _abi.check(f"ofrl_{self._name}_destroy", getattr(self._lib, f"ofrl_{self._name}_destroy")(self.handle))
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _poll(self, stream=None):
+        words = (C.c_int32 * _abi.STAT_WORDS)()
+        name = f"ofrl_{self._name}_poll_status"
+        _abi.check(name, getattr(self._lib, name)(self.handle, _stream(stream), words))
+        return {"bad_index": words[_abi.STAT_BAD_INDEX]}
+
+
+class CausalConv(_Workspace):
+    """Workspace of the short causal convolution (ofrl_conv_create); the only allocation.
+
+    channels: a multiple of 8; width: 2, 3 or 4 taps; activation: "none" or "silu".  backward=False reserves no
+    memory for conv_backward, which is then refused."""
+
+    def __init__(self, channels: int, width: int = 4, activation: str = "silu", dtype: str = "bf16",
+                 max_tokens: int = 16384, max_episodes: int = 1024, backward: bool = True):
+        self.shape = _abi.ConvShape(channels, width, ACTIVATION[activation], DTYPE[dtype])
+        self.channels, self.width, self.activation = channels, width, activation
+        self.dtype = _TORCH_DTYPE[dtype]
+        self.max_tokens, self.max_episodes, self.backward = max_tokens, max_episodes, bool(backward)
+        self._create("conv", C.byref(self.shape), max_tokens, max_episodes, int(self.backward))
+
+    def poll_status(self, stream=None):
+        return self._poll(stream)
+
+    def workspace_bytes(self) -> int:
+        return int(self._lib.ofrl_conv_workspace_bytes(C.byref(self.shape), self.max_tokens, self.max_episodes,
+                                                       int(self.backward)))
+
+
+class SelectiveScan(_Workspace):
+    """Workspace of the selective scan (ofrl_scan_create); the only allocation.
+
+    state_dim: 4 to 64, a multiple of 4; groups of channels share B and C; channels / groups: a multiple of 8.
+    softplus=False takes dt + dt_bias as it is.  backward=False reserves no memory for scan_backward, which is then
+    refused."""
+
+    def __init__(self, channels: int, state_dim: int = 16, groups: int = 1, dtype: str = "bf16", softplus: bool = True,
+                 max_tokens: int = 16384, max_episodes: int = 1024, backward: bool = True):
+        self.shape = _abi.ScanShape(channels, state_dim, groups, DTYPE[dtype], int(bool(softplus)))
+        self.channels, self.state_dim, self.groups = channels, state_dim, groups
+        self.dtype = _TORCH_DTYPE[dtype]
+        self.max_tokens, self.max_episodes, self.backward = max_tokens, max_episodes, bool(backward)
+        self._create("scan", C.byref(self.shape), max_tokens, max_episodes, int(self.backward))
+
+    def poll_status(self, stream=None):
+        return self._poll(stream)
+
+    def workspace_bytes(self) -> int:
+        return int(self._lib.ofrl_scan_workspace_bytes(C.byref(self.shape), self.max_tokens, self.max_episodes,
+                                                       int(self.backward)))
+
+    def saved(self, tokens: int) -> torch.Tensor:
+        """A buffer for the states that scan_forward hands to scan_backward."""
+        n = int(self._lib.ofrl_scan_saved_bytes(C.byref(self.shape), tokens))
+        if n < 0:
+            raise ValueError(f"ofrl_scan_saved_bytes: invalid arguments (tokens={tokens})")
+        return torch.empty(max(n, 1), device=f"cuda:{self.device}", dtype=torch.uint8)
+
+
+class BlockNorm(_Workspace):
+    """Workspace of the gated norm and the residual norm (ofrl_norm_create); the only allocation.
+
+    Each of `groups` equal groups of channels is normed by itself.  residual_dtype: the residual stream's type, "fp32"
+    or dtype (the default).  backward=False reserves no memory for the gradients, which are then refused."""
+
+    def __init__(self, channels: int, groups: int = 1, dtype: str = "bf16", residual_dtype: Optional[str] = None,
+                 backward: bool = True):
+        residual_dtype = dtype if residual_dtype is None else residual_dtype
+        self.shape = _abi.NormShape(channels, groups, DTYPE[dtype], DTYPE[residual_dtype])
+        self.channels, self.groups = channels, groups
+        self.dtype, self.residual_dtype = _TORCH_DTYPE[dtype], _TORCH_DTYPE[residual_dtype]
+        self.backward = bool(backward)
+        self._create("norm", C.byref(self.shape), int(self.backward))
+
+    def workspace_bytes(self) -> int:
+        return int(self._lib.ofrl_norm_workspace_bytes(C.byref(self.shape), int(self.backward)))
+
+
+def _open_ctx(ctx, kind):
+    """The handle of a workspace of this class that is open."""
+    if not isinstance(ctx, kind):
+        raise TypeError(f"ctx must be a {kind.__name__}")
+    if ctx.handle is None:
+        raise ValueError(f"the {kind.__name__} is closed")
+    return ctx.handle
+
+
+def _tokens_of(x, channels: int, dtype, name: str) -> int:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _refuse(x, dtype, ("tokens", channels), name)
+    return x.shape[0]
+
+
+_pack_conv_tokens = struct.Struct(_abi.CONV_TOKENS_FMT).pack
+_pack_conv_grads = struct.Struct(_abi.CONV_GRADS_FMT).pack
+_pack_scan_tokens = struct.Struct(_abi.SCAN_TOKENS_FMT).pack
+_pack_scan_grads = struct.Struct(_abi.SCAN_GRADS_FMT).pack
+_pack_gated_rows = struct.Struct(_abi.GATED_ROWS_FMT).pack
+_pack_residual_rows = struct.Struct(_abi.RESIDUAL_ROWS_FMT).pack
+
+
+def _conv_tokens(ctx: CausalConv, x, weight, bias):
+    """The packed ofrl_conv_tokens and the shape of x."""
+    d = ctx.channels
+    rows = (_tokens_of(x, d, ctx.dtype, "x"), d)
+    x, xs = _rows2(x, ctx.dtype, rows, "x")
+    return _pack_conv_tokens(x, _dense(weight, F32, (d, ctx.width), "weight"), _dense(bias, F32, (d,), "bias"), xs,
+                             rows[0]), rows
+
+
+def conv_forward(ctx: CausalConv, x, weight, episode_ends, out, bias=None, init_state=None, final_state=None, stream=None):
+    """out = act(causal convolution of x) over packed episodes: x, out [tokens, channels] (may be slices with dense
+    rows), weight float32 [channels, width] (the last tap takes the token itself), bias float32 [channels];
+    episode_ends int32 [episodes].  init_state, final_state: [episodes, channels, width - 1] of x's type, the inputs
+    before an episode and its last ones."""
+    handle = _open_ctx(ctx, CausalConv)
+    t, rows = _conv_tokens(ctx, x, weight, bias)
+    ne = episode_ends.numel()
+    state = (ne, ctx.channels, ctx.width - 1)
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_conv_forward(
+        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, ctx.dtype, state, "init_state"),
+        o, os, _dense(final_state, ctx.dtype, state, "final_state"), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_conv_forward", code)
+
+
+def conv_backward(ctx: CausalConv, x, weight, episode_ends, dout, dx, dweight, bias=None, dbias=None, init_state=None,
+                  d_final=None, d_init=None, stream=None):
+    """Gradients of the conv_forward call with the same inputs: of out in dout, of final_state in d_final (of x's type;
+    None: zero); written to dx, dweight, dbias and d_init (float32; the last two may be None)."""
+    handle = _open_ctx(ctx, CausalConv)
+    t, rows = _conv_tokens(ctx, x, weight, bias)
+    ne, d = episode_ends.numel(), ctx.channels
+    state = (ne, d, ctx.width - 1)
+    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
+    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    if dweight is None:
+        raise TypeError("dweight must be a CUDA tensor")
+    code = ctx._lib.ofrl_conv_backward(
+        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, ctx.dtype, state, "init_state"),
+        g, gs, _dense(d_final, ctx.dtype, state, "d_final"),
+        _pack_conv_grads(dx, _dense(dweight, F32, (d, ctx.width), "dweight"), _dense(dbias, F32, (d,), "dbias"), xs),
+        _dense(d_init, F32, state, "d_init"), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_conv_backward", code)
+
+
+def _state_pair(state, new_state, dtype, tail):
+    """Addresses of a step's states and how many slots they have."""
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        _refuse(state, dtype, ("slots", *tail), "state")
+    shape = (state.shape[0], *tail)
+    at = _dense(state, dtype, shape, "state")
+    return at, at if new_state is None else _dense(new_state, dtype, shape, "new_state"), shape[0]
+
+
+def conv_step(ctx: CausalConv, x, weight, state, out, bias=None, new_state=None, slots=None, stream=None):
+    """One token for each environment: tensors as conv_forward's with tokens = environments; state [slots, channels,
+    width - 1], updated in place or written to new_state; slots: int32 [tokens], the state of each token (None: token
+    i has state i)."""
+    handle = _open_ctx(ctx, CausalConv)
+    t, rows = _conv_tokens(ctx, x, weight, bias)
+    at, to, ns = _state_pair(state, new_state, ctx.dtype, (ctx.channels, ctx.width - 1))
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_conv_step(handle, t, _dense(slots, I32, (rows[0],), "slots"), ns, at, to, o, os,
+                                   _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_conv_step", code)
+
+
+def _scan_tokens(ctx: SelectiveScan, x, dt, A, B, C_, D, z, dt_bias):
+    """The packed ofrl_scan_tokens and the shapes of x and of B."""
+    d, n, ty = ctx.channels, ctx.state_dim, ctx.dtype
+    rows = (_tokens_of(x, d, ty, "x"), d)
+    bc = (rows[0], ctx.groups, n)
+    x, xs = _rows2(x, ty, rows, "x")
+    dt, ds = _rows2(dt, ty, rows, "dt")
+    B, bs = _rows3(B, ty, bc, "B")
+    C_, cs = _rows3(C_, ty, bc, "C")
+    z, zs = (0, 0) if z is None else _rows2(z, ty, rows, "z")
+    if A is None:
+        raise TypeError("A must be a CUDA tensor")
+    return _pack_scan_tokens(x, dt, B, C_, z, _dense(A, F32, (d, n), "A"), _dense(D, F32, (d,), "D"),
+                             _dense(dt_bias, F32, (d,), "dt_bias"), xs, ds, bs, cs, zs, rows[0]), rows, bc
+
+
+def _scan_saved(ctx: SelectiveScan, saved, tokens: int):
+    if saved is None:
+        return 0
+    need = ctx._lib.ofrl_scan_saved_bytes(C.byref(ctx.shape), tokens)
+    if saved.numel() < need:
+        raise ValueError(f"saved has {saved.numel()} bytes, {need} are needed: use ctx.saved(tokens)")
+    return _dense(saved, torch.uint8, saved.shape, "saved")
+
+
+def scan_forward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, out, D=None, z=None, dt_bias=None, init_state=None,
+                 final_state=None, saved=None, stream=None):
+    """The selective scan over packed episodes: x, dt, z, out [tokens, channels], B, C [tokens, groups, state_dim] (all
+    may be slices with dense rows); A float32 [channels, state_dim] (negative), D and dt_bias float32 [channels];
+    episode_ends int32 [episodes].  init_state, final_state: float32 [episodes, channels, state_dim].  saved:
+    ctx.saved(tokens), filled for scan_backward."""
+    handle = _open_ctx(ctx, SelectiveScan)
+    t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
+    ne = episode_ends.numel()
+    state = (ne, ctx.channels, ctx.state_dim)
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_scan_forward(
+        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, F32, state, "init_state"), o, os,
+        _dense(final_state, F32, state, "final_state"), _scan_saved(ctx, saved, rows[0]), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_scan_forward", code)
+
+
+def scan_backward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, saved, dout, dx, ddt, dA, dB, dC, D=None, z=None,
+                  dt_bias=None, dD=None, dz=None, ddt_bias=None, init_state=None, d_final=None, d_init=None, stream=None):
+    """Gradients of the scan_forward call that filled `saved`, with the same inputs: of out in dout, of final_state in
+    d_final (None: zero); written to dx, ddt, dB, dC, dz (given where z is; slices with dense rows), and to dA, dD,
+    ddt_bias and d_init (float32; the last three may be None)."""
+    handle = _open_ctx(ctx, SelectiveScan)
+    t, rows, bc = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
+    if saved is None:
+        raise TypeError("saved must be the buffer that scan_forward filled")
+    if dA is None:
+        raise TypeError("dA must be a CUDA tensor")
+    ne, d, ty = episode_ends.numel(), ctx.channels, ctx.dtype
+    state = (ne, d, ctx.state_dim)
+    g, gs = _rows2(dout, ty, rows, "dout")
+    dx, xs = _rows2(dx, ty, rows, "dx")
+    ddt, ds = _rows2(ddt, ty, rows, "ddt")
+    dB, bs = _rows3(dB, ty, bc, "dB")
+    dC, cs = _rows3(dC, ty, bc, "dC")
+    dz, zs = (0, 0) if dz is None else _rows2(dz, ty, rows, "dz")
+    code = ctx._lib.ofrl_scan_backward(
+        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, F32, state, "init_state"),
+        _scan_saved(ctx, saved, rows[0]), g, gs, _dense(d_final, F32, state, "d_final"),
+        _pack_scan_grads(dx, ddt, dB, dC, dz, _dense(dA, F32, (d, ctx.state_dim), "dA"), _dense(dD, F32, (d,), "dD"),
+                         _dense(ddt_bias, F32, (d,), "ddt_bias"), xs, ds, bs, cs, zs),
+        _dense(d_init, F32, state, "d_init"), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_scan_backward", code)
+
+
+def scan_step(ctx: SelectiveScan, x, dt, A, B, C, state, out, D=None, z=None, dt_bias=None, new_state=None, slots=None,
+              stream=None):
+    """One token for each environment: tensors as scan_forward's with tokens = environments; state float32 [slots,
+    channels, state_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each token
+    (None: token i has state i)."""
+    handle = _open_ctx(ctx, SelectiveScan)
+    t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
+    at, to, ns = _state_pair(state, new_state, F32, (ctx.channels, ctx.state_dim))
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_scan_step(handle, t, _dense(slots, I32, (rows[0],), "slots"), ns, at, to, o, os,
+                                   _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_scan_step", code)
+
+
+def _norm_weight(ctx: BlockNorm, weight, name="weight"):
+    if weight is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _dense(weight, F32, (ctx.channels,), name)
+
+
+def _gated_rows(ctx: BlockNorm, x, z, weight, eps, gate_first):
+    rows = (_tokens_of(x, ctx.channels, ctx.dtype, "x"), ctx.channels)
+    x, xs = _rows2(x, ctx.dtype, rows, "x")
+    z, zs = _rows2(z, ctx.dtype, rows, "z")
+    return _pack_gated_rows(x, z, _norm_weight(ctx, weight), xs, zs, rows[0], eps, bool(gate_first)), rows
+
+
+def gated_norm(ctx: BlockNorm, x, z, weight, out, eps: float = 1e-5, gate_first: bool = False, stream=None):
+    """out = weight x / rms(x) silu(z), or the norm of x silu(z) (gate_first), over each group of channels: x, z, out
+    [rows, channels] (may be slices with dense rows; out may be x), weight float32 [channels]."""
+    handle = _open_ctx(ctx, BlockNorm)
+    t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_gated_norm(handle, t, o, os, _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_gated_norm", code)
+
+
+def gated_norm_backward(ctx: BlockNorm, x, z, weight, dout, dx, dz, dweight, eps: float = 1e-5, gate_first: bool = False,
+                        stream=None):
+    """Gradients of the gated_norm call with the same inputs, written to dx, dz (slices with dense rows) and dweight."""
+    handle = _open_ctx(ctx, BlockNorm)
+    t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
+    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
+    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    dz, zs = _rows2(dz, ctx.dtype, rows, "dz")
+    code = ctx._lib.ofrl_gated_norm_backward(handle, t, g, gs, dx, xs, dz, zs, _norm_weight(ctx, dweight, "dweight"),
+                                             _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_gated_norm_backward", code)
+
+
+def _residual_rows(ctx: BlockNorm, x, residual, scale, weight, eps):
+    rows = (_tokens_of(x, ctx.channels, ctx.dtype, "x"), ctx.channels)
+    x, xs = _rows2(x, ctx.dtype, rows, "x")
+    residual, rs = _rows2(residual, ctx.residual_dtype, rows, "residual")
+    return _pack_residual_rows(x, residual, _dense(scale, F32, (ctx.channels,), "scale"), _norm_weight(ctx, weight), xs, rs,
+                               rows[0], eps), rows
+
+
+def residual_norm(ctx: BlockNorm, x, residual, weight, residual_out, out, scale=None, eps: float = 1e-5, stream=None):
+    """residual_out = residual + scale x and out = weight residual_out / rms(residual_out) (of the sum before it is
+    rounded to its type): x, out [rows, channels], residual, residual_out of the residual's type (all may be slices
+    with dense rows; residual_out may be residual, out may be x), scale (None: one) and weight float32 [channels]."""
+    handle = _open_ctx(ctx, BlockNorm)
+    t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
+    r, rs = _rows2(residual_out, ctx.residual_dtype, rows, "residual_out")
+    o, os = _rows2(out, ctx.dtype, rows, "out")
+    code = ctx._lib.ofrl_residual_norm(handle, t, r, rs, o, os, _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_residual_norm", code)
+
+
+def residual_norm_backward(ctx: BlockNorm, x, residual, weight, dout, dx, dresidual, dweight, scale=None, dscale=None,
+                           d_residual_out=None, eps: float = 1e-5, stream=None):
+    """Gradients of the residual_norm call with the same inputs: of out in dout, of residual_out in d_residual_out
+    (None: zero); written to dx, dresidual (slices with dense rows), dweight, and dscale (given where scale is)."""
+    handle = _open_ctx(ctx, BlockNorm)
+    t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
+    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
+    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    dr, drs = _rows2(dresidual, ctx.residual_dtype, rows, "dresidual")
+    do, dos = (0, 0) if d_residual_out is None else _rows2(d_residual_out, ctx.residual_dtype, rows, "d_residual_out")
+    code = ctx._lib.ofrl_residual_norm_backward(
+        handle, t, g, gs, do, dos, dx, xs, dr, drs, _norm_weight(ctx, dweight, "dweight"),
+        _dense(dscale, F32, (ctx.channels,), "dscale"), _raw_stream(stream, ctx.device))
+    if code != _abi.OK:
+        _abi.check("ofrl_residual_norm_backward", code)
 
 
 # ---- gradients kept in many tensors --------------------------------------------------------------------------------

@@ -71,6 +71,59 @@ class DeltaGrads(C.Structure):
 DELTA_TOKENS_FMT = "5Q6qf4x"
 DELTA_GRADS_FMT = "5Q5q"
 
+ACT_NONE, ACT_SILU = 0, 1
+
+
+class ConvShape(C.Structure):
+    _fields_ = [("channels", C.c_int32), ("width", C.c_int32), ("activation", C.c_int32), ("dtype", C.c_int32)]
+
+
+class ConvTokens(C.Structure):
+    _fields_ = [("x", vp), ("weight", vp), ("bias", vp), ("x_stride", C.c_int64), ("tokens", C.c_int64)]
+
+
+class ConvGrads(C.Structure):
+    _fields_ = [("dx", vp), ("dweight", vp), ("dbias", vp), ("x_stride", C.c_int64)]
+
+
+class ScanShape(C.Structure):
+    _fields_ = [("channels", C.c_int32), ("state_dim", C.c_int32), ("groups", C.c_int32), ("dtype", C.c_int32),
+                ("softplus", C.c_int32)]
+
+
+class ScanTokens(C.Structure):
+    _fields_ = [("x", vp), ("dt", vp), ("b", vp), ("c", vp), ("z", vp), ("a", vp), ("d", vp), ("dt_bias", vp),
+                ("x_stride", C.c_int64), ("dt_stride", C.c_int64), ("b_stride", C.c_int64), ("c_stride", C.c_int64),
+                ("z_stride", C.c_int64), ("tokens", C.c_int64)]
+
+
+class ScanGrads(C.Structure):
+    _fields_ = [("dx", vp), ("ddt", vp), ("db", vp), ("dc", vp), ("dz", vp), ("da", vp), ("dd", vp), ("ddt_bias", vp),
+                ("x_stride", C.c_int64), ("dt_stride", C.c_int64), ("b_stride", C.c_int64), ("c_stride", C.c_int64),
+                ("z_stride", C.c_int64)]
+
+
+class NormShape(C.Structure):
+    _fields_ = [("channels", C.c_int32), ("groups", C.c_int32), ("dtype", C.c_int32), ("residual_dtype", C.c_int32)]
+
+
+class GatedRows(C.Structure):
+    _fields_ = [("x", vp), ("z", vp), ("weight", vp), ("x_stride", C.c_int64), ("z_stride", C.c_int64),
+                ("rows", C.c_int64), ("eps", C.c_float), ("gate_first", C.c_int32)]
+
+
+class ResidualRows(C.Structure):
+    _fields_ = [("x", vp), ("residual", vp), ("scale", vp), ("weight", vp), ("x_stride", C.c_int64),
+                ("residual_stride", C.c_int64), ("rows", C.c_int64), ("eps", C.c_float)]
+
+
+CONV_TOKENS_FMT = "3Q2q"
+CONV_GRADS_FMT = "3Qq"
+SCAN_TOKENS_FMT = "8Q6q"
+SCAN_GRADS_FMT = "8Q5q"
+GATED_ROWS_FMT = "3Q3qfi"
+RESIDUAL_ROWS_FMT = "4Q3qf4x"
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "ofrl_create": (C.c_int32, [C.POINTER(VShape), C.c_int32, C.c_int32, C.POINTER(vp)]),
@@ -126,6 +179,30 @@ SIGNATURES = {
     "ofrl_tensors_destroy": (C.c_int32, [vp]),
     "ofrl_global_norm": (C.c_int32, [vp, vp, vp]),
     "ofrl_global_norm_clip": (C.c_int32, [vp, C.c_float, vp, vp, vp]),
+    # token, row and gradient structs as packed bytes, as above
+    "ofrl_conv_create": (C.c_int32, [C.POINTER(ConvShape), C.c_int64, C.c_int32, C.c_int32, C.POINTER(vp)]),
+    "ofrl_conv_destroy": (C.c_int32, [vp]),
+    "ofrl_conv_poll_status": (C.c_int32, [vp, vp, C.POINTER(C.c_int32)]),
+    "ofrl_conv_workspace_bytes": (C.c_int64, [C.POINTER(ConvShape), C.c_int64, C.c_int32, C.c_int32]),
+    "ofrl_conv_forward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, C.c_int64, vp, vp]),
+    "ofrl_conv_backward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, C.c_int64, vp, C.c_char_p, vp, vp]),
+    "ofrl_conv_step": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, C.c_int64, vp]),
+    "ofrl_scan_create": (C.c_int32, [C.POINTER(ScanShape), C.c_int64, C.c_int32, C.c_int32, C.POINTER(vp)]),
+    "ofrl_scan_destroy": (C.c_int32, [vp]),
+    "ofrl_scan_poll_status": (C.c_int32, [vp, vp, C.POINTER(C.c_int32)]),
+    "ofrl_scan_workspace_bytes": (C.c_int64, [C.POINTER(ScanShape), C.c_int64, C.c_int32, C.c_int32]),
+    "ofrl_scan_saved_bytes": (C.c_int64, [C.POINTER(ScanShape), C.c_int64]),
+    "ofrl_scan_forward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, C.c_int64, vp, vp, vp]),
+    "ofrl_scan_backward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, C.c_int64, vp, C.c_char_p, vp, vp]),
+    "ofrl_scan_step": (C.c_int32, [vp, C.c_char_p, vp, C.c_int32, vp, vp, vp, C.c_int64, vp]),
+    "ofrl_norm_create": (C.c_int32, [C.POINTER(NormShape), C.c_int32, C.POINTER(vp)]),
+    "ofrl_norm_destroy": (C.c_int32, [vp]),
+    "ofrl_norm_workspace_bytes": (C.c_int64, [C.POINTER(NormShape), C.c_int32]),
+    "ofrl_gated_norm": (C.c_int32, [vp, C.c_char_p, vp, C.c_int64, vp]),
+    "ofrl_gated_norm_backward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, vp, vp]),
+    "ofrl_residual_norm": (C.c_int32, [vp, C.c_char_p, vp, C.c_int64, vp, C.c_int64, vp]),
+    "ofrl_residual_norm_backward": (C.c_int32, [vp, C.c_char_p, vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, vp,
+                                                C.c_int64, vp, vp, vp]),
     "ofrl_profile_begin": (C.c_int32, [vp, C.c_int32]),
     "ofrl_profile_end": (C.c_int32, [vp, C.POINTER(C.c_float), C.POINTER(C.c_int32)]),
 }

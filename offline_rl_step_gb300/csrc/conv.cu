@@ -1,0 +1,724 @@
+// Short causal convolution over packed episodes: forward, gradients, one token.
+//
+//   pre_t = bias + sum_{j < W} w_j x_{t-W+1+j},  out = act(pre)
+//   dpre_t = dout_t act'(pre_t),  dx_t = sum_j w_{W-1-j} dpre_{t+j},
+//   dw_j = sum_t dpre_t x_{t-W+1+j},  dbias = sum_t dpre_t
+//
+// A thread has a few neighbouring channels and goes down a run of tokens with
+// the last W - 1 inputs in registers, so each input is read once but for the
+// W - 1 tokens before a run (and, for gradients, after it).  Which tokens begin
+// an episode is a bit mask in shared memory, made from the ends once a CTA.
+// Bound by HBM.
+
+#include <cstring>
+#include <new>
+
+#include "episodes.cuh"
+#include "lanes.cuh"
+#include "rows.cuh"
+
+struct ofrl_conv {
+    int device;
+    int num_sms;
+    ofrl_conv_shape shape;
+    int64_t max_tokens;
+    int32_t max_episodes;
+    int32_t backward;
+    void* base;          // the single cudaMalloc of the context
+    int64_t bytes;
+    int32_t* status;     // [OFRL_STAT_WORDS]
+    float* parts;        // gradients: [CTAs over tokens][channels][width + 1]
+};
+
+namespace ofrl {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 4;      // channels of a thread
+constexpr int kMinRun = 8, kMaxRun = 64;
+constexpr int kMaskWords = kThreads * kMaxRun / 32 + 2;
+
+struct ConvLaunch {
+    ofrl_conv_shape shape;
+    ofrl_conv_tokens in;
+    const int32_t* ends;
+    int32_t episodes;
+    const void* init;
+    void* out;
+    int64_t out_stride;
+    void* final_state;
+    const void* dout;
+    int64_t dout_stride;
+    const void* d_final;
+    ofrl_conv_grads grads;
+    float* d_init;
+    float* parts;
+    int32_t* status;
+    int lanes;           // threads along a row, a power of two up to 32
+    int run;             // tokens a thread goes down
+};
+
+struct ConvStepLaunch {
+    ofrl_conv_shape shape;
+    ofrl_conv_tokens in;
+    const int32_t* slot_idx;
+    int32_t slots;
+    const void* state_in;
+    void* state_out;
+    void* out;
+    int64_t out_stride;
+    int32_t* status;
+    int per_thread;      // tokens a thread takes
+};
+
+// How a call is cut: CTAs of (kThreads / lanes) runs by `lanes` vectors.
+struct ConvCut {
+    int lanes, run, cols;      // cols: CTAs along a row
+    int64_t rows;              // CTAs over the tokens, at least 1
+};
+ConvCut conv_cut(int channels, int64_t tokens, int num_sms) {
+    ConvCut c;
+    const int vecs = channels / kVec;
+    c.lanes = 1;
+    while (c.lanes < 32 && c.lanes < vecs) c.lanes *= 2;
+    c.cols = (vecs + c.lanes - 1) / c.lanes;
+    const int64_t runs = kThreads / c.lanes, target = (int64_t)num_sms * 8 / c.cols + 1;
+    c.run = kMinRun;
+    while (c.run < kMaxRun && (tokens + runs * c.run - 1) / (runs * c.run) > target) c.run *= 2;
+    c.rows = (tokens + runs * c.run - 1) / (runs * c.run);
+    if (c.rows < 1) c.rows = 1;
+    return c;
+}
+// CTAs over the tokens of any call of at most max_tokens: at the longest run, or
+// no more than the target.
+int64_t conv_rows_most(int channels, int64_t max_tokens, int num_sms) {
+    const ConvCut c = conv_cut(channels, max_tokens, num_sms);
+    const int64_t runs = kThreads / c.lanes, target = (int64_t)num_sms * 8 / c.cols + 1;
+    const int64_t longest = (max_tokens + runs * kMaxRun - 1) / (runs * kMaxRun),
+                  shortest = (max_tokens + runs * kMinRun - 1) / (runs * kMinRun);
+    const int64_t few = target < shortest ? target : shortest;
+    return longest > few ? longest : few > 1 ? few : 1;
+}
+
+__device__ __forceinline__ float act_of(float pre, int activation) {
+    return activation == OFRL_ACT_SILU ? pre * sigmoid(pre) : pre;
+}
+__device__ __forceinline__ float act_slope(float pre, int activation) {
+    if (activation != OFRL_ACT_SILU) return 1.0f;
+    const float s = sigmoid(pre);
+    return s * (1.0f + pre * (1.0f - s));
+}
+
+// The first episode that ends after token t; one thread.
+__device__ __forceinline__ int episode_at(const int32_t* ends, int episodes, int tokens, int t) {
+    int lo = 0, hi = episodes;
+    while (lo < hi) {
+        const int mid = (int)(((int64_t)lo + hi) / 2);
+        if (episode_end(ends, mid, tokens) > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return min(lo, episodes - 1);
+}
+
+// What a CTA knows of its tokens [s0, s1) and the W - 1 around them.
+struct Marks {
+    uint32_t mask[kMaskWords];
+    int m0;              // the token of bit 0
+    Range range;         // of [m0, ..)
+    __device__ bool starts(int t) const { return mask[(t - m0) >> 5] >> ((t - m0) & 31) & 1; }
+    // token t, below range.end, is its episode's last
+    __device__ bool last(int t) const { return t + 1 < range.end ? starts(t + 1) : range.closed != 0; }
+};
+
+template <int W>
+__device__ __forceinline__ void make_marks(Marks& m, const ConvLaunch& a, int s0, int64_t s1, bool count) {
+    const int tokens = (int)a.in.tokens;
+    for (int i = threadIdx.x; i < kMaskWords; i += kThreads) m.mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int m0 = max(0, s0 - (W - 1)), m1 = (int)min(s1 + W, (int64_t)tokens);
+        const Range r = mark_starts(a.ends, a.episodes, tokens, m0, max(m0, m1), m.mask);
+        if (threadIdx.x == 0) {
+            m.m0 = m0;
+            m.range = r;
+        }
+        if (count) {
+            const int bad = count_bad_ends(a.ends, a.episodes, tokens, blockIdx.x, gridDim.x);
+            if (threadIdx.x == 0 && bad) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, bad);
+        }
+    }
+    __syncthreads();
+}
+
+// Inputs that a run carries along: win[i] stands W - 1 - i tokens back.
+template <typename T, int V, int W>
+struct Window {
+    float win[W - 1][V];
+    __device__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) win[i][k] = 0.0f;
+    }
+    __device__ void push(const float (&x)[V]) {
+#pragma unroll
+        for (int i = 0; i + 1 < W - 1; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) win[i][k] = win[i + 1][k];
+#pragma unroll
+        for (int k = 0; k < V; ++k) win[W - 2][k] = x[k];
+    }
+    __device__ void enter(const ConvLaunch& a, int t, int ch) {
+        clear();
+        if (a.init == nullptr) return;
+        const int e = episode_at(a.ends, a.episodes, (int)a.in.tokens, t);
+        const T* p = static_cast<const T*>(a.init) + ((int64_t)e * a.shape.channels + ch) * (W - 1);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) win[i][k] = to_float(p[k * (W - 1) + i]);
+    }
+};
+
+template <int V, int W>
+struct Taps {
+    float w[W][V], bias[V];
+    __device__ void load(const ConvLaunch& a, int ch) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][k] = a.in.weight[(int64_t)(ch + k) * W + j];
+            bias[k] = a.in.bias != nullptr ? a.in.bias[ch + k] : 0.0f;
+        }
+    }
+    template <typename T>
+    __device__ float pre(const Window<T, V, W>& win, const float (&x)[V], int k) const {
+        float s = bias[k];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][k], win.win[j][k], s);
+        return fmaf(w[W - 1][k], x[k], s);
+    }
+};
+
+constexpr int kAtOnce = 8;      // tokens whose loads are in flight together
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) conv_forward_kernel(const __grid_constant__ ConvLaunch a) {
+    constexpr int V = kVec;
+    __shared__ Marks m;
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, d = a.shape.channels;
+    const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
+    const int64_t from = (int64_t)blockIdx.x * runs * a.run;
+    const int s0 = (int)from;
+    make_marks<W>(m, a, s0, from + (int64_t)runs * a.run, blockIdx.y == 0);
+    const int ch = ((int)blockIdx.y * a.lanes + lane) * V;
+    const int64_t begin64 = from + (int64_t)y * a.run;
+    const int end = (int)min(begin64 + a.run, (int64_t)m.range.end), begin = (int)min(begin64, (int64_t)end);
+    if (ch < d && begin < end) {
+        Taps<V, W> taps;
+        taps.load(a, ch);
+        Window<T, V, W> win;
+        win.clear();
+        const T* in = static_cast<const T*>(a.in.x) + ch;
+        T* out = static_cast<T*>(a.out) + ch;
+        for (int t0 = begin - (W - 1); t0 < end; t0 += kAtOnce) {
+            float x[kAtOnce][V];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (t0 + i >= 0 && t0 + i < end) load_vec<T, V>(x[i], in + (int64_t)(t0 + i) * a.in.x_stride);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int t = t0 + i;
+                if (t < 0 || t >= end) continue;
+                if (m.starts(t)) win.enter(a, t, ch);
+                if (t >= begin) {
+                    float o[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) o[k] = act_of(taps.pre(win, x[i], k), a.shape.activation);
+                    store_vec<T, V>(out + (int64_t)t * a.out_stride, o);
+                }
+                win.push(x[i]);
+                if (a.final_state != nullptr && t >= begin && m.last(t)) {
+                    const int e = episode_at(a.ends, a.episodes, tokens, t);
+                    T* p = static_cast<T*>(a.final_state) + ((int64_t)e * d + ch) * (W - 1);
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) p[k * (W - 1) + j] = from_float<T>(win.win[j][k]);
+                }
+            }
+        }
+    }
+    // Episodes without tokens end as they began.
+    if (a.final_state != nullptr) {
+        const int ln = threadIdx.x & 31;
+        const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+        const int ch0 = (int)blockIdx.y * a.lanes * V, width = min(a.lanes * V, d - ch0) * (W - 1);
+        for (int64_t base = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 32; base < a.episodes;
+             base += warps * 32) {
+            const int64_t at = base + ln;
+            unsigned empty = __ballot_sync(0xffffffffu, at < a.episodes && episode_end(a.ends, (int)at, tokens) <=
+                                                                             episode_start(a.ends, (int)at, tokens));
+            for (; empty; empty &= empty - 1) {
+                const int64_t o = ((base + __ffs(empty) - 1) * d + ch0) * (W - 1);
+                for (int i = ln; i < width; i += 32)
+                    static_cast<T*>(a.final_state)[o + i] =
+                        a.init != nullptr ? static_cast<const T*>(a.init)[o + i] : from_float<T>(0.0f);
+            }
+        }
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) conv_grad_kernel(const __grid_constant__ ConvLaunch a) {
+    constexpr int V = kVec, kLoads = 4;
+    __shared__ Marks m;
+    __shared__ float red[kThreads * V * (W + 1)];
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, d = a.shape.channels;
+    const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
+    const int64_t from = (int64_t)blockIdx.x * runs * a.run;
+    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, false);
+    const int ch = ((int)blockIdx.y * a.lanes + lane) * V;
+    const int64_t begin64 = from + (int64_t)y * a.run;
+    const int live = m.range.end;
+    const int end = (int)min(begin64 + a.run, (int64_t)live), begin = (int)min(begin64, (int64_t)end);
+    float dw[W + 1][V];      // the taps, then the bias
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) dw[j][k] = 0.0f;
+    if (ch < d && begin < end) {
+        Taps<V, W> taps;
+        taps.load(a, ch);
+        Window<T, V, W> win;
+        win.clear();
+        float pend[W - 1][V];      // dx of the W - 1 tokens before, so far
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int k = 0; k < V; ++k) pend[j][k] = 0.0f;
+        int age = W;               // tokens since the episode began
+        const T* in = static_cast<const T*>(a.in.x) + ch;
+        const T* go = static_cast<const T*>(a.dout) + ch;
+        const int stop = (int)min((int64_t)end + W - 1, (int64_t)live);      // dpre of the tokens after the run
+        // one more round for each pending token
+        for (int t0 = begin - (W - 1); t0 < end + W - 1; t0 += kLoads) {
+            float x[kLoads][V], g[kLoads][V];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int t = t0 + i;
+                if (t >= 0 && t < stop) load_vec<T, V>(x[i], in + (int64_t)t * a.in.x_stride);
+                if (t >= begin && t < stop) load_vec<T, V>(g[i], go + (int64_t)t * a.dout_stride);
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int t = t0 + i;
+                if (t < 0) continue;
+                float now[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) now[k] = 0.0f;
+                if (t < stop) {
+                    if (m.starts(t)) {
+                        win.enter(a, t, ch);
+                        age = 0;
+                    }
+                    if (t >= begin) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) {
+                            const float dp = g[i][k] * act_slope(taps.pre(win, x[i], k), a.shape.activation);
+                            now[k] = taps.w[W - 1][k] * dp;
+#pragma unroll
+                            for (int j = 1; j < W; ++j)
+                                if (j <= age) pend[W - 1 - j][k] = fmaf(taps.w[W - 1 - j][k], dp, pend[W - 1 - j][k]);
+                            if (t < end) {
+#pragma unroll
+                                for (int j = 0; j < W - 1; ++j) dw[j][k] = fmaf(dp, win.win[j][k], dw[j][k]);
+                                dw[W - 1][k] = fmaf(dp, x[i][k], dw[W - 1][k]);
+                                dw[W][k] += dp;
+                            }
+                        }
+                        if (a.d_final != nullptr && t < end) {
+                            int left = 0;      // tokens of the episode from t on, up to W - 1; 0: more
+                            for (int j = 1; j < W && left == 0; ++j)
+                                if (t + j <= live && m.last(t + j - 1)) left = j;
+                            if (left > 0) {
+                                const int e = episode_at(a.ends, a.episodes, tokens, t);
+                                const T* p = static_cast<const T*>(a.d_final) + ((int64_t)e * d + ch) * (W - 1);
+#pragma unroll
+                                for (int k = 0; k < V; ++k) now[k] += to_float(p[k * (W - 1) + W - 1 - left]);
+                            }
+                        }
+                    }
+                    win.push(x[i]);
+                    ++age;
+                }
+                const int done = t - (W - 1);
+                if (done >= begin && done < end)
+                    store_vec<T, V>(static_cast<T*>(a.grads.dx) + (int64_t)done * a.grads.x_stride + ch, pend[0]);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) pend[j][k] = pend[j + 1][k];
+#pragma unroll
+                for (int k = 0; k < V; ++k) pend[W - 2][k] = now[k];
+            }
+        }
+    }
+    // over the CTA's runs
+    const int row = a.lanes * V * (W + 1);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int j = 0; j <= W; ++j) red[y * row + (lane * V + k) * (W + 1) + j] = dw[j][k];
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.y * row, all = (int64_t)d * (W + 1);
+    for (int i = threadIdx.x; i < row && first + i < all; i += kThreads) {
+        float v = 0.0f;
+        for (int k = 0; k < runs; ++k) v += red[k * row + i];
+        a.parts[blockIdx.x * all + first + i] = v;
+    }
+}
+
+// dweight and dbias over the CTAs: 32 outputs a CTA, eight threads to an output.
+constexpr int kSlices = kThreads / 32;
+
+__global__ void __launch_bounds__(kThreads) conv_join_kernel(const __grid_constant__ ConvLaunch a, int64_t rows) {
+    __shared__ float red[kSlices][33];
+    pdl_wait();
+    pdl_trigger();
+    const int w = a.shape.width;
+    const int64_t all = (int64_t)a.shape.channels * (w + 1), i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+    const int slice = threadIdx.x / 32;
+    float v = 0.0f;
+    if (i < all) {
+#pragma unroll 8
+        for (int64_t j = slice; j < rows; j += kSlices) v += a.parts[j * all + i];
+    }
+    red[slice][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (slice > 0 || i >= all) return;
+    v = 0.0f;
+    for (int k = 0; k < kSlices; ++k) v += red[k][threadIdx.x];
+    const int64_t ch = i / (w + 1);
+    const int j = (int)(i - ch * (w + 1));
+    if (j < w)
+        a.grads.dweight[ch * w + j] = v;
+    else if (a.grads.dbias != nullptr)
+        a.grads.dbias[ch] = v;
+}
+
+// Gradient of the initial states: one thread for each episode and channel, which
+// goes over the first W - 1 tokens again.  Slot k stands W - 1 - k tokens before
+// the episode: token i takes it with tap k - i.
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) conv_init_grad_kernel(const __grid_constant__ ConvLaunch a) {
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, d = a.shape.channels;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, e = i / d;
+    const int ch = (int)(i - e * d);
+    if (e >= a.episodes) return;
+    const int lo = episode_start(a.ends, (int)e, tokens), len = max(0, episode_end(a.ends, (int)e, tokens) - lo);
+    Taps<1, W> taps;
+    taps.load(a, ch);
+    const int64_t at = (e * d + ch) * (W - 1);
+    Window<T, 1, W> win;
+    float g[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        win.win[k][0] = a.init != nullptr ? to_float(static_cast<const T*>(a.init)[at + k]) : 0.0f;
+        // a short episode's final state still holds initial inputs
+        g[k] = a.d_final != nullptr && k >= len ? to_float(static_cast<const T*>(a.d_final)[at + k - len]) : 0.0f;
+    }
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+        if (t >= len) break;
+        float x[1] = {to_float(static_cast<const T*>(a.in.x)[(int64_t)(lo + t) * a.in.x_stride + ch])};
+        const float dp = to_float(static_cast<const T*>(a.dout)[(int64_t)(lo + t) * a.dout_stride + ch]) *
+                         act_slope(taps.pre(win, x, 0), a.shape.activation);
+#pragma unroll
+        for (int k = t; k < W - 1; ++k) g[k] = fmaf(taps.w[k - t][0], dp, g[k]);
+        win.push(x);
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) a.d_init[at + k] = g[k];
+}
+
+// One token of per_thread environments, eight channels a thread.
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_constant__ ConvStepLaunch a) {
+    constexpr int V = 16 / (int)sizeof(T), kVecs = 8 / V, S = W - 1;
+    pdl_wait();
+    pdl_trigger();
+    const int d = a.shape.channels, cols = d / 8;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, row = i / cols;
+    const int ch = (int)(i - row * cols) * 8;
+    const int64_t tok0 = row * a.per_thread, tok1 = min(tok0 + a.per_thread, a.in.tokens);
+    if (tok0 >= tok1) return;
+    float w[8][W], bias[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[k][j] = a.in.weight[(int64_t)(ch + k) * W + j];
+        bias[k] = a.in.bias != nullptr ? a.in.bias[ch + k] : 0.0f;
+    }
+    for (int64_t tok = tok0; tok < tok1; ++tok) {
+        const int32_t slot = a.slot_idx ? a.slot_idx[tok] : (int32_t)tok;
+        T* out = static_cast<T*>(a.out) + tok * a.out_stride + ch;
+        const bool ok = slot >= 0 && slot < a.slots;
+        if (!ok && ch == 0) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, 1);
+        Vec<T, V> xv[kVecs], state[kVecs * S], o[kVecs];
+        const T* x = static_cast<const T*>(a.in.x) + tok * a.in.x_stride + ch;
+        const int64_t at = ((int64_t)(ok ? slot : 0) * d + ch) * S;
+        if (ok) {
+#pragma unroll
+            for (int k = 0; k < kVecs * S; ++k)
+                state[k] = *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.state_in) + at + k * V);
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) xv[k] = *reinterpret_cast<const Vec<T, V>*>(x + k * V);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float s = bias[k];
+#pragma unroll
+                for (int j = 0; j < S; ++j) s = fmaf(w[k][j], to_float(state[(k * S + j) / V].v[(k * S + j) % V]), s);
+                s = fmaf(w[k][S], to_float(xv[k / V].v[k % V]), s);
+                o[k / V].v[k % V] = from_float<T>(act_of(s, a.shape.activation));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+#pragma unroll
+                for (int j = 0; j + 1 < S; ++j) state[(k * S + j) / V].v[(k * S + j) % V] =
+                    state[(k * S + j + 1) / V].v[(k * S + j + 1) % V];
+                state[(k * S + S - 1) / V].v[(k * S + S - 1) % V] = xv[k / V].v[k % V];
+            }
+#pragma unroll
+            for (int k = 0; k < kVecs * S; ++k)
+                *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.state_out) + at + k * V) = state[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k / V].v[k % V] = from_float<T>(0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) *reinterpret_cast<Vec<T, V>*>(out + k * V) = o[k];
+    }
+}
+
+template <typename T, int W>
+cudaError_t forward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    ConvLaunch a = in;
+    const ConvCut c = conv_cut(a.shape.channels, a.in.tokens, num_sms);
+    a.lanes = c.lanes;
+    a.run = c.run;
+    if (c.rows > INT32_MAX) return cudaErrorInvalidValue;
+    const cudaError_t e = opt_in_once(conv_forward_kernel<T, W>, 0, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(conv_forward_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
+}
+
+template <typename T, int W>
+cudaError_t backward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0}, join_done{0}, init_done{0};
+    ConvLaunch a = in;
+    const ConvCut c = conv_cut(a.shape.channels, a.in.tokens, num_sms);
+    a.lanes = c.lanes;
+    a.run = c.run;
+    const int64_t outs = (int64_t)a.shape.channels * (W + 1);
+    cudaError_t e = opt_in_once(conv_grad_kernel<T, W>, 0, done);
+    if (e == cudaSuccess) e = opt_in_once(conv_join_kernel, 0, join_done);
+    if (e == cudaSuccess)
+        e = launch_pdl(conv_grad_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
+    if (e == cudaSuccess)
+        e = launch_pdl(conv_join_kernel, dim3((unsigned)((outs + 31) / 32)), dim3(kThreads), 0, st, a, c.rows);
+    if (e == cudaSuccess && a.d_init != nullptr) {
+        const int64_t grid = ((int64_t)a.episodes * a.shape.channels + kThreads - 1) / kThreads;
+        if (grid > INT32_MAX) return cudaErrorInvalidValue;
+        e = opt_in_once(conv_init_grad_kernel<T, W>, 0, init_done);
+        if (e == cudaSuccess && grid > 0)
+            e = launch_pdl(conv_init_grad_kernel<T, W>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+    }
+    return e;
+}
+
+template <typename T, int W>
+cudaError_t step(const ConvStepLaunch& in, int num_sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    ConvStepLaunch a = in;
+    const int64_t cols = a.shape.channels / 8, full = (int64_t)num_sms * 4 * kThreads;
+    // weights are loaded once a thread: more tokens a thread once the GPU is full
+    a.per_thread = 1;
+    while (a.per_thread < 8 && a.in.tokens * cols > full * 2 * a.per_thread) a.per_thread *= 2;
+    const int64_t rows = (a.in.tokens + a.per_thread - 1) / a.per_thread, grid = (rows * cols + kThreads - 1) / kThreads;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const cudaError_t e = opt_in_once(conv_step_kernel<T, W>, 0, done);
+    return e != cudaSuccess ? e : launch_pdl(conv_step_kernel<T, W>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+}
+
+// fn<T, W>(args...) for the shape's type and width.
+#define OFRL_CONV_DISPATCH(shape, fn, ...)                                                                             \
+    ((shape).dtype == OFRL_DTYPE_F32                                                                                   \
+         ? ((shape).width == 2 ? fn<float, 2>(__VA_ARGS__)                                                             \
+                               : (shape).width == 3 ? fn<float, 3>(__VA_ARGS__) : fn<float, 4>(__VA_ARGS__))           \
+         : ((shape).width == 2 ? fn<__nv_bfloat16, 2>(__VA_ARGS__)                                                     \
+                               : (shape).width == 3 ? fn<__nv_bfloat16, 3>(__VA_ARGS__)                                \
+                                                    : fn<__nv_bfloat16, 4>(__VA_ARGS__)))
+
+ofrl_status check_shape(const ofrl_conv_shape* s) {
+    if (s == nullptr || s->channels < 1 || s->width < 1 || !dtype_ok(s->dtype) ||
+        (s->activation != OFRL_ACT_NONE && s->activation != OFRL_ACT_SILU))
+        return OFRL_EINVAL;
+    if (s->channels > 65536 || s->channels % 8 != 0 || s->width < 2 || s->width > 4) return OFRL_EUNSUPPORTED;
+    return OFRL_OK;
+}
+
+ofrl_status check_tokens(const ofrl_conv* ctx, const ofrl_conv_tokens* t) {
+    if (t == nullptr || t->tokens < 0 || t->tokens > INT32_MAX) return OFRL_EINVAL;
+    if (t->weight == nullptr || !aligned_to(t->weight, 4) || !aligned_to(t->bias, 4)) return OFRL_EINVAL;
+    if (t->tokens > 0 && !rows_ok(t->x, t->x_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
+    return OFRL_OK;
+}
+
+ofrl_status check_sequence(const ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* ends, int32_t episodes) {
+    ofrl_status s = check_device(ctx);
+    if (s == OFRL_OK) s = check_tokens(ctx, in);
+    if (s != OFRL_OK) return s;
+    if (episodes < 0 || (episodes > 0 && (ends == nullptr || !aligned_to(ends, 4)))) return OFRL_EINVAL;
+    if (in->tokens > 0 && episodes == 0) return OFRL_EINVAL;
+    if (in->tokens > ctx->max_tokens || episodes > ctx->max_episodes) return OFRL_EINVAL;
+    return OFRL_OK;
+}
+
+int64_t conv_bytes(const ofrl_conv_shape& s, int64_t max_tokens, int num_sms, bool backward) {
+    return 256 + (backward ? conv_rows_most(s.channels, max_tokens, num_sms) * s.channels * (s.width + 1) * 4 : 0);
+}
+
+ConvLaunch base_launch(const ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* ends, int32_t episodes) {
+    ConvLaunch a;
+    std::memset(&a, 0, sizeof(a));
+    a.shape = ctx->shape;
+    a.in = *in;
+    a.ends = ends;
+    a.episodes = episodes;
+    a.parts = ctx->parts;
+    a.status = ctx->status;
+    return a;
+}
+
+}  // namespace
+}  // namespace ofrl
+
+using namespace ofrl;
+
+extern "C" {
+
+int64_t ofrl_conv_workspace_bytes(const ofrl_conv_shape* shape, int64_t max_tokens, int32_t max_episodes,
+                                  int32_t backward) {
+    if (check_shape(shape) != OFRL_OK || !counts_ok(max_tokens, max_episodes) || (backward != 0 && backward != 1))
+        return -1;
+    int device = 0;
+    const int sms = current_sms(&device);
+    return conv_bytes(*shape, max_tokens, sms > 0 ? sms : 1, backward != 0);
+}
+
+ofrl_status ofrl_conv_create(const ofrl_conv_shape* shape, int64_t max_tokens, int32_t max_episodes, int32_t backward,
+                             ofrl_conv** out) {
+    if (out == nullptr) return OFRL_EINVAL;
+    *out = nullptr;
+    const ofrl_status s = check_shape(shape);
+    if (s != OFRL_OK) return s;
+    if (!counts_ok(max_tokens, max_episodes) || (backward != 0 && backward != 1)) return OFRL_EINVAL;
+    ofrl_conv* ctx = new (std::nothrow) ofrl_conv;
+    if (ctx == nullptr) return OFRL_ECUDA;
+    std::memset(ctx, 0, sizeof(*ctx));
+    ctx->num_sms = current_sms(&ctx->device);
+    ctx->shape = *shape;
+    ctx->max_tokens = max_tokens;
+    ctx->max_episodes = max_episodes;
+    ctx->backward = backward;
+    if (ctx->num_sms > 0) ctx->bytes = conv_bytes(*shape, max_tokens, ctx->num_sms, backward != 0);
+    if (ctx->num_sms == 0 || take_memory(&ctx->base, ctx->bytes) != cudaSuccess) {
+        delete ctx;
+        return OFRL_ECUDA;
+    }
+    ctx->status = static_cast<int32_t*>(ctx->base);
+    ctx->parts = reinterpret_cast<float*>(static_cast<char*>(ctx->base) + 256);
+    *out = ctx;
+    return OFRL_OK;
+}
+
+ofrl_status ofrl_conv_destroy(ofrl_conv* ctx) { return release_memory(ctx); }
+
+ofrl_status ofrl_conv_poll_status(ofrl_conv* ctx, void* stream, int32_t* words_out) {
+    return poll_words(ctx, stream, words_out);
+}
+
+ofrl_status ofrl_conv_forward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
+                              int32_t num_episodes, const void* init_state, void* out, int64_t out_stride,
+                              void* final_state, void* stream) {
+    const ofrl_status s = check_sequence(ctx, in, episode_ends, num_episodes);
+    if (s != OFRL_OK) return s;
+    if (num_episodes == 0) return OFRL_OK;
+    const int64_t e = dtype_size(ctx->shape.dtype);
+    if (in->tokens > 0 && !rows_ok(out, out_stride, ctx->shape.channels, e)) return OFRL_EINVAL;
+    if (!aligned_to(init_state, 16) || !aligned_to(final_state, 16)) return OFRL_EINVAL;
+    ConvLaunch a = base_launch(ctx, in, episode_ends, num_episodes);
+    a.init = init_state;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.final_state = final_state;
+    return cuda_status(OFRL_CONV_DISPATCH(ctx->shape, forward, a, ctx->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+ofrl_status ofrl_conv_backward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
+                               int32_t num_episodes, const void* init_state, const void* dout, int64_t dout_stride,
+                               const void* d_final, const ofrl_conv_grads* grads, float* d_init, void* stream) {
+    const ofrl_status s = check_sequence(ctx, in, episode_ends, num_episodes);
+    if (s != OFRL_OK) return s;
+    if (!ctx->backward || grads == nullptr || grads->dweight == nullptr) return OFRL_EINVAL;
+    if (!aligned_to(grads->dweight, 4) || !aligned_to(grads->dbias, 4)) return OFRL_EINVAL;
+    if (!aligned_to(init_state, 16) || !aligned_to(d_final, 16) || !aligned_to(d_init, 16)) return OFRL_EINVAL;
+    const int64_t e = dtype_size(ctx->shape.dtype);
+    if (in->tokens > 0 && (!rows_ok(dout, dout_stride, ctx->shape.channels, e) ||
+                           !rows_ok(grads->dx, grads->x_stride, ctx->shape.channels, e)))
+        return OFRL_EINVAL;
+    ConvLaunch a = base_launch(ctx, in, episode_ends, num_episodes);
+    a.init = init_state;
+    a.dout = dout;
+    a.dout_stride = dout_stride;
+    a.d_final = d_final;
+    a.grads = *grads;
+    a.d_init = d_init;
+    return cuda_status(OFRL_CONV_DISPATCH(ctx->shape, backward, a, ctx->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+ofrl_status ofrl_conv_step(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* slot_idx, int32_t slots,
+                           const void* state_in, void* state_out, void* out, int64_t out_stride, void* stream) {
+    ofrl_status s = check_device(ctx);
+    if (s == OFRL_OK) s = check_tokens(ctx, in);
+    if (s != OFRL_OK) return s;
+    if (slots < 0 || !aligned_to(slot_idx, 4) || (slot_idx == nullptr && slots < in->tokens)) return OFRL_EINVAL;
+    if (in->tokens == 0) return OFRL_OK;
+    if (!rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
+    if (!aligned_to(state_in, 16) || !aligned_to(state_out, 16)) return OFRL_EINVAL;
+    if (slots > 0 && (!state_in || !state_out)) return OFRL_EINVAL;
+    ConvStepLaunch a;
+    std::memset(&a, 0, sizeof(a));
+    a.shape = ctx->shape;
+    a.in = *in;
+    a.slot_idx = slot_idx;
+    a.slots = slots;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.status = ctx->status;
+    return cuda_status(OFRL_CONV_DISPATCH(ctx->shape, step, a, ctx->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

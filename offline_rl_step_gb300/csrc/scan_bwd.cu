@@ -1,0 +1,580 @@
+// Selective scan, gradients.
+//
+// With lam_t = dL/dh_t = dy_t C_t + a_{t+1} lam_{t+1}, dy = dout silu(z):
+//   dx_t = delta_t sum_n lam_t B_t + D dy_t          dC_t = sum_d dy_t h_t
+//   ddelta_t = x_t sum_n lam_t B_t + sum_n A lam_t p_t    dB_t = sum_d lam_t delta_t x_t
+//   dA = sum_t delta_t lam_t p_t,  p_t = a_t h_{t-1},  h_t = p_t + delta_t B_t x_t.
+// States come from the ones that the forward pass saved every kTile tokens:
+// half a tile at a time is gone over forward, p kept in shared memory, then
+// backward.  The sums over a token's channels (dB, dC) are made over a warp's
+// lanes, the CTA's warps and the CTAs, in that order.
+
+#include "scan.cuh"
+
+namespace ofrl {
+namespace scan {
+namespace {
+
+constexpr int kSub = kTile / 2;      // tokens whose p is kept at once
+
+template <int LS, int CPT>
+struct GradShared {
+    using L = Lay<LS, CPT>;
+    alignas(16) float delta[kTile][L::CB];
+    alignas(16) float dx[kTile][L::CB];      // delta x
+    alignas(16) float dy[kTile][L::CB];
+    alignas(16) float b[kTile * L::kStWidth];
+    alignas(16) float c[kTile * L::kStWidth];
+    alignas(16) float sum_b[kSub][L::CB];    // sum_n lam B
+    alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
+    alignas(16) float y[kSub][L::CB];
+    alignas(16) float dbc[kSub][kWarps][2 * L::NP];
+    alignas(16) ulonglong2 p[kSub][L::kPairs / 2][kThreads];
+    uint32_t mask[kMaxSegment / 32];
+    Range range;
+};
+
+// Sums over the 32 / LS lanes that share a state group: v[0..3] dB of the
+// thread's states, v[4..7] dC.  Lane bits pick what a lane keeps: first dB or
+// dC, then the states' half, then one state; bits left over only add.
+template <int LS>
+__device__ __forceinline__ void sum_channels(float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    int n = 8;
+#pragma unroll
+    for (int o = LS; o < 32; o <<= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) {
+                    const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+}
+// Writes what sum_channels left in this lane to a token's [2 NP].
+template <int LS>
+__device__ __forceinline__ void put_channels(float* dst, const float (&v)[8], int n0) {
+    const int lane = threadIdx.x & 31;
+    constexpr int NP = 4 * LS;
+    float* p = dst + (lane & LS ? NP : 0) + n0;
+    if constexpr (LS == 16) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (LS == 8) {
+        *reinterpret_cast<float2*>(p + (lane & 16 ? 2 : 0)) = make_float2(v[0], v[1]);
+    } else {
+        if ((lane & ~(8 * LS - 1)) == 0) p[(lane & 2 * LS ? 2 : 0) + (lane & 4 * LS ? 1 : 0)] = v[0];
+    }
+}
+
+template <int ROWS, typename T, int LS, int CPT>
+__device__ __forceinline__ void put_deltas(float (*delta)[Lay<LS, CPT>::CB], float (*dx)[Lay<LS, CPT>::CB],
+                                           float (*dy)[Lay<LS, CPT>::CB], const Launch& a, const Block& b, int t0, int rows,
+                                           const float (&bias)[Tiling<T, Lay<LS, CPT>::CB, ROWS>::V]) {
+    constexpr int CB = Lay<LS, CPT>::CB;
+    using Ti = Tiling<T, CB, ROWS>;
+    RowsHeld<T, CB, ROWS> x, dt, z, g;
+    if (dx != nullptr) x.load(a.in.x, a.in.x_stride, b, t0, rows);
+    dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+    if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
+    g.load(a.dout, a.dout_stride, b, t0, rows);
+#pragma unroll
+    for (int j = 0; j < Ti::NV; ++j) {
+        const int r = Ti::row(j);
+        if (r >= ROWS) continue;
+        float d[Ti::V], xs[Ti::V], gy[Ti::V];
+#pragma unroll
+        for (int i = 0; i < Ti::V; ++i) {
+            d[i] = delta_of(dt.at(j, i), bias[i], a.shape.softplus);
+            if (dx != nullptr) xs[i] = d[i] * x.at(j, i);
+            gy[i] = g.at(j, i);
+            if (a.in.z != nullptr) gy[i] *= z.at(j, i) * sigmoid(z.at(j, i));
+        }
+        put_floats(&delta[r][Ti::col()], d);
+        if (dx != nullptr) put_floats(&dx[r][Ti::col()], xs);
+        put_floats(&dy[r][Ti::col()], gy);
+    }
+}
+
+// The adjoint a segment hands to the one before it.
+template <typename T, int LS, int CPT>
+__global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_constant__ Launch a) {
+    using L = Lay<LS, CPT>;
+    using Ti = Tiling<T, L::CB, kTile>;
+    __shared__ struct {
+        alignas(16) float delta[kTile][L::CB];
+        alignas(16) float dy[kTile][L::CB];
+        alignas(16) float c[kTile * L::kStWidth];
+        uint32_t mask[kMaxSegment / 32];
+        Range range;
+    } s;
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
+    const int s0 = (int)((int64_t)blockIdx.x * a.seg), s1 = (int)min((int64_t)s0 + a.seg, (int64_t)tokens);
+    for (int i = threadIdx.x; i < kMaxSegment / 32; i += kThreads) s.mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const Range r = mark_starts(a.ends, a.episodes, tokens, s0, s1, s.mask);
+        if (threadIdx.x == 0) s.range = r;
+    }
+    __syncthreads();
+    if ((s.mask[0] & 1) || s.range.end <= s0) {      // nothing goes to the segment before
+        if (threadIdx.x == 0 && blockIdx.y == 0) a.kind[blockIdx.x] = kTailNone;
+        return;
+    }
+    int end = s.range.end;
+    bool own = s.range.closed;
+    for (int w = 0; w <= (end - s0 - 1) >> 5; ++w)
+        if (s.mask[w]) {
+            end = s0 + w * 32 + __ffs(s.mask[w]) - 1;
+            own = true;
+            break;
+        }
+    if (threadIdx.x == 0 && blockIdx.y == 0) a.kind[blockIdx.x] = own ? kTailOwn : kTailJoin;
+
+    const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
+    const Place<LS, CPT> p(b);
+    f2 a2[L::kPairs], lam[L::kPairs], sum[L::kCh];
+    load_decays<LS, CPT>(a2, a, p);
+    float bias[Ti::V];
+    load_params<T, L::CB, kTile>(bias, a.in.dt_bias, b);
+#pragma unroll
+    for (int i = 0; i < L::kCh; ++i) sum[i] = f2_of(0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < L::kPairs; ++q) lam[q] = f2_of(0.0f, 0.0f);
+    if (own && a.d_final != nullptr && s.range.e0 < a.episodes)
+        load_states<LS, CPT>(lam, a.d_final + (int64_t)s.range.e0 * a.shape.channels * n, n, p.ch, p.count, p.n0);
+    const f2 one = f2_of(1.0f, 1.0f);
+    for (int t0 = s0 + (end - 1 - s0) / kTile * kTile; t0 >= s0; t0 -= kTile) {
+        const int rows = min(kTile, end - t0);
+        StatesHeld<T, LS, CPT> cs;
+        cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+        __syncthreads();
+        put_deltas<kTile, T, LS, CPT>(s.delta, nullptr, s.dy, a, b, t0, rows, bias);
+        cs.put(s.c);
+        __syncthreads();
+        auto step = [&](int i) {
+            f2 de[L::kCh], gy[L::kCh], cv[L::kSt];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(gy, &s.dy[i][p.local]);
+            L::states(cv, s.c + i * L::kStWidth + L::state_at((threadIdx.x & 31) % LS));
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                lam[q] = f2_mul(decay, f2_fma(gy[L::ci(q)], cv[L::si(q)], lam[q]));
+            }
+#pragma unroll
+            for (int k = 0; k < L::kCh; ++k) sum[k] = f2_fma(de[k], one, sum[k]);
+        };
+        if (rows == kTile) {
+#pragma unroll 4
+            for (int i = kTile - 1; i >= 0; --i) step(i);
+        } else {
+            for (int i = rows - 1; i >= 0; --i) step(i);
+        }
+    }
+    store_states<LS, CPT>(a.tail + (int64_t)blockIdx.x * a.shape.channels * n, lam, n, p.ch, p.count, p.n0);
+    if ((threadIdx.x & 31) % LS == 0) {
+        float* out = a.sum + (int64_t)blockIdx.x * a.shape.channels + p.ch;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            float lo, hi;
+            f2_split(sum[i / 2], lo, hi);
+            if (i < p.count) out[i] = i & 1 ? hi : lo;
+        }
+    }
+}
+
+template <typename T, int LS, int CPT>
+__global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_constant__ Launch a) {
+    using L = Lay<LS, CPT>;
+    using Ti = Tiling<T, L::CB, kSub>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    GradShared<LS, CPT>& s = *reinterpret_cast<GradShared<LS, CPT>*>(smem);
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
+    const int64_t row_states = (int64_t)a.shape.channels * n;
+    const int s0 = (int)((int64_t)blockIdx.x * a.seg), s1 = (int)min((int64_t)s0 + a.seg, (int64_t)tokens);
+    for (int i = threadIdx.x; i < kMaxSegment / 32; i += kThreads) s.mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const Range r = mark_starts(a.ends, a.episodes, tokens, s0, s1, s.mask);
+        if (threadIdx.x == 0) s.range = r;
+    }
+    const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
+    const Place<LS, CPT> p(b);
+    const bool mine = p.n0 < n;
+    const int parts = a.blocks / a.shape.groups;      // CTAs that share a group's dB and dC
+    f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs];
+    load_decays<LS, CPT>(a2, a, p);
+    float bias[Ti::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
+    load_params<T, L::CB, kSub>(bias, a.in.dt_bias, b);
+    load_params<T, L::CB, kSub>(skip, a.in.d, b);
+#pragma unroll
+    for (int i = 0; i < Ti::V; ++i) dskip[i] = dbias[i] = 0.0f;
+    const f2 zero = f2_of(0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < L::kPairs; ++q) da[q] = lam[q] = zero;
+    __syncthreads();
+    const int end = s.range.end;
+
+    // the adjoint of an episode's last state, t its last token
+    auto enter = [&](int t) {
+#pragma unroll
+        for (int q = 0; q < L::kPairs; ++q) lam[q] = zero;
+        if (a.d_final == nullptr) return;
+        const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
+        if (e < a.episodes) load_states<LS, CPT>(lam, a.d_final + e * row_states, n, p.ch, p.count, p.n0);
+    };
+    // the state before token t, which begins an episode
+    auto begin = [&](int t) {
+#pragma unroll
+        for (int q = 0; q < L::kPairs; ++q) h[q] = zero;
+        if (a.init == nullptr) return;
+        const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
+        if (e < a.episodes) load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
+    };
+    if (end > s0) {
+        if (s.range.closed)
+            enter(end - 1);
+        else
+            load_states<LS, CPT>(lam, a.tail + (int64_t)blockIdx.x * row_states, n, p.ch, p.count, p.n0);
+    }
+    const int at_state = L::state_at((threadIdx.x & 31) % LS);
+
+    for (int t0 = s0 + (end - 1 - s0) / kTile * kTile; t0 >= s0 && end > s0; t0 -= kTile) {
+        const int rows = min(kTile, end - t0);
+        StatesHeld<T, LS, CPT> bs, cs;
+        bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
+        cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+        __syncthreads();      // the tile before is through
+        put_deltas<kSub, T, LS, CPT>(s.delta, s.dx, s.dy, a, b, t0, rows, bias);
+        if (rows > kSub)
+            put_deltas<kSub, T, LS, CPT>(s.delta + kSub, s.dx + kSub, s.dy + kSub, a, b, t0 + kSub, rows - kSub, bias);
+        bs.put(s.b);
+        cs.put(s.c);
+        __syncthreads();
+        const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
+
+        auto forward = [&](int i, bool keep) {
+            if (starts >> i & 1) begin(t0 + i);
+            f2 de[L::kCh], dx[L::kCh], bv[L::kSt], was[L::kPairs];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            L::states(bv, s.b + i * L::kStWidth + at_state);
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
+                h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
+            }
+            if (keep)
+#pragma unroll
+                for (int q = 0; q < L::kPairs; q += 2)
+                    s.p[i % kSub][q / 2][threadIdx.x] = make_ulonglong2(was[q], was[q + 1]);
+        };
+        auto backward = [&](int i) {
+            const int r = i % kSub;
+            f2 de[L::kCh], dx[L::kCh], gy[L::kCh], bv[L::kSt], cv[L::kSt];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            L::channels(gy, &s.dy[i][p.local]);
+            L::states(bv, s.b + i * L::kStWidth + at_state);
+            L::states(cv, s.c + i * L::kStWidth + at_state);
+            f2 sb[L::kCh], sa[L::kCh], sy[L::kCh], db[L::kSt], dc[L::kSt];
+#pragma unroll
+            for (int k = 0; k < L::kCh; ++k) sb[k] = sa[k] = sy[k] = zero;
+#pragma unroll
+            for (int k = 0; k < L::kSt; ++k) db[k] = dc[k] = zero;
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                const int c = L::ci(q), k = L::si(q);
+                const ulonglong2 two = s.p[r][q / 2][threadIdx.x];
+                const f2 was = q & 1 ? two.y : two.x;
+                const f2 now = f2_fma(dx[c], bv[k], was);
+                const f2 l = f2_fma(gy[c], cv[k], lam[q]);
+                dc[k] = f2_fma(gy[c], now, dc[k]);
+                db[k] = f2_fma(l, dx[c], db[k]);
+                sb[c] = f2_fma(l, bv[k], sb[c]);
+                sy[c] = f2_fma(cv[k], now, sy[c]);
+                const f2 w = f2_mul(l, was);
+                sa[c] = f2_fma(w, a2[q], sa[c]);
+                da[q] = f2_fma(w, de[c], da[q]);
+                lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
+            }
+            float v[8], ch[3][CPT];
+            if constexpr (L::kWide) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = f2_sum(db[k]);
+                    v[4 + k] = f2_sum(dc[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < L::kCh; ++k) {
+                    f2_split(sb[k], ch[0][2 * k], ch[0][2 * k + 1]);
+                    f2_split(sa[k], ch[1][2 * k], ch[1][2 * k + 1]);
+                    f2_split(sy[k], ch[2][2 * k], ch[2][2 * k + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f2_split(db[k], v[2 * k], v[2 * k + 1]);
+                    f2_split(dc[k], v[4 + 2 * k], v[4 + 2 * k + 1]);
+                }
+                ch[0][0] = f2_sum(sb[0]);
+                ch[1][0] = f2_sum(sa[0]);
+                ch[2][0] = f2_sum(sy[0]);
+            }
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+                if (!mine) ch[0][k] = ch[1][k] = ch[2][k] = 0.0f;
+            sum_channels<LS>(v);
+            put_channels<LS>(s.dbc[r][threadIdx.x >> 5], v, p.n0);
+            const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]), y = sum_states<LS, CPT>(ch[2]);
+            if (returns_channel<LS, CPT>()) {
+                const int at = p.local + which_channel<LS, CPT>();
+                s.sum_b[r][at] = to_b;
+                s.sum_a[r][at] = to_a;
+                s.y[r][at] = y;
+            }
+            if (starts >> i & 1) {
+                const int t = t0 + i;
+                if (a.d_init != nullptr) {
+                    const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
+                    if (e < a.episodes) store_states<LS, CPT>(a.d_init + e * row_states, lam, n, p.ch, p.count, p.n0);
+                }
+                if (t > s0) enter(t - 1);
+            }
+        };
+        // rows [r0, r0 + count) of the tile, from shared memory to the gradients
+        auto finish = [&](int r0, int count) {
+            const int t1 = t0 + r0;
+            RowsHeld<T, L::CB, kSub> x, dt, z, g;
+            x.load(a.in.x, a.in.x_stride, b, t1, count);
+            if (a.shape.softplus) dt.load(a.in.dt, a.in.dt_stride, b, t1, count);
+            if (a.in.z != nullptr) {
+                z.load(a.in.z, a.in.z_stride, b, t1, count);
+                g.load(a.dout, a.dout_stride, b, t1, count);
+            }
+            const int64_t ch = b.ch0 + Ti::col();
+#pragma unroll
+            for (int j = 0; j < Ti::NV; ++j) {
+                const int r = Ti::row(j);
+                if (r >= count || Ti::col() >= b.count) continue;
+                float dxs[Ti::V], ddt[Ti::V], dz[Ti::V];
+#pragma unroll
+                for (int i = 0; i < Ti::V; ++i) {
+                    const int c = Ti::col() + i;
+                    const float xv = x.at(j, i), gy = s.dy[r0 + r][c], to_b = s.sum_b[r][c];
+                    dxs[i] = s.delta[r0 + r][c] * to_b;
+                    if (a.in.d != nullptr) dxs[i] = fmaf(skip[i], gy, dxs[i]);
+                    ddt[i] = fmaf(xv, to_b, s.sum_a[r][c] * kLn2);
+                    if (a.shape.softplus) ddt[i] *= sigmoid(dt.at(j, i) + bias[i]);
+                    if (a.in.z != nullptr) {
+                        float y = s.y[r][c];
+                        if (a.in.d != nullptr) y = fmaf(skip[i], xv, y);
+                        const float zv = z.at(j, i), sg = sigmoid(zv);
+                        dz[i] = g.at(j, i) * y * sg * (1.0f + zv * (1.0f - sg));
+                    }
+                    dskip[i] = fmaf(gy, xv, dskip[i]);
+                    dbias[i] += ddt[i];
+                }
+                const int64_t t = t1 + r;
+                store_vec<T, Ti::V>(static_cast<T*>(a.grads.dx) + t * a.grads.x_stride + ch, dxs);
+                store_vec<T, Ti::V>(static_cast<T*>(a.grads.ddt) + t * a.grads.dt_stride + ch, ddt);
+                if (a.in.z != nullptr)
+                    store_vec<T, Ti::V>(static_cast<T*>(a.grads.dz) + t * a.grads.z_stride + ch, dz);
+            }
+            for (int i = threadIdx.x; i < count * 2 * L::NP; i += kThreads) {
+                const int r = i / (2 * L::NP), k = i % (2 * L::NP), st = k % L::NP;
+                float v = s.dbc[r][0][k];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v += s.dbc[r][w][k];
+                const int64_t t = t1 + r;
+                if (parts > 1) {
+                    a.dbc[(((int64_t)(blockIdx.y % parts) * tokens + t) * a.shape.groups + b.group) * (2 * L::NP) + k] = v;
+                } else if (st < n) {
+                    if (k < L::NP)
+                        static_cast<T*>(a.grads.db)[t * a.grads.b_stride + b.group * n + st] = from_float<T>(v);
+                    else
+                        static_cast<T*>(a.grads.dc)[t * a.grads.c_stride + b.group * n + st] = from_float<T>(v);
+                }
+            }
+        };
+        auto before_tile = [&]() {
+            if (!(starts & 1))
+                load_states<LS, CPT>(h, a.saved + (int64_t)(t0 / kTile) * row_states, n, p.ch, p.count, p.n0);
+        };
+
+        before_tile();
+        if (rows > kSub) {
+            for (int i = 0; i < kSub; ++i) forward(i, false);
+            for (int i = kSub; i < rows; ++i) forward(i, true);
+            for (int i = rows - 1; i >= kSub; --i) backward(i);
+            __syncthreads();
+            finish(kSub, rows - kSub);
+            before_tile();
+            __syncthreads();
+        }
+        const int first = min(rows, kSub);
+        for (int i = 0; i < first; ++i) forward(i, true);
+        for (int i = first - 1; i >= 0; --i) backward(i);
+        __syncthreads();
+        finish(0, first);
+    }
+
+    store_states<LS, CPT>(a.da + (int64_t)blockIdx.x * row_states, da, n, p.ch, p.count, p.n0);
+    // dD and ddt_bias over the threads of a column
+    float(*red)[2][L::CB] = reinterpret_cast<float(*)[2][L::CB]>(&s.delta[0][0]);
+    static_assert(sizeof(float) * Ti::kRowStep * 2 * L::CB <= sizeof(s) - sizeof(s.mask) - sizeof(s.range), "");
+    __syncthreads();
+    put_floats(&red[threadIdx.x / Ti::kCols][0][Ti::col()], dskip);
+    put_floats(&red[threadIdx.x / Ti::kCols][1][Ti::col()], dbias);
+    __syncthreads();
+    for (int c = threadIdx.x; c < b.count; c += kThreads) {
+        float v = 0.0f, w = 0.0f;
+        for (int k = 0; k < Ti::kRowStep; ++k) {
+            v += red[k][0][c];
+            w += red[k][1][c];
+        }
+        a.dd[(int64_t)blockIdx.x * a.shape.channels + b.ch0 + c] = v;
+        a.dd[((int64_t)a.n_seg + blockIdx.x) * a.shape.channels + b.ch0 + c] = w;
+    }
+
+    // Episodes without tokens: the gradient passes through.
+    if (a.d_init != nullptr) {
+        const int lane = threadIdx.x & 31;
+        for (int64_t base = (int64_t)blockIdx.x * 32; base < a.episodes; base += (int64_t)gridDim.x * 32) {
+            const int64_t at = base + lane;
+            unsigned empty = __ballot_sync(0xffffffffu, at < a.episodes && episode_end(a.ends, (int)at, tokens) <=
+                                                                             episode_start(a.ends, (int)at, tokens));
+            for (; empty; empty &= empty - 1) {
+                const int64_t ep = base + __ffs(empty) - 1;
+#pragma unroll
+                for (int q = 0; q < L::kPairs; ++q) h[q] = zero;
+                if (a.d_final != nullptr) load_states<LS, CPT>(h, a.d_final + ep * row_states, n, p.ch, p.count, p.n0);
+                store_states<LS, CPT>(a.d_init + ep * row_states, h, n, p.ch, p.count, p.n0);
+            }
+        }
+    }
+}
+
+// Joins the parts: dA, dD and ddt_bias over the segments, dB and dC over a
+// group's CTAs.  CTAs [0, over): 32 outputs each, eight threads to an output;
+// the rest: an output a thread.
+constexpr int kJoinThreads = 256, kSlices = 8;
+
+__device__ __forceinline__ float slice_sum(const float* p, int64_t stride, int parts, float (*red)[33]) {
+    const int col = threadIdx.x % 32, slice = threadIdx.x / 32;
+    float v = 0.0f;
+    if (p != nullptr) {
+#pragma unroll 8
+        for (int j = slice; j < parts; j += kSlices) v += p[j * stride];
+    }
+    red[slice][col] = v;
+    __syncthreads();
+    float sum = 0.0f;
+    if (slice == 0)
+        for (int k = 0; k < kSlices; ++k) sum += red[k][col];
+    return sum;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) scan_grad_join_kernel(const __grid_constant__ Launch a, int np, unsigned over) {
+    __shared__ float red[kSlices][33];
+    pdl_wait();
+    pdl_trigger();
+    const int n = a.shape.state_dim, d = a.shape.channels;
+    if (blockIdx.x < over) {
+        const int64_t states = (int64_t)d * n, i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+        const float* p = nullptr;
+        float* out = nullptr;
+        int64_t stride = 0;
+        if (i < states) {
+            p = a.da + i;
+            stride = states;
+            out = a.grads.da + i;
+        } else if (i < states + 2 * (int64_t)d) {
+            const int64_t k = i - states;
+            p = a.dd + (k < d ? k : (int64_t)a.n_seg * d + k - d);
+            stride = d;
+            out = k < d ? a.grads.dd : a.grads.ddt_bias;
+            if (out != nullptr) out += k < d ? k : k - d;
+        }
+        const float v = slice_sum(p, stride, a.n_seg, red);
+        if (threadIdx.x < 32 && out != nullptr) *out = v;
+        return;
+    }
+    const int tokens = (int)a.in.tokens, live = episode_end(a.ends, a.episodes - 1, tokens);
+    const int64_t per = (int64_t)a.shape.groups * 2 * np, total = (int64_t)live * per;
+    const int parts = a.blocks / a.shape.groups;
+    const int64_t i = ((int64_t)blockIdx.x - over) * kJoinThreads + threadIdx.x;
+    if (i >= total) return;
+    const int64_t t = i / per;
+    const int rest = (int)(i - t * per), group = rest / (2 * np), k = rest % (2 * np), st = k % np;
+    if (st >= n) return;
+    float v = a.dbc[i];
+    for (int j = 1; j < parts; ++j) v += a.dbc[(int64_t)j * tokens * per + i];
+    if (k < np)
+        static_cast<T*>(a.grads.db)[t * a.grads.b_stride + group * n + st] = from_float<T>(v);
+    else
+        static_cast<T*>(a.grads.dc)[t * a.grads.c_stride + group * n + st] = from_float<T>(v);
+}
+
+template <typename T>
+cudaError_t join(const Launch& a, const Cut& c, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = opt_in_once(scan_grad_join_kernel<T>, 0, done);
+    if (e != cudaSuccess) return e;
+    const int np = 4 * c.ls;
+    const int64_t outs = (int64_t)a.shape.channels * (a.shape.state_dim + 2), over = (outs + 31) / 32;
+    int64_t more = 0;
+    if (c.blocks > a.shape.groups)
+        more = (a.in.tokens * a.shape.groups * 2 * np + kJoinThreads - 1) / kJoinThreads;
+    if (over + more > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_ex(scan_grad_join_kernel<T>, dim3((unsigned)(over + more)), dim3(kJoinThreads), 0, st, 1, false, a, np,
+                     (unsigned)over);
+}
+
+template <typename T, int LS, int CPT>
+cudaError_t go(const Launch& a, const Cut& c, cudaStream_t st) {
+    static std::atomic<uint64_t> tail_done{0}, done{0};
+    const dim3 grid((unsigned)c.n_seg, (unsigned)c.blocks);
+    const int smem = (int)sizeof(GradShared<LS, CPT>);
+    cudaError_t e = opt_in_once(scan_grad_kernel<T, LS, CPT>, smem, done);
+    if (c.n_seg > 1) {
+        if (e == cudaSuccess) e = opt_in_once(scan_grad_tail_kernel<T, LS, CPT>, 0, tail_done);
+        if (e == cudaSuccess) e = launch_pdl(scan_grad_tail_kernel<T, LS, CPT>, grid, dim3(kThreads), 0, st, a);
+        if (e == cudaSuccess) e = launch_carry(a, true, st);
+    }
+    if (e == cudaSuccess) e = launch_pdl(scan_grad_kernel<T, LS, CPT>, grid, dim3(kThreads), smem, st, a);
+    if (e == cudaSuccess) e = join<T>(a, c, st);
+    return e;
+}
+
+template <typename T>
+cudaError_t run(const Launch& a, const Cut& c, cudaStream_t st) {
+    const bool wide = c.cpt > 1;
+    switch (c.ls) {
+        case 1: return go<T, 1, 1>(a, c, st);
+        case 2: return wide ? go<T, 2, 2>(a, c, st) : go<T, 2, 1>(a, c, st);
+        case 4: return wide ? go<T, 4, 4>(a, c, st) : go<T, 4, 1>(a, c, st);
+        case 8: return wide ? go<T, 8, 4>(a, c, st) : go<T, 8, 1>(a, c, st);
+        default: return wide ? go<T, 16, 4>(a, c, st) : go<T, 16, 1>(a, c, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_backward(const Launch& a, const Cut& c, cudaStream_t st) {
+    return a.shape.dtype == OFRL_DTYPE_F32 ? run<float>(a, c, st) : run<__nv_bfloat16>(a, c, st);
+}
+
+}  // namespace scan
+}  // namespace ofrl

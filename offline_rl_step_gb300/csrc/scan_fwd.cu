@@ -1,0 +1,383 @@
+// Selective scan, forward: tails of segments, their join, the segments.
+
+#include "scan.cuh"
+
+namespace ofrl {
+namespace scan {
+namespace {
+
+template <int LS, int CPT>
+struct Shared {
+    using L = Lay<LS, CPT>;
+    alignas(16) float delta[kTile][L::CB];
+    alignas(16) float dx[kTile][L::CB];      // delta x
+    alignas(16) float b[kTile * L::kStWidth];
+    uint32_t mask[kMaxSegment / 32];
+    Range range;
+};
+template <int LS, int CPT>
+struct SharedAll : Shared<LS, CPT> {
+    using L = Lay<LS, CPT>;
+    alignas(16) float y[kTile][L::CB];
+    alignas(16) float c[kTile * L::kStWidth];
+};
+
+// delta and delta x of a tile, to shared memory.
+template <typename T, int LS, int CPT>
+__device__ __forceinline__ void put_rows(Shared<LS, CPT>& s, const RowsHeld<T, Lay<LS, CPT>::CB, kTile>& x,
+                                         const RowsHeld<T, Lay<LS, CPT>::CB, kTile>& dt,
+                                         const float (&bias)[Tiling<T, Lay<LS, CPT>::CB, kTile>::V], int with_softplus) {
+    using Ti = Tiling<T, Lay<LS, CPT>::CB, kTile>;
+#pragma unroll
+    for (int j = 0; j < Ti::NV; ++j) {
+        if (Ti::row(j) >= kTile) continue;
+        float d[Ti::V], dx[Ti::V];
+#pragma unroll
+        for (int i = 0; i < Ti::V; ++i) {
+            d[i] = delta_of(dt.at(j, i), bias[i], with_softplus);
+            dx[i] = d[i] * x.at(j, i);
+        }
+        put_floats(&s.delta[Ti::row(j)][Ti::col()], d);
+        put_floats(&s.dx[Ti::row(j)][Ti::col()], dx);
+    }
+}
+
+// 1. The state a segment ends with, as far as it is the segment's own.
+template <typename T, int LS, int CPT>
+__global__ void __launch_bounds__(kThreads) scan_tail_kernel(const __grid_constant__ Launch a) {
+    using L = Lay<LS, CPT>;
+    using Ti = Tiling<T, L::CB, kTile>;
+    __shared__ Shared<LS, CPT> s;
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
+    const int s0 = (int)((int64_t)blockIdx.x * a.seg), s1 = (int)min((int64_t)s0 + a.seg, (int64_t)tokens);
+    for (int i = threadIdx.x; i < kMaxSegment / 32; i += kThreads) s.mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const Range r = mark_starts(a.ends, a.episodes, tokens, s0, s1, s.mask);
+        if (threadIdx.x == 0) s.range = r;
+    }
+    __syncthreads();
+    if (s.range.closed) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) a.kind[blockIdx.x] = kTailNone;
+        return;
+    }
+    int begin = s0, own = 0;
+    for (int w = (s1 - s0 - 1) >> 5; w >= 0; --w)
+        if (s.mask[w]) {
+            begin = s0 + w * 32 + 31 - __clz(s.mask[w]);
+            own = 1;
+            break;
+        }
+    if (threadIdx.x == 0 && blockIdx.y == 0) a.kind[blockIdx.x] = own ? kTailOwn : kTailJoin;
+
+    const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
+    const Place<LS, CPT> p(b);
+    RowsHeld<T, L::CB, kTile> x, dt;
+    StatesHeld<T, LS, CPT> bs;
+    auto fetch = [&](int t0) {
+        const int rows = min(kTile, s1 - t0);
+        x.load(a.in.x, a.in.x_stride, b, t0, rows);
+        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+        bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
+    };
+    fetch(begin);
+    f2 a2[L::kPairs], h[L::kPairs], sum[L::kCh];
+    load_decays<LS, CPT>(a2, a, p);
+    float bias[Ti::V];
+    load_params<T, L::CB, kTile>(bias, a.in.dt_bias, b);
+#pragma unroll
+    for (int i = 0; i < L::kCh; ++i) sum[i] = f2_of(0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < L::kPairs; ++q) h[q] = f2_of(0.0f, 0.0f);
+    if (own && a.init != nullptr) {
+        const int e = find_episode(a.ends, s.range.e0, a.episodes, tokens, s1 - 1);
+        load_states<LS, CPT>(h, a.init + (int64_t)min(e, a.episodes - 1) * a.shape.channels * n, n, p.ch, p.count, p.n0);
+    }
+    const f2 one = f2_of(1.0f, 1.0f);
+    for (int t0 = begin; t0 < s1; t0 += kTile) {
+        const int rows = min(kTile, s1 - t0);
+        __syncthreads();
+        put_rows<T, LS, CPT>(s, x, dt, bias, a.shape.softplus);
+        bs.put(s.b);
+        __syncthreads();
+        if (t0 + kTile < s1) fetch(t0 + kTile);
+        auto step = [&](int i) {
+            f2 de[L::kCh], dx[L::kCh], bv[L::kSt];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            L::states(bv, s.b + i * L::kStWidth + L::state_at((threadIdx.x & 31) % LS));
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], f2_mul(decay, h[q]));
+            }
+#pragma unroll
+            for (int k = 0; k < L::kCh; ++k) sum[k] = f2_fma(de[k], one, sum[k]);
+        };
+        if (rows == kTile) {
+#pragma unroll 4
+            for (int i = 0; i < kTile; ++i) step(i);
+        } else {
+            for (int i = 0; i < rows; ++i) step(i);
+        }
+    }
+    store_states<LS, CPT>(a.tail + (int64_t)blockIdx.x * a.shape.channels * n, h, n, p.ch, p.count, p.n0);
+    if ((threadIdx.x & 31) % LS == 0) {
+        float* out = a.sum + (int64_t)blockIdx.x * a.shape.channels + p.ch;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            float lo, hi;
+            f2_split(sum[i / 2], lo, hi);
+            if (i < p.count) out[i] = i & 1 ? hi : lo;
+        }
+    }
+}
+
+// 2. What each segment takes over, in the place of its tail.  Backward: from the
+// last segment to the first.  A thread has one state of one channel; the loads
+// of kAhead segments are in flight while those before are joined.
+constexpr int kAhead = 16;
+
+__global__ void __launch_bounds__(kThreads) scan_carry_kernel(const __grid_constant__ Launch a, int backward) {
+    pdl_wait();
+    pdl_trigger();
+    const int n = a.shape.state_dim;
+    const int64_t states = (int64_t)a.shape.channels * n, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= states) return;
+    const float a2 = a.in.a[i] * kLog2e;
+    const int64_t ch = i / n;
+    float carry = 0.0f;
+    float tail[kAhead], sum[kAhead];
+    int kind[kAhead];
+    auto fetch = [&](int from) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
+            if (from + k < a.n_seg) {
+                kind[k] = a.kind[j];
+                tail[k] = a.tail[j * states + i];
+                sum[k] = a.sum[(int64_t)j * a.shape.channels + ch];
+            }
+        }
+    };
+    fetch(0);
+    for (int from = 0; from < a.n_seg; from += kAhead) {
+        float own[kAhead], decay[kAhead];
+        int what[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            own[k] = tail[k];
+            decay[k] = exp2_of(a2 * sum[k]);
+            what[k] = kind[k];
+        }
+        if (from + kAhead < a.n_seg) fetch(from + kAhead);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (from + k >= a.n_seg) break;
+            const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
+            a.tail[j * states + i] = carry;
+            // selected, not multiplied: what an unused tail holds stays out
+            carry = what[k] == kTailJoin ? fmaf(decay[k], carry, own[k]) : what[k] == kTailOwn ? own[k] : 0.0f;
+        }
+    }
+}
+
+// 3. The segments.
+template <typename T, int LS, int CPT>
+__global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_constant__ Launch a) {
+    using L = Lay<LS, CPT>;
+    using Ti = Tiling<T, L::CB, kTile>;
+    __shared__ SharedAll<LS, CPT> s;
+    pdl_wait();
+    pdl_trigger();
+    const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
+    const int64_t row_states = (int64_t)a.shape.channels * n;
+    const int s0 = (int)((int64_t)blockIdx.x * a.seg), s1 = (int)min((int64_t)s0 + a.seg, (int64_t)tokens);
+    const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
+    const Place<LS, CPT> p(b);
+    const bool mine = p.n0 < n;     // threads past the last state take no part in sums
+    RowsHeld<T, L::CB, kTile> x, dt;
+    StatesHeld<T, LS, CPT> bs, cs;
+    auto fetch = [&](int t0) {
+        const int rows = min(kTile, s1 - t0);
+        x.load(a.in.x, a.in.x_stride, b, t0, rows);
+        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+        bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
+        cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+    };
+    if (s0 < s1) fetch(s0);
+    for (int i = threadIdx.x; i < kMaxSegment / 32; i += kThreads) s.mask[i] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const Range r = mark_starts(a.ends, a.episodes, tokens, s0, s1, s.mask);
+        if (threadIdx.x == 0) s.range = r;
+        if (blockIdx.y == 0) {
+            const int bad = count_bad_ends(a.ends, a.episodes, tokens, blockIdx.x, gridDim.x);
+            if (threadIdx.x == 0 && bad) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, bad);
+        }
+    }
+    f2 a2[L::kPairs], h[L::kPairs];
+    load_decays<LS, CPT>(a2, a, p);
+    float bias[Ti::V], skip[Ti::V];
+    load_params<T, L::CB, kTile>(bias, a.in.dt_bias, b);
+    load_params<T, L::CB, kTile>(skip, a.in.d, b);
+    __syncthreads();
+    const int end = s.range.end;
+    int e = s.range.e0;
+#pragma unroll
+    for (int q = 0; q < L::kPairs; ++q) h[q] = f2_of(0.0f, 0.0f);
+    if (s0 > 0 && s0 < end && !(s.mask[0] & 1))
+        load_states<LS, CPT>(h, a.tail + (int64_t)blockIdx.x * row_states, n, p.ch, p.count, p.n0);
+
+    auto leave = [&]() {     // the episode's last token is done
+        if (a.final_state != nullptr && e < a.episodes)
+            store_states<LS, CPT>(a.final_state + e * row_states, h, n, p.ch, p.count, p.n0);
+    };
+    for (int t0 = s0; t0 < end; t0 += kTile) {
+        const int rows = min(kTile, end - t0);
+        if (t0 > s0) __syncthreads();      // the tile before is through
+        put_rows<T, LS, CPT>(s, x, dt, bias, a.shape.softplus);
+        bs.put(s.b);
+        cs.put(s.c);
+        const RowsHeld<T, L::CB, kTile> x_now = x;
+        RowsHeld<T, L::CB, kTile> z;
+        __syncthreads();
+        if (t0 + kTile < end) fetch(t0 + kTile);
+        if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
+        const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
+        if (a.saved != nullptr && !(starts & 1))
+            store_states<LS, CPT>(a.saved + (int64_t)(t0 / kTile) * row_states, h, n, p.ch, p.count, p.n0);
+        auto step = [&](int i) {
+            f2 de[L::kCh], dx[L::kCh], bv[L::kSt], cv[L::kSt];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            const int at = i * L::kStWidth + L::state_at((threadIdx.x & 31) % LS);
+            L::states(bv, s.b + at);
+            L::states(cv, s.c + at);
+            f2 acc[L::kCh];
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], f2_mul(decay, h[q]));
+                acc[L::ci(q)] = L::si(q) == 0 ? f2_mul(cv[0], h[q]) : f2_fma(cv[L::si(q)], h[q], acc[L::ci(q)]);
+            }
+            float y[CPT];
+            if constexpr (CPT == 1) {
+                y[0] = f2_sum(acc[0]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < L::kCh; ++k) f2_split(acc[k], y[2 * k], y[2 * k + 1]);
+            }
+            if (!mine)
+#pragma unroll
+                for (int k = 0; k < CPT; ++k) y[k] = 0.0f;
+            const float sum = sum_states<LS, CPT>(y);
+            if (returns_channel<LS, CPT>()) s.y[i][p.local + which_channel<LS, CPT>()] = sum;
+        };
+        if (starts == 0 && rows == kTile) {
+#pragma unroll 4
+            for (int i = 0; i < kTile; ++i) step(i);
+        } else {
+            for (int i = 0; i < rows; ++i) {
+                if (starts >> i & 1) {
+                    if (t0 + i > s0) {
+                        leave();
+                        if (a.final_state != nullptr || a.init != nullptr)
+                            e = next_episode(a.ends, e, a.episodes, tokens, t0 + i);
+                    }
+                    if (a.init != nullptr && e < a.episodes) {
+                        load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < L::kPairs; ++q) h[q] = f2_of(0.0f, 0.0f);
+                    }
+                }
+                step(i);
+            }
+        }
+        __syncthreads();
+        T* out = static_cast<T*>(a.out) + b.ch0 + Ti::col();
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j) {
+            const int r = Ti::row(j);
+            if (r >= rows || Ti::col() >= b.count) continue;
+            float y[Ti::V];
+#pragma unroll
+            for (int i = 0; i < Ti::V; ++i) {
+                y[i] = s.y[r][Ti::col() + i];
+                if (a.in.d != nullptr) y[i] = fmaf(skip[i], x_now.at(j, i), y[i]);
+                if (a.in.z != nullptr) {
+                    const float g = z.at(j, i);
+                    y[i] *= g * sigmoid(g);
+                }
+            }
+            store_vec<T, Ti::V>(out + (int64_t)(t0 + r) * a.out_stride, y);
+        }
+    }
+    if (s.range.closed && end > s0) leave();
+
+    // Episodes without tokens end as they began: every gridDim.x-th 32 of them.
+    if (a.final_state != nullptr) {
+        const int lane = threadIdx.x & 31;
+        for (int64_t base = (int64_t)blockIdx.x * 32; base < a.episodes; base += (int64_t)gridDim.x * 32) {
+            const int64_t at = base + lane;
+            unsigned empty = __ballot_sync(0xffffffffu, at < a.episodes && episode_end(a.ends, (int)at, tokens) <=
+                                                                             episode_start(a.ends, (int)at, tokens));
+            for (; empty; empty &= empty - 1) {
+                const int64_t ep = base + __ffs(empty) - 1;
+                f2 v[L::kPairs];
+#pragma unroll
+                for (int q = 0; q < L::kPairs; ++q) v[q] = f2_of(0.0f, 0.0f);
+                if (a.init != nullptr) load_states<LS, CPT>(v, a.init + ep * row_states, n, p.ch, p.count, p.n0);
+                store_states<LS, CPT>(a.final_state + ep * row_states, v, n, p.ch, p.count, p.n0);
+            }
+        }
+    }
+}
+
+template <typename T, int LS, int CPT>
+cudaError_t go(const Launch& a, const Cut& c, cudaStream_t st) {
+    static std::atomic<uint64_t> tail_done{0}, done{0};
+    const dim3 grid((unsigned)c.n_seg, (unsigned)c.blocks);
+    cudaError_t e = opt_in_once(scan_forward_kernel<T, LS, CPT>, 0, done);
+    if (c.n_seg > 1) {
+        if (e == cudaSuccess) e = opt_in_once(scan_tail_kernel<T, LS, CPT>, 0, tail_done);
+        if (e == cudaSuccess) e = launch_pdl(scan_tail_kernel<T, LS, CPT>, grid, dim3(kThreads), 0, st, a);
+        if (e == cudaSuccess) e = launch_carry(a, false, st);
+    }
+    if (e == cudaSuccess) e = launch_pdl(scan_forward_kernel<T, LS, CPT>, grid, dim3(kThreads), 0, st, a);
+    return e;
+}
+
+template <typename T>
+cudaError_t run(const Launch& a, const Cut& c, cudaStream_t st) {
+    const bool wide = c.cpt > 1;
+    switch (c.ls) {
+        case 1: return go<T, 1, 1>(a, c, st);
+        case 2: return wide ? go<T, 2, 2>(a, c, st) : go<T, 2, 1>(a, c, st);
+        case 4: return wide ? go<T, 4, 4>(a, c, st) : go<T, 4, 1>(a, c, st);
+        case 8: return wide ? go<T, 8, 4>(a, c, st) : go<T, 8, 1>(a, c, st);
+        default: return wide ? go<T, 16, 4>(a, c, st) : go<T, 16, 1>(a, c, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_carry(const Launch& a, bool backward, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = opt_in_once(scan_carry_kernel, 0, done);
+    const int64_t states = (int64_t)a.shape.channels * a.shape.state_dim;
+    if (e == cudaSuccess)
+        e = launch_pdl(scan_carry_kernel, dim3((unsigned)((states + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a,
+                       (int)backward);
+    return e;
+}
+
+cudaError_t launch_forward(const Launch& a, const Cut& c, cudaStream_t st) {
+    return a.shape.dtype == OFRL_DTYPE_F32 ? run<float>(a, c, st) : run<__nv_bfloat16>(a, c, st);
+}
+
+}  // namespace scan
+}  // namespace ofrl
