@@ -8,8 +8,7 @@
 // e w u) come from one read of it, which stays in registers until its outputs
 // are written, so each tensor moves once.  Bound by HBM.
 //
-// A group of channels has up to 32 lanes of a warp, or a whole CTA, at most 16
-// elements a thread.  Threads keep their columns over the rows they take, so
+// A group of channels has up to 32 lanes of a warp, or a whole CTA.  Threads keep their columns over the rows they take, so
 // a weight's gradient is a register until the end; then it is added over the
 // CTA, and by a second launch over the CTAs, in a fixed order.
 
@@ -28,13 +27,14 @@ struct ofrl_norm {
     void* base;          // the single cudaMalloc of the context
     int64_t bytes;
     float* parts;        // gradients: [2][CTAs over rows][channels]
+    int per_sm[2][2];    // CTAs an SM holds: [residual, gated][forward, backward]
 };
 
 namespace ofrl {
 namespace {
 
 constexpr int kWarpThreads = 128;        // of a CTA that has a warp or less for a group
-constexpr int kMaxParts = 2048;          // CTAs over rows of a backward call, at most
+constexpr int kMaxParts = 4096;          // CTAs over rows, at most
 
 struct NormArgs {
     const void* x;
@@ -66,21 +66,19 @@ struct NormArgs {
     int channels;
 };
 
-// Vectors of a thread, at most: 16 elements, which with their gradients and
-// weights stay in registers.
-constexpr int most_vecs(int elem) { return elem == 2 ? 2 : 4; }
-
-// What a launch's threads are to its rows.
+// What a launch's threads are to its rows.  A thread has eight elements of a row,
+// so that these, the next row's and a weight's gradient stay in registers; rows
+// of more than 4096 channels have sixteen, and no row ahead.
 struct NormCut {
     bool cta;
     int threads, tg, nv, groups_at_once;
 };
 NormCut norm_cut(int width, int elem) {
-    const int vecs = width * elem / 16, most = most_vecs(elem);
+    const int vecs = width * elem / 16, usual = elem == 2 ? 1 : 2;
     NormCut c;
-    c.cta = vecs > 32 * most;
+    c.cta = vecs > 32 * usual;
     c.tg = c.cta ? 64 : 1;
-    while (c.cta ? c.tg * most < vecs : c.tg < 32 && c.tg < vecs) c.tg *= 2;
+    while (c.cta ? c.tg < 512 && c.tg * usual < vecs : c.tg < 32 && c.tg < vecs) c.tg *= 2;
     c.threads = c.cta ? c.tg : kWarpThreads;
     const int nv = (vecs + c.tg - 1) / c.tg;
     c.nv = nv <= 1 ? 1 : nv <= 2 ? 2 : 4;
@@ -114,42 +112,41 @@ __device__ __forceinline__ void sum_group(float& a, float& b, int tg) {
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
-// NV vectors of V elements a thread, zero past the group's width.
+// A thread's part of a row of S: NV times V elements, raw, zero past the group's
+// width.  V is the vector of the row's narrower type, so fp32 beside bf16 takes two loads
+// of 16 bytes for each.
 template <typename S, int V, int NV>
-__device__ __forceinline__ void load_row(float (&v)[NV][V], const void* base, int64_t at, int lane, int tg, int width,
-                                         bool on) {
-    const S* p = static_cast<const S*>(base) + at;
+struct Part {
+    static constexpr int kPiece = V < 16 / (int)sizeof(S) ? V : 16 / (int)sizeof(S), kPieces = V / kPiece;
+    Vec<S, kPiece> v[NV][kPieces];
+    __device__ void load(const void* base, int64_t at, int lane, int tg, int width, bool on) {
+        const S* p = static_cast<const S*>(base) + at;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (lane + j * tg) * V;
-        if (on && c < width) {
-            if constexpr (V * sizeof(S) == 32) {
-                load_vec<S, 4>(*reinterpret_cast<float(*)[4]>(&v[j][0]), p + c);
-                load_vec<S, 4>(*reinterpret_cast<float(*)[4]>(&v[j][4]), p + c + 4);
+        for (int j = 0; j < NV; ++j) {
+            const int c = (lane + j * tg) * V;
+            if (on && c < width) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) v[j][i] = *reinterpret_cast<const Vec<S, kPiece>*>(p + c + i * kPiece);
             } else {
-                load_vec<S, V>(v[j], p + c);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[j][i / kPiece].v[i % kPiece] = from_float<S>(0.0f);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[j][k] = 0.0f;
         }
     }
-}
-template <typename S, int V, int NV>
-__device__ __forceinline__ void store_row(void* base, int64_t at, const float (&v)[NV][V], int lane, int tg, int width) {
-    S* p = static_cast<S*>(base) + at;
+    __device__ void store(void* base, int64_t at, int lane, int tg, int width) const {
+        S* p = static_cast<S*>(base) + at;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (lane + j * tg) * V;
-        if (c >= width) continue;
-        if constexpr (V * sizeof(S) == 32) {
-            store_vec<S, 4>(p + c, *reinterpret_cast<const float(*)[4]>(&v[j][0]));
-            store_vec<S, 4>(p + c + 4, *reinterpret_cast<const float(*)[4]>(&v[j][4]));
-        } else {
-            store_vec<S, V>(p + c, v[j]);
+        for (int j = 0; j < NV; ++j) {
+            const int c = (lane + j * tg) * V;
+            if (c >= width) continue;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) *reinterpret_cast<Vec<S, kPiece>*>(p + c + i * kPiece) = v[j][i];
         }
     }
-}
+    // elements 2 k and 2 k + 1 of vector j
+    __device__ f2 pair(int j, int k) const { return vec_pair(v[j][2 * k / kPiece], k % (kPiece / 2)); }
+    __device__ void set(int j, int k, f2 x) { set_vec_pair(v[j][2 * k / kPiece], k % (kPiece / 2), x); }
+};
 
 // The thread's place: which rows, which columns.
 template <bool CTA>
@@ -168,38 +165,65 @@ __device__ __forceinline__ float rstd_of(float squares, const NormArgs& a) {
     return rsqrtf(squares / (float)a.width + a.eps);
 }
 
+// Rows go by with the next one's loads in flight where AHEAD: fetch(row, on)
+// loads, body(row, on) starts with a copy of what was loaded and then calls the
+// function it is given.
+template <bool AHEAD, bool CTA, typename Fetch, typename Body>
+__device__ __forceinline__ void for_rows(const NormArgs& a, const Seat<CTA>& s, const Fetch& fetch, const Body& body) {
+    const int64_t step = (int64_t)gridDim.x * s.at_once;
+    int64_t row0 = (int64_t)blockIdx.x * s.at_once;
+    if (AHEAD) fetch(row0 + s.seat, row0 + s.seat < a.rows);
+    for (; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + s.seat, after = row + step;
+        if (!AHEAD) fetch(row, row < a.rows);
+        body(row, row < a.rows, [&]() {
+            if (AHEAD) fetch(after, after < a.rows);
+        });
+    }
+}
+template <typename T, int NV>
+constexpr bool kRowAhead = NV * kVec<T> <= 8;
+
 template <typename T, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    float w[NV][V];
-    load_row<float, V, NV>(w, a.weight, s.col0, s.lane, a.tg, a.width, true);
-    for (int64_t row0 = (int64_t)blockIdx.x * s.at_once; row0 < a.rows; row0 += (int64_t)gridDim.x * s.at_once) {
-        const int64_t row = row0 + s.seat;
-        const bool on = row < a.rows;
-        float x[NV][V], z[NV][V];
-        load_row<T, V, NV>(x, a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<T, V, NV>(z, a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
-        float sq = 0.0f, none = 0.0f;
+    Part<float, V, NV> w;
+    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
+    Part<T, V, NV> next_x, next_z;
+    auto fetch = [&](int64_t row, bool on) {
+        next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_z.load(a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
+    };
+    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+        Part<T, V, NV> x = next_x, z = next_z;
+        loaded();
+        f2 u[NV][V / 2], g[NV][V / 2], sq = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float gate = z[j][k] * sigmoid(z[j][k]);
-                if (a.gate_first) x[j][k] *= gate;
-                z[j][k] = a.gate_first ? w[j][k] : w[j][k] * gate;
-                sq = fmaf(x[j][k], x[j][k], sq);
+            for (int k = 0; k < V / 2; ++k) {
+                u[j][k] = x.pair(j, k);
+                g[j][k] = silu(z.pair(j, k));
+                if (a.gate_first) {
+                    u[j][k] = f2_mul(u[j][k], g[j][k]);
+                    g[j][k] = w.pair(j, k);
+                } else {
+                    g[j][k] = f2_mul(g[j][k], w.pair(j, k));
+                }
+                sq = f2_fma(u[j][k], u[j][k], sq);
             }
-        sum_group<CTA>(sq, none, a.tg);
-        const float r = rstd_of(sq, a);
+        float sum = f2_sum(sq), none = 0.0f;
+        sum_group<CTA>(sum, none, a.tg);
+        const f2 r = f2_both(rstd_of(sum, a));
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[j][k] = x[j][k] * r * z[j][k];
-        if (on) store_row<T, V, NV>(a.out, row * a.out_stride + s.col0, x, s.lane, a.tg, a.width);
-    }
+            for (int k = 0; k < V / 2; ++k) x.set(j, k, f2_mul(f2_mul(u[j][k], r), g[j][k]));
+        if (on) x.store(a.out, row * a.out_stride + s.col0, s.lane, a.tg, a.width);
+    });
 }
 
 // T: x and out, R: the residual.
@@ -209,47 +233,52 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_kernel
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    float w[NV][V], scale[NV][V];
-    load_row<float, V, NV>(w, a.weight, s.col0, s.lane, a.tg, a.width, true);
-    if (a.scale != nullptr) load_row<float, V, NV>(scale, a.scale, s.col0, s.lane, a.tg, a.width, true);
-    for (int64_t row0 = (int64_t)blockIdx.x * s.at_once; row0 < a.rows; row0 += (int64_t)gridDim.x * s.at_once) {
-        const int64_t row = row0 + s.seat;
-        const bool on = row < a.rows;
-        float x[NV][V], h[NV][V];
-        load_row<T, V, NV>(x, a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<R, V, NV>(h, a.residual, row * a.residual_stride + s.col0, s.lane, a.tg, a.width, on);
-        float sq = 0.0f, none = 0.0f;
+    Part<float, V, NV> w, scale;
+    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
+    if (a.scale != nullptr) scale.load(a.scale, s.col0, s.lane, a.tg, a.width, true);
+    Part<T, V, NV> next_x;
+    Part<R, V, NV> next_h;
+    auto fetch = [&](int64_t row, bool on) {
+        next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_h.load(a.residual, row * a.residual_stride + s.col0, s.lane, a.tg, a.width, on);
+    };
+    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+        Part<T, V, NV> x = next_x;
+        Part<R, V, NV> res = next_h;
+        loaded();
+        f2 h[NV][V / 2], sq = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                h[j][k] = a.scale != nullptr ? fmaf(scale[j][k], x[j][k], h[j][k]) : h[j][k] + x[j][k];
-                sq = fmaf(h[j][k], h[j][k], sq);
+            for (int k = 0; k < V / 2; ++k) {
+                h[j][k] = a.scale != nullptr ? f2_fma(scale.pair(j, k), x.pair(j, k), res.pair(j, k))
+                                             : f2_add(x.pair(j, k), res.pair(j, k));
+                sq = f2_fma(h[j][k], h[j][k], sq);
+                res.set(j, k, h[j][k]);
             }
-        if (on) store_row<R, V, NV>(a.residual_out, row * a.residual_out_stride + s.col0, h, s.lane, a.tg, a.width);
-        sum_group<CTA>(sq, none, a.tg);
-        const float r = rstd_of(sq, a);
+        if (on) res.store(a.residual_out, row * a.residual_out_stride + s.col0, s.lane, a.tg, a.width);
+        float sum = f2_sum(sq), none = 0.0f;
+        sum_group<CTA>(sum, none, a.tg);
+        const f2 r = f2_both(rstd_of(sum, a));
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) h[j][k] = h[j][k] * r * w[j][k];
-        if (on) store_row<T, V, NV>(a.out, row * a.out_stride + s.col0, h, s.lane, a.tg, a.width);
-    }
+            for (int k = 0; k < V / 2; ++k) x.set(j, k, f2_mul(f2_mul(h[j][k], r), w.pair(j, k)));
+        if (on) x.store(a.out, row * a.out_stride + s.col0, s.lane, a.tg, a.width);
+    });
 }
 
 // A column's gradient over the CTA's seats, to the CTA's place in parts.
 template <int V, int NV, bool CTA>
-__device__ __forceinline__ void put_parts(const NormArgs& a, const Seat<CTA>& s, float (&g)[NV][V], int which, float* red) {
+__device__ __forceinline__ void put_parts(const NormArgs& a, const Seat<CTA>& s, const Part<float, V, NV>& g, int which,
+                                          float* red) {
     float* out = a.parts + ((int64_t)which * gridDim.x + blockIdx.x) * a.channels + s.col0;
     if constexpr (CTA) {
-        store_row<float, V, NV>(out, 0, g, s.lane, a.tg, a.width);
+        g.store(out, 0, s.lane, a.tg, a.width);
     } else {
         __syncthreads();
         const int row = a.tg * NV * V;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int k = 0; k < V; ++k) red[s.seat * row + (s.lane + j * a.tg) * V + k] = g[j][k];
+        g.store(red, s.seat * row, s.lane, a.tg, row);
         __syncthreads();
         for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
             float v = 0.0f;
@@ -262,111 +291,127 @@ __device__ __forceinline__ void put_parts(const NormArgs& a, const Seat<CTA>& s,
 template <typename T, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
-    __shared__ float red[CTA ? 1 : kWarpThreads * NV * V];
+    __shared__ __align__(16) float red[CTA ? 4 : kWarpThreads * NV * V];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    float w[NV][V], dw[NV][V];
-    load_row<float, V, NV>(w, a.weight, s.col0, s.lane, a.tg, a.width, true);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < V; ++k) dw[j][k] = 0.0f;
-    for (int64_t row0 = (int64_t)blockIdx.x * s.at_once; row0 < a.rows; row0 += (int64_t)gridDim.x * s.at_once) {
-        const int64_t row = row0 + s.seat;
-        const bool on = row < a.rows;
-        float x[NV][V], z[NV][V], g[NV][V];
-        load_row<T, V, NV>(x, a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<T, V, NV>(z, a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<T, V, NV>(g, a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
-        float sq = 0.0f, dot = 0.0f;
+    Part<float, V, NV> w, dw;
+    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
+    dw.load(a.weight, 0, s.lane, a.tg, a.width, false);      // zero
+    Part<T, V, NV> next_x, next_z, next_g;
+    auto fetch = [&](int64_t row, bool on) {
+        next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_z.load(a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_g.load(a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
+    };
+    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+        Part<T, V, NV> x = next_x, z = next_z, g = next_g;
+        loaded();
+        f2 sq = f2_both(0.0f), ip = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float gate = z[j][k] * sigmoid(z[j][k]);
-                const float u = a.gate_first ? x[j][k] * gate : x[j][k], e = a.gate_first ? g[j][k] : g[j][k] * gate;
-                sq = fmaf(u, u, sq);
-                dot = fmaf(e * w[j][k], u, dot);
+            for (int k = 0; k < V / 2; ++k) {
+                const f2 gate = silu(z.pair(j, k));
+                f2 u = x.pair(j, k), e = g.pair(j, k);
+                if (a.gate_first)
+                    u = f2_mul(u, gate);
+                else
+                    e = f2_mul(e, gate);
+                sq = f2_fma(u, u, sq);
+                ip = f2_fma(f2_mul(e, w.pair(j, k)), u, ip);
             }
-        sum_group<CTA>(sq, dot, a.tg);
-        const float r = rstd_of(sq, a), back = r * r * dot / (float)a.width;
+        float sum = f2_sum(sq), dot = f2_sum(ip);
+        sum_group<CTA>(sum, dot, a.tg);
+        const float rs = rstd_of(sum, a);
+        const f2 r = f2_both(rs), back = f2_both(-rs * rs * dot / (float)a.width);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float sg = sigmoid(z[j][k]), gate = z[j][k] * sg;
-                const float u = a.gate_first ? x[j][k] * gate : x[j][k], e = a.gate_first ? g[j][k] : g[j][k] * gate;
-                const float unit = u * r, du = r * fmaf(e, w[j][k], -u * back);
-                dw[j][k] = fmaf(e, unit, dw[j][k]);
-                const float dgate = a.gate_first ? du * x[j][k] : g[j][k] * unit * w[j][k];
-                x[j][k] = a.gate_first ? du * gate : du;
-                z[j][k] = dgate * sg * (1.0f + z[j][k] * (1.0f - sg));
+            for (int k = 0; k < V / 2; ++k) {
+                const f2 zv = z.pair(j, k), sg = sigmoid(zv), gate = f2_mul(zv, sg), wv = w.pair(j, k), xv = x.pair(j, k);
+                f2 u = xv, e = g.pair(j, k), dgate;
+                if (a.gate_first)
+                    u = f2_mul(u, gate);
+                else
+                    e = f2_mul(e, gate);
+                const f2 unit = f2_mul(u, r), du = f2_mul(r, f2_fma(e, wv, f2_mul(u, back)));
+                dw.set(j, k, f2_fma(e, unit, dw.pair(j, k)));
+                dgate = a.gate_first ? f2_mul(du, xv) : f2_mul(f2_mul(g.pair(j, k), unit), wv);
+                x.set(j, k, a.gate_first ? f2_mul(du, gate) : du);
+                z.set(j, k, f2_mul(dgate, silu_slope(zv, sg)));
             }
         if (on) {
-            store_row<T, V, NV>(a.dx, row * a.dx_stride + s.col0, x, s.lane, a.tg, a.width);
-            store_row<T, V, NV>(a.dz, row * a.dz_stride + s.col0, z, s.lane, a.tg, a.width);
+            x.store(a.dx, row * a.dx_stride + s.col0, s.lane, a.tg, a.width);
+            z.store(a.dz, row * a.dz_stride + s.col0, s.lane, a.tg, a.width);
         }
-    }
+    });
     put_parts<V, NV, CTA>(a, s, dw, 0, red);
 }
 
 template <typename T, typename R, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
-    __shared__ float red[CTA ? 1 : kWarpThreads * NV * V];
+    __shared__ __align__(16) float red[CTA ? 4 : kWarpThreads * NV * V];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    float w[NV][V], scale[NV][V], dw[NV][V], ds[NV][V];
-    load_row<float, V, NV>(w, a.weight, s.col0, s.lane, a.tg, a.width, true);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            dw[j][k] = ds[j][k] = 0.0f;
-            scale[j][k] = 1.0f;
-        }
-    if (a.scale != nullptr) load_row<float, V, NV>(scale, a.scale, s.col0, s.lane, a.tg, a.width, true);
-    for (int64_t row0 = (int64_t)blockIdx.x * s.at_once; row0 < a.rows; row0 += (int64_t)gridDim.x * s.at_once) {
-        const int64_t row = row0 + s.seat;
-        const bool on = row < a.rows;
-        float x[NV][V], h[NV][V], g[NV][V], dh[NV][V];
-        load_row<T, V, NV>(x, a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<R, V, NV>(h, a.residual, row * a.residual_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<T, V, NV>(g, a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
-        load_row<R, V, NV>(dh, a.dres, row * a.dres_stride + s.col0, s.lane, a.tg, a.width, on && a.dres != nullptr);
-        float sq = 0.0f, dot = 0.0f;
+    Part<float, V, NV> w, scale, dw, ds;
+    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
+    if (a.scale != nullptr) scale.load(a.scale, s.col0, s.lane, a.tg, a.width, true);
+    dw.load(a.weight, 0, s.lane, a.tg, a.width, false);      // zero
+    ds.load(a.weight, 0, s.lane, a.tg, a.width, false);
+    Part<T, V, NV> next_x, next_g;
+    Part<R, V, NV> next_h, next_d;
+    auto fetch = [&](int64_t row, bool on) {
+        next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_h.load(a.residual, row * a.residual_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_g.load(a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
+        next_d.load(a.dres, row * a.dres_stride + s.col0, s.lane, a.tg, a.width, on && a.dres != nullptr);
+    };
+    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+        Part<T, V, NV> x = next_x, g = next_g;
+        Part<R, V, NV> res = next_h, d = next_d;
+        loaded();
+        f2 h[NV][V / 2], sq = f2_both(0.0f), ip = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                h[j][k] = fmaf(scale[j][k], x[j][k], h[j][k]);
-                sq = fmaf(h[j][k], h[j][k], sq);
-                dot = fmaf(g[j][k] * w[j][k], h[j][k], dot);
+            for (int k = 0; k < V / 2; ++k) {
+                h[j][k] = a.scale != nullptr ? f2_fma(scale.pair(j, k), x.pair(j, k), res.pair(j, k))
+                                             : f2_add(x.pair(j, k), res.pair(j, k));
+                sq = f2_fma(h[j][k], h[j][k], sq);
+                ip = f2_fma(f2_mul(g.pair(j, k), w.pair(j, k)), h[j][k], ip);
             }
-        sum_group<CTA>(sq, dot, a.tg);
-        const float r = rstd_of(sq, a), back = r * r * dot / (float)a.width;
+        float sum = f2_sum(sq), dot = f2_sum(ip);
+        sum_group<CTA>(sum, dot, a.tg);
+        const float rs = rstd_of(sum, a);
+        const f2 r = f2_both(rs), back = f2_both(-rs * rs * dot / (float)a.width);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                dh[j][k] = fmaf(r, fmaf(g[j][k], w[j][k], -h[j][k] * back), dh[j][k]);
-                dw[j][k] = fmaf(g[j][k], h[j][k] * r, dw[j][k]);
-                ds[j][k] = fmaf(dh[j][k], x[j][k], ds[j][k]);
-                x[j][k] = scale[j][k] * dh[j][k];
+            for (int k = 0; k < V / 2; ++k) {
+                const f2 gv = g.pair(j, k), dh = f2_fma(r, f2_fma(gv, w.pair(j, k), f2_mul(h[j][k], back)), d.pair(j, k));
+                dw.set(j, k, f2_fma(gv, f2_mul(h[j][k], r), dw.pair(j, k)));
+                if (a.scale != nullptr) {
+                    ds.set(j, k, f2_fma(dh, x.pair(j, k), ds.pair(j, k)));
+                    x.set(j, k, f2_mul(scale.pair(j, k), dh));
+                } else {
+                    x.set(j, k, dh);
+                }
+                d.set(j, k, dh);
             }
         if (on) {
-            store_row<T, V, NV>(a.dx, row * a.dx_stride + s.col0, x, s.lane, a.tg, a.width);
-            store_row<R, V, NV>(a.dresidual, row * a.dresidual_stride + s.col0, dh, s.lane, a.tg, a.width);
+            x.store(a.dx, row * a.dx_stride + s.col0, s.lane, a.tg, a.width);
+            d.store(a.dresidual, row * a.dresidual_stride + s.col0, s.lane, a.tg, a.width);
         }
-    }
+    });
     put_parts<V, NV, CTA>(a, s, dw, 0, red);
     if (a.scale != nullptr) put_parts<V, NV, CTA>(a, s, ds, 1, red);
 }
 
-// Weight gradients over the CTAs: 32 columns a CTA, eight threads to a column.
-constexpr int kJoinThreads = 256, kSlices = kJoinThreads / 32;
+// Weight gradients over the CTAs: 32 columns a CTA, 32 threads to a column.
+constexpr int kJoinThreads = 1024, kSlices = kJoinThreads / 32;
 struct NormJoin {
     const float* parts;
     int n_parts, channels;
@@ -402,12 +447,11 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const __grid_co
 
 using NormKernel = void (*)(NormArgs);
 
-// CTAs over rows: enough to fill the SMs, no more than there is work.
-int rows_grid(const NormArgs& a, const NormCut& c, int groups, int num_sms, bool backward) {
-    const int64_t all = (a.rows + c.groups_at_once - 1) / c.groups_at_once;
-    const int64_t per_sm = backward ? 2048 / c.threads / 4 : 2048 / c.threads;
+// CTAs over rows: what the GPU holds at once, no more than there is work.
+int rows_grid(int64_t rows, const NormCut& c, int groups, int num_sms, int per_sm) {
+    const int64_t all = (rows + c.groups_at_once - 1) / c.groups_at_once;
     int64_t most = ((int64_t)num_sms * per_sm + groups - 1) / groups;
-    if (backward && most > kMaxParts) most = kMaxParts;
+    if (most > kMaxParts) most = kMaxParts;
     return (int)(all < 1 ? 1 : all < most ? all : most);
 }
 
@@ -506,11 +550,11 @@ ofrl_status run_forward(const ofrl_norm* ctx, const NormCut& c, const NormArgs& 
     if (a.rows == 0) return OFRL_OK;
     const int groups = ctx->shape.groups;
     return cuda_status(launch_rows(forward_kernel(ctx->shape, c, gated), a, c, groups,
-                                   rows_grid(a, c, groups, ctx->num_sms, false), st));
+                                   rows_grid(a.rows, c, groups, ctx->num_sms, ctx->per_sm[gated][0]), st));
 }
 ofrl_status run_backward(const ofrl_norm* ctx, const NormCut& c, const NormArgs& a, bool gated, float* dweight,
                          float* dscale, cudaStream_t st) {
-    const int groups = ctx->shape.groups, grid = rows_grid(a, c, groups, ctx->num_sms, true);
+    const int groups = ctx->shape.groups, grid = rows_grid(a.rows, c, groups, ctx->num_sms, ctx->per_sm[gated][1]);
     cudaError_t e = launch_rows(backward_kernel(ctx->shape, c, gated), a, c, groups, grid, st);
     if (e == cudaSuccess) {
         NormJoin j;
@@ -525,13 +569,22 @@ ofrl_status run_backward(const ofrl_norm* ctx, const NormCut& c, const NormArgs&
     return cuda_status(e);
 }
 
-int64_t norm_bytes(const ofrl_norm_shape& s, int num_sms, bool backward) {
+int64_t norm_bytes(const ofrl_norm_shape& s, int num_sms, int per_sm, bool backward) {
     if (!backward) return 256;
     const NormCut c = norm_cut(s.channels / s.groups, (int)dtype_size(s.dtype));
-    NormArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.rows = INT32_MAX;
-    return 256 + 2 * (int64_t)rows_grid(a, c, s.groups, num_sms, true) * s.channels * 4;
+    return 256 + 2 * (int64_t)rows_grid(INT32_MAX, c, s.groups, num_sms, per_sm) * s.channels * 4;
+}
+// CTAs of each kernel that an SM holds.
+cudaError_t find_per_sm(const ofrl_norm_shape& s, int (&per_sm)[2][2]) {
+    const NormCut c = norm_cut(s.channels / s.groups, (int)dtype_size(s.dtype));
+    cudaError_t e = cudaSuccess;
+    for (int gated = 0; gated < 2; ++gated)
+        for (int back = 0; back < 2; ++back) {
+            NormKernel k = back ? backward_kernel(s, c, gated != 0) : forward_kernel(s, c, gated != 0);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[gated][back], k, c.threads, 0);
+            if (per_sm[gated][back] < 1) per_sm[gated][back] = 1;
+        }
+    return e;
 }
 
 }  // namespace
@@ -543,9 +596,13 @@ extern "C" {
 
 int64_t ofrl_norm_workspace_bytes(const ofrl_norm_shape* shape, int32_t backward) {
     if (check_shape(shape) != OFRL_OK || (backward != 0 && backward != 1)) return -1;
-    int device = 0;
+    int device = 0, per_sm[2][2] = {};
     const int sms = current_sms(&device);
-    return norm_bytes(*shape, sms > 0 ? sms : 1, backward != 0);
+    if (sms == 0 || find_per_sm(*shape, per_sm) != cudaSuccess) {      // no GPU to be asked
+        cudaGetLastError();
+        return norm_bytes(*shape, 1, 1, backward != 0);
+    }
+    return norm_bytes(*shape, sms, per_sm[0][1] > per_sm[1][1] ? per_sm[0][1] : per_sm[1][1], backward != 0);
 }
 
 ofrl_status ofrl_norm_create(const ofrl_norm_shape* shape, int32_t backward, ofrl_norm** out) {
@@ -560,8 +617,14 @@ ofrl_status ofrl_norm_create(const ofrl_norm_shape* shape, int32_t backward, ofr
     ctx->num_sms = current_sms(&ctx->device);
     ctx->shape = *shape;
     ctx->backward = backward;
-    if (ctx->num_sms > 0) ctx->bytes = norm_bytes(*shape, ctx->num_sms, backward != 0);
-    if (ctx->num_sms == 0 || take_memory(&ctx->base, ctx->bytes) != cudaSuccess) {
+    if (ctx->num_sms == 0 || find_per_sm(*shape, ctx->per_sm) != cudaSuccess) {
+        cudaGetLastError();
+        delete ctx;
+        return OFRL_ECUDA;
+    }
+    ctx->bytes = norm_bytes(*shape, ctx->num_sms, ctx->per_sm[0][1] > ctx->per_sm[1][1] ? ctx->per_sm[0][1] : ctx->per_sm[1][1],
+                            backward != 0);
+    if (take_memory(&ctx->base, ctx->bytes) != cudaSuccess) {
         delete ctx;
         return OFRL_ECUDA;
     }

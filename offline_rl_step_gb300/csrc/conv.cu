@@ -34,9 +34,11 @@ namespace ofrl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;      // channels of a thread
+// Channels of a thread: 16 bytes of them forward, four for gradients, whose
+// taps, windows and sums would not stay in registers.
+constexpr int vec_of(int elem, bool backward) { return elem == 4 || backward ? 4 : 8; }
 constexpr int kMinRun = 8, kMaxRun = 64;
-constexpr int kMaskWords = kThreads * kMaxRun / 32 + 2;
+constexpr int kMaskWords = kThreads * kMaxRun / 32 + 4;
 
 struct ConvLaunch {
     ofrl_conv_shape shape;
@@ -76,9 +78,9 @@ struct ConvCut {
     int lanes, run, cols;      // cols: CTAs along a row
     int64_t rows;              // CTAs over the tokens, at least 1
 };
-ConvCut conv_cut(int channels, int64_t tokens, int num_sms) {
+ConvCut conv_cut(int channels, int vec, int64_t tokens, int num_sms) {
     ConvCut c;
-    const int vecs = channels / kVec;
+    const int vecs = channels / vec;
     c.lanes = 1;
     while (c.lanes < 32 && c.lanes < vecs) c.lanes *= 2;
     c.cols = (vecs + c.lanes - 1) / c.lanes;
@@ -91,8 +93,8 @@ ConvCut conv_cut(int channels, int64_t tokens, int num_sms) {
 }
 // CTAs over the tokens of any call of at most max_tokens: at the longest run, or
 // no more than the target.
-int64_t conv_rows_most(int channels, int64_t max_tokens, int num_sms) {
-    const ConvCut c = conv_cut(channels, max_tokens, num_sms);
+int64_t conv_rows_most(int channels, int vec, int64_t max_tokens, int num_sms) {
+    const ConvCut c = conv_cut(channels, vec, max_tokens, num_sms);
     const int64_t runs = kThreads / c.lanes, target = (int64_t)num_sms * 8 / c.cols + 1;
     const int64_t longest = (max_tokens + runs * kMaxRun - 1) / (runs * kMaxRun),
                   shortest = (max_tokens + runs * kMinRun - 1) / (runs * kMinRun);
@@ -100,13 +102,9 @@ int64_t conv_rows_most(int channels, int64_t max_tokens, int num_sms) {
     return longest > few ? longest : few > 1 ? few : 1;
 }
 
-__device__ __forceinline__ float act_of(float pre, int activation) {
-    return activation == OFRL_ACT_SILU ? pre * sigmoid(pre) : pre;
-}
-__device__ __forceinline__ float act_slope(float pre, int activation) {
-    if (activation != OFRL_ACT_SILU) return 1.0f;
-    const float s = sigmoid(pre);
-    return s * (1.0f + pre * (1.0f - s));
+__device__ __forceinline__ f2 act_of(f2 pre, int activation) { return activation == OFRL_ACT_SILU ? silu(pre) : pre; }
+__device__ __forceinline__ f2 act_slope(f2 pre, int activation) {
+    return activation == OFRL_ACT_SILU ? silu_slope(pre, sigmoid(pre)) : f2_both(1.0f);
 }
 
 // The first episode that ends after token t; one thread.
@@ -128,6 +126,11 @@ struct Marks {
     int m0;              // the token of bit 0
     Range range;         // of [m0, ..)
     __device__ bool starts(int t) const { return mask[(t - m0) >> 5] >> ((t - m0) & 31) & 1; }
+    // bit i: token t + i begins an episode, for 32 tokens from t >= m0 on
+    __device__ uint32_t from(int t) const {
+        const int o = t - m0;
+        return __funnelshift_r(mask[o >> 5], mask[(o >> 5) + 1], o & 31);
+    }
     // token t, below range.end, is its episode's last
     __device__ bool last(int t) const { return t + 1 < range.end ? starts(t + 1) : range.closed != 0; }
 };
@@ -155,58 +158,71 @@ __device__ __forceinline__ void make_marks(Marks& m, const ConvLaunch& a, int s0
 // Inputs that a run carries along: win[i] stands W - 1 - i tokens back.
 template <typename T, int V, int W>
 struct Window {
-    float win[W - 1][V];
+    f2 win[W - 1][V / 2];
     __device__ void clear() {
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k) win[i][k] = 0.0f;
+            for (int k = 0; k < V / 2; ++k) win[i][k] = f2_both(0.0f);
     }
-    __device__ void push(const float (&x)[V]) {
+    __device__ void push(const f2 (&x)[V / 2]) {
 #pragma unroll
         for (int i = 0; i + 1 < W - 1; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k) win[i][k] = win[i + 1][k];
+            for (int k = 0; k < V / 2; ++k) win[i][k] = win[i + 1][k];
 #pragma unroll
-        for (int k = 0; k < V; ++k) win[W - 2][k] = x[k];
+        for (int k = 0; k < V / 2; ++k) win[W - 2][k] = x[k];
     }
+    // token t begins an episode
     __device__ void enter(const ConvLaunch& a, int t, int ch) {
         clear();
         if (a.init == nullptr) return;
         const int e = episode_at(a.ends, a.episodes, (int)a.in.tokens, t);
         const T* p = static_cast<const T*>(a.init) + ((int64_t)e * a.shape.channels + ch) * (W - 1);
 #pragma unroll
-        for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V / 2; ++k)
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) win[i][k] = to_float(p[k * (W - 1) + i]);
+            for (int i = 0; i < W - 1; ++i)
+                win[i][k] = f2_of(to_float(p[2 * k * (W - 1) + i]), to_float(p[(2 * k + 1) * (W - 1) + i]));
+    }
+    // token t ends an episode
+    __device__ void leave(const ConvLaunch& a, int t, int ch) const {
+        const int e = episode_at(a.ends, a.episodes, (int)a.in.tokens, t);
+        T* p = static_cast<T*>(a.final_state) + ((int64_t)e * a.shape.channels + ch) * (W - 1);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k)
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                p[2 * k * (W - 1) + i] = from_float<T>(f2_lo(win[i][k]));
+                p[(2 * k + 1) * (W - 1) + i] = from_float<T>(f2_hi(win[i][k]));
+            }
     }
 };
 
 template <int V, int W>
 struct Taps {
-    float w[W][V], bias[V];
+    f2 w[W][V / 2], bias[V / 2];
     __device__ void load(const ConvLaunch& a, int ch) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
+        for (int k = 0; k < V / 2; ++k) {
+            const float* p = a.in.weight + (int64_t)(ch + 2 * k) * W;
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][k] = a.in.weight[(int64_t)(ch + k) * W + j];
-            bias[k] = a.in.bias != nullptr ? a.in.bias[ch + k] : 0.0f;
+            for (int j = 0; j < W; ++j) w[j][k] = f2_of(p[j], p[W + j]);
+            bias[k] = a.in.bias != nullptr ? f2_of(a.in.bias[ch + 2 * k], a.in.bias[ch + 2 * k + 1]) : f2_both(0.0f);
         }
     }
     template <typename T>
-    __device__ float pre(const Window<T, V, W>& win, const float (&x)[V], int k) const {
-        float s = bias[k];
+    __device__ f2 pre(const Window<T, V, W>& win, const f2 (&x)[V / 2], int k) const {
+        f2 s = bias[k];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][k], win.win[j][k], s);
-        return fmaf(w[W - 1][k], x[k], s);
+        for (int j = 0; j < W - 1; ++j) s = f2_fma(w[j][k], win.win[j][k], s);
+        return f2_fma(w[W - 1][k], x[k], s);
     }
 };
 
-constexpr int kAtOnce = 8;      // tokens whose loads are in flight together
-
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_forward_kernel(const __grid_constant__ ConvLaunch a) {
-    constexpr int V = kVec;
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_constant__ ConvLaunch a) {
+    constexpr int kAtOnce = 4;      // tokens of a round; the next round's inputs are on their way meanwhile
     __shared__ Marks m;
     pdl_wait();
     pdl_trigger();
@@ -225,31 +241,43 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(const __grid_con
         win.clear();
         const T* in = static_cast<const T*>(a.in.x) + ch;
         T* out = static_cast<T*>(a.out) + ch;
-        for (int t0 = begin - (W - 1); t0 < end; t0 += kAtOnce) {
-            float x[kAtOnce][V];
+        const int first = max(begin - (W - 1), 0);
+        Vec<T, V> next[kAtOnce];
+        auto fetch = [&](int t0) {
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
-                if (t0 + i >= 0 && t0 + i < end) load_vec<T, V>(x[i], in + (int64_t)(t0 + i) * a.in.x_stride);
+                if (t0 + i < end) next[i] = *reinterpret_cast<const Vec<T, V>*>(in + (int64_t)(t0 + i) * a.in.x_stride);
+        };
+        fetch(first);
+        for (int t0 = first; t0 < end; t0 += kAtOnce) {
+            Vec<T, V> now[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) now[i] = next[i];
+            fetch(t0 + kAtOnce);
+            const uint32_t starts = m.from(t0);
+            auto token = [&](int i) {
+                f2 x[V / 2];
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) x[k] = vec_pair(now[i], k);
+                Vec<T, V> o;
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) set_vec_pair(o, k, act_of(taps.pre(win, x, k), a.shape.activation));
+                if (t0 + i >= begin) *reinterpret_cast<Vec<T, V>*>(out + (int64_t)(t0 + i) * a.out_stride) = o;
+                win.push(x);
+            };
+            // the usual round: whole, within an episode
+            if (t0 + kAtOnce <= end && (starts & ((2u << kAtOnce) - 1)) == 0 && t0 + kAtOnce < m.range.end) {
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) token(i);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 const int t = t0 + i;
-                if (t < 0 || t >= end) continue;
-                if (m.starts(t)) win.enter(a, t, ch);
-                if (t >= begin) {
-                    float o[V];
-#pragma unroll
-                    for (int k = 0; k < V; ++k) o[k] = act_of(taps.pre(win, x[i], k), a.shape.activation);
-                    store_vec<T, V>(out + (int64_t)t * a.out_stride, o);
-                }
-                win.push(x[i]);
-                if (a.final_state != nullptr && t >= begin && m.last(t)) {
-                    const int e = episode_at(a.ends, a.episodes, tokens, t);
-                    T* p = static_cast<T*>(a.final_state) + ((int64_t)e * d + ch) * (W - 1);
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) p[k * (W - 1) + j] = from_float<T>(win.win[j][k]);
-                }
+                if (t >= end) break;
+                if (starts >> i & 1) win.enter(a, t, ch);
+                token(i);
+                if (a.final_state != nullptr && t >= begin && m.last(t)) win.leave(a, t, ch);
             }
         }
     }
@@ -274,8 +302,8 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(const __grid_con
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_grad_kernel(const __grid_constant__ ConvLaunch a) {
-    constexpr int V = kVec, kLoads = 4;
+__global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_constant__ ConvLaunch a) {
+    constexpr int V = vec_of(sizeof(T), true), kAtOnce = sizeof(T) == 4 ? 2 : 4, P = V / 2;
     __shared__ Marks m;
     __shared__ float red[kThreads * V * (W + 1)];
     pdl_wait();
@@ -288,94 +316,143 @@ __global__ void __launch_bounds__(kThreads) conv_grad_kernel(const __grid_consta
     const int64_t begin64 = from + (int64_t)y * a.run;
     const int live = m.range.end;
     const int end = (int)min(begin64 + a.run, (int64_t)live), begin = (int)min(begin64, (int64_t)end);
-    float dw[W + 1][V];      // the taps, then the bias
+    f2 dw[W + 1][P];      // the taps, then the bias
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int k = 0; k < V; ++k) dw[j][k] = 0.0f;
+        for (int k = 0; k < P; ++k) dw[j][k] = f2_both(0.0f);
     if (ch < d && begin < end) {
         Taps<V, W> taps;
         taps.load(a, ch);
         Window<T, V, W> win;
         win.clear();
-        float pend[W - 1][V];      // dx of the W - 1 tokens before, so far
+        f2 pend[W - 1][P];      // dx of the W - 1 tokens before, so far
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int k = 0; k < V; ++k) pend[j][k] = 0.0f;
-        int age = W;               // tokens since the episode began
+            for (int k = 0; k < P; ++k) pend[j][k] = f2_both(0.0f);
+        int age = W;            // tokens since the episode began
         const T* in = static_cast<const T*>(a.in.x) + ch;
         const T* go = static_cast<const T*>(a.dout) + ch;
+        T* out = static_cast<T*>(a.grads.dx) + ch;
         const int stop = (int)min((int64_t)end + W - 1, (int64_t)live);      // dpre of the tokens after the run
-        // one more round for each pending token
-        for (int t0 = begin - (W - 1); t0 < end + W - 1; t0 += kLoads) {
-            float x[kLoads][V], g[kLoads][V];
+        const int first = max(begin - (W - 1), 0);
+        Vec<T, V> next_x[kAtOnce], next_g[kAtOnce];
+        auto fetch = [&](int t0) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int t = t0 + i;
-                if (t >= 0 && t < stop) load_vec<T, V>(x[i], in + (int64_t)t * a.in.x_stride);
-                if (t >= begin && t < stop) load_vec<T, V>(g[i], go + (int64_t)t * a.dout_stride);
+            for (int i = 0; i < kAtOnce; ++i)
+                if (t0 + i < stop) {
+                    next_x[i] = *reinterpret_cast<const Vec<T, V>*>(in + (int64_t)(t0 + i) * a.in.x_stride);
+                    next_g[i] = *reinterpret_cast<const Vec<T, V>*>(go + (int64_t)(t0 + i) * a.dout_stride);
+                }
+        };
+        fetch(first);
+        // W - 1 tokens more than the run: their gradients reach back into it
+        for (int t0 = first; t0 < end + W - 1; t0 += kAtOnce) {
+            Vec<T, V> now_x[kAtOnce], now_g[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                now_x[i] = next_x[i];
+                now_g[i] = next_g[i];
+            }
+            fetch(t0 + kAtOnce);
+            const uint32_t starts = m.from(t0);
+            // a token's own dx is begun, those before it get their share (as far as `reach` back)
+            auto token = [&](int i, int reach, bool sums, f2 (&own)[P]) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    f2 x[P];
+#pragma unroll
+                    for (int c = 0; c < P; ++c) x[c] = vec_pair(now_x[i], c);
+                    const f2 dp = f2_mul(vec_pair(now_g[i], k), act_slope(taps.pre(win, x, k), a.shape.activation));
+                    own[k] = f2_mul(taps.w[W - 1][k], dp);
+#pragma unroll
+                    for (int j = 1; j < W; ++j)
+                        if (j <= reach) pend[W - 1 - j][k] = f2_fma(taps.w[W - 1 - j][k], dp, pend[W - 1 - j][k]);
+                    if (sums) {
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) dw[j][k] = f2_fma(dp, win.win[j][k], dw[j][k]);
+                        dw[W - 1][k] = f2_fma(dp, x[k], dw[W - 1][k]);
+                        dw[W][k] = f2_add(dw[W][k], dp);
+                    }
+                }
+            };
+            auto finish = [&](int t, const f2 (&own)[P]) {      // token t - (W - 1) is complete
+                const int done = t - (W - 1);
+                if (done >= begin && done < end) {
+                    Vec<T, V> o;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) set_vec_pair(o, k, pend[0][k]);
+                    *reinterpret_cast<Vec<T, V>*>(out + (int64_t)done * a.grads.x_stride) = o;
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) pend[j][k] = pend[j + 1][k];
+#pragma unroll
+                for (int k = 0; k < P; ++k) pend[W - 2][k] = own[k];
+            };
+            auto advance = [&](int i) {
+                f2 x[P];
+#pragma unroll
+                for (int k = 0; k < P; ++k) x[k] = vec_pair(now_x[i], k);
+                win.push(x);
+            };
+            // the usual round: whole, within the run and an episode, no gradient of a final state
+            if (t0 >= begin && t0 + kAtOnce <= end && (starts & ((1u << kAtOnce) - 1)) == 0 && a.d_final == nullptr &&
+                age >= W - 1) {
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    f2 own[P];
+                    token(i, W - 1, true, own);
+                    advance(i);
+                    finish(t0 + i, own);
+                }
+                continue;
             }
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
+            for (int i = 0; i < kAtOnce; ++i) {
                 const int t = t0 + i;
-                if (t < 0) continue;
-                float now[V];
+                f2 own[P];
 #pragma unroll
-                for (int k = 0; k < V; ++k) now[k] = 0.0f;
+                for (int k = 0; k < P; ++k) own[k] = f2_both(0.0f);
                 if (t < stop) {
-                    if (m.starts(t)) {
+                    if (starts >> i & 1) {
                         win.enter(a, t, ch);
                         age = 0;
                     }
                     if (t >= begin) {
-#pragma unroll
-                        for (int k = 0; k < V; ++k) {
-                            const float dp = g[i][k] * act_slope(taps.pre(win, x[i], k), a.shape.activation);
-                            now[k] = taps.w[W - 1][k] * dp;
-#pragma unroll
-                            for (int j = 1; j < W; ++j)
-                                if (j <= age) pend[W - 1 - j][k] = fmaf(taps.w[W - 1 - j][k], dp, pend[W - 1 - j][k]);
-                            if (t < end) {
-#pragma unroll
-                                for (int j = 0; j < W - 1; ++j) dw[j][k] = fmaf(dp, win.win[j][k], dw[j][k]);
-                                dw[W - 1][k] = fmaf(dp, x[i][k], dw[W - 1][k]);
-                                dw[W][k] += dp;
-                            }
-                        }
+                        token(i, age, t < end, own);
                         if (a.d_final != nullptr && t < end) {
                             int left = 0;      // tokens of the episode from t on, up to W - 1; 0: more
                             for (int j = 1; j < W && left == 0; ++j)
                                 if (t + j <= live && m.last(t + j - 1)) left = j;
                             if (left > 0) {
                                 const int e = episode_at(a.ends, a.episodes, tokens, t);
-                                const T* p = static_cast<const T*>(a.d_final) + ((int64_t)e * d + ch) * (W - 1);
+                                const T* p = static_cast<const T*>(a.d_final) + ((int64_t)e * d + ch) * (W - 1) + W - 1 - left;
 #pragma unroll
-                                for (int k = 0; k < V; ++k) now[k] += to_float(p[k * (W - 1) + W - 1 - left]);
+                                for (int k = 0; k < P; ++k)
+                                    own[k] = f2_add(own[k], f2_of(to_float(p[2 * k * (W - 1)]), to_float(p[(2 * k + 1) * (W - 1)])));
                             }
                         }
                     }
-                    win.push(x[i]);
-                    ++age;
+                    advance(i);
+                    age = min(age + 1, W);
                 }
-                const int done = t - (W - 1);
-                if (done >= begin && done < end)
-                    store_vec<T, V>(static_cast<T*>(a.grads.dx) + (int64_t)done * a.grads.x_stride + ch, pend[0]);
-#pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) pend[j][k] = pend[j + 1][k];
-#pragma unroll
-                for (int k = 0; k < V; ++k) pend[W - 2][k] = now[k];
+                finish(t, own);
             }
         }
     }
     // over the CTA's runs
     const int row = a.lanes * V * (W + 1);
 #pragma unroll
-    for (int k = 0; k < V; ++k)
+    for (int k = 0; k < P; ++k)
 #pragma unroll
-        for (int j = 0; j <= W; ++j) red[y * row + (lane * V + k) * (W + 1) + j] = dw[j][k];
+        for (int j = 0; j <= W; ++j) {
+            float* p = red + y * row + (lane * V + 2 * k) * (W + 1) + j;
+            p[0] = f2_lo(dw[j][k]);
+            p[W + 1] = f2_hi(dw[j][k]);
+        }
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.y * row, all = (int64_t)d * (W + 1);
     for (int i = threadIdx.x; i < row && first + i < all; i += kThreads) {
@@ -385,10 +462,10 @@ __global__ void __launch_bounds__(kThreads) conv_grad_kernel(const __grid_consta
     }
 }
 
-// dweight and dbias over the CTAs: 32 outputs a CTA, eight threads to an output.
-constexpr int kSlices = kThreads / 32;
+// dweight and dbias over the CTAs: 32 outputs a CTA, 32 threads to an output.
+constexpr int kJoinThreads = 1024, kSlices = kJoinThreads / 32;
 
-__global__ void __launch_bounds__(kThreads) conv_join_kernel(const __grid_constant__ ConvLaunch a, int64_t rows) {
+__global__ void __launch_bounds__(kJoinThreads) conv_join_kernel(const __grid_constant__ ConvLaunch a, int64_t rows) {
     __shared__ float red[kSlices][33];
     pdl_wait();
     pdl_trigger();
@@ -413,41 +490,48 @@ __global__ void __launch_bounds__(kThreads) conv_join_kernel(const __grid_consta
         a.grads.dbias[ch] = v;
 }
 
-// Gradient of the initial states: one thread for each episode and channel, which
-// goes over the first W - 1 tokens again.  Slot k stands W - 1 - k tokens before
-// the episode: token i takes it with tap k - i.
+// Gradient of the initial states: one thread for each episode and two channels,
+// which goes over the first W - 1 tokens again.  Slot k stands W - 1 - k tokens
+// before the episode: token i takes it with tap k - i.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_init_grad_kernel(const __grid_constant__ ConvLaunch a) {
     pdl_wait();
     pdl_trigger();
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, e = i / d;
-    const int ch = (int)(i - e * d);
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, e = i / (d / 2);
+    const int ch = (int)(i - e * (d / 2)) * 2;
     if (e >= a.episodes) return;
     const int lo = episode_start(a.ends, (int)e, tokens), len = max(0, episode_end(a.ends, (int)e, tokens) - lo);
-    Taps<1, W> taps;
+    Taps<2, W> taps;
     taps.load(a, ch);
     const int64_t at = (e * d + ch) * (W - 1);
-    Window<T, 1, W> win;
-    float g[W - 1];
+    Window<T, 2, W> win;
+    f2 g[W - 1];
+    auto pair = [&](const void* p, int64_t o, int64_t apart) {
+        const T* q = static_cast<const T*>(p) + o;
+        return f2_of(to_float(q[0]), to_float(q[apart]));
+    };
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-        win.win[k][0] = a.init != nullptr ? to_float(static_cast<const T*>(a.init)[at + k]) : 0.0f;
+        win.win[k][0] = a.init != nullptr ? pair(a.init, at + k, W - 1) : f2_both(0.0f);
         // a short episode's final state still holds initial inputs
-        g[k] = a.d_final != nullptr && k >= len ? to_float(static_cast<const T*>(a.d_final)[at + k - len]) : 0.0f;
+        g[k] = a.d_final != nullptr && k >= len ? pair(a.d_final, at + k - len, W - 1) : f2_both(0.0f);
     }
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
         if (t >= len) break;
-        float x[1] = {to_float(static_cast<const T*>(a.in.x)[(int64_t)(lo + t) * a.in.x_stride + ch])};
-        const float dp = to_float(static_cast<const T*>(a.dout)[(int64_t)(lo + t) * a.dout_stride + ch]) *
-                         act_slope(taps.pre(win, x, 0), a.shape.activation);
+        const f2 x[1] = {pair(a.in.x, (int64_t)(lo + t) * a.in.x_stride + ch, 1)};
+        const f2 dp = f2_mul(pair(a.dout, (int64_t)(lo + t) * a.dout_stride + ch, 1),
+                             act_slope(taps.pre(win, x, 0), a.shape.activation));
 #pragma unroll
-        for (int k = t; k < W - 1; ++k) g[k] = fmaf(taps.w[k - t][0], dp, g[k]);
+        for (int k = t; k < W - 1; ++k) g[k] = f2_fma(taps.w[k - t][0], dp, g[k]);
         win.push(x);
     }
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) a.d_init[at + k] = g[k];
+    for (int k = 0; k < W - 1; ++k) {
+        a.d_init[at + k] = f2_lo(g[k]);
+        a.d_init[at + W - 1 + k] = f2_hi(g[k]);
+    }
 }
 
 // One token of per_thread environments, eight channels a thread.
@@ -488,7 +572,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < S; ++j) s = fmaf(w[k][j], to_float(state[(k * S + j) / V].v[(k * S + j) % V]), s);
                 s = fmaf(w[k][S], to_float(xv[k / V].v[k % V]), s);
-                o[k / V].v[k % V] = from_float<T>(act_of(s, a.shape.activation));
+                o[k / V].v[k % V] = from_float<T>(a.shape.activation == OFRL_ACT_SILU ? s * sigmoid(s) : s);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -511,22 +595,23 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_consta
 
 template <typename T, int W>
 cudaError_t forward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
+    constexpr int V = vec_of(sizeof(T), false);
     static std::atomic<uint64_t> done{0};
     ConvLaunch a = in;
-    const ConvCut c = conv_cut(a.shape.channels, a.in.tokens, num_sms);
+    const ConvCut c = conv_cut(a.shape.channels, V, a.in.tokens, num_sms);
     a.lanes = c.lanes;
     a.run = c.run;
     if (c.rows > INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = opt_in_once(conv_forward_kernel<T, W>, 0, done);
+    const cudaError_t e = opt_in_once(conv_forward_kernel<T, W, V>, 0, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(conv_forward_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
+    return launch_pdl(conv_forward_kernel<T, W, V>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
 }
 
 template <typename T, int W>
 cudaError_t backward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0}, join_done{0}, init_done{0};
     ConvLaunch a = in;
-    const ConvCut c = conv_cut(a.shape.channels, a.in.tokens, num_sms);
+    const ConvCut c = conv_cut(a.shape.channels, vec_of(sizeof(T), true), a.in.tokens, num_sms);
     a.lanes = c.lanes;
     a.run = c.run;
     const int64_t outs = (int64_t)a.shape.channels * (W + 1);
@@ -535,9 +620,9 @@ cudaError_t backward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
     if (e == cudaSuccess)
         e = launch_pdl(conv_grad_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
     if (e == cudaSuccess)
-        e = launch_pdl(conv_join_kernel, dim3((unsigned)((outs + 31) / 32)), dim3(kThreads), 0, st, a, c.rows);
+        e = launch_pdl(conv_join_kernel, dim3((unsigned)((outs + 31) / 32)), dim3(kJoinThreads), 0, st, a, c.rows);
     if (e == cudaSuccess && a.d_init != nullptr) {
-        const int64_t grid = ((int64_t)a.episodes * a.shape.channels + kThreads - 1) / kThreads;
+        const int64_t grid = ((int64_t)a.episodes * (a.shape.channels / 2) + kThreads - 1) / kThreads;
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
         e = opt_in_once(conv_init_grad_kernel<T, W>, 0, init_done);
         if (e == cudaSuccess && grid > 0)
@@ -595,7 +680,7 @@ ofrl_status check_sequence(const ofrl_conv* ctx, const ofrl_conv_tokens* in, con
 }
 
 int64_t conv_bytes(const ofrl_conv_shape& s, int64_t max_tokens, int num_sms, bool backward) {
-    return 256 + (backward ? conv_rows_most(s.channels, max_tokens, num_sms) * s.channels * (s.width + 1) * 4 : 0);
+    return 256 + (backward ? conv_rows_most(s.channels, vec_of(4, true), max_tokens, num_sms) * s.channels * (s.width + 1) * 4 : 0);
 }
 
 ConvLaunch base_launch(const ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* ends, int32_t episodes) {

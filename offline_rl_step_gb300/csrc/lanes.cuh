@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <cmath>
 
 #include "common.cuh"
 
@@ -53,6 +54,16 @@ __device__ __forceinline__ f2 f2_of(float lo, float hi) {
 __device__ __forceinline__ void f2_split(f2 x, float& lo, float& hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
 }
+__device__ __forceinline__ float f2_lo(f2 x) {
+    float lo, hi;
+    f2_split(x, lo, hi);
+    return lo;
+}
+__device__ __forceinline__ float f2_hi(f2 x) {
+    float lo, hi;
+    f2_split(x, lo, hi);
+    return hi;
+}
 __device__ __forceinline__ float f2_sum(f2 x) {
     float lo, hi;
     f2_split(x, lo, hi);
@@ -81,25 +92,81 @@ __device__ __forceinline__ f2 f2_exp2(f2 x) {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Elements 2 i and 2 i + 1 of a raw vector, and a vector from pairs.
+template <typename T, int V>
+__device__ __forceinline__ f2 vec_pair(const Vec<T, V>& u, int i) {
+    return f2_of(to_float(u.v[2 * i]), to_float(u.v[2 * i + 1]));
+}
+template <typename T, int V>
+__device__ __forceinline__ void set_vec_pair(Vec<T, V>& u, int i, f2 x) {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(x), f2_hi(x));
+        u.v[2 * i] = h.x;
+        u.v[2 * i + 1] = h.y;
+    } else {
+        u.v[2 * i] = f2_lo(x);
+        u.v[2 * i + 1] = f2_hi(x);
+    }
+}
+
 // ---- gates -----------------------------------------------------------------------
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_both(float x) { return f2_of(x, x); }
+__device__ __forceinline__ float rcp_of(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float max_or_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in [0, 1]; log1p(u) / u by a
 // polynomial fitted here to a relative error of 5e-9 over that range, so small
-// steps keep all their bits (log(1 + u) would not).
-__device__ __forceinline__ float softplus(float v) {
-    const float u = expf(-fabsf(v));
-    float p = -0.003244024235755205f;
-    p = fmaf(p, u, 0.019851457327604294f);
-    p = fmaf(p, u, -0.056959524750709534f);
-    p = fmaf(p, u, 0.10603654384613037f);
-    p = fmaf(p, u, -0.15305592119693756f);
-    p = fmaf(p, u, 0.1967593878507614f);
-    p = fmaf(p, u, -0.24954134225845337f);
-    p = fmaf(p, u, 0.3332996368408203f);
-    p = fmaf(p, u, -0.4999990165233612f);
-    p = fmaf(p, u, 1.0f);
-    return fmaf(p, u, fmaxf(v, 0.0f));
+// steps keep all their bits (log(1 + u) would not).  u is 2^x with what rounding
+// x = -|v| log2 e leaves put back, or far steps would lose bits.
+__device__ __forceinline__ f2 softplus(f2 v) {
+    float a, b, lo, hi;
+    f2_split(v, a, b);
+    // below -200, u is zero anyway and infinities would leave a rest that is no number
+    const f2 n = f2_of(fmaxf(-fabsf(a), -200.0f), fmaxf(-fabsf(b), -200.0f));
+    const f2 x = f2_mul(n, f2_both(kLog2e));
+    f2_split(x, lo, hi);
+    f2 rest = f2_fma(n, f2_both(kLog2e), f2_of(-lo, -hi));
+    rest = f2_fma(n, f2_both(1.92596299e-8f), rest);      // log2 e less its fp32 value
+    f2 u = f2_of(exp2_of(lo), exp2_of(hi));
+    u = f2_fma(f2_mul(u, f2_both(kLn2)), rest, u);
+    f2 p = f2_both(-0.003244024235755205f);
+    p = f2_fma(p, u, f2_both(0.019851457327604294f));
+    p = f2_fma(p, u, f2_both(-0.056959524750709534f));
+    p = f2_fma(p, u, f2_both(0.10603654384613037f));
+    p = f2_fma(p, u, f2_both(-0.15305592119693756f));
+    p = f2_fma(p, u, f2_both(0.1967593878507614f));
+    p = f2_fma(p, u, f2_both(-0.24954134225845337f));
+    p = f2_fma(p, u, f2_both(0.3332996368408203f));
+    p = f2_fma(p, u, f2_both(-0.4999990165233612f));
+    p = f2_fma(p, u, f2_both(1.0f));
+    return f2_fma(p, u, f2_of(max_or_nan(a, 0.0f), max_or_nan(b, 0.0f)));
 }
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// 1 / (1 + e^-v): a few 2^-22 off up to |v| of 8 or so, where it matters.
+__device__ __forceinline__ f2 sigmoid(f2 v) {
+    const f2 e = f2_add(f2_exp2(f2_mul(v, f2_both(-kLog2e))), f2_both(1.0f));
+    return f2_of(rcp_of(f2_lo(e)), rcp_of(f2_hi(e)));
+}
+__device__ __forceinline__ float sigmoid(float v) { return rcp_of(1.0f + exp2_of(-kLog2e * v)); }
+__device__ __forceinline__ float softplus(float v) { return f2_lo(softplus(f2_of(v, v))); }
+// v sigmoid(v), and its slope s (1 + v (1 - s)) given s = sigmoid(v).
+__device__ __forceinline__ f2 silu(f2 v) { return f2_mul(v, sigmoid(v)); }
+__device__ __forceinline__ f2 silu_slope(f2 v, f2 s) {
+    return f2_fma(f2_mul(v, s), f2_fma(s, f2_both(-1.0f), f2_both(1.0f)), s);
+}
 
 // Opt a kernel into its dynamic shared memory and the largest carveout, once
 // per device (the calls cost a few microseconds).

@@ -45,7 +45,9 @@ constexpr int kMinSegment = 64;
 // How a state of [channels, N] lies on a warp: LS lanes share a channel, four
 // states each, and a thread has CPT channels.
 constexpr int lanes_of(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
-constexpr int wide_of(int ls) { return ls < 4 ? ls : 4; }                // CPT of the wide form; the narrow one has 1
+// CPT of the wide form; the narrow one has 1.  Gradients keep twice as many
+// values a state in registers and shared memory.
+constexpr int wide_of(int ls, bool backward) { return ls < 2 ? 1 : ls < 4 || backward ? 2 : 4; }
 constexpr int block_of(int ls, int cpt) { return kWarps * (32 / ls) * cpt; }      // channels of a CTA
 
 // How one call is cut.
@@ -112,6 +114,8 @@ struct StepLaunch {
     void* out;
     int64_t out_stride;
     int32_t* status;
+    int num_sms;
+    int whole_states;    // B and C can be read four elements at a time
 };
 
 cudaError_t launch_forward(const Launch& a, const Cut& c, cudaStream_t st);
@@ -236,9 +240,20 @@ __device__ __forceinline__ void store_states(float* base, const f2 (&h)[2 * CPT]
                 make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
 }
 
-__device__ __forceinline__ float delta_of(float dt, float bias, int with_softplus) {
-    const float v = dt + bias;
+__device__ __forceinline__ f2 delta_of(f2 dt, f2 bias, int with_softplus) {
+    const f2 v = f2_add(dt, bias);
     return with_softplus ? softplus(v) : v;
+}
+
+// Elements i and i + 1 of a thread's V (one element stands twice).
+template <int V>
+__device__ __forceinline__ f2 pair_at(const float (&x)[V], int i) {
+    return f2_of(x[i], x[V > 1 ? i + 1 : i]);
+}
+template <int V>
+__device__ __forceinline__ void set_pair(float (&x)[V], int i, f2 v) {
+    x[i] = f2_lo(v);
+    if constexpr (V > 1) x[i + 1] = f2_hi(v);
 }
 
 // Sums over the LS lanes of a channel.  Wide forms hand the channels out: the
@@ -316,7 +331,7 @@ struct RowsHeld {
                 for (int i = 0; i < Ti::V; ++i) v[j].v[i] = from_float<T>(0.0f);
         }
     }
-    __device__ float at(int j, int i) const { return to_float(v[j].v[i]); }
+    __device__ f2 pair(int j, int i) const { return f2_of(to_float(v[j].v[i]), to_float(v[j].v[Ti::V > 1 ? i + 1 : i])); }
 };
 
 // B or C of a tile, in flight.

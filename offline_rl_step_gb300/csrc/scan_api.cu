@@ -20,14 +20,14 @@ int blocks_of(const ofrl_scan_shape& s, int ls, int cpt) {
 }
 // Segments wanted for `blocks` CTAs each: `per_sm` CTAs on every SM.
 int64_t wanted(int blocks, int num_sms, int per_sm) { return div_up((int64_t)num_sms * per_sm, blocks); }
-int per_sm_of(bool backward) { return backward ? 2 : 5; }
+int per_sm_of(bool backward) { return backward ? 3 : 5; }
 
 }  // namespace
 
 Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int num_sms, bool backward) {
     Cut c;
     c.ls = lanes_of(s.state_dim);
-    for (int cpt = wide_of(c.ls);; cpt = 1) {
+    for (int cpt = wide_of(c.ls, backward);; cpt = 1) {
         c.cpt = cpt;
         c.blocks = blocks_of(s, c.ls, cpt);
         const int64_t even = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward))), kTile);
@@ -64,7 +64,7 @@ int64_t work_bytes(const ofrl_scan_shape& s, int64_t max_tokens, int num_sms, bo
     Cut c;
     c.ls = lanes_of(s.state_dim);
     for (int back = 0; back <= (backward ? 1 : 0); ++back)
-        for (int cpt = wide_of(c.ls);; cpt = 1) {
+        for (int cpt = wide_of(c.ls, back != 0);; cpt = 1) {
             c.cpt = cpt;
             c.blocks = blocks_of(s, c.ls, cpt);
             // a segment is no shorter than an even share and than kMinSegment, or it is kMaxSegment
@@ -271,6 +271,9 @@ ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int
     a.out = out;
     a.out_stride = out_stride;
     a.status = ctx->status;
+    a.num_sms = ctx->num_sms;
+    const int64_t four = 4 * dtype_size(ctx->shape.dtype);
+    a.whole_states = aligned_to(in->b, four) && aligned_to(in->c, four) && in->b_stride % 4 == 0 && in->c_stride % 4 == 0;
     return cuda_status(launch_step(a, static_cast<cudaStream_t>(stream)));
 }
 

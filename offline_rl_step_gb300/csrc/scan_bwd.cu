@@ -9,6 +9,8 @@
 // backward.  The sums over a token's channels (dB, dC) are made over a warp's
 // lanes, the CTA's warps and the CTAs, in that order.
 
+#include <cstddef>
+
 #include "scan.cuh"
 
 namespace ofrl {
@@ -20,6 +22,7 @@ constexpr int kSub = kTile / 2;      // tokens whose p is kept at once
 template <int LS, int CPT>
 struct GradShared {
     using L = Lay<LS, CPT>;
+    static constexpr int kSlots = L::kPairs / 2 > 2 ? L::kPairs / 2 : 2;
     alignas(16) float delta[kTile][L::CB];
     alignas(16) float dx[kTile][L::CB];      // delta x
     alignas(16) float dy[kTile][L::CB];
@@ -28,78 +31,83 @@ struct GradShared {
     alignas(16) float sum_b[kSub][L::CB];    // sum_n lam B
     alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
     alignas(16) float y[kSub][L::CB];
-    alignas(16) float dbc[kSub][kWarps][2 * L::NP];
-    alignas(16) ulonglong2 p[kSub][L::kPairs / 2][kThreads];
+    alignas(16) ulonglong2 p[kSub][kSlots][kThreads];      // then parts of dB and dC
     uint32_t mask[kMaxSegment / 32];
     Range range;
 };
 
-// Sums over the 32 / LS lanes that share a state group: v[0..3] dB of the
-// thread's states, v[4..7] dC.  Lane bits pick what a lane keeps: first dB or
-// dC, then the states' half, then one state; bits left over only add.
-template <int LS>
-__device__ __forceinline__ void sum_channels(float (&v)[8]) {
-    const int lane = threadIdx.x & 31;
-    int n = 8;
+// dB and dC of a token are sums over the CTA's channels.  A thread's part, four
+// floats of each, replaces the p it has just used; then every thread adds up
+// what 128 / max(8, LS) threads with its states left for one (token, dB or dC),
+// and lanes that share states add theirs.  (Summing over a warp's lanes by
+// shuffles instead: 28 instructions more for each token.)
+template <int LS, int SLOTS>
+struct ChannelSums {
+    static constexpr int kWidth = LS > 8 ? LS : 8;      // threads that read one sum's parts
+    static constexpr int kAtOnce = kThreads / kWidth;   // sums of a round
+    static constexpr int kRounds = 2 * kSub / kAtOnce;
+    // put(row, half, first state, values) for each of the 2 * count sums
+    template <typename Put>
+    __device__ static void run(const float4* parts, int count, const Put& put) {
+        const int j = threadIdx.x % kWidth;
 #pragma unroll
-    for (int o = LS; o < 32; o <<= 1) {
-        if (n > 1) {
-            n >>= 1;
-            const bool up = lane & o;
+        for (int round = 0; round < kRounds; ++round) {
+            const int rh = round * kAtOnce + (int)threadIdx.x / kWidth;
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+            for (int k = j; k < kThreads; k += kWidth) {
+                const float4 u = parts[((rh / 2) * SLOTS + rh % 2) * kThreads + k];
+                v.x += u.x;
+                v.y += u.y;
+                v.z += u.z;
+                v.w += u.w;
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) {
-                    const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            for (int o = LS; o < kWidth; o <<= 1) {
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+                v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+            }
+            if (j < LS && rh / 2 < count) put(rh / 2, rh % 2, 4 * j, v);
         }
     }
-}
-// Writes what sum_channels left in this lane to a token's [2 NP].
-template <int LS>
-__device__ __forceinline__ void put_channels(float* dst, const float (&v)[8], int n0) {
-    const int lane = threadIdx.x & 31;
-    constexpr int NP = 4 * LS;
-    float* p = dst + (lane & LS ? NP : 0) + n0;
-    if constexpr (LS == 16) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if constexpr (LS == 8) {
-        *reinterpret_cast<float2*>(p + (lane & 16 ? 2 : 0)) = make_float2(v[0], v[1]);
-    } else {
-        if ((lane & ~(8 * LS - 1)) == 0) p[(lane & 2 * LS ? 2 : 0) + (lane & 4 * LS ? 1 : 0)] = v[0];
-    }
-}
+};
 
-template <int ROWS, typename T, int LS, int CPT>
-__device__ __forceinline__ void put_deltas(float (*delta)[Lay<LS, CPT>::CB], float (*dx)[Lay<LS, CPT>::CB],
-                                           float (*dy)[Lay<LS, CPT>::CB], const Launch& a, const Block& b, int t0, int rows,
-                                           const float (&bias)[Tiling<T, Lay<LS, CPT>::CB, ROWS>::V]) {
-    constexpr int CB = Lay<LS, CPT>::CB;
-    using Ti = Tiling<T, CB, ROWS>;
-    RowsHeld<T, CB, ROWS> x, dt, z, g;
-    if (dx != nullptr) x.load(a.in.x, a.in.x_stride, b, t0, rows);
-    dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
-    if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
-    g.load(a.dout, a.dout_stride, b, t0, rows);
-#pragma unroll
-    for (int j = 0; j < Ti::NV; ++j) {
-        const int r = Ti::row(j);
-        if (r >= ROWS) continue;
-        float d[Ti::V], xs[Ti::V], gy[Ti::V];
-#pragma unroll
-        for (int i = 0; i < Ti::V; ++i) {
-            d[i] = delta_of(dt.at(j, i), bias[i], a.shape.softplus);
-            if (dx != nullptr) xs[i] = d[i] * x.at(j, i);
-            gy[i] = g.at(j, i);
-            if (a.in.z != nullptr) gy[i] *= z.at(j, i) * sigmoid(z.at(j, i));
-        }
-        put_floats(&delta[r][Ti::col()], d);
-        if (dx != nullptr) put_floats(&dx[r][Ti::col()], xs);
-        put_floats(&dy[r][Ti::col()], gy);
+// What a tile's tokens need before the states see them, in flight.
+template <typename T, int CB, bool WITH_X>
+struct TileHeld {
+    using Ti = Tiling<T, CB, kTile>;
+    RowsHeld<T, CB, kTile> x, dt, z, g;
+    __device__ void load(const Launch& a, const Block& b, int t0, int rows) {
+        if constexpr (WITH_X) x.load(a.in.x, a.in.x_stride, b, t0, rows);
+        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+        if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
+        g.load(a.dout, a.dout_stride, b, t0, rows);
     }
-}
+    // delta, delta x and dy to shared memory
+    __device__ void put(float (*delta)[CB], float (*dx)[CB], float (*dy)[CB], const Launch& a,
+                        const float (&bias)[Ti::V]) const {
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j) {
+            const int r = Ti::row(j);
+            if (r >= kTile) continue;
+            float d[Ti::V], xs[Ti::V], gy[Ti::V];
+#pragma unroll
+            for (int i = 0; i < Ti::V; i += 2) {
+                const f2 de = delta_of(dt.pair(j, i), pair_at(bias, i), a.shape.softplus);
+                f2 gp = g.pair(j, i);
+                if (a.in.z != nullptr) gp = f2_mul(gp, silu(z.pair(j, i)));
+                set_pair(d, i, de);
+                if constexpr (WITH_X) set_pair(xs, i, f2_mul(de, x.pair(j, i)));
+                set_pair(gy, i, gp);
+            }
+            put_floats(&delta[r][Ti::col()], d);
+            if constexpr (WITH_X) put_floats(&dx[r][Ti::col()], xs);
+            put_floats(&dy[r][Ti::col()], gy);
+        }
+    }
+};
 
 // The adjoint a segment hands to the one before it.
 template <typename T, int LS, int CPT>
@@ -151,14 +159,22 @@ __global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_c
     if (own && a.d_final != nullptr && s.range.e0 < a.episodes)
         load_states<LS, CPT>(lam, a.d_final + (int64_t)s.range.e0 * a.shape.channels * n, n, p.ch, p.count, p.n0);
     const f2 one = f2_of(1.0f, 1.0f);
-    for (int t0 = s0 + (end - 1 - s0) / kTile * kTile; t0 >= s0; t0 -= kTile) {
+    const int last = s0 + (end - 1 - s0) / kTile * kTile;
+    TileHeld<T, L::CB, false> rows_in;
+    StatesHeld<T, LS, CPT> cs;
+    auto fetch = [&](int t0) {
         const int rows = min(kTile, end - t0);
-        StatesHeld<T, LS, CPT> cs;
+        rows_in.load(a, b, t0, rows);
         cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+    };
+    fetch(last);
+    for (int t0 = last; t0 >= s0; t0 -= kTile) {
+        const int rows = min(kTile, end - t0);
         __syncthreads();
-        put_deltas<kTile, T, LS, CPT>(s.delta, nullptr, s.dy, a, b, t0, rows, bias);
+        rows_in.put(s.delta, nullptr, s.dy, a, bias);
         cs.put(s.c);
         __syncthreads();
+        if (t0 > s0) fetch(t0 - kTile);
         auto step = [&](int i) {
             f2 de[L::kCh], gy[L::kCh], cv[L::kSt];
             L::channels(de, &s.delta[i][p.local]);
@@ -191,9 +207,17 @@ __global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_c
     }
 }
 
+// CTAs of an SM: what shared memory allows, and registers enough for them.
+template <int LS, int CPT>
+constexpr int grad_ctas() {
+    constexpr int n = (227 * 1024) / ((int)sizeof(GradShared<LS, CPT>) + 1024);
+    return n > 3 ? 3 : n;
+}
+
 template <typename T, int LS, int CPT>
-__global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_constant__ Launch a) {
+__global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kernel(const __grid_constant__ Launch a) {
     using L = Lay<LS, CPT>;
+    using Tile = Tiling<T, L::CB, kTile>;
     using Ti = Tiling<T, L::CB, kSub>;
     extern __shared__ __align__(16) uint8_t smem[];
     GradShared<LS, CPT>& s = *reinterpret_cast<GradShared<LS, CPT>*>(smem);
@@ -212,9 +236,12 @@ __global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_consta
     const Place<LS, CPT> p(b);
     const bool mine = p.n0 < n;
     const int parts = a.blocks / a.shape.groups;      // CTAs that share a group's dB and dC
-    f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs];
+    const int64_t dbc_stride = (int64_t)a.shape.groups * 2 * L::NP;
+    float* dbc = a.dbc + (int64_t)(blockIdx.y % parts) * tokens * dbc_stride + b.group * 2 * L::NP;
+    f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs], first[L::kPairs], next[L::kPairs];
     load_decays<LS, CPT>(a2, a, p);
-    float bias[Ti::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
+    float tile_bias[Tile::V], bias[Ti::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
+    load_params<T, L::CB, kTile>(tile_bias, a.in.dt_bias, b);
     load_params<T, L::CB, kSub>(bias, a.in.dt_bias, b);
     load_params<T, L::CB, kSub>(skip, a.in.d, b);
 #pragma unroll
@@ -241,7 +268,19 @@ __global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_consta
         const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
         if (e < a.episodes) load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
     };
+    const int last = s0 + (end - 1 - s0) / kTile * kTile;
+    TileHeld<T, L::CB, true> rows_in;
+    StatesHeld<T, LS, CPT> bs, cs;
+    auto fetch = [&](int t0) {
+        const int rows = min(kTile, end - t0);
+        rows_in.load(a, b, t0, rows);
+        bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
+        cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+        // not written, and not used, where the tile begins an episode
+        load_states<LS, CPT>(next, a.saved + (int64_t)(t0 / kTile) * row_states, n, p.ch, p.count, p.n0);
+    };
     if (end > s0) {
+        fetch(last);
         if (s.range.closed)
             enter(end - 1);
         else
@@ -249,112 +288,21 @@ __global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_consta
     }
     const int at_state = L::state_at((threadIdx.x & 31) % LS);
 
-    for (int t0 = s0 + (end - 1 - s0) / kTile * kTile; t0 >= s0 && end > s0; t0 -= kTile) {
+    for (int t0 = last; t0 >= s0 && end > s0; t0 -= kTile) {
         const int rows = min(kTile, end - t0);
-        StatesHeld<T, LS, CPT> bs, cs;
-        bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
-        cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
-        __syncthreads();      // the tile before is through
-        put_deltas<kSub, T, LS, CPT>(s.delta, s.dx, s.dy, a, b, t0, rows, bias);
-        if (rows > kSub)
-            put_deltas<kSub, T, LS, CPT>(s.delta + kSub, s.dx + kSub, s.dy + kSub, a, b, t0 + kSub, rows - kSub, bias);
+        rows_in.put(s.delta, s.dx, s.dy, a, tile_bias);      // the tile before is through
         bs.put(s.b);
         cs.put(s.c);
+#pragma unroll
+        for (int q = 0; q < L::kPairs; ++q) first[q] = next[q];
         __syncthreads();
+        if (t0 > s0) fetch(t0 - kTile);
         const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
 
-        auto forward = [&](int i, bool keep) {
-            if (starts >> i & 1) begin(t0 + i);
-            f2 de[L::kCh], dx[L::kCh], bv[L::kSt], was[L::kPairs];
-            L::channels(de, &s.delta[i][p.local]);
-            L::channels(dx, &s.dx[i][p.local]);
-            L::states(bv, s.b + i * L::kStWidth + at_state);
-#pragma unroll
-            for (int q = 0; q < L::kPairs; ++q) {
-                was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
-                h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
-            }
-            if (keep)
-#pragma unroll
-                for (int q = 0; q < L::kPairs; q += 2)
-                    s.p[i % kSub][q / 2][threadIdx.x] = make_ulonglong2(was[q], was[q + 1]);
-        };
-        auto backward = [&](int i) {
-            const int r = i % kSub;
-            f2 de[L::kCh], dx[L::kCh], gy[L::kCh], bv[L::kSt], cv[L::kSt];
-            L::channels(de, &s.delta[i][p.local]);
-            L::channels(dx, &s.dx[i][p.local]);
-            L::channels(gy, &s.dy[i][p.local]);
-            L::states(bv, s.b + i * L::kStWidth + at_state);
-            L::states(cv, s.c + i * L::kStWidth + at_state);
-            f2 sb[L::kCh], sa[L::kCh], sy[L::kCh], db[L::kSt], dc[L::kSt];
-#pragma unroll
-            for (int k = 0; k < L::kCh; ++k) sb[k] = sa[k] = sy[k] = zero;
-#pragma unroll
-            for (int k = 0; k < L::kSt; ++k) db[k] = dc[k] = zero;
-#pragma unroll
-            for (int q = 0; q < L::kPairs; ++q) {
-                const int c = L::ci(q), k = L::si(q);
-                const ulonglong2 two = s.p[r][q / 2][threadIdx.x];
-                const f2 was = q & 1 ? two.y : two.x;
-                const f2 now = f2_fma(dx[c], bv[k], was);
-                const f2 l = f2_fma(gy[c], cv[k], lam[q]);
-                dc[k] = f2_fma(gy[c], now, dc[k]);
-                db[k] = f2_fma(l, dx[c], db[k]);
-                sb[c] = f2_fma(l, bv[k], sb[c]);
-                sy[c] = f2_fma(cv[k], now, sy[c]);
-                const f2 w = f2_mul(l, was);
-                sa[c] = f2_fma(w, a2[q], sa[c]);
-                da[q] = f2_fma(w, de[c], da[q]);
-                lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
-            }
-            float v[8], ch[3][CPT];
-            if constexpr (L::kWide) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k] = f2_sum(db[k]);
-                    v[4 + k] = f2_sum(dc[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < L::kCh; ++k) {
-                    f2_split(sb[k], ch[0][2 * k], ch[0][2 * k + 1]);
-                    f2_split(sa[k], ch[1][2 * k], ch[1][2 * k + 1]);
-                    f2_split(sy[k], ch[2][2 * k], ch[2][2 * k + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    f2_split(db[k], v[2 * k], v[2 * k + 1]);
-                    f2_split(dc[k], v[4 + 2 * k], v[4 + 2 * k + 1]);
-                }
-                ch[0][0] = f2_sum(sb[0]);
-                ch[1][0] = f2_sum(sa[0]);
-                ch[2][0] = f2_sum(sy[0]);
-            }
-#pragma unroll
-            for (int k = 0; k < CPT; ++k)
-                if (!mine) ch[0][k] = ch[1][k] = ch[2][k] = 0.0f;
-            sum_channels<LS>(v);
-            put_channels<LS>(s.dbc[r][threadIdx.x >> 5], v, p.n0);
-            const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]), y = sum_states<LS, CPT>(ch[2]);
-            if (returns_channel<LS, CPT>()) {
-                const int at = p.local + which_channel<LS, CPT>();
-                s.sum_b[r][at] = to_b;
-                s.sum_a[r][at] = to_a;
-                s.y[r][at] = y;
-            }
-            if (starts >> i & 1) {
-                const int t = t0 + i;
-                if (a.d_init != nullptr) {
-                    const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
-                    if (e < a.episodes) store_states<LS, CPT>(a.d_init + e * row_states, lam, n, p.ch, p.count, p.n0);
-                }
-                if (t > s0) enter(t - 1);
-            }
-        };
-        // rows [r0, r0 + count) of the tile, from shared memory to the gradients
-        auto finish = [&](int r0, int count) {
-            const int t1 = t0 + r0;
+#pragma unroll 1
+        for (int r0 = rows > kSub ? kSub : 0; r0 >= 0; r0 -= kSub) {
+            const int stop = min(rows, r0 + kSub), t1 = t0 + r0, count = stop - r0;
+            // what the rows' gradients need besides, in flight
             RowsHeld<T, L::CB, kSub> x, dt, z, g;
             x.load(a.in.x, a.in.x_stride, b, t1, count);
             if (a.shape.softplus) dt.load(a.in.dt, a.in.dt_stride, b, t1, count);
@@ -362,78 +310,156 @@ __global__ void __launch_bounds__(kThreads) scan_grad_kernel(const __grid_consta
                 z.load(a.in.z, a.in.z_stride, b, t1, count);
                 g.load(a.dout, a.dout_stride, b, t1, count);
             }
+            // forward over the tile to the rows, and over them with p kept
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) h[q] = first[q];
+#pragma unroll 2
+            for (int i = 0; i < stop; ++i) {
+                if (starts >> i & 1) begin(t0 + i);
+                f2 de[L::kCh], dx[L::kCh], bv[L::kSt], was[L::kPairs];
+                L::channels(de, &s.delta[i][p.local]);
+                L::channels(dx, &s.dx[i][p.local]);
+                L::states(bv, s.b + i * L::kStWidth + at_state);
+#pragma unroll
+                for (int q = 0; q < L::kPairs; ++q) {
+                    was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
+                    h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
+                }
+                if (i >= r0)
+#pragma unroll
+                    for (int q = 0; q < L::kPairs; q += 2)
+                        s.p[i - r0][q / 2][threadIdx.x] = make_ulonglong2(was[q], was[q + 1]);
+            }
+#pragma unroll 1
+            for (int i = stop - 1; i >= r0; --i) {
+                const int r = i - r0;
+                f2 de[L::kCh], dx[L::kCh], gy[L::kCh], bv[L::kSt], cv[L::kSt];
+                L::channels(de, &s.delta[i][p.local]);
+                L::channels(dx, &s.dx[i][p.local]);
+                L::channels(gy, &s.dy[i][p.local]);
+                L::states(bv, s.b + i * L::kStWidth + at_state);
+                L::states(cv, s.c + i * L::kStWidth + at_state);
+                f2 sb[L::kCh], sa[L::kCh], sy[L::kCh], db[L::kSt], dc[L::kSt];
+#pragma unroll
+                for (int q = 0; q < L::kPairs; ++q) {
+                    const int c = L::ci(q), k = L::si(q);
+                    const ulonglong2 two = s.p[r][q / 2][threadIdx.x];
+                    const f2 was = q & 1 ? two.y : two.x;
+                    const f2 now = f2_fma(dx[c], bv[k], was);
+                    const f2 l = f2_fma(gy[c], cv[k], lam[q]);
+                    const f2 w = f2_mul(l, was);
+                    dc[k] = c == 0 ? f2_mul(gy[c], now) : f2_fma(gy[c], now, dc[k]);
+                    db[k] = c == 0 ? f2_mul(l, dx[c]) : f2_fma(l, dx[c], db[k]);
+                    sb[c] = k == 0 ? f2_mul(l, bv[k]) : f2_fma(l, bv[k], sb[c]);
+                    sy[c] = k == 0 ? f2_mul(cv[k], now) : f2_fma(cv[k], now, sy[c]);
+                    sa[c] = k == 0 ? f2_mul(w, a2[q]) : f2_fma(w, a2[q], sa[c]);
+                    da[q] = f2_fma(w, de[c], da[q]);
+                    lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
+                }
+                float v[8], ch[3][CPT];
+                if constexpr (L::kWide) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[k] = f2_sum(db[k]);
+                        v[4 + k] = f2_sum(dc[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < L::kCh; ++k) {
+                        f2_split(sb[k], ch[0][2 * k], ch[0][2 * k + 1]);
+                        f2_split(sa[k], ch[1][2 * k], ch[1][2 * k + 1]);
+                        f2_split(sy[k], ch[2][2 * k], ch[2][2 * k + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        f2_split(db[k], v[2 * k], v[2 * k + 1]);
+                        f2_split(dc[k], v[4 + 2 * k], v[4 + 2 * k + 1]);
+                    }
+                    ch[0][0] = f2_sum(sb[0]);
+                    ch[1][0] = f2_sum(sa[0]);
+                    ch[2][0] = f2_sum(sy[0]);
+                }
+                if (n < L::NP)      // threads past the last state take no part in sums
+#pragma unroll
+                    for (int k = 0; k < CPT; ++k)
+                        if (!mine) ch[0][k] = ch[1][k] = ch[2][k] = 0.0f;
+                float4* part = reinterpret_cast<float4*>(&s.p[r][0][threadIdx.x]);
+                part[0] = make_float4(v[0], v[1], v[2], v[3]);
+                part[kThreads] = make_float4(v[4], v[5], v[6], v[7]);
+                const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]),
+                            y = sum_states<LS, CPT>(ch[2]);
+                if (returns_channel<LS, CPT>()) {
+                    const int at = p.local + which_channel<LS, CPT>();
+                    s.sum_b[r][at] = to_b;
+                    s.sum_a[r][at] = to_a;
+                    s.y[r][at] = y;
+                }
+                if (starts >> i & 1) {
+                    const int t = t0 + i;
+                    if (a.d_init != nullptr) {
+                        const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
+                        if (e < a.episodes) store_states<LS, CPT>(a.d_init + e * row_states, lam, n, p.ch, p.count, p.n0);
+                    }
+                    if (t > s0) enter(t - 1);
+                }
+            }
+            __syncthreads();
+            // from shared memory to the gradients
             const int64_t ch = b.ch0 + Ti::col();
 #pragma unroll
             for (int j = 0; j < Ti::NV; ++j) {
                 const int r = Ti::row(j);
                 if (r >= count || Ti::col() >= b.count) continue;
-                float dxs[Ti::V], ddt[Ti::V], dz[Ti::V];
+                float out_x[Ti::V], out_dt[Ti::V], out_z[Ti::V];
 #pragma unroll
-                for (int i = 0; i < Ti::V; ++i) {
-                    const int c = Ti::col() + i;
-                    const float xv = x.at(j, i), gy = s.dy[r0 + r][c], to_b = s.sum_b[r][c];
-                    dxs[i] = s.delta[r0 + r][c] * to_b;
-                    if (a.in.d != nullptr) dxs[i] = fmaf(skip[i], gy, dxs[i]);
-                    ddt[i] = fmaf(xv, to_b, s.sum_a[r][c] * kLn2);
-                    if (a.shape.softplus) ddt[i] *= sigmoid(dt.at(j, i) + bias[i]);
+                for (int i = 0; i < Ti::V; i += 2) {
+                    const int c = Ti::col() + i, c1 = Ti::V > 1 ? c + 1 : c;
+                    auto at = [&](const float* row) { return f2_of(row[c], row[c1]); };
+                    const f2 xv = x.pair(j, i), gy = at(s.dy[r0 + r]), to_b = at(s.sum_b[r]), sk = pair_at(skip, i);
+                    f2 v = f2_mul(at(s.delta[r0 + r]), to_b);
+                    if (a.in.d != nullptr) v = f2_fma(sk, gy, v);
+                    set_pair(out_x, i, v);
+                    v = f2_fma(xv, to_b, f2_mul(at(s.sum_a[r]), f2_both(kLn2)));
+                    if (a.shape.softplus) v = f2_mul(v, sigmoid(f2_add(dt.pair(j, i), pair_at(bias, i))));
+                    set_pair(out_dt, i, v);
+                    set_pair(dskip, i, f2_fma(gy, xv, pair_at(dskip, i)));
+                    set_pair(dbias, i, f2_add(v, pair_at(dbias, i)));
                     if (a.in.z != nullptr) {
-                        float y = s.y[r][c];
-                        if (a.in.d != nullptr) y = fmaf(skip[i], xv, y);
-                        const float zv = z.at(j, i), sg = sigmoid(zv);
-                        dz[i] = g.at(j, i) * y * sg * (1.0f + zv * (1.0f - sg));
+                        f2 y = at(s.y[r]);
+                        if (a.in.d != nullptr) y = f2_fma(sk, xv, y);
+                        const f2 zv = z.pair(j, i);
+                        set_pair(out_z, i, f2_mul(f2_mul(g.pair(j, i), y), silu_slope(zv, sigmoid(zv))));
                     }
-                    dskip[i] = fmaf(gy, xv, dskip[i]);
-                    dbias[i] += ddt[i];
                 }
                 const int64_t t = t1 + r;
-                store_vec<T, Ti::V>(static_cast<T*>(a.grads.dx) + t * a.grads.x_stride + ch, dxs);
-                store_vec<T, Ti::V>(static_cast<T*>(a.grads.ddt) + t * a.grads.dt_stride + ch, ddt);
+                store_vec<T, Ti::V>(static_cast<T*>(a.grads.dx) + t * a.grads.x_stride + ch, out_x);
+                store_vec<T, Ti::V>(static_cast<T*>(a.grads.ddt) + t * a.grads.dt_stride + ch, out_dt);
                 if (a.in.z != nullptr)
-                    store_vec<T, Ti::V>(static_cast<T*>(a.grads.dz) + t * a.grads.z_stride + ch, dz);
+                    store_vec<T, Ti::V>(static_cast<T*>(a.grads.dz) + t * a.grads.z_stride + ch, out_z);
             }
-            for (int i = threadIdx.x; i < count * 2 * L::NP; i += kThreads) {
-                const int r = i / (2 * L::NP), k = i % (2 * L::NP), st = k % L::NP;
-                float v = s.dbc[r][0][k];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) v += s.dbc[r][w][k];
+            ChannelSums<LS, GradShared<LS, CPT>::kSlots>::run(reinterpret_cast<const float4*>(s.p), count, [&](int r, int half, int st, const float4& v) {
                 const int64_t t = t1 + r;
                 if (parts > 1) {
-                    a.dbc[(((int64_t)(blockIdx.y % parts) * tokens + t) * a.shape.groups + b.group) * (2 * L::NP) + k] = v;
+                    *reinterpret_cast<float4*>(dbc + t * dbc_stride + half * L::NP + st) = v;
                 } else if (st < n) {
-                    if (k < L::NP)
-                        static_cast<T*>(a.grads.db)[t * a.grads.b_stride + b.group * n + st] = from_float<T>(v);
-                    else
-                        static_cast<T*>(a.grads.dc)[t * a.grads.c_stride + b.group * n + st] = from_float<T>(v);
+                    T* out = half ? static_cast<T*>(a.grads.dc) + t * a.grads.c_stride
+                                  : static_cast<T*>(a.grads.db) + t * a.grads.b_stride;
+                    out += b.group * n + st;
+                    out[0] = from_float<T>(v.x);
+                    out[1] = from_float<T>(v.y);
+                    out[2] = from_float<T>(v.z);
+                    out[3] = from_float<T>(v.w);
                 }
-            }
-        };
-        auto before_tile = [&]() {
-            if (!(starts & 1))
-                load_states<LS, CPT>(h, a.saved + (int64_t)(t0 / kTile) * row_states, n, p.ch, p.count, p.n0);
-        };
-
-        before_tile();
-        if (rows > kSub) {
-            for (int i = 0; i < kSub; ++i) forward(i, false);
-            for (int i = kSub; i < rows; ++i) forward(i, true);
-            for (int i = rows - 1; i >= kSub; --i) backward(i);
-            __syncthreads();
-            finish(kSub, rows - kSub);
-            before_tile();
+            });
             __syncthreads();
         }
-        const int first = min(rows, kSub);
-        for (int i = 0; i < first; ++i) forward(i, true);
-        for (int i = first - 1; i >= 0; --i) backward(i);
-        __syncthreads();
-        finish(0, first);
     }
 
     store_states<LS, CPT>(a.da + (int64_t)blockIdx.x * row_states, da, n, p.ch, p.count, p.n0);
     // dD and ddt_bias over the threads of a column
     float(*red)[2][L::CB] = reinterpret_cast<float(*)[2][L::CB]>(&s.delta[0][0]);
-    static_assert(sizeof(float) * Ti::kRowStep * 2 * L::CB <= sizeof(s) - sizeof(s.mask) - sizeof(s.range), "");
-    __syncthreads();
+    using S = GradShared<LS, CPT>;
+    static_assert(sizeof(float) * Ti::kRowStep * 2 * L::CB <= offsetof(S, mask), "");
     put_floats(&red[threadIdx.x / Ti::kCols][0][Ti::col()], dskip);
     put_floats(&red[threadIdx.x / Ti::kCols][1][Ti::col()], dbias);
     __syncthreads();
@@ -564,9 +590,9 @@ cudaError_t run(const Launch& a, const Cut& c, cudaStream_t st) {
     switch (c.ls) {
         case 1: return go<T, 1, 1>(a, c, st);
         case 2: return wide ? go<T, 2, 2>(a, c, st) : go<T, 2, 1>(a, c, st);
-        case 4: return wide ? go<T, 4, 4>(a, c, st) : go<T, 4, 1>(a, c, st);
-        case 8: return wide ? go<T, 8, 4>(a, c, st) : go<T, 8, 1>(a, c, st);
-        default: return wide ? go<T, 16, 4>(a, c, st) : go<T, 16, 1>(a, c, st);
+        case 4: return wide ? go<T, 4, 2>(a, c, st) : go<T, 4, 1>(a, c, st);
+        case 8: return wide ? go<T, 8, 2>(a, c, st) : go<T, 8, 1>(a, c, st);
+        default: return wide ? go<T, 16, 2>(a, c, st) : go<T, 16, 1>(a, c, st);
     }
 }
 

@@ -33,9 +33,10 @@ __device__ __forceinline__ void put_rows(Shared<LS, CPT>& s, const RowsHeld<T, L
         if (Ti::row(j) >= kTile) continue;
         float d[Ti::V], dx[Ti::V];
 #pragma unroll
-        for (int i = 0; i < Ti::V; ++i) {
-            d[i] = delta_of(dt.at(j, i), bias[i], with_softplus);
-            dx[i] = d[i] * x.at(j, i);
+        for (int i = 0; i < Ti::V; i += 2) {
+            const f2 de = delta_of(dt.pair(j, i), pair_at(bias, i), with_softplus);
+            set_pair(d, i, de);
+            set_pair(dx, i, f2_mul(de, x.pair(j, i)));
         }
         put_floats(&s.delta[Ti::row(j)][Ti::col()], d);
         put_floats(&s.dx[Ti::row(j)][Ti::col()], dx);
@@ -305,13 +306,12 @@ __global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_con
             if (r >= rows || Ti::col() >= b.count) continue;
             float y[Ti::V];
 #pragma unroll
-            for (int i = 0; i < Ti::V; ++i) {
-                y[i] = s.y[r][Ti::col() + i];
-                if (a.in.d != nullptr) y[i] = fmaf(skip[i], x_now.at(j, i), y[i]);
-                if (a.in.z != nullptr) {
-                    const float g = z.at(j, i);
-                    y[i] *= g * sigmoid(g);
-                }
+            for (int i = 0; i < Ti::V; i += 2) {
+                const float* p = &s.y[r][Ti::col() + i];
+                f2 v = f2_of(p[0], p[Ti::V > 1 ? 1 : 0]);
+                if (a.in.d != nullptr) v = f2_fma(pair_at(skip, i), x_now.pair(j, i), v);
+                if (a.in.z != nullptr) v = f2_mul(v, silu(z.pair(j, i)));
+                set_pair(y, i, v);
             }
             store_vec<T, Ti::V>(out + (int64_t)(t0 + r) * a.out_stride, y);
         }

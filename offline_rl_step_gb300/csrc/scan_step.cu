@@ -6,102 +6,143 @@ namespace ofrl {
 namespace scan {
 namespace {
 
-constexpr int kAtOnce = 4;         // channels of a lane group, all in flight
 constexpr int kStepThreads = 128;
 
-// LS lanes have a channel's state, four floats each; a lane group has kAtOnce
-// channels, which share what it loads of B and C.
-template <typename T, int LS>
+// LS lanes share a channel's state, four floats each; a thread has CPT channels,
+// of which it makes one's delta and gate and hands them round.  A CTA keeps its
+// channels (decays, biases) over the tokens it takes, and the next token's state
+// and inputs are on their way while one is worked on.  Bound by HBM: 16384
+// environments, 256 channels of 16 states, bf16: 537 MB of states.
+template <typename T, int LS, int CPT>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const __grid_constant__ StepLaunch a) {
+    constexpr int kChannels = kStepThreads / LS * CPT, kOwn = CPT < LS ? CPT : LS;
+    static_assert(kOwn == CPT, "each channel has a lane that makes its delta");
+    const int d = a.shape.channels, n = a.shape.state_dim, per = d / a.shape.groups;
+    const int lane = (int)threadIdx.x % LS, n0 = lane * 4;
+    const int ch0 = (int)blockIdx.y * kChannels + (int)threadIdx.x / LS * CPT;      // of CPT, in one group
+    const int mine = ch0 + (lane < CPT ? which_channel<LS, CPT>() : 0);
+    const bool on = n0 < n && ch0 < d, own = lane < CPT && mine < d;
+    const int group = min(ch0, d - 1) / per;
     pdl_wait();
     pdl_trigger();
-    constexpr int kGroups = kStepThreads / LS, kChannels = kGroups * kAtOnce;
-    const int d = a.shape.channels, n = a.shape.state_dim, per = d / a.shape.groups;
-    const unsigned slices = (unsigned)(d + kChannels - 1) / kChannels;
-    const int64_t tok = blockIdx.x / slices;
-    const int ch0 = (int)(blockIdx.x % slices) * kChannels + (int)threadIdx.x / LS;
-    const int n0 = (int)threadIdx.x % LS * 4;
-    const bool on = n0 < n;
-    const int32_t slot = a.slot_idx ? a.slot_idx[tok] : (int32_t)tok;
-    T* out = static_cast<T*>(a.out) + tok * a.out_stride;
-    if (slot < 0 || slot >= a.slots) {
-        if (threadIdx.x == 0 && blockIdx.x % slices == 0) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, 1);
-        if (threadIdx.x % LS == 0)
-            for (int i = 0; i < kAtOnce; ++i)
-                if (ch0 + i * kGroups < d) out[ch0 + i * kGroups] = from_float<T>(0.0f);
-        return;
+    float4 a2[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        a2[i] = make_float4(0, 0, 0, 0);
+        if (on) a2[i] = *reinterpret_cast<const float4*>(a.in.a + (int64_t)(ch0 + i) * n + n0);
+        a2[i].x *= kLog2e;
+        a2[i].y *= kLog2e;
+        a2[i].z *= kLog2e;
+        a2[i].w *= kLog2e;
     }
-    const int64_t base = (int64_t)slot * d * n + n0;
-    float4 h[kAtOnce], a2[kAtOnce];
-    float x[kAtOnce], dt[kAtOnce];
+    const float bias = own && a.in.dt_bias != nullptr ? a.in.dt_bias[mine] : 0.0f;
+    const float skip = own && a.in.d != nullptr ? a.in.d[mine] : 0.0f;
+
+    struct Token {
+        float4 h[CPT];
+        Vec<T, 4> b, c;
+        T x, dt, z;
+        int32_t slot;
+    };
+    auto fetch = [&](Token& k, int64_t tok, int32_t slot) {
+        k.slot = slot;
+        if (slot < 0 || slot >= a.slots) return;
+        const float* h = a.state_in + ((int64_t)slot * d + ch0) * n + n0;
+        const T* bp = static_cast<const T*>(a.in.b) + tok * a.in.b_stride + group * n + n0;
+        const T* cp = static_cast<const T*>(a.in.c) + tok * a.in.c_stride + group * n + n0;
+        if (on) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-        const int ch = ch0 + i * kGroups;
-        h[i] = a2[i] = make_float4(0, 0, 0, 0);
-        x[i] = dt[i] = 0.0f;
-        if (ch >= d) continue;
-        if (on) h[i] = __ldcs(reinterpret_cast<const float4*>(a.state_in + base + (int64_t)ch * n));
-        if (on) a2[i] = *reinterpret_cast<const float4*>(a.in.a + (int64_t)ch * n + n0);
-        x[i] = to_float(static_cast<const T*>(a.in.x)[tok * a.in.x_stride + ch]);
-        dt[i] = to_float(static_cast<const T*>(a.in.dt)[tok * a.in.dt_stride + ch]);
-    }
-    int group = -1;
-    float b[4], c[4];
+            for (int i = 0; i < CPT; ++i) k.h[i] = __ldcs(reinterpret_cast<const float4*>(h + (int64_t)i * n));
+            if (a.whole_states) {
+                k.b = *reinterpret_cast<const Vec<T, 4>*>(bp);
+                k.c = *reinterpret_cast<const Vec<T, 4>*>(cp);
+            } else {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-        const int ch = ch0 + i * kGroups;
-        if (ch < d && ch / per != group) {
-            group = ch / per;
-            const T* bp = static_cast<const T*>(a.in.b) + tok * a.in.b_stride + group * n + n0;
-            const T* cp = static_cast<const T*>(a.in.c) + tok * a.in.c_stride + group * n + n0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                b[k] = on ? to_float(bp[k]) : 0.0f;
-                c[k] = on ? to_float(cp[k]) : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    k.b.v[i] = bp[i];
+                    k.c.v[i] = cp[i];
+                }
             }
         }
-        float y = 0.0f;
-        if (ch < d && on) {
-            const float delta = delta_of(dt[i], a.in.dt_bias != nullptr ? a.in.dt_bias[ch] : 0.0f, a.shape.softplus);
-            const float dx = delta * x[i], l = delta * kLog2e;
-            h[i].x = fmaf(exp2_of(l * a2[i].x), h[i].x, dx * b[0]);
-            h[i].y = fmaf(exp2_of(l * a2[i].y), h[i].y, dx * b[1]);
-            h[i].z = fmaf(exp2_of(l * a2[i].z), h[i].z, dx * b[2]);
-            h[i].w = fmaf(exp2_of(l * a2[i].w), h[i].w, dx * b[3]);
-            __stcs(reinterpret_cast<float4*>(a.state_out + base + (int64_t)ch * n), h[i]);
-            y = c[0] * h[i].x + c[1] * h[i].y + c[2] * h[i].z + c[3] * h[i].w;
+        if (own) {
+            k.x = static_cast<const T*>(a.in.x)[tok * a.in.x_stride + mine];
+            k.dt = static_cast<const T*>(a.in.dt)[tok * a.in.dt_stride + mine];
+            if (a.in.z != nullptr) k.z = static_cast<const T*>(a.in.z)[tok * a.in.z_stride + mine];
         }
+    };
+    auto slot_of = [&](int64_t tok) {
+        return tok >= a.in.tokens ? -1 : a.slot_idx != nullptr ? a.slot_idx[tok] : (int32_t)tok;
+    };
+    const int64_t step = gridDim.x;
+    int64_t tok = blockIdx.x;
+    Token next;
+    fetch(next, tok, slot_of(tok));
+    int32_t after = slot_of(tok + step);
+    for (; tok < a.in.tokens; tok += step) {
+        Token k = next;
+        if (tok + step < a.in.tokens) fetch(next, tok + step, after);
+        after = slot_of(tok + 2 * step);
+        T* out = static_cast<T*>(a.out) + tok * a.out_stride + mine;
+        if (k.slot < 0 || k.slot >= a.slots) {
+            if (threadIdx.x == 0 && blockIdx.y == 0) atomicAdd(a.status + OFRL_STAT_BAD_INDEX, 1);
+            if (own) *out = from_float<T>(0.0f);
+            continue;
+        }
+        float delta = 0.0f, dx = 0.0f;
+        if (own) {
+            delta = to_float(k.dt) + bias;
+            if (a.shape.softplus) delta = softplus(delta);
+            dx = delta * to_float(k.x);
+        }
+        float y[CPT];
+        float* h = a.state_out + ((int64_t)k.slot * d + ch0) * n + n0;
 #pragma unroll
-        for (int o = LS / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (ch < d && n0 == 0) {
-            if (a.in.d != nullptr) y = fmaf(a.in.d[ch], x[i], y);
+        for (int i = 0; i < CPT; ++i) {
+            // the lane that made channel i's delta
+            const int from = CPT == 4 ? (i >> 1 & 1) + 2 * (i & 1) : i;
+            const float de = __shfl_sync(0xffffffffu, delta, from, LS), u = __shfl_sync(0xffffffffu, dx, from, LS);
+            float4& v = k.h[i];
+            v.x = fmaf(exp2_of(de * a2[i].x), v.x, u * to_float(k.b.v[0]));
+            v.y = fmaf(exp2_of(de * a2[i].y), v.y, u * to_float(k.b.v[1]));
+            v.z = fmaf(exp2_of(de * a2[i].z), v.z, u * to_float(k.b.v[2]));
+            v.w = fmaf(exp2_of(de * a2[i].w), v.w, u * to_float(k.b.v[3]));
+            if (on) __stcs(reinterpret_cast<float4*>(h + (int64_t)i * n), v);
+            y[i] = on ? to_float(k.c.v[0]) * v.x + to_float(k.c.v[1]) * v.y + to_float(k.c.v[2]) * v.z +
+                            to_float(k.c.v[3]) * v.w
+                      : 0.0f;
+        }
+        float sum = sum_states<LS, CPT>(y);
+        if (own) {
+            if (a.in.d != nullptr) sum = fmaf(skip, to_float(k.x), sum);
             if (a.in.z != nullptr) {
-                const float z = to_float(static_cast<const T*>(a.in.z)[tok * a.in.z_stride + ch]);
-                y *= z * sigmoid(z);
+                const float z = to_float(k.z);
+                sum *= z * sigmoid(z);
             }
-            out[ch] = from_float<T>(y);
+            *out = from_float<T>(sum);
         }
     }
 }
 
-template <typename T, int LS>
+template <typename T, int LS, int CPT>
 cudaError_t go(const StepLaunch& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const int channels = kStepThreads / LS * kAtOnce;
-    const int64_t grid = a.in.tokens * ((a.shape.channels + channels - 1) / channels);
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = opt_in_once(scan_step_kernel<T, LS>, 0, done);
-    return e != cudaSuccess ? e : launch_pdl(scan_step_kernel<T, LS>, dim3((unsigned)grid), dim3(kStepThreads), 0, st, a);
+    constexpr int kChannels = kStepThreads / LS * CPT, kCtasPerSm = 4;
+    const int cols = (a.shape.channels + kChannels - 1) / kChannels;
+    const int64_t most = ((int64_t)a.num_sms * kCtasPerSm + cols - 1) / cols;
+    const int64_t rows = a.in.tokens < most ? a.in.tokens : most;
+    const cudaError_t e = opt_in_once(scan_step_kernel<T, LS, CPT>, 0, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(scan_step_kernel<T, LS, CPT>, dim3((unsigned)rows, (unsigned)cols), dim3(kStepThreads), 0, st, a);
 }
 
 template <typename T>
 cudaError_t run(const StepLaunch& a, cudaStream_t st) {
     switch (lanes_of(a.shape.state_dim)) {
-        case 1: return go<T, 1>(a, st);
-        case 2: return go<T, 2>(a, st);
-        case 4: return go<T, 4>(a, st);
-        case 8: return go<T, 8>(a, st);
-        default: return go<T, 16>(a, st);
+        case 1: return go<T, 1, 1>(a, st);
+        case 2: return go<T, 2, 2>(a, st);
+        case 4: return go<T, 4, 4>(a, st);
+        case 8: return go<T, 8, 4>(a, st);
+        default: return go<T, 16, 4>(a, st);
     }
 }
 
