@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kWarpThreads = 128;        // of a CTA that has a warp or less for a group
 constexpr int kMaxParts = 4096;          // CTAs over rows, at most
+constexpr int kMostShared = 64 * 1024;   // weights and scales of 8192 channels
 
 struct NormArgs {
     const void* x;
@@ -66,46 +67,49 @@ struct NormArgs {
     int channels;
 };
 
-// What a launch's threads are to its rows.  A thread has eight elements of a row,
-// so that these, the next row's and a weight's gradient stay in registers; rows
-// of more than 4096 channels have sixteen, and no row ahead.
+// What a launch's threads are to its rows: a group of channels is a warp's (or
+// less) as long as a lane's elements, `most`, stay in registers, else a CTA's.
 struct NormCut {
     bool cta;
     int threads, tg, nv, groups_at_once;
 };
-NormCut norm_cut(int width, int elem) {
-    const int vecs = width * elem / 16, usual = elem == 2 ? 1 : 2;
+NormCut norm_cut(int width, int elem, bool backward) {
+    const int vec = 16 / elem, vecs = width / vec, most = (backward ? 16 : 32) / vec;
+    const int most_cta = 16 / vec;
     NormCut c;
-    c.cta = vecs > 32 * usual;
+    c.cta = vecs > 32 * most;
     c.tg = c.cta ? 64 : 1;
-    while (c.cta ? c.tg < 512 && c.tg * usual < vecs : c.tg < 32 && c.tg < vecs) c.tg *= 2;
+    while (c.cta ? c.tg * most_cta < vecs : c.tg < 32 && c.tg < vecs) c.tg *= 2;
     c.threads = c.cta ? c.tg : kWarpThreads;
     const int nv = (vecs + c.tg - 1) / c.tg;
-    c.nv = nv <= 1 ? 1 : nv <= 2 ? 2 : 4;
+    c.nv = nv <= 1 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : 8;
     c.groups_at_once = c.threads / c.tg;
     return c;
 }
+// Floats of one weight row in shared memory, as the threads index it.
+__host__ __device__ constexpr int weight_floats(int tg, int nv, int vec) { return tg * nv * vec; }
 
-// Sums of a and b over the group's threads, to all of them.
-template <bool CTA>
-__device__ __forceinline__ void sum_group(float& a, float& b, int tg) {
+// Sums of N values over the group's threads, to all of them.
+template <bool CTA, int N>
+__device__ __forceinline__ void sum_group(float (&v)[N], int tg) {
     if constexpr (!CTA) {
-        for (int o = tg >> 1; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
+        for (int o = tg >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     } else {
-        __shared__ float2 p[16];
-        a = warp_sum(a);
-        b = warp_sum(b);
-        __syncthreads();          // the row before has read its sums
-        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
+        __shared__ float p[16][N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[threadIdx.x >> 5][i] = v[i];
         __syncthreads();
-        a = b = 0.0f;
-        for (int i = 0; i < tg / 32; ++i) {
-            a += p[i].x;
-            b += p[i].y;
-        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.0f;
+        for (int w = 0; w < tg / 32; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += p[w][i];
+        __syncthreads();
     }
 }
 
@@ -165,63 +169,79 @@ __device__ __forceinline__ float rstd_of(float squares, const NormArgs& a) {
     return rsqrtf(squares / (float)a.width + a.eps);
 }
 
-// Rows go by with the next one's loads in flight where AHEAD: fetch(row, on)
-// loads, body(row, on) starts with a copy of what was loaded and then calls the
-// function it is given.
-template <bool AHEAD, bool CTA, typename Fetch, typename Body>
-__device__ __forceinline__ void for_rows(const NormArgs& a, const Seat<CTA>& s, const Fetch& fetch, const Body& body) {
+// The group's weights (and scales) in shared memory, as Part indexes a row; zero
+// past its width.
+template <int V, int NV>
+__device__ __forceinline__ void stage_weights(float* dst, const float* src, const NormArgs& a) {
+    const int n = weight_floats(a.tg, NV, V);
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        dst[i] = i < a.width ? src[(int64_t)blockIdx.y * a.width + i] : 0.0f;
+}
+template <int V>
+struct Weights {
+    const float* p;      // the thread's first element
+    int step;            // floats between its vectors
+    __device__ Weights(const float* base, int lane, int tg) : p(base + lane * V), step(tg * V) {}
+    __device__ f2 pair(int j, int k) const { return *reinterpret_cast<const f2*>(p + j * step + 2 * k); }
+};
+
+// Rows go by, row(i, on) each.  Few elements a thread: the next row's loads are in
+// flight meanwhile (fetch); more of them: other warps' are.
+template <int ELEMENTS, bool CTA, typename Fetch, typename Row>
+__device__ __forceinline__ void for_rows(const NormArgs& a, const Seat<CTA>& s, const Fetch& fetch, const Row& row) {
+    constexpr bool kAhead = ELEMENTS <= 8;
     const int64_t step = (int64_t)gridDim.x * s.at_once;
     int64_t row0 = (int64_t)blockIdx.x * s.at_once;
-    if (AHEAD) fetch(row0 + s.seat, row0 + s.seat < a.rows);
+    if (kAhead) fetch(row0 + s.seat, row0 + s.seat < a.rows);
     for (; row0 < a.rows; row0 += step) {
-        const int64_t row = row0 + s.seat, after = row + step;
-        if (!AHEAD) fetch(row, row < a.rows);
-        body(row, row < a.rows, [&]() {
-            if (AHEAD) fetch(after, after < a.rows);
+        const int64_t i = row0 + s.seat, after = i + step;
+        if (!kAhead) fetch(i, i < a.rows);
+        row(i, i < a.rows, [&]() {
+            if (kAhead) fetch(after, after < a.rows);
         });
     }
 }
-template <typename T, int NV>
-constexpr bool kRowAhead = NV * kVec<T> <= 8;
 
 template <typename T, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
+    extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    Part<float, V, NV> w;
-    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
+    stage_weights<V, NV>(dynamic, a.weight, a);
+    __syncthreads();
+    const Weights<V> w(dynamic, s.lane, a.tg);
     Part<T, V, NV> next_x, next_z;
     auto fetch = [&](int64_t row, bool on) {
         next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
         next_z.load(a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
     };
-    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+    for_rows<NV * V>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
         Part<T, V, NV> x = next_x, z = next_z;
         loaded();
-        f2 u[NV][V / 2], g[NV][V / 2], sq = f2_both(0.0f);
+        f2 sq = f2_both(0.0f);
+        // the gate first: u = x silu(z) is needed twice and rounded nowhere
+        f2 u[NV][V / 2];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) {
                 u[j][k] = x.pair(j, k);
-                g[j][k] = silu(z.pair(j, k));
-                if (a.gate_first) {
-                    u[j][k] = f2_mul(u[j][k], g[j][k]);
-                    g[j][k] = w.pair(j, k);
-                } else {
-                    g[j][k] = f2_mul(g[j][k], w.pair(j, k));
-                }
+                if (a.gate_first) u[j][k] = f2_mul(u[j][k], silu(z.pair(j, k)));
                 sq = f2_fma(u[j][k], u[j][k], sq);
             }
-        float sum = f2_sum(sq), none = 0.0f;
-        sum_group<CTA>(sum, none, a.tg);
-        const f2 r = f2_both(rstd_of(sum, a));
+        float sum[1] = {f2_sum(sq)};
+        sum_group<CTA>(sum, a.tg);
+        const f2 r = f2_both(rstd_of(sum[0], a));
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) x.set(j, k, f2_mul(f2_mul(u[j][k], r), g[j][k]));
+            for (int k = 0; k < V / 2; ++k) {
+                f2 g = f2_mul(r, w.pair(j, k));
+                if (!a.gate_first) g = f2_mul(g, silu(z.pair(j, k)));
+                x.set(j, k, f2_mul(u[j][k], g));
+            }
         if (on) x.store(a.out, row * a.out_stride + s.col0, s.lane, a.tg, a.width);
     });
 }
@@ -230,19 +250,22 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_kernel(co
 template <typename T, typename R, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
+    extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    Part<float, V, NV> w, scale;
-    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
-    if (a.scale != nullptr) scale.load(a.scale, s.col0, s.lane, a.tg, a.width, true);
+    float* scales = dynamic + weight_floats(a.tg, NV, V);
+    stage_weights<V, NV>(dynamic, a.weight, a);
+    if (a.scale != nullptr) stage_weights<V, NV>(scales, a.scale, a);
+    __syncthreads();
+    const Weights<V> w(dynamic, s.lane, a.tg), scale(scales, s.lane, a.tg);
     Part<T, V, NV> next_x;
     Part<R, V, NV> next_h;
     auto fetch = [&](int64_t row, bool on) {
         next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
         next_h.load(a.residual, row * a.residual_stride + s.col0, s.lane, a.tg, a.width, on);
     };
-    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+    for_rows<NV * V>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
         Part<T, V, NV> x = next_x;
         Part<R, V, NV> res = next_h;
         loaded();
@@ -257,9 +280,9 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_kernel
                 res.set(j, k, h[j][k]);
             }
         if (on) res.store(a.residual_out, row * a.residual_out_stride + s.col0, s.lane, a.tg, a.width);
-        float sum = f2_sum(sq), none = 0.0f;
-        sum_group<CTA>(sum, none, a.tg);
-        const f2 r = f2_both(rstd_of(sum, a));
+        float sum[1] = {f2_sum(sq)};
+        sum_group<CTA>(sum, a.tg);
+        const f2 r = f2_both(rstd_of(sum[0], a));
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -268,43 +291,54 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_kernel
     });
 }
 
-// A column's gradient over the CTA's seats, to the CTA's place in parts.
-template <int V, int NV, bool CTA>
-__device__ __forceinline__ void put_parts(const NormArgs& a, const Seat<CTA>& s, const Part<float, V, NV>& g, int which,
-                                          float* red) {
-    float* out = a.parts + ((int64_t)which * gridDim.x + blockIdx.x) * a.channels + s.col0;
-    if constexpr (CTA) {
-        g.store(out, 0, s.lane, a.tg, a.width);
-    } else {
+// A thread's sums over its rows of one weight's gradient.
+template <int V, int NV>
+struct ColumnSums {
+    f2 v[NV][V / 2];
+    __device__ ColumnSums() {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) v[j][k] = f2_both(0.0f);
+    }
+    // over the CTA's seats, to the CTA's place in parts; red holds a row a seat
+    template <bool CTA>
+    __device__ void put(const NormArgs& a, const Seat<CTA>& s, int which, float* red) const {
+        float* out = a.parts + ((int64_t)which * gridDim.x + blockIdx.x) * a.channels + s.col0;
+        const int row = weight_floats(a.tg, NV, V);
         __syncthreads();
-        const int row = a.tg * NV * V;
-        g.store(red, s.seat * row, s.lane, a.tg, row);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k)
+                *reinterpret_cast<f2*>(red + s.seat * row + (s.lane + j * a.tg) * V + 2 * k) = v[j][k];
         __syncthreads();
         for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-            float v = 0.0f;
-            for (int i = 0; i < s.at_once; ++i) v += red[i * row + c];
-            out[c] = v;
+            float x = 0.0f;
+            for (int i = 0; i < s.at_once; ++i) x += red[i * row + c];
+            out[c] = x;
         }
     }
-}
+};
 
 template <typename T, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
-    __shared__ __align__(16) float red[CTA ? 4 : kWarpThreads * NV * V];
+    extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    Part<float, V, NV> w, dw;
-    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
-    dw.load(a.weight, 0, s.lane, a.tg, a.width, false);      // zero
+    stage_weights<V, NV>(dynamic, a.weight, a);
+    __syncthreads();
+    const Weights<V> w(dynamic, s.lane, a.tg);
+    ColumnSums<V, NV> dw;
     Part<T, V, NV> next_x, next_z, next_g;
     auto fetch = [&](int64_t row, bool on) {
         next_x.load(a.x, row * a.x_stride + s.col0, s.lane, a.tg, a.width, on);
         next_z.load(a.z, row * a.z_stride + s.col0, s.lane, a.tg, a.width, on);
         next_g.load(a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
     };
-    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+    for_rows<NV * V>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
         Part<T, V, NV> x = next_x, z = next_z, g = next_g;
         loaded();
         f2 sq = f2_both(0.0f), ip = f2_both(0.0f);
@@ -321,23 +355,20 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_grad_kern
                 sq = f2_fma(u, u, sq);
                 ip = f2_fma(f2_mul(e, w.pair(j, k)), u, ip);
             }
-        float sum = f2_sum(sq), dot = f2_sum(ip);
-        sum_group<CTA>(sum, dot, a.tg);
-        const float rs = rstd_of(sum, a);
-        const f2 r = f2_both(rs), back = f2_both(-rs * rs * dot / (float)a.width);
+        float sum[2] = {f2_sum(sq), f2_sum(ip)};
+        sum_group<CTA>(sum, a.tg);
+        const float rs = rstd_of(sum[0], a);
+        const f2 r = f2_both(rs), back = f2_both(-rs * rs * sum[1] / (float)a.width);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) {
-                const f2 zv = z.pair(j, k), sg = sigmoid(zv), gate = f2_mul(zv, sg), wv = w.pair(j, k), xv = x.pair(j, k);
-                f2 u = xv, e = g.pair(j, k), dgate;
-                if (a.gate_first)
-                    u = f2_mul(u, gate);
-                else
-                    e = f2_mul(e, gate);
+                const f2 zv = z.pair(j, k), sg = sigmoid(zv), gate = f2_mul(zv, sg), wv = w.pair(j, k), xv = x.pair(j, k),
+                         gv = g.pair(j, k);
+                const f2 u = a.gate_first ? f2_mul(xv, gate) : xv, e = a.gate_first ? gv : f2_mul(gv, gate);
                 const f2 unit = f2_mul(u, r), du = f2_mul(r, f2_fma(e, wv, f2_mul(u, back)));
-                dw.set(j, k, f2_fma(e, unit, dw.pair(j, k)));
-                dgate = a.gate_first ? f2_mul(du, xv) : f2_mul(f2_mul(g.pair(j, k), unit), wv);
+                dw.v[j][k] = f2_fma(e, unit, dw.v[j][k]);
+                const f2 dgate = a.gate_first ? f2_mul(du, xv) : f2_mul(f2_mul(gv, unit), wv);
                 x.set(j, k, a.gate_first ? f2_mul(du, gate) : du);
                 z.set(j, k, f2_mul(dgate, silu_slope(zv, sg)));
             }
@@ -346,21 +377,22 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_grad_kern
             z.store(a.dz, row * a.dz_stride + s.col0, s.lane, a.tg, a.width);
         }
     });
-    put_parts<V, NV, CTA>(a, s, dw, 0, red);
+    dw.put(a, s, 0, dynamic);
 }
 
 template <typename T, typename R, int NV, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = kVec<T>;
-    __shared__ __align__(16) float red[CTA ? 4 : kWarpThreads * NV * V];
+    extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
     pdl_trigger();
     const Seat<CTA> s(a);
-    Part<float, V, NV> w, scale, dw, ds;
-    w.load(a.weight, s.col0, s.lane, a.tg, a.width, true);
-    if (a.scale != nullptr) scale.load(a.scale, s.col0, s.lane, a.tg, a.width, true);
-    dw.load(a.weight, 0, s.lane, a.tg, a.width, false);      // zero
-    ds.load(a.weight, 0, s.lane, a.tg, a.width, false);
+    float* scales = dynamic + weight_floats(a.tg, NV, V);
+    stage_weights<V, NV>(dynamic, a.weight, a);
+    if (a.scale != nullptr) stage_weights<V, NV>(scales, a.scale, a);
+    __syncthreads();
+    const Weights<V> w(dynamic, s.lane, a.tg), scale(scales, s.lane, a.tg);
+    ColumnSums<V, NV> dw, ds;
     Part<T, V, NV> next_x, next_g;
     Part<R, V, NV> next_h, next_d;
     auto fetch = [&](int64_t row, bool on) {
@@ -369,32 +401,36 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_grad_k
         next_g.load(a.dout, row * a.dout_stride + s.col0, s.lane, a.tg, a.width, on);
         next_d.load(a.dres, row * a.dres_stride + s.col0, s.lane, a.tg, a.width, on && a.dres != nullptr);
     };
-    for_rows<kRowAhead<T, NV>>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
+    for_rows<NV * V>(a, s, fetch, [&](int64_t row, bool on, auto loaded) {
         Part<T, V, NV> x = next_x, g = next_g;
         Part<R, V, NV> res = next_h, d = next_d;
         loaded();
-        f2 h[NV][V / 2], sq = f2_both(0.0f), ip = f2_both(0.0f);
+        f2 sq = f2_both(0.0f), ip = f2_both(0.0f);
+        auto sum_of = [&](int j, int k) {
+            return a.scale != nullptr ? f2_fma(scale.pair(j, k), x.pair(j, k), res.pair(j, k))
+                                      : f2_add(x.pair(j, k), res.pair(j, k));
+        };
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) {
-                h[j][k] = a.scale != nullptr ? f2_fma(scale.pair(j, k), x.pair(j, k), res.pair(j, k))
-                                             : f2_add(x.pair(j, k), res.pair(j, k));
-                sq = f2_fma(h[j][k], h[j][k], sq);
-                ip = f2_fma(f2_mul(g.pair(j, k), w.pair(j, k)), h[j][k], ip);
+                const f2 h = sum_of(j, k);
+                sq = f2_fma(h, h, sq);
+                ip = f2_fma(f2_mul(g.pair(j, k), w.pair(j, k)), h, ip);
             }
-        float sum = f2_sum(sq), dot = f2_sum(ip);
-        sum_group<CTA>(sum, dot, a.tg);
-        const float rs = rstd_of(sum, a);
-        const f2 r = f2_both(rs), back = f2_both(-rs * rs * dot / (float)a.width);
+        float sum[2] = {f2_sum(sq), f2_sum(ip)};
+        sum_group<CTA>(sum, a.tg);
+        const float rs = rstd_of(sum[0], a);
+        const f2 r = f2_both(rs), back = f2_both(-rs * rs * sum[1] / (float)a.width);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) {
-                const f2 gv = g.pair(j, k), dh = f2_fma(r, f2_fma(gv, w.pair(j, k), f2_mul(h[j][k], back)), d.pair(j, k));
-                dw.set(j, k, f2_fma(gv, f2_mul(h[j][k], r), dw.pair(j, k)));
+                const f2 h = sum_of(j, k), gv = g.pair(j, k);
+                const f2 dh = f2_fma(r, f2_fma(gv, w.pair(j, k), f2_mul(h, back)), d.pair(j, k));
+                dw.v[j][k] = f2_fma(gv, f2_mul(h, r), dw.v[j][k]);
                 if (a.scale != nullptr) {
-                    ds.set(j, k, f2_fma(dh, x.pair(j, k), ds.pair(j, k)));
+                    ds.v[j][k] = f2_fma(dh, x.pair(j, k), ds.v[j][k]);
                     x.set(j, k, f2_mul(scale.pair(j, k), dh));
                 } else {
                     x.set(j, k, dh);
@@ -406,8 +442,8 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_grad_k
             d.store(a.dresidual, row * a.dresidual_stride + s.col0, s.lane, a.tg, a.width);
         }
     });
-    put_parts<V, NV, CTA>(a, s, dw, 0, red);
-    if (a.scale != nullptr) put_parts<V, NV, CTA>(a, s, ds, 1, red);
+    dw.put(a, s, 0, dynamic);
+    if (a.scale != nullptr) ds.put(a, s, 1, dynamic);
 }
 
 // Weight gradients over the CTAs: 32 columns a CTA, 32 threads to a column.
@@ -438,12 +474,14 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const __grid_co
     out[c] = v;
 }
 
-// fn<.., NV, CTA> for a cut (bf16 rows never have four vectors a thread).
-#define OFRL_NORM_PICK(c, fn, ...)                                                                                 \
-    ((c).cta ? ((c).nv == 1 ? fn<__VA_ARGS__, 1, true> : fn<__VA_ARGS__, 2, true>)                                 \
-             : ((c).nv == 1 ? fn<__VA_ARGS__, 1, false> : fn<__VA_ARGS__, 2, false>))
-#define OFRL_NORM_PICK4(c, fn, ...)                                                                                \
-    ((c).nv < 4 ? OFRL_NORM_PICK(c, fn, __VA_ARGS__) : (c).cta ? fn<__VA_ARGS__, 4, true> : fn<__VA_ARGS__, 4, false>)
+// fn<.., NV, CTA> for a cut: a CTA's threads have `cta` vectors each, a lane one,
+// two, four or eight, up to `most`.
+#define OFRL_NORM_PICK(c, cta_nv, most, fn, ...)                                                                   \
+    ((c).cta        ? fn<__VA_ARGS__, cta_nv, true>                                                                \
+     : (c).nv == 1  ? fn<__VA_ARGS__, 1, false>                                                                    \
+     : (c).nv == 2  ? fn<__VA_ARGS__, 2, false>                                                                    \
+     : (c).nv == 4  ? fn<__VA_ARGS__, most < 4 ? most : 4, false>                                                  \
+                    : fn<__VA_ARGS__, most, false>)
 
 using NormKernel = void (*)(NormArgs);
 
@@ -455,24 +493,37 @@ int rows_grid(int64_t rows, const NormCut& c, int groups, int num_sms, int per_s
     return (int)(all < 1 ? 1 : all < most ? all : most);
 }
 
-cudaError_t launch_rows(NormKernel kernel, const NormArgs& a, const NormCut& c, int groups, int grid, cudaStream_t st) {
-    return launch_pdl(kernel, dim3((unsigned)grid, (unsigned)groups), dim3(c.threads), 0, st, a);
-}
-
 NormKernel forward_kernel(const ofrl_norm_shape& s, const NormCut& c, bool gated) {
     const bool f = s.dtype == OFRL_DTYPE_F32, rf = s.residual_dtype == OFRL_DTYPE_F32;
-    if (gated) return f ? OFRL_NORM_PICK4(c, gated_norm_kernel, float) : OFRL_NORM_PICK(c, gated_norm_kernel, __nv_bfloat16);
-    if (f) return OFRL_NORM_PICK4(c, residual_norm_kernel, float, float);
-    return rf ? OFRL_NORM_PICK(c, residual_norm_kernel, __nv_bfloat16, float)
-              : OFRL_NORM_PICK(c, residual_norm_kernel, __nv_bfloat16, __nv_bfloat16);
+    if (gated)
+        return f ? OFRL_NORM_PICK(c, 4, 8, gated_norm_kernel, float) : OFRL_NORM_PICK(c, 2, 4, gated_norm_kernel, __nv_bfloat16);
+    if (f) return OFRL_NORM_PICK(c, 4, 8, residual_norm_kernel, float, float);
+    return rf ? OFRL_NORM_PICK(c, 2, 4, residual_norm_kernel, __nv_bfloat16, float)
+              : OFRL_NORM_PICK(c, 2, 4, residual_norm_kernel, __nv_bfloat16, __nv_bfloat16);
 }
 NormKernel backward_kernel(const ofrl_norm_shape& s, const NormCut& c, bool gated) {
     const bool f = s.dtype == OFRL_DTYPE_F32, rf = s.residual_dtype == OFRL_DTYPE_F32;
     if (gated)
-        return f ? OFRL_NORM_PICK4(c, gated_norm_grad_kernel, float) : OFRL_NORM_PICK(c, gated_norm_grad_kernel, __nv_bfloat16);
-    if (f) return OFRL_NORM_PICK4(c, residual_norm_grad_kernel, float, float);
-    return rf ? OFRL_NORM_PICK(c, residual_norm_grad_kernel, __nv_bfloat16, float)
-              : OFRL_NORM_PICK(c, residual_norm_grad_kernel, __nv_bfloat16, __nv_bfloat16);
+        return f ? OFRL_NORM_PICK(c, 4, 4, gated_norm_grad_kernel, float)
+                 : OFRL_NORM_PICK(c, 2, 2, gated_norm_grad_kernel, __nv_bfloat16);
+    if (f) return OFRL_NORM_PICK(c, 4, 4, residual_norm_grad_kernel, float, float);
+    return rf ? OFRL_NORM_PICK(c, 2, 2, residual_norm_grad_kernel, __nv_bfloat16, float)
+              : OFRL_NORM_PICK(c, 2, 2, residual_norm_grad_kernel, __nv_bfloat16, __nv_bfloat16);
+}
+
+NormCut cut_of(const ofrl_norm_shape& s, bool backward) {
+    return norm_cut(s.channels / s.groups, (int)dtype_size(s.dtype), backward);
+}
+// Shared memory of a launch: weights and scales, later (gradients) a row a seat.
+int shared_of(const ofrl_norm_shape& s, const NormCut& c) {
+    const int row = weight_floats(c.tg, c.nv, 16 / (int)dtype_size(s.dtype));
+    return 4 * row * (c.groups_at_once > 2 ? c.groups_at_once : 2);
+}
+
+cudaError_t launch_rows(const ofrl_norm_shape& s, bool gated, bool backward, const NormArgs& a, const NormCut& c, int grid,
+                        cudaStream_t st) {
+    NormKernel k = backward ? backward_kernel(s, c, gated) : forward_kernel(s, c, gated);
+    return launch_pdl(k, dim3((unsigned)grid, (unsigned)s.groups), dim3(c.threads), (size_t)shared_of(s, c), st, a);
 }
 
 ofrl_status check_shape(const ofrl_norm_shape* s) {
@@ -518,9 +569,6 @@ NormArgs base_args(const ofrl_norm* ctx, const NormCut& c) {
     a.parts = ctx->parts;
     return a;
 }
-NormCut cut_of(const ofrl_norm* ctx) {
-    return norm_cut(ctx->shape.channels / ctx->shape.groups, (int)dtype_size(ctx->shape.dtype));
-}
 NormArgs args_of(const ofrl_norm* ctx, const NormCut& c, const ofrl_gated_rows* in) {
     NormArgs a = base_args(ctx, c);
     a.x = in->x;
@@ -548,14 +596,13 @@ NormArgs args_of(const ofrl_norm* ctx, const NormCut& c, const ofrl_residual_row
 
 ofrl_status run_forward(const ofrl_norm* ctx, const NormCut& c, const NormArgs& a, bool gated, cudaStream_t st) {
     if (a.rows == 0) return OFRL_OK;
-    const int groups = ctx->shape.groups;
-    return cuda_status(launch_rows(forward_kernel(ctx->shape, c, gated), a, c, groups,
-                                   rows_grid(a.rows, c, groups, ctx->num_sms, ctx->per_sm[gated][0]), st));
+    const int grid = rows_grid(a.rows, c, ctx->shape.groups, ctx->num_sms, ctx->per_sm[gated][0]);
+    return cuda_status(launch_rows(ctx->shape, gated, false, a, c, grid, st));
 }
 ofrl_status run_backward(const ofrl_norm* ctx, const NormCut& c, const NormArgs& a, bool gated, float* dweight,
                          float* dscale, cudaStream_t st) {
-    const int groups = ctx->shape.groups, grid = rows_grid(a.rows, c, groups, ctx->num_sms, ctx->per_sm[gated][1]);
-    cudaError_t e = launch_rows(backward_kernel(ctx->shape, c, gated), a, c, groups, grid, st);
+    const int grid = rows_grid(a.rows, c, ctx->shape.groups, ctx->num_sms, ctx->per_sm[gated][1]);
+    cudaError_t e = launch_rows(ctx->shape, gated, true, a, c, grid, st);
     if (e == cudaSuccess) {
         NormJoin j;
         j.parts = a.parts;
@@ -571,17 +618,19 @@ ofrl_status run_backward(const ofrl_norm* ctx, const NormCut& c, const NormArgs&
 
 int64_t norm_bytes(const ofrl_norm_shape& s, int num_sms, int per_sm, bool backward) {
     if (!backward) return 256;
-    const NormCut c = norm_cut(s.channels / s.groups, (int)dtype_size(s.dtype));
-    return 256 + 2 * (int64_t)rows_grid(INT32_MAX, c, s.groups, num_sms, per_sm) * s.channels * 4;
+    return 256 + 2 * (int64_t)rows_grid(INT32_MAX, cut_of(s, true), s.groups, num_sms, per_sm) * s.channels * 4;
 }
-// CTAs of each kernel that an SM holds.
+// CTAs of each kernel that an SM holds; opts the kernels into their shared memory.
 cudaError_t find_per_sm(const ofrl_norm_shape& s, int (&per_sm)[2][2]) {
-    const NormCut c = norm_cut(s.channels / s.groups, (int)dtype_size(s.dtype));
     cudaError_t e = cudaSuccess;
     for (int gated = 0; gated < 2; ++gated)
         for (int back = 0; back < 2; ++back) {
+            const NormCut c = cut_of(s, back != 0);
             NormKernel k = back ? backward_kernel(s, c, gated != 0) : forward_kernel(s, c, gated != 0);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[gated][back], k, c.threads, 0);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+            if (e == cudaSuccess) e = set_max_shared_carveout(k);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm[gated][back], k, c.threads, (size_t)shared_of(s, c));
             if (per_sm[gated][back] < 1) per_sm[gated][back] = 1;
         }
     return e;
@@ -639,7 +688,7 @@ ofrl_status ofrl_gated_norm(ofrl_norm* ctx, const ofrl_gated_rows* in, void* out
     const ofrl_status s = check_gated(ctx, in);
     if (s != OFRL_OK) return s;
     if (in->rows > 0 && !rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
-    const NormCut c = cut_of(ctx);
+    const NormCut c = cut_of(ctx->shape, false);
     NormArgs a = args_of(ctx, c, in);
     a.out = out;
     a.out_stride = out_stride;
@@ -656,7 +705,7 @@ ofrl_status ofrl_gated_norm_backward(ofrl_norm* ctx, const ofrl_gated_rows* in, 
     if (in->rows > 0 &&
         (!rows_ok(dout, dout_stride, d, e) || !rows_ok(dx, dx_stride, d, e) || !rows_ok(dz, dz_stride, d, e)))
         return OFRL_EINVAL;
-    const NormCut c = cut_of(ctx);
+    const NormCut c = cut_of(ctx->shape, true);
     NormArgs a = args_of(ctx, c, in);
     a.dout = dout;
     a.dout_stride = dout_stride;
@@ -675,7 +724,7 @@ ofrl_status ofrl_residual_norm(ofrl_norm* ctx, const ofrl_residual_rows* in, voi
     if (in->rows > 0 && (!rows_ok(out, out_stride, d, dtype_size(ctx->shape.dtype)) ||
                          !rows_ok(residual_out, residual_out_stride, d, dtype_size(ctx->shape.residual_dtype))))
         return OFRL_EINVAL;
-    const NormCut c = cut_of(ctx);
+    const NormCut c = cut_of(ctx->shape, false);
     NormArgs a = args_of(ctx, c, in);
     a.residual_out = residual_out;
     a.residual_out_stride = residual_out_stride;
@@ -698,7 +747,7 @@ ofrl_status ofrl_residual_norm_backward(ofrl_norm* ctx, const ofrl_residual_rows
                          !rows_ok(dresidual, dresidual_stride, d, re) ||
                          (d_residual_out != nullptr && !rows_ok(d_residual_out, d_residual_out_stride, d, re))))
         return OFRL_EINVAL;
-    const NormCut c = cut_of(ctx);
+    const NormCut c = cut_of(ctx->shape, true);
     NormArgs a = args_of(ctx, c, in);
     a.dout = dout;
     a.dout_stride = dout_stride;

@@ -220,66 +220,84 @@ struct Taps {
     }
 };
 
+// A run's inputs come through a ring in shared memory of which every thread has
+// its own column: kRound tokens a group, kDepth groups on their way, no barrier.
+constexpr int kRound = 4, kDepth = 3;
+template <typename T, int V, int N>
+struct Ring {
+    Vec<T, V> slot[N][kDepth][kRound][kThreads];
+};
+
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_constant__ ConvLaunch a) {
-    constexpr int kAtOnce = 4;      // tokens of a round; the next round's inputs are on their way meanwhile
+    constexpr int P = V / 2, kBytes = V * (int)sizeof(T);
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Ring<T, V, 1>& ring = *reinterpret_cast<Ring<T, V, 1>*>(dynamic);
     __shared__ Marks m;
     pdl_wait();
     pdl_trigger();
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
     const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
     const int64_t from = (int64_t)blockIdx.x * runs * a.run;
-    const int s0 = (int)from;
-    make_marks<W>(m, a, s0, from + (int64_t)runs * a.run, blockIdx.y == 0);
+    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, blockIdx.y == 0);
     const int ch = ((int)blockIdx.y * a.lanes + lane) * V;
     const int64_t begin64 = from + (int64_t)y * a.run;
-    const int end = (int)min(begin64 + a.run, (int64_t)m.range.end), begin = (int)min(begin64, (int64_t)end);
+    const int live = m.range.end, end = (int)min(begin64 + a.run, (int64_t)live), begin = (int)min(begin64, (int64_t)end);
     if (ch < d && begin < end) {
+        const int first = max(begin - (W - 1), 0);
+        const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
+        T* out = static_cast<T*>(a.out) + (int64_t)first * a.out_stride + ch;
+        int asked = first, to = 0;      // the next token to be asked for, and its group
+        auto ask = [&]() {
+#pragma unroll
+            for (int i = 0; i < kRound; ++i) {
+                if (asked + i < end) copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
+                in += a.in.x_stride;
+            }
+            copies_commit();
+            asked += kRound;
+            to = to + 1 == kDepth ? 0 : to + 1;
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth - 1; ++i) ask();
         Taps<V, W> taps;
         taps.load(a, ch);
         Window<T, V, W> win;
         win.clear();
-        const T* in = static_cast<const T*>(a.in.x) + ch;
-        T* out = static_cast<T*>(a.out) + ch;
-        const int first = max(begin - (W - 1), 0);
-        Vec<T, V> next[kAtOnce];
-        auto fetch = [&](int t0) {
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (t0 + i < end) next[i] = *reinterpret_cast<const Vec<T, V>*>(in + (int64_t)(t0 + i) * a.in.x_stride);
-        };
-        fetch(first);
-        for (int t0 = first; t0 < end; t0 += kAtOnce) {
-            Vec<T, V> now[kAtOnce];
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) now[i] = next[i];
-            fetch(t0 + kAtOnce);
+        int group = 0;
+        for (int t0 = first; t0 < end; t0 += kRound) {
+            ask();
+            copies_wait<kDepth - 1>();
             const uint32_t starts = m.from(t0);
-            auto token = [&](int i) {
-                f2 x[V / 2];
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) x[k] = vec_pair(now[i], k);
+            auto token = [&](int i, bool write) {
+                const Vec<T, V> u = ring.slot[0][group][i][threadIdx.x];
+                f2 x[P];
                 Vec<T, V> o;
 #pragma unroll
-                for (int k = 0; k < V / 2; ++k) set_vec_pair(o, k, act_of(taps.pre(win, x, k), a.shape.activation));
-                if (t0 + i >= begin) *reinterpret_cast<Vec<T, V>*>(out + (int64_t)(t0 + i) * a.out_stride) = o;
+                for (int k = 0; k < P; ++k) {
+                    x[k] = vec_pair(u, k);
+                    set_vec_pair(o, k, act_of(taps.pre(win, x, k), a.shape.activation));
+                }
+                if (write) *reinterpret_cast<Vec<T, V>*>(out) = o;
+                out += a.out_stride;
                 win.push(x);
             };
-            // the usual round: whole, within an episode
-            if (t0 + kAtOnce <= end && (starts & ((2u << kAtOnce) - 1)) == 0 && t0 + kAtOnce < m.range.end) {
+            // the usual round: whole, within the run and an episode
+            if (t0 >= begin && t0 + kRound <= end && (starts & ((2u << kRound) - 1)) == 0 && t0 + kRound < live) {
 #pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) token(i);
-                continue;
+                for (int i = 0; i < kRound; ++i) token(i, true);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kRound && t0 + i < end; ++i) {
+                    const int t = t0 + i;
+                    if (starts >> i & 1) win.enter(a, t, ch);
+                    token(i, t >= begin);
+                    if (a.final_state != nullptr && t >= begin && m.last(t)) win.leave(a, t, ch);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const int t = t0 + i;
-                if (t >= end) break;
-                if (starts >> i & 1) win.enter(a, t, ch);
-                token(i);
-                if (a.final_state != nullptr && t >= begin && m.last(t)) win.leave(a, t, ch);
-            }
+            group = group + 1 == kDepth ? 0 : group + 1;
         }
+        copies_wait<0>();
     }
     // Episodes without tokens end as they began.
     if (a.final_state != nullptr) {
@@ -303,9 +321,10 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_constant__ ConvLaunch a) {
-    constexpr int V = vec_of(sizeof(T), true), kAtOnce = sizeof(T) == 4 ? 2 : 4, P = V / 2;
+    constexpr int V = vec_of(sizeof(T), true), P = V / 2, kBytes = V * (int)sizeof(T);
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Ring<T, V, 2>& ring = *reinterpret_cast<Ring<T, V, 2>*>(dynamic);
     __shared__ Marks m;
-    __shared__ float red[kThreads * V * (W + 1)];
     pdl_wait();
     pdl_trigger();
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
@@ -322,6 +341,29 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < P; ++k) dw[j][k] = f2_both(0.0f);
     if (ch < d && begin < end) {
+        const int stop = (int)min((int64_t)end + W - 1, (int64_t)live);      // dpre of the tokens after the run
+        const int first = max(begin - (W - 1), 0);
+        const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
+        const T* go = static_cast<const T*>(a.dout) + (int64_t)first * a.dout_stride + ch;
+        // dx of the token W - 1 before, which is complete: not dereferenced before the run begins
+        T* out = static_cast<T*>(a.grads.dx) + (int64_t)(first - (W - 1)) * a.grads.x_stride + ch;
+        int asked = first, to = 0;
+        auto ask = [&]() {
+#pragma unroll
+            for (int i = 0; i < kRound; ++i) {
+                if (asked + i < stop) {
+                    copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
+                    copy_async<kBytes>(&ring.slot[1][to][i][threadIdx.x], go);
+                }
+                in += a.in.x_stride;
+                go += a.dout_stride;
+            }
+            copies_commit();
+            asked += kRound;
+            to = to + 1 == kDepth ? 0 : to + 1;
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth - 1; ++i) ask();
         Taps<V, W> taps;
         taps.load(a, ch);
         Window<T, V, W> win;
@@ -332,39 +374,18 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < P; ++k) pend[j][k] = f2_both(0.0f);
         int age = W;            // tokens since the episode began
-        const T* in = static_cast<const T*>(a.in.x) + ch;
-        const T* go = static_cast<const T*>(a.dout) + ch;
-        T* out = static_cast<T*>(a.grads.dx) + ch;
-        const int stop = (int)min((int64_t)end + W - 1, (int64_t)live);      // dpre of the tokens after the run
-        const int first = max(begin - (W - 1), 0);
-        Vec<T, V> next_x[kAtOnce], next_g[kAtOnce];
-        auto fetch = [&](int t0) {
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (t0 + i < stop) {
-                    next_x[i] = *reinterpret_cast<const Vec<T, V>*>(in + (int64_t)(t0 + i) * a.in.x_stride);
-                    next_g[i] = *reinterpret_cast<const Vec<T, V>*>(go + (int64_t)(t0 + i) * a.dout_stride);
-                }
-        };
-        fetch(first);
+        int group = 0;
         // W - 1 tokens more than the run: their gradients reach back into it
-        for (int t0 = first; t0 < end + W - 1; t0 += kAtOnce) {
-            Vec<T, V> now_x[kAtOnce], now_g[kAtOnce];
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                now_x[i] = next_x[i];
-                now_g[i] = next_g[i];
-            }
-            fetch(t0 + kAtOnce);
+        for (int t0 = first; t0 < end + W - 1; t0 += kRound) {
+            ask();
+            copies_wait<kDepth - 1>();
             const uint32_t starts = m.from(t0);
             // a token's own dx is begun, those before it get their share (as far as `reach` back)
-            auto token = [&](int i, int reach, bool sums, f2 (&own)[P]) {
+            auto token = [&](const f2 (&x)[P], int i, int reach, bool sums, f2 (&own)[P]) {
+                const Vec<T, V> g = ring.slot[1][group][i][threadIdx.x];
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    f2 x[P];
-#pragma unroll
-                    for (int c = 0; c < P; ++c) x[c] = vec_pair(now_x[i], c);
-                    const f2 dp = f2_mul(vec_pair(now_g[i], k), act_slope(taps.pre(win, x, k), a.shape.activation));
+                    const f2 dp = f2_mul(vec_pair(g, k), act_slope(taps.pre(win, x, k), a.shape.activation));
                     own[k] = f2_mul(taps.w[W - 1][k], dp);
 #pragma unroll
                     for (int j = 1; j < W; ++j)
@@ -377,14 +398,19 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
                     }
                 }
             };
-            auto finish = [&](int t, const f2 (&own)[P]) {      // token t - (W - 1) is complete
-                const int done = t - (W - 1);
-                if (done >= begin && done < end) {
+            auto take = [&](int i, f2 (&x)[P]) {
+                const Vec<T, V> u = ring.slot[0][group][i][threadIdx.x];
+#pragma unroll
+                for (int k = 0; k < P; ++k) x[k] = vec_pair(u, k);
+            };
+            auto finish = [&](bool write, const f2 (&own)[P]) {      // the token W - 1 before is complete
+                if (write) {
                     Vec<T, V> o;
 #pragma unroll
                     for (int k = 0; k < P; ++k) set_vec_pair(o, k, pend[0][k]);
-                    *reinterpret_cast<Vec<T, V>*>(out + (int64_t)done * a.grads.x_stride) = o;
+                    *reinterpret_cast<Vec<T, V>*>(out) = o;
                 }
+                out += a.grads.x_stride;
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
@@ -392,57 +418,59 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < P; ++k) pend[W - 2][k] = own[k];
             };
-            auto advance = [&](int i) {
-                f2 x[P];
-#pragma unroll
-                for (int k = 0; k < P; ++k) x[k] = vec_pair(now_x[i], k);
-                win.push(x);
-            };
             // the usual round: whole, within the run and an episode, no gradient of a final state
-            if (t0 >= begin && t0 + kAtOnce <= end && (starts & ((1u << kAtOnce) - 1)) == 0 && a.d_final == nullptr &&
+            if (t0 >= begin + W - 1 && t0 + kRound <= end && (starts & ((1u << kRound) - 1)) == 0 && a.d_final == nullptr &&
                 age >= W - 1) {
 #pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    f2 own[P];
-                    token(i, W - 1, true, own);
-                    advance(i);
-                    finish(t0 + i, own);
+                for (int i = 0; i < kRound; ++i) {
+                    f2 own[P], x[P];
+                    take(i, x);
+                    token(x, i, W - 1, true, own);
+                    win.push(x);
+                    finish(true, own);
                 }
-                continue;
-            }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kRound; ++i) {
+                    const int t = t0 + i, done = t - (W - 1);
+                    f2 own[P], x[P];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const int t = t0 + i;
-                f2 own[P];
+                    for (int k = 0; k < P; ++k) own[k] = f2_both(0.0f);
+                    if (t < stop) {
+                        take(i, x);
+                        if (starts >> i & 1) {
+                            win.enter(a, t, ch);
+                            age = 0;
+                        }
+                        if (t >= begin) {
+                            token(x, i, age, t < end, own);
+                            if (a.d_final != nullptr && t < end) {
+                                int left = 0;      // tokens of the episode from t on, up to W - 1; 0: more
+                                for (int j = 1; j < W && left == 0; ++j)
+                                    if (t + j <= live && m.last(t + j - 1)) left = j;
+                                if (left > 0) {
+                                    const int e = episode_at(a.ends, a.episodes, tokens, t);
+                                    const T* p = static_cast<const T*>(a.d_final) + ((int64_t)e * d + ch) * (W - 1) + W - 1 - left;
 #pragma unroll
-                for (int k = 0; k < P; ++k) own[k] = f2_both(0.0f);
-                if (t < stop) {
-                    if (starts >> i & 1) {
-                        win.enter(a, t, ch);
-                        age = 0;
-                    }
-                    if (t >= begin) {
-                        token(i, age, t < end, own);
-                        if (a.d_final != nullptr && t < end) {
-                            int left = 0;      // tokens of the episode from t on, up to W - 1; 0: more
-                            for (int j = 1; j < W && left == 0; ++j)
-                                if (t + j <= live && m.last(t + j - 1)) left = j;
-                            if (left > 0) {
-                                const int e = episode_at(a.ends, a.episodes, tokens, t);
-                                const T* p = static_cast<const T*>(a.d_final) + ((int64_t)e * d + ch) * (W - 1) + W - 1 - left;
-#pragma unroll
-                                for (int k = 0; k < P; ++k)
-                                    own[k] = f2_add(own[k], f2_of(to_float(p[2 * k * (W - 1)]), to_float(p[(2 * k + 1) * (W - 1)])));
+                                    for (int k = 0; k < P; ++k)
+                                        own[k] = f2_add(own[k], f2_of(to_float(p[2 * k * (W - 1)]),
+                                                                      to_float(p[(2 * k + 1) * (W - 1)])));
+                                }
                             }
                         }
+                        win.push(x);
+                        age = min(age + 1, W);
                     }
-                    advance(i);
-                    age = min(age + 1, W);
+                    finish(done >= begin && done < end, own);
                 }
-                finish(t, own);
             }
+            group = group + 1 == kDepth ? 0 : group + 1;
         }
+        copies_wait<0>();
     }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(dynamic);
+    static_assert(sizeof(Ring<T, V, 2>) >= sizeof(float) * kThreads * V * (W + 1), "");
     // over the CTA's runs
     const int row = a.lanes * V * (W + 1);
 #pragma unroll
@@ -602,9 +630,10 @@ cudaError_t forward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
     a.lanes = c.lanes;
     a.run = c.run;
     if (c.rows > INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = opt_in_once(conv_forward_kernel<T, W, V>, 0, done);
+    const cudaError_t e = opt_in_once(conv_forward_kernel<T, W, V>, (int)sizeof(Ring<T, V, 1>), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(conv_forward_kernel<T, W, V>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
+    return launch_pdl(conv_forward_kernel<T, W, V>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads),
+                      sizeof(Ring<T, V, 1>), st, a);
 }
 
 template <typename T, int W>
@@ -615,10 +644,11 @@ cudaError_t backward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
     a.lanes = c.lanes;
     a.run = c.run;
     const int64_t outs = (int64_t)a.shape.channels * (W + 1);
-    cudaError_t e = opt_in_once(conv_grad_kernel<T, W>, 0, done);
+    using R = Ring<T, vec_of(sizeof(T), true), 2>;
+    cudaError_t e = opt_in_once(conv_grad_kernel<T, W>, (int)sizeof(R), done);
     if (e == cudaSuccess) e = opt_in_once(conv_join_kernel, 0, join_done);
     if (e == cudaSuccess)
-        e = launch_pdl(conv_grad_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), 0, st, a);
+        e = launch_pdl(conv_grad_kernel<T, W>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads), sizeof(R), st, a);
     if (e == cudaSuccess)
         e = launch_pdl(conv_join_kernel, dim3((unsigned)((outs + 31) / 32)), dim3(kJoinThreads), 0, st, a, c.rows);
     if (e == cudaSuccess && a.d_init != nullptr) {

@@ -44,6 +44,21 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
     *reinterpret_cast<Vec<T, V>*>(p) = u;
 }
 
+// Asynchronous copies of BYTES (4, 8 or 16) to shared memory, in groups.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // ---- pairs of fp32 -------------------------------------------------------------
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 f2_of(float lo, float hi) {
@@ -95,14 +110,18 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Elements 2 i and 2 i + 1 of a raw vector, and a vector from pairs.
 template <typename T, int V>
 __device__ __forceinline__ f2 vec_pair(const Vec<T, V>& u, int i) {
-    return f2_of(to_float(u.v[2 * i]), to_float(u.v[2 * i + 1]));
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(u.v)[i];
+        return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    } else {
+        return f2_of(u.v[2 * i], u.v[2 * i + 1]);
+    }
 }
 template <typename T, int V>
 __device__ __forceinline__ void set_vec_pair(Vec<T, V>& u, int i, f2 x) {
     if constexpr (sizeof(T) == 2) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(x), f2_hi(x));
-        u.v[2 * i] = h.x;
-        u.v[2 * i + 1] = h.y;
+        reinterpret_cast<uint32_t*>(u.v)[i] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
         u.v[2 * i] = f2_lo(x);
         u.v[2 * i + 1] = f2_hi(x);
@@ -177,7 +196,7 @@ inline cudaError_t opt_in_once(K kernel, int smem, std::atomic<uint64_t>& done) 
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (device & 63);
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = set_max_shared_carveout(kernel);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
