@@ -37,7 +37,7 @@ constexpr int kThreads = 256;
 // Channels of a thread: 16 bytes of them forward, four for gradients, whose
 // taps, windows and sums would not stay in registers.
 constexpr int vec_of(int elem, bool backward) { return elem == 4 || backward ? 4 : 8; }
-constexpr int kMinRun = 8, kMaxRun = 64;
+constexpr int kMinRun = 8, kMaxRun = 256, kCtasPerSm = 2;
 constexpr int kMaskWords = kThreads * kMaxRun / 32 + 4;
 
 struct ConvLaunch {
@@ -77,28 +77,29 @@ struct ConvStepLaunch {
 struct ConvCut {
     int lanes, run, cols;      // cols: CTAs along a row
     int64_t rows;              // CTAs over the tokens, at least 1
+    int64_t fill;              // CTAs over the tokens that fill the GPU once
 };
+int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 ConvCut conv_cut(int channels, int vec, int64_t tokens, int num_sms) {
     ConvCut c;
     const int vecs = channels / vec;
     c.lanes = 1;
     while (c.lanes < 32 && c.lanes < vecs) c.lanes *= 2;
-    c.cols = (vecs + c.lanes - 1) / c.lanes;
-    const int64_t runs = kThreads / c.lanes, target = (int64_t)num_sms * 8 / c.cols + 1;
-    c.run = kMinRun;
-    while (c.run < kMaxRun && (tokens + runs * c.run - 1) / (runs * c.run) > target) c.run *= 2;
-    c.rows = (tokens + runs * c.run - 1) / (runs * c.run);
+    c.cols = (int)div_up(vecs, c.lanes);
+    const int64_t runs = kThreads / c.lanes;
+    c.fill = div_up((int64_t)num_sms * kCtasPerSm, c.cols);
+    const int64_t run = div_up(div_up(tokens, runs * c.fill), kMinRun) * kMinRun;
+    c.run = (int)(run < kMinRun ? kMinRun : run > kMaxRun ? kMaxRun : run);
+    c.rows = div_up(tokens, runs * c.run);
     if (c.rows < 1) c.rows = 1;
     return c;
 }
 // CTAs over the tokens of any call of at most max_tokens: at the longest run, or
-// no more than the target.
+// no more than fill the GPU.
 int64_t conv_rows_most(int channels, int vec, int64_t max_tokens, int num_sms) {
     const ConvCut c = conv_cut(channels, vec, max_tokens, num_sms);
-    const int64_t runs = kThreads / c.lanes, target = (int64_t)num_sms * 8 / c.cols + 1;
-    const int64_t longest = (max_tokens + runs * kMaxRun - 1) / (runs * kMaxRun),
-                  shortest = (max_tokens + runs * kMinRun - 1) / (runs * kMinRun);
-    const int64_t few = target < shortest ? target : shortest;
+    const int64_t runs = kThreads / c.lanes, longest = div_up(max_tokens, runs * kMaxRun),
+                  shortest = div_up(max_tokens, runs * kMinRun), few = c.fill < shortest ? c.fill : shortest;
     return longest > few ? longest : few > 1 ? few : 1;
 }
 
@@ -239,27 +240,28 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
     const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
     const int64_t from = (int64_t)blockIdx.x * runs * a.run;
-    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, blockIdx.y == 0);
     const int ch = ((int)blockIdx.y * a.lanes + lane) * V;
     const int64_t begin64 = from + (int64_t)y * a.run;
+    // inputs are asked for before it is known which tokens episodes have
+    const int bound = (int)min(begin64 + a.run, (int64_t)tokens), first = (int)min(max(begin64 - (W - 1), (int64_t)0), (int64_t)tokens);
+    const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
+    int left = bound - first, to = 0;      // tokens to be asked for yet, the next ones' group
+    auto ask = [&]() {
+#pragma unroll
+        for (int i = 0; i < kRound; ++i) {
+            if (ch < d && i < left) copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
+            in += a.in.x_stride;
+        }
+        copies_commit();
+        left -= kRound;
+        to = to + 1 == kDepth ? 0 : to + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) ask();
+    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, blockIdx.y == 0);
     const int live = m.range.end, end = (int)min(begin64 + a.run, (int64_t)live), begin = (int)min(begin64, (int64_t)end);
     if (ch < d && begin < end) {
-        const int first = max(begin - (W - 1), 0);
-        const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
         T* out = static_cast<T*>(a.out) + (int64_t)first * a.out_stride + ch;
-        int asked = first, to = 0;      // the next token to be asked for, and its group
-        auto ask = [&]() {
-#pragma unroll
-            for (int i = 0; i < kRound; ++i) {
-                if (asked + i < end) copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
-                in += a.in.x_stride;
-            }
-            copies_commit();
-            asked += kRound;
-            to = to + 1 == kDepth ? 0 : to + 1;
-        };
-#pragma unroll
-        for (int i = 0; i < kDepth - 1; ++i) ask();
         Taps<V, W> taps;
         taps.load(a, ch);
         Window<T, V, W> win;
@@ -297,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_
             }
             group = group + 1 == kDepth ? 0 : group + 1;
         }
-        copies_wait<0>();
     }
+    copies_wait<0>();
     // Episodes without tokens end as they began.
     if (a.final_state != nullptr) {
         const int ln = threadIdx.x & 31;
@@ -330,9 +332,29 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
     const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
     const int64_t from = (int64_t)blockIdx.x * runs * a.run;
-    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, false);
     const int ch = ((int)blockIdx.y * a.lanes + lane) * V;
     const int64_t begin64 = from + (int64_t)y * a.run;
+    const int bound = (int)min(begin64 + a.run + W - 1, (int64_t)tokens), first = (int)min(max(begin64 - (W - 1), (int64_t)0), (int64_t)tokens);
+    const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
+    const T* go = static_cast<const T*>(a.dout) + (int64_t)first * a.dout_stride + ch;
+    int left = bound - first, to = 0;      // tokens to be asked for yet, the next ones' group
+    auto ask = [&]() {
+#pragma unroll
+        for (int i = 0; i < kRound; ++i) {
+            if (ch < d && i < left) {
+                copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
+                copy_async<kBytes>(&ring.slot[1][to][i][threadIdx.x], go);
+            }
+            in += a.in.x_stride;
+            go += a.dout_stride;
+        }
+        copies_commit();
+        left -= kRound;
+        to = to + 1 == kDepth ? 0 : to + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) ask();
+    make_marks<W>(m, a, (int)from, from + (int64_t)runs * a.run, false);
     const int live = m.range.end;
     const int end = (int)min(begin64 + a.run, (int64_t)live), begin = (int)min(begin64, (int64_t)end);
     f2 dw[W + 1][P];      // the taps, then the bias
@@ -342,28 +364,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
         for (int k = 0; k < P; ++k) dw[j][k] = f2_both(0.0f);
     if (ch < d && begin < end) {
         const int stop = (int)min((int64_t)end + W - 1, (int64_t)live);      // dpre of the tokens after the run
-        const int first = max(begin - (W - 1), 0);
-        const T* in = static_cast<const T*>(a.in.x) + (int64_t)first * a.in.x_stride + ch;
-        const T* go = static_cast<const T*>(a.dout) + (int64_t)first * a.dout_stride + ch;
         // dx of the token W - 1 before, which is complete: not dereferenced before the run begins
         T* out = static_cast<T*>(a.grads.dx) + (int64_t)(first - (W - 1)) * a.grads.x_stride + ch;
-        int asked = first, to = 0;
-        auto ask = [&]() {
-#pragma unroll
-            for (int i = 0; i < kRound; ++i) {
-                if (asked + i < stop) {
-                    copy_async<kBytes>(&ring.slot[0][to][i][threadIdx.x], in);
-                    copy_async<kBytes>(&ring.slot[1][to][i][threadIdx.x], go);
-                }
-                in += a.in.x_stride;
-                go += a.dout_stride;
-            }
-            copies_commit();
-            asked += kRound;
-            to = to + 1 == kDepth ? 0 : to + 1;
-        };
-#pragma unroll
-        for (int i = 0; i < kDepth - 1; ++i) ask();
         Taps<V, W> taps;
         taps.load(a, ch);
         Window<T, V, W> win;
@@ -466,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
             }
             group = group + 1 == kDepth ? 0 : group + 1;
         }
-        copies_wait<0>();
     }
+    copies_wait<0>();
     __syncthreads();
     float* red = reinterpret_cast<float*>(dynamic);
     static_assert(sizeof(Ring<T, V, 2>) >= sizeof(float) * kThreads * V * (W + 1), "");
@@ -482,11 +484,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_grad_kernel(const __grid_con
             p[W + 1] = f2_hi(dw[j][k]);
         }
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.y * row, all = (int64_t)d * (W + 1);
-    for (int i = threadIdx.x; i < row && first + i < all; i += kThreads) {
+    const int64_t first_out = (int64_t)blockIdx.y * row, all = (int64_t)d * (W + 1);
+    for (int i = threadIdx.x; i < row && first_out + i < all; i += kThreads) {
         float v = 0.0f;
         for (int k = 0; k < runs; ++k) v += red[k * row + i];
-        a.parts[blockIdx.x * all + first + i] = v;
+        a.parts[blockIdx.x * all + first_out + i] = v;
     }
 }
 

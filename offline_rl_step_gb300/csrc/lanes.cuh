@@ -59,6 +59,11 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// Asks for `bytes` (a multiple of 16, 16-byte aligned) to be brought into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ---- pairs of fp32 -------------------------------------------------------------
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 f2_of(float lo, float hi) {
