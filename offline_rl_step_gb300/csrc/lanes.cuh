@@ -156,7 +156,7 @@ __device__ __forceinline__ float max_or_nan(float x, float y) {
 // polynomial fitted here to a relative error of 5e-9 over that range, so small
 // steps keep all their bits (log(1 + u) would not).  u is 2^x with what rounding
 // x = -|v| log2 e leaves put back, or far steps would lose bits.
-__device__ __forceinline__ f2 softplus(f2 v) {
+__device__ __forceinline__ f2 softplus(f2 v, f2& u) {
     float a, b, lo, hi;
     f2_split(v, a, b);
     // below -200, u is zero anyway and infinities would leave a rest that is no number
@@ -165,7 +165,7 @@ __device__ __forceinline__ f2 softplus(f2 v) {
     f2_split(x, lo, hi);
     f2 rest = f2_fma(n, f2_both(kLog2e), f2_of(-lo, -hi));
     rest = f2_fma(n, f2_both(1.92596299e-8f), rest);      // log2 e less its fp32 value
-    f2 u = f2_of(exp2_of(lo), exp2_of(hi));
+    u = f2_of(exp2_of(lo), exp2_of(hi));
     u = f2_fma(f2_mul(u, f2_both(kLn2)), rest, u);
     f2 p = f2_both(-0.003244024235755205f);
     p = f2_fma(p, u, f2_both(0.019851457327604294f));
@@ -178,6 +178,18 @@ __device__ __forceinline__ f2 softplus(f2 v) {
     p = f2_fma(p, u, f2_both(-0.4999990165233612f));
     p = f2_fma(p, u, f2_both(1.0f));
     return f2_fma(p, u, f2_of(max_or_nan(a, 0.0f), max_or_nan(b, 0.0f)));
+}
+__device__ __forceinline__ f2 softplus(f2 v) {
+    f2 u;
+    return softplus(v, u);
+}
+// softplus and its slope, the sigmoid: 1 / (1 + u) or u / (1 + u).
+__device__ __forceinline__ f2 softplus_slope(f2 v, f2& slope) {
+    f2 u;
+    const f2 y = softplus(v, u), e = f2_add(u, f2_both(1.0f));
+    const float r0 = rcp_of(f2_lo(e)), r1 = rcp_of(f2_hi(e));
+    slope = f2_of(f2_lo(v) < 0.0f ? f2_lo(u) * r0 : r0, f2_hi(v) < 0.0f ? f2_hi(u) * r1 : r1);
+    return y;
 }
 // 1 / (1 + e^-v): a few 2^-22 off up to |v| of 8 or so, where it matters.
 __device__ __forceinline__ f2 sigmoid(f2 v) {

@@ -313,25 +313,84 @@ __device__ __forceinline__ void put_floats(float* dst, const float (&x)[V]) {
     }
 }
 
-// A tile's rows of one buffer, in flight: raw vectors in registers.
-template <typename T, int CB, int ROWS>
-struct RowsHeld {
-    using Ti = Tiling<T, CB, ROWS>;
-    Vec<T, Ti::V> v[Ti::NV];
-    __device__ void load(const void* src, int64_t stride, const Block& b, int t0, int rows) {
-        const T* p = static_cast<const T*>(src) + b.ch0 + Ti::col();
-        const bool on = Ti::col() < b.count;
+// A row buffer as a CTA goes along it: the thread's first vector of a tile, and how
+// far apart its vectors are.
+template <typename T, int CB>
+struct Rows {
+    using Ti = Tiling<T, CB, kTile>;
+    const T* p;
+    int64_t stride, apart;
+    bool on;
+    __device__ Rows(const void* src, int64_t stride_, const Block& b, int t0) {
+        stride = stride_;
+        apart = Ti::kRowStep * stride;
+        on = Ti::col() < b.count;
+        p = static_cast<const T*>(src) + (int64_t)(t0 + Ti::row(0)) * stride + b.ch0 + Ti::col();
+    }
+    __device__ void move(int tiles) { p += tiles * kTile * stride; }
+};
+
+// A tile of one row buffer in shared memory, as it came: every thread copies what
+// it reads itself, so it has to wait for its own copies only.
+template <typename T, int CB>
+struct RowsCopied {
+    using Ti = Tiling<T, CB, kTile>;
+    Vec<T, Ti::V> v[Ti::NV][kThreads];
+    // once: vectors past the CTA's channels stay zero
+    __device__ void clear() {
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j)
+#pragma unroll
+            for (int i = 0; i < Ti::V; ++i) v[j][threadIdx.x].v[i] = from_float<T>(0.0f);
+    }
+    __device__ void ask(const Rows<T, CB>& from, int rows) {
+        constexpr int kBytes = Ti::V * (int)sizeof(T);
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
-            const int r = Ti::row(j);
-            if (on && r < rows)
-                v[j] = *reinterpret_cast<const Vec<T, Ti::V>*>(p + (int64_t)(t0 + r) * stride);
+            if (!from.on || Ti::row(j) >= rows) continue;
+            if constexpr (kBytes >= 4)
+                copy_async<kBytes>(&v[j][threadIdx.x], from.p + j * from.apart);
             else
-#pragma unroll
-                for (int i = 0; i < Ti::V; ++i) v[j].v[i] = from_float<T>(0.0f);
+                v[j][threadIdx.x] = *reinterpret_cast<const Vec<T, Ti::V>*>(from.p + j * from.apart);
         }
     }
-    __device__ f2 pair(int j, int i) const { return f2_of(to_float(v[j].v[i]), to_float(v[j].v[Ti::V > 1 ? i + 1 : i])); }
+    __device__ Vec<T, Ti::V> at(int j) const { return v[j][threadIdx.x]; }
+};
+// Elements i and i + 1 of a vector (one element stands twice).
+template <typename T, int V>
+__device__ __forceinline__ f2 pair_of(const Vec<T, V>& u, int i) {
+    if constexpr (V > 1)
+        return vec_pair(u, i / 2);
+    else
+        return f2_both(to_float(u.v[0]));
+}
+
+// A tile of one row buffer on its way in registers.  The loads stay where they
+// are asked for: the compiler would move them to their use.
+template <typename T, int CB>
+struct RowsHeld {
+    using Ti = Tiling<T, CB, kTile>;
+    Vec<T, Ti::V> v[Ti::NV];
+    __device__ void ask(const Rows<T, CB>& from, int rows) {
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < Ti::V; ++i) v[j].v[i] = from_float<T>(0.0f);
+            if (!from.on || Ti::row(j) >= rows) continue;
+            const T* src = from.p + j * from.apart;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+            if constexpr (sizeof(v[j]) == 16)
+                asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(src) : "memory");
+            else if constexpr (sizeof(v[j]) == 8)
+                asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src) : "memory");
+            else if constexpr (sizeof(v[j]) == 4)
+                asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(src) : "memory");
+            else
+                v[j] = *reinterpret_cast<const Vec<T, Ti::V>*>(src);
+        }
+    }
+    __device__ const Vec<T, Ti::V>& at(int j) const { return v[j]; }
 };
 
 // B or C of a tile, in flight.

@@ -23,14 +23,18 @@ template <int LS, int CPT>
 struct GradShared {
     using L = Lay<LS, CPT>;
     static constexpr int kSlots = L::kPairs / 2 > 2 ? L::kPairs / 2 : 2;
+    // of each token and channel: what the states need ...
     alignas(16) float delta[kTile][L::CB];
-    alignas(16) float dx[kTile][L::CB];      // delta x
+    alignas(16) float dx[kTile][L::CB];      // delta x, then sum_n lam B
     alignas(16) float dy[kTile][L::CB];
+    // ... and what its own gradients need besides
+    alignas(16) float x[kTile][L::CB];
+    alignas(16) float slope[kTile][L::CB];   // of delta by dt
+    alignas(16) float gate[kTile][L::CB];    // dout silu'(z)
+    alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
+    alignas(16) float y[kSub][L::CB];        // sum_n C h
     alignas(16) float b[kTile * L::kStWidth];
     alignas(16) float c[kTile * L::kStWidth];
-    alignas(16) float sum_b[kSub][L::CB];    // sum_n lam B
-    alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
-    alignas(16) float y[kSub][L::CB];
     alignas(16) ulonglong2 p[kSub][kSlots][kThreads];      // then parts of dB and dC
     uint32_t mask[kMaxSegment / 32];
     Range range;
@@ -74,37 +78,75 @@ struct ChannelSums {
     }
 };
 
-// What a tile's tokens need before the states see them, in flight.
+// The row buffers of a call, tile by tile from the last: on their way in registers,
+// then, as what their gradients are made of, in shared memory.
 template <typename T, int CB, bool WITH_X>
 struct TileHeld {
     using Ti = Tiling<T, CB, kTile>;
-    RowsHeld<T, CB, kTile> x, dt, z, g;
-    __device__ void load(const Launch& a, const Block& b, int t0, int rows) {
-        if constexpr (WITH_X) x.load(a.in.x, a.in.x_stride, b, t0, rows);
-        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
-        if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
-        g.load(a.dout, a.dout_stride, b, t0, rows);
+    Rows<T, CB> from_x, from_dt, from_z, from_g;
+    RowsHeld<T, CB> x, dt, z, g;
+    __device__ TileHeld(const Launch& a, const Block& b, int t0)
+        : from_x(a.in.x, a.in.x_stride, b, t0), from_dt(a.in.dt, a.in.dt_stride, b, t0),
+          from_z(a.in.z, a.in.z_stride, b, t0), from_g(a.dout, a.dout_stride, b, t0) {}
+    // the tile before the ones asked for
+    __device__ void ask(const Launch& a, int rows) {
+        if constexpr (WITH_X) x.ask(from_x, rows);
+        dt.ask(from_dt, rows);
+        if (a.in.z != nullptr) z.ask(from_z, rows);
+        g.ask(from_g, rows);
+        from_x.move(-1);
+        from_dt.move(-1);
+        from_z.move(-1);
+        from_g.move(-1);
     }
-    // delta, delta x and dy to shared memory
-    __device__ void put(float (*delta)[CB], float (*dx)[CB], float (*dy)[CB], const Launch& a,
-                        const float (&bias)[Ti::V]) const {
+    // delta and dy
+    __device__ void put(float (*delta)[CB], float (*dy)[CB], const Launch& a, const float (&bias)[Ti::V]) const {
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
             const int r = Ti::row(j);
             if (r >= kTile) continue;
-            float d[Ti::V], xs[Ti::V], gy[Ti::V];
+            float d[Ti::V], gy[Ti::V];
 #pragma unroll
             for (int i = 0; i < Ti::V; i += 2) {
-                const f2 de = delta_of(dt.pair(j, i), pair_at(bias, i), a.shape.softplus);
-                f2 gp = g.pair(j, i);
-                if (a.in.z != nullptr) gp = f2_mul(gp, silu(z.pair(j, i)));
-                set_pair(d, i, de);
-                if constexpr (WITH_X) set_pair(xs, i, f2_mul(de, x.pair(j, i)));
-                set_pair(gy, i, gp);
+                set_pair(d, i, delta_of(pair_of(dt.at(j), i), pair_at(bias, i), a.shape.softplus));
+                f2 v = pair_of(g.at(j), i);
+                if (a.in.z != nullptr) v = f2_mul(v, silu(pair_of(z.at(j), i)));
+                set_pair(gy, i, v);
             }
             put_floats(&delta[r][Ti::col()], d);
-            if constexpr (WITH_X) put_floats(&dx[r][Ti::col()], xs);
             put_floats(&dy[r][Ti::col()], gy);
+        }
+    }
+    template <typename S>
+    __device__ void put_all(S& s, const Launch& a, const float (&bias)[Ti::V]) const {
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j) {
+            const int r = Ti::row(j);
+            if (r >= kTile) continue;
+            float d[Ti::V], u[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V];
+#pragma unroll
+            for (int i = 0; i < Ti::V; i += 2) {
+                const f2 v = f2_add(pair_of(dt.at(j), i), pair_at(bias, i)), xv = pair_of(x.at(j), i);
+                f2 slope = f2_both(1.0f), gv = pair_of(g.at(j), i);
+                const f2 de = a.shape.softplus ? softplus_slope(v, slope) : v;
+                if (a.in.z != nullptr) {
+                    const f2 zv = pair_of(z.at(j), i), sg = sigmoid(zv);
+                    set_pair(gt, i, f2_mul(gv, silu_slope(zv, sg)));
+                    gv = f2_mul(gv, f2_mul(zv, sg));
+                }
+                set_pair(d, i, de);
+                set_pair(u, i, f2_mul(de, xv));
+                set_pair(gy, i, gv);
+                set_pair(xs, i, xv);
+                set_pair(sl, i, slope);
+            }
+            const int c = Ti::col();
+            put_floats(&s.delta[r][c], d);
+            put_floats(&s.dx[r][c], u);
+            put_floats(&s.dy[r][c], gy);
+            put_floats(&s.x[r][c], xs);
+            put_floats(&s.slope[r][c], sl);
+            if (a.in.z != nullptr) put_floats(&s.gate[r][c], gt);
         }
     }
 };
@@ -160,18 +202,18 @@ __global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_c
         load_states<LS, CPT>(lam, a.d_final + (int64_t)s.range.e0 * a.shape.channels * n, n, p.ch, p.count, p.n0);
     const f2 one = f2_of(1.0f, 1.0f);
     const int last = s0 + (end - 1 - s0) / kTile * kTile;
-    TileHeld<T, L::CB, false> rows_in;
+    TileHeld<T, L::CB, false> rows_in(a, b, last);
     StatesHeld<T, LS, CPT> cs;
     auto fetch = [&](int t0) {
         const int rows = min(kTile, end - t0);
-        rows_in.load(a, b, t0, rows);
+        rows_in.ask(a, rows);
         cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
     };
     fetch(last);
     for (int t0 = last; t0 >= s0; t0 -= kTile) {
         const int rows = min(kTile, end - t0);
-        __syncthreads();
-        rows_in.put(s.delta, nullptr, s.dy, a, bias);
+        __syncthreads();      // the tile before is through
+        rows_in.put(s.delta, s.dy, a, bias);
         cs.put(s.c);
         __syncthreads();
         if (t0 > s0) fetch(t0 - kTile);
@@ -240,9 +282,8 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
     float* dbc = a.dbc + (int64_t)(blockIdx.y % parts) * tokens * dbc_stride + b.group * 2 * L::NP;
     f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs], first[L::kPairs], next[L::kPairs];
     load_decays<LS, CPT>(a2, a, p);
-    float tile_bias[Tile::V], bias[Ti::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
-    load_params<T, L::CB, kTile>(tile_bias, a.in.dt_bias, b);
-    load_params<T, L::CB, kSub>(bias, a.in.dt_bias, b);
+    float bias[Tile::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
+    load_params<T, L::CB, kTile>(bias, a.in.dt_bias, b);
     load_params<T, L::CB, kSub>(skip, a.in.d, b);
 #pragma unroll
     for (int i = 0; i < Ti::V; ++i) dskip[i] = dbias[i] = 0.0f;
@@ -269,11 +310,11 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
         if (e < a.episodes) load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
     };
     const int last = s0 + (end - 1 - s0) / kTile * kTile;
-    TileHeld<T, L::CB, true> rows_in;
+    TileHeld<T, L::CB, true> rows_in(a, b, last);
     StatesHeld<T, LS, CPT> bs, cs;
     auto fetch = [&](int t0) {
         const int rows = min(kTile, end - t0);
-        rows_in.load(a, b, t0, rows);
+        rows_in.ask(a, rows);
         bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
         cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
         // not written, and not used, where the tile begins an episode
@@ -290,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
 
     for (int t0 = last; t0 >= s0 && end > s0; t0 -= kTile) {
         const int rows = min(kTile, end - t0);
-        rows_in.put(s.delta, s.dx, s.dy, a, tile_bias);      // the tile before is through
+        rows_in.put_all(s, a, bias);      // the tile before is through
         bs.put(s.b);
         cs.put(s.c);
 #pragma unroll
@@ -302,14 +343,6 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
 #pragma unroll 1
         for (int r0 = rows > kSub ? kSub : 0; r0 >= 0; r0 -= kSub) {
             const int stop = min(rows, r0 + kSub), t1 = t0 + r0, count = stop - r0;
-            // what the rows' gradients need besides, in flight
-            RowsHeld<T, L::CB, kSub> x, dt, z, g;
-            x.load(a.in.x, a.in.x_stride, b, t1, count);
-            if (a.shape.softplus) dt.load(a.in.dt, a.in.dt_stride, b, t1, count);
-            if (a.in.z != nullptr) {
-                z.load(a.in.z, a.in.z_stride, b, t1, count);
-                g.load(a.dout, a.dout_stride, b, t1, count);
-            }
             // forward over the tile to the rows, and over them with p kept
 #pragma unroll
             for (int q = 0; q < L::kPairs; ++q) h[q] = first[q];
@@ -388,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
                 part[kThreads] = make_float4(v[4], v[5], v[6], v[7]);
                 const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]),
                             y = sum_states<LS, CPT>(ch[2]);
+                __syncwarp();      // every lane has read this token's dx
                 if (returns_channel<LS, CPT>()) {
                     const int at = p.local + which_channel<LS, CPT>();
-                    s.sum_b[r][at] = to_b;
+                    s.dx[i][at] = to_b;
                     s.sum_a[r][at] = to_a;
                     s.y[r][at] = y;
                 }
@@ -408,27 +442,34 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
             const int64_t ch = b.ch0 + Ti::col();
 #pragma unroll
             for (int j = 0; j < Ti::NV; ++j) {
-                const int r = Ti::row(j);
+                const int r = Ti::row(j), i = r0 + r;
                 if (r >= count || Ti::col() >= b.count) continue;
                 float out_x[Ti::V], out_dt[Ti::V], out_z[Ti::V];
+                float d[Ti::V], to_b[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V], to_a[Ti::V], y[Ti::V];
+                load_vec<float, Ti::V>(d, &s.delta[i][Ti::col()]);
+                load_vec<float, Ti::V>(to_b, &s.dx[i][Ti::col()]);
+                load_vec<float, Ti::V>(gy, &s.dy[i][Ti::col()]);
+                load_vec<float, Ti::V>(xs, &s.x[i][Ti::col()]);
+                load_vec<float, Ti::V>(sl, &s.slope[i][Ti::col()]);
+                load_vec<float, Ti::V>(to_a, &s.sum_a[r][Ti::col()]);
+                if (a.in.z != nullptr) {
+                    load_vec<float, Ti::V>(gt, &s.gate[i][Ti::col()]);
+                    load_vec<float, Ti::V>(y, &s.y[r][Ti::col()]);
+                }
 #pragma unroll
-                for (int i = 0; i < Ti::V; i += 2) {
-                    const int c = Ti::col() + i, c1 = Ti::V > 1 ? c + 1 : c;
-                    auto at = [&](const float* row) { return f2_of(row[c], row[c1]); };
-                    const f2 xv = x.pair(j, i), gy = at(s.dy[r0 + r]), to_b = at(s.sum_b[r]), sk = pair_at(skip, i);
-                    f2 v = f2_mul(at(s.delta[r0 + r]), to_b);
-                    if (a.in.d != nullptr) v = f2_fma(sk, gy, v);
-                    set_pair(out_x, i, v);
-                    v = f2_fma(xv, to_b, f2_mul(at(s.sum_a[r]), f2_both(kLn2)));
-                    if (a.shape.softplus) v = f2_mul(v, sigmoid(f2_add(dt.pair(j, i), pair_at(bias, i))));
-                    set_pair(out_dt, i, v);
-                    set_pair(dskip, i, f2_fma(gy, xv, pair_at(dskip, i)));
-                    set_pair(dbias, i, f2_add(v, pair_at(dbias, i)));
+                for (int k = 0; k < Ti::V; k += 2) {
+                    const f2 xv = pair_at(xs, k), gv = pair_at(gy, k), tb = pair_at(to_b, k), sk = pair_at(skip, k);
+                    f2 v = f2_mul(pair_at(d, k), tb);
+                    if (a.in.d != nullptr) v = f2_fma(sk, gv, v);
+                    set_pair(out_x, k, v);
+                    v = f2_mul(f2_fma(xv, tb, f2_mul(pair_at(to_a, k), f2_both(kLn2))), pair_at(sl, k));
+                    set_pair(out_dt, k, v);
+                    set_pair(dskip, k, f2_fma(gv, xv, pair_at(dskip, k)));
+                    set_pair(dbias, k, f2_add(v, pair_at(dbias, k)));
                     if (a.in.z != nullptr) {
-                        f2 y = at(s.y[r]);
-                        if (a.in.d != nullptr) y = f2_fma(sk, xv, y);
-                        const f2 zv = z.pair(j, i);
-                        set_pair(out_z, i, f2_mul(f2_mul(g.pair(j, i), y), silu_slope(zv, sigmoid(zv))));
+                        f2 yv = pair_at(y, k);
+                        if (a.in.d != nullptr) yv = f2_fma(sk, xv, yv);
+                        set_pair(out_z, k, f2_mul(pair_at(gt, k), yv));
                     }
                 }
                 const int64_t t = t1 + r;
@@ -493,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
 
 // Joins the parts: dA, dD and ddt_bias over the segments, dB and dC over a
 // group's CTAs.  CTAs [0, over): 32 outputs each, eight threads to an output;
-// the rest: an output a thread.
+// the rest: four outputs a thread.
 constexpr int kJoinThreads = 256, kSlices = 8;
 
 __device__ __forceinline__ float slice_sum(const float* p, int64_t stride, int parts, float (*red)[33]) {
@@ -540,17 +581,26 @@ __global__ void __launch_bounds__(kJoinThreads) scan_grad_join_kernel(const __gr
     const int tokens = (int)a.in.tokens, live = episode_end(a.ends, a.episodes - 1, tokens);
     const int64_t per = (int64_t)a.shape.groups * 2 * np, total = (int64_t)live * per;
     const int parts = a.blocks / a.shape.groups;
-    const int64_t i = ((int64_t)blockIdx.x - over) * kJoinThreads + threadIdx.x;
+    const int64_t i = (((int64_t)blockIdx.x - over) * kJoinThreads + threadIdx.x) * 4;
     if (i >= total) return;
     const int64_t t = i / per;
     const int rest = (int)(i - t * per), group = rest / (2 * np), k = rest % (2 * np), st = k % np;
     if (st >= n) return;
-    float v = a.dbc[i];
-    for (int j = 1; j < parts; ++j) v += a.dbc[(int64_t)j * tokens * per + i];
-    if (k < np)
-        static_cast<T*>(a.grads.db)[t * a.grads.b_stride + group * n + st] = from_float<T>(v);
-    else
-        static_cast<T*>(a.grads.dc)[t * a.grads.c_stride + group * n + st] = from_float<T>(v);
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int j = 0; j < parts; ++j) {
+        const float4 u = *reinterpret_cast<const float4*>(a.dbc + (int64_t)j * tokens * per + i);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+    }
+    T* out = k < np ? static_cast<T*>(a.grads.db) + t * a.grads.b_stride : static_cast<T*>(a.grads.dc) + t * a.grads.c_stride;
+    out += group * n + st;
+    out[0] = from_float<T>(v.x);
+    out[1] = from_float<T>(v.y);
+    out[2] = from_float<T>(v.z);
+    out[3] = from_float<T>(v.w);
 }
 
 template <typename T>
@@ -562,7 +612,7 @@ cudaError_t join(const Launch& a, const Cut& c, cudaStream_t st) {
     const int64_t outs = (int64_t)a.shape.channels * (a.shape.state_dim + 2), over = (outs + 31) / 32;
     int64_t more = 0;
     if (c.blocks > a.shape.groups)
-        more = (a.in.tokens * a.shape.groups * 2 * np + kJoinThreads - 1) / kJoinThreads;
+        more = (a.in.tokens * a.shape.groups * 2 * np / 4 + kJoinThreads - 1) / kJoinThreads;
     if (over + more > INT32_MAX) return cudaErrorInvalidValue;
     return launch_ex(scan_grad_join_kernel<T>, dim3((unsigned)(over + more)), dim3(kJoinThreads), 0, st, 1, false, a, np,
                      (unsigned)over);

@@ -6,49 +6,58 @@ namespace ofrl {
 namespace scan {
 namespace {
 
-template <int LS, int CPT>
-struct Shared {
+template <typename T, int LS, int CPT>
+struct TailShared {
     using L = Lay<LS, CPT>;
     alignas(16) float delta[kTile][L::CB];
     alignas(16) float dx[kTile][L::CB];      // delta x
     alignas(16) float b[kTile * L::kStWidth];
+    alignas(16) RowsCopied<T, L::CB> x, dt;
     uint32_t mask[kMaxSegment / 32];
     Range range;
 };
-template <int LS, int CPT>
-struct SharedAll : Shared<LS, CPT> {
+template <typename T, int LS, int CPT>
+struct ForwardShared {
     using L = Lay<LS, CPT>;
-    alignas(16) float y[kTile][L::CB];
+    alignas(16) float delta[kTile][L::CB];
+    alignas(16) float dx[kTile][L::CB];      // delta x, then sum_n C h
+    alignas(16) float b[kTile * L::kStWidth];
     alignas(16) float c[kTile * L::kStWidth];
+    alignas(16) RowsCopied<T, L::CB> x[2], dt, z;
+    uint32_t mask[kMaxSegment / 32];
+    Range range;
 };
 
-// delta and delta x of a tile, to shared memory.
-template <typename T, int LS, int CPT>
-__device__ __forceinline__ void put_rows(Shared<LS, CPT>& s, const RowsHeld<T, Lay<LS, CPT>::CB, kTile>& x,
-                                         const RowsHeld<T, Lay<LS, CPT>::CB, kTile>& dt,
-                                         const float (&bias)[Tiling<T, Lay<LS, CPT>::CB, kTile>::V], int with_softplus) {
-    using Ti = Tiling<T, Lay<LS, CPT>::CB, kTile>;
+// delta and delta x of a tile.
+template <typename T, int CB>
+__device__ __forceinline__ void put_rows(float (*delta)[CB], float (*dx)[CB], const RowsCopied<T, CB>& x,
+                                         const RowsCopied<T, CB>& dt, const float (&bias)[Tiling<T, CB, kTile>::V],
+                                         int with_softplus) {
+    using Ti = Tiling<T, CB, kTile>;
 #pragma unroll
     for (int j = 0; j < Ti::NV; ++j) {
-        if (Ti::row(j) >= kTile) continue;
-        float d[Ti::V], dx[Ti::V];
+        const int r = Ti::row(j);
+        if (r >= kTile) continue;
+        const Vec<T, Ti::V> xv = x.at(j), dv = dt.at(j);
+        float d[Ti::V], u[Ti::V];
 #pragma unroll
         for (int i = 0; i < Ti::V; i += 2) {
-            const f2 de = delta_of(dt.pair(j, i), pair_at(bias, i), with_softplus);
+            const f2 de = delta_of(pair_of(dv, i), pair_at(bias, i), with_softplus);
             set_pair(d, i, de);
-            set_pair(dx, i, f2_mul(de, x.pair(j, i)));
+            set_pair(u, i, f2_mul(de, pair_of(xv, i)));
         }
-        put_floats(&s.delta[Ti::row(j)][Ti::col()], d);
-        put_floats(&s.dx[Ti::row(j)][Ti::col()], dx);
+        put_floats(&delta[r][Ti::col()], d);
+        put_floats(&dx[r][Ti::col()], u);
     }
 }
 
 // 1. The state a segment ends with, as far as it is the segment's own.
 template <typename T, int LS, int CPT>
-__global__ void __launch_bounds__(kThreads) scan_tail_kernel(const __grid_constant__ Launch a) {
+__global__ void __launch_bounds__(kThreads, 4) scan_tail_kernel(const __grid_constant__ Launch a) {
     using L = Lay<LS, CPT>;
     using Ti = Tiling<T, L::CB, kTile>;
-    __shared__ Shared<LS, CPT> s;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    auto& s = *reinterpret_cast<TailShared<T, LS, CPT>*>(dynamic);
     pdl_wait();
     pdl_trigger();
     const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
@@ -75,14 +84,19 @@ __global__ void __launch_bounds__(kThreads) scan_tail_kernel(const __grid_consta
 
     const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
     const Place<LS, CPT> p(b);
-    RowsHeld<T, L::CB, kTile> x, dt;
+    Rows<T, L::CB> x(a.in.x, a.in.x_stride, b, begin), dt(a.in.dt, a.in.dt_stride, b, begin);
     StatesHeld<T, LS, CPT> bs;
-    auto fetch = [&](int t0) {
+    auto fetch = [&](int t0) {      // the tile after the ones asked for
         const int rows = min(kTile, s1 - t0);
-        x.load(a.in.x, a.in.x_stride, b, t0, rows);
-        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+        s.x.ask(x, rows);
+        s.dt.ask(dt, rows);
+        copies_commit();
         bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
+        x.move(1);
+        dt.move(1);
     };
+    s.x.clear();
+    s.dt.clear();
     fetch(begin);
     f2 a2[L::kPairs], h[L::kPairs], sum[L::kCh];
     load_decays<LS, CPT>(a2, a, p);
@@ -99,8 +113,9 @@ __global__ void __launch_bounds__(kThreads) scan_tail_kernel(const __grid_consta
     const f2 one = f2_of(1.0f, 1.0f);
     for (int t0 = begin; t0 < s1; t0 += kTile) {
         const int rows = min(kTile, s1 - t0);
-        __syncthreads();
-        put_rows<T, LS, CPT>(s, x, dt, bias, a.shape.softplus);
+        copies_wait<0>();
+        __syncthreads();      // the tile before is through
+        put_rows(s.delta, s.dx, s.x, s.dt, bias, a.shape.softplus);
         bs.put(s.b);
         __syncthreads();
         if (t0 + kTile < s1) fetch(t0 + kTile);
@@ -137,60 +152,81 @@ __global__ void __launch_bounds__(kThreads) scan_tail_kernel(const __grid_consta
 }
 
 // 2. What each segment takes over, in the place of its tail.  Backward: from the
-// last segment to the first.  A thread has one state of one channel; the loads
-// of kAhead segments are in flight while those before are joined.
-constexpr int kAhead = 16;
+// last segment to the first.  32 states a CTA; its warps have a slice of the
+// segments each, join it from nothing, learn through shared memory what the slices
+// before come to, and go over theirs again.  187 segments of 512 channels of 16
+// states 4 us, with one thread for a state 16.
+constexpr int kCarryWarps = 8, kAhead = 8;
 
-__global__ void __launch_bounds__(kThreads) scan_carry_kernel(const __grid_constant__ Launch a, int backward) {
+struct Joined {      // carry <- decay carry + own
+    float decay, own;
+};
+
+__global__ void __launch_bounds__(32 * kCarryWarps) scan_carry_kernel(const __grid_constant__ Launch a, int backward) {
+    __shared__ Joined slices[kCarryWarps][32];
     pdl_wait();
     pdl_trigger();
-    const int n = a.shape.state_dim;
-    const int64_t states = (int64_t)a.shape.channels * n, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= states) return;
-    const float a2 = a.in.a[i] * kLog2e;
+    const int n = a.shape.state_dim, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int64_t states = (int64_t)a.shape.channels * n, i = (int64_t)blockIdx.x * 32 + lane;
+    const bool on = i < states;
+    const float a2 = on ? a.in.a[i] * kLog2e : 0.0f;
     const int64_t ch = i / n;
-    float carry = 0.0f;
-    float tail[kAhead], sum[kAhead];
-    int kind[kAhead];
-    auto fetch = [&](int from) {
+    const int each = (a.n_seg + kCarryWarps - 1) / kCarryWarps, lo = min(slice * each, a.n_seg), hi = min(lo + each, a.n_seg);
+    // body(segment, what it makes of a carry), the loads of kAhead segments at once
+    auto over = [&](auto&& body) {
+        for (int from = lo; from < hi; from += kAhead) {
+            float tail[kAhead], sum[kAhead];
+            int kind[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
-            if (from + k < a.n_seg) {
-                kind[k] = a.kind[j];
-                tail[k] = a.tail[j * states + i];
-                sum[k] = a.sum[(int64_t)j * a.shape.channels + ch];
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
+                kind[k] = kTailNone;
+                if (on && from + k < hi) {
+                    kind[k] = a.kind[j];
+                    tail[k] = a.tail[j * states + i];
+                    sum[k] = a.sum[(int64_t)j * a.shape.channels + ch];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!on || from + k >= hi) break;
+                const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
+                // selected, not multiplied: what an unused tail holds stays out
+                Joined x = {0.0f, 0.0f};
+                if (kind[k] != kTailNone) x.own = tail[k];
+                if (kind[k] == kTailJoin) x.decay = exp2_of(a2 * sum[k]);
+                body(j, kind[k] == kTailJoin, x);
             }
         }
     };
-    fetch(0);
-    for (int from = 0; from < a.n_seg; from += kAhead) {
-        float own[kAhead], decay[kAhead];
-        int what[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            own[k] = tail[k];
-            decay[k] = exp2_of(a2 * sum[k]);
-            what[k] = kind[k];
-        }
-        if (from + kAhead < a.n_seg) fetch(from + kAhead);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (from + k >= a.n_seg) break;
-            const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
-            a.tail[j * states + i] = carry;
-            // selected, not multiplied: what an unused tail holds stays out
-            carry = what[k] == kTailJoin ? fmaf(decay[k], carry, own[k]) : what[k] == kTailOwn ? own[k] : 0.0f;
-        }
+    Joined all = {1.0f, 0.0f};
+    bool open = true;      // what came before the slice still counts
+    over([&](int, bool joins, const Joined& x) {
+        all.own = joins ? fmaf(x.decay, all.own, x.own) : x.own;
+        all.decay = joins ? x.decay * all.decay : 0.0f;
+        open = open && joins;
+    });
+    if (!open) all.decay = -1.0f;      // a decay is never negative
+    slices[slice][lane] = all;
+    __syncthreads();
+    float carry = 0.0f;
+    for (int k = 0; k < slice; ++k) {
+        const Joined x = slices[k][lane];
+        carry = x.decay < 0.0f ? x.own : fmaf(x.decay, carry, x.own);
     }
+    over([&](int j, bool joins, const Joined& x) {
+        a.tail[j * states + i] = carry;
+        carry = joins ? fmaf(x.decay, carry, x.own) : x.own;
+    });
 }
 
 // 3. The segments.
 template <typename T, int LS, int CPT>
-__global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_constant__ Launch a) {
+__global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_constant__ Launch a) {
     using L = Lay<LS, CPT>;
     using Ti = Tiling<T, L::CB, kTile>;
-    __shared__ SharedAll<LS, CPT> s;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    auto& s = *reinterpret_cast<ForwardShared<T, LS, CPT>*>(dynamic);
     pdl_wait();
     pdl_trigger();
     const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
@@ -199,16 +235,22 @@ __global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_con
     const Block b = block_at(a.shape, a.blocks, L::CB, blockIdx.y);
     const Place<LS, CPT> p(b);
     const bool mine = p.n0 < n;     // threads past the last state take no part in sums
-    RowsHeld<T, L::CB, kTile> x, dt;
+    Rows<T, L::CB> x(a.in.x, a.in.x_stride, b, s0), dt(a.in.dt, a.in.dt_stride, b, s0), z(a.in.z, a.in.z_stride, b, s0);
     StatesHeld<T, LS, CPT> bs, cs;
-    auto fetch = [&](int t0) {
+    auto fetch = [&](int t0, int stage) {      // the tile after the ones asked for
         const int rows = min(kTile, s1 - t0);
-        x.load(a.in.x, a.in.x_stride, b, t0, rows);
-        dt.load(a.in.dt, a.in.dt_stride, b, t0, rows);
+        s.x[stage].ask(x, rows);
+        s.dt.ask(dt, rows);
         bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
         cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
+        x.move(1);
+        dt.move(1);
     };
-    if (s0 < s1) fetch(s0);
+    s.x[0].clear();
+    s.x[1].clear();
+    s.dt.clear();
+    if (s0 < s1) fetch(s0, 0);
+    copies_commit();
     for (int i = threadIdx.x; i < kMaxSegment / 32; i += kThreads) s.mask[i] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -236,17 +278,20 @@ __global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_con
         if (a.final_state != nullptr && e < a.episodes)
             store_states<LS, CPT>(a.final_state + e * row_states, h, n, p.ch, p.count, p.n0);
     };
-    for (int t0 = s0; t0 < end; t0 += kTile) {
+    int stage = 0;
+    for (int t0 = s0; t0 < end; t0 += kTile, stage ^= 1) {
         const int rows = min(kTile, end - t0);
-        if (t0 > s0) __syncthreads();      // the tile before is through
-        put_rows<T, LS, CPT>(s, x, dt, bias, a.shape.softplus);
+        copies_wait<0>();
+        put_rows(s.delta, s.dx, s.x[stage], s.dt, bias, a.shape.softplus);
         bs.put(s.b);
         cs.put(s.c);
-        const RowsHeld<T, L::CB, kTile> x_now = x;
-        RowsHeld<T, L::CB, kTile> z;
         __syncthreads();
-        if (t0 + kTile < end) fetch(t0 + kTile);
-        if (a.in.z != nullptr) z.load(a.in.z, a.in.z_stride, b, t0, rows);
+        if (t0 + kTile < end) fetch(t0 + kTile, stage ^ 1);
+        if (a.in.z != nullptr) {
+            s.z.ask(z, rows);
+            z.move(1);
+        }
+        copies_commit();
         const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
         if (a.saved != nullptr && !(starts & 1))
             store_states<LS, CPT>(a.saved + (int64_t)(t0 / kTile) * row_states, h, n, p.ch, p.count, p.n0);
@@ -275,7 +320,8 @@ __global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < CPT; ++k) y[k] = 0.0f;
             const float sum = sum_states<LS, CPT>(y);
-            if (returns_channel<LS, CPT>()) s.y[i][p.local + which_channel<LS, CPT>()] = sum;
+            __syncwarp();      // every lane has read this token's dx
+            if (returns_channel<LS, CPT>()) s.dx[i][p.local + which_channel<LS, CPT>()] = sum;
         };
         if (starts == 0 && rows == kTile) {
 #pragma unroll 4
@@ -299,21 +345,23 @@ __global__ void __launch_bounds__(kThreads) scan_forward_kernel(const __grid_con
             }
         }
         __syncthreads();
-        T* out = static_cast<T*>(a.out) + b.ch0 + Ti::col();
+        copies_wait<0>();
+        T* out = static_cast<T*>(a.out) + (int64_t)t0 * a.out_stride + b.ch0 + Ti::col();
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
             const int r = Ti::row(j);
             if (r >= rows || Ti::col() >= b.count) continue;
+            const Vec<T, Ti::V> xv = s.x[stage].at(j), zv = s.z.at(j);
             float y[Ti::V];
 #pragma unroll
             for (int i = 0; i < Ti::V; i += 2) {
-                const float* p = &s.y[r][Ti::col() + i];
-                f2 v = f2_of(p[0], p[Ti::V > 1 ? 1 : 0]);
-                if (a.in.d != nullptr) v = f2_fma(pair_at(skip, i), x_now.pair(j, i), v);
-                if (a.in.z != nullptr) v = f2_mul(v, silu(z.pair(j, i)));
+                const float* q = &s.dx[r][Ti::col() + i];
+                f2 v = f2_of(q[0], q[Ti::V > 1 ? 1 : 0]);
+                if (a.in.d != nullptr) v = f2_fma(pair_at(skip, i), pair_of(xv, i), v);
+                if (a.in.z != nullptr) v = f2_mul(v, silu(pair_of(zv, i)));
                 set_pair(y, i, v);
             }
-            store_vec<T, Ti::V>(out + (int64_t)(t0 + r) * a.out_stride, y);
+            store_vec<T, Ti::V>(out + r * a.out_stride, y);
         }
     }
     if (s.range.closed && end > s0) leave();
@@ -341,13 +389,14 @@ template <typename T, int LS, int CPT>
 cudaError_t go(const Launch& a, const Cut& c, cudaStream_t st) {
     static std::atomic<uint64_t> tail_done{0}, done{0};
     const dim3 grid((unsigned)c.n_seg, (unsigned)c.blocks);
-    cudaError_t e = opt_in_once(scan_forward_kernel<T, LS, CPT>, 0, done);
+    constexpr int tail_smem = (int)sizeof(TailShared<T, LS, CPT>), smem = (int)sizeof(ForwardShared<T, LS, CPT>);
+    cudaError_t e = opt_in_once(scan_forward_kernel<T, LS, CPT>, smem, done);
     if (c.n_seg > 1) {
-        if (e == cudaSuccess) e = opt_in_once(scan_tail_kernel<T, LS, CPT>, 0, tail_done);
-        if (e == cudaSuccess) e = launch_pdl(scan_tail_kernel<T, LS, CPT>, grid, dim3(kThreads), 0, st, a);
+        if (e == cudaSuccess) e = opt_in_once(scan_tail_kernel<T, LS, CPT>, tail_smem, tail_done);
+        if (e == cudaSuccess) e = launch_pdl(scan_tail_kernel<T, LS, CPT>, grid, dim3(kThreads), tail_smem, st, a);
         if (e == cudaSuccess) e = launch_carry(a, false, st);
     }
-    if (e == cudaSuccess) e = launch_pdl(scan_forward_kernel<T, LS, CPT>, grid, dim3(kThreads), 0, st, a);
+    if (e == cudaSuccess) e = launch_pdl(scan_forward_kernel<T, LS, CPT>, grid, dim3(kThreads), smem, st, a);
     return e;
 }
 
@@ -370,8 +419,7 @@ cudaError_t launch_carry(const Launch& a, bool backward, cudaStream_t st) {
     cudaError_t e = opt_in_once(scan_carry_kernel, 0, done);
     const int64_t states = (int64_t)a.shape.channels * a.shape.state_dim;
     if (e == cudaSuccess)
-        e = launch_pdl(scan_carry_kernel, dim3((unsigned)((states + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, a,
-                       (int)backward);
+        e = launch_pdl(scan_carry_kernel, dim3((unsigned)((states + 31) / 32)), dim3(32 * kCarryWarps), 0, st, a, (int)backward);
     return e;
 }
 
