@@ -57,7 +57,7 @@ struct Cut {
     int seg;             // tokens of a segment
     int n_seg;           // at least 1
 };
-Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int num_sms, bool backward);
+Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_sms, bool backward);
 
 // Bytes from the workspace's start.
 struct Work {

@@ -20,21 +20,27 @@ int blocks_of(const ofrl_scan_shape& s, int ls, int cpt) {
 }
 // Segments wanted for `blocks` CTAs each: `per_sm` CTAs on every SM.
 int64_t wanted(int blocks, int num_sms, int per_sm) { return div_up((int64_t)num_sms * per_sm, blocks); }
-int per_sm_of(bool backward) { return backward ? 3 : 5; }
+int per_sm_of(bool backward) { return backward ? 3 : 4; }
 
 }  // namespace
 
-Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int num_sms, bool backward) {
+Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_sms, bool backward) {
     Cut c;
     c.ls = lanes_of(s.state_dim);
+    const int64_t mean = round_up(div_up(tokens, episodes > 0 ? episodes : 1), kTile);
     for (int cpt = wide_of(c.ls, backward);; cpt = 1) {
         c.cpt = cpt;
         c.blocks = blocks_of(s, c.ls, cpt);
-        const int64_t even = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward))), kTile);
-        c.seg = (int)(even < kMinSegment ? kMinSegment : even > kMaxSegment ? kMaxSegment : even);
-        const int64_t n = div_up(tokens, c.seg);
+        int64_t seg = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward))), kTile);
+        seg = seg < kMinSegment ? kMinSegment : seg > kMaxSegment ? kMaxSegment : seg;
+        // whole episodes of equal lengths have no tails
+        const bool whole = mean > seg && mean <= 4 * seg && mean <= kMaxSegment &&
+                           (int64_t)c.blocks * div_up(tokens, mean) >= num_sms;
+        if (whole) seg = mean;
+        c.seg = (int)seg;
+        const int64_t n = div_up(tokens, seg);
         c.n_seg = (int)(n > 1 ? n : 1);
-        if (cpt == 1 || (int64_t)c.blocks * c.n_seg >= 2 * num_sms) return c;
+        if (cpt == 1 || whole || (int64_t)c.blocks * c.n_seg >= 2 * num_sms) return c;
     }
 }
 
@@ -205,7 +211,7 @@ ofrl_status ofrl_scan_forward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const 
     if (num_episodes == 0) return OFRL_OK;
     if (in->tokens > 0 && !rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
     if (!aligned_to(init_state, 16) || !aligned_to(final_state, 16) || !aligned_to(saved, 16)) return OFRL_EINVAL;
-    const Cut c = cut_of(ctx->shape, in->tokens, ctx->num_sms, false);
+    const Cut c = cut_of(ctx->shape, in->tokens, num_episodes, ctx->num_sms, false);
     scan::Launch a = base_launch(ctx, in, episode_ends, num_episodes, c, false);
     a.init = init_state;
     a.out = out;
@@ -238,7 +244,7 @@ ofrl_status ofrl_scan_backward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const
             !stride_ok(grads->b_stride, bc) || !stride_ok(grads->c_stride, bc))
             return OFRL_EINVAL;
     }
-    const Cut c = cut_of(h, in->tokens, ctx->num_sms, true);
+    const Cut c = cut_of(h, in->tokens, num_episodes, ctx->num_sms, true);
     scan::Launch a = base_launch(ctx, in, episode_ends, num_episodes, c, true);
     a.init = init_state;
     a.saved = static_cast<float*>(const_cast<void*>(saved));

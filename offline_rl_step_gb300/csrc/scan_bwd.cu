@@ -25,12 +25,13 @@ struct GradShared {
     static constexpr int kSlots = L::kPairs / 2 > 2 ? L::kPairs / 2 : 2;
     // of each token and channel: what the states need ...
     alignas(16) float delta[kTile][L::CB];
-    alignas(16) float dx[kTile][L::CB];      // delta x, then sum_n lam B
+    alignas(16) float dx[kTile][L::CB];      // delta x
     alignas(16) float dy[kTile][L::CB];
     // ... and what its own gradients need besides
     alignas(16) float x[kTile][L::CB];
     alignas(16) float slope[kTile][L::CB];   // of delta by dt
     alignas(16) float gate[kTile][L::CB];    // dout silu'(z)
+    alignas(16) float sum_b[kSub][L::CB];    // sum_n lam B
     alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
     alignas(16) float y[kSub][L::CB];        // sum_n C h
     alignas(16) float b[kTile * L::kStWidth];
@@ -421,10 +422,9 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
                 part[kThreads] = make_float4(v[4], v[5], v[6], v[7]);
                 const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]),
                             y = sum_states<LS, CPT>(ch[2]);
-                __syncwarp();      // every lane has read this token's dx
                 if (returns_channel<LS, CPT>()) {
                     const int at = p.local + which_channel<LS, CPT>();
-                    s.dx[i][at] = to_b;
+                    s.sum_b[r][at] = to_b;
                     s.sum_a[r][at] = to_a;
                     s.y[r][at] = y;
                 }
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
                 float out_x[Ti::V], out_dt[Ti::V], out_z[Ti::V];
                 float d[Ti::V], to_b[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V], to_a[Ti::V], y[Ti::V];
                 load_vec<float, Ti::V>(d, &s.delta[i][Ti::col()]);
-                load_vec<float, Ti::V>(to_b, &s.dx[i][Ti::col()]);
+                load_vec<float, Ti::V>(to_b, &s.sum_b[r][Ti::col()]);
                 load_vec<float, Ti::V>(gy, &s.dy[i][Ti::col()]);
                 load_vec<float, Ti::V>(xs, &s.x[i][Ti::col()]);
                 load_vec<float, Ti::V>(sl, &s.slope[i][Ti::col()]);

@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
         const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
         if (a.saved != nullptr && !(starts & 1))
             store_states<LS, CPT>(a.saved + (int64_t)(t0 / kTile) * row_states, h, n, p.ch, p.count, p.n0);
-        auto step = [&](int i) {
+        // a token's part of sum_n C h, from this thread's states
+        auto step = [&](int i, float (&y)[CPT]) {
             f2 de[L::kCh], dx[L::kCh], bv[L::kSt], cv[L::kSt];
             L::channels(de, &s.delta[i][p.local]);
             L::channels(dx, &s.dx[i][p.local]);
@@ -309,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
                 h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], f2_mul(decay, h[q]));
                 acc[L::ci(q)] = L::si(q) == 0 ? f2_mul(cv[0], h[q]) : f2_fma(cv[L::si(q)], h[q], acc[L::ci(q)]);
             }
-            float y[CPT];
             if constexpr (CPT == 1) {
                 y[0] = f2_sum(acc[0]);
             } else {
@@ -319,14 +319,27 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
             if (!mine)
 #pragma unroll
                 for (int k = 0; k < CPT; ++k) y[k] = 0.0f;
-            const float sum = sum_states<LS, CPT>(y);
-            __syncwarp();      // every lane has read this token's dx
+        };
+        // the sums of tokens i .. take the place of their dx, which every lane has read
+        auto put = [&](int i, float sum) {
             if (returns_channel<LS, CPT>()) s.dx[i][p.local + which_channel<LS, CPT>()] = sum;
         };
         if (starts == 0 && rows == kTile) {
-#pragma unroll 4
-            for (int i = 0; i < kTile; ++i) step(i);
+            // four tokens between two barriers of the warp, so that their latencies overlap
+            constexpr int kTogether = 4;
+#pragma unroll 1
+            for (int i = 0; i < kTile; i += kTogether) {
+                float y[kTogether][CPT], sum[kTogether];
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) step(i + k, y[k]);
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) sum[k] = sum_states<LS, CPT>(y[k]);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) put(i + k, sum[k]);
+            }
         } else {
+#pragma unroll 1
             for (int i = 0; i < rows; ++i) {
                 if (starts >> i & 1) {
                     if (t0 + i > s0) {
@@ -341,7 +354,11 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
                         for (int q = 0; q < L::kPairs; ++q) h[q] = f2_of(0.0f, 0.0f);
                     }
                 }
-                step(i);
+                float y[CPT];
+                step(i, y);
+                const float sum = sum_states<LS, CPT>(y);
+                __syncwarp();
+                put(i, sum);
             }
         }
         __syncthreads();
