@@ -38,16 +38,17 @@ namespace ofrl {
 namespace scan {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 16;            // tokens brought into shared memory at once; states are saved as often
+constexpr int kTile = 16;            // tokens brought into shared memory at once
+constexpr int kSave = 8;             // tokens between saved states: a tile of the gradients
 constexpr int kMaxSegment = 4096;    // tokens of a segment (its mask of starts is in shared memory)
 constexpr int kMinSegment = 64;
 
 // How a state of [channels, N] lies on a warp: LS lanes share a channel, four
 // states each, and a thread has CPT channels.
 constexpr int lanes_of(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
-// CPT of the wide form; the narrow one has 1.  Gradients keep twice as many
-// values a state in registers and shared memory.
-constexpr int wide_of(int ls, bool backward) { return ls < 2 ? 1 : ls < 4 || backward ? 2 : 4; }
+// CPT of a call's two forms, the wide one and the one for little work.
+constexpr int wide_of(int ls) { return ls < 2 ? 1 : ls < 4 ? 2 : 4; }
+constexpr int narrow_of(int ls, bool backward) { return backward && ls >= 4 ? 2 : 1; }
 constexpr int block_of(int ls, int cpt) { return kWarps * (32 / ls) * cpt; }      // channels of a CTA
 
 // How one call is cut.
@@ -88,7 +89,7 @@ struct Launch {
     void* out;
     int64_t out_stride;
     float* final_state;
-    float* saved;        // [tokens / kTile][channels][N]
+    float* saved;        // [tokens / kSave][channels][N]
     const void* dout;
     int64_t dout_stride;
     const float* d_final;
@@ -131,7 +132,8 @@ int64_t saved_bytes(const ofrl_scan_shape& s, int64_t tokens);
 template <typename T, int CB, int ROWS>
 struct Tiling {
     static constexpr int kEach = ROWS * CB / kThreads;
-    static constexpr int kMost = 16 / (int)sizeof(T);
+    // gradients: four, whose fp32 forms threads write side by side without conflicts
+    static constexpr int kMost = ROWS < kTile ? 4 : 16 / (int)sizeof(T);
     static constexpr int V = kEach < 1 ? 1 : kEach < kMost ? kEach : kMost;
     static constexpr int NV = kEach < V ? 1 : kEach / V;
     static constexpr int kCols = CB / V;             // threads along a row
@@ -315,9 +317,9 @@ __device__ __forceinline__ void put_floats(float* dst, const float (&x)[V]) {
 
 // A row buffer as a CTA goes along it: the thread's first vector of a tile, and how
 // far apart its vectors are.
-template <typename T, int CB>
+template <typename T, int CB, int ROWS = kTile>
 struct Rows {
-    using Ti = Tiling<T, CB, kTile>;
+    using Ti = Tiling<T, CB, ROWS>;
     const T* p;
     int64_t stride, apart;
     bool on;
@@ -327,7 +329,7 @@ struct Rows {
         on = Ti::col() < b.count;
         p = static_cast<const T*>(src) + (int64_t)(t0 + Ti::row(0)) * stride + b.ch0 + Ti::col();
     }
-    __device__ void move(int tiles) { p += tiles * kTile * stride; }
+    __device__ void move(int tiles) { p += tiles * ROWS * stride; }
 };
 
 // A tile of one row buffer in shared memory, as it came: every thread copies what
@@ -367,11 +369,11 @@ __device__ __forceinline__ f2 pair_of(const Vec<T, V>& u, int i) {
 
 // A tile of one row buffer on its way in registers.  The loads stay where they
 // are asked for: the compiler would move them to their use.
-template <typename T, int CB>
+template <typename T, int CB, int ROWS>
 struct RowsHeld {
-    using Ti = Tiling<T, CB, kTile>;
+    using Ti = Tiling<T, CB, ROWS>;
     Vec<T, Ti::V> v[Ti::NV];
-    __device__ void ask(const Rows<T, CB>& from, int rows) {
+    __device__ void ask(const Rows<T, CB, ROWS>& from, int rows) {
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
 #pragma unroll

@@ -20,7 +20,8 @@ int blocks_of(const ofrl_scan_shape& s, int ls, int cpt) {
 }
 // Segments wanted for `blocks` CTAs each: `per_sm` CTAs on every SM.
 int64_t wanted(int blocks, int num_sms, int per_sm) { return div_up((int64_t)num_sms * per_sm, blocks); }
-int per_sm_of(bool backward) { return backward ? 3 : 4; }
+// What its registers and shared memory let an SM hold.
+int per_sm_of(bool backward, int cpt) { return !backward ? 4 : cpt == 4 ? 2 : 3; }
 
 }  // namespace
 
@@ -28,10 +29,11 @@ Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_s
     Cut c;
     c.ls = lanes_of(s.state_dim);
     const int64_t mean = round_up(div_up(tokens, episodes > 0 ? episodes : 1), kTile);
-    for (int cpt = wide_of(c.ls, backward);; cpt = 1) {
+    const int narrow = narrow_of(c.ls, backward);
+    for (int cpt = wide_of(c.ls);; cpt = narrow) {
         c.cpt = cpt;
         c.blocks = blocks_of(s, c.ls, cpt);
-        int64_t seg = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward))), kTile);
+        int64_t seg = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward, cpt))), kTile);
         seg = seg < kMinSegment ? kMinSegment : seg > kMaxSegment ? kMaxSegment : seg;
         // whole episodes of equal lengths have no tails
         const bool whole = mean > seg && mean <= 4 * seg && mean <= kMaxSegment &&
@@ -40,7 +42,7 @@ Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_s
         c.seg = (int)seg;
         const int64_t n = div_up(tokens, seg);
         c.n_seg = (int)(n > 1 ? n : 1);
-        if (cpt == 1 || whole || (int64_t)c.blocks * c.n_seg >= 2 * num_sms) return c;
+        if (cpt == narrow || whole || (int64_t)c.blocks * c.n_seg >= 2 * num_sms) return c;
     }
 }
 
@@ -70,24 +72,24 @@ int64_t work_bytes(const ofrl_scan_shape& s, int64_t max_tokens, int num_sms, bo
     Cut c;
     c.ls = lanes_of(s.state_dim);
     for (int back = 0; back <= (backward ? 1 : 0); ++back)
-        for (int cpt = wide_of(c.ls, back != 0);; cpt = 1) {
+        for (int cpt = wide_of(c.ls);; cpt = narrow_of(c.ls, back != 0)) {
             c.cpt = cpt;
             c.blocks = blocks_of(s, c.ls, cpt);
             // a segment is no shorter than an even share and than kMinSegment, or it is kMaxSegment
-            const int64_t even = wanted(c.blocks, num_sms, per_sm_of(back != 0)), least = div_up(max_tokens, kMinSegment),
+            const int64_t even = wanted(c.blocks, num_sms, per_sm_of(back != 0, cpt)), least = div_up(max_tokens, kMinSegment),
                           longest = div_up(max_tokens, kMaxSegment);
             const int64_t few = even < least ? even : least;
             const int64_t n = longest > few ? longest : few;
             c.n_seg = (int)(n > 1 ? n : 1);
             const int64_t bytes = work_of(s, max_tokens, c, back != 0).total;
             most = bytes > most ? bytes : most;
-            if (cpt == 1) break;
+            if (cpt == narrow_of(c.ls, back != 0)) break;
         }
     return most;
 }
 
 int64_t saved_bytes(const ofrl_scan_shape& s, int64_t tokens) {
-    return div_up(tokens, kTile) * s.channels * s.state_dim * 4;
+    return div_up(tokens, kSave) * s.channels * s.state_dim * 4;
 }
 
 }  // namespace scan

@@ -4,10 +4,9 @@
 //   dx_t = delta_t sum_n lam_t B_t + D dy_t          dC_t = sum_d dy_t h_t
 //   ddelta_t = x_t sum_n lam_t B_t + sum_n A lam_t p_t    dB_t = sum_d lam_t delta_t x_t
 //   dA = sum_t delta_t lam_t p_t,  p_t = a_t h_{t-1},  h_t = p_t + delta_t B_t x_t.
-// States come from the ones that the forward pass saved every kTile tokens:
-// half a tile at a time is gone over forward, p kept in shared memory, then
-// backward.  The sums over a token's channels (dB, dC) are made over a warp's
-// lanes, the CTA's warps and the CTAs, in that order.
+// States come from the ones that the forward pass saved every kSave tokens: a tile
+// is gone over forward, p kept in shared memory, then backward.  The sums over a
+// token's channels (dB, dC) are made over the CTA's threads, then over the CTAs.
 
 #include <cstddef>
 
@@ -17,26 +16,26 @@ namespace ofrl {
 namespace scan {
 namespace {
 
-constexpr int kSub = kTile / 2;      // tokens whose p is kept at once
+constexpr int kBack = kSave;      // tokens of a tile: their p is in shared memory
 
 template <int LS, int CPT>
 struct GradShared {
     using L = Lay<LS, CPT>;
     static constexpr int kSlots = L::kPairs / 2 > 2 ? L::kPairs / 2 : 2;
     // of each token and channel: what the states need ...
-    alignas(16) float delta[kTile][L::CB];
-    alignas(16) float dx[kTile][L::CB];      // delta x
-    alignas(16) float dy[kTile][L::CB];
+    alignas(16) float delta[kBack][L::CB];
+    alignas(16) float dx[kBack][L::CB];      // delta x
+    alignas(16) float dy[kBack][L::CB];
     // ... and what its own gradients need besides
-    alignas(16) float x[kTile][L::CB];
-    alignas(16) float slope[kTile][L::CB];   // of delta by dt
-    alignas(16) float gate[kTile][L::CB];    // dout silu'(z)
-    alignas(16) float sum_b[kSub][L::CB];    // sum_n lam B
-    alignas(16) float sum_a[kSub][L::CB];    // sum_n A2 lam p
-    alignas(16) float y[kSub][L::CB];        // sum_n C h
-    alignas(16) float b[kTile * L::kStWidth];
-    alignas(16) float c[kTile * L::kStWidth];
-    alignas(16) ulonglong2 p[kSub][kSlots][kThreads];      // then parts of dB and dC
+    alignas(16) float x[kBack][L::CB];
+    alignas(16) float slope[kBack][L::CB];   // of delta by dt
+    alignas(16) float gate[kBack][L::CB];    // dout silu'(z)
+    alignas(16) float sum_b[kBack][L::CB];    // sum_n lam B
+    alignas(16) float sum_a[kBack][L::CB];    // sum_n A2 lam p
+    alignas(16) float y[kBack][L::CB];        // sum_n C h
+    alignas(16) float b[kBack * L::kStWidth];
+    alignas(16) float c[kBack * L::kStWidth];
+    alignas(16) ulonglong2 p[kBack][kSlots][kThreads];      // then parts of dB and dC
     uint32_t mask[kMaxSegment / 32];
     Range range;
 };
@@ -50,8 +49,8 @@ template <int LS, int SLOTS>
 struct ChannelSums {
     static constexpr int kWidth = LS > 8 ? LS : 8;      // threads that read one sum's parts
     static constexpr int kAtOnce = kThreads / kWidth;   // sums of a round
-    static constexpr int kRounds = 2 * kSub / kAtOnce;
-    // put(row, half, first state, values) for each of the 2 * count sums
+    static constexpr int kRounds = 2 * kBack / kAtOnce;
+    // put(row, half, first state, values) for each of the 2 count sums
     template <typename Put>
     __device__ static void run(const float4* parts, int count, const Put& put) {
         const int j = threadIdx.x % kWidth;
@@ -81,11 +80,11 @@ struct ChannelSums {
 
 // The row buffers of a call, tile by tile from the last: on their way in registers,
 // then, as what their gradients are made of, in shared memory.
-template <typename T, int CB, bool WITH_X>
+template <typename T, int CB, int ROWS, bool WITH_X>
 struct TileHeld {
-    using Ti = Tiling<T, CB, kTile>;
-    Rows<T, CB> from_x, from_dt, from_z, from_g;
-    RowsHeld<T, CB> x, dt, z, g;
+    using Ti = Tiling<T, CB, ROWS>;
+    Rows<T, CB, ROWS> from_x, from_dt, from_z, from_g;
+    RowsHeld<T, CB, ROWS> x, dt, z, g;
     __device__ TileHeld(const Launch& a, const Block& b, int t0)
         : from_x(a.in.x, a.in.x_stride, b, t0), from_dt(a.in.dt, a.in.dt_stride, b, t0),
           from_z(a.in.z, a.in.z_stride, b, t0), from_g(a.dout, a.dout_stride, b, t0) {}
@@ -105,7 +104,7 @@ struct TileHeld {
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
             const int r = Ti::row(j);
-            if (r >= kTile) continue;
+            if (r >= ROWS) continue;
             float d[Ti::V], gy[Ti::V];
 #pragma unroll
             for (int i = 0; i < Ti::V; i += 2) {
@@ -123,7 +122,7 @@ struct TileHeld {
 #pragma unroll
         for (int j = 0; j < Ti::NV; ++j) {
             const int r = Ti::row(j);
-            if (r >= kTile) continue;
+            if (r >= ROWS) continue;
             float d[Ti::V], u[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V];
 #pragma unroll
             for (int i = 0; i < Ti::V; i += 2) {
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_c
         load_states<LS, CPT>(lam, a.d_final + (int64_t)s.range.e0 * a.shape.channels * n, n, p.ch, p.count, p.n0);
     const f2 one = f2_of(1.0f, 1.0f);
     const int last = s0 + (end - 1 - s0) / kTile * kTile;
-    TileHeld<T, L::CB, false> rows_in(a, b, last);
+    TileHeld<T, L::CB, kTile, false> rows_in(a, b, last);
     StatesHeld<T, LS, CPT> cs;
     auto fetch = [&](int t0) {
         const int rows = min(kTile, end - t0);
@@ -260,8 +259,7 @@ constexpr int grad_ctas() {
 template <typename T, int LS, int CPT>
 __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kernel(const __grid_constant__ Launch a) {
     using L = Lay<LS, CPT>;
-    using Tile = Tiling<T, L::CB, kTile>;
-    using Ti = Tiling<T, L::CB, kSub>;
+    using Ti = Tiling<T, L::CB, kBack>;
     extern __shared__ __align__(16) uint8_t smem[];
     GradShared<LS, CPT>& s = *reinterpret_cast<GradShared<LS, CPT>*>(smem);
     pdl_wait();
@@ -281,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
     const int parts = a.blocks / a.shape.groups;      // CTAs that share a group's dB and dC
     const int64_t dbc_stride = (int64_t)a.shape.groups * 2 * L::NP;
     float* dbc = a.dbc + (int64_t)(blockIdx.y % parts) * tokens * dbc_stride + b.group * 2 * L::NP;
-    f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs], first[L::kPairs], next[L::kPairs];
+    f2 a2[L::kPairs], da[L::kPairs], lam[L::kPairs], h[L::kPairs], next[L::kPairs];
     load_decays<LS, CPT>(a2, a, p);
-    float bias[Tile::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
-    load_params<T, L::CB, kTile>(bias, a.in.dt_bias, b);
-    load_params<T, L::CB, kSub>(skip, a.in.d, b);
+    float bias[Ti::V], skip[Ti::V], dskip[Ti::V], dbias[Ti::V];
+    load_params<T, L::CB, kBack>(bias, a.in.dt_bias, b);
+    load_params<T, L::CB, kBack>(skip, a.in.d, b);
 #pragma unroll
     for (int i = 0; i < Ti::V; ++i) dskip[i] = dbias[i] = 0.0f;
     const f2 zero = f2_of(0.0f, 0.0f);
@@ -310,16 +308,16 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
         const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
         if (e < a.episodes) load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
     };
-    const int last = s0 + (end - 1 - s0) / kTile * kTile;
-    TileHeld<T, L::CB, true> rows_in(a, b, last);
-    StatesHeld<T, LS, CPT> bs, cs;
+    const int last = s0 + (end - 1 - s0) / kBack * kBack;
+    TileHeld<T, L::CB, kBack, true> rows_in(a, b, last);
+    StatesHeld<T, LS, CPT, kBack> bs, cs;
     auto fetch = [&](int t0) {
-        const int rows = min(kTile, end - t0);
+        const int rows = min(kBack, end - t0);
         rows_in.ask(a, rows);
         bs.load(a.in.b, a.in.b_stride, b.group, n, t0, rows);
         cs.load(a.in.c, a.in.c_stride, b.group, n, t0, rows);
         // not written, and not used, where the tile begins an episode
-        load_states<LS, CPT>(next, a.saved + (int64_t)(t0 / kTile) * row_states, n, p.ch, p.count, p.n0);
+        load_states<LS, CPT>(next, a.saved + (int64_t)(t0 / kBack) * row_states, n, p.ch, p.count, p.n0);
     };
     if (end > s0) {
         fetch(last);
@@ -330,170 +328,159 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
     }
     const int at_state = L::state_at((threadIdx.x & 31) % LS);
 
-    for (int t0 = last; t0 >= s0 && end > s0; t0 -= kTile) {
-        const int rows = min(kTile, end - t0);
+    for (int t0 = last; t0 >= s0 && end > s0; t0 -= kBack) {
+        const int rows = min(kBack, end - t0);
         rows_in.put_all(s, a, bias);      // the tile before is through
         bs.put(s.b);
         cs.put(s.c);
 #pragma unroll
-        for (int q = 0; q < L::kPairs; ++q) first[q] = next[q];
+        for (int q = 0; q < L::kPairs; ++q) h[q] = next[q];
         __syncthreads();
-        if (t0 > s0) fetch(t0 - kTile);
-        const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
-
-#pragma unroll 1
-        for (int r0 = rows > kSub ? kSub : 0; r0 >= 0; r0 -= kSub) {
-            const int stop = min(rows, r0 + kSub), t1 = t0 + r0, count = stop - r0;
-            // forward over the tile to the rows, and over them with p kept
-#pragma unroll
-            for (int q = 0; q < L::kPairs; ++q) h[q] = first[q];
+        if (t0 > s0) fetch(t0 - kBack);
+        const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kBack) - 1);
 #pragma unroll 2
-            for (int i = 0; i < stop; ++i) {
-                if (starts >> i & 1) begin(t0 + i);
-                f2 de[L::kCh], dx[L::kCh], bv[L::kSt], was[L::kPairs];
-                L::channels(de, &s.delta[i][p.local]);
-                L::channels(dx, &s.dx[i][p.local]);
-                L::states(bv, s.b + i * L::kStWidth + at_state);
+        for (int i = 0; i < rows; ++i) {
+            if (starts >> i & 1) begin(t0 + i);
+            f2 de[L::kCh], dx[L::kCh], bv[L::kSt], was[L::kPairs];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            L::states(bv, s.b + i * L::kStWidth + at_state);
 #pragma unroll
-                for (int q = 0; q < L::kPairs; ++q) {
-                    was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
-                    h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
-                }
-                if (i >= r0)
-#pragma unroll
-                    for (int q = 0; q < L::kPairs; q += 2)
-                        s.p[i - r0][q / 2][threadIdx.x] = make_ulonglong2(was[q], was[q + 1]);
+            for (int q = 0; q < L::kPairs; ++q) {
+                was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
+                h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
             }
-#pragma unroll 1
-            for (int i = stop - 1; i >= r0; --i) {
-                const int r = i - r0;
-                f2 de[L::kCh], dx[L::kCh], gy[L::kCh], bv[L::kSt], cv[L::kSt];
-                L::channels(de, &s.delta[i][p.local]);
-                L::channels(dx, &s.dx[i][p.local]);
-                L::channels(gy, &s.dy[i][p.local]);
-                L::states(bv, s.b + i * L::kStWidth + at_state);
-                L::states(cv, s.c + i * L::kStWidth + at_state);
-                f2 sb[L::kCh], sa[L::kCh], sy[L::kCh], db[L::kSt], dc[L::kSt];
 #pragma unroll
-                for (int q = 0; q < L::kPairs; ++q) {
-                    const int c = L::ci(q), k = L::si(q);
-                    const ulonglong2 two = s.p[r][q / 2][threadIdx.x];
-                    const f2 was = q & 1 ? two.y : two.x;
-                    const f2 now = f2_fma(dx[c], bv[k], was);
-                    const f2 l = f2_fma(gy[c], cv[k], lam[q]);
-                    const f2 w = f2_mul(l, was);
-                    dc[k] = c == 0 ? f2_mul(gy[c], now) : f2_fma(gy[c], now, dc[k]);
-                    db[k] = c == 0 ? f2_mul(l, dx[c]) : f2_fma(l, dx[c], db[k]);
-                    sb[c] = k == 0 ? f2_mul(l, bv[k]) : f2_fma(l, bv[k], sb[c]);
-                    sy[c] = k == 0 ? f2_mul(cv[k], now) : f2_fma(cv[k], now, sy[c]);
-                    sa[c] = k == 0 ? f2_mul(w, a2[q]) : f2_fma(w, a2[q], sa[c]);
-                    da[q] = f2_fma(w, de[c], da[q]);
-                    lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
-                }
-                float v[8], ch[3][CPT];
-                if constexpr (L::kWide) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        v[k] = f2_sum(db[k]);
-                        v[4 + k] = f2_sum(dc[k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < L::kCh; ++k) {
-                        f2_split(sb[k], ch[0][2 * k], ch[0][2 * k + 1]);
-                        f2_split(sa[k], ch[1][2 * k], ch[1][2 * k + 1]);
-                        f2_split(sy[k], ch[2][2 * k], ch[2][2 * k + 1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        f2_split(db[k], v[2 * k], v[2 * k + 1]);
-                        f2_split(dc[k], v[4 + 2 * k], v[4 + 2 * k + 1]);
-                    }
-                    ch[0][0] = f2_sum(sb[0]);
-                    ch[1][0] = f2_sum(sa[0]);
-                    ch[2][0] = f2_sum(sy[0]);
-                }
-                if (n < L::NP)      // threads past the last state take no part in sums
-#pragma unroll
-                    for (int k = 0; k < CPT; ++k)
-                        if (!mine) ch[0][k] = ch[1][k] = ch[2][k] = 0.0f;
-                float4* part = reinterpret_cast<float4*>(&s.p[r][0][threadIdx.x]);
-                part[0] = make_float4(v[0], v[1], v[2], v[3]);
-                part[kThreads] = make_float4(v[4], v[5], v[6], v[7]);
-                const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]),
-                            y = sum_states<LS, CPT>(ch[2]);
-                if (returns_channel<LS, CPT>()) {
-                    const int at = p.local + which_channel<LS, CPT>();
-                    s.sum_b[r][at] = to_b;
-                    s.sum_a[r][at] = to_a;
-                    s.y[r][at] = y;
-                }
-                if (starts >> i & 1) {
-                    const int t = t0 + i;
-                    if (a.d_init != nullptr) {
-                        const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
-                        if (e < a.episodes) store_states<LS, CPT>(a.d_init + e * row_states, lam, n, p.ch, p.count, p.n0);
-                    }
-                    if (t > s0) enter(t - 1);
-                }
-            }
-            __syncthreads();
-            // from shared memory to the gradients
-            const int64_t ch = b.ch0 + Ti::col();
-#pragma unroll
-            for (int j = 0; j < Ti::NV; ++j) {
-                const int r = Ti::row(j), i = r0 + r;
-                if (r >= count || Ti::col() >= b.count) continue;
-                float out_x[Ti::V], out_dt[Ti::V], out_z[Ti::V];
-                float d[Ti::V], to_b[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V], to_a[Ti::V], y[Ti::V];
-                load_vec<float, Ti::V>(d, &s.delta[i][Ti::col()]);
-                load_vec<float, Ti::V>(to_b, &s.sum_b[r][Ti::col()]);
-                load_vec<float, Ti::V>(gy, &s.dy[i][Ti::col()]);
-                load_vec<float, Ti::V>(xs, &s.x[i][Ti::col()]);
-                load_vec<float, Ti::V>(sl, &s.slope[i][Ti::col()]);
-                load_vec<float, Ti::V>(to_a, &s.sum_a[r][Ti::col()]);
-                if (a.in.z != nullptr) {
-                    load_vec<float, Ti::V>(gt, &s.gate[i][Ti::col()]);
-                    load_vec<float, Ti::V>(y, &s.y[r][Ti::col()]);
-                }
-#pragma unroll
-                for (int k = 0; k < Ti::V; k += 2) {
-                    const f2 xv = pair_at(xs, k), gv = pair_at(gy, k), tb = pair_at(to_b, k), sk = pair_at(skip, k);
-                    f2 v = f2_mul(pair_at(d, k), tb);
-                    if (a.in.d != nullptr) v = f2_fma(sk, gv, v);
-                    set_pair(out_x, k, v);
-                    v = f2_mul(f2_fma(xv, tb, f2_mul(pair_at(to_a, k), f2_both(kLn2))), pair_at(sl, k));
-                    set_pair(out_dt, k, v);
-                    set_pair(dskip, k, f2_fma(gv, xv, pair_at(dskip, k)));
-                    set_pair(dbias, k, f2_add(v, pair_at(dbias, k)));
-                    if (a.in.z != nullptr) {
-                        f2 yv = pair_at(y, k);
-                        if (a.in.d != nullptr) yv = f2_fma(sk, xv, yv);
-                        set_pair(out_z, k, f2_mul(pair_at(gt, k), yv));
-                    }
-                }
-                const int64_t t = t1 + r;
-                store_vec<T, Ti::V>(static_cast<T*>(a.grads.dx) + t * a.grads.x_stride + ch, out_x);
-                store_vec<T, Ti::V>(static_cast<T*>(a.grads.ddt) + t * a.grads.dt_stride + ch, out_dt);
-                if (a.in.z != nullptr)
-                    store_vec<T, Ti::V>(static_cast<T*>(a.grads.dz) + t * a.grads.z_stride + ch, out_z);
-            }
-            ChannelSums<LS, GradShared<LS, CPT>::kSlots>::run(reinterpret_cast<const float4*>(s.p), count, [&](int r, int half, int st, const float4& v) {
-                const int64_t t = t1 + r;
-                if (parts > 1) {
-                    *reinterpret_cast<float4*>(dbc + t * dbc_stride + half * L::NP + st) = v;
-                } else if (st < n) {
-                    T* out = half ? static_cast<T*>(a.grads.dc) + t * a.grads.c_stride
-                                  : static_cast<T*>(a.grads.db) + t * a.grads.b_stride;
-                    out += b.group * n + st;
-                    out[0] = from_float<T>(v.x);
-                    out[1] = from_float<T>(v.y);
-                    out[2] = from_float<T>(v.z);
-                    out[3] = from_float<T>(v.w);
-                }
-            });
-            __syncthreads();
+            for (int q = 0; q < L::kPairs; q += 2) s.p[i][q / 2][threadIdx.x] = make_ulonglong2(was[q], was[q + 1]);
         }
+#pragma unroll 1
+        for (int i = rows - 1; i >= 0; --i) {
+            f2 de[L::kCh], dx[L::kCh], gy[L::kCh], bv[L::kSt], cv[L::kSt];
+            L::channels(de, &s.delta[i][p.local]);
+            L::channels(dx, &s.dx[i][p.local]);
+            L::channels(gy, &s.dy[i][p.local]);
+            L::states(bv, s.b + i * L::kStWidth + at_state);
+            L::states(cv, s.c + i * L::kStWidth + at_state);
+            f2 sb[L::kCh], sa[L::kCh], sy[L::kCh], db[L::kSt], dc[L::kSt];
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) {
+                const int c = L::ci(q), k = L::si(q);
+                const ulonglong2 two = s.p[i][q / 2][threadIdx.x];
+                const f2 was = q & 1 ? two.y : two.x;
+                const f2 now = f2_fma(dx[c], bv[k], was);
+                const f2 l = f2_fma(gy[c], cv[k], lam[q]);
+                const f2 w = f2_mul(l, was);
+                dc[k] = c == 0 ? f2_mul(gy[c], now) : f2_fma(gy[c], now, dc[k]);
+                db[k] = c == 0 ? f2_mul(l, dx[c]) : f2_fma(l, dx[c], db[k]);
+                sb[c] = k == 0 ? f2_mul(l, bv[k]) : f2_fma(l, bv[k], sb[c]);
+                sy[c] = k == 0 ? f2_mul(cv[k], now) : f2_fma(cv[k], now, sy[c]);
+                sa[c] = k == 0 ? f2_mul(w, a2[q]) : f2_fma(w, a2[q], sa[c]);
+                da[q] = f2_fma(w, de[c], da[q]);
+                lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
+            }
+            float v[8], ch[3][CPT];
+            if constexpr (L::kWide) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = f2_sum(db[k]);
+                    v[4 + k] = f2_sum(dc[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < L::kCh; ++k) {
+                    f2_split(sb[k], ch[0][2 * k], ch[0][2 * k + 1]);
+                    f2_split(sa[k], ch[1][2 * k], ch[1][2 * k + 1]);
+                    f2_split(sy[k], ch[2][2 * k], ch[2][2 * k + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f2_split(db[k], v[2 * k], v[2 * k + 1]);
+                    f2_split(dc[k], v[4 + 2 * k], v[4 + 2 * k + 1]);
+                }
+                ch[0][0] = f2_sum(sb[0]);
+                ch[1][0] = f2_sum(sa[0]);
+                ch[2][0] = f2_sum(sy[0]);
+            }
+            if (n < L::NP)      // threads past the last state take no part in sums
+#pragma unroll
+                for (int k = 0; k < CPT; ++k)
+                    if (!mine) ch[0][k] = ch[1][k] = ch[2][k] = 0.0f;
+            float4* part = reinterpret_cast<float4*>(&s.p[i][0][threadIdx.x]);
+            part[0] = make_float4(v[0], v[1], v[2], v[3]);
+            part[kThreads] = make_float4(v[4], v[5], v[6], v[7]);
+            const float to_b = sum_states<LS, CPT>(ch[0]), to_a = sum_states<LS, CPT>(ch[1]),
+                        y = sum_states<LS, CPT>(ch[2]);
+            if (returns_channel<LS, CPT>()) {
+                const int at = p.local + which_channel<LS, CPT>();
+                s.sum_b[i][at] = to_b;
+                s.sum_a[i][at] = to_a;
+                s.y[i][at] = y;
+            }
+            if (starts >> i & 1) {
+                const int t = t0 + i;
+                if (a.d_init != nullptr) {
+                    const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
+                    if (e < a.episodes) store_states<LS, CPT>(a.d_init + e * row_states, lam, n, p.ch, p.count, p.n0);
+                }
+                if (t > s0) enter(t - 1);
+            }
+        }
+        __syncthreads();
+        // from shared memory to the gradients
+        const int64_t ch = b.ch0 + Ti::col();
+#pragma unroll
+        for (int j = 0; j < Ti::NV; ++j) {
+            const int r = Ti::row(j);
+            if (r >= rows || Ti::col() >= b.count) continue;
+            float out_x[Ti::V], out_dt[Ti::V], out_z[Ti::V];
+            float d[Ti::V], to_b[Ti::V], gy[Ti::V], xs[Ti::V], sl[Ti::V], gt[Ti::V], to_a[Ti::V], y[Ti::V];
+            load_vec<float, Ti::V>(d, &s.delta[r][Ti::col()]);
+            load_vec<float, Ti::V>(to_b, &s.sum_b[r][Ti::col()]);
+            load_vec<float, Ti::V>(gy, &s.dy[r][Ti::col()]);
+            load_vec<float, Ti::V>(xs, &s.x[r][Ti::col()]);
+            load_vec<float, Ti::V>(sl, &s.slope[r][Ti::col()]);
+            load_vec<float, Ti::V>(to_a, &s.sum_a[r][Ti::col()]);
+            if (a.in.z != nullptr) {
+                load_vec<float, Ti::V>(gt, &s.gate[r][Ti::col()]);
+                load_vec<float, Ti::V>(y, &s.y[r][Ti::col()]);
+            }
+#pragma unroll
+            for (int k = 0; k < Ti::V; k += 2) {
+                const f2 xv = pair_at(xs, k), gv = pair_at(gy, k), tb = pair_at(to_b, k), sk = pair_at(skip, k);
+                f2 v = f2_mul(pair_at(d, k), tb);
+                if (a.in.d != nullptr) v = f2_fma(sk, gv, v);
+                set_pair(out_x, k, v);
+                v = f2_mul(f2_fma(xv, tb, f2_mul(pair_at(to_a, k), f2_both(kLn2))), pair_at(sl, k));
+                set_pair(out_dt, k, v);
+                set_pair(dskip, k, f2_fma(gv, xv, pair_at(dskip, k)));
+                set_pair(dbias, k, f2_add(v, pair_at(dbias, k)));
+                if (a.in.z != nullptr) {
+                    f2 yv = pair_at(y, k);
+                    if (a.in.d != nullptr) yv = f2_fma(sk, xv, yv);
+                    set_pair(out_z, k, f2_mul(pair_at(gt, k), yv));
+                }
+            }
+            const int64_t t = t0 + r;
+            store_vec<T, Ti::V>(static_cast<T*>(a.grads.dx) + t * a.grads.x_stride + ch, out_x);
+            store_vec<T, Ti::V>(static_cast<T*>(a.grads.ddt) + t * a.grads.dt_stride + ch, out_dt);
+            if (a.in.z != nullptr)
+                store_vec<T, Ti::V>(static_cast<T*>(a.grads.dz) + t * a.grads.z_stride + ch, out_z);
+        }
+        ChannelSums<LS, GradShared<LS, CPT>::kSlots>::run(reinterpret_cast<const float4*>(s.p), rows, [&](int r, int half, int st, const float4& v) {
+            const int64_t t = t0 + r;
+            if (parts > 1) {
+                *reinterpret_cast<float4*>(dbc + t * dbc_stride + half * L::NP + st) = v;
+            } else if (st < n) {
+                T* out = half ? static_cast<T*>(a.grads.dc) + t * a.grads.c_stride
+                              : static_cast<T*>(a.grads.db) + t * a.grads.b_stride;
+                out += b.group * n + st;
+                out[0] = from_float<T>(v.x);
+                out[1] = from_float<T>(v.y);
+                out[2] = from_float<T>(v.z);
+                out[3] = from_float<T>(v.w);
+            }
+        });
+        __syncthreads();
     }
 
     store_states<LS, CPT>(a.da + (int64_t)blockIdx.x * row_states, da, n, p.ch, p.count, p.n0);
@@ -636,13 +623,13 @@ cudaError_t go(const Launch& a, const Cut& c, cudaStream_t st) {
 
 template <typename T>
 cudaError_t run(const Launch& a, const Cut& c, cudaStream_t st) {
-    const bool wide = c.cpt > 1;
+    const bool wide = c.cpt == wide_of(c.ls);
     switch (c.ls) {
         case 1: return go<T, 1, 1>(a, c, st);
         case 2: return wide ? go<T, 2, 2>(a, c, st) : go<T, 2, 1>(a, c, st);
-        case 4: return wide ? go<T, 4, 2>(a, c, st) : go<T, 4, 1>(a, c, st);
-        case 8: return wide ? go<T, 8, 2>(a, c, st) : go<T, 8, 1>(a, c, st);
-        default: return wide ? go<T, 16, 2>(a, c, st) : go<T, 16, 1>(a, c, st);
+        case 4: return wide ? go<T, 4, 4>(a, c, st) : go<T, 4, 2>(a, c, st);
+        case 8: return wide ? go<T, 8, 4>(a, c, st) : go<T, 8, 2>(a, c, st);
+        default: return wide ? go<T, 16, 4>(a, c, st) : go<T, 16, 2>(a, c, st);
     }
 }
 

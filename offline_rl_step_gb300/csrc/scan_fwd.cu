@@ -293,8 +293,11 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
         }
         copies_commit();
         const uint32_t starts = (s.mask[(t0 - s0) >> 5] >> ((t0 - s0) & 31)) & ((1u << kTile) - 1);
-        if (a.saved != nullptr && !(starts & 1))
-            store_states<LS, CPT>(a.saved + (int64_t)(t0 / kTile) * row_states, h, n, p.ch, p.count, p.n0);
+        // the state before token i, unless an episode begins there
+        auto save = [&](int i) {
+            if (a.saved != nullptr && !(starts >> i & 1))
+                store_states<LS, CPT>(a.saved + (int64_t)((t0 + i) / kSave) * row_states, h, n, p.ch, p.count, p.n0);
+        };
         // a token's part of sum_n C h, from this thread's states
         auto step = [&](int i, float (&y)[CPT]) {
             f2 de[L::kCh], dx[L::kCh], bv[L::kSt], cv[L::kSt];
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
             constexpr int kTogether = 4;
 #pragma unroll 1
             for (int i = 0; i < kTile; i += kTogether) {
+                if (i % kSave == 0) save(i);
                 float y[kTogether][CPT], sum[kTogether];
 #pragma unroll
                 for (int k = 0; k < kTogether; ++k) step(i + k, y[k]);
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
         } else {
 #pragma unroll 1
             for (int i = 0; i < rows; ++i) {
+                if (i % kSave == 0) save(i);
                 if (starts >> i & 1) {
                     if (t0 + i > s0) {
                         leave();

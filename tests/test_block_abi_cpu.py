@@ -55,10 +55,10 @@ def test_struct_layouts(tmp_path):
 def test_sizes(lib):
     from offline_rl_step_gb300 import _abi
     ok = _abi.ScanShape(512, 16, 1, 1, 1)
-    # a state for every sixteen tokens
-    assert lib.ofrl_scan_saved_bytes(C.byref(ok), 33) == 3 * 512 * 16 * 4
+    # a state for every eight tokens
+    assert lib.ofrl_scan_saved_bytes(C.byref(ok), 33) == 5 * 512 * 16 * 4
     assert lib.ofrl_scan_saved_bytes(C.byref(ok), 0) == 0
-    assert lib.ofrl_scan_saved_bytes(C.byref(_abi.ScanShape(4096, 64, 1, 1, 1)), 2 ** 20) == 2 ** 36      # past 32 bits
+    assert lib.ofrl_scan_saved_bytes(C.byref(_abi.ScanShape(4096, 64, 1, 1, 1)), 2 ** 20) == 2 ** 37      # past 32 bits
     for bad in (-1, 2 ** 31):
         assert lib.ofrl_scan_saved_bytes(C.byref(ok), bad) == -1
         assert lib.ofrl_scan_workspace_bytes(C.byref(ok), bad, 1, 1) == -1
