@@ -42,7 +42,7 @@ Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_s
         c.seg = (int)seg;
         const int64_t n = div_up(tokens, seg);
         c.n_seg = (int)(n > 1 ? n : 1);
-        if (cpt == narrow || whole || (int64_t)c.blocks * c.n_seg >= 2 * num_sms) return c;
+        if (cpt == narrow || whole || 2 * (int64_t)c.blocks * c.n_seg >= (backward ? 3 : 4) * num_sms) return c;
     }
 }
 
