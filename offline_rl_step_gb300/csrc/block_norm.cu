@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) gated_norm_kernel(co
     constexpr int V = kVec<T>;
     extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
-    pdl_trigger();
     const Seat<CTA> s(a);
     auto stage = [&]() { stage_weights<V, NV>(dynamic, a.weight, a); };
     const Weights<V> w(dynamic, s.lane, a.tg);
@@ -286,7 +285,6 @@ __global__ void __launch_bounds__(CTA ? 512 : kWarpThreads) residual_norm_kernel
     constexpr int V = kVec<T>;
     extern __shared__ __align__(16) float dynamic[];
     pdl_wait();
-    pdl_trigger();
     const Seat<CTA> s(a);
     float* scales = dynamic + weight_floats(a.tg, NV, V);
     auto stage = [&]() {
@@ -527,7 +525,6 @@ struct NormJoin {
 __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const __grid_constant__ NormJoin a) {
     __shared__ float red[kSlices][33];
     pdl_wait();
-    pdl_trigger();
     const int c = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
     float* out = a.out[blockIdx.y];
     if (out == nullptr) return;

@@ -236,7 +236,6 @@ __global__ void __launch_bounds__(kThreads, 2) conv_forward_kernel(const __grid_
     Ring<T, V, 1>& ring = *reinterpret_cast<Ring<T, V, 1>*>(dynamic);
     __shared__ Marks m;
     pdl_wait();
-    pdl_trigger();
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
     const int runs = kThreads / a.lanes, lane = threadIdx.x % a.lanes, y = threadIdx.x / a.lanes;
     const int64_t from = (int64_t)blockIdx.x * runs * a.run;
@@ -498,7 +497,7 @@ constexpr int kJoinThreads = 1024, kSlices = kJoinThreads / 32;
 __global__ void __launch_bounds__(kJoinThreads) conv_join_kernel(const __grid_constant__ ConvLaunch a, int64_t rows) {
     __shared__ float red[kSlices][33];
     pdl_wait();
-    pdl_trigger();
+    if (a.d_init != nullptr) pdl_trigger();      // conv_init_grad_kernel is next
     const int w = a.shape.width;
     const int64_t all = (int64_t)a.shape.channels * (w + 1), i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
     const int slice = threadIdx.x / 32;
@@ -526,7 +525,6 @@ __global__ void __launch_bounds__(kJoinThreads) conv_join_kernel(const __grid_co
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_init_grad_kernel(const __grid_constant__ ConvLaunch a) {
     pdl_wait();
-    pdl_trigger();
     const int tokens = (int)a.in.tokens, d = a.shape.channels;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, e = i / (d / 2);
     const int ch = (int)(i - e * (d / 2)) * 2;
@@ -569,7 +567,6 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_constant__ ConvStepLaunch a) {
     constexpr int V = 16 / (int)sizeof(T), kVecs = 8 / V, S = W - 1;
     pdl_wait();
-    pdl_trigger();
     const int d = a.shape.channels, cols = d / 8;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, row = i / cols;
     const int ch = (int)(i - row * cols) * 8;

@@ -543,7 +543,6 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) scan_grad_join_kernel(const __grid_constant__ Launch a, int np, unsigned over) {
     __shared__ float red[kSlices][33];
     pdl_wait();
-    pdl_trigger();
     const int n = a.shape.state_dim, d = a.shape.channels;
     if (blockIdx.x < over) {
         const int64_t states = (int64_t)d * n, i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;

@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
     extern __shared__ __align__(16) uint8_t dynamic[];
     auto& s = *reinterpret_cast<ForwardShared<T, LS, CPT>*>(dynamic);
     pdl_wait();
-    pdl_trigger();
     const int tokens = (int)a.in.tokens, n = a.shape.state_dim;
     const int64_t row_states = (int64_t)a.shape.channels * n;
     const int s0 = (int)((int64_t)blockIdx.x * a.seg), s1 = (int)min((int64_t)s0 + a.seg, (int64_t)tokens);

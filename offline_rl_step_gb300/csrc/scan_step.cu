@@ -24,7 +24,6 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const __grid_co
     const bool on = n0 < n && ch0 < d, own = lane < CPT && mine < d;
     const int group = min(ch0, d - 1) / per;
     pdl_wait();
-    pdl_trigger();
     float4 a2[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {

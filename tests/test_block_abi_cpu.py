@@ -155,3 +155,23 @@ def test_binding_refuses_wrong_contexts():
     closed.handle = None
     with pytest.raises(ValueError, match="closed"):
         ofrl.residual_norm(closed, None, None, None, None, None)
+
+
+def test_last_kernels_of_a_call_do_not_let_go_early():
+    """What follows a call may be a kernel that reads its results before it waits: only kernels that one of the same
+    call follows let it start ahead."""
+    src = os.path.join(ROOT, "offline_rl_step_gb300", "csrc")
+    last = {"conv.cu": ("conv_forward_kernel", "conv_init_grad_kernel", "conv_step_kernel"),
+            "block_norm.cu": ("gated_norm_kernel", "residual_norm_kernel", "norm_join_kernel"),
+            "scan_fwd.cu": ("scan_forward_kernel",), "scan_bwd.cu": ("scan_grad_join_kernel",),
+            "scan_step.cu": ("scan_step_kernel",)}
+    for name, kernels in last.items():
+        text = open(os.path.join(src, name)).read()
+        bodies = text.split("__global__")[1:]
+        for k in kernels:
+            mine = [b for b in bodies if f" {k}(const __grid_constant__" in b.split("{")[0]]
+            assert len(mine) == 1 and "pdl_wait();" in mine[0] and "pdl_trigger" not in mine[0], k
+        for b in bodies:      # every kernel waits before it lets go
+            assert "pdl_wait();" in b
+            if "pdl_trigger" in b:
+                assert b.index("pdl_wait();") < b.index("pdl_trigger")
