@@ -626,7 +626,7 @@ typedef struct {
     const float* weight;    /* [channels, width] */
     const float* bias;      /* [channels] or NULL */
     int64_t x_stride;
-    int64_t tokens;         /* 0 .. 2^31-1 */
+    int64_t tokens;         /* 0 .. 2^31 - 2^17 */
 } ofrl_conv_tokens;
 
 /* Gradients, written (not accumulated). */
@@ -701,7 +701,7 @@ typedef struct {
     const float* d;         /* [channels] or NULL (zero) */
     const float* dt_bias;   /* [channels] or NULL (zero) */
     int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
-    int64_t tokens;         /* 0 .. 2^31-1 */
+    int64_t tokens;         /* 0 .. 2^31 - 2^17 */
 } ofrl_scan_tokens;
 
 /* Gradients, written (not accumulated); same layouts, alignments and stride

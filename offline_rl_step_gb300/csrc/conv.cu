@@ -628,7 +628,6 @@ cudaError_t forward(const ConvLaunch& in, int num_sms, cudaStream_t st) {
     const ConvCut c = conv_cut(a.shape.channels, V, a.in.tokens, num_sms);
     a.lanes = c.lanes;
     a.run = c.run;
-    if (c.rows > INT32_MAX) return cudaErrorInvalidValue;
     const cudaError_t e = opt_in_once(conv_forward_kernel<T, W, V>, (int)sizeof(Ring<T, V, 1>), done);
     if (e != cudaSuccess) return e;
     return launch_pdl(conv_forward_kernel<T, W, V>, dim3((unsigned)c.rows, (unsigned)c.cols), dim3(kThreads),
@@ -692,7 +691,7 @@ ofrl_status check_shape(const ofrl_conv_shape* s) {
 }
 
 ofrl_status check_tokens(const ofrl_conv* ctx, const ofrl_conv_tokens* t) {
-    if (t == nullptr || t->tokens < 0 || t->tokens > INT32_MAX) return OFRL_EINVAL;
+    if (t == nullptr || t->tokens < 0 || t->tokens > kMaxTokens) return OFRL_EINVAL;
     if (t->weight == nullptr || !aligned_to(t->weight, 4) || !aligned_to(t->bias, 4)) return OFRL_EINVAL;
     if (t->tokens > 0 && !rows_ok(t->x, t->x_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
     return OFRL_OK;

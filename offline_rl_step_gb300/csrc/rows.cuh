@@ -10,8 +10,10 @@ namespace ofrl {
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int64_t dtype_size(int32_t dtype) { return dtype == OFRL_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_ok(int32_t dtype) { return dtype == OFRL_DTYPE_F32 || dtype == OFRL_DTYPE_BF16; }
+// Tokens of a call, at most: an index may run a CTA's tokens past them.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - ((int64_t)1 << 17);
 inline bool counts_ok(int64_t tokens, int64_t episodes) {
-    return tokens >= 0 && tokens <= INT32_MAX && episodes >= 0 && episodes <= INT32_MAX;
+    return tokens >= 0 && tokens <= kMaxTokens && episodes >= 0 && episodes <= INT32_MAX;
 }
 // Rows of `width` elements: at least that far apart, addressable.
 inline bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride <= (int64_t)1 << 40; }

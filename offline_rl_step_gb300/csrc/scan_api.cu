@@ -110,7 +110,7 @@ ofrl_status check_shape(const ofrl_scan_shape* s) {
 }
 
 ofrl_status check_tokens(const ofrl_scan* ctx, const ofrl_scan_tokens* t) {
-    if (t == nullptr || t->tokens < 0 || t->tokens > INT32_MAX) return OFRL_EINVAL;
+    if (t == nullptr || t->tokens < 0 || t->tokens > kMaxTokens) return OFRL_EINVAL;
     const ofrl_scan_shape& s = ctx->shape;
     if (t->a == nullptr || !aligned_to(t->a, 16) || !aligned_to(t->d, 4) || !aligned_to(t->dt_bias, 4)) return OFRL_EINVAL;
     if (t->tokens == 0) return OFRL_OK;

@@ -59,7 +59,7 @@ def test_sizes(lib):
     assert lib.ofrl_scan_saved_bytes(C.byref(ok), 33) == 5 * 512 * 16 * 4
     assert lib.ofrl_scan_saved_bytes(C.byref(ok), 0) == 0
     assert lib.ofrl_scan_saved_bytes(C.byref(_abi.ScanShape(4096, 64, 1, 1, 1)), 2 ** 20) == 2 ** 37      # past 32 bits
-    for bad in (-1, 2 ** 31):
+    for bad in (-1, 2 ** 31 - 2 ** 17 + 1, 2 ** 31):
         assert lib.ofrl_scan_saved_bytes(C.byref(ok), bad) == -1
         assert lib.ofrl_scan_workspace_bytes(C.byref(ok), bad, 1, 1) == -1
     reading = lib.ofrl_scan_workspace_bytes(C.byref(ok), 65536, 228, 0)
@@ -77,7 +77,7 @@ def test_workspace_covers_smaller_calls(lib):
     from offline_rl_step_gb300 import _abi
     for shape in ((8, 4, 1), (512, 16, 1), (1024, 64, 2), (72, 12, 3), (65536, 8, 1)):
         s, last = C.byref(_abi.ScanShape(shape[0], shape[1], shape[2], 1, 1)), 0
-        for t in (0, 1, 15, 16, 63, 64, 65, 1000, 4096, 50000, 10 ** 6, 10 ** 7, 2 ** 31 - 1):
+        for t in (0, 1, 15, 16, 63, 64, 65, 1000, 4096, 50000, 10 ** 6, 10 ** 7, 2 ** 31 - 2 ** 17):
             n = lib.ofrl_scan_workspace_bytes(s, t, 1, 1)
             assert n >= last
             last = n
