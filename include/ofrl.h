@@ -651,16 +651,17 @@ int64_t ofrl_conv_workspace_bytes(const ofrl_conv_shape* shape, int64_t max_toke
                                   int32_t backward);
 
 /* init_state, final_state: [num_episodes, channels, width - 1] in the tokens'
- * type, or NULL (zeros; not wanted).  final_state holds each episode's last
- * width - 1 inputs (an episode of fewer ends on its initial ones); it may be
- * init_state only where no backward call follows. */
+ * type, 16-byte aligned, or NULL (zeros; not wanted).  final_state holds each
+ * episode's last width - 1 inputs (an episode of fewer ends on its initial
+ * ones).  They must not overlap: parts of an episode run at the same time. */
 ofrl_status ofrl_conv_forward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
                               int32_t num_episodes, const void* init_state, void* out, int64_t out_stride,
                               void* final_state, void* stream);
 
 /* Gradients of the forward call with the same inputs: dout rows of out's
  * gradient; d_final: gradient of final_state, in the tokens' type, or NULL;
- * d_init: gradient of init_state, fp32, or NULL (not wanted). */
+ * d_init: gradient of init_state, fp32, or NULL (not wanted); it must not
+ * overlap the other states. */
 ofrl_status ofrl_conv_backward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* episode_ends,
                                int32_t num_episodes, const void* init_state, const void* dout, int64_t dout_stride,
                                const void* d_final, const ofrl_conv_grads* grads, float* d_init, void* stream);
@@ -734,15 +735,16 @@ int64_t ofrl_scan_workspace_bytes(const ofrl_scan_shape* shape, int64_t max_toke
 int64_t ofrl_scan_saved_bytes(const ofrl_scan_shape* shape, int64_t tokens);
 
 /* init_state, final_state: device fp32 [num_episodes, channels, N], 16-byte
- * aligned, or NULL (zero; not wanted); the same buffer only where no backward
- * call follows.  saved: as above, or NULL (no backward call will follow). */
+ * aligned, or NULL (zero; not wanted).  They must not overlap: parts of an
+ * episode run at the same time.  saved: as above, or NULL (no backward call will follow). */
 ofrl_status ofrl_scan_forward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* episode_ends,
                               int32_t num_episodes, const float* init_state, void* out, int64_t out_stride,
                               float* final_state, void* saved, void* stream);
 
 /* Gradients of the forward call that filled `saved` with the same inputs: dout
  * rows of out's gradient; d_final: gradient of final_state, or NULL (zero);
- * d_init: gradient of init_state, or NULL (not wanted); may be d_final. */
+ * d_init: gradient of init_state, or NULL (not wanted); it must not overlap the
+ * other states. */
 ofrl_status ofrl_scan_backward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* episode_ends,
                                int32_t num_episodes, const float* init_state, const void* saved, const void* dout,
                                int64_t dout_stride, const float* d_final, const ofrl_scan_grads* grads, float* d_init,

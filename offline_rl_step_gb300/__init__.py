@@ -826,6 +826,13 @@ def _open_ctx(ctx, kind):
     return ctx.handle
 
 
+def _same_device(ctx, *tensors):
+    """Raise for a tensor that is on another device than the workspace: a kernel would follow its address there."""
+    for t in tensors:
+        if t is not None and t.get_device() != ctx.device:
+            raise ValueError(f"every tensor must be on cuda:{ctx.device}, where the {type(ctx).__name__} is")
+
+
 def _tokens_of(x, channels: int, dtype, name: str) -> int:
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         _refuse(x, dtype, ("tokens", channels), name)
@@ -853,15 +860,16 @@ def conv_forward(ctx: CausalConv, x, weight, episode_ends, out, bias=None, init_
     """out = act(causal convolution of x) over packed episodes: x, out [tokens, channels] (may be slices with dense
     rows), weight float32 [channels, width] (the last tap takes the token itself), bias float32 [channels];
     episode_ends int32 [episodes].  init_state, final_state: [episodes, channels, width - 1] of x's type, the inputs
-    before an episode and its last ones."""
+    before an episode and its last ones (two buffers)."""
     handle = _open_ctx(ctx, CausalConv)
     t, rows = _conv_tokens(ctx, x, weight, bias)
     ne = episode_ends.numel()
     state = (ne, ctx.channels, ctx.width - 1)
     o, os = _rows2(out, ctx.dtype, rows, "out")
-    code = ctx._lib.ofrl_conv_forward(
-        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, ctx.dtype, state, "init_state"),
-        o, os, _dense(final_state, ctx.dtype, state, "final_state"), _raw_stream(stream, ctx.device))
+    init, final = _dense(init_state, ctx.dtype, state, "init_state"), _dense(final_state, ctx.dtype, state, "final_state")
+    ends = _dense(episode_ends, I32, (ne,), "episode_ends")
+    _same_device(ctx, x, weight, bias, episode_ends, out, init_state, final_state)
+    code = ctx._lib.ofrl_conv_forward(handle, t, ends, ne, init, o, os, final, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_conv_forward", code)
 
@@ -875,14 +883,14 @@ def conv_backward(ctx: CausalConv, x, weight, episode_ends, dout, dx, dweight, b
     ne, d = episode_ends.numel(), ctx.channels
     state = (ne, d, ctx.width - 1)
     g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
     if dweight is None:
         raise TypeError("dweight must be a CUDA tensor")
-    code = ctx._lib.ofrl_conv_backward(
-        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, ctx.dtype, state, "init_state"),
-        g, gs, _dense(d_final, ctx.dtype, state, "d_final"),
-        _pack_conv_grads(dx, _dense(dweight, F32, (d, ctx.width), "dweight"), _dense(dbias, F32, (d,), "dbias"), xs),
-        _dense(d_init, F32, state, "d_init"), _raw_stream(stream, ctx.device))
+    init, dfin = _dense(init_state, ctx.dtype, state, "init_state"), _dense(d_final, ctx.dtype, state, "d_final")
+    dini, ends = _dense(d_init, F32, state, "d_init"), _dense(episode_ends, I32, (ne,), "episode_ends")
+    grads = _pack_conv_grads(dxp, _dense(dweight, F32, (d, ctx.width), "dweight"), _dense(dbias, F32, (d,), "dbias"), xs)
+    _same_device(ctx, x, weight, bias, episode_ends, dout, dx, dweight, dbias, init_state, d_final, d_init)
+    code = ctx._lib.ofrl_conv_backward(handle, t, ends, ne, init, g, gs, dfin, grads, dini, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_conv_backward", code)
 
@@ -904,8 +912,9 @@ def conv_step(ctx: CausalConv, x, weight, state, out, bias=None, new_state=None,
     t, rows = _conv_tokens(ctx, x, weight, bias)
     at, to, ns = _state_pair(state, new_state, ctx.dtype, (ctx.channels, ctx.width - 1))
     o, os = _rows2(out, ctx.dtype, rows, "out")
-    code = ctx._lib.ofrl_conv_step(handle, t, _dense(slots, I32, (rows[0],), "slots"), ns, at, to, o, os,
-                                   _raw_stream(stream, ctx.device))
+    slot_idx = _dense(slots, I32, (rows[0],), "slots")
+    _same_device(ctx, x, weight, bias, state, new_state, slots, out)
+    code = ctx._lib.ofrl_conv_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_conv_step", code)
 
@@ -939,16 +948,17 @@ def scan_forward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, out, D=None, 
                  final_state=None, saved=None, stream=None):
     """The selective scan over packed episodes: x, dt, z, out [tokens, channels], B, C [tokens, groups, state_dim] (all
     may be slices with dense rows); A float32 [channels, state_dim] (negative), D and dt_bias float32 [channels];
-    episode_ends int32 [episodes].  init_state, final_state: float32 [episodes, channels, state_dim].  saved:
-    ctx.saved(tokens), filled for scan_backward."""
+    episode_ends int32 [episodes].  init_state, final_state: float32 [episodes, channels, state_dim] (two buffers).
+    saved: ctx.saved(tokens), filled for scan_backward."""
     handle = _open_ctx(ctx, SelectiveScan)
     t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
     ne = episode_ends.numel()
     state = (ne, ctx.channels, ctx.state_dim)
     o, os = _rows2(out, ctx.dtype, rows, "out")
-    code = ctx._lib.ofrl_scan_forward(
-        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, F32, state, "init_state"), o, os,
-        _dense(final_state, F32, state, "final_state"), _scan_saved(ctx, saved, rows[0]), _raw_stream(stream, ctx.device))
+    init, final = _dense(init_state, F32, state, "init_state"), _dense(final_state, F32, state, "final_state")
+    ends, kept = _dense(episode_ends, I32, (ne,), "episode_ends"), _scan_saved(ctx, saved, rows[0])
+    _same_device(ctx, x, dt, A, B, C, episode_ends, out, D, z, dt_bias, init_state, final_state, saved)
+    code = ctx._lib.ofrl_scan_forward(handle, t, ends, ne, init, o, os, final, kept, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_scan_forward", code)
 
@@ -967,17 +977,20 @@ def scan_backward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, saved, dout,
     ne, d, ty = episode_ends.numel(), ctx.channels, ctx.dtype
     state = (ne, d, ctx.state_dim)
     g, gs = _rows2(dout, ty, rows, "dout")
-    dx, xs = _rows2(dx, ty, rows, "dx")
-    ddt, ds = _rows2(ddt, ty, rows, "ddt")
-    dB, bs = _rows3(dB, ty, bc, "dB")
-    dC, cs = _rows3(dC, ty, bc, "dC")
-    dz, zs = (0, 0) if dz is None else _rows2(dz, ty, rows, "dz")
-    code = ctx._lib.ofrl_scan_backward(
-        handle, t, _dense(episode_ends, I32, (ne,), "episode_ends"), ne, _dense(init_state, F32, state, "init_state"),
-        _scan_saved(ctx, saved, rows[0]), g, gs, _dense(d_final, F32, state, "d_final"),
-        _pack_scan_grads(dx, ddt, dB, dC, dz, _dense(dA, F32, (d, ctx.state_dim), "dA"), _dense(dD, F32, (d,), "dD"),
-                         _dense(ddt_bias, F32, (d,), "ddt_bias"), xs, ds, bs, cs, zs),
-        _dense(d_init, F32, state, "d_init"), _raw_stream(stream, ctx.device))
+    dxp, xs = _rows2(dx, ty, rows, "dx")
+    ddtp, ds = _rows2(ddt, ty, rows, "ddt")
+    dBp, bs = _rows3(dB, ty, bc, "dB")
+    dCp, cs = _rows3(dC, ty, bc, "dC")
+    dzp, zs = (0, 0) if dz is None else _rows2(dz, ty, rows, "dz")
+    init, dfin = _dense(init_state, F32, state, "init_state"), _dense(d_final, F32, state, "d_final")
+    dini, ends = _dense(d_init, F32, state, "d_init"), _dense(episode_ends, I32, (ne,), "episode_ends")
+    kept = _scan_saved(ctx, saved, rows[0])
+    grads = _pack_scan_grads(dxp, ddtp, dBp, dCp, dzp, _dense(dA, F32, (d, ctx.state_dim), "dA"), _dense(dD, F32, (d,), "dD"),
+                             _dense(ddt_bias, F32, (d,), "ddt_bias"), xs, ds, bs, cs, zs)
+    _same_device(ctx, x, dt, A, B, C, episode_ends, saved, dout, dx, ddt, dA, dB, dC, D, z, dt_bias, dD, dz, ddt_bias,
+                 init_state, d_final, d_init)
+    code = ctx._lib.ofrl_scan_backward(handle, t, ends, ne, init, kept, g, gs, dfin, grads, dini,
+                                       _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_scan_backward", code)
 
@@ -991,8 +1004,9 @@ def scan_step(ctx: SelectiveScan, x, dt, A, B, C, state, out, D=None, z=None, dt
     t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
     at, to, ns = _state_pair(state, new_state, F32, (ctx.channels, ctx.state_dim))
     o, os = _rows2(out, ctx.dtype, rows, "out")
-    code = ctx._lib.ofrl_scan_step(handle, t, _dense(slots, I32, (rows[0],), "slots"), ns, at, to, o, os,
-                                   _raw_stream(stream, ctx.device))
+    slot_idx = _dense(slots, I32, (rows[0],), "slots")
+    _same_device(ctx, x, dt, A, B, C, state, new_state, slots, out, D, z, dt_bias)
+    code = ctx._lib.ofrl_scan_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_scan_step", code)
 
@@ -1016,6 +1030,7 @@ def gated_norm(ctx: BlockNorm, x, z, weight, out, eps: float = 1e-5, gate_first:
     handle = _open_ctx(ctx, BlockNorm)
     t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
     o, os = _rows2(out, ctx.dtype, rows, "out")
+    _same_device(ctx, x, z, weight, out)
     code = ctx._lib.ofrl_gated_norm(handle, t, o, os, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_gated_norm", code)
@@ -1027,10 +1042,11 @@ def gated_norm_backward(ctx: BlockNorm, x, z, weight, dout, dx, dz, dweight, eps
     handle = _open_ctx(ctx, BlockNorm)
     t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
     g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
-    dz, zs = _rows2(dz, ctx.dtype, rows, "dz")
-    code = ctx._lib.ofrl_gated_norm_backward(handle, t, g, gs, dx, xs, dz, zs, _norm_weight(ctx, dweight, "dweight"),
-                                             _raw_stream(stream, ctx.device))
+    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    dzp, zs = _rows2(dz, ctx.dtype, rows, "dz")
+    dw = _norm_weight(ctx, dweight, "dweight")
+    _same_device(ctx, x, z, weight, dout, dx, dz, dweight)
+    code = ctx._lib.ofrl_gated_norm_backward(handle, t, g, gs, dxp, xs, dzp, zs, dw, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_gated_norm_backward", code)
 
@@ -1051,6 +1067,7 @@ def residual_norm(ctx: BlockNorm, x, residual, weight, residual_out, out, scale=
     t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
     r, rs = _rows2(residual_out, ctx.residual_dtype, rows, "residual_out")
     o, os = _rows2(out, ctx.dtype, rows, "out")
+    _same_device(ctx, x, residual, weight, residual_out, out, scale)
     code = ctx._lib.ofrl_residual_norm(handle, t, r, rs, o, os, _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_residual_norm", code)
@@ -1063,12 +1080,13 @@ def residual_norm_backward(ctx: BlockNorm, x, residual, weight, dout, dx, dresid
     handle = _open_ctx(ctx, BlockNorm)
     t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
     g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dx, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
     dr, drs = _rows2(dresidual, ctx.residual_dtype, rows, "dresidual")
     do, dos = (0, 0) if d_residual_out is None else _rows2(d_residual_out, ctx.residual_dtype, rows, "d_residual_out")
-    code = ctx._lib.ofrl_residual_norm_backward(
-        handle, t, g, gs, do, dos, dx, xs, dr, drs, _norm_weight(ctx, dweight, "dweight"),
-        _dense(dscale, F32, (ctx.channels,), "dscale"), _raw_stream(stream, ctx.device))
+    dw, dsc = _norm_weight(ctx, dweight, "dweight"), _dense(dscale, F32, (ctx.channels,), "dscale")
+    _same_device(ctx, x, residual, weight, dout, dx, dresidual, dweight, scale, dscale, d_residual_out)
+    code = ctx._lib.ofrl_residual_norm_backward(handle, t, g, gs, do, dos, dxp, xs, dr, drs, dw, dsc,
+                                                _raw_stream(stream, ctx.device))
     if code != _abi.OK:
         _abi.check("ofrl_residual_norm_backward", code)
 

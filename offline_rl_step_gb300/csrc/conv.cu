@@ -780,6 +780,8 @@ ofrl_status ofrl_conv_forward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const 
     const int64_t e = dtype_size(ctx->shape.dtype);
     if (in->tokens > 0 && !rows_ok(out, out_stride, ctx->shape.channels, e)) return OFRL_EINVAL;
     if (!aligned_to(init_state, 16) || !aligned_to(final_state, 16)) return OFRL_EINVAL;
+    const int64_t state = (int64_t)num_episodes * ctx->shape.channels * (ctx->shape.width - 1);
+    if (overlap(init_state, state * e, final_state, state * e)) return OFRL_EINVAL;
     ConvLaunch a = base_launch(ctx, in, episode_ends, num_episodes);
     a.init = init_state;
     a.out = out;
@@ -799,6 +801,9 @@ ofrl_status ofrl_conv_backward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const
     const int64_t e = dtype_size(ctx->shape.dtype);
     if (in->tokens > 0 && (!rows_ok(dout, dout_stride, ctx->shape.channels, e) ||
                            !rows_ok(grads->dx, grads->x_stride, ctx->shape.channels, e)))
+        return OFRL_EINVAL;
+    const int64_t state = (int64_t)num_episodes * ctx->shape.channels * (ctx->shape.width - 1);
+    if (overlap(init_state, state * e, d_init, state * 4) || overlap(d_final, state * e, d_init, state * 4))
         return OFRL_EINVAL;
     ConvLaunch a = base_launch(ctx, in, episode_ends, num_episodes);
     a.init = init_state;

@@ -21,6 +21,12 @@ inline bool stride_ok(int64_t stride, int64_t width) { return stride >= width &&
 inline bool rows_ok(const void* p, int64_t stride, int64_t width, int64_t elem) {
     return p != nullptr && aligned_to(p, 16) && stride_ok(stride, width) && stride * elem % 16 == 0;
 }
+// Buffers of so many bytes that share memory (NULL shares none).
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    if (a == nullptr || b == nullptr) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
 inline ofrl_status cuda_status(cudaError_t e) { return e == cudaSuccess ? OFRL_OK : OFRL_ECUDA; }
 // The context's device must be the current one.
 template <typename Ctx>

@@ -213,6 +213,8 @@ ofrl_status ofrl_scan_forward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const 
     if (num_episodes == 0) return OFRL_OK;
     if (in->tokens > 0 && !rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
     if (!aligned_to(init_state, 16) || !aligned_to(final_state, 16) || !aligned_to(saved, 16)) return OFRL_EINVAL;
+    const int64_t state = (int64_t)num_episodes * ctx->shape.channels * ctx->shape.state_dim * 4;
+    if (overlap(init_state, state, final_state, state)) return OFRL_EINVAL;
     const Cut c = cut_of(ctx->shape, in->tokens, num_episodes, ctx->num_sms, false);
     scan::Launch a = base_launch(ctx, in, episode_ends, num_episodes, c, false);
     a.init = init_state;
@@ -235,6 +237,8 @@ ofrl_status ofrl_scan_backward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const
     if (!aligned_to(init_state, 16) || !aligned_to(saved, 16) || !aligned_to(d_final, 16) || !aligned_to(d_init, 16))
         return OFRL_EINVAL;
     const ofrl_scan_shape& h = ctx->shape;
+    const int64_t state = (int64_t)num_episodes * h.channels * h.state_dim * 4;
+    if (overlap(init_state, state, d_init, state) || overlap(d_final, state, d_init, state)) return OFRL_EINVAL;
     if (in->tokens > 0) {
         const int64_t e = dtype_size(h.dtype), d = h.channels, bc = (int64_t)h.groups * h.state_dim;
         if (saved == nullptr || !rows_ok(dout, dout_stride, d, e)) return OFRL_EINVAL;
