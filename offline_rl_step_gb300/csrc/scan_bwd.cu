@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) scan_grad_tail_kernel(const __grid_c
             L::states(cv, s.c + i * L::kStWidth + L::state_at((threadIdx.x & 31) % LS));
 #pragma unroll
             for (int q = 0; q < L::kPairs; ++q) {
-                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                const f2 decay = f2_decay(de[L::ci(q)], a2[q]);
                 lam[q] = f2_mul(decay, f2_fma(gy[L::ci(q)], cv[L::si(q)], lam[q]));
             }
 #pragma unroll
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
             L::states(bv, s.b + i * L::kStWidth + at_state);
 #pragma unroll
             for (int q = 0; q < L::kPairs; ++q) {
-                was[q] = f2_mul(f2_exp2(f2_mul(de[L::ci(q)], a2[q])), h[q]);
+                was[q] = f2_mul(f2_decay(de[L::ci(q)], a2[q]), h[q]);
                 h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], was[q]);
             }
 #pragma unroll
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
                 sy[c] = k == 0 ? f2_mul(cv[k], now) : f2_fma(cv[k], now, sy[c]);
                 sa[c] = k == 0 ? f2_mul(w, a2[q]) : f2_fma(w, a2[q], sa[c]);
                 da[q] = f2_fma(w, de[c], da[q]);
-                lam[q] = f2_mul(f2_exp2(f2_mul(de[c], a2[q])), l);
+                lam[q] = f2_mul(f2_decay(de[c], a2[q]), l);
             }
             float v[8], ch[3][CPT];
             if constexpr (L::kWide) {

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_tail_kernel(const __grid_con
             L::states(bv, s.b + i * L::kStWidth + L::state_at((threadIdx.x & 31) % LS));
 #pragma unroll
             for (int q = 0; q < L::kPairs; ++q) {
-                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                const f2 decay = f2_decay(de[L::ci(q)], a2[q]);
                 h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], f2_mul(decay, h[q]));
             }
 #pragma unroll
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_forward_kernel(const __grid_
             f2 acc[L::kCh];
 #pragma unroll
             for (int q = 0; q < L::kPairs; ++q) {
-                const f2 decay = f2_exp2(f2_mul(de[L::ci(q)], a2[q]));
+                const f2 decay = f2_decay(de[L::ci(q)], a2[q]);
                 h[q] = f2_fma(dx[L::ci(q)], bv[L::si(q)], f2_mul(decay, h[q]));
                 acc[L::ci(q)] = L::si(q) == 0 ? f2_mul(cv[0], h[q]) : f2_fma(cv[L::si(q)], h[q], acc[L::ci(q)]);
             }

@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const __grid_co
             const int from = CPT == 4 ? (i >> 1 & 1) + 2 * (i & 1) : i;
             const float de = __shfl_sync(0xffffffffu, delta, from, LS), u = __shfl_sync(0xffffffffu, dx, from, LS);
             float4& v = k.h[i];
-            v.x = fmaf(exp2_of(de * a2[i].x), v.x, u * to_float(k.b.v[0]));
-            v.y = fmaf(exp2_of(de * a2[i].y), v.y, u * to_float(k.b.v[1]));
-            v.z = fmaf(exp2_of(de * a2[i].z), v.z, u * to_float(k.b.v[2]));
-            v.w = fmaf(exp2_of(de * a2[i].w), v.w, u * to_float(k.b.v[3]));
+            v.x = fmaf(decay_of(de, a2[i].x), v.x, u * to_float(k.b.v[0]));
+            v.y = fmaf(decay_of(de, a2[i].y), v.y, u * to_float(k.b.v[1]));
+            v.z = fmaf(decay_of(de, a2[i].z), v.z, u * to_float(k.b.v[2]));
+            v.w = fmaf(decay_of(de, a2[i].w), v.w, u * to_float(k.b.v[3]));
             if (on) __stcs(reinterpret_cast<float4*>(h + (int64_t)i * n), v);
             y[i] = on ? to_float(k.c.v[0]) * v.x + to_float(k.c.v[1]) * v.y + to_float(k.c.v[2]) * v.z +
                             to_float(k.c.v[3]) * v.w

@@ -178,6 +178,39 @@ def test_small_steps_keep_their_bits():
     np.testing.assert_allclose(first, want, rtol=2e-5)
 
 
+def test_steps_of_zero_keep_the_state():
+    import offline_rl_step_gb300 as ofrl
+    need_gpu()
+    t, c, n = 700, 16, 16
+    d = scan_inputs([t], c, n, 1, 3, "fp32")
+    d["dt"][:] = 0
+    got = _run(d, [t], "fp32", parts=(), softplus=False)
+    assert np.array_equal(got["final"], host(dev(d["init"])))
+    assert not got["x"].any()
+    ctx = ofrl.SelectiveScan(c, n, 1, "fp32", False, 0, 0, backward=False)
+    x, dt, A, B, C = (dev(d[k][:1] if k != "A" else d[k]) for k in ("x", "dt", "A", "B", "C"))
+    state = dev(d["init"])
+    was = state.clone()
+    for _ in range(10):
+        ofrl.scan_step(ctx, x, dt, A, B, C, state, torch.empty_like(x))
+    assert torch.equal(state, was)
+
+
+def test_slow_states():
+    """A state that remembers M = 120 tokens multiplies the mean error of a decay, 1.3e-8 at most, by M: 1.6e-6.  The
+    roundings of the decays, 3e-8 each, and of the sums, at most 2^-24, are independent and add sqrt(M / 2) times
+    themselves each: 2.3e-7 and 4.6e-7."""
+    need_gpu()
+    t, c, n = 3000, 64, 16
+    d = scan_inputs([t], c, n, 1, 4, "fp32")
+    rng = np.random.default_rng(5)
+    d["dt"] = (rng.uniform(2.0 ** -7, 2.0 ** -6, (t, c)) * np.log(2)).astype(np.float32)
+    d["x"], d["A"], d["B"] = np.ones_like(d["x"]), -np.ones_like(d["A"]), np.ones_like(d["B"])
+    got = _run(d, [t], "fp32", parts=(), states=False, grads=False, softplus=False)
+    want, _ = block.scan_forward(*(d[k] for k in ("x", "dt", "A", "B", "C")), ends_of([t]), softplus=False)
+    assert np.linalg.norm(got["out"] - want) <= 2.3e-6 * np.linalg.norm(want)
+
+
 def test_states_that_grow():
     """A above zero: nothing is clamped."""
     need_gpu()
