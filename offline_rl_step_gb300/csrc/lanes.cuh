@@ -145,7 +145,7 @@ __device__ __forceinline__ f2 f2_both(float x) { return f2_of(x, x); }
 // of ex2.approx, measured over exponents of -2^-16 .. -1, is -5e-9 .. -2.7e-8 of the
 // value, and its rounding 3e-8.  With this added to the exponent, which the product
 // takes along for nothing, it is within 1.3e-8 of zero (dA of 65 thousand tokens:
-// 1.2e-6 off, then 7.1e-7).  Steps of zero still give exactly 1.
+// 1.2e-6 off, then 7.8e-7).  Steps of zero still give exactly 1.
 constexpr float kDecayBias = 2e-8f;
 __device__ __forceinline__ float decay_of(float delta, float a2) { return exp2_of(fmaf(delta, a2, kDecayBias)); }
 __device__ __forceinline__ f2 f2_decay(f2 delta, f2 a2) { return f2_exp2(f2_fma(delta, a2, f2_both(kDecayBias))); }

@@ -17,6 +17,9 @@ namespace scan {
 namespace {
 
 constexpr int kBack = kSave;      // tokens of a tile: their p is in shared memory
+// Tokens whose terms of dA are summed in registers, before they join the segment's sum
+// in memory: one running sum over a segment of thousands rounds every term to its own size.
+constexpr int kSum = 128;
 
 template <int LS, int CPT>
 struct GradShared {
@@ -308,6 +311,19 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
         const int e = find_episode(a.ends, 0, a.episodes, tokens, t);
         if (e < a.episodes) load_states<LS, CPT>(h, a.init + e * row_states, n, p.ch, p.count, p.n0);
     };
+    float* const da_at = a.da + (int64_t)blockIdx.x * row_states;
+    bool summed = false;
+    auto sum_da = [&] {      // between tiles, where h is free
+        if (summed) {
+            load_states<LS, CPT>(h, da_at, n, p.ch, p.count, p.n0);
+#pragma unroll
+            for (int q = 0; q < L::kPairs; ++q) da[q] = f2_add(da[q], h[q]);
+        }
+        store_states<LS, CPT>(da_at, da, n, p.ch, p.count, p.n0);
+#pragma unroll
+        for (int q = 0; q < L::kPairs; ++q) da[q] = zero;
+        summed = true;
+    };
     const int last = s0 + (end - 1 - s0) / kBack * kBack;
     TileHeld<T, L::CB, kBack, true> rows_in(a, b, last);
     StatesHeld<T, LS, CPT, kBack> bs, cs;
@@ -480,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, grad_ctas<LS, CPT>()) scan_grad_kern
                 out[3] = from_float<T>(v.w);
             }
         });
+        if (t0 > s0 && (t0 - s0) % kSum == 0) sum_da();
         __syncthreads();
     }
-
-    store_states<LS, CPT>(a.da + (int64_t)blockIdx.x * row_states, da, n, p.ch, p.count, p.n0);
+    sum_da();
     // dD and ddt_bias over the threads of a column
     float(*red)[2][L::CB] = reinterpret_cast<float(*)[2][L::CB]>(&s.delta[0][0]);
     using S = GradShared<LS, CPT>;

@@ -115,3 +115,38 @@ def test_norms():
         assert (dw - small).norm() <= 1e-5 * small.norm()
         assert all((a[:rows - tail] == 0).all() for a in whole)
         del whole, part
+
+
+def test_a_gradient_summed_over_long_segments():
+    """dA of terms of one sign, over segments of up to 4096 tokens and 32768 in all.  With decays of about one half, a
+    mean error of 5e-8 each makes the two factors of a term 1.0e-7 + 0.5e-7 and 1.0e-7 off.  Running sums of 128 terms
+    round by 2.5e-8 of themselves a step, sqrt(128 / 3) times that in all: 1.6e-7; of the 32 sums of a segment and of
+    the segments, 0.8e-7 and less.  The steps and A log2 e are rounded once, 3e-8 each, of no sign."""
+    import numpy as np
+
+    import offline_rl_step_gb300 as ofrl
+    _room(20)
+    t, c, n, few = 32768, 4864, 16, 64
+    rng = np.random.default_rng(0)
+    A = (-np.log(2) * rng.uniform(0.8, 1.2, (c, n))).astype(np.float32)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    dt = torch.rand(t, c, device="cuda", generator=gen) * 0.4 + 0.8
+    x, b, a = torch.ones(t, c, device="cuda"), torch.ones(t, 1, n, device="cuda"), torch.from_numpy(A).cuda()
+    ctx = ofrl.SelectiveScan(c, n, 1, "fp32", False, t, 1)
+    saved, out, dx, ddt = ctx.saved(t), torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    da, db, dc = torch.empty_like(a), torch.empty_like(b), torch.empty_like(b)
+    ends = torch.tensor([t], dtype=torch.int32, device="cuda")
+    ofrl.scan_forward(ctx, x, dt, a, b, b, ends, out, saved=saved)
+    ofrl.scan_backward(ctx, x, dt, a, b, b, ends, saved, x, dx, ddt, da, db, dc)
+    got, steps, A = da[:few].double().cpu().numpy(), dt[:, :few].double().cpu().numpy(), A[:few].astype(np.float64)
+    h, lam, want = np.zeros((few, n)), np.zeros((few, n)), np.zeros((few, n))
+    past = np.empty((t, few, n))
+    for i in range(t):
+        past[i] = h
+        h = np.exp(steps[i, :, None] * A) * h + steps[i, :, None]
+    for i in range(t - 1, -1, -1):
+        lam += 1
+        decay = np.exp(steps[i, :, None] * A)
+        want += steps[i, :, None] * lam * decay * past[i]
+        lam *= decay
+    assert np.linalg.norm(got - want) <= 6e-7 * np.linalg.norm(want)
