@@ -25,25 +25,56 @@ int per_sm_of(bool backward, int cpt) { return !backward ? 4 : cpt == 4 ? 2 : 3;
 
 }  // namespace
 
+// The cut of a call.  All in us, tokens in bf16 with a gate unless said otherwise.
+//
+// 1. Whole episodes to a segment, since those have no tails, where their number
+//    divides the tokens (the host does not know their lengths) and there is a CTA for
+//    every SM: 64 episodes of 256, 512 channels of 16 states read 64 (even shares 88),
+//    256 of 64 118 (156), 1024 of 8 76 (105); 100 of 160, 256 of 16, trained 167 (186).
+//    But a whole episode is longer than an even share, and fewer CTAs hide less
+//    latency: 32 of 512, 256 of 64, read 221 (156); gradients of 1024 channels of 8
+//    states for them 379 (275); so there are limits on how much longer.
+// 2. Even shares in the wide form (a token's deltas and inputs are read by fewer
+//    threads, its B and C serve more channels), where its CTAs fill half
+//    (gradients: three quarters) of the GPU: 16384 tokens of 512 channels of 16 states
+//    read 88 (narrow 111 to 116), trained 331 (358).
+// 3. Even shares in the narrow one: 8 episodes of 128 to 384, 128 channels of 16
+//    states, read 17 (wide 25), trained 58 (79).
 Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_sms, bool backward) {
     Cut c;
     c.ls = lanes_of(s.state_dim);
-    const int64_t mean = round_up(div_up(tokens, episodes > 0 ? episodes : 1), kTile);
-    const int narrow = narrow_of(c.ls, backward);
-    for (int cpt = wide_of(c.ls);; cpt = narrow) {
+    // of episodes that may all be that long, in whole tiles
+    const int64_t mean = episodes > 0 && tokens % episodes == 0 && tokens / episodes % kTile == 0 ? tokens / episodes : 0;
+    const int wide = wide_of(c.ls), narrow = narrow_of(c.ls, backward);
+    // an even share of the tokens for each CTA that the GPU holds
+    auto share = [&](int cpt) {
         c.cpt = cpt;
         c.blocks = blocks_of(s, c.ls, cpt);
-        int64_t seg = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward, cpt))), kTile);
-        seg = seg < kMinSegment ? kMinSegment : seg > kMaxSegment ? kMaxSegment : seg;
-        // whole episodes of equal lengths have no tails
-        const bool whole = mean > seg && mean <= 4 * seg && mean <= kMaxSegment &&
-                           (int64_t)c.blocks * div_up(tokens, mean) >= num_sms;
-        if (whole) seg = mean;
+        const int64_t seg = round_up(div_up(tokens, wanted(c.blocks, num_sms, per_sm_of(backward, cpt))), kTile);
+        c.seg = (int)(seg < kMinSegment ? kMinSegment : seg > kMaxSegment ? kMaxSegment : seg);
+    };
+    auto cut = [&](int64_t seg) {
         c.seg = (int)seg;
         const int64_t n = div_up(tokens, seg);
         c.n_seg = (int)(n > 1 ? n : 1);
-        if (cpt == narrow || whole || 2 * (int64_t)c.blocks * c.n_seg >= (backward ? 3 : 4) * num_sms) return c;
+    };
+    for (int cpt = wide;; cpt = narrow) {
+        share(cpt);
+        const int64_t most = backward ? 5 * (int64_t)c.seg / 4 : cpt == wide && c.ls < 16 ? 5 * (int64_t)c.seg / 2
+                                                                                           : 3 * (int64_t)c.seg / 2;
+        if (mean > c.seg && mean <= most && mean <= kMaxSegment && (int64_t)c.blocks * div_up(tokens, mean) >= num_sms) {
+            cut(mean);
+            return c;
+        }
+        if (cpt == narrow) break;
     }
+    share(wide);
+    cut(c.seg);
+    if (wide != narrow && 2 * (int64_t)c.blocks * c.n_seg < (backward ? 3 : 4) * num_sms) {
+        share(narrow);
+        cut(c.seg);
+    }
+    return c;
 }
 
 Work work_of(const ofrl_scan_shape& s, int64_t tokens, const Cut& c, bool backward) {
