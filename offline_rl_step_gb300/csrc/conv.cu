@@ -8,7 +8,10 @@
 // the last W - 1 inputs in registers, so each input is read once but for the
 // W - 1 tokens before a run (and, for gradients, after it).  Which tokens begin
 // an episode is a bit mask in shared memory, made from the ends once a CTA.
-// Bound by HBM.
+// Bound by HBM in bytes; 65536 tokens of 1024 bf16 channels, four taps, silu:
+// forward 51 us, 5.3 TB/s (the special functions' pipe 30% busy, issue 40%),
+// gradients 88 us, 4.6 TB/s (issue 53%: two CTAs an SM, which their registers
+// allow, and instructions that wait for each other), their join 4 us.
 
 #include <cstring>
 #include <new>
@@ -223,6 +226,8 @@ struct Taps {
 
 // A run's inputs come through a ring in shared memory of which every thread has
 // its own column: kRound tokens a group, kDepth groups on their way, no barrier.
+// (The first inputs asked for after the marks, and several waves of CTAs: trained
+// 196 us against 148.)
 constexpr int kRound = 4, kDepth = 3;
 template <typename T, int V, int N>
 struct Ring {
