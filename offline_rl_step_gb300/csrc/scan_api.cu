@@ -40,12 +40,18 @@ int per_sm_of(bool backward, int cpt) { return !backward ? 4 : cpt == 4 ? 2 : 3;
 //    read 88 (narrow 111 to 116), trained 331 (358).
 // 3. Even shares in the narrow one: 8 episodes of 128 to 384, 128 channels of 16
 //    states, read 17 (wide 25), trained 58 (79).
+// Only the narrow form where the wide one leaves a quarter more threads without a
+// channel: 228 episodes of 64 to 512, 144 channels of 16 states, read 124 (wide 154),
+// trained 486 (604); two groups of 72, read 143 (155).
 Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_sms, bool backward) {
     Cut c;
     c.ls = lanes_of(s.state_dim);
     // of episodes that may all be that long, in whole tiles
     const int64_t mean = episodes > 0 && tokens % episodes == 0 && tokens / episodes % kTile == 0 ? tokens / episodes : 0;
-    const int wide = wide_of(c.ls), narrow = narrow_of(c.ls, backward);
+    const int narrow = narrow_of(c.ls, backward);
+    // channels that the CTAs have threads for
+    auto padded = [&](int cpt) { return blocks_of(s, c.ls, cpt) * block_of(c.ls, cpt); };
+    const int wide = 5 * (int64_t)padded(narrow) <= 4 * (int64_t)padded(wide_of(c.ls)) ? narrow : wide_of(c.ls);
     // an even share of the tokens for each CTA that the GPU holds
     auto share = [&](int cpt) {
         c.cpt = cpt;
