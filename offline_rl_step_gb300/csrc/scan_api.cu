@@ -64,21 +64,25 @@ Cut cut_of(const ofrl_scan_shape& s, int64_t tokens, int64_t episodes, int num_s
         const int64_t n = div_up(tokens, seg);
         c.n_seg = (int)(n > 1 ? n : 1);
     };
-    for (int cpt = wide;; cpt = narrow) {
-        share(cpt);
-        const int64_t most = backward ? 5 * (int64_t)c.seg / 4 : cpt == wide && c.ls < 16 ? 5 * (int64_t)c.seg / 2
-                                                                                           : 3 * (int64_t)c.seg / 2;
-        if (mean > c.seg && mean <= most && mean <= kMaxSegment && (int64_t)c.blocks * div_up(tokens, mean) >= num_sms) {
-            cut(mean);
-            return c;
-        }
-        if (cpt == narrow) break;
-    }
+    // cut to whole episodes, of at most that many quarters of an even share, if there is a CTA for every SM
+    auto whole = [&](int quarters) {
+        if (mean <= c.seg || 4 * mean > (int64_t)quarters * c.seg || mean > kMaxSegment ||
+            (int64_t)c.blocks * div_up(tokens, mean) < num_sms)
+            return false;
+        cut(mean);
+        return true;
+    };
+    const int most = backward ? 5 : c.ls == 16 ? 6 : 10;
+    share(wide);
+    if (whole(most)) return c;
+    // before even shares of the wide form: 64 of 256, 256 channels of 16 states, read 48 (63)
+    share(narrow);
+    if (whole(backward ? 5 : 6)) return c;
     share(wide);
     cut(c.seg);
     if (wide != narrow && 2 * (int64_t)c.blocks * c.n_seg < (backward ? 3 : 4) * num_sms) {
         share(narrow);
-        cut(c.seg);
+        if (!whole(most)) cut(c.seg);      // 64 of 256, 128 channels of 16 states, read 36 (39), trained 114 (117)
     }
     return c;
 }
