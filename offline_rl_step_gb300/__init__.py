@@ -826,11 +826,46 @@ def _open_ctx(ctx, kind):
     return ctx.handle
 
 
-def _same_device(ctx, *tensors):
-    """Raise for a tensor that is on another device than the workspace: a kernel would follow its address there."""
-    for t in tensors:
-        if t is not None and t.get_device() != ctx.device:
-            raise ValueError(f"every tensor must be on cuda:{ctx.device}, where the {type(ctx).__name__} is")
+def _refuse_at(t, dtype, shape, name, device):
+    """Raise unless this is a CUDA tensor of this type and shape on the workspace's device: a kernel would follow its
+    address there."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        _refuse(t, dtype, shape, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, where the workspace is, got {t.device}")
+
+
+def _rows3_at(t, dtype, shape, name, device):
+    """Address and row stride (elements) of a tensor [tokens, groups, states] on this device whose rows are dense."""
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse_at(t, dtype, shape, name, device)
+    s0, s1, s2 = t.stride()
+    n, h, d = shape
+    if n and (s2 != 1 and d > 1 or s1 != d and h > 1):
+        raise ValueError(f"{name} must have dense rows (groups and states contiguous within a token)")
+    return t.data_ptr(), s0 if n > 1 else h * d
+
+
+def _rows2_at(t, dtype, shape, name, device):
+    """Address and row stride (elements) of a tensor [tokens, channels] on this device whose rows are dense."""
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse_at(t, dtype, shape, name, device)
+    s0, s1 = t.stride()
+    n, h = shape
+    if n and s1 != 1 and h > 1:
+        raise ValueError(f"{name} must have dense rows (channels contiguous within a token)")
+    return t.data_ptr(), s0 if n > 1 else h
+
+
+def _dense_at(t, dtype, shape, name, device):
+    """Address of a contiguous tensor of this shape on this device (0 for None)."""
+    if t is None:
+        return 0
+    if type(t) is not _TENSOR or t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse_at(t, dtype, shape, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _tokens_of(x, channels: int, dtype, name: str) -> int:
@@ -849,11 +884,12 @@ _pack_residual_rows = struct.Struct(_abi.RESIDUAL_ROWS_FMT).pack
 
 def _conv_tokens(ctx: CausalConv, x, weight, bias):
     """The packed ofrl_conv_tokens and the shape of x."""
+    dev = ctx.device
     d = ctx.channels
     rows = (_tokens_of(x, d, ctx.dtype, "x"), d)
-    x, xs = _rows2(x, ctx.dtype, rows, "x")
-    return _pack_conv_tokens(x, _dense(weight, F32, (d, ctx.width), "weight"), _dense(bias, F32, (d,), "bias"), xs,
-                             rows[0]), rows
+    x, xs = _rows2_at(x, ctx.dtype, rows, "x", dev)
+    w = _dense_at(weight, F32, (d, ctx.width), "weight", dev)
+    return _pack_conv_tokens(x, w, _dense_at(bias, F32, (d,), "bias", dev), xs, rows[0]), rows
 
 
 def conv_forward(ctx: CausalConv, x, weight, episode_ends, out, bias=None, init_state=None, final_state=None, stream=None):
@@ -862,14 +898,15 @@ def conv_forward(ctx: CausalConv, x, weight, episode_ends, out, bias=None, init_
     episode_ends int32 [episodes].  init_state, final_state: [episodes, channels, width - 1] of x's type, the inputs
     before an episode and its last ones (two buffers)."""
     handle = _open_ctx(ctx, CausalConv)
+    dev = ctx.device
     t, rows = _conv_tokens(ctx, x, weight, bias)
     ne = episode_ends.numel()
     state = (ne, ctx.channels, ctx.width - 1)
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    init, final = _dense(init_state, ctx.dtype, state, "init_state"), _dense(final_state, ctx.dtype, state, "final_state")
-    ends = _dense(episode_ends, I32, (ne,), "episode_ends")
-    _same_device(ctx, x, weight, bias, episode_ends, out, init_state, final_state)
-    code = ctx._lib.ofrl_conv_forward(handle, t, ends, ne, init, o, os, final, _raw_stream(stream, ctx.device))
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    init = _dense_at(init_state, ctx.dtype, state, "init_state", dev)
+    final = _dense_at(final_state, ctx.dtype, state, "final_state", dev)
+    ends = _dense_at(episode_ends, I32, (ne,), "episode_ends", dev)
+    code = ctx._lib.ofrl_conv_forward(handle, t, ends, ne, init, o, os, final, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_conv_forward", code)
 
@@ -879,29 +916,31 @@ def conv_backward(ctx: CausalConv, x, weight, episode_ends, dout, dx, dweight, b
     """Gradients of the conv_forward call with the same inputs: of out in dout, of final_state in d_final (of x's type;
     None: zero); written to dx, dweight, dbias and d_init (float32; the last two may be None)."""
     handle = _open_ctx(ctx, CausalConv)
+    dev = ctx.device
     t, rows = _conv_tokens(ctx, x, weight, bias)
     ne, d = episode_ends.numel(), ctx.channels
     state = (ne, d, ctx.width - 1)
-    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
+    g, gs = _rows2_at(dout, ctx.dtype, rows, "dout", dev)
+    dxp, xs = _rows2_at(dx, ctx.dtype, rows, "dx", dev)
     if dweight is None:
         raise TypeError("dweight must be a CUDA tensor")
-    init, dfin = _dense(init_state, ctx.dtype, state, "init_state"), _dense(d_final, ctx.dtype, state, "d_final")
-    dini, ends = _dense(d_init, F32, state, "d_init"), _dense(episode_ends, I32, (ne,), "episode_ends")
-    grads = _pack_conv_grads(dxp, _dense(dweight, F32, (d, ctx.width), "dweight"), _dense(dbias, F32, (d,), "dbias"), xs)
-    _same_device(ctx, x, weight, bias, episode_ends, dout, dx, dweight, dbias, init_state, d_final, d_init)
-    code = ctx._lib.ofrl_conv_backward(handle, t, ends, ne, init, g, gs, dfin, grads, dini, _raw_stream(stream, ctx.device))
+    init = _dense_at(init_state, ctx.dtype, state, "init_state", dev)
+    dfin = _dense_at(d_final, ctx.dtype, state, "d_final", dev)
+    dini, ends = _dense_at(d_init, F32, state, "d_init", dev), _dense_at(episode_ends, I32, (ne,), "episode_ends", dev)
+    dw = _dense_at(dweight, F32, (d, ctx.width), "dweight", dev)
+    grads = _pack_conv_grads(dxp, dw, _dense_at(dbias, F32, (d,), "dbias", dev), xs)
+    code = ctx._lib.ofrl_conv_backward(handle, t, ends, ne, init, g, gs, dfin, grads, dini, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_conv_backward", code)
 
 
-def _state_pair(state, new_state, dtype, tail):
+def _state_pair(state, new_state, dtype, tail, dev):
     """Addresses of a step's states and how many slots they have."""
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         _refuse(state, dtype, ("slots", *tail), "state")
     shape = (state.shape[0], *tail)
-    at = _dense(state, dtype, shape, "state")
-    return at, at if new_state is None else _dense(new_state, dtype, shape, "new_state"), shape[0]
+    at = _dense_at(state, dtype, shape, "state", dev)
+    return at, at if new_state is None else _dense_at(new_state, dtype, shape, "new_state", dev), shape[0]
 
 
 def conv_step(ctx: CausalConv, x, weight, state, out, bias=None, new_state=None, slots=None, stream=None):
@@ -909,30 +948,31 @@ def conv_step(ctx: CausalConv, x, weight, state, out, bias=None, new_state=None,
     width - 1], updated in place or written to new_state; slots: int32 [tokens], the state of each token (None: token
     i has state i)."""
     handle = _open_ctx(ctx, CausalConv)
+    dev = ctx.device
     t, rows = _conv_tokens(ctx, x, weight, bias)
-    at, to, ns = _state_pair(state, new_state, ctx.dtype, (ctx.channels, ctx.width - 1))
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    slot_idx = _dense(slots, I32, (rows[0],), "slots")
-    _same_device(ctx, x, weight, bias, state, new_state, slots, out)
-    code = ctx._lib.ofrl_conv_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, ctx.device))
+    at, to, ns = _state_pair(state, new_state, ctx.dtype, (ctx.channels, ctx.width - 1), dev)
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    slot_idx = _dense_at(slots, I32, (rows[0],), "slots", dev)
+    code = ctx._lib.ofrl_conv_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_conv_step", code)
 
 
 def _scan_tokens(ctx: SelectiveScan, x, dt, A, B, C_, D, z, dt_bias):
     """The packed ofrl_scan_tokens and the shapes of x and of B."""
+    dev = ctx.device
     d, n, ty = ctx.channels, ctx.state_dim, ctx.dtype
     rows = (_tokens_of(x, d, ty, "x"), d)
     bc = (rows[0], ctx.groups, n)
-    x, xs = _rows2(x, ty, rows, "x")
-    dt, ds = _rows2(dt, ty, rows, "dt")
-    B, bs = _rows3(B, ty, bc, "B")
-    C_, cs = _rows3(C_, ty, bc, "C")
-    z, zs = (0, 0) if z is None else _rows2(z, ty, rows, "z")
+    x, xs = _rows2_at(x, ty, rows, "x", dev)
+    dt, ds = _rows2_at(dt, ty, rows, "dt", dev)
+    B, bs = _rows3_at(B, ty, bc, "B", dev)
+    C_, cs = _rows3_at(C_, ty, bc, "C", dev)
+    z, zs = (0, 0) if z is None else _rows2_at(z, ty, rows, "z", dev)
     if A is None:
         raise TypeError("A must be a CUDA tensor")
-    return _pack_scan_tokens(x, dt, B, C_, z, _dense(A, F32, (d, n), "A"), _dense(D, F32, (d,), "D"),
-                             _dense(dt_bias, F32, (d,), "dt_bias"), xs, ds, bs, cs, zs, rows[0]), rows, bc
+    return _pack_scan_tokens(x, dt, B, C_, z, _dense_at(A, F32, (d, n), "A", dev), _dense_at(D, F32, (d,), "D", dev),
+                             _dense_at(dt_bias, F32, (d,), "dt_bias", dev), xs, ds, bs, cs, zs, rows[0]), rows, bc
 
 
 def _scan_saved(ctx: SelectiveScan, saved, tokens: int):
@@ -941,7 +981,7 @@ def _scan_saved(ctx: SelectiveScan, saved, tokens: int):
     need = ctx._lib.ofrl_scan_saved_bytes(C.byref(ctx.shape), tokens)
     if saved.numel() < need:
         raise ValueError(f"saved has {saved.numel()} bytes, {need} are needed: use ctx.saved(tokens)")
-    return _dense(saved, torch.uint8, saved.shape, "saved")
+    return _dense_at(saved, torch.uint8, saved.shape, "saved", ctx.device)
 
 
 def scan_forward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, out, D=None, z=None, dt_bias=None, init_state=None,
@@ -951,14 +991,15 @@ def scan_forward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, out, D=None, 
     episode_ends int32 [episodes].  init_state, final_state: float32 [episodes, channels, state_dim] (two buffers).
     saved: ctx.saved(tokens), filled for scan_backward."""
     handle = _open_ctx(ctx, SelectiveScan)
+    dev = ctx.device
     t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
     ne = episode_ends.numel()
     state = (ne, ctx.channels, ctx.state_dim)
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    init, final = _dense(init_state, F32, state, "init_state"), _dense(final_state, F32, state, "final_state")
-    ends, kept = _dense(episode_ends, I32, (ne,), "episode_ends"), _scan_saved(ctx, saved, rows[0])
-    _same_device(ctx, x, dt, A, B, C, episode_ends, out, D, z, dt_bias, init_state, final_state, saved)
-    code = ctx._lib.ofrl_scan_forward(handle, t, ends, ne, init, o, os, final, kept, _raw_stream(stream, ctx.device))
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    init = _dense_at(init_state, F32, state, "init_state", dev)
+    final = _dense_at(final_state, F32, state, "final_state", dev)
+    ends, kept = _dense_at(episode_ends, I32, (ne,), "episode_ends", dev), _scan_saved(ctx, saved, rows[0])
+    code = ctx._lib.ofrl_scan_forward(handle, t, ends, ne, init, o, os, final, kept, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_scan_forward", code)
 
@@ -969,6 +1010,7 @@ def scan_backward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, saved, dout,
     d_final (None: zero); written to dx, ddt, dB, dC, dz (given where z is; slices with dense rows), and to dA, dD,
     ddt_bias and d_init (float32; the last three may be None)."""
     handle = _open_ctx(ctx, SelectiveScan)
+    dev = ctx.device
     t, rows, bc = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
     if saved is None:
         raise TypeError("saved must be the buffer that scan_forward filled")
@@ -976,21 +1018,20 @@ def scan_backward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, saved, dout,
         raise TypeError("dA must be a CUDA tensor")
     ne, d, ty = episode_ends.numel(), ctx.channels, ctx.dtype
     state = (ne, d, ctx.state_dim)
-    g, gs = _rows2(dout, ty, rows, "dout")
-    dxp, xs = _rows2(dx, ty, rows, "dx")
-    ddtp, ds = _rows2(ddt, ty, rows, "ddt")
-    dBp, bs = _rows3(dB, ty, bc, "dB")
-    dCp, cs = _rows3(dC, ty, bc, "dC")
-    dzp, zs = (0, 0) if dz is None else _rows2(dz, ty, rows, "dz")
-    init, dfin = _dense(init_state, F32, state, "init_state"), _dense(d_final, F32, state, "d_final")
-    dini, ends = _dense(d_init, F32, state, "d_init"), _dense(episode_ends, I32, (ne,), "episode_ends")
+    g, gs = _rows2_at(dout, ty, rows, "dout", dev)
+    dxp, xs = _rows2_at(dx, ty, rows, "dx", dev)
+    ddtp, ds = _rows2_at(ddt, ty, rows, "ddt", dev)
+    dBp, bs = _rows3_at(dB, ty, bc, "dB", dev)
+    dCp, cs = _rows3_at(dC, ty, bc, "dC", dev)
+    dzp, zs = (0, 0) if dz is None else _rows2_at(dz, ty, rows, "dz", dev)
+    init, dfin = _dense_at(init_state, F32, state, "init_state", dev), _dense_at(d_final, F32, state, "d_final", dev)
+    dini, ends = _dense_at(d_init, F32, state, "d_init", dev), _dense_at(episode_ends, I32, (ne,), "episode_ends", dev)
     kept = _scan_saved(ctx, saved, rows[0])
-    grads = _pack_scan_grads(dxp, ddtp, dBp, dCp, dzp, _dense(dA, F32, (d, ctx.state_dim), "dA"), _dense(dD, F32, (d,), "dD"),
-                             _dense(ddt_bias, F32, (d,), "ddt_bias"), xs, ds, bs, cs, zs)
-    _same_device(ctx, x, dt, A, B, C, episode_ends, saved, dout, dx, ddt, dA, dB, dC, D, z, dt_bias, dD, dz, ddt_bias,
-                 init_state, d_final, d_init)
+    dAp, dDp = _dense_at(dA, F32, (d, ctx.state_dim), "dA", dev), _dense_at(dD, F32, (d,), "dD", dev)
+    grads = _pack_scan_grads(dxp, ddtp, dBp, dCp, dzp, dAp, dDp, _dense_at(ddt_bias, F32, (d,), "ddt_bias", dev), xs, ds, bs,
+                             cs, zs)
     code = ctx._lib.ofrl_scan_backward(handle, t, ends, ne, init, kept, g, gs, dfin, grads, dini,
-                                       _raw_stream(stream, ctx.device))
+                                       _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_scan_backward", code)
 
@@ -1001,12 +1042,12 @@ def scan_step(ctx: SelectiveScan, x, dt, A, B, C, state, out, D=None, z=None, dt
     channels, state_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each token
     (None: token i has state i)."""
     handle = _open_ctx(ctx, SelectiveScan)
+    dev = ctx.device
     t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)
-    at, to, ns = _state_pair(state, new_state, F32, (ctx.channels, ctx.state_dim))
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    slot_idx = _dense(slots, I32, (rows[0],), "slots")
-    _same_device(ctx, x, dt, A, B, C, state, new_state, slots, out, D, z, dt_bias)
-    code = ctx._lib.ofrl_scan_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, ctx.device))
+    at, to, ns = _state_pair(state, new_state, F32, (ctx.channels, ctx.state_dim), dev)
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    slot_idx = _dense_at(slots, I32, (rows[0],), "slots", dev)
+    code = ctx._lib.ofrl_scan_step(handle, t, slot_idx, ns, at, to, o, os, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_scan_step", code)
 
@@ -1014,13 +1055,14 @@ def scan_step(ctx: SelectiveScan, x, dt, A, B, C, state, out, D=None, z=None, dt
 def _norm_weight(ctx: BlockNorm, weight, name="weight"):
     if weight is None:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return _dense(weight, F32, (ctx.channels,), name)
+    return _dense_at(weight, F32, (ctx.channels,), name, ctx.device)
 
 
 def _gated_rows(ctx: BlockNorm, x, z, weight, eps, gate_first):
+    dev = ctx.device
     rows = (_tokens_of(x, ctx.channels, ctx.dtype, "x"), ctx.channels)
-    x, xs = _rows2(x, ctx.dtype, rows, "x")
-    z, zs = _rows2(z, ctx.dtype, rows, "z")
+    x, xs = _rows2_at(x, ctx.dtype, rows, "x", dev)
+    z, zs = _rows2_at(z, ctx.dtype, rows, "z", dev)
     return _pack_gated_rows(x, z, _norm_weight(ctx, weight), xs, zs, rows[0], eps, bool(gate_first)), rows
 
 
@@ -1028,10 +1070,10 @@ def gated_norm(ctx: BlockNorm, x, z, weight, out, eps: float = 1e-5, gate_first:
     """out = weight x / rms(x) silu(z), or the norm of x silu(z) (gate_first), over each group of channels: x, z, out
     [rows, channels] (may be slices with dense rows; out may be x), weight float32 [channels]."""
     handle = _open_ctx(ctx, BlockNorm)
+    dev = ctx.device
     t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    _same_device(ctx, x, z, weight, out)
-    code = ctx._lib.ofrl_gated_norm(handle, t, o, os, _raw_stream(stream, ctx.device))
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    code = ctx._lib.ofrl_gated_norm(handle, t, o, os, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_gated_norm", code)
 
@@ -1040,23 +1082,24 @@ def gated_norm_backward(ctx: BlockNorm, x, z, weight, dout, dx, dz, dweight, eps
                         stream=None):
     """Gradients of the gated_norm call with the same inputs, written to dx, dz (slices with dense rows) and dweight."""
     handle = _open_ctx(ctx, BlockNorm)
+    dev = ctx.device
     t, rows = _gated_rows(ctx, x, z, weight, eps, gate_first)
-    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
-    dzp, zs = _rows2(dz, ctx.dtype, rows, "dz")
+    g, gs = _rows2_at(dout, ctx.dtype, rows, "dout", dev)
+    dxp, xs = _rows2_at(dx, ctx.dtype, rows, "dx", dev)
+    dzp, zs = _rows2_at(dz, ctx.dtype, rows, "dz", dev)
     dw = _norm_weight(ctx, dweight, "dweight")
-    _same_device(ctx, x, z, weight, dout, dx, dz, dweight)
-    code = ctx._lib.ofrl_gated_norm_backward(handle, t, g, gs, dxp, xs, dzp, zs, dw, _raw_stream(stream, ctx.device))
+    code = ctx._lib.ofrl_gated_norm_backward(handle, t, g, gs, dxp, xs, dzp, zs, dw, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_gated_norm_backward", code)
 
 
 def _residual_rows(ctx: BlockNorm, x, residual, scale, weight, eps):
+    dev = ctx.device
     rows = (_tokens_of(x, ctx.channels, ctx.dtype, "x"), ctx.channels)
-    x, xs = _rows2(x, ctx.dtype, rows, "x")
-    residual, rs = _rows2(residual, ctx.residual_dtype, rows, "residual")
-    return _pack_residual_rows(x, residual, _dense(scale, F32, (ctx.channels,), "scale"), _norm_weight(ctx, weight), xs, rs,
-                               rows[0], eps), rows
+    x, xs = _rows2_at(x, ctx.dtype, rows, "x", dev)
+    residual, rs = _rows2_at(residual, ctx.residual_dtype, rows, "residual", dev)
+    scale = _dense_at(scale, F32, (ctx.channels,), "scale", dev)
+    return _pack_residual_rows(x, residual, scale, _norm_weight(ctx, weight), xs, rs, rows[0], eps), rows
 
 
 def residual_norm(ctx: BlockNorm, x, residual, weight, residual_out, out, scale=None, eps: float = 1e-5, stream=None):
@@ -1064,11 +1107,11 @@ def residual_norm(ctx: BlockNorm, x, residual, weight, residual_out, out, scale=
     rounded to its type): x, out [rows, channels], residual, residual_out of the residual's type (all may be slices
     with dense rows; residual_out may be residual, out may be x), scale (None: one) and weight float32 [channels]."""
     handle = _open_ctx(ctx, BlockNorm)
+    dev = ctx.device
     t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
-    r, rs = _rows2(residual_out, ctx.residual_dtype, rows, "residual_out")
-    o, os = _rows2(out, ctx.dtype, rows, "out")
-    _same_device(ctx, x, residual, weight, residual_out, out, scale)
-    code = ctx._lib.ofrl_residual_norm(handle, t, r, rs, o, os, _raw_stream(stream, ctx.device))
+    r, rs = _rows2_at(residual_out, ctx.residual_dtype, rows, "residual_out", dev)
+    o, os = _rows2_at(out, ctx.dtype, rows, "out", dev)
+    code = ctx._lib.ofrl_residual_norm(handle, t, r, rs, o, os, _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_residual_norm", code)
 
@@ -1078,15 +1121,17 @@ def residual_norm_backward(ctx: BlockNorm, x, residual, weight, dout, dx, dresid
     """Gradients of the residual_norm call with the same inputs: of out in dout, of residual_out in d_residual_out
     (None: zero); written to dx, dresidual (slices with dense rows), dweight, and dscale (given where scale is)."""
     handle = _open_ctx(ctx, BlockNorm)
+    dev = ctx.device
     t, rows = _residual_rows(ctx, x, residual, scale, weight, eps)
-    g, gs = _rows2(dout, ctx.dtype, rows, "dout")
-    dxp, xs = _rows2(dx, ctx.dtype, rows, "dx")
-    dr, drs = _rows2(dresidual, ctx.residual_dtype, rows, "dresidual")
-    do, dos = (0, 0) if d_residual_out is None else _rows2(d_residual_out, ctx.residual_dtype, rows, "d_residual_out")
-    dw, dsc = _norm_weight(ctx, dweight, "dweight"), _dense(dscale, F32, (ctx.channels,), "dscale")
-    _same_device(ctx, x, residual, weight, dout, dx, dresidual, dweight, scale, dscale, d_residual_out)
+    g, gs = _rows2_at(dout, ctx.dtype, rows, "dout", dev)
+    dxp, xs = _rows2_at(dx, ctx.dtype, rows, "dx", dev)
+    dr, drs = _rows2_at(dresidual, ctx.residual_dtype, rows, "dresidual", dev)
+    do = dos = 0
+    if d_residual_out is not None:
+        do, dos = _rows2_at(d_residual_out, ctx.residual_dtype, rows, "d_residual_out", dev)
+    dw, dsc = _norm_weight(ctx, dweight, "dweight"), _dense_at(dscale, F32, (ctx.channels,), "dscale", dev)
     code = ctx._lib.ofrl_residual_norm_backward(handle, t, g, gs, do, dos, dxp, xs, dr, drs, dw, dsc,
-                                                _raw_stream(stream, ctx.device))
+                                                _raw_stream(stream, dev))
     if code != _abi.OK:
         _abi.check("ofrl_residual_norm_backward", code)
 
