@@ -227,8 +227,9 @@ struct Taps {
 // A run's inputs come through a ring in shared memory of which every thread has
 // its own column: kRound tokens a group, kDepth groups on their way, no barrier.
 // (The first inputs asked for after the marks, and several waves of CTAs: trained
-// 196 us against 148.)
-constexpr int kRound = 4, kDepth = 3;
+// 196 us against 148.  Three groups 146.5, four 147.5, two 144; two of eight tokens
+// 150; forward four channels a thread and three or four CTAs an SM 145.5 and 148.)
+constexpr int kRound = 4, kDepth = 2;
 template <typename T, int V, int N>
 struct Ring {
     Vec<T, V> slot[N][kDepth][kRound][kThreads];
