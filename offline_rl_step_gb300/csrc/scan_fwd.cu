@@ -161,9 +161,21 @@ __global__ void __launch_bounds__(kThreads, 4) scan_tail_kernel(const __grid_con
 // states 9 us, 152 of 512 10 (one thread for a state: 12 us more over 187 of 512).
 constexpr int kCarryWarps = 8, kAhead = 8;
 
-struct Joined {      // carry <- decay carry + own
-    float decay, own;
+struct Joined {      // carry <- 2^rate carry + own, or own alone
+    float rate, own;
+    bool open;
 };
+
+// Decays are kept as exponents until they meet a state.  A state that grows may have
+// one past fp32's range: then in three factors, so that a state of zero stays zero
+// (infinity times zero is no number); 2^378 takes any other state past the range.
+__device__ __forceinline__ float joined(float rate, float carry, float own) {
+    if (rate > 126.0f && rate < INFINITY) {
+        const float k = exp2_of(fminf(rate, 378.0f) * (1.0f / 3.0f));
+        return fmaf(carry * k * k, k, own);
+    }
+    return fmaf(exp2_of(rate), carry, own);
+}
 
 __global__ void __launch_bounds__(32 * kCarryWarps) scan_carry_kernel(const __grid_constant__ Launch a, int backward) {
     __shared__ Joined slices[kCarryWarps][32];
@@ -195,31 +207,29 @@ __global__ void __launch_bounds__(32 * kCarryWarps) scan_carry_kernel(const __gr
                 if (!on || from + k >= hi) break;
                 const int j = backward ? a.n_seg - 1 - (from + k) : from + k;
                 // selected, not multiplied: what an unused tail holds stays out
-                Joined x = {0.0f, 0.0f};
+                Joined x = {0.0f, 0.0f, kind[k] == kTailJoin};
                 if (kind[k] != kTailNone) x.own = tail[k];
-                if (kind[k] == kTailJoin) x.decay = exp2_of(a2 * sum[k]);
-                body(j, kind[k] == kTailJoin, x);
+                if (x.open) x.rate = a2 * sum[k];
+                body(j, x);
             }
         }
     };
-    Joined all = {1.0f, 0.0f};
-    bool open = true;      // what came before the slice still counts
-    over([&](int, bool joins, const Joined& x) {
-        all.own = joins ? fmaf(x.decay, all.own, x.own) : x.own;
-        all.decay = joins ? x.decay * all.decay : 0.0f;
-        open = open && joins;
+    Joined all = {0.0f, 0.0f, true};      // open: what came before the slice still counts
+    over([&](int, const Joined& x) {
+        all.own = x.open ? joined(x.rate, all.own, x.own) : x.own;
+        all.rate += x.rate;
+        all.open = all.open && x.open;
     });
-    if (!open) all.decay = -1.0f;      // a decay is never negative
     slices[slice][lane] = all;
     __syncthreads();
     float carry = 0.0f;
     for (int k = 0; k < slice; ++k) {
         const Joined x = slices[k][lane];
-        carry = x.decay < 0.0f ? x.own : fmaf(x.decay, carry, x.own);
+        carry = x.open ? joined(x.rate, carry, x.own) : x.own;
     }
-    over([&](int j, bool joins, const Joined& x) {
+    over([&](int j, const Joined& x) {
         a.tail[j * states + i] = carry;
-        carry = joins ? fmaf(x.decay, carry, x.own) : x.own;
+        carry = x.open ? joined(x.rate, carry, x.own) : x.own;
     });
 }
 
