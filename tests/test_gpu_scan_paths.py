@@ -26,3 +26,34 @@ def test_a_state_of_zero_stays_where_others_would_grow():
     got = _run(d, ln, "fp32", parts, states=False, softplus=False)
     assert all(np.isfinite(v).all() for v in got.values() if v is not None)
     _check(d, ln, "fp32", got, parts, states=False, softplus=False)
+
+
+@pytest.mark.parametrize("step", [0.001, 0.1])
+def test_steps_summed_over_long_segments(step):
+    """A segment of 4096 equal steps, whose sum S decays what comes before it by exp(A S) = 1 / e.  An addition rounds by
+    at most 2^-24 of its result: a tile's 16 steps by sum(k / 16) = 8.5 of that, the 256 tiles of a segment by
+    sum(k / 256) = 128.5, together 8.2e-6.  A S log2 e and the decay are rounded at 2^-23 and 2^-22, A and A log2 e at
+    2^-24 each: 5e-7.  In one running sum the steps are 6e-5 off."""
+    import offline_rl_step_gb300 as ofrl
+    need_gpu()
+    if torch.cuda.mem_get_info()[0] < 12 * 2 ** 30:
+        pytest.skip("needs 12 GB of free memory")
+    t, c, n, seg = 3 * 4096, 6528, 64, 4096      # channels enough that a segment is as long as one may be
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    dt = (step * 10 ** torch.rand(c, device="cuda", generator=gen)).expand(t, c).contiguous()
+    A = (-1.0 / (dt[0] * seg)).view(c, 1).expand(c, n).contiguous()
+    first, zero = torch.zeros(t, 1, n, device="cuda"), torch.zeros(t, c, device="cuda")
+    first[:, :, 0] = 1
+    ctx = ofrl.SelectiveScan(c, n, 1, "fp32", False, t, 2)
+    out, saved, init = torch.empty_like(zero), ctx.saved(t), torch.ones(2, c, n, device="cuda")
+    rate = A[:, 0].double() * dt[0].double()
+    # forward, from the last token of the first segment over the second one
+    ends = torch.tensor([seg - 1, t], dtype=torch.int32, device="cuda")
+    ofrl.scan_forward(ctx, zero, dt, A, first, first, ends, out, init_state=init)
+    assert (out[2 * seg] / torch.exp(rate * (seg + 2)) - 1).abs().max() <= 9e-6
+    # gradients, from the first token of the third segment back
+    ends = torch.tensor([2 * seg + 1, t], dtype=torch.int32, device="cuda")
+    ofrl.scan_forward(ctx, zero, dt, A, first, first, ends, out, saved=saved)
+    dx, ddt, dA, dB, dC = (torch.empty_like(v) for v in (zero, zero, A, first, first))
+    ofrl.scan_backward(ctx, zero, dt, A, first, first, ends, saved, zero, dx, ddt, dA, dB, dC, d_final=init)
+    assert (dx[seg - 1] / (dt[0] * torch.exp(rate * (seg + 1))) - 1).abs().max() <= 9e-6
