@@ -667,8 +667,8 @@ ofrl_status ofrl_conv_backward(ofrl_conv* ctx, const ofrl_conv_tokens* in, const
                                const void* d_final, const ofrl_conv_grads* grads, float* d_init, void* stream);
 
 /* One token for each of in->tokens environments: state_in, state_out [slots,
- * channels, width - 1] (the same buffer updates in place); slot_idx as
- * ofrl_delta_step's. */
+ * channels, width - 1] (the same buffer updates in place; buffers that overlap
+ * otherwise are refused); slot_idx as ofrl_delta_step's. */
 ofrl_status ofrl_conv_step(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int32_t* slot_idx, int32_t slots,
                            const void* state_in, void* state_out, void* out, int64_t out_stride, void* stream);
 
@@ -751,8 +751,8 @@ ofrl_status ofrl_scan_backward(ofrl_scan* ctx, const ofrl_scan_tokens* in, const
                                void* stream);
 
 /* One token for each of in->tokens environments: state_in, state_out fp32
- * [slots, channels, N], 16-byte aligned (the same buffer updates in place);
- * slot_idx as ofrl_delta_step's. */
+ * [slots, channels, N], 16-byte aligned (the same buffer updates in place;
+ * buffers that overlap otherwise are refused); slot_idx as ofrl_delta_step's. */
 ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int32_t* slot_idx, int32_t slots,
                            const float* state_in, float* state_out, void* out, int64_t out_stride, void* stream);
 

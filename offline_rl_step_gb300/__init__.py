@@ -945,8 +945,8 @@ def _state_pair(state, new_state, dtype, tail, dev):
 
 def conv_step(ctx: CausalConv, x, weight, state, out, bias=None, new_state=None, slots=None, stream=None):
     """One token for each environment: tensors as conv_forward's with tokens = environments; state [slots, channels,
-    width - 1], updated in place or written to new_state; slots: int32 [tokens], the state of each token (None: token
-    i has state i)."""
+    width - 1], updated in place or written to new_state (which shares no memory with it); slots: int32 [tokens], the
+    state of each token (None: token i has state i)."""
     handle = _open_ctx(ctx, CausalConv)
     dev = ctx.device
     t, rows = _conv_tokens(ctx, x, weight, bias)
@@ -1039,8 +1039,8 @@ def scan_backward(ctx: SelectiveScan, x, dt, A, B, C, episode_ends, saved, dout,
 def scan_step(ctx: SelectiveScan, x, dt, A, B, C, state, out, D=None, z=None, dt_bias=None, new_state=None, slots=None,
               stream=None):
     """One token for each environment: tensors as scan_forward's with tokens = environments; state float32 [slots,
-    channels, state_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each token
-    (None: token i has state i)."""
+    channels, state_dim], updated in place or written to new_state (which shares no memory with it); slots: int32
+    [tokens], the state of each token (None: token i has state i)."""
     handle = _open_ctx(ctx, SelectiveScan)
     dev = ctx.device
     t, rows, _ = _scan_tokens(ctx, x, dt, A, B, C, D, z, dt_bias)

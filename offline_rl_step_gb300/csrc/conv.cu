@@ -828,9 +828,12 @@ ofrl_status ofrl_conv_step(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int
     if (s != OFRL_OK) return s;
     if (slots < 0 || !aligned_to(slot_idx, 4) || (slot_idx == nullptr && slots < in->tokens)) return OFRL_EINVAL;
     if (in->tokens == 0) return OFRL_OK;
-    if (!rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
+    const int64_t e = dtype_size(ctx->shape.dtype);
+    if (!rows_ok(out, out_stride, ctx->shape.channels, e)) return OFRL_EINVAL;
     if (!aligned_to(state_in, 16) || !aligned_to(state_out, 16)) return OFRL_EINVAL;
     if (slots > 0 && (!state_in || !state_out)) return OFRL_EINVAL;
+    if (!step_states_ok(state_in, state_out, (int64_t)slots * ctx->shape.channels * (ctx->shape.width - 1) * e))
+        return OFRL_EINVAL;
     ConvStepLaunch a;
     std::memset(&a, 0, sizeof(a));
     a.shape = ctx->shape;
