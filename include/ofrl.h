@@ -559,7 +559,8 @@ int64_t ofrl_delta_saved_bytes(const ofrl_delta_shape* shape, int64_t tokens, in
 /* Forward over packed episodes.  episode_ends: device [num_episodes].
  * init_state: device fp32 [num_episodes, v_heads, v_dim, k_dim], 16-byte
  * aligned, or NULL (zero).  out: device [tokens, v_heads, v_dim], contiguous,
- * 16-byte aligned.  final_state: as init_state, or NULL; may be init_state.
+ * 16-byte aligned.  final_state: as init_state, or NULL; may be init_state
+ * (buffers that overlap otherwise are refused).
  * saved: device, ofrl_delta_saved_bytes, or NULL (no backward will follow). */
 ofrl_status ofrl_delta_forward(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* episode_ends,
                                int32_t num_episodes, const float* init_state, void* out, float* final_state,
@@ -567,16 +568,17 @@ ofrl_status ofrl_delta_forward(ofrl_delta* ctx, const ofrl_delta_tokens* in, con
 
 /* Backward of the forward call that filled `saved` with the same tokens and
  * ends: dout as `out`; d_final: gradient of final_state, fp32, or NULL (zero);
- * d_init: gradient of init_state, fp32, or NULL (not wanted); may be d_final. */
+ * d_init: gradient of init_state, fp32, or NULL (not wanted); may be d_final
+ * (buffers that overlap otherwise are refused). */
 ofrl_status ofrl_delta_backward(ofrl_delta* ctx, const ofrl_delta_tokens* in, const int32_t* episode_ends,
                                 int32_t num_episodes, const void* saved, const void* dout, const float* d_final,
                                 const ofrl_delta_grads* grads, float* d_init, void* stream);
 
 /* One token for each of in->tokens environments, each with a state of its
  * own: state_in, state_out device fp32 [slots, v_heads, v_dim, k_dim], 16-byte
- * aligned (the same buffer updates in place); slot_idx: device int32
- * [tokens], the state of each token, or NULL (token i has state i, slots >=
- * tokens).  Two tokens of one call must not name one slot.  A slot outside
+ * aligned (the same buffer updates in place; buffers that overlap otherwise
+ * are refused); slot_idx: device int32 [tokens], the state of each token, or
+ * NULL (token i has state i, slots >= tokens).  Two tokens of one call must not name one slot.  A slot outside
  * [0, slots) is counted in OFRL_STAT_BAD_INDEX: its token's output is zero
  * and no state is written.  With slot_idx, slots of state_out that no token
  * names are left as they are. */

@@ -697,8 +697,8 @@ def delta_backward(ctx: DeltaRule, q, k, v, g, beta, episode_ends, saved, dout, 
 
 def delta_step(ctx: DeltaRule, q, k, v, g, beta, state, out, scale=None, new_state=None, slots=None, stream=None):
     """One token for each environment: tensors as delta_forward's with tokens = environments; state float32 [slots,
-    v_heads, v_dim, k_dim], updated in place or written to new_state; slots: int32 [tokens], the state of each
-    token (None: token i has state i)."""
+    v_heads, v_dim, k_dim], updated in place or written to new_state (which shares no memory with it); slots: int32
+    [tokens], the state of each token (None: token i has state i)."""
     t, n, _, vv, _ = _delta_tokens(ctx, q, k, v, g, beta, scale)
     ns = state.shape[0]
     shape = (ns, ctx.v_heads, ctx.v_dim, ctx.k_dim)

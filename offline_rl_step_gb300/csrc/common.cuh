@@ -466,4 +466,17 @@ cudaError_t launch_policy(const float* q, const float* v, int batch, int num_act
                           float* pi_out, int32_t* argmax_out, int64_t net_stride_v,
                           int n_nets, cudaStream_t st);
 
+// Buffers of so many bytes that share memory (NULL shares none).
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    if (a == nullptr || b == nullptr) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+// States that a call reads and ones that it writes: one buffer, or two that share
+// nothing.  States that are shifted against each other would be written by one CTA
+// before another one has read them.
+inline bool same_or_apart(const void* in, const void* out, int64_t bytes) {
+    return in == out || !overlap(in, bytes, out, bytes);
+}
+
 }  // namespace ofrl

@@ -832,7 +832,7 @@ ofrl_status ofrl_conv_step(ofrl_conv* ctx, const ofrl_conv_tokens* in, const int
     if (!rows_ok(out, out_stride, ctx->shape.channels, e)) return OFRL_EINVAL;
     if (!aligned_to(state_in, 16) || !aligned_to(state_out, 16)) return OFRL_EINVAL;
     if (slots > 0 && (!state_in || !state_out)) return OFRL_EINVAL;
-    if (!step_states_ok(state_in, state_out, (int64_t)slots * ctx->shape.channels * (ctx->shape.width - 1) * e))
+    if (!same_or_apart(state_in, state_out, (int64_t)slots * ctx->shape.channels * (ctx->shape.width - 1) * e))
         return OFRL_EINVAL;
     ConvStepLaunch a;
     std::memset(&a, 0, sizeof(a));

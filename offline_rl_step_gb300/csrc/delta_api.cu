@@ -31,6 +31,7 @@ bool counts_ok(int64_t tokens, int64_t episodes) {
 }
 
 int64_t elem_size(const ofrl_delta_shape& s) { return s.dtype == OFRL_DTYPE_F32 ? 4 : 2; }
+int64_t states_bytes(const ofrl_delta_shape& s, int64_t count) { return count * s.v_heads * s.v_dim * s.k_dim * 4; }
 
 struct Layout {
     int64_t off_status, off_counter, off_scratch, off_parts, total;
@@ -198,7 +199,8 @@ ofrl_status ofrl_delta_forward(ofrl_delta* ctx, const ofrl_delta_tokens* in, con
     if (num_episodes == 0) return OFRL_OK;
     if (in->tokens > 0 && out == nullptr) return OFRL_EINVAL;
     if (!aligned16(out) || !aligned16(init_state) || !aligned16(final_state) ||
-        (reinterpret_cast<uintptr_t>(saved) & 255u))
+        (reinterpret_cast<uintptr_t>(saved) & 255u) ||
+        !same_or_apart(init_state, final_state, states_bytes(ctx->shape, num_episodes)))
         return OFRL_EINVAL;
     SeqLaunch a = base_launch(ctx, in, episode_ends, num_episodes);
     a.init = init_state;
@@ -216,7 +218,9 @@ ofrl_status ofrl_delta_backward(ofrl_delta* ctx, const ofrl_delta_tokens* in, co
     if (!ctx->backward) return OFRL_EINVAL;
     if (num_episodes == 0) return OFRL_OK;
     if (saved == nullptr || (reinterpret_cast<uintptr_t>(saved) & 255u) || grads == nullptr) return OFRL_EINVAL;
-    if (!aligned16(dout) || !aligned16(d_final) || !aligned16(d_init)) return OFRL_EINVAL;
+    if (!aligned16(dout) || !aligned16(d_final) || !aligned16(d_init) ||
+        !same_or_apart(d_final, d_init, states_bytes(ctx->shape, num_episodes)))
+        return OFRL_EINVAL;
     if (in->tokens > 0) {
         const ofrl_delta_shape& h = ctx->shape;
         const int64_t e = elem_size(h), qk = (int64_t)h.k_heads * h.k_dim, vv = (int64_t)h.v_heads * h.v_dim;
@@ -247,6 +251,7 @@ ofrl_status ofrl_delta_step(ofrl_delta* ctx, const ofrl_delta_tokens* in, const 
     if (in->tokens == 0) return OFRL_OK;
     if (!out || !aligned16(out) || !aligned16(state_in) || !aligned16(state_out)) return OFRL_EINVAL;
     if (slots > 0 && (!state_in || !state_out)) return OFRL_EINVAL;
+    if (!same_or_apart(state_in, state_out, states_bytes(ctx->shape, slots))) return OFRL_EINVAL;
     StepLaunch a;
     std::memset(&a, 0, sizeof(a));
     a.shape = ctx->shape;

@@ -21,18 +21,6 @@ inline bool stride_ok(int64_t stride, int64_t width) { return stride >= width &&
 inline bool rows_ok(const void* p, int64_t stride, int64_t width, int64_t elem) {
     return p != nullptr && aligned_to(p, 16) && stride_ok(stride, width) && stride * elem % 16 == 0;
 }
-// Buffers of so many bytes that share memory (NULL shares none).
-inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    if (a == nullptr || b == nullptr) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
-}
-// A step's states: updated in place, or written to a buffer that shares nothing with
-// theirs.  Slots that are shifted against each other would be written by one CTA
-// before another one has read them.
-inline bool step_states_ok(const void* in, const void* out, int64_t bytes) {
-    return in == out || !overlap(in, bytes, out, bytes);
-}
 inline ofrl_status cuda_status(cudaError_t e) { return e == cudaSuccess ? OFRL_OK : OFRL_ECUDA; }
 // The context's device must be the current one.
 template <typename Ctx>

@@ -313,7 +313,7 @@ ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int
     if (!rows_ok(out, out_stride, ctx->shape.channels, dtype_size(ctx->shape.dtype))) return OFRL_EINVAL;
     if (!aligned_to(state_in, 16) || !aligned_to(state_out, 16)) return OFRL_EINVAL;
     if (slots > 0 && (!state_in || !state_out)) return OFRL_EINVAL;
-    if (!step_states_ok(state_in, state_out, (int64_t)slots * ctx->shape.channels * ctx->shape.state_dim * 4))
+    if (!same_or_apart(state_in, state_out, (int64_t)slots * ctx->shape.channels * ctx->shape.state_dim * 4))
         return OFRL_EINVAL;
     scan::StepLaunch a;
     std::memset(&a, 0, sizeof(a));
