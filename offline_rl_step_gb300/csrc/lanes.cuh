@@ -162,9 +162,14 @@ __device__ __forceinline__ float max_or_nan(float x, float y) {
 }
 
 // log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in [0, 1]; log1p(u) / u by a
-// polynomial fitted here to a relative error of 5e-9 over that range, so small
+// polynomial fitted here, one coefficient after the other rounded to fp32 and held
+// while the rest were fitted again: 5.4e-9 of the value off over that range, so small
 // steps keep all their bits (log(1 + u) would not).  u is 2^x with what rounding
-// x = -|v| log2 e leaves put back, or far steps would lose bits.
+// x = -|v| log2 e leaves put back, or far steps would lose bits; with it goes part of
+// ex2.approx's mean error, -5e-8 of the value below 2^-1, -2e-8 above (measured).  More
+// than 2.9e-8 would round values above 2^-1 up.  What is left in a step's mean error is
+// at most 2.6e-8 (without: 5.4e-8).
+constexpr float kExp2Mean = 2.8e-8f;
 __device__ __forceinline__ f2 softplus(f2 v, f2& u) {
     float a, b, lo, hi;
     f2_split(v, a, b);
@@ -175,16 +180,16 @@ __device__ __forceinline__ f2 softplus(f2 v, f2& u) {
     f2 rest = f2_fma(n, f2_both(kLog2e), f2_of(-lo, -hi));
     rest = f2_fma(n, f2_both(1.92596299e-8f), rest);      // log2 e less its fp32 value
     u = f2_of(exp2_of(lo), exp2_of(hi));
-    u = f2_fma(f2_mul(u, f2_both(kLn2)), rest, u);
-    f2 p = f2_both(-0.003244024235755205f);
-    p = f2_fma(p, u, f2_both(0.019851457327604294f));
-    p = f2_fma(p, u, f2_both(-0.056959524750709534f));
-    p = f2_fma(p, u, f2_both(0.10603654384613037f));
-    p = f2_fma(p, u, f2_both(-0.15305592119693756f));
-    p = f2_fma(p, u, f2_both(0.1967593878507614f));
-    p = f2_fma(p, u, f2_both(-0.24954134225845337f));
-    p = f2_fma(p, u, f2_both(0.3332996368408203f));
-    p = f2_fma(p, u, f2_both(-0.4999990165233612f));
+    u = f2_fma(u, f2_fma(rest, f2_both(kLn2), f2_both(kExp2Mean)), u);
+    f2 p = f2_both(-0.0033244711812585592f);
+    p = f2_fma(p, u, f2_both(0.02023317851126194f));
+    p = f2_fma(p, u, f2_both(-0.05772183835506439f));
+    p = f2_fma(p, u, f2_both(0.1068684533238411f));
+    p = f2_fma(p, u, f2_both(-0.1535947173833847f));
+    p = f2_fma(p, u, f2_both(0.19696977734565735f));
+    p = f2_fma(p, u, f2_both(-0.24958936870098114f));
+    p = f2_fma(p, u, f2_both(0.3333055078983307f));
+    p = f2_fma(p, u, f2_both(-0.49999934434890747f));
     p = f2_fma(p, u, f2_both(1.0f));
     return f2_fma(p, u, f2_of(max_or_nan(a, 0.0f), max_or_nan(b, 0.0f)));
 }
