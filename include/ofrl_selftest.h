@@ -1,7 +1,8 @@
 /*
- * ofrl_selftest.h -- self-test hook of the ofrl library's tensor-core
- * building blocks (not part of the method; the tests use it to check the
- * shared-memory descriptors and MMA kinds the hot-path kernels rely on).
+ * ofrl_selftest.h -- self-test hooks of the ofrl library (not part of the
+ * method): tensor-core building blocks, to check the shared-memory descriptors
+ * and MMA kinds the hot-path kernels rely on; a barrier that gives up; how a
+ * call of the selective scan is cut.
  */
 #ifndef OFRL_SELFTEST_H
 #define OFRL_SELFTEST_H
@@ -48,6 +49,15 @@ ofrl_status ofrl_selftest_umma(const float* a, const float* b, float* d, int32_t
  * count stays consistent, so the next normal step runs as usual.  Returns
  * OFRL_EINVAL for a null ctx or values out of range; launches nothing. */
 ofrl_status ofrl_selftest_barrier(ofrl_ctx* ctx, uint64_t wait_ns, int32_t unreachable);
+
+/* How the selective scan cuts a call on a device of num_sms SMs, so that tests
+ * can pick calls that take each of its paths (host only; launches nothing).
+ * out[0] lanes of a channel, [1] channels of a thread, [2] CTAs over the
+ * channels, [3] tokens of a segment, [4] segments, [5] bytes of workspace that
+ * the call uses, [6] bytes that a workspace for max_tokens holds.  Returns the
+ * errors of ofrl_scan_create for shape and counts. */
+ofrl_status ofrl_selftest_scan_cut(const ofrl_scan_shape* shape, int64_t tokens, int32_t episodes, int64_t max_tokens,
+                                   int32_t num_sms, int32_t backward, int64_t* out);
 
 #ifdef __cplusplus
 }

@@ -165,6 +165,7 @@ SIGNATURES = {
     "ofrl_selftest_umma": (C.c_int32, [vp, vp, vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
                                        C.c_int32, vp, vp]),
     "ofrl_selftest_barrier": (C.c_int32, [vp, C.c_uint64, C.c_int32]),
+    "ofrl_selftest_scan_cut": (C.c_int32, [vp, C.c_int64, C.c_int32, C.c_int64, C.c_int32, C.c_int32, vp]),
     "ofrl_delta_create": (C.c_int32, [C.POINTER(DeltaShape), C.c_int64, C.c_int32, C.c_int32, C.POINTER(vp)]),
     "ofrl_delta_destroy": (C.c_int32, [vp]),
     "ofrl_delta_poll_status": (C.c_int32, [vp, vp, C.POINTER(C.c_int32)]),

@@ -6,6 +6,7 @@
 
 #include "rows.cuh"
 #include "scan.cuh"
+#include "../../include/ofrl_selftest.h"
 
 namespace ofrl {
 namespace scan {
@@ -330,6 +331,24 @@ ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int
     const int64_t four = 4 * dtype_size(ctx->shape.dtype);
     a.whole_states = aligned_to(in->b, four) && aligned_to(in->c, four) && in->b_stride % 4 == 0 && in->c_stride % 4 == 0;
     return cuda_status(launch_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+ofrl_status ofrl_selftest_scan_cut(const ofrl_scan_shape* shape, int64_t tokens, int32_t episodes, int64_t max_tokens,
+                                   int32_t num_sms, int32_t backward, int64_t* out) {
+    const ofrl_status s = check_shape(shape);
+    if (s != OFRL_OK) return s;
+    if (!counts_ok(tokens, episodes) || !counts_ok(max_tokens, 0) || num_sms < 1 || (backward != 0 && backward != 1) ||
+        out == nullptr)
+        return OFRL_EINVAL;
+    const Cut c = cut_of(*shape, tokens, episodes, num_sms, backward != 0);
+    out[0] = c.ls;
+    out[1] = c.cpt;
+    out[2] = c.blocks;
+    out[3] = c.seg;
+    out[4] = c.n_seg;
+    out[5] = work_of(*shape, tokens, c, backward != 0).total;
+    out[6] = work_bytes(*shape, max_tokens, num_sms, backward != 0);
+    return OFRL_OK;
 }
 
 }  // extern "C"

@@ -1,11 +1,12 @@
-"""The selective scan where its paths differ: states that are joined while they grow, sums over long segments, rollouts
-of many tokens a CTA, segments that are whole episodes."""
+"""The selective scan where its paths differ: states that are joined while they grow, sums over long segments, steps, segments
+that are whole episodes."""
 import numpy as np
 import pytest
 import torch
 
 from _block import dev, host, junk, scan_inputs
 from _gpu import need_gpu
+from _scan_cut import WHOLE, cut_of
 from test_gpu_scan import _check, _run
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,22 @@ def test_mean_error_of_softplus(lo, hi):
     v = v.astype(np.float64)
     want = np.maximum(v, 0) + np.log1p(np.exp(-np.abs(v)))
     assert abs((host(out) / want - 1).mean()) <= 3e-8
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("case", list(WHOLE), ids=str)
+def test_segments_of_whole_episodes(case, ragged):
+    """Segments as long as the mean episode: episodes of that length, and as many of any length, hardly one of which ends
+    where a segment does."""
+    need_gpu()
+    (c, n, groups), e, length, backward, each = WHOLE[case]
+    t = e * length
+    cut = cut_of((c, n, groups), t, e, torch.cuda.get_device_properties(0).multi_processor_count, backward)
+    assert (cut.seg, cut.segments, cut.each) == (length, e, each)
+    ln, dtype = [length] * e, "bf16"
+    if ragged:
+        at = np.sort(np.random.default_rng(e).integers(0, t + 1, e - 1))
+        ln, dtype = [int(x) for x in np.diff(np.r_[0, at, t])], "fp32"
+        assert max(ln) > 2 * length and min(ln) < length // 8
+    d = scan_inputs(ln, c, n, groups, 12, dtype)
+    _check(d, ln, dtype, _run(d, ln, dtype, slices=True))
