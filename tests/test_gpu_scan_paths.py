@@ -1,10 +1,10 @@
 """The selective scan where its paths differ: states that are joined while they grow, sums over long segments, steps, segments
-that are whole episodes."""
+that are whole episodes, rollouts of many tokens a CTA."""
 import numpy as np
 import pytest
 import torch
 
-from _block import dev, host, junk, scan_inputs
+from _block import ROUNDED, SCAN, check, dev, host, junk, scan_inputs
 from _gpu import need_gpu
 from _scan_cut import WHOLE, cut_of
 from test_gpu_scan import _check, _run
@@ -98,3 +98,56 @@ def test_segments_of_whole_episodes(case, ragged):
         assert max(ln) > 2 * length and min(ln) < length // 8
     d = scan_inputs(ln, c, n, groups, 12, dtype)
     _check(d, ln, dtype, _run(d, ln, dtype, slices=True))
+
+
+def _one_token(d, state, softplus):
+    """The step's outputs and states in 64 bits, a state a token."""
+    x, dt, A, B, C, D, z, b = (d[k].astype(np.float64) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias"))
+    per = x.shape[1] // B.shape[1]
+    delta = np.logaddexp(dt + b, 0.0) if softplus else dt + b
+    h = np.exp(delta[:, :, None] * A) * state + (delta * x)[:, :, None] * np.repeat(B, per, 1)
+    return ((h * np.repeat(C, per, 1)).sum(2) + D * x) * z / (1 + np.exp(-z)), h
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("c,n,groups", [(24, 4, 1), (24, 8, 3), (48, 16, 1), (144, 12, 2), (40, 32, 1), (264, 32, 1), (40, 44, 1),
+                                        (16, 64, 2)])
+def test_rollout_of_many_tokens(dtype, in_place, c, n, groups):
+    """Four to six tokens a CTA, by a list of slots: a third of the tokens name none, in the middle of a CTA's tokens too.
+    B and C of odd offset and stride in one of the two ways."""
+    import offline_rl_step_gb300 as ofrl
+    need_gpu()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    lanes = cut_of((c, n, groups), 16, 1, sms, False).lanes
+    columns = -(-c // (128 // lanes * min(lanes, 4)))
+    ctas = -(-4 * sms // columns)      # along the tokens
+    t = 5 * ctas + ctas // 2 + 1
+    d = scan_inputs([t], c, n, groups, 21, dtype)
+    r = np.random.default_rng(3)
+    slots = t + 50
+    at = r.permutation(slots)[:t].astype(np.int32)
+    bad = r.random(t) < 1 / 3
+    at[bad] = r.choice([-1, slots, -2 ** 31, 2 ** 31 - 1, slots + 7], bad.sum())
+    before = np.float32(r.standard_normal((slots, c, n)))
+    x, dt, B, C, z = (dev(d[k], dtype) for k in ("x", "dt", "B", "C", "z"))
+    if in_place:
+        wide = torch.zeros(t, 2 * groups * n + 3, device="cuda", dtype=B.dtype)
+        wide[:, 1:] = torch.cat([B.flatten(1), C.flatten(1), B[:, 0, :2]], 1)
+        B = wide[:, 1:1 + groups * n].unflatten(1, (groups, n))
+        C = wide[:, 1 + groups * n:1 + 2 * groups * n].unflatten(1, (groups, n))
+    out, state = junk(t, c, dtype=dtype), dev(before)
+    new = state if in_place else torch.full_like(state, 7.0)
+    ctx = ofrl.SelectiveScan(c, n, groups, dtype, True, 0, 0, backward=False)
+    ofrl.scan_step(ctx, x, dt, dev(d["A"]), B, C, state, out, D=dev(d["D"]), z=z, dt_bias=dev(d["dt_bias"]),
+                   new_state=None if in_place else new, slots=torch.from_numpy(at).cuda())
+    assert ctx.poll_status()["bad_index"] == bad.sum()
+    want, h = _one_token(d, before[np.where(bad, 0, at)], True)
+    got, after = host(out), host(new)
+    assert (got[bad] == 0).all()
+    check(got[~bad], want[~bad], SCAN + ROUNDED[dtype], "out")
+    check(after[at[~bad]], h[~bad], SCAN, "state")
+    others = np.setdiff1d(np.arange(slots), at[~bad])
+    assert (after[others] == (before[others] if in_place else 7.0)).all()
+    if not in_place:
+        assert np.array_equal(host(state), before.astype(np.float64))
