@@ -768,7 +768,8 @@ ofrl_status ofrl_scan_step(ofrl_scan* ctx, const ofrl_scan_tokens* in, const int
  * A row is read whole before its outputs are written, so in a forward call out
  * may be x (same stride), and residual_out may be residual where no backward
  * call follows.  What is not finite stays in its row and group (and in the
- * sums over rows that are the weights' gradients). */
+ * sums over rows that are the weights' gradients).  Squares are summed in fp32 as
+ * they are: values from about 1e18 on have an infinite rms. */
 typedef struct {
     int32_t channels;        /* 8 .. 65536 */
     int32_t groups;          /* divides channels; channels / groups a multiple of 8, at most 8192 */
@@ -799,7 +800,10 @@ typedef struct {
 typedef struct ofrl_norm ofrl_norm;
 
 /* The workspace (its size does not depend on the rows; backward = 0 refuses the
- * backward calls).  The only allocating call; binds to the current device. */
+ * backward calls).  The only allocating call; binds to the current device.
+ * Backward calls keep their parts of the weights' gradients in it: one ofrl_norm
+ * must not be used by two of them that overlap on the GPU.  Forward calls use
+ * none of it. */
 ofrl_status ofrl_norm_create(const ofrl_norm_shape* shape, int32_t backward, ofrl_norm** out);
 ofrl_status ofrl_norm_destroy(ofrl_norm* ctx);
 int64_t ofrl_norm_workspace_bytes(const ofrl_norm_shape* shape, int32_t backward);

@@ -802,7 +802,8 @@ class BlockNorm(_Workspace):
     """Workspace of the gated norm and the residual norm (ofrl_norm_create); the only allocation.
 
     Each of `groups` equal groups of channels is normed by itself.  residual_dtype: the residual stream's type, "fp32"
-    or dtype (the default).  backward=False reserves no memory for the gradients, which are then refused."""
+    or dtype (the default).  backward=False reserves no memory for the gradients, which are then refused.  Two backward
+    calls with one workspace must not overlap on the GPU: it holds their parts of the weights' gradients."""
 
     def __init__(self, channels: int, groups: int = 1, dtype: str = "bf16", residual_dtype: Optional[str] = None,
                  backward: bool = True):
