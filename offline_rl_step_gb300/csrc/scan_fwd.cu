@@ -172,15 +172,13 @@ struct Joined {      // carry <- 2^rate carry + own, or own alone
     bool open;
 };
 
-// Decays are kept as exponents until they meet a state.  A state that grows may have
-// one past fp32's range: then in three factors, so that a state of zero stays zero
-// (infinity times zero is no number); 2^378 takes any other state past the range.
-__device__ __forceinline__ float joined(float rate, float carry, float own) {
-    if (rate > 126.0f && rate < INFINITY) {
-        const float k = exp2_of(fminf(rate, 378.0f) * (1.0f / 3.0f));
-        return fmaf(carry * k * k, k, own);
-    }
-    return fmaf(exp2_of(rate), carry, own);
+// Decays are kept as exponents until they meet a state, then in two halves: that of a
+// state that grows may pass fp32's range, and a state of zero stays zero all the same
+// (infinity times zero is no number).  2^254 takes every normal state past the range.
+// Where the rate is no number, own is none either.
+__device__ __forceinline__ float joined(const Joined& x, float carry) {
+    const float half = exp2_of(fminf(x.rate, 254.0f) * 0.5f);
+    return x.open ? fmaf(carry * half, half, x.own) : x.own;
 }
 
 __global__ void __launch_bounds__(32 * kCarryWarps) scan_carry_kernel(const __grid_constant__ Launch a, int backward) {
@@ -222,20 +220,17 @@ __global__ void __launch_bounds__(32 * kCarryWarps) scan_carry_kernel(const __gr
     };
     Joined all = {0.0f, 0.0f, true};      // open: what came before the slice still counts
     over([&](int, const Joined& x) {
-        all.own = x.open ? joined(x.rate, all.own, x.own) : x.own;
+        all.own = joined(x, all.own);
         all.rate += x.rate;
         all.open = all.open && x.open;
     });
     slices[slice][lane] = all;
     __syncthreads();
     float carry = 0.0f;
-    for (int k = 0; k < slice; ++k) {
-        const Joined x = slices[k][lane];
-        carry = x.open ? joined(x.rate, carry, x.own) : x.own;
-    }
+    for (int k = 0; k < slice; ++k) carry = joined(slices[k][lane], carry);
     over([&](int j, const Joined& x) {
         a.tail[j * states + i] = carry;
-        carry = x.open ? joined(x.rate, carry, x.own) : x.own;
+        carry = joined(x, carry);
     });
 }
 
