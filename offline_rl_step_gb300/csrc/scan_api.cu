@@ -36,9 +36,9 @@ int per_sm_of(bool backward, int cpt) { return !backward ? 4 : cpt == 4 ? 2 : 3;
 //    latency: 32 of 512, 256 of 64, read 221 (156); gradients of 1024 channels of 8
 //    states for them 379 (275); so there are limits on how much longer.
 // 2. Even shares in the wide form (a token's deltas and inputs are read by fewer
-//    threads, its B and C serve more channels), where its CTAs fill half
-//    (gradients: three quarters) of the GPU: 16384 tokens of 512 channels of 16 states
-//    read 88 (narrow 111 to 116), trained 331 (358).
+//    threads, its B and C serve more channels), where that makes two CTAs an SM
+//    (gradients: one and a half), whatever an SM holds of that form: 16384 tokens of
+//    512 channels of 16 states read 88 (narrow 111 to 116), trained 331 (358).
 // 3. Even shares in the narrow one: 8 episodes of 128 to 384, 128 channels of 16
 //    states, read 17 (wide 25), trained 58 (79).
 // Only the narrow form where the wide one leaves a quarter more threads without a

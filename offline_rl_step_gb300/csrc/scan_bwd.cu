@@ -9,9 +9,9 @@
 // token's channels (dB, dC) are made over the CTA's threads, then over the CTAs.
 //
 // 228 episodes of 64 to 512 tokens, 65536 in all, 512 channels of 16 states, bf16: tails
-// 89 us, their join 7, the gradients 700, the joins of their parts 11.  The gradients'
+// 90 us, their join 7, the gradients 700, the joins of their parts 11.  The gradients'
 // 15 fp32 operations and two exp2 for each state would be 230 us; a thread has 16
-// states, 240 registers and 48 bytes of p and parts a state in shared memory, so an SM
+// states, 232 registers and 48 bytes of p and parts a state in shared memory, so an SM
 // holds eight warps, which keep issue 47% and shared memory 56% busy.  (States saved
 // every 16 tokens and two channels a thread: 74 us more.  The loops unrolled, or
 // stores that loads may pass: no change.)
