@@ -63,8 +63,8 @@ def test_steps_summed_over_long_segments(step):
 @pytest.mark.parametrize("lo,hi", [(-80, -30), (-30, -10), (-10, -6), (-6, -4), (-4, -3), (-3, -2), (-2, -1), (-1, -0.5),
                                    (-0.5, -0.1), (-0.1, 0), (0, 0.1), (0.1, 0.5), (0.5, 1), (1, 3), (3, 10), (10, 30)], ids=str)
 def test_mean_error_of_softplus(lo, hi):
-    """Slow states sum their steps' mean error up, not each one's rounding.  The exponential's is at most 5.2e-8 (as the
-    decays' in size), 2.8e-8 of which is taken out; the polynomial is up to 5.4e-9 off.  The mean of 2^18 roundings, 7e-8
+    """Slow states sum their steps' mean error up, not each one's rounding.  The exponential's is at most 5.2e-8 over each
+    of these ranges, 2.8e-8 of which is taken out; the polynomial is up to 5.4e-9 off.  The mean of 2^18 roundings, 7e-8
     each in the mean square, is 1.4e-10."""
     import offline_rl_step_gb300 as ofrl
     need_gpu()
